@@ -35,6 +35,7 @@
  *     head h reads query/key head h / (Hv / Hk) (repeat_interleave on the
  *     head dimension, [HP-CP] the P2P wrapper's forward).
  *   - Supported: dk, dv in {32, 64, 128}; conv kernel size 1..4; chunk 64.
+ *     (The selective scan layer and the block norm, at the end, state their own.)
  *   - dtype GDN_BF16: q/k/v/x/beta/o/conv weights in bf16, arithmetic and
  *     the state in fp32.  GDN_F32: everything fp32.  g is always fp32.
  *   - Errors detectable on the host return a non-OK status before anything
@@ -461,6 +462,179 @@ gdn_status gdn_shard_fwd_noalloc(const void *x, const void *conv_w, const void *
                                  int32_t Hk, int32_t Hv, int32_t dk, int32_t dv, float scale,
                                  uint32_t flags, int32_t n_shards, gdn_dtype dtype, void *o,
                                  float *h_final, int32_t *plan_out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Selective scan layer.  The entry points below have no counterpart on the
+ * source pages: they are the other recurrent layer that a stack of gated
+ * linear-attention layers holds, over the same packed tokens (cu_seqlens) and
+ * with the same conventions, and the norms between two blocks of such a stack.
+ *
+ * Causal depthwise conv1d + SiLU with a state per sequence
+ *
+ *   y[t, c] = silu(bias[c] + sum_{j < conv_k} w[c, j] * x'[t - conv_k + 1 + j, c])
+ *
+ * x' is x within the token's own sequence n and state[n] before its start:
+ * row conv_k - 2 of state[n] is the token just before the sequence's first.
+ *   x, y      device [T, channels] dtype, row strides ldx, ldy; no overlap
+ *   w         device [channels, conv_k] dtype;  bias device [channels] or NULL
+ *   state     device [num_seqs, conv_k - 1, channels] dtype, or NULL (zeros)
+ *   state_out device, as state, or NULL: the last conv_k - 1 rows of
+ *             (state[n], x of sequence n), so that a prompt may be fed in
+ *             pieces; must not overlap state
+ * Needs channels % 8 == 0, conv_k 1..4, row strides multiples of 8 and
+ * 16-byte aligned x, y, state and state_out.  fp32 accumulation.  The SiLU is
+ * a / (1 + e^-a) for both types (gdn_conv_silu takes a hardware tanh for
+ * bf16).  A malformed cu_seqlens gives unspecified results, never an access
+ * outside the arrays (this holds for every entry point below).
+ *
+ * gdn_ssm_conv_bwd: gradients of the above for dy and dstate_out
+ *   dy         device [T, channels] dtype, row stride lddy
+ *   dstate_out device [num_seqs, conv_k - 1, channels] fp32, or NULL (zero)
+ *   dx         device [T, channels] dtype, row stride lddx
+ *   dw         device [channels, conv_k] fp32;  dbias device [channels] fp32
+ *              or NULL;  dstate device [num_seqs, conv_k - 1, channels] fp32
+ *              or NULL
+ *   workspace  device, >= gdn_ssm_conv_bwd_workspace_size(...) bytes, 256-byte
+ *              aligned, contents on entry irrelevant
+ * Sums are taken in a fixed order: equal calls give equal bits.
+ *
+ * gdn_ssm_conv_step: one token of `batch` requests over a cache of states
+ *   x, y    device [batch, channels] dtype, row strides ldx, ldy
+ *   states  device [num_slots, conv_k - 1, channels] dtype
+ *   src, dst device int32 [batch] or NULL (slot i for request i): request i
+ *           reads slot src[i] and writes the state after its token to slot
+ *           dst[i] (equal for an update in place).  src[i] < 0: a zero state
+ *           (a new request).  dst[i] < 0: a padded row, for which nothing is
+ *           read or written but zeros to y.  A slot number >= num_slots is
+ *           taken as negative.  No slot may be the dst of two requests, nor
+ *           the dst of one and the src of another.
+ * ---------------------------------------------------------------------- */
+gdn_status gdn_ssm_conv_fwd(const void *x, int64_t ldx, gdn_dtype dtype, int32_t T,
+                            int32_t channels, const void *w, const void *bias, int32_t conv_k,
+                            const int32_t *cu_seqlens, int32_t num_seqs, const void *state,
+                            void *state_out, void *y, int64_t ldy, void *stream);
+size_t gdn_ssm_conv_bwd_workspace_size(int32_t T, int32_t channels, int32_t conv_k);
+gdn_status gdn_ssm_conv_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                            gdn_dtype dtype, int32_t T, int32_t channels, const void *w,
+                            const void *bias, int32_t conv_k, const int32_t *cu_seqlens,
+                            int32_t num_seqs, const void *state, const float *dstate_out, void *dx,
+                            int64_t lddx, float *dw, float *dbias, float *dstate, void *workspace,
+                            size_t workspace_bytes, void *stream);
+gdn_status gdn_ssm_conv_step(const void *x, int64_t ldx, gdn_dtype dtype, int32_t batch,
+                             int32_t channels, const void *w, const void *bias, int32_t conv_k,
+                             void *states, int32_t num_slots, const int32_t *src,
+                             const int32_t *dst, void *y, int64_t ldy, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Selective state space scan: per sequence and channel c (group
+ * q = c / (channels / groups)), with N = d_state diagonal states in fp32,
+ *
+ *   delta_t = softplus(dt_t + dt_bias)         (softplus(v) = v for v > 20)
+ *   h_n    <- exp(-exp(A_log[c, n]) delta_t) h_n + delta_t x_t B_t[q, n]
+ *   y_t     = (sum_n C_t[q, n] h_n + D x_t) * silu(z_t)
+ *
+ *   x, dt   device [T, channels] dtype, row strides ldx, lddt
+ *   z       as x with row stride ldz, or NULL (no gate)
+ *   B, C    device [T, groups, N] dtype at B + t * ldb + q * N + n (C: ldc);
+ *           any alignment and row stride
+ *   A_log   device [channels, N] fp32;  D, dt_bias device [channels] fp32 or
+ *           NULL (zero)
+ *   h0      device [num_seqs, channels, N] fp32 or NULL (zero)
+ *   y       device [T, channels] dtype, row stride ldy
+ *   h_final device [num_seqs, channels, N] fp32, or NULL: the state after each
+ *           sequence's last token (h0 or 0 for an empty sequence); must not
+ *           overlap h0
+ *   ckpt    device fp32 [gdn_ssm_scan_ckpt_floats(...)], or NULL: the states
+ *           before every 64th packed token, for gdn_ssm_scan_bwd
+ *   workspace device, >= gdn_ssm_scan_workspace_size(...) bytes, 256-byte
+ *           aligned, contents on entry irrelevant
+ * Needs channels / groups a multiple of 8, N in 1..64, row strides of x, dt,
+ * z, y multiples of 8 and those arrays 16-byte aligned.  All arithmetic in
+ * fp32 whatever the dtype; y is rounded once.  The packed tokens are cut into
+ * segments that run at the same time; a first pass gives each segment's own
+ * end state where the next one continues its sequence.
+ *
+ * gdn_ssm_scan_bwd: gradients for dy (w.r.t. y) and dh_final (fp32
+ * [num_seqs, channels, N] or NULL = zero), with the forward's inputs and ckpt
+ *   dx, ddt, dz  device [T, channels] dtype, dense (dz NULL iff z is)
+ *   dB, dC       device [T, groups, N] dtype, dense
+ *   dA_log       device [channels, N] fp32;  dD, ddt_bias device [channels]
+ *                fp32 or NULL;  dh0 device [num_seqs, channels, N] fp32 or NULL
+ *   workspace    device, >= gdn_ssm_scan_bwd_workspace_size(...) bytes,
+ *                256-byte aligned, contents on entry irrelevant
+ * Sums are taken in a fixed order: equal calls give equal bits.
+ *
+ * gdn_ssm_scan_step: one token of `batch` requests over a cache of states
+ *   x, dt, z, B, C, y  as above with batch rows in place of T
+ *   states  device [num_slots, channels, N] fp32, 16-byte aligned
+ *   src, dst           as in gdn_ssm_conv_step
+ * ---------------------------------------------------------------------- */
+size_t gdn_ssm_scan_ckpt_floats(int32_t T, int32_t channels, int32_t d_state);
+size_t gdn_ssm_scan_workspace_size(int32_t T, int32_t channels, int32_t d_state, int32_t groups);
+gdn_status gdn_ssm_scan_fwd(const void *x, int64_t ldx, const void *dt, int64_t lddt, const void *z,
+                            int64_t ldz, const void *B, int64_t ldb, const void *C, int64_t ldc,
+                            gdn_dtype dtype, const float *A_log, const float *D,
+                            const float *dt_bias, const float *h0, const int32_t *cu_seqlens,
+                            int32_t num_seqs, int32_t T, int32_t channels, int32_t d_state,
+                            int32_t groups, void *y, int64_t ldy, float *h_final, float *ckpt,
+                            void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn_ssm_scan_bwd_workspace_size(int32_t T, int32_t channels, int32_t d_state,
+                                       int32_t groups);
+gdn_status gdn_ssm_scan_bwd(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                            const void *dt, int64_t lddt, const void *z, int64_t ldz, const void *B,
+                            int64_t ldb, const void *C, int64_t ldc, gdn_dtype dtype,
+                            const float *A_log, const float *D, const float *dt_bias,
+                            const float *h0, const float *ckpt, const float *dh_final,
+                            const int32_t *cu_seqlens, int32_t num_seqs, int32_t T,
+                            int32_t channels, int32_t d_state, int32_t groups, void *dx, void *ddt,
+                            void *dz, void *dB, void *dC, float *dA_log, float *dD, float *ddt_bias,
+                            float *dh0, void *workspace, size_t workspace_bytes, void *stream);
+gdn_status gdn_ssm_scan_step(const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                             const void *z, int64_t ldz, const void *B, int64_t ldb, const void *C,
+                             int64_t ldc, gdn_dtype dtype, const float *A_log, const float *D,
+                             const float *dt_bias, int32_t batch, int32_t channels,
+                             int32_t d_state, int32_t groups, float *states, int32_t num_slots,
+                             const int32_t *src, const int32_t *dst, void *y, int64_t ldy,
+                             void *stream);
+
+/* ------------------------------------------------------------------------
+ * Block norm: what stands between two blocks of a stack, in one pass.  Per
+ * token row of `width` values, rms(v) = sqrt(mean(v^2) + eps):
+ *
+ *   p       = w_post * o / rms(o)                   (w_post NULL: p = o)
+ *   res_out = res + scale * sigmoid(gate) * p       (gate, scale NULL: 1)
+ *   y       = w_pre * res_out / rms(res_out)        (res_out before rounding)
+ *
+ *   o       device [T, width] dtype: the block's output;  gate as o (raw), or
+ *           NULL;  y as o: the next block's input
+ *   res, res_out device [T, width] res_dtype (dtype or GDN_F32): the residual
+ *           stream; res_out may be res
+ *   w_post, w_pre device [width] dtype;  scale device [width] fp32
+ * All arrays dense but for the token row strides ldo, ldgate (multiples of
+ * 8); 16-byte aligned; width % 8 == 0, width <= 16384.
+ *
+ * gdn_block_norm_bwd: gradients for dy and dres_out (res_dtype, or NULL =
+ * zero).  res_out is the stored stream; the pre norm is taken at it.
+ *   d_o, dgate device [T, width] dtype (dgate NULL iff gate is)
+ *   dres       device [T, width] res_dtype; may be dres_out
+ *   dw_pre, dw_post, dscale device [width] fp32 (the latter two NULL iff
+ *              w_post / scale is)
+ *   workspace  device, >= gdn_block_norm_bwd_workspace_size(...) bytes,
+ *              256-byte aligned, contents on entry irrelevant
+ * Sums are taken in a fixed order: equal calls give equal bits.
+ * ---------------------------------------------------------------------- */
+gdn_status gdn_block_norm_fwd(const void *o, int64_t ldo, const void *gate, int64_t ldgate,
+                              gdn_dtype dtype, const void *res, gdn_dtype res_dtype,
+                              const void *w_post, const void *w_pre, const float *scale, float eps,
+                              int32_t T, int32_t width, void *res_out, void *y, void *stream);
+size_t gdn_block_norm_bwd_workspace_size(int32_t T, int32_t width);
+gdn_status gdn_block_norm_bwd(const void *dy, const void *dres_out, const void *o, int64_t ldo,
+                              const void *gate, int64_t ldgate, gdn_dtype dtype,
+                              const void *res_out, gdn_dtype res_dtype, const void *w_post,
+                              const void *w_pre, const float *scale, float eps, int32_t T,
+                              int32_t width, void *d_o, void *dgate, void *dres, float *dw_pre,
+                              float *dw_post, float *dscale, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

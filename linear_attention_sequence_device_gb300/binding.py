@@ -73,6 +73,28 @@ SIGNATURES = {
     "gdn_shard_fwd_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32,
                                              _i32, _i32, _i32, _i32, _f32, _u32, _i32,
                                              ctypes.c_int, _vp, _vp, _vp, _vp]),
+    # the selective scan layer and the block norm (front end: ssm.py)
+    "gdn_ssm_conv_fwd": (ctypes.c_int, [_vp, _i64, ctypes.c_int, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp,
+                                        _vp, _i64, _vp]),
+    "gdn_ssm_conv_bwd_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "gdn_ssm_conv_bwd": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _i32, _i32, _vp, _vp, _i32, _vp, _i32,
+                                        _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "gdn_ssm_conv_step": (ctypes.c_int, [_vp, _i64, ctypes.c_int, _i32, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp,
+                                         _vp, _i64, _vp]),
+    "gdn_ssm_scan_ckpt_floats": (_sz, [_i32, _i32, _i32]),
+    "gdn_ssm_scan_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
+    "gdn_ssm_scan_fwd": (ctypes.c_int, [_vp, _i64] * 5 + [ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                                                          _i32, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "gdn_ssm_scan_bwd_workspace_size": (_sz, [_i32, _i32, _i32, _i32]),
+    "gdn_ssm_scan_bwd": (ctypes.c_int, [_vp, _i64] * 6 + [ctypes.c_int] + [_vp] * 7 + [_i32] * 5 + [_vp] * 10 +
+                         [_sz, _vp]),
+    "gdn_ssm_scan_step": (ctypes.c_int, [_vp, _i64] * 5 + [ctypes.c_int, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                                                           _i32, _vp, _vp, _vp, _i64, _vp]),
+    "gdn_block_norm_fwd": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _vp, _f32,
+                                          _i32, _i32, _vp, _vp, _vp]),
+    "gdn_block_norm_bwd_workspace_size": (_sz, [_i32, _i32]),
+    "gdn_block_norm_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
+                                          _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 32 << 20
 

@@ -1,0 +1,418 @@
+// The selective scan layer's short convolution: its gradient, its single-token
+// form and the C entry points (the prompt's forward is conv.cu's STATE form).
+//
+// Forward: pre[t] = b + sum_j w[j] x'[t - K + 1 + j], y = pre s(pre), s the
+// logistic function.  Backward, with ds[t] = dy s (1 + pre (1 - s)):
+//   dx'[t] = sum_j w[j] ds[t + K - 1 - j] within the sequence,
+//   dw[j] = sum_t ds[t] x'[t - K + 1 + j],  db = sum_t ds[t];
+// the gradients of the K - 1 rows before a sequence's start are its state's,
+// and dstate_out adds to the last K - 1 rows.
+#include "ssm_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int NT = 128;
+constexpr int CV = 4;   // channels per thread of the backward
+constexpr int RB = 4;   // rows loaded ahead
+
+template <typename T> struct Raw4;
+template <> struct Raw4<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void unpack(float (&f)[4]) const {
+        f[0] = __uint_as_float(v.x << 16);
+        f[1] = __uint_as_float(v.x & 0xffff0000u);
+        f[2] = __uint_as_float(v.y << 16);
+        f[3] = __uint_as_float(v.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[4]) {
+        uint2 r;
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&r);
+        h[0] = __floats2bfloat162_rn(f[0], f[1]);
+        h[1] = __floats2bfloat162_rn(f[2], f[3]);
+        *reinterpret_cast<uint2*>(p) = r;
+    }
+};
+template <> struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void unpack(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+
+struct ConvBwdParams {
+    const void* dy; int64_t lddy;
+    const void* x; int64_t ldx;
+    const void* w; const void* b;
+    int T, C;
+    const int32_t* cu; int num_seqs;
+    const void* state; const float* dso;
+    void* dx; int64_t lddx;
+    float* dstate;
+    float* part;  // [strips, C K + C]
+    int rows;     // rows per strip
+};
+
+// HBM-bound: x and dy in, dx out, each once.  A thread owns four channels of a
+// strip of rows and walks down it with a window of the last K - 1 inputs and of
+// the K - 1 rows whose dx is not complete yet.  A strip runs K - 1 rows past
+// its end (within the sequence) for the dx of its own last rows; those rows'
+// dw and db belong to the next strip.
+template <typename T, int K>
+__global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
+    constexpr int H = K > 1 ? K - 1 : 1;
+    const int c0 = (blockIdx.x * NT + threadIdx.x) * CV;
+    if (c0 >= p.C) return;
+    const int nseq = p.num_seqs;
+    const int32_t* cu = p.cu;
+    const T* x = static_cast<const T*>(p.x) + c0;
+    const T* dy = static_cast<const T*>(p.dy) + c0;
+    T* dx = static_cast<T*>(p.dx) + c0;
+
+    auto end_grad = [&](int seq, int j, float (&f)[4]) {  // dstate_out row j
+        if (p.dso) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p.dso + ((int64_t)seq * (K - 1) + j) * p.C + c0));
+            f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+        } else {
+            f[0] = f[1] = f[2] = f[3] = 0.f;
+        }
+    };
+    auto put_state = [&](int seq, int j, const float (&f)[4]) {
+        if (p.dstate) Raw4<float>::store(p.dstate + ((int64_t)seq * (K - 1) + j) * p.C + c0, f);
+    };
+    auto pass_empty = [&](int seq) {  // its final state is its initial one
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            float f[4];
+            end_grad(seq, j, f);
+            put_state(seq, j, f);
+        }
+    };
+
+    float w[K][4], b[4], dw[K][4], db[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            w[j][c] = Elem<T>::to_f(static_cast<const T*>(p.w)[(int64_t)(c0 + c) * K + j]);
+            dw[j][c] = 0.f;
+        }
+        b[c] = p.b ? Elem<T>::to_f(static_cast<const T*>(p.b)[c0 + c]) : 0.f;
+        db[c] = 0.f;
+    }
+    const int lt0 = blockIdx.y * p.rows, lt1 = min(p.T, lt0 + p.rows);
+    if (p.T == 0) {
+        if (blockIdx.y == 0)
+            for (int m = 0; m < nseq; ++m) pass_empty(m);
+    } else if (lt0 < p.T) {
+        int seg = seq_of(cu, nseq, lt0);
+        int start = __ldg(cu + seg), next = __ldg(cu + seg + 1);
+        if (start == lt0)  // empty sequences that end where this strip starts
+            for (int m = seg - 1; m >= 0 && __ldg(cu + m) == lt0; --m) pass_empty(m);
+        float win[H][4], acc[H][4];
+        auto load_state = [&](int j, float (&f)[4]) {
+            if (p.state) {
+                Raw4<T> r;
+                r.load(static_cast<const T*>(p.state) + ((int64_t)seg * (K - 1) + j) * p.C + c0);
+                r.unpack(f);
+            } else {
+                f[0] = f[1] = f[2] = f[3] = 0.f;
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const int row = lt0 - (K - 1) + j, m = K - 1 - (start - row);
+            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+            if (row >= start && row >= 0) {
+                Raw4<T> r;
+                r.load(x + (int64_t)row * p.ldx);
+                r.unpack(win[j]);
+            } else if (m >= 0 && m < K - 1) {
+                load_state(m, win[j]);
+            } else {
+                win[j][0] = win[j][1] = win[j][2] = win[j][3] = 0.f;
+            }
+        }
+        auto emit = [&](int row, const float (&f)[4]) {
+            if (row >= start) {
+                if (row >= lt0 && row < lt1) Raw4<T>::store(dx + (int64_t)row * p.lddx, f);
+            } else if (start >= lt0) {
+                const int m = K - 1 - (start - row);
+                if (m >= 0 && m < K - 1) put_state(seg, m, f);
+            }
+        };
+        const int tend = min(p.T, lt1 + K - 1);
+        Raw4<T> nx[RB], ny[RB];
+        auto fetch = [&](int t) {
+#pragma unroll
+            for (int u = 0; u < RB; ++u) {
+                const int r = min(t + u, p.T - 1);
+                nx[u].load(x + (int64_t)r * p.ldx);
+                ny[u].load(dy + (int64_t)r * p.lddy);
+            }
+        };
+        fetch(lt0);
+        bool done = false;
+        for (int tb = lt0; tb < tend && !done; tb += RB) {
+            Raw4<T> cx[RB], cy[RB];
+#pragma unroll
+            for (int u = 0; u < RB; ++u) {
+                cx[u] = nx[u];
+                cy[u] = ny[u];
+            }
+            if (tb + RB < tend) fetch(tb + RB);
+#pragma unroll
+            for (int u = 0; u < RB; ++u) {
+                const int t = tb + u;
+                if (t == next && !done) {  // a new sequence
+                    if (t >= lt1) done = true;
+                    else {
+                        while (seg + 1 < nseq) {
+                            ++seg;
+                            next = __ldg(cu + seg + 1);
+                            if (next != t) break;
+                            pass_empty(seg);
+                        }
+                        start = t;
+#pragma unroll
+                        for (int j = 0; j < K - 1; ++j) {
+                            load_state(j, win[j]);
+                            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+                        }
+                    }
+                }
+                if (done || t >= tend) continue;
+                float xv[4], g[4];
+                cx[u].unpack(xv);
+                cy[u].unpack(g);
+                const bool own = t < lt1;
+                float first[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float pre = b[c];
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) pre = fmaf(w[j][c], win[j][c], pre);
+                    pre = fmaf(w[K - 1][c], xv[c], pre);
+                    const float s = sigmoid_fast(pre);
+                    const float ds = g[c] * s * fmaf(pre, 1.f - s, 1.f);
+                    const float dsw = own ? ds : 0.f;
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) dw[j][c] = fmaf(dsw, win[j][c], dw[j][c]);
+                    dw[K - 1][c] = fmaf(dsw, xv[c], dw[K - 1][c]);
+                    db[c] += dsw;
+                    first[c] = fmaf(w[0][c], ds, K > 1 ? acc[0][c] : 0.f);
+#pragma unroll
+                    for (int j = 0; j + 1 < K - 1; ++j) {
+                        acc[j][c] = fmaf(w[j + 1][c], ds, acc[j + 1][c]);
+                        win[j][c] = win[j + 1][c];
+                    }
+                    if (K > 1) {
+                        acc[H - 1][c] = w[K - 1][c] * ds;
+                        win[H - 1][c] = xv[c];
+                    }
+                }
+                emit(t - (K - 1), first);
+                if (t + 1 == next) {  // the sequence ends: its last rows are complete
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) {
+                        float f[4];
+                        end_grad(seg, j, f);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) f[c] += acc[j][c];
+                        emit(t - (K - 1) + 1 + j, f);
+                    }
+                }
+            }
+        }
+        if (lt1 == p.T && next == p.T)
+            for (int m = seg + 1; m < nseq; ++m) pass_empty(m);
+    }
+    float* part = p.part + (int64_t)blockIdx.y * p.C * (K + 1);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < K; ++j) part[(int64_t)(c0 + c) * K + j] = dw[j][c];
+    Raw4<float>::store(part + (int64_t)p.C * K + c0, db);
+}
+
+// One token per request: read K - 1 state rows, write K - 1 (shifted) and y.
+// Bound by those bytes (or, for a few requests, by the launch).
+template <typename T, int K>
+__global__ void __launch_bounds__(NT) conv_step_kernel(const T* x, int64_t ldx, int C, const T* w, const T* bias,
+                                                       T* states, int num_slots, const int32_t* src,
+                                                       const int32_t* dst, T* y, int64_t ldy) {
+    const int c0 = (blockIdx.x * NT + threadIdx.x) * 8, r = blockIdx.y;
+    if (c0 >= C) return;
+    int from = src ? __ldg(src + r) : r, to = dst ? __ldg(dst + r) : r;
+    if (from >= num_slots) from = -1;
+    float f[8];
+    T* yr = y + (int64_t)r * ldy + c0;
+    if (to < 0 || to >= num_slots) {  // a padded row
+#pragma unroll
+        for (int c = 0; c < 8; ++c) f[c] = 0.f;
+        store8(yr, f);
+        return;
+    }
+    float acc[8], row[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = bias ? Elem<T>::to_f(bias[c0 + c]) : 0.f;
+    T* out = states + (int64_t)to * (K - 1) * C + c0;
+    const T* in = states + (int64_t)from * (K - 1) * C + c0;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        if (j == K - 1) load8(x + (int64_t)r * ldx + c0, row);
+        else if (from >= 0) load8_rw(in + (int64_t)j * C, row);
+        else
+#pragma unroll
+            for (int c = 0; c < 8; ++c) row[c] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(Elem<T>::to_f(w[(int64_t)(c0 + c) * K + j]), row[c], acc[c]);
+        if (j > 0) store8(out + (int64_t)(j - 1) * C, row);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) f[c] = silu_fast(acc[c]);
+    store8(yr, f);
+}
+
+// Strips of the backward: enough blocks for four resident ones an SM, strips of
+// 64 rows at least.
+int bwd_strips(int T, int C) {
+    const int nx = (C / CV + NT - 1) / NT;
+    int n = device_sm_count() * 4 / nx;
+    const int most = T / 64;
+    if (n > most) n = most;
+    if (n > 65535) n = 65535;
+    return n < 1 ? 1 : n;
+}
+
+template <typename T>
+gdn_status run_bwd(ConvBwdParams p, int K, cudaStream_t s) {
+    const int strips = bwd_strips(p.T, p.C);
+    p.rows = p.T > 0 ? (p.T + strips - 1) / strips : 1;
+    const dim3 grid((p.C / CV + NT - 1) / NT, strips);
+    switch (K) {
+        case 1: conv_bwd_kernel<T, 1><<<grid, NT, 0, s>>>(p); break;
+        case 2: conv_bwd_kernel<T, 2><<<grid, NT, 0, s>>>(p); break;
+        case 3: conv_bwd_kernel<T, 3><<<grid, NT, 0, s>>>(p); break;
+        default: conv_bwd_kernel<T, 4><<<grid, NT, 0, s>>>(p); break;
+    }
+    return check_launch("conv_bwd_kernel");
+}
+
+template <typename T>
+gdn_status run_step(const void* x, int64_t ldx, int batch, int C, const void* w, const void* bias, int K, void* states,
+                    int num_slots, const int32_t* src, const int32_t* dst, void* y, int64_t ldy, cudaStream_t s) {
+    const dim3 grid((C / 8 + NT - 1) / NT, batch);
+    const T *xt = static_cast<const T*>(x), *wt = static_cast<const T*>(w), *bt = static_cast<const T*>(bias);
+    T *st = static_cast<T*>(states), *yt = static_cast<T*>(y);
+    switch (K) {
+        case 1: conv_step_kernel<T, 1><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+        case 2: conv_step_kernel<T, 2><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+        case 3: conv_step_kernel<T, 3><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+        default: conv_step_kernel<T, 4><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+    }
+    return check_launch("conv_step_kernel");
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+gdn_status check_conv(gdn_dtype dtype, int rows, int channels, const void* w, int conv_k) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+    if (rows < 0 || channels < 1) return fail(GDN_ERR_INVALID_ARG, "rows=%d channels=%d", rows, channels);
+    if (channels % 8 != 0) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "channels=%d not a multiple of 8", channels);
+    if (conv_k < 1 || conv_k > 4) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "conv_k=%d not in 1..4", conv_k);
+    if (!w) return fail(GDN_ERR_INVALID_ARG, "w is NULL");
+    return GDN_OK;
+}
+
+gdn_status check_rows(const void* p, int64_t ld, int64_t least, const char* name) {
+    if (!p || !al16(p)) return fail(GDN_ERR_INVALID_ARG, "%s must be 16-byte aligned and not NULL", name);
+    if (ld < least || ld % 8 != 0)
+        return fail(GDN_ERR_INVALID_ARG, "row stride of %s (%lld) must be >= %lld and a multiple of 8", name,
+                    (long long)ld, (long long)least);
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_ssm_conv_fwd(const void* x, int64_t ldx, gdn_dtype dtype, int32_t T, int32_t channels, const void* w,
+                            const void* bias, int32_t conv_k, const int32_t* cu_seqlens, int32_t num_seqs,
+                            const void* state, void* state_out, void* y, int64_t ldy, void* stream) {
+    gdn_status st = check_conv(dtype, T, channels, w, conv_k);
+    if (st != GDN_OK) return st;
+    if (num_seqs < 1 || !cu_seqlens) return fail(GDN_ERR_INVALID_ARG, "num_seqs=%d or cu_seqlens is NULL", num_seqs);
+    if (!al16(state) || !al16(state_out))
+        return fail(GDN_ERR_INVALID_ARG, "state and state_out must be 16-byte aligned");
+    if (state && state == state_out) return fail(GDN_ERR_INVALID_ARG, "state_out must not be state");
+    if (T > 0) {
+        if ((st = check_rows(x, ldx, channels, "x")) != GDN_OK) return st;
+        if ((st = check_rows(y, ldy, channels, "y")) != GDN_OK) return st;
+    }
+    return launch_conv_state(x, ldx, dtype, T, channels, w, bias, conv_k, cu_seqlens, num_seqs, state, state_out, y,
+                             ldy, (cudaStream_t)stream);
+}
+
+size_t gdn_ssm_conv_bwd_workspace_size(int32_t T, int32_t channels, int32_t conv_k) {
+    if (T < 0 || channels < 1 || channels % 8 != 0 || conv_k < 1 || conv_k > 4) return 0;
+    return (sizeof(float) * (size_t)channels * (conv_k + 1) * bwd_strips(T, channels) + 255) & ~size_t(255);
+}
+
+gdn_status gdn_ssm_conv_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, gdn_dtype dtype, int32_t T,
+                            int32_t channels, const void* w, const void* bias, int32_t conv_k,
+                            const int32_t* cu_seqlens, int32_t num_seqs, const void* state, const float* dstate_out,
+                            void* dx, int64_t lddx, float* dw, float* dbias, float* dstate, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    gdn_status st = check_conv(dtype, T, channels, w, conv_k);
+    if (st != GDN_OK) return st;
+    if (num_seqs < 1 || !cu_seqlens) return fail(GDN_ERR_INVALID_ARG, "num_seqs=%d or cu_seqlens is NULL", num_seqs);
+    if (!al16(state) || !al16(dstate_out) || !al16(dstate))
+        return fail(GDN_ERR_INVALID_ARG, "state, dstate_out and dstate must be 16-byte aligned");
+    if (!dw) return fail(GDN_ERR_INVALID_ARG, "dw is NULL");
+    if (T > 0) {
+        if ((st = check_rows(dy, lddy, channels, "dy")) != GDN_OK) return st;
+        if ((st = check_rows(x, ldx, channels, "x")) != GDN_OK) return st;
+        if ((st = check_rows(dx, lddx, channels, "dx")) != GDN_OK) return st;
+    }
+    const size_t need = gdn_ssm_conv_bwd_workspace_size(T, channels, conv_k);
+    if (!workspace || workspace_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes < required %zu", workspace ? workspace_bytes : 0, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    ConvBwdParams p{dy, lddy, x, ldx, w, bias, T, channels, cu_seqlens, num_seqs, state, dstate_out, dx, lddx, dstate,
+                    static_cast<float*>(workspace), 0};
+    cudaStream_t s = (cudaStream_t)stream;
+    st = dtype == GDN_BF16 ? run_bwd<__nv_bfloat16>(p, conv_k, s) : run_bwd<float>(p, conv_k, s);
+    if (st != GDN_OK) return st;
+    const int64_t nw = (int64_t)channels * conv_k, all = nw + channels;
+    return launch_column_sum(p.part, bwd_strips(T, channels), all, nw, all, dw, dbias, nullptr, s);
+}
+
+gdn_status gdn_ssm_conv_step(const void* x, int64_t ldx, gdn_dtype dtype, int32_t batch, int32_t channels,
+                             const void* w, const void* bias, int32_t conv_k, void* states, int32_t num_slots,
+                             const int32_t* src, const int32_t* dst, void* y, int64_t ldy, void* stream) {
+    gdn_status st = check_conv(dtype, batch, channels, w, conv_k);
+    if (st != GDN_OK) return st;
+    if (batch > 65535) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "batch=%d above 65535", batch);
+    if (num_slots < 0) return fail(GDN_ERR_INVALID_ARG, "num_slots=%d", num_slots);
+    if ((!src || !dst) && num_slots < batch)
+        return fail(GDN_ERR_INVALID_ARG, "num_slots=%d < batch=%d without slot numbers", num_slots, batch);
+    if (batch == 0) return GDN_OK;
+    if ((st = check_rows(x, ldx, channels, "x")) != GDN_OK) return st;
+    if ((st = check_rows(y, ldy, channels, "y")) != GDN_OK) return st;
+    if (conv_k > 1 && (!states || !al16(states)))
+        return fail(GDN_ERR_INVALID_ARG, "states must be 16-byte aligned and not NULL");
+    cudaStream_t s = (cudaStream_t)stream;
+    return dtype == GDN_BF16
+               ? run_step<__nv_bfloat16>(x, ldx, batch, channels, w, bias, conv_k, states, num_slots, src, dst, y, ldy, s)
+               : run_step<float>(x, ldx, batch, channels, w, bias, conv_k, states, num_slots, src, dst, y, ldy, s);
+}
+
+}  // extern "C"
