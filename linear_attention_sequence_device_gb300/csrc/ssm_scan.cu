@@ -5,12 +5,19 @@
 //   delta = softplus(dt + dt_bias), a_n = 2^(delta A2_n), A2 = -exp(A_log) log2 e,
 //   h_n <- a_n h_n + (delta x) B_n,   y = (sum_n C_n h_n + D x) silu(z).
 //
-// Work split.  K lanes share a channel, each with NS states in registers; a
-// thread may hold NC channels, so that one read of B and C from shared memory
-// serves NC of them.  A block walks down a range of packed tokens in tiles of
-// TT: its threads first turn the tile's x, dt into (delta, delta x) in shared
-// memory, 16 bytes of a row at a time, then run the recurrence, leaving the
-// sums over n in place, and last apply skip and gate and store, again by rows.
+// Work split.  A lane holds up to 16 states of one channel in registers, so that
+// for N <= 16 a warp is 32 channels side by side and nothing crosses lanes: the
+// lane reads its channel's x, dt and z, forms delta, runs the recurrence and
+// stores y; the loads of the next four tokens are under way meanwhile.  Above 16
+// states K = 2 or 4 adjacent lanes share a channel and add their sums by
+// exchanges.  B and C, which all channels of a group read, go through shared
+// memory as fp32, a tile of TT tokens ahead, and come back as broadcasts.
+//
+// What bounds it: the 16 exponentials a token and channel (the special function
+// unit: 4 cycles a warp each) and as many cycles of the FMA pipe (four
+// operations a state), with about 95 issue slots against 64 + 16 cycles of
+// either.  Pairs of states go through the two-wide fp32 instructions, without
+// which the issue slots would come first.
 //
 // Parallelism over tokens.  The packed tokens are cut into S segments of equal
 // length, whatever the sequences' lengths.  A first launch runs each segment's
@@ -24,7 +31,8 @@
 namespace gdn {
 namespace {
 
-constexpr int TT = 32;     // tokens per tile
+constexpr int TT = 32;     // tokens per tile of B and C
+constexpr int UN = 4;      // tokens loaded ahead
 constexpr int NTH = 128;   // threads per block
 
 struct ScanParams {
@@ -43,101 +51,58 @@ struct ScanParams {
     float* H; float* sd;             // [S, ch, N], [S, ch]
 };
 
-// Sum over the K lanes of a channel (adjacent lanes), four tokens at a time:
-// the exchange halves the values, so that each lane ends with the tokens of its
-// own index.  K = 4: lane k holds token (k & 1) * 2 + (k >> 1).
-template <int K>
-__device__ __forceinline__ void lane_sums(float (&v)[4], int k) {
-    if (K == 1) return;
-    const bool b0 = k & 1;
-    float s0 = b0 ? v[0] : v[2], s1 = b0 ? v[1] : v[3];
-    float k0 = b0 ? v[2] : v[0], k1 = b0 ? v[3] : v[1];
-    k0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-    k1 += __shfl_xor_sync(0xffffffffu, s1, 1);
-    if (K == 2) {
-        v[0] = k0;
-        v[1] = k1;
-        return;
-    }
-    const bool b1 = k & 2;
-    const float snd = b1 ? k0 : k1, kp = b1 ? k1 : k0;
-    v[0] = kp + __shfl_xor_sync(0xffffffffu, snd, 2);
-}
-
-template <int K, int NS, int NC>
-struct Shape {
-    static constexpr int CPW = 32 / K;                 // channels side by side in a warp
-    static constexpr int CH = NTH / 32 * CPW * NC;     // channels per block
-    static constexpr int NP = K * NS;                  // padded states
-    static constexpr size_t smem = sizeof(float2) * TT * CH + sizeof(float) * 2 * TT * NP;
-};
-
-// LAST: the segment's end state only (no y, no C).
-template <typename E, int K, int NS, int NC, bool LAST>
-__global__ void __launch_bounds__(NTH) scan_kernel(const ScanParams p) {
-    using Sh = Shape<K, NS, NC>;
-    constexpr int CH = Sh::CH, NP = Sh::NP, CPW = Sh::CPW;
-    extern __shared__ float4 smem4[];
-    float2* du = reinterpret_cast<float2*>(smem4);       // [TT][CH]
-    float* Bs = reinterpret_cast<float*>(du + TT * CH);  // [TT][NP]
-    float* Cs = Bs + TT * NP;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// LAST: the segment's end state and sum of delta only (no y, no C).
+template <typename E, int K, int NS, bool LAST>
+__global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
+    constexpr int NP = K * NS, CH = NTH / K, NB = LAST ? NP : 2 * NP;  // B, or B and C, per token
+    constexpr int PER = TT * NB / NTH;                                // elements of a tile each thread stages
+    static_assert(TT * NB % NTH == 0 && TT % UN == 0, "tile shape");
+    __shared__ __align__(16) float bcs[2][TT][NB];
+    const int tid = threadIdx.x, k = tid % K, cl = tid / K;
     const int grp = blockIdx.x / p.tiles;
-    const int cbase = grp * p.per + (blockIdx.x % p.tiles) * CH;  // first channel
-    const int cend = (grp + 1) * p.per;                           // end of the group's channels
-    const int nv = min(CH, cend - cbase) >> 3;                    // vectors of eight channels
+    const int cend = (grp + 1) * p.per;
+    const int c = grp * p.per + (blockIdx.x % p.tiles) * CH + cl;
+    const bool in = c < cend;
+    const int cc = in ? c : cend - 1;  // a channel to read for lanes without one
     const int s = blockIdx.y;
     int t0 = s * p.seg;
     const int te = min(p.T, t0 + p.seg);
-    const int k = lane % K;
-    int cl[NC];  // channel within the block
-    float A2[NC][NS], h[NC][NS];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        cl[i] = (i * (NTH / 32) + warp) * CPW + lane / K;
-        const int c = cbase + cl[i];
+    F2 A2[NS / 2], h[NS / 2];
+    {
+        float* a = reinterpret_cast<float*>(A2);
+        float* hh = reinterpret_cast<float*>(h);
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
             const int st = k * NS + n;
-            A2[i][n] = c < cend && st < p.N ? -expf(__ldg(p.A_log + (int64_t)c * p.N + st)) * kLog2e : 0.f;
-            h[i][n] = 0.f;
+            a[n] = st < p.N ? -expf(__ldg(p.A_log + (int64_t)cc * p.N + st)) * kLog2e : 0.f;
+            hh[n] = 0.f;
         }
     }
+    const bool vec = p.N % 4 == 0;
     auto load_state = [&](const float* src, int64_t row) {  // src [rows, ch, N] or null
+        float* hh = reinterpret_cast<float*>(h);
+        const float* q = src + (row * p.ch + cc) * p.N + k * NS;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = cbase + cl[i];
-#pragma unroll
-            for (int n = 0; n < NS; ++n) {
-                const int st = k * NS + n;
-                h[i][n] = src && c < cend && st < p.N ? __ldg(src + (row * p.ch + c) * p.N + st) : 0.f;
-            }
-        }
+        for (int n = 0; n < NS; ++n) hh[n] = src && k * NS + n < p.N ? __ldg(q + n) : 0.f;
     };
     auto store_state = [&](float* dst, int64_t row) {
+        const float* hh = reinterpret_cast<const float*>(h);
+        float* q = dst + (row * p.ch + cc) * p.N + k * NS;
+        if (!in) return;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = cbase + cl[i];
-            if (c < cend) {
-                float* q = dst + (row * p.ch + c) * p.N + k * NS;
-                if (NS % 4 == 0 && p.N % 4 == 0) {
+        for (int n = 0; n < NS; n += 4) {
+            if (vec) {
+                if (k * NS + n < p.N) *reinterpret_cast<float4*>(q + n) = make_float4(hh[n], hh[n + 1], hh[n + 2], hh[n + 3]);
+            } else {
 #pragma unroll
-                    for (int n = 0; n < NS; n += 4)
-                        if (k * NS + n < p.N)
-                            *reinterpret_cast<float4*>(q + n) = make_float4(h[i][n], h[i][n + 1], h[i][n + 2], h[i][n + 3]);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        if (k * NS + n < p.N) q[n] = h[i][n];
-                }
+                for (int i = n; i < n + 4; ++i)
+                    if (k * NS + i < p.N) q[i] = hh[i];
             }
         }
     };
     // the sequence at the first token, and the state there
-    int next;  // first token of the next sequence
-    float dsum[NC];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) dsum[i] = 0.f;
+    int next = p.T;  // first token of the next sequence
+    float dsum = 0.f;
     if (LAST) {
         const int n = seq_of(p.cu, p.num_seqs, te - 1);
         if (__ldg(p.cu + n + 1) <= te) return;  // nothing goes on into the next segment
@@ -146,7 +111,6 @@ __global__ void __launch_bounds__(NTH) scan_kernel(const ScanParams p) {
             t0 = min(start, te - 1);
             load_state(p.h0, n);
         }
-        next = p.T;
     } else {
         if (p.T == 0) {  // every sequence is empty
             if (p.h_final)
@@ -167,68 +131,89 @@ __global__ void __launch_bounds__(NTH) scan_kernel(const ScanParams p) {
                 }
             load_state(p.h0, n);
         } else {
-            for (int j = max(start, 0) / p.seg; j < s; ++j) {
-                const bool first = max(start, 0) / p.seg == j;
+            const int j0 = max(start, 0) / p.seg;
+            load_state(p.H, j0);
+            for (int j = j0 + 1; j < s; ++j) {
+                const int64_t row = (int64_t)j * p.ch + cc;
+                const F2 d = f2_dup(__ldg(p.sd + row));
+                const float* Hj = p.H + row * p.N + k * NS;
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const int c = cbase + cl[i];
-                    if (c < cend) {
-                        const int64_t row = (int64_t)j * p.ch + c;
-                        const float d = first ? 0.f : __ldg(p.sd + row);
-#pragma unroll
-                        for (int q = 0; q < NS; ++q) {
-                            const int st = k * NS + q;
-                            const float Hj = st < p.N ? __ldg(p.H + row * p.N + st) : 0.f;
-                            h[i][q] = first ? Hj : fmaf(exp2_fast(d * A2[i][q]), h[i][q], Hj);
-                        }
-                    }
+                for (int q = 0; q < NS / 2; ++q) {
+                    const F2 add{k * NS + 2 * q < p.N ? __ldg(Hj + 2 * q) : 0.f,
+                                 k * NS + 2 * q + 1 < p.N ? __ldg(Hj + 2 * q + 1) : 0.f};
+                    h[q] = f2_fma(f2_exp2(f2_mul(d, A2[q])), h[q], add);
                 }
             }
         }
     }
 
-    for (int tb = t0 - (LAST ? t0 % TT : 0); tb < te; tb += TT) {
-        // (delta, delta x) of the tile; rows outside [t0, te) leave the state alone
-        for (int it = tid; it < TT * nv; it += NTH) {
-            const int r = it / nv, v = it - r * nv, t = tb + r;
-            float2* out = du + r * CH + 8 * v;
-            if (t >= t0 && t < te) {
-                float xv[8], dv[8];
-                load8(static_cast<const E*>(p.x) + (int64_t)t * p.ldx + cbase + 8 * v, xv);
-                load8(static_cast<const E*>(p.dt) + (int64_t)t * p.lddt + cbase + 8 * v, dv);
+    const E* xp = static_cast<const E*>(p.x) + cc;
+    const E* dp = static_cast<const E*>(p.dt) + cc;
+    const E* zp = p.z ? static_cast<const E*>(p.z) + cc : nullptr;
+    E* yp = static_cast<E*>(p.y) + cc;
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + cc) : 0.f, Dc = p.D ? __ldg(p.D + cc) : 0.f;
+    E xr[UN], dr[UN], zr[UN];
+    auto fetch = [&](int t) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float dl = softplus_f(dv[i] + (p.dt_bias ? __ldg(p.dt_bias + cbase + 8 * v + i) : 0.f));
-                    out[i] = make_float2(dl, dl * xv[i]);
-                }
-            } else {
+        for (int u = 0; u < UN; ++u) {
+            const int64_t r = min(t + u, te - 1);
+            xr[u] = __ldg(xp + r * p.ldx);
+            dr[u] = __ldg(dp + r * p.lddt);
+            if (!LAST && zp) zr[u] = __ldg(zp + r * p.ldz);
+        }
+    };
+    E bc[PER];
+    const int64_t goff = (int64_t)grp * p.N;
+    auto fetch_bc = [&](int tb) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) out[i] = make_float2(0.f, 0.f);
-            }
+        for (int i = 0; i < PER; ++i) {
+            const int it = tid + i * NTH, r = it / NB, j = it % NB, n = j % NP;
+            const int64_t t = min(tb + r, te - 1);
+            const E* q = (j < NP ? static_cast<const E*>(p.B) + t * p.ldb : static_cast<const E*>(p.C) + t * p.ldc) + goff;
+            bc[i] = n < p.N ? __ldg(q + n) : Elem<E>::from_f(0.f);
         }
-        for (int it = tid; it < TT * NP; it += NTH) {
-            const int r = it / NP, n = it - r * NP, t = tb + r;
-            const bool in = t >= t0 && t < te && n < p.N;
-            const int64_t off = (int64_t)grp * p.N + n;
-            Bs[it] = in ? Elem<E>::load(static_cast<const E*>(p.B) + t * p.ldb + off) : 0.f;
-            if (!LAST) Cs[it] = in ? Elem<E>::load(static_cast<const E*>(p.C) + t * p.ldc + off) : 0.f;
+    };
+    auto put_bc = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int it = tid + i * NTH;
+            bcs[b][it / NB][it % NB] = Elem<E>::to_f(bc[i]);
         }
-        __syncthreads();
+    };
+    fetch(t0);
+    fetch_bc(t0);
+    put_bc(0);
+    __syncthreads();
+    int buf = 0;
+    for (int tb = t0; tb < te; tb += TT, buf ^= 1) {
+        const bool more = tb + TT < te;
+        if (more) fetch_bc(tb + TT);
         if (!LAST && p.ckpt && (tb & 63) == 0) store_state(p.ckpt, tb >> 6);
 #pragma unroll 1
-        for (int r0 = 0; r0 < TT; r0 += 4) {
-            float ys[NC][4];
-            const bool plain = LAST || next >= tb + r0 + 4 || next >= te;
+        for (int r0 = 0; r0 < TT; r0 += UN) {
+            const int tg = tb + r0;
+            if (tg >= te) break;
+            float dl[UN], u_[UN], xv[UN], zv[UN];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int r = r0 + u;
-                if (!LAST && !plain && tb + r == next && next < te) {  // a sequence ends and another starts
+            for (int u = 0; u < UN; ++u) {
+                xv[u] = Elem<E>::to_f(xr[u]);
+                const float d = softplus_f(Elem<E>::to_f(dr[u]) + bias);
+                dl[u] = tg + u < te ? d : 0.f;  // past the end: the state stays
+                u_[u] = tg + u < te ? d * xv[u] : 0.f;
+                if (!LAST && zp) zv[u] = Elem<E>::to_f(zr[u]);
+                if (LAST) dsum += dl[u];
+            }
+            if (tg + UN < te) fetch(tg + UN);
+            const bool plain = LAST || next >= tg + UN || next >= te;
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+                if (!LAST && !plain && tg + u == next && next < te) {  // a sequence ends and another starts
                     const int n = seq_of(p.cu, p.num_seqs, next);
                     int m = n - 1;  // the sequence that ended: empty ones may lie between
                     while (m >= 0 && __ldg(p.cu + m) == next) --m;
                     if (p.h_final) {
                         if (m >= 0) store_state(p.h_final, m);
-                        for (int e = max(m, 0) + 1; e < n; ++e) {
+                        for (int e = max(m, 0) + (m >= 0); e < n; ++e) {
                             load_state(p.h0, e);
                             store_state(p.h_final, e);
                         }
@@ -236,74 +221,37 @@ __global__ void __launch_bounds__(NTH) scan_kernel(const ScanParams p) {
                     load_state(p.h0, n);
                     next = __ldg(p.cu + n + 1);
                 }
-                float Bv[NS], Cv[NS];
+                const float* row = bcs[buf][r0 + u] + k * NS;
+                const F2 d = f2_dup(dl[u]), uu = f2_dup(u_[u]);
+                F2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
                 for (int n = 0; n < NS; n += 4) {
-                    const float4 b = *reinterpret_cast<const float4*>(Bs + r * NP + k * NS + n);
-                    Bv[n] = b.x; Bv[n + 1] = b.y; Bv[n + 2] = b.z; Bv[n + 3] = b.w;
+                    const float4 b = *reinterpret_cast<const float4*>(row + n);
+                    const int q = n / 2;
+                    h[q] = f2_fma(f2_exp2(f2_mul(d, A2[q])), h[q], f2_mul(uu, F2{b.x, b.y}));
+                    h[q + 1] = f2_fma(f2_exp2(f2_mul(d, A2[q + 1])), h[q + 1], f2_mul(uu, F2{b.z, b.w}));
                     if (!LAST) {
-                        const float4 c = *reinterpret_cast<const float4*>(Cs + r * NP + k * NS + n);
-                        Cv[n] = c.x; Cv[n + 1] = c.y; Cv[n + 2] = c.z; Cv[n + 3] = c.w;
+                        const float4 cv = *reinterpret_cast<const float4*>(row + NP + n);
+                        acc[0] = f2_fma(h[q], F2{cv.x, cv.y}, acc[0]);
+                        acc[1] = f2_fma(h[q + 1], F2{cv.z, cv.w}, acc[1]);
                     }
                 }
+                if (!LAST) {
+                    float o = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const float2 d = du[r * CH + cl[i]];
-                    float acc = 0.f;
-#pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        h[i][n] = fmaf(exp2_fast(d.x * A2[i][n]), h[i][n], d.y * Bv[n]);
-                        if (!LAST) acc = fmaf(h[i][n], Cv[n], acc);
-                    }
-                    if (LAST) dsum[i] += d.x;
-                    else ys[i][u] = acc;
-                }
-            }
-            if (!LAST) {
-#pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    lane_sums<K>(ys[i], k);
-                    if (K == 1) {
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) du[(r0 + u) * CH + cl[i]].x = ys[i][u];
-                    } else if (K == 2) {
-                        du[(r0 + 2 * k) * CH + cl[i]].x = ys[i][0];
-                        du[(r0 + 2 * k + 1) * CH + cl[i]].x = ys[i][1];
-                    } else {
-                        du[(r0 + (k & 1) * 2 + (k >> 1)) * CH + cl[i]].x = ys[i][0];
-                    }
+                    for (int m = 1; m < K; m <<= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
+                    o = fmaf(Dc, xv[u], o);
+                    if (zp) o *= silu_fast(zv[u]);
+                    if (in && k == 0 && tg + u < te) yp[(int64_t)(tg + u) * p.ldy] = Elem<E>::from_f(o);
                 }
             }
         }
+        if (more) put_bc(buf ^ 1);
         __syncthreads();
-        if (!LAST) {
-            for (int it = tid; it < TT * nv; it += NTH) {
-                const int r = it / nv, v = it - r * nv, t = tb + r;
-                if (t >= te) continue;
-                float o[8], f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = du[r * CH + 8 * v + i].x;
-                if (p.D) {
-                    load8(static_cast<const E*>(p.x) + (int64_t)t * p.ldx + cbase + 8 * v, f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = fmaf(__ldg(p.D + cbase + 8 * v + i), f[i], o[i]);
-                }
-                if (p.z) {
-                    load8(static_cast<const E*>(p.z) + (int64_t)t * p.ldz + cbase + 8 * v, f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] *= silu_fast(f[i]);
-                }
-                store8(static_cast<E*>(p.y) + (int64_t)t * p.ldy + cbase + 8 * v, o);
-            }
-            __syncthreads();
-        }
     }
     if (LAST) {
         store_state(p.H, s);
-        if (k == 0)
-#pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (cbase + cl[i] < cend) p.sd[(int64_t)s * p.ch + cbase + cl[i]] = dsum[i];
+        if (k == 0 && in) p.sd[(int64_t)s * p.ch + c] = dsum;
     } else if (p.h_final && next <= te) {  // the sequence ends with the segment
         const int m = seq_of(p.cu, p.num_seqs, te - 1);
         store_state(p.h_final, m);
@@ -381,11 +329,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p, floa
 
 // ---- host ----------------------------------------------------------------------
 
-int lanes_of(int N) { return N <= 4 ? 1 : (N <= 8 ? 2 : 4); }
-int channels_per_block(int N) {
-    const int K = lanes_of(N), NC = 1;
-    return NTH / 32 * (32 / K) * NC;
-}
+int lanes_of(int N) { return N <= 4 ? 1 : (N <= 8 ? 2 : 4); }  // of the step: four states each
+int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH / 4); }
 
 // Segments of a call: enough blocks for four resident ones an SM, of 64 tokens
 // or more; multiples of 64 so that the backward's state checkpoints fall on
@@ -404,28 +349,27 @@ void segments(int T, int ch, int N, int groups, int& seg, int& S) {
     if (S < 1) S = 1;
 }
 
-template <typename E, int K, int NS, int NC>
+template <typename E, int K, int NS>
 gdn_status run_scan(ScanParams p, int groups, cudaStream_t s) {
-    using Sh = Shape<K, NS, NC>;
-    p.tiles = (p.per + Sh::CH - 1) / Sh::CH;
+    p.tiles = (p.per + NTH / K - 1) / (NTH / K);
     dim3 grid(groups * p.tiles, p.S);
     if (p.S > 1) {
         dim3 g1(grid.x, p.S - 1);
-        scan_kernel<E, K, NS, NC, true><<<g1, NTH, Sh::smem, s>>>(p);
+        scan_kernel<E, K, NS, true><<<g1, NTH, 0, s>>>(p);
         const gdn_status st = check_launch("scan_kernel (end states)");
         if (st != GDN_OK) return st;
     }
-    scan_kernel<E, K, NS, NC, false><<<grid, NTH, Sh::smem, s>>>(p);
+    scan_kernel<E, K, NS, false><<<grid, NTH, 0, s>>>(p);
     return check_launch("scan_kernel");
 }
 
 template <typename E>
 gdn_status dispatch_scan(const ScanParams& p, int groups, cudaStream_t s) {
-    if (p.N <= 4) return run_scan<E, 1, 4, 1>(p, groups, s);
-    if (p.N <= 8) return run_scan<E, 2, 4, 1>(p, groups, s);
-    if (p.N <= 16) return run_scan<E, 4, 4, 1>(p, groups, s);
-    if (p.N <= 32) return run_scan<E, 4, 8, 1>(p, groups, s);
-    return run_scan<E, 4, 16, 1>(p, groups, s);
+    if (p.N <= 4) return run_scan<E, 1, 4>(p, groups, s);
+    if (p.N <= 8) return run_scan<E, 1, 8>(p, groups, s);
+    if (p.N <= 16) return run_scan<E, 1, 16>(p, groups, s);
+    if (p.N <= 32) return run_scan<E, 2, 16>(p, groups, s);
+    return run_scan<E, 4, 16>(p, groups, s);
 }
 
 template <typename E>
