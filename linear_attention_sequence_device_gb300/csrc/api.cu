@@ -30,7 +30,7 @@ gdn_status check_launch(const char* what) {
 
 // cudaFuncAttributeMaxDynamicSharedMemorySize, set once per (device, kernel).
 gdn_status set_smem_attr(const void* func, size_t bytes) {
-    constexpr int kMaxDev = 64, kMaxFn = 32;
+    constexpr int kMaxDev = 64, kMaxFn = 64;
     static thread_local const void* done[kMaxDev][kMaxFn] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev)

@@ -52,6 +52,19 @@ __device__ __forceinline__ void load8_rw(const float* p, float (&f)[8]) {
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
+// one element by a load that stays where it is written: the compiler would move
+// an ordinary load down to its first use, a whole tile later
+__device__ __forceinline__ __nv_bfloat16 load_now(const __nv_bfloat16* p) {
+    unsigned short r;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
+    return __ushort_as_bfloat16(r);
+}
+__device__ __forceinline__ float load_now(const float* p) {
+    float r;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r) : "l"(p));
+    return r;
+}
+
 // 2^v by the special function unit (relative error 2^-22; -inf gives 0)
 __device__ __forceinline__ float exp2_fast(float v) {
     float r;
@@ -59,20 +72,20 @@ __device__ __forceinline__ float exp2_fast(float v) {
     return r;
 }
 // 1 / (1 + e^-v): an infinite e^-v gives 0, a NaN goes through
-__device__ __forceinline__ float sigmoid_fast(float v) { return __fdividef(1.f, 1.f + exp2_fast(-kLog2e * v)); }
+__device__ __forceinline__ float rcp_fast(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float sigmoid_fast(float v) { return rcp_fast(1.f + exp2_fast(-kLog2e * v)); }
 __device__ __forceinline__ float silu_fast(float v) { return v * sigmoid_fast(v); }
 // log(1 + e^v) = max(v, 0) + log(1 + t), t = e^-|v| in (0, 1]: the first term is
 // all of it above 20, the gates' threshold.  log(1 + t) is t times a polynomial
 // of degree 9 interpolated at the Chebyshev points of [0, 1] (relative error
 // 5e-9, with fp32 coefficients and steps 1.6e-7), so that delta keeps its digits
-// where it is small, which the hardware logarithm of 1 + t would not; t's
-// argument keeps its rounding error in a second term.
+// where it is small, which the hardware logarithm of 1 + t would not.
 __device__ __forceinline__ float softplus_f(float v) {
-    constexpr float kLog2eLo = 1.925963033500011e-8f;  // log2(e) = kLog2e + this, kLog2e as rounded to fp32
-    const float w = -fminf(fabsf(v), 150.f), hi = w * kLog2e;
-    const float lo = fmaf(w, kLog2eLo, fmaf(w, kLog2e, -hi));
-    float t = exp2_fast(hi);
-    t = fmaf(t, lo * 0.6931471805599453f, t);
+    const float t = exp2_fast(-fabsf(v) * kLog2e);
     float q = -0.0031760570127516985f;
     q = fmaf(q, t, 0.019542526453733444f);
     q = fmaf(q, t, -0.056373611092567444f);
@@ -83,8 +96,16 @@ __device__ __forceinline__ float softplus_f(float v) {
     q = fmaf(q, t, 0.33329710364341736f);
     q = fmaf(q, t, -0.49999892711639404f);
     q = fmaf(q, t, 1.f);
-    return fmaf(t, q, fmaf(0.5f, fabsf(v), 0.5f * v));  // a NaN goes through the last term
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(v), "f"(0.f));
+    return fmaf(t, q, m);
 }
+// The decay 2^(d A2) of a step.  The special function unit's results for
+// arguments in [-1, -1e-3] lie 2e-8 (a third of half a step) below the value on
+// average, which a state multiplied a thousand times adds up; the constant in
+// the argument, which costs nothing inside the product, takes that back.
+constexpr float kDecayBias = 2.6e-8f;
+__device__ __forceinline__ float decay_fast(float d, float A2) { return exp2_fast(fmaf(d, A2, kDecayBias)); }
 
 // two fp32 operations in one instruction (the pipe's rate is the same, the issue slots are half)
 struct F2 {
@@ -112,6 +133,7 @@ __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
 }
 __device__ __forceinline__ F2 f2_exp2(F2 a) { return F2{exp2_fast(a.x), exp2_fast(a.y)}; }
 __device__ __forceinline__ F2 f2_dup(float v) { return F2{v, v}; }
+__device__ __forceinline__ F2 f2_decay(F2 d, F2 A2) { return f2_exp2(f2_fma(d, A2, f2_dup(kDecayBias))); }
 
 // the sequence that holds packed token t: the last n with cu[n] <= t, which is
 // not empty; clamped to a sequence for a malformed cu

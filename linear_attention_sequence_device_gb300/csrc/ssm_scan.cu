@@ -8,10 +8,11 @@
 // Work split.  A lane holds up to 16 states of one channel in registers, so that
 // for N <= 16 a warp is 32 channels side by side and nothing crosses lanes: the
 // lane reads its channel's x, dt and z, forms delta, runs the recurrence and
-// stores y; the loads of the next four tokens are under way meanwhile.  Above 16
-// states K = 2 or 4 adjacent lanes share a channel and add their sums by
-// exchanges.  B and C, which all channels of a group read, go through shared
-// memory as fp32, a tile of TT tokens ahead, and come back as broadcasts.
+// stores y.  Above 16 states K = 2 or 4 adjacent lanes share a channel and add
+// their sums by exchanges.  x, dt and z come by 16-byte asynchronous copies into
+// a ring of three tiles of TT tokens in shared memory, so that two tiles are
+// under way without holding registers; B and C, which all channels of a group
+// read, are laid beside them as fp32 and come back as broadcasts.
 //
 // What bounds it: the 16 exponentials a token and channel (the special function
 // unit: 4 cycles a warp each) and as many cycles of the FMA pipe (four
@@ -26,13 +27,24 @@
 // the sum of delta; from the first token of a segment that continues a
 // sequence, the state is the fold  h <- 2^(A2 sum delta_j) h + H_j  over the
 // segments before it, which each block does for its own channels.
+#include "chunk_common.cuh"
 #include "ssm_common.cuh"
 
 namespace gdn {
+
+gdn_status set_smem_attr(const void* func, size_t bytes);
+
 namespace {
 
-constexpr int TT = 32;     // tokens per tile of B and C
-constexpr int UN = 4;      // tokens loaded ahead
+constexpr int TT = 16;     // tokens per tile
+constexpr int UN = 4;      // tokens handled together
+#ifndef SCAN_OCC
+#define SCAN_OCC 4
+#endif
+#ifndef SCAN_W
+#define SCAN_W 4
+#endif
+constexpr int NST = 3;     // tiles of x, dt and z in flight or in use
 constexpr int NTH = 128;   // threads per block
 
 struct ScanParams {
@@ -53,11 +65,11 @@ struct ScanParams {
 
 // LAST: the segment's end state and sum of delta only (no y, no C).
 template <typename E, int K, int NS, bool LAST>
-__global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p) {
     constexpr int NP = K * NS, CH = NTH / K, NB = LAST ? NP : 2 * NP;  // B, or B and C, per token
-    constexpr int PER = TT * NB / NTH;                                // elements of a tile each thread stages
-    static_assert(TT * NB % NTH == 0 && TT % UN == 0, "tile shape");
-    __shared__ __align__(16) float bcs[2][TT][NB];
+    constexpr int PER = (TT * NB + NTH - 1) / NTH;                    // elements of a tile each thread stages
+    constexpr int NA = LAST ? 2 : 3;                                  // arrays in the ring
+    extern __shared__ float4 smem4[];
     const int tid = threadIdx.x, k = tid % K, cl = tid / K;
     const int grp = blockIdx.x / p.tiles;
     const int cend = (grp + 1) * p.per;
@@ -101,7 +113,7 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
         }
     };
     // the sequence at the first token, and the state there
-    int next = p.T;  // first token of the next sequence
+    int next = 0x7fffffff;  // first token of the next sequence
     float dsum = 0.f;
     if (LAST) {
         const int n = seq_of(p.cu, p.num_seqs, te - 1);
@@ -141,26 +153,36 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
                 for (int q = 0; q < NS / 2; ++q) {
                     const F2 add{k * NS + 2 * q < p.N ? __ldg(Hj + 2 * q) : 0.f,
                                  k * NS + 2 * q + 1 < p.N ? __ldg(Hj + 2 * q + 1) : 0.f};
-                    h[q] = f2_fma(f2_exp2(f2_mul(d, A2[q])), h[q], add);
+                    h[q] = f2_fma(f2_exp2(f2_mul(d, A2[q])), h[q], add);  // one exponential for the whole segment
                 }
             }
         }
     }
 
-    const E* xp = static_cast<const E*>(p.x) + cc;
-    const E* dp = static_cast<const E*>(p.dt) + cc;
-    const E* zp = p.z ? static_cast<const E*>(p.z) + cc : nullptr;
     E* yp = static_cast<E*>(p.y) + cc;
+    const bool gate = !LAST && p.z;
     const float bias = p.dt_bias ? __ldg(p.dt_bias + cc) : 0.f, Dc = p.D ? __ldg(p.D + cc) : 0.f;
-    E xr[UN], dr[UN], zr[UN];
-    auto fetch = [&](int t) {
+    // the ring: [NST][x, dt, z][TT][CH]
+    E* ring = reinterpret_cast<E*>(smem4);
+    float* bcs = reinterpret_cast<float*>(ring + NST * NA * TT * CH);  // [2][TT][NB]
+    constexpr int VEC = 16 / sizeof(E), VR = CH / VEC;  // 16-byte vectors a row
+    const int c0 = grp * p.per + (blockIdx.x % p.tiles) * CH;
+    auto copy = [&](int tb, int st) {
+        if (tb < te) {
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            const int64_t r = min(t + u, te - 1);
-            xr[u] = __ldg(xp + r * p.ldx);
-            dr[u] = __ldg(dp + r * p.lddt);
-            if (!LAST && zp) zr[u] = __ldg(zp + r * p.ldz);
+            for (int it = tid; it < TT * VR; it += NTH) {
+                const int r = it / VR, v = it - r * VR;
+                const bool ok = tb + r < te && c0 + v * VEC < cend;
+                const int64_t t = ok ? tb + r : t0;
+                const int cv = ok ? c0 + v * VEC : c0;
+                E* d = ring + (st * NA * TT + r) * CH + v * VEC;
+                const int bytes = ok ? 16 : 0;
+                cp_async16(d, static_cast<const E*>(p.x) + t * p.ldx + cv, bytes);
+                cp_async16(d + TT * CH, static_cast<const E*>(p.dt) + t * p.lddt + cv, bytes);
+                if (gate) cp_async16(d + 2 * TT * CH, static_cast<const E*>(p.z) + t * p.ldz + cv, bytes);
+            }
         }
+        cp_async_commit();
     };
     E bc[PER];
     const int64_t goff = (int64_t)grp * p.N;
@@ -170,85 +192,102 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
             const int it = tid + i * NTH, r = it / NB, j = it % NB, n = j % NP;
             const int64_t t = min(tb + r, te - 1);
             const E* q = (j < NP ? static_cast<const E*>(p.B) + t * p.ldb : static_cast<const E*>(p.C) + t * p.ldc) + goff;
-            bc[i] = n < p.N ? __ldg(q + n) : Elem<E>::from_f(0.f);
+            bc[i] = it < TT * NB && n < p.N ? load_now(q + n) : Elem<E>::from_f(0.f);
         }
     };
     auto put_bc = [&](int b) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int it = tid + i * NTH;
-            bcs[b][it / NB][it % NB] = Elem<E>::to_f(bc[i]);
+            if (it < TT * NB) bcs[b * TT * NB + it] = Elem<E>::to_f(bc[i]);
         }
     };
-    fetch(t0);
+    // one token: state and y
+    auto token = [&](const float* row, float dlt, float u, float xv, float sil, E* yo) {
+        const F2 d = f2_dup(dlt), uu = f2_dup(u);
+        F2 acc[2];
+#pragma unroll
+        for (int n = 0; n < NS; n += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(row + n);
+            const int q = n / 2;
+            h[q] = f2_fma(f2_decay(d, A2[q]), h[q], f2_mul(uu, F2{b.x, b.y}));
+            h[q + 1] = f2_fma(f2_decay(d, A2[q + 1]), h[q + 1], f2_mul(uu, F2{b.z, b.w}));
+            if (!LAST) {
+                const float4 cv = *reinterpret_cast<const float4*>(row + NP + n);
+                const F2 c0{cv.x, cv.y}, c1{cv.z, cv.w};
+                acc[0] = n ? f2_fma(h[q], c0, acc[0]) : f2_mul(h[q], c0);
+                acc[1] = n ? f2_fma(h[q + 1], c1, acc[1]) : f2_mul(h[q + 1], c1);
+            }
+        }
+        if (LAST) {
+            dsum += dlt;
+        } else {
+            float o = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+#pragma unroll
+            for (int m = 1; m < K; m <<= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
+            o = fmaf(Dc, xv, o);
+            if (gate) o *= sil;
+            if (in && k == 0) *yo = Elem<E>::from_f(o);
+        }
+    };
     fetch_bc(t0);
     put_bc(0);
-    __syncthreads();
-    int buf = 0;
-    for (int tb = t0; tb < te; tb += TT, buf ^= 1) {
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) copy(t0 + i * TT, i);
+    int buf = 0, st = 0;
+    for (int tb = t0; tb < te; tb += TT, buf ^= 1, st = st == NST - 1 ? 0 : st + 1) {
+        cp_async_wait<NST - 2>();
+        __syncthreads();  // this tile's copies are in; the last tile's readers are done
+        copy(tb + (NST - 1) * TT, st == 0 ? NST - 1 : st - 1);
         const bool more = tb + TT < te;
         if (more) fetch_bc(tb + TT);
         if (!LAST && p.ckpt && (tb & 63) == 0) store_state(p.ckpt, tb >> 6);
+        const E* xs = ring + st * NA * TT * CH + cl;
 #pragma unroll 1
         for (int r0 = 0; r0 < TT; r0 += UN) {
             const int tg = tb + r0;
             if (tg >= te) break;
-            float dl[UN], u_[UN], xv[UN], zv[UN];
+            const float* row = bcs + (buf * TT + r0) * NB + k * NS;
+            const E* xg = xs + r0 * CH;
+            E* yo = yp + (int64_t)tg * p.ldy;
+            if (tg + UN <= te && next >= tg + UN) {
+                float dl[UN], sil[UN];
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                xv[u] = Elem<E>::to_f(xr[u]);
-                const float d = softplus_f(Elem<E>::to_f(dr[u]) + bias);
-                dl[u] = tg + u < te ? d : 0.f;  // past the end: the state stays
-                u_[u] = tg + u < te ? d * xv[u] : 0.f;
-                if (!LAST && zp) zv[u] = Elem<E>::to_f(zr[u]);
-                if (LAST) dsum += dl[u];
-            }
-            if (tg + UN < te) fetch(tg + UN);
-            const bool plain = LAST || next >= tg + UN || next >= te;
+                for (int u = 0; u < UN; ++u) dl[u] = softplus_f(Elem<E>::to_f(xg[(TT + u) * CH]) + bias);
 #pragma unroll
-            for (int u = 0; u < UN; ++u) {
-                if (!LAST && !plain && tg + u == next && next < te) {  // a sequence ends and another starts
-                    const int n = seq_of(p.cu, p.num_seqs, next);
-                    int m = n - 1;  // the sequence that ended: empty ones may lie between
-                    while (m >= 0 && __ldg(p.cu + m) == next) --m;
-                    if (p.h_final) {
-                        if (m >= 0) store_state(p.h_final, m);
-                        for (int e = max(m, 0) + (m >= 0); e < n; ++e) {
-                            load_state(p.h0, e);
-                            store_state(p.h_final, e);
+                for (int u = 0; u < UN; ++u) sil[u] = gate ? silu_fast(Elem<E>::to_f(xg[(2 * TT + u) * CH])) : 1.f;
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    const float xv = Elem<E>::to_f(xg[u * CH]);
+                    token(row + u * NB, dl[u], dl[u] * xv, xv, sil[u], yo + u * p.ldy);
+                }
+            } else {  // a sequence's end or the segment's is near: one by one
+#pragma unroll 1
+                for (int u = 0; u < UN && tg + u < te; ++u) {
+                    if (!LAST && tg + u == next) {
+                        const int n = seq_of(p.cu, p.num_seqs, next);
+                        int m = n - 1;  // the sequence that ended: empty ones may lie between
+                        while (m >= 0 && __ldg(p.cu + m) == next) --m;
+                        if (p.h_final) {
+                            if (m >= 0) store_state(p.h_final, m);
+                            for (int e = m + 1; e < n; ++e) {
+                                load_state(p.h0, e);
+                                store_state(p.h_final, e);
+                            }
                         }
+                        load_state(p.h0, n);
+                        next = __ldg(p.cu + n + 1);
                     }
-                    load_state(p.h0, n);
-                    next = __ldg(p.cu + n + 1);
-                }
-                const float* row = bcs[buf][r0 + u] + k * NS;
-                const F2 d = f2_dup(dl[u]), uu = f2_dup(u_[u]);
-                F2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-                for (int n = 0; n < NS; n += 4) {
-                    const float4 b = *reinterpret_cast<const float4*>(row + n);
-                    const int q = n / 2;
-                    h[q] = f2_fma(f2_exp2(f2_mul(d, A2[q])), h[q], f2_mul(uu, F2{b.x, b.y}));
-                    h[q + 1] = f2_fma(f2_exp2(f2_mul(d, A2[q + 1])), h[q + 1], f2_mul(uu, F2{b.z, b.w}));
-                    if (!LAST) {
-                        const float4 cv = *reinterpret_cast<const float4*>(row + NP + n);
-                        acc[0] = f2_fma(h[q], F2{cv.x, cv.y}, acc[0]);
-                        acc[1] = f2_fma(h[q + 1], F2{cv.z, cv.w}, acc[1]);
-                    }
-                }
-                if (!LAST) {
-                    float o = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-#pragma unroll
-                    for (int m = 1; m < K; m <<= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
-                    o = fmaf(Dc, xv[u], o);
-                    if (zp) o *= silu_fast(zv[u]);
-                    if (in && k == 0 && tg + u < te) yp[(int64_t)(tg + u) * p.ldy] = Elem<E>::from_f(o);
+                    const float xv = Elem<E>::to_f(xg[u * CH]);
+                    const float d = softplus_f(Elem<E>::to_f(xg[(TT + u) * CH]) + bias);
+                    token(row + u * NB, d, d * xv, xv, gate ? silu_fast(Elem<E>::to_f(xg[(2 * TT + u) * CH])) : 1.f,
+                          yo + u * p.ldy);
                 }
             }
         }
         if (more) put_bc(buf ^ 1);
-        __syncthreads();
     }
+    cp_async_wait<0>();
     if (LAST) {
         store_state(p.H, s);
         if (k == 0 && in) p.sd[(int64_t)s * p.ch + c] = dsum;
@@ -307,7 +346,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p, floa
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 if (n0 + n < p.N) {
-                    h[n] = fmaf(exp2_fast(-expf(a[n]) * kLog2e * dl), h[n], u * Elem<E>::load(B + n0 + n));
+                    h[n] = fmaf(decay_fast(dl, -expf(a[n]) * kLog2e), h[n], u * Elem<E>::load(B + n0 + n));
                     acc = fmaf(h[n], Elem<E>::load(C + n0 + n), acc);
                 }
             }
@@ -338,7 +377,7 @@ int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH 
 void segments(int T, int ch, int N, int groups, int& seg, int& S) {
     const int per = ch / groups, cb = channels_per_block(N);
     const int64_t blocks = (int64_t)groups * ((per + cb - 1) / cb);
-    int64_t want = (int64_t)device_sm_count() * 4 / blocks;
+    int64_t want = (int64_t)device_sm_count() * SCAN_W / blocks;
     if (want < 1) want = 1;
     const int64_t most = (T + 63) / 64;
     if (want > most) want = most;
@@ -349,17 +388,29 @@ void segments(int T, int ch, int N, int groups, int& seg, int& S) {
     if (S < 1) S = 1;
 }
 
+constexpr size_t kSmemPlain = 48 << 10;  // dynamic shared memory that needs no attribute
+
+template <typename E, int K, int NS, bool LAST>
+constexpr size_t scan_smem() {
+    return sizeof(E) * NST * (LAST ? 2 : 3) * TT * (NTH / K) + sizeof(float) * 2 * TT * K * NS * (LAST ? 1 : 2);
+}
+
 template <typename E, int K, int NS>
 gdn_status run_scan(ScanParams p, int groups, cudaStream_t s) {
     p.tiles = (p.per + NTH / K - 1) / (NTH / K);
     dim3 grid(groups * p.tiles, p.S);
+    gdn_status st;
     if (p.S > 1) {
+        constexpr size_t smem = scan_smem<E, K, NS, true>();
+        if (smem > kSmemPlain && (st = set_smem_attr((const void*)scan_kernel<E, K, NS, true>, smem)) != GDN_OK)
+            return st;
         dim3 g1(grid.x, p.S - 1);
-        scan_kernel<E, K, NS, true><<<g1, NTH, 0, s>>>(p);
-        const gdn_status st = check_launch("scan_kernel (end states)");
-        if (st != GDN_OK) return st;
+        scan_kernel<E, K, NS, true><<<g1, NTH, smem, s>>>(p);
+        if ((st = check_launch("scan_kernel (end states)")) != GDN_OK) return st;
     }
-    scan_kernel<E, K, NS, false><<<grid, NTH, 0, s>>>(p);
+    constexpr size_t smem = scan_smem<E, K, NS, false>();
+    if (smem > kSmemPlain && (st = set_smem_attr((const void*)scan_kernel<E, K, NS, false>, smem)) != GDN_OK) return st;
+    scan_kernel<E, K, NS, false><<<grid, NTH, smem, s>>>(p);
     return check_launch("scan_kernel");
 }
 

@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(BShape<K>::NT) scan_bwd_kernel(const ScanBwdPa
                 const float4 cv4 = *reinterpret_cast<const float4*>(Cs + r * NP + k * NS);
                 const float cc[4] = {cv4.x, cv4.y, cv4.z, cv4.w};
 #pragma unroll
-                for (int n = 0; n < NS; ++n) dh[n] = fmaf(g, cc[n], dh[n]) * exp2_fast(d * A2[n]);
+                for (int n = 0; n < NS; ++n) dh[n] = fmaf(g, cc[n], dh[n]) * decay_fast(d, A2[n]);
                 dsum += d;
             }
             __syncthreads();
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(BShape<K>::NT) scan_bwd_kernel(const ScanBwdPa
                 const float4 b4 = *reinterpret_cast<const float4*>(Bs + r * NP + k * NS);
                 const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-                for (int n = 0; n < NS; ++n) h[n] = fmaf(exp2_fast(d * A2[n]), h[n], u * bb[n]);
+                for (int n = 0; n < NS; ++n) h[n] = fmaf(decay_fast(d, A2[n]), h[n], u * bb[n]);
             }
         }
         // the pieces, last to first
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(BShape<K>::NT) scan_bwd_kernel(const ScanBwdPa
                     float acc = 0.f;
 #pragma unroll
                     for (int n = 0; n < NS; ++n) {
-                        a[i][n] = exp2_fast(d * A2[n]);
+                        a[i][n] = decay_fast(d, A2[n]);
                         hb[i][n] = h[n];
                         h[n] = fmaf(a[i][n], h[n], u * bb[n]);
                         acc = fmaf(h[n], cc[n], acc);
