@@ -28,7 +28,7 @@
 // sequence, the state is the fold  h <- 2^(A2 sum delta_j) h + H_j  over the
 // segments before it, which each block does for its own channels.
 #include "chunk_common.cuh"
-#include "ssm_common.cuh"
+#include "ssm_scan.cuh"
 
 namespace gdn {
 
@@ -38,37 +38,16 @@ namespace {
 
 constexpr int TT = 16;     // tokens per tile
 constexpr int UN = 4;      // tokens handled together
-#ifndef SCAN_OCC
-#define SCAN_OCC 4
-#endif
-#ifndef SCAN_W
-#define SCAN_W 4
-#endif
 constexpr int NST = 3;     // tiles of x, dt and z in flight or in use
 constexpr int NTH = 128;   // threads per block
 
-struct ScanParams {
-    const void* x; int64_t ldx;
-    const void* dt; int64_t lddt;
-    const void* z; int64_t ldz;
-    const void* B; int64_t ldb;
-    const void* C; int64_t ldc;
-    const float* A_log; const float* D; const float* dt_bias; const float* h0;
-    const int32_t* cu;
-    int num_seqs, T, ch, N, per;     // per = channels per group
-    int tiles;                       // channel tiles per group
-    void* y; int64_t ldy;
-    float* h_final; float* ckpt;
-    int seg, S;                      // tokens per segment, segments
-    float* H; float* sd;             // [S, ch, N], [S, ch]
-};
-
-// LAST: the segment's end state and sum of delta only (no y, no C).
-template <typename E, int K, int NS, bool LAST>
-__global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p) {
+template <typename E, int K, int NS, int MODE>
+__global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
+    constexpr bool LAST = MODE != SCAN_FULL;  // a state and the sum of delta only: no y, no C
+    constexpr bool REV = MODE == SCAN_START_GRAD;
     constexpr int NP = K * NS, CH = NTH / K, NB = LAST ? NP : 2 * NP;  // B, or B and C, per token
     constexpr int PER = (TT * NB + NTH - 1) / NTH;                    // elements of a tile each thread stages
-    constexpr int NA = LAST ? 2 : 3;                                  // arrays in the ring
+    constexpr int NA = MODE == SCAN_END ? 2 : 3;                      // arrays in the ring
     extern __shared__ float4 smem4[];
     const int tid = threadIdx.x, k = tid % K, cl = tid / K;
     const int grp = blockIdx.x / p.tiles;
@@ -76,9 +55,8 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
     const int c = grp * p.per + (blockIdx.x % p.tiles) * CH + cl;
     const bool in = c < cend;
     const int cc = in ? c : cend - 1;  // a channel to read for lanes without one
-    const int s = blockIdx.y;
-    int t0 = s * p.seg;
-    const int te = min(p.T, t0 + p.seg);
+    const int s = REV ? blockIdx.y + 1 : blockIdx.y;
+    int t0 = s * p.seg, te = min(p.T, t0 + p.seg);
     F2 A2[NS / 2], h[NS / 2];
     {
         float* a = reinterpret_cast<float*>(A2);
@@ -115,7 +93,15 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
     // the sequence at the first token, and the state there
     int next = 0x7fffffff;  // first token of the next sequence
     float dsum = 0.f;
-    if (LAST) {
+    if (REV) {
+        const int n = seq_of(p.cu, p.num_seqs, t0);
+        if (__ldg(p.cu + n) >= t0) return;  // nothing came in
+        const int end = __ldg(p.cu + n + 1);
+        if (end <= te) {
+            te = max(end, t0 + 1);
+            load_state(p.h0, n);
+        }
+    } else if (LAST) {
         const int n = seq_of(p.cu, p.num_seqs, te - 1);
         if (__ldg(p.cu + n + 1) <= te) return;  // nothing goes on into the next segment
         const int start = __ldg(p.cu + n);
@@ -160,20 +146,23 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
     }
 
     E* yp = static_cast<E*>(p.y) + cc;
-    const bool gate = !LAST && p.z;
+    const bool gate = MODE != SCAN_END && p.z;
     const float bias = p.dt_bias ? __ldg(p.dt_bias + cc) : 0.f, Dc = p.D ? __ldg(p.D + cc) : 0.f;
     // the ring: [NST][x, dt, z][TT][CH]
     E* ring = reinterpret_cast<E*>(smem4);
     float* bcs = reinterpret_cast<float*>(ring + NST * NA * TT * CH);  // [2][TT][NB]
     constexpr int VEC = 16 / sizeof(E), VR = CH / VEC;  // 16-byte vectors a row
     const int c0 = grp * p.per + (blockIdx.x % p.tiles) * CH;
-    auto copy = [&](int tb, int st) {
-        if (tb < te) {
+    // row j of the walk is token t0 + j, or te - 1 - j backwards
+    const int len = te - t0;
+    auto tok = [&](int j) { return (int64_t)(REV ? te - 1 - j : t0 + j); };
+    auto copy = [&](int jb, int st) {
+        if (jb < len) {
 #pragma unroll
             for (int it = tid; it < TT * VR; it += NTH) {
                 const int r = it / VR, v = it - r * VR;
-                const bool ok = tb + r < te && c0 + v * VEC < cend;
-                const int64_t t = ok ? tb + r : t0;
+                const bool ok = jb + r < len && c0 + v * VEC < cend;
+                const int64_t t = ok ? tok(jb + r) : t0;
                 const int cv = ok ? c0 + v * VEC : c0;
                 E* d = ring + (st * NA * TT + r) * CH + v * VEC;
                 const int bytes = ok ? 16 : 0;
@@ -186,11 +175,11 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
     };
     E bc[PER];
     const int64_t goff = (int64_t)grp * p.N;
-    auto fetch_bc = [&](int tb) {
+    auto fetch_bc = [&](int jb) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int it = tid + i * NTH, r = it / NB, j = it % NB, n = j % NP;
-            const int64_t t = min(tb + r, te - 1);
+            const int64_t t = tok(min(jb + r, len - 1));
             const E* q = (j < NP ? static_cast<const E*>(p.B) + t * p.ldb : static_cast<const E*>(p.C) + t * p.ldc) + goff;
             bc[i] = it < TT * NB && n < p.N ? load_now(q + n) : Elem<E>::from_f(0.f);
         }
@@ -210,8 +199,13 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
         for (int n = 0; n < NS; n += 4) {
             const float4 b = *reinterpret_cast<const float4*>(row + n);
             const int q = n / 2;
-            h[q] = f2_fma(f2_decay(d, A2[q]), h[q], f2_mul(uu, F2{b.x, b.y}));
-            h[q + 1] = f2_fma(f2_decay(d, A2[q + 1]), h[q + 1], f2_mul(uu, F2{b.z, b.w}));
+            if (REV) {
+                h[q] = f2_mul(f2_decay(d, A2[q]), f2_fma(uu, F2{b.x, b.y}, h[q]));
+                h[q + 1] = f2_mul(f2_decay(d, A2[q + 1]), f2_fma(uu, F2{b.z, b.w}, h[q + 1]));
+            } else {
+                h[q] = f2_fma(f2_decay(d, A2[q]), h[q], f2_mul(uu, F2{b.x, b.y}));
+                h[q + 1] = f2_fma(f2_decay(d, A2[q + 1]), h[q + 1], f2_mul(uu, F2{b.z, b.w}));
+            }
             if (!LAST) {
                 const float4 cv = *reinterpret_cast<const float4*>(row + NP + n);
                 const F2 c0{cv.x, cv.y}, c1{cv.z, cv.w};
@@ -230,27 +224,27 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
             if (in && k == 0) *yo = Elem<E>::from_f(o);
         }
     };
-    fetch_bc(t0);
+    fetch_bc(0);
     put_bc(0);
 #pragma unroll
-    for (int i = 0; i < NST - 1; ++i) copy(t0 + i * TT, i);
+    for (int i = 0; i < NST - 1; ++i) copy(i * TT, i);
     int buf = 0, st = 0;
-    for (int tb = t0; tb < te; tb += TT, buf ^= 1, st = st == NST - 1 ? 0 : st + 1) {
+    for (int jb = 0; jb < len; jb += TT, buf ^= 1, st = st == NST - 1 ? 0 : st + 1) {
         cp_async_wait<NST - 2>();
         __syncthreads();  // this tile's copies are in; the last tile's readers are done
-        copy(tb + (NST - 1) * TT, st == 0 ? NST - 1 : st - 1);
-        const bool more = tb + TT < te;
-        if (more) fetch_bc(tb + TT);
-        if (!LAST && p.ckpt && (tb & 63) == 0) store_state(p.ckpt, tb >> 6);
+        copy(jb + (NST - 1) * TT, st == 0 ? NST - 1 : st - 1);
+        const bool more = jb + TT < len;
+        if (more) fetch_bc(jb + TT);
+        if (!LAST && p.ckpt) store_state(p.ckpt, (t0 + jb) / kCkpt);
         const E* xs = ring + st * NA * TT * CH + cl;
 #pragma unroll 1
         for (int r0 = 0; r0 < TT; r0 += UN) {
-            const int tg = tb + r0;
-            if (tg >= te) break;
+            const int jg = jb + r0, tg = t0 + jg;  // tg: the first of the group's tokens (forwards)
+            if (jg >= len) break;
             const float* row = bcs + (buf * TT + r0) * NB + k * NS;
             const E* xg = xs + r0 * CH;
             E* yo = yp + (int64_t)tg * p.ldy;
-            if (tg + UN <= te && next >= tg + UN) {
+            if (jg + UN <= len && next >= tg + UN) {
                 float dl[UN], sil[UN];
 #pragma unroll
                 for (int u = 0; u < UN; ++u) dl[u] = softplus_f(Elem<E>::to_f(xg[(TT + u) * CH]) + bias);
@@ -259,11 +253,11 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
 #pragma unroll
                 for (int u = 0; u < UN; ++u) {
                     const float xv = Elem<E>::to_f(xg[u * CH]);
-                    token(row + u * NB, dl[u], dl[u] * xv, xv, sil[u], yo + u * p.ldy);
+                    token(row + u * NB, dl[u], (REV ? sil[u] : dl[u]) * xv, xv, sil[u], yo + u * p.ldy);
                 }
             } else {  // a sequence's end or the segment's is near: one by one
 #pragma unroll 1
-                for (int u = 0; u < UN && tg + u < te; ++u) {
+                for (int u = 0; u < UN && jg + u < len; ++u) {
                     if (!LAST && tg + u == next) {
                         const int n = seq_of(p.cu, p.num_seqs, next);
                         int m = n - 1;  // the sequence that ended: empty ones may lie between
@@ -280,8 +274,8 @@ __global__ void __launch_bounds__(NTH, SCAN_OCC) scan_kernel(const ScanParams p)
                     }
                     const float xv = Elem<E>::to_f(xg[u * CH]);
                     const float d = softplus_f(Elem<E>::to_f(xg[(TT + u) * CH]) + bias);
-                    token(row + u * NB, d, d * xv, xv, gate ? silu_fast(Elem<E>::to_f(xg[(2 * TT + u) * CH])) : 1.f,
-                          yo + u * p.ldy);
+                    const float sl = gate ? silu_fast(Elem<E>::to_f(xg[(2 * TT + u) * CH])) : 1.f;
+                    token(row + u * NB, d, (REV ? sl : d) * xv, xv, sl, yo + u * p.ldy);
                 }
             }
         }
@@ -372,12 +366,11 @@ int lanes_of(int N) { return N <= 4 ? 1 : (N <= 8 ? 2 : 4); }  // of the step: f
 int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH / 4); }
 
 // Segments of a call: enough blocks for four resident ones an SM, of 64 tokens
-// or more; multiples of 64 so that the backward's state checkpoints fall on
-// segment starts.
+// or more; multiples of 64 so that the checkpoints fall on tile starts.
 void segments(int T, int ch, int N, int groups, int& seg, int& S) {
     const int per = ch / groups, cb = channels_per_block(N);
     const int64_t blocks = (int64_t)groups * ((per + cb - 1) / cb);
-    int64_t want = (int64_t)device_sm_count() * SCAN_W / blocks;
+    int64_t want = (int64_t)device_sm_count() * 4 / blocks;
     if (want < 1) want = 1;
     const int64_t most = (T + 63) / 64;
     if (want > most) want = most;
@@ -390,37 +383,42 @@ void segments(int T, int ch, int N, int groups, int& seg, int& S) {
 
 constexpr size_t kSmemPlain = 48 << 10;  // dynamic shared memory that needs no attribute
 
-template <typename E, int K, int NS, bool LAST>
+template <typename E, int K, int NS, int MODE>
 constexpr size_t scan_smem() {
-    return sizeof(E) * NST * (LAST ? 2 : 3) * TT * (NTH / K) + sizeof(float) * 2 * TT * K * NS * (LAST ? 1 : 2);
+    return sizeof(E) * NST * (MODE == SCAN_END ? 2 : 3) * TT * (NTH / K) +
+           sizeof(float) * 2 * TT * K * NS * (MODE == SCAN_FULL ? 2 : 1);
 }
 
-template <typename E, int K, int NS>
-gdn_status run_scan(ScanParams p, int groups, cudaStream_t s) {
-    p.tiles = (p.per + NTH / K - 1) / (NTH / K);
-    dim3 grid(groups * p.tiles, p.S);
-    gdn_status st;
-    if (p.S > 1) {
-        constexpr size_t smem = scan_smem<E, K, NS, true>();
-        if (smem > kSmemPlain && (st = set_smem_attr((const void*)scan_kernel<E, K, NS, true>, smem)) != GDN_OK)
-            return st;
-        dim3 g1(grid.x, p.S - 1);
-        scan_kernel<E, K, NS, true><<<g1, NTH, smem, s>>>(p);
-        if ((st = check_launch("scan_kernel (end states)")) != GDN_OK) return st;
+template <typename E, int K, int NS, int MODE>
+gdn_status run_mode(const ScanParams& p, dim3 grid, cudaStream_t s) {
+    constexpr size_t smem = scan_smem<E, K, NS, MODE>();
+    if (smem > kSmemPlain) {
+        const gdn_status st = set_smem_attr((const void*)scan_kernel<E, K, NS, MODE>, smem);
+        if (st != GDN_OK) return st;
     }
-    constexpr size_t smem = scan_smem<E, K, NS, false>();
-    if (smem > kSmemPlain && (st = set_smem_attr((const void*)scan_kernel<E, K, NS, false>, smem)) != GDN_OK) return st;
-    scan_kernel<E, K, NS, false><<<grid, NTH, smem, s>>>(p);
+    scan_kernel<E, K, NS, MODE><<<grid, NTH, smem, s>>>(p);
     return check_launch("scan_kernel");
 }
 
+template <typename E, int K, int NS>
+gdn_status run_scan(ScanParams p, int groups, bool grad, cudaStream_t s) {
+    p.tiles = (p.per + NTH / K - 1) / (NTH / K);
+    const dim3 all(groups * p.tiles, p.S), joints(groups * p.tiles, p.S - 1);
+    if (grad) return p.S > 1 ? run_mode<E, K, NS, SCAN_START_GRAD>(p, joints, s) : GDN_OK;
+    if (p.S > 1) {
+        const gdn_status st = run_mode<E, K, NS, SCAN_END>(p, joints, s);
+        if (st != GDN_OK) return st;
+    }
+    return run_mode<E, K, NS, SCAN_FULL>(p, all, s);
+}
+
 template <typename E>
-gdn_status dispatch_scan(const ScanParams& p, int groups, cudaStream_t s) {
-    if (p.N <= 4) return run_scan<E, 1, 4>(p, groups, s);
-    if (p.N <= 8) return run_scan<E, 1, 8>(p, groups, s);
-    if (p.N <= 16) return run_scan<E, 1, 16>(p, groups, s);
-    if (p.N <= 32) return run_scan<E, 2, 16>(p, groups, s);
-    return run_scan<E, 4, 16>(p, groups, s);
+gdn_status dispatch_scan(const ScanParams& p, int groups, bool grad, cudaStream_t s) {
+    if (p.N <= 4) return run_scan<E, 1, 4>(p, groups, grad, s);
+    if (p.N <= 8) return run_scan<E, 1, 8>(p, groups, grad, s);
+    if (p.N <= 16) return run_scan<E, 1, 16>(p, groups, grad, s);
+    if (p.N <= 32) return run_scan<E, 2, 16>(p, groups, grad, s);
+    return run_scan<E, 4, 16>(p, groups, grad, s);
 }
 
 template <typename E>
@@ -437,6 +435,10 @@ gdn_status run_step(const ScanParams& p, int batch, float* states, int num_slots
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
+
+gdn_status launch_scan_start_grad(const ScanParams& p, gdn_dtype dtype, int groups, cudaStream_t s) {
+    return dtype == GDN_BF16 ? dispatch_scan<__nv_bfloat16>(p, groups, true, s) : dispatch_scan<float>(p, groups, true, s);
+}
 
 gdn_status check_scan_shape(gdn_dtype dtype, int rows, int ch, int N, int groups) {
     if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dtype);
@@ -475,7 +477,7 @@ extern "C" {
 
 size_t gdn_ssm_scan_ckpt_floats(int32_t T, int32_t channels, int32_t d_state) {
     if (T < 0 || channels < 1 || d_state < 1) return 0;
-    return (size_t)((T + 63) / 64) * channels * d_state;
+    return (size_t)((T + kCkpt - 1) / kCkpt) * channels * d_state;
 }
 
 size_t gdn_ssm_scan_workspace_size(int32_t T, int32_t channels, int32_t d_state, int32_t groups) {
@@ -517,7 +519,8 @@ gdn_status gdn_ssm_scan_fwd(const void* x, int64_t ldx, const void* dt, int64_t 
     p.H = static_cast<float*>(workspace);
     p.sd = p.H + (size_t)p.S * channels * d_state;
     cudaStream_t s = (cudaStream_t)stream;
-    return dtype == GDN_BF16 ? dispatch_scan<__nv_bfloat16>(p, groups, s) : dispatch_scan<float>(p, groups, s);
+    return dtype == GDN_BF16 ? dispatch_scan<__nv_bfloat16>(p, groups, false, s)
+                             : dispatch_scan<float>(p, groups, false, s);
 }
 
 gdn_status gdn_ssm_scan_step(const void* x, int64_t ldx, const void* dt, int64_t lddt, const void* z, int64_t ldz,

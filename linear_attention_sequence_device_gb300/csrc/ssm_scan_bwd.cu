@@ -8,36 +8,46 @@
 //   dA_log_n = A_n sum_t delta m_n,   dx = du delta + D ds,   dD = sum ds x,
 //   ddt = ddelta s(dt + bias),   dz = dy (sum_n C_n h_n + D x) silu'(z).
 //
-// The states before each token come from the forward's checkpoints (every 64
-// packed tokens): a block of 64 tokens is run forward once, keeping the state
-// at every eighth token in shared memory, then its eight-token pieces are
-// taken from the last to the first: forward again with the eight states and
-// decays in registers, then backward.  A channel's states are spread over K
-// lanes with four each; the sums over a channel's lanes (y, du, ddelta) and the
-// sums over channels (dB, dC) are halving exchanges within the warp, the latter
-// go on over the block's warps through shared memory and over the blocks
-// through one partial per channel tile, added by a second kernel.  All orders
-// of summation are fixed.
+// The states before each token come from the forward's checkpoints (every 16
+// packed tokens).  A block of 16 tokens is run forward once, keeping the state
+// before every fourth token in shared memory; then its pieces of four tokens are
+// taken from the last to the first: forward again, with the decays a and the
+// products a h in registers, then backward, where m = dh a h.
+//
+// Work split.  A channel's states lie on K lanes with four each, and a lane
+// holds four channels, so a warp works on 128 / K channels and a lane on 16
+// states a token.  The sums over channels (dB, dC) are taken over the lane's own
+// four channels first, then by halving exchanges over the lanes K apart, over the
+// block's four warps through shared memory, and over the channel tiles through
+// one partial each, added by a second kernel.  The sums over a channel's states
+// (y, du, ddelta) go by halving exchanges over its K lanes, which leave each lane
+// with one of its four channels: that lane writes the channel's outputs.  All
+// orders of summation are fixed.
+//
+// x, dt, dy and z of the next block come by asynchronous copies while this one
+// is worked on; every warp stages its own channels, one channel a lane, so that
+// the warps meet only at the sums of dB and dC, once a block.
 //
 // Parallelism over tokens as in the forward: segments of equal length; a first
 // launch runs each segment's part of the sequence that came in from the segment
 // before, backwards from zero (or from dh_final where the sequence ends in it),
 // and a block of the main launch folds the segments behind its own.
-#include "ssm_common.cuh"
+//
+// What bounds it: issue slots.  Per token and 32 channels about 120 two-wide
+// operations (two slots each), 28 exponentials, 100 instructions of exchanges and
+// shared memory traffic and 70 for the element-wise parts.
+#include "chunk_common.cuh"
+#include "ssm_scan.cuh"
 
 namespace gdn {
-
-gdn_status check_scan_shape(gdn_dtype dtype, int rows, int ch, int N, int groups);
-gdn_status check_scan_row(const void* p, int64_t ld, int64_t least, const char* name);
-gdn_status check_scan_inputs(const void* x, int64_t ldx, const void* dt, int64_t lddt, const void* z, int64_t ldz,
-                             const void* B, int64_t ldb, const void* C, int64_t ldc, const float* A_log, int ch,
-                             int N, int groups);
-
 namespace {
 
-constexpr int BT = 64;   // tokens per block (the checkpoints' spacing)
-constexpr int Q = 8;     // tokens per piece
-constexpr int NS = 4;    // states per lane
+constexpr int BT = kCkpt;  // tokens per block
+constexpr int Q = 4;       // tokens per piece
+constexpr int NS = 4;      // states per lane and channel
+constexpr int NC = 4;      // channels per lane
+constexpr int NW = 4;      // warps per block
+constexpr int NT = 32 * NW;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct ScanBwdParams {
@@ -57,172 +67,145 @@ struct ScanBwdParams {
     float* par;            // [S, ch N + 2 ch]: partial dA_log, dD, ddt_bias
 };
 
-template <int K>
+template <typename E, int K>
 struct BShape {
-    static constexpr int CH = K <= 4 ? 64 : 256 / K;  // channels per block
-    static constexpr int NT = CH * K;
-    static constexpr int NW = NT / 32;
-    static constexpr int CPW = 32 / K;
-    static constexpr int NP = NS * K;
-    static constexpr int VR = CH / 8;                 // 16-byte vectors (of bf16) per row
-    // floats: delta, u, ds [BT][CH]; B, C [BT][NP]; states [BT / Q][NS][NT]; slabs [2][NW][Q][2 NP]
-    static constexpr size_t words = 3 * BT * CH + 2 * BT * NP + BT / Q * NS * NT + 2 * NW * Q * 2 * NP;
-    static constexpr size_t smem = 4 * words + 16;
-    static constexpr size_t smem_summary = 4 * (2 * BT * CH + BT * NP) + 16;
+    static constexpr int WC = NC * 32 / K;  // channels per warp
+    static constexpr int CH = NW * WC;      // channels per block
+    static constexpr int NP = NS * K;       // padded states
+    // a warp's floats: delta, u, ds, slope, q1, x [BT][WC] each; the states before each piece [BT / Q][NC][32] float4
+    static constexpr int AR = BT * WC;
+    static constexpr int WARP = 6 * AR + BT / Q * NC * 32 * 4;
+    static constexpr size_t raw_bytes = sizeof(E) * 4 * BT * CH;  // x, dt, dy, z as they come
+    // B and C of two blocks [2][BT][2 NP]; the warps' dB and dC [NW][BT][2 NP]
+    static constexpr size_t smem = 4 * (size_t)(NW * WARP + 2 * BT * 2 * NP + NW * BT * 2 * NP) + raw_bytes;
 };
 
-// Sum over a channel's K adjacent lanes of four tokens' values; lane k (its two
-// low bits) ends with token (k & 1) * 2 + (k >> 1 & 1) in v[0] (K >= 4), with
-// tokens 2 k, 2 k + 1 in v[0], v[1] (K = 2).
+// Sums over a channel's K adjacent lanes of the lane's four channels; lane k ends
+// with the sum of channel k % 4.
 template <int K>
-__device__ __forceinline__ void sum_lanes4(float (&v)[4], int k) {
-    if constexpr (K == 1) return;
-    if constexpr (K > 4) {
+__device__ __forceinline__ float sum_states(float v0, float v1, float v2, float v3, int k) {
 #pragma unroll
-        for (int m = 4; m < K; m <<= 1)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
+    for (int m = 4; m < K; m <<= 1) {
+        v0 += __shfl_xor_sync(0xffffffffu, v0, m);
+        v1 += __shfl_xor_sync(0xffffffffu, v1, m);
+        v2 += __shfl_xor_sync(0xffffffffu, v2, m);
+        v3 += __shfl_xor_sync(0xffffffffu, v3, m);
     }
-    const bool b0 = k & 1;
-    const float s0 = b0 ? v[0] : v[2], s1 = b0 ? v[1] : v[3];
-    float k0 = b0 ? v[2] : v[0], k1 = b0 ? v[3] : v[1];
-    k0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-    k1 += __shfl_xor_sync(0xffffffffu, s1, 1);
-    if (K == 2) {
-        v[0] = k0;
-        v[1] = k1;
-        return;
-    }
-    const bool b1 = k & 2;
-    const float snd = b1 ? k0 : k1, kp = b1 ? k1 : k0;
-    v[0] = kp + __shfl_xor_sync(0xffffffffu, snd, 2);
-}
-// which tokens of four the lane holds afterwards, and whether it is the one to store them
-template <int K>
-__device__ __forceinline__ void put_lanes4(float* row0, int64_t stride, const float (&v)[4], int k) {
-    if (K == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) row0[i * stride] = v[i];
-    } else if (K == 2) {
-        row0[(2 * k) * stride] = v[0];
-        row0[(2 * k + 1) * stride] = v[1];
-    } else if (k < 4) {
-        row0[((k & 1) * 2 + (k >> 1)) * stride] = v[0];
-    }
+    const bool b0 = k & 1, b1 = k & 2;
+    const float s0 = b0 ? v0 : v1, s1 = b0 ? v2 : v3;
+    float a = b0 ? v1 : v0, b = b0 ? v3 : v2;
+    a += __shfl_xor_sync(0xffffffffu, s0, 1);
+    b += __shfl_xor_sync(0xffffffffu, s1, 1);
+    const float s2 = b1 ? a : b, c = b1 ? b : a;
+    return c + __shfl_xor_sync(0xffffffffu, s2, 2);
 }
 
-// Sum of eight values (two tokens x four states) over the warp's channels
-// (lanes K apart).  Halves the values while lanes are left, so the lane ends with
-// 8 / min(8, CPW) of them, the first of index `first`; lanes whose channel bits
-// beyond those are set hold copies.
+// Sums over the warp's lanes K apart of eight values (two tokens x four states).
+// Halves the values while lanes are left: the lane ends with kLeft8 of them, the
+// first of index `first`.
 template <int K>
-__device__ __forceinline__ void sum_channels8(float (&v)[8], int lane, int& first, bool& keep) {
+constexpr int kLeft8 = K / 4;
+template <int K>
+__device__ __forceinline__ void sum_channels8(float (&v)[8], int lane, int& first) {
     first = 0;
-    keep = true;
     int cnt = 8;
 #pragma unroll
     for (int m = K; m < 32; m <<= 1) {
         const bool up = lane & m;
-        if (cnt > 1) {
-            cnt >>= 1;
+        cnt >>= 1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < cnt) {
-                    const float snd = up ? v[i] : v[i + cnt], kp = up ? v[i + cnt] : v[i];
-                    v[i] = kp + __shfl_xor_sync(0xffffffffu, snd, m);
-                }
-            if (up) first += cnt;
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-            if (up) keep = false;
-        }
+        for (int i = 0; i < 4; ++i)
+            if (i < cnt) {
+                const float snd = up ? v[i] : v[i + cnt], kp = up ? v[i + cnt] : v[i];
+                v[i] = kp + __shfl_xor_sync(0xffffffffu, snd, m);
+            }
+        if (up) first += cnt;
     }
 }
-template <int K>
-constexpr int kLeft8 = 32 / K >= 8 ? 1 : 8 * K / 32;
 
-template <typename E, int K, bool SUMMARY>
-__global__ void __launch_bounds__(BShape<K>::NT) scan_bwd_kernel(const ScanBwdParams p) {
-    using Sh = BShape<K>;
-    constexpr int CH = Sh::CH, NT = Sh::NT, NP = Sh::NP, CPW = Sh::CPW, VR = Sh::VR, NW = Sh::NW;
+__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+template <typename E, int K>
+__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) {
+    using Sh = BShape<E, K>;
+    constexpr int WC = Sh::WC, CH = Sh::CH, NP = Sh::NP, AR = Sh::AR;
+    constexpr int TPS = 32 / WC;  // tokens that a warp stages at a time, a channel a lane
+    constexpr int VEC = 16 / sizeof(E), VR = WC / VEC;
+    static_assert(K >= 4 && K <= 16, "a lane's four channels spread over four lanes at least");
     extern __shared__ float4 smem4[];
-    uint32_t* mask = reinterpret_cast<uint32_t*>(smem4);   // which of the block's tokens start a sequence
-    float* dl = reinterpret_cast<float*>(smem4 + 1);       // [BT][CH] delta, then ddelta's sum over n
-    float* ds = dl + BT * CH;                              // ds, then the sum C h
-    float* Cs = ds + BT * CH;                              // [BT][NP]
-    float* uu = Cs + BT * NP;                              // u, then du
-    float* Bs = uu + BT * CH;
-    float* hs = Bs + BT * NP;                              // [BT / Q][NS][NT]
-    float* slab = hs + BT / Q * NS * NT;                   // [2][NW][Q][2 NP]
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = lane % K;
-    const int grp = blockIdx.x / p.tiles;
-    const int cbase = grp * p.per + (blockIdx.x % p.tiles) * CH, cend = (grp + 1) * p.per;
-    const int s = SUMMARY ? blockIdx.y + 1 : blockIdx.y;
-    const int t0 = s * p.seg, te = min(p.T, t0 + p.seg);
-    const int cl = warp * CPW + lane / K, c = cbase + cl;
-    const bool cin = c < cend;
-    float A2[NS], dh[NS], h[NS], dA[NS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = lane % K, cg = lane / K;
+    float* wb = reinterpret_cast<float*>(smem4) + warp * Sh::WARP;
+    float *dl = wb, *uu = wb + AR, *dsv = wb + 2 * AR, *slope = wb + 3 * AR, *q1 = wb + 4 * AR, *xx = wb + 5 * AR;
+    float4* hs = reinterpret_cast<float4*>(wb + 6 * AR);                       // [BT / Q][NC][32]
+    float* bcs = reinterpret_cast<float*>(smem4) + NW * Sh::WARP;              // [2][BT][2 NP]
+    float* slab = bcs + 2 * BT * 2 * NP;                                       // [NW][BT][2 NP]
+    E* raw = reinterpret_cast<E*>(slab + NW * BT * 2 * NP) + warp * 4 * BT * WC;  // [x, dt, dy, z][BT][WC]
+    const int grp = blockIdx.x / p.tiles, cend = (grp + 1) * p.per;
+    const int wc0 = grp * p.per + (blockIdx.x % p.tiles) * CH + warp * WC;  // the warp's first channel
+    const int c4 = wc0 + cg * NC;                                          // the lane's first channel
+    const int s = blockIdx.y, t0 = s * p.seg, te = min(p.T, t0 + p.seg);
+
+    F2 A2[NC][2], dh[NC][2], h[NC][2], dA[NC][2];
+    auto load_state = [&](F2 (&f)[NC][2], const float* src, int64_t row) {  // src [rows, ch, N] or null
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-        const int st = k * NS + n;
-        A2[n] = cin && st < p.N ? -expf(__ldg(p.A_log + (int64_t)c * p.N + st)) * kLog2e : 0.f;
-        dh[n] = h[n] = dA[n] = 0.f;
-    }
-    auto load_state = [&](float (&f)[NS], const float* src, int64_t row) {
+        for (int i = 0; i < NC; ++i) {
+            float* q = reinterpret_cast<float*>(f[i]);
+            const bool ok = src && c4 + i < cend;
+            const float* g = src + (row * p.ch + c4 + i) * p.N + k * NS;
+            if (p.N % 4 == 0) {
+                const float4 v = ok && k * NS < p.N ? __ldg(reinterpret_cast<const float4*>(g)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+            } else {
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const int st = k * NS + n;
-            f[n] = src && cin && st < p.N ? __ldg(src + (row * p.ch + c) * p.N + st) : 0.f;
+                for (int n = 0; n < NS; ++n) q[n] = ok && k * NS + n < p.N ? __ldg(g + n) : 0.f;
+            }
         }
     };
-    auto store_state = [&](float* dst, int64_t row, const float (&f)[NS]) {
-        if (!cin) return;
+    auto store_state = [&](float* dst, int64_t row, const F2 (&f)[NC][2]) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-            if (k * NS + n < p.N) dst[(row * p.ch + c) * p.N + k * NS + n] = f[n];
+        for (int i = 0; i < NC; ++i) {
+            const float* q = reinterpret_cast<const float*>(f[i]);
+            if (c4 + i < cend)
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    if (k * NS + n < p.N) dst[(row * p.ch + c4 + i) * p.N + k * NS + n] = q[n];
+        }
     };
     auto pass_empty = [&](int m) {  // an empty sequence's final state is its initial one
         if (!p.dh0) return;
-        float f[NS];
+        F2 f[NC][2];
         load_state(f, p.dhf, m);
         store_state(p.dh0, m, f);
     };
-    // row vectors of the block: fixed columns per thread
-    const int vcol = tid % VR, vrow = tid / VR;
-    const int cv = cbase + 8 * vcol;
-    const bool vin = cv < cend;
-    float bias[8], Dv[8], aD[8], aT[8];
+    load_state(A2, p.A_log, 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = vin && p.dt_bias ? __ldg(p.dt_bias + cv + i) : 0.f;
-        Dv[i] = vin && p.D ? __ldg(p.D + cv + i) : 0.f;
-        aD[i] = aT[i] = 0.f;
-    }
-
-    int first_t = t0;  // SUMMARY: the first token to take
-    int last_t = te;   // one past the last
-    float dsum = 0.f;
-    if (SUMMARY) {
-        const int n = seq_of(p.cu, p.num_seqs, t0);
-        if (__ldg(p.cu + n) >= t0) return;  // nothing came in
-        const int end = __ldg(p.cu + n + 1);
-        if (end <= te) {
-            last_t = max(end, t0);
-            load_state(dh, p.dhf, n);
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int st = k * NS + 2 * q;
+            const bool ok = c4 + i < cend;
+            A2[i][q].x = ok && st < p.N ? -expf(A2[i][q].x) * kLog2e : 0.f;
+            A2[i][q].y = ok && st + 1 < p.N ? -expf(A2[i][q].y) * kLog2e : 0.f;
+            dh[i][q] = h[i][q] = dA[i][q] = F2{0.f, 0.f};
         }
-    } else if (p.T > 0) {
+    // the gradient of the state behind the segment's last token
+    if (p.T > 0) {
         const int n = seq_of(p.cu, p.num_seqs, te - 1);
         const int end = __ldg(p.cu + n + 1);
         if (end <= te) {
             load_state(dh, p.dhf, n);
         } else {
             const int je = (min(end, p.T) - 1) / p.seg;
-            for (int j = je; j > s; --j) {
-                const float d = j < je && cin ? __ldg(p.sd + (int64_t)j * p.ch + c) : 0.f;
-                float g[NS];
+            load_state(dh, p.G, je);
+            for (int j = je - 1; j > s; --j) {
+                F2 g[NC][2];
                 load_state(g, p.G, j);
 #pragma unroll
-                for (int q = 0; q < NS; ++q) dh[q] = j == je ? g[q] : fmaf(exp2_fast(d * A2[q]), dh[q], g[q]);
+                for (int i = 0; i < NC; ++i) {
+                    const F2 d = f2_dup(c4 + i < cend ? __ldg(p.sd + (int64_t)j * p.ch + c4 + i) : 0.f);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) dh[i][q] = f2_fma(f2_exp2(f2_mul(d, A2[i][q])), dh[i][q], g[i][q]);
+                }
             }
         }
         if (te == p.T)
@@ -231,251 +214,249 @@ __global__ void __launch_bounds__(BShape<K>::NT) scan_bwd_kernel(const ScanBwdPa
         for (int m = 0; m < p.num_seqs; ++m) pass_empty(m);
     }
 
-    const int nblk = (last_t - t0 + BT - 1) / BT;
-    int done = -1;  // token of the block whose sums wait in shared memory
-    for (int b = nblk - 1; b >= -1; --b) {
-        const int tb = t0 + b * BT;
-        // the finished block's outputs, then the next block's inputs, row by row
-        for (int r = vrow; r < BT; r += NT / VR) {
-            const int i0 = r * CH + 8 * vcol;
-            if (!SUMMARY && done >= 0 && vin && done + r < te) {
-                const int64_t t = done + r;
-                float xv[8], raw[8], gy[8], o[8], o2[8];
-                load8(static_cast<const E*>(p.x) + t * p.ldx + cv, xv);
-                load8(static_cast<const E*>(p.dt) + t * p.lddt + cv, raw);
-                load8(static_cast<const E*>(p.dy) + t * p.lddy + cv, gy);
-                float sil[8];
-                if (p.z) {
-                    float zv[8];
-                    load8(static_cast<const E*>(p.z) + t * p.ldz + cv, zv);
+    // the channel that this lane stages and the one whose outputs it writes
+    const int sch = lane % WC, och = cg * NC + (k & 3);
+    const bool writer = k < 4 && wc0 + och < cend;
+    const float sbias = p.dt_bias && wc0 + sch < cend ? __ldg(p.dt_bias + wc0 + sch) : 0.f;
+    const float Do = p.D && wc0 + och < cend ? __ldg(p.D + wc0 + och) : 0.f;
+    float aD = 0.f, aT = 0.f;
+    E* dxp = static_cast<E*>(p.dx) + wc0 + och;
+    E* dtp = static_cast<E*>(p.ddt) + wc0 + och;
+    E* dzp = static_cast<E*>(p.dz) + wc0 + och;
+
+    auto copy = [&](int tb) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float sg = sigmoid_fast(zv[i]);
-                        sil[i] = zv[i] * sg;
-                        o[i] = gy[i] * fmaf(Dv[i], xv[i], ds[i0 + i]) * sg * fmaf(zv[i], 1.f - sg, 1.f);
-                    }
-                    store8(static_cast<E*>(p.dz) + t * p.ch + cv, o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sil[i] = 1.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float v = raw[i] + bias[i], g = gy[i] * sil[i], du = uu[i0 + i];
-                    const float delta = softplus_f(v);
-                    o[i] = fmaf(du, delta, Dv[i] * g);
-                    o2[i] = fmaf(kLn2, dl[i0 + i], du * xv[i]) * (v > 20.f ? 1.f : sigmoid_fast(v));
-                    aD[i] = fmaf(g, xv[i], aD[i]);
-                    aT[i] += o2[i];
-                }
-                store8(static_cast<E*>(p.dx) + t * p.ch + cv, o);
-                store8(static_cast<E*>(p.ddt) + t * p.ch + cv, o2);
-            }
-            if (b >= 0) {
-                const int64_t t = tb + r;
-                float a[8], u[8], g[8];
-                if (vin && t >= first_t && t < last_t) {
-                    load8(static_cast<const E*>(p.dt) + t * p.lddt + cv, a);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = softplus_f(a[i] + bias[i]);
-                    load8(static_cast<const E*>(p.dy) + t * p.lddy + cv, g);
-                    if (p.z) {
-                        float zv[8];
-                        load8(static_cast<const E*>(p.z) + t * p.ldz + cv, zv);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) g[i] *= silu_fast(zv[i]);
-                    }
-                    if (!SUMMARY) {
-                        load8(static_cast<const E*>(p.x) + t * p.ldx + cv, u);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) u[i] *= a[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = u[i] = g[i] = 0.f;
-                }
-                store8(dl + i0, a);
-                store8(ds + i0, g);
-                if (!SUMMARY) store8(uu + i0, u);
-            }
+        for (int it = lane; it < BT * VR; it += 32) {
+            const int r = it / VR, v = it % VR;
+            const bool ok = tb + r < te && wc0 + v * VEC < cend;
+            const int64_t t = ok ? tb + r : t0;
+            const int cv = ok ? wc0 + v * VEC : grp * p.per;
+            E* d = raw + r * WC + v * VEC;
+            const int bytes = ok ? 16 : 0;
+            cp_async16(d, static_cast<const E*>(p.x) + t * p.ldx + cv, bytes);
+            cp_async16(d + BT * WC, static_cast<const E*>(p.dt) + t * p.lddt + cv, bytes);
+            cp_async16(d + 2 * BT * WC, static_cast<const E*>(p.dy) + t * p.lddy + cv, bytes);
+            if (p.z) cp_async16(d + 3 * BT * WC, static_cast<const E*>(p.z) + t * p.ldz + cv, bytes);
         }
-        if (b < 0) break;
-        for (int it = tid; it < BT * NP; it += NT) {
-            const int r = it / NP, n = it - r * NP;
-            const int64_t t = tb + r;
-            const bool in = t < last_t && n < p.N;
-            const int64_t off = (int64_t)grp * p.N + n;
-            Cs[it] = in ? Elem<E>::load(static_cast<const E*>(p.C) + t * p.ldc + off) : 0.f;
-            if (!SUMMARY) Bs[it] = in ? Elem<E>::load(static_cast<const E*>(p.B) + t * p.ldb + off) : 0.f;
+        cp_async_commit();
+    };
+    constexpr int PER = BT * 2 * NP / NT;
+    E bc[PER];
+    auto fetch_bc = [&](int tb) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int it = tid + i * NT, r = it / (2 * NP), j = it % (2 * NP), n = j % NP;
+            const int64_t t = min(tb + r, te - 1);
+            const E* q = (j < NP ? static_cast<const E*>(p.B) + t * p.ldb : static_cast<const E*>(p.C) + t * p.ldc) +
+                         (int64_t)grp * p.N;
+            bc[i] = n < p.N ? load_now(q + n) : Elem<E>::from_f(0.f);
         }
-        if (!SUMMARY && tid < BT) {
-            const int t = tb + tid;
-            const bool st = t < te && __ldg(p.cu + seq_of(p.cu, p.num_seqs, t)) == t;
-            const uint32_t m = __ballot_sync(0xffffffffu, st);
-            if (lane == 0) mask[warp] = m;
-        }
+    };
+    auto put_bc = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) bcs[b * BT * 2 * NP + tid + i * NT] = Elem<E>::to_f(bc[i]);
+    };
+
+    const int nblk = (te - t0 + BT - 1) / BT;
+    if (nblk > 0) {
+        copy(t0 + (nblk - 1) * BT);
+        fetch_bc(t0 + (nblk - 1) * BT);
+        put_bc(0);
         __syncthreads();
-        if (SUMMARY) {
-#pragma unroll 4
-            for (int r = BT - 1; r >= 0; --r) {
-                const float d = dl[r * CH + cl], g = ds[r * CH + cl];
-                const float4 cv4 = *reinterpret_cast<const float4*>(Cs + r * NP + k * NS);
-                const float cc[4] = {cv4.x, cv4.y, cv4.z, cv4.w};
-#pragma unroll
-                for (int n = 0; n < NS; ++n) dh[n] = fmaf(g, cc[n], dh[n]) * decay_fast(d, A2[n]);
-                dsum += d;
-            }
-            __syncthreads();
-            continue;
-        }
-        const uint64_t starts = (uint64_t)mask[0] | (uint64_t)mask[1] << 32;
-        // forward over the block: the state before every piece
+    }
+    int buf = 0;
+    for (int b = nblk - 1; b >= 0; --b, buf ^= 1) {
+        const int tb = t0 + b * BT;
         load_state(h, p.ckpt, tb / BT);
+        uint32_t starts = 0;  // which of the block's tokens start a sequence
+        {
+            const int t = tb + lane;
+            const bool st = lane < BT && t < te && __ldg(p.cu + seq_of(p.cu, p.num_seqs, t)) == t;
+            starts = __ballot_sync(0xffffffffu, st);
+        }
+        cp_async_wait_all();
+        __syncwarp();
+#pragma unroll 4
+        for (int r0 = 0; r0 < BT; r0 += TPS) {
+            const int i = r0 * WC + lane;  // token r0 + lane / WC, channel sch
+            const bool ok = tb + r0 + lane / WC < te;
+            const float xv = Elem<E>::to_f(raw[i]), gy = Elem<E>::to_f(raw[2 * BT * WC + i]);
+            const float v = Elem<E>::to_f(raw[BT * WC + i]) + sbias;
+            const float d = softplus_f(v);
+            float g = gy, qv = 0.f;
+            if (p.z) {
+                const float zv = Elem<E>::to_f(raw[3 * BT * WC + i]), sg = sigmoid_fast(zv);
+                g = gy * (zv * sg);
+                qv = gy * sg * fmaf(zv, 1.f - sg, 1.f);
+            }
+            dl[i] = ok ? d : 0.f;
+            uu[i] = ok ? d * xv : 0.f;
+            dsv[i] = ok ? g : 0.f;
+            slope[i] = v > 20.f ? 1.f : sigmoid_fast(v);
+            q1[i] = qv;
+            xx[i] = xv;
+        }
+        __syncwarp();
+        if (b > 0) {
+            copy(tb - BT);
+            fetch_bc(tb - BT);
+        }
+        const float* bcb = bcs + buf * BT * 2 * NP + k * NS;
+        const int co = cg * NC;
+        // forward: the state before every piece
+#pragma unroll 1
         for (int q = 0; q < BT / Q; ++q) {
 #pragma unroll
-            for (int n = 0; n < NS; ++n) hs[(q * NS + n) * NT + tid] = h[n];
+            for (int i = 0; i < NC; ++i) hs[(q * NC + i) * 32 + lane] = make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
             if (q == BT / Q - 1) break;
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                const int r = q * Q + i;
+            for (int e = 0; e < Q; ++e) {
+                const int r = q * Q + e;
                 if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
-                const float d = dl[r * CH + cl], u = uu[r * CH + cl];
-                const float4 b4 = *reinterpret_cast<const float4*>(Bs + r * NP + k * NS);
-                const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+                const float4 d4 = lds4(dl + r * WC + co), u4 = lds4(uu + r * WC + co), b4 = lds4(bcb + r * 2 * NP);
+                const float d_[4] = {d4.x, d4.y, d4.z, d4.w}, u_[4] = {u4.x, u4.y, u4.z, u4.w};
+                const F2 bb[2] = {{b4.x, b4.y}, {b4.z, b4.w}};
 #pragma unroll
-                for (int n = 0; n < NS; ++n) h[n] = fmaf(decay_fast(d, A2[n]), h[n], u * bb[n]);
+                for (int i = 0; i < NC; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        h[i][j] = f2_fma(f2_dup(u_[i]), bb[j], f2_mul(f2_decay(f2_dup(d_[i]), A2[i][j]), h[i][j]));
             }
         }
         // the pieces, last to first
+#pragma unroll 1
         for (int q = BT / Q - 1; q >= 0; --q) {
-            float* sl = slab + ((q & 1) * NW + warp) * Q * 2 * NP;
-            float a[Q][NS], hb[Q][NS], ys[2][4];
+            F2 a[Q][NC][2], w[Q][NC][2];
+            float ys[Q];
 #pragma unroll
-            for (int n = 0; n < NS; ++n) h[n] = hs[(q * NS + n) * NT + tid];
+            for (int i = 0; i < NC; ++i) {
+                const float4 v = hs[(q * NC + i) * 32 + lane];
+                h[i][0] = F2{v.x, v.y};
+                h[i][1] = F2{v.z, v.w};
+            }
+            float* sl = slab + warp * BT * 2 * NP + k * NS;
 #pragma unroll
-            for (int i2 = 0; i2 < Q; i2 += 2) {
+            for (int e2 = 0; e2 < Q; e2 += 2) {
                 float v8[8];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = i2 + e, r = q * Q + i;
+                for (int o = 0; o < 2; ++o) {
+                    const int e = e2 + o, r = q * Q + e;
                     if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
-                    const float d = dl[r * CH + cl], u = uu[r * CH + cl], g = ds[r * CH + cl];
-                    const float4 b4 = *reinterpret_cast<const float4*>(Bs + r * NP + k * NS);
-                    const float4 c4 = *reinterpret_cast<const float4*>(Cs + r * NP + k * NS);
-                    const float bb[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-                    float acc = 0.f;
+                    const float4 d4 = lds4(dl + r * WC + co), u4 = lds4(uu + r * WC + co), g4 = lds4(dsv + r * WC + co);
+                    const float4 b4 = lds4(bcb + r * 2 * NP), c4v = lds4(bcb + r * 2 * NP + NP);
+                    const float d_[4] = {d4.x, d4.y, d4.z, d4.w}, u_[4] = {u4.x, u4.y, u4.z, u4.w};
+                    const float g_[4] = {g4.x, g4.y, g4.z, g4.w};
+                    const F2 bb[2] = {{b4.x, b4.y}, {b4.z, b4.w}}, cc[2] = {{c4v.x, c4v.y}, {c4v.z, c4v.w}};
+                    F2 dc[2];
+                    float yv[NC];
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        a[i][n] = decay_fast(d, A2[n]);
-                        hb[i][n] = h[n];
-                        h[n] = fmaf(a[i][n], h[n], u * bb[n]);
-                        acc = fmaf(h[n], cc[n], acc);
-                        v8[4 * e + n] = cin ? g * h[n] : 0.f;
+                    for (int i = 0; i < NC; ++i) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            a[e][i][j] = f2_decay(f2_dup(d_[i]), A2[i][j]);
+                            w[e][i][j] = f2_mul(a[e][i][j], h[i][j]);
+                            h[i][j] = f2_fma(f2_dup(u_[i]), bb[j], w[e][i][j]);
+                            dc[j] = i ? f2_fma(f2_dup(g_[i]), h[i][j], dc[j]) : f2_mul(f2_dup(g_[i]), h[i][j]);
+                        }
+                        const F2 t = f2_fma(h[i][1], cc[1], f2_mul(h[i][0], cc[0]));
+                        yv[i] = t.x + t.y;
                     }
-                    ys[i >> 2][i & 3] = acc;
+                    ys[e] = sum_states<K>(yv[0], yv[1], yv[2], yv[3], k);
+                    v8[4 * o] = dc[0].x;
+                    v8[4 * o + 1] = dc[0].y;
+                    v8[4 * o + 2] = dc[1].x;
+                    v8[4 * o + 3] = dc[1].y;
                 }
                 int first;
-                bool keep;
-                sum_channels8<K>(v8, lane, first, keep);
-                if (keep)
+                sum_channels8<K>(v8, lane, first);
 #pragma unroll
-                    for (int j = 0; j < kLeft8<K>; ++j) {
-                        const int idx = first + j;
-                        sl[(i2 + (idx >> 2)) * 2 * NP + NP + k * NS + (idx & 3)] = v8[j];
-                    }
+                for (int j = 0; j < kLeft8<K>; ++j)
+                    sl[(q * Q + e2 + ((first + j) >> 2)) * 2 * NP + NP + ((first + j) & 3)] = v8[j];
             }
-            sum_lanes4<K>(ys[0], k);
-            sum_lanes4<K>(ys[1], k);
-            float du4[4], dd4[4];
 #pragma unroll
-            for (int i2 = Q - 2; i2 >= 0; i2 -= 2) {
+            for (int e2 = Q - 2; e2 >= 0; e2 -= 2) {
                 float v8[8];
 #pragma unroll
-                for (int e = 1; e >= 0; --e) {
-                    const int i = i2 + e, r = q * Q + i;
-                    const float d = dl[r * CH + cl], u = uu[r * CH + cl], g = ds[r * CH + cl];
-                    const float4 b4 = *reinterpret_cast<const float4*>(Bs + r * NP + k * NS);
-                    const float4 c4 = *reinterpret_cast<const float4*>(Cs + r * NP + k * NS);
-                    const float bb[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-                    float du = 0.f, dd = 0.f;
+                for (int o = 1; o >= 0; --o) {
+                    const int e = e2 + o, r = q * Q + e, t = tb + r;
+                    const float4 d4 = lds4(dl + r * WC + co), u4 = lds4(uu + r * WC + co), g4 = lds4(dsv + r * WC + co);
+                    const float4 b4 = lds4(bcb + r * 2 * NP), c4v = lds4(bcb + r * 2 * NP + NP);
+                    const float d_[4] = {d4.x, d4.y, d4.z, d4.w}, u_[4] = {u4.x, u4.y, u4.z, u4.w};
+                    const float g_[4] = {g4.x, g4.y, g4.z, g4.w};
+                    const F2 bb[2] = {{b4.x, b4.y}, {b4.z, b4.w}}, cc[2] = {{c4v.x, c4v.y}, {c4v.z, c4v.w}};
+                    F2 db[2];
+                    float du[NC], dd[NC];
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        dh[n] = fmaf(g, cc[n], dh[n]);
-                        v8[4 * e + n] = cin ? dh[n] * u : 0.f;
-                        du = fmaf(dh[n], bb[n], du);
-                        dh[n] *= a[i][n];
-                        const float m = dh[n] * hb[i][n];
-                        dd = fmaf(A2[n], m, dd);
-                        dA[n] = fmaf(d, m, dA[n]);
+                    for (int i = 0; i < NC; ++i) {
+                        F2 m[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            dh[i][j] = f2_fma(f2_dup(g_[i]), cc[j], dh[i][j]);
+                            db[j] = i ? f2_fma(f2_dup(u_[i]), dh[i][j], db[j]) : f2_mul(f2_dup(u_[i]), dh[i][j]);
+                            m[j] = f2_mul(dh[i][j], w[e][i][j]);
+                            dA[i][j] = f2_fma(f2_dup(d_[i]), m[j], dA[i][j]);
+                        }
+                        const F2 t1 = f2_fma(dh[i][1], bb[1], f2_mul(dh[i][0], bb[0]));
+                        const F2 t2 = f2_fma(m[1], A2[i][1], f2_mul(m[0], A2[i][0]));
+                        du[i] = t1.x + t1.y;
+                        dd[i] = t2.x + t2.y;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) dh[i][j] = f2_mul(dh[i][j], a[e][i][j]);
                     }
-                    du4[i & 3] = du;
-                    dd4[i & 3] = dd;
+                    v8[4 * o] = db[0].x;
+                    v8[4 * o + 1] = db[0].y;
+                    v8[4 * o + 2] = db[1].x;
+                    v8[4 * o + 3] = db[1].y;
+                    const float dus = sum_states<K>(du[0], du[1], du[2], du[3], k);
+                    const float dds = sum_states<K>(dd[0], dd[1], dd[2], dd[3], k);
                     if (starts >> r & 1) {  // the token starts a sequence: dh is the gradient of its h0
-                        const int t = tb + r, n = seq_of(p.cu, p.num_seqs, t);
+                        const int n = seq_of(p.cu, p.num_seqs, t);
                         if (p.dh0) store_state(p.dh0, n, dh);
                         int m = n - 1;
                         while (m >= 0 && __ldg(p.cu + m) == t) pass_empty(m--);
                         load_state(dh, m >= 0 ? p.dhf : nullptr, m >= 0 ? m : 0);
                     }
+                    // the outputs of the lane's channel
+                    const int i = r * WC + och;
+                    if (writer && t < te) {
+                        const float g = dsv[i], xv = xx[i];
+                        const float gd = fmaf(kLn2, dds, dus * xv) * slope[i];
+                        dxp[(int64_t)t * p.ch] = Elem<E>::from_f(fmaf(dus, dl[i], Do * g));
+                        dtp[(int64_t)t * p.ch] = Elem<E>::from_f(gd);
+                        if (p.z) dzp[(int64_t)t * p.ch] = Elem<E>::from_f(fmaf(Do, xv, ys[e]) * q1[i]);
+                        aD = fmaf(g, xv, aD);
+                        aT += gd;
+                    }
                 }
                 int first;
-                bool keep;
-                sum_channels8<K>(v8, lane, first, keep);
-                if (keep)
+                sum_channels8<K>(v8, lane, first);
 #pragma unroll
-                    for (int j = 0; j < kLeft8<K>; ++j) {
-                        const int idx = first + j;
-                        sl[(i2 + (idx >> 2)) * 2 * NP + k * NS + (idx & 3)] = v8[j];
-                    }
-                if ((i2 & 2) == 0) {  // four tokens are done: their inputs are dead, their sums take the place
-                    sum_lanes4<K>(du4, k);
-                    sum_lanes4<K>(dd4, k);
-                    const int r = q * Q + i2;
-                    put_lanes4<K>(uu + r * CH + cl, CH, du4, k);
-                    put_lanes4<K>(dl + r * CH + cl, CH, dd4, k);
-                    put_lanes4<K>(ds + r * CH + cl, CH, ys[i2 >> 2], k);
-                }
-            }
-            __syncthreads();
-            // dB, dC of the piece over the block's warps
-            for (int it = tid; it < Q * 2 * NP; it += NT) {
-                const int i = it / (2 * NP), j = it - i * 2 * NP, n = j % NP, which = j / NP;
-                const int64_t t = tb + q * Q + i;
-                if (t < te && n < p.N) {
-                    const float* sp = slab + (q & 1) * NW * Q * 2 * NP + it;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) sum += sp[w * Q * 2 * NP];
-                    p.bc[(((int64_t)blockIdx.x * p.T + t) * 2 + which) * p.N + n] = sum;
-                }
+                for (int j = 0; j < kLeft8<K>; ++j)
+                    sl[(q * Q + e2 + ((first + j) >> 2)) * 2 * NP + ((first + j) & 3)] = v8[j];
             }
         }
-        done = tb;
-    }
-    if (SUMMARY) {
-        store_state(p.G, s, dh);
-        if (k == 0 && cin) p.sd[(int64_t)s * p.ch + c] = dsum;
-        return;
+        if (b > 0) put_bc(buf ^ 1);  // last read a block ago
+        __syncthreads();
+        // dB, dC of the block over its warps
+        for (int it = tid; it < BT * 2 * NP; it += NT) {
+            const int r = it / (2 * NP), j = it % (2 * NP), n = j % NP, which = j / NP;
+            float sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < NW; ++v) sum += slab[v * BT * 2 * NP + it];
+            if (tb + r < te && n < p.N) p.bc[(((int64_t)blockIdx.x * p.T + tb + r) * 2 + which) * p.N + n] = sum;
+        }
+        __syncthreads();  // the slabs are read
     }
     // the parameters' partial gradients of this segment
     float* par = p.par + (int64_t)s * p.ch * (p.N + 2);
-    if (cin)
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-            if (k * NS + n < p.N) par[(int64_t)c * p.N + k * NS + n] = dA[n] * A2[n] * kLn2;
-    __syncthreads();
-    float* red = dl;  // [2][NT / VR][CH]: the tiles are dead
-    constexpr int RR = NT / VR;
-    static_assert(2 * RR * CH <= 2 * BT * CH + BT * NP, "the partial sums lie in the tiles' place");
-    store8(red + vrow * CH + 8 * vcol, aD);
-    store8(red + (RR + vrow) * CH + 8 * vcol, aT);
-    __syncthreads();
-    for (int i = tid; i < 2 * CH; i += NT) {
-        const int cc = i % CH;
-        const float* src = i < CH ? red : red + RR * CH;
-        float sum = 0.f;
-        for (int r = 0; r < RR; ++r) sum += src[r * CH + cc];
-        if (cbase + cc < cend) par[(int64_t)p.ch * p.N + (i < CH ? 0 : p.ch) + cbase + cc] = sum;
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) dA[i][j] = f2_mul(f2_mul(dA[i][j], A2[i][j]), f2_dup(kLn2));
+    store_state(par, 0, dA);
+    if (writer) {
+        par[(int64_t)p.ch * p.N + wc0 + och] = aD;
+        par[(int64_t)p.ch * p.N + p.ch + wc0 + och] = aT;
     }
 }
 
@@ -497,15 +478,8 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const float* bc, int T, in
     out[(t * groups + g) * N + n] = Elem<E>::from_f(s);
 }
 
-int lanes_of(int N) {
-    int K = 1;
-    while (4 * K < N) K <<= 1;
-    return K;
-}
-int block_channels(int N) {
-    const int K = lanes_of(N);
-    return K <= 4 ? 64 : 256 / K;
-}
+int lanes_of(int N) { return N <= 16 ? 4 : (N <= 32 ? 8 : 16); }
+int block_channels(int N) { return NW * NC * 32 / lanes_of(N); }
 
 // Segments: enough blocks for two resident ones an SM, 64 tokens or more.
 void segments(int T, int ch, int N, int groups, int& tiles, int& seg, int& S) {
@@ -546,17 +520,10 @@ namespace {
 
 template <typename E, int K>
 gdn_status run_bwd(const ScanBwdParams& p, int groups, cudaStream_t s) {
-    using Sh = BShape<K>;
-    gdn_status st = set_smem_attr((const void*)scan_bwd_kernel<E, K, false>, Sh::smem);
+    using Sh = BShape<E, K>;
+    const gdn_status st = set_smem_attr((const void*)scan_bwd_kernel<E, K>, Sh::smem);
     if (st != GDN_OK) return st;
-    if ((st = set_smem_attr((const void*)scan_bwd_kernel<E, K, true>, Sh::smem_summary)) != GDN_OK) return st;
-    dim3 grid(groups * p.tiles, p.S);
-    if (p.S > 1) {
-        dim3 g1(grid.x, p.S - 1);
-        scan_bwd_kernel<E, K, true><<<g1, Sh::NT, Sh::smem_summary, s>>>(p);
-        if ((st = check_launch("scan_bwd_kernel (start gradients)")) != GDN_OK) return st;
-    }
-    scan_bwd_kernel<E, K, false><<<grid, Sh::NT, Sh::smem, s>>>(p);
+    scan_bwd_kernel<E, K><<<dim3(groups * p.tiles, p.S), NT, Sh::smem, s>>>(p);
     return check_launch("scan_bwd_kernel");
 }
 
@@ -564,8 +531,6 @@ template <typename E>
 gdn_status dispatch_bwd(const ScanBwdParams& p, int groups, void* dB, void* dC, cudaStream_t s) {
     gdn_status st;
     switch (lanes_of(p.N)) {
-        case 1: st = run_bwd<E, 1>(p, groups, s); break;
-        case 2: st = run_bwd<E, 2>(p, groups, s); break;
         case 4: st = run_bwd<E, 4>(p, groups, s); break;
         case 8: st = run_bwd<E, 8>(p, groups, s); break;
         default: st = run_bwd<E, 16>(p, groups, s); break;
@@ -613,6 +578,8 @@ gdn_status gdn_ssm_scan_bwd(const void* dy, int64_t lddy, const void* x, int64_t
         if (!al16(dx) || !al16(ddt) || !al16(dz))
             return fail(GDN_ERR_INVALID_ARG, "dx, ddt and dz must be 16-byte aligned");
     }
+    if (!al16(A_log) || !al16(h0) || !al16(ckpt) || !al16(dh_final))
+        return fail(GDN_ERR_INVALID_ARG, "A_log, h0, ckpt and dh_final must be 16-byte aligned");
     if (dh_final && dh_final == dh0) return fail(GDN_ERR_INVALID_ARG, "dh0 must not be dh_final");
     const Layout L = layout(T, channels, d_state, groups);
     if (!workspace || workspace_bytes < L.total)
@@ -632,6 +599,13 @@ gdn_status gdn_ssm_scan_bwd(const void* dy, int64_t lddy, const void* x, int64_t
     p.bc = reinterpret_cast<float*>(ws + L.bc);
     p.par = reinterpret_cast<float*>(ws + L.par);
     cudaStream_t s = (cudaStream_t)stream;
+    if (T > 0) {
+        ScanParams g{};
+        g.x = dy; g.ldx = lddy; g.dt = dt; g.lddt = lddt; g.z = z; g.ldz = ldz; g.B = C; g.ldb = ldc; g.C = C; g.ldc = ldc;
+        g.A_log = A_log; g.dt_bias = dt_bias; g.h0 = dh_final; g.cu = cu_seqlens; g.num_seqs = num_seqs; g.T = T;
+        g.ch = channels; g.N = d_state; g.per = channels / groups; g.seg = p.seg; g.S = p.S; g.H = p.G; g.sd = p.sd;
+        if ((st = launch_scan_start_grad(g, dtype, groups, s)) != GDN_OK) return st;
+    }
     st = dtype == GDN_BF16 ? dispatch_bwd<__nv_bfloat16>(p, groups, dB, dC, s) : dispatch_bwd<float>(p, groups, dB, dC, s);
     if (st != GDN_OK) return st;
     const int64_t nA = (int64_t)channels * d_state;
