@@ -545,7 +545,7 @@ gdn_status gdn_ssm_conv_step(const void *x, int64_t ldx, gdn_dtype dtype, int32_
  *           sequence's last token (h0 or 0 for an empty sequence); must not
  *           overlap h0
  *   ckpt    device fp32 [gdn_ssm_scan_ckpt_floats(...)], or NULL: the states
- *           before every 16th packed token, for gdn_ssm_scan_bwd
+ *           before every 8th packed token, for gdn_ssm_scan_bwd
  *   workspace device, >= gdn_ssm_scan_workspace_size(...) bytes, 256-byte
  *           aligned, contents on entry irrelevant
  * Needs channels / groups a multiple of 8, N in 1..64, row strides of x, dt,

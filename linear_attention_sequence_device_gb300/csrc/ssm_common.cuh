@@ -107,33 +107,50 @@ __device__ __forceinline__ float softplus_f(float v) {
 constexpr float kDecayBias = 2.6e-8f;
 __device__ __forceinline__ float decay_fast(float d, float A2) { return exp2_fast(fmaf(d, A2, kDecayBias)); }
 
-// two fp32 operations in one instruction (the pipe's rate is the same, the issue slots are half)
+// Two fp32 values in a register pair, for the two-wide instructions: the pipe's
+// rate is the same, the instructions are half.  Kept as 64 bits, so that the pair
+// is not taken apart and put together again between operations.
 struct F2 {
-    float x, y;
+    unsigned long long b;
+    __device__ __forceinline__ float x() const { return __uint_as_float((unsigned)b); }
+    __device__ __forceinline__ float y() const { return __uint_as_float((unsigned)(b >> 32)); }
 };
-__device__ __forceinline__ unsigned long long f2_bits(F2 v) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.b) : "f"(x), "f"(y));
     return r;
 }
-__device__ __forceinline__ F2 f2_of(unsigned long long b) {
-    F2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
-    return v;
-}
 __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
-    return f2_of(r);
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.b) : "l"(a.b), "l"(b.b), "l"(c.b));
+    return r;
 }
 __device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
-    return f2_of(r);
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
 }
-__device__ __forceinline__ F2 f2_exp2(F2 a) { return F2{exp2_fast(a.x), exp2_fast(a.y)}; }
-__device__ __forceinline__ F2 f2_dup(float v) { return F2{v, v}; }
+__device__ __forceinline__ F2 f2_exp2(F2 a) {
+    F2 r;
+    asm("{\n\t.reg .f32 lo, hi;\n\tmov.b64 {lo, hi}, %1;\n\tex2.approx.ftz.f32 lo, lo;\n\tex2.approx.ftz.f32 hi, hi;\n\t"
+        "mov.b64 %0, {lo, hi};\n\t}"
+        : "=l"(r.b)
+        : "l"(a.b));
+    return r;
+}
+__device__ __forceinline__ F2 f2_dup(float v) { return f2(v, v); }
 __device__ __forceinline__ F2 f2_decay(F2 d, F2 A2) { return f2_exp2(f2_fma(d, A2, f2_dup(kDecayBias))); }
+__device__ __forceinline__ float f2_sum(F2 a) { return a.x() + a.y(); }
+// one pair, or two, from shared memory
+__device__ __forceinline__ F2 f2_load(const float* p) { return F2{*reinterpret_cast<const unsigned long long*>(p)}; }
+__device__ __forceinline__ void f2_load2(const float* p, F2& a, F2& b) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    a.b = v.x;
+    b.b = v.y;
+}
+__device__ __forceinline__ void f2_store2(void* p, F2 a, F2 b) {
+    *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(a.b, b.b);
+}
 
 // the sequence that holds packed token t: the last n with cu[n] <= t, which is
 // not empty; clamped to a sequence for a malformed cu

@@ -58,35 +58,35 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
     const int s = REV ? blockIdx.y + 1 : blockIdx.y;
     int t0 = s * p.seg, te = min(p.T, t0 + p.seg);
     F2 A2[NS / 2], h[NS / 2];
-    {
-        float* a = reinterpret_cast<float*>(A2);
-        float* hh = reinterpret_cast<float*>(h);
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const int st = k * NS + n;
-            a[n] = st < p.N ? -expf(__ldg(p.A_log + (int64_t)cc * p.N + st)) * kLog2e : 0.f;
-            hh[n] = 0.f;
-        }
+    for (int q = 0; q < NS / 2; ++q) {
+        const int st = k * NS + 2 * q;
+        const float* g = p.A_log + (int64_t)cc * p.N + st;
+        A2[q] = f2(st < p.N ? -expf(__ldg(g)) * kLog2e : 0.f, st + 1 < p.N ? -expf(__ldg(g + 1)) * kLog2e : 0.f);
+        h[q] = f2_dup(0.f);
     }
     const bool vec = p.N % 4 == 0;
     auto load_state = [&](const float* src, int64_t row) {  // src [rows, ch, N] or null
-        float* hh = reinterpret_cast<float*>(h);
-        const float* q = src + (row * p.ch + cc) * p.N + k * NS;
+        const float* g = src + (row * p.ch + cc) * p.N + k * NS;
 #pragma unroll
-        for (int n = 0; n < NS; ++n) hh[n] = src && k * NS + n < p.N ? __ldg(q + n) : 0.f;
+        for (int q = 0; q < NS / 2; ++q) {
+            const int st = k * NS + 2 * q;
+            h[q] = f2(src && st < p.N ? __ldg(g + 2 * q) : 0.f, src && st + 1 < p.N ? __ldg(g + 2 * q + 1) : 0.f);
+        }
     };
     auto store_state = [&](float* dst, int64_t row) {
-        const float* hh = reinterpret_cast<const float*>(h);
-        float* q = dst + (row * p.ch + cc) * p.N + k * NS;
+        float* g = dst + (row * p.ch + cc) * p.N + k * NS;
         if (!in) return;
 #pragma unroll
-        for (int n = 0; n < NS; n += 4) {
+        for (int q = 0; q < NS / 2; q += 2) {
+            const int st = k * NS + 2 * q;
             if (vec) {
-                if (k * NS + n < p.N) *reinterpret_cast<float4*>(q + n) = make_float4(hh[n], hh[n + 1], hh[n + 2], hh[n + 3]);
+                if (st < p.N) f2_store2(g + 2 * q, h[q], h[q + 1]);
             } else {
-#pragma unroll
-                for (int i = n; i < n + 4; ++i)
-                    if (k * NS + i < p.N) q[i] = hh[i];
+                if (st < p.N) g[2 * q] = h[q].x();
+                if (st + 1 < p.N) g[2 * q + 1] = h[q].y();
+                if (st + 2 < p.N) g[2 * q + 2] = h[q + 1].x();
+                if (st + 3 < p.N) g[2 * q + 3] = h[q + 1].y();
             }
         }
     };
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
                 const float* Hj = p.H + row * p.N + k * NS;
 #pragma unroll
                 for (int q = 0; q < NS / 2; ++q) {
-                    const F2 add{k * NS + 2 * q < p.N ? __ldg(Hj + 2 * q) : 0.f,
-                                 k * NS + 2 * q + 1 < p.N ? __ldg(Hj + 2 * q + 1) : 0.f};
+                    const F2 add = f2(k * NS + 2 * q < p.N ? __ldg(Hj + 2 * q) : 0.f,
+                                      k * NS + 2 * q + 1 < p.N ? __ldg(Hj + 2 * q + 1) : 0.f);
                     h[q] = f2_fma(f2_exp2(f2_mul(d, A2[q])), h[q], add);  // one exponential for the whole segment
                 }
             }
@@ -196,27 +196,27 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
         const F2 d = f2_dup(dlt), uu = f2_dup(u);
         F2 acc[2];
 #pragma unroll
-        for (int n = 0; n < NS; n += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(row + n);
-            const int q = n / 2;
+        for (int q = 0; q < NS / 2; q += 2) {
+            F2 b0, b1;
+            f2_load2(row + 2 * q, b0, b1);
             if (REV) {
-                h[q] = f2_mul(f2_decay(d, A2[q]), f2_fma(uu, F2{b.x, b.y}, h[q]));
-                h[q + 1] = f2_mul(f2_decay(d, A2[q + 1]), f2_fma(uu, F2{b.z, b.w}, h[q + 1]));
+                h[q] = f2_mul(f2_decay(d, A2[q]), f2_fma(uu, b0, h[q]));
+                h[q + 1] = f2_mul(f2_decay(d, A2[q + 1]), f2_fma(uu, b1, h[q + 1]));
             } else {
-                h[q] = f2_fma(f2_decay(d, A2[q]), h[q], f2_mul(uu, F2{b.x, b.y}));
-                h[q + 1] = f2_fma(f2_decay(d, A2[q + 1]), h[q + 1], f2_mul(uu, F2{b.z, b.w}));
+                h[q] = f2_fma(f2_decay(d, A2[q]), h[q], f2_mul(uu, b0));
+                h[q + 1] = f2_fma(f2_decay(d, A2[q + 1]), h[q + 1], f2_mul(uu, b1));
             }
             if (!LAST) {
-                const float4 cv = *reinterpret_cast<const float4*>(row + NP + n);
-                const F2 c0{cv.x, cv.y}, c1{cv.z, cv.w};
-                acc[0] = n ? f2_fma(h[q], c0, acc[0]) : f2_mul(h[q], c0);
-                acc[1] = n ? f2_fma(h[q + 1], c1, acc[1]) : f2_mul(h[q + 1], c1);
+                F2 c0, c1;
+                f2_load2(row + NP + 2 * q, c0, c1);
+                acc[0] = q ? f2_fma(h[q], c0, acc[0]) : f2_mul(h[q], c0);
+                acc[1] = q ? f2_fma(h[q + 1], c1, acc[1]) : f2_mul(h[q + 1], c1);
             }
         }
         if (LAST) {
             dsum += dlt;
         } else {
-            float o = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            float o = f2_sum(acc[0]) + f2_sum(acc[1]);
 #pragma unroll
             for (int m = 1; m < K; m <<= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
             o = fmaf(Dc, xv, o);
@@ -235,12 +235,12 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
         copy(jb + (NST - 1) * TT, st == 0 ? NST - 1 : st - 1);
         const bool more = jb + TT < len;
         if (more) fetch_bc(jb + TT);
-        if (!LAST && p.ckpt) store_state(p.ckpt, (t0 + jb) / kCkpt);
         const E* xs = ring + st * NA * TT * CH + cl;
 #pragma unroll 1
         for (int r0 = 0; r0 < TT; r0 += UN) {
             const int jg = jb + r0, tg = t0 + jg;  // tg: the first of the group's tokens (forwards)
             if (jg >= len) break;
+            if (!LAST && p.ckpt && tg % kCkpt == 0) store_state(p.ckpt, tg / kCkpt);
             const float* row = bcs + (buf * TT + r0) * NB + k * NS;
             const E* xg = xs + r0 * CH;
             E* yo = yp + (int64_t)tg * p.ldy;

@@ -5,7 +5,7 @@
 
 namespace gdn {
 
-constexpr int kCkpt = 16;  // tokens between the forward's checkpoints for the backward
+constexpr int kCkpt = 8;  // tokens between the forward's checkpoints for the backward
 
 struct ScanParams {
     const void* x; int64_t ldx;

@@ -8,16 +8,20 @@
 //   dA_log_n = A_n sum_t delta m_n,   dx = du delta + D ds,   dD = sum ds x,
 //   ddt = ddelta s(dt + bias),   dz = dy (sum_n C_n h_n + D x) silu'(z).
 //
-// The states before each token come from the forward's checkpoints (every 16
-// packed tokens).  A block of 16 tokens is run forward once, keeping the state
-// before every fourth token in shared memory; then its pieces of four tokens are
+// The states before each token come from the forward's checkpoints (every 8
+// packed tokens).  A block of 8 tokens is run forward once, keeping the state
+// before every second token in shared memory; then its pieces of two tokens are
 // taken from the last to the first: forward again, with the decays a and the
-// products a h in registers, then backward, where m = dh a h.
+// products a h in registers, then backward, where m = dh a h.  Longer pieces need
+// registers (two warps a scheduler instead of three: 3.1 against 2.9 ms on 32768
+// tokens of 4096 channels), longer blocks shared memory.
 //
 // Work split.  A channel's states lie on K lanes with four each, and a lane
-// holds four channels, so a warp works on 128 / K channels and a lane on 16
-// states a token.  The sums over channels (dB, dC) are taken over the lane's own
-// four channels first, then by halving exchanges over the lanes K apart, over the
+// holds four channels as two pairs, so a warp works on 128 / K channels and a
+// lane on 16 states a token.  delta, u and ds of a pair are read as one operand
+// of the two-wide instructions; B and C lie in shared memory twice each for the
+// same reason.  The sums over channels (dB, dC) are taken over the lane's own
+// channels first, then by halving exchanges over the lanes K apart, over the
 // block's four warps through shared memory, and over the channel tiles through
 // one partial each, added by a second kernel.  The sums over a channel's states
 // (y, du, ddelta) go by halving exchanges over its K lanes, which leave each lane
@@ -25,17 +29,19 @@
 // orders of summation are fixed.
 //
 // x, dt, dy and z of the next block come by asynchronous copies while this one
-// is worked on; every warp stages its own channels, one channel a lane, so that
-// the warps meet only at the sums of dB and dC, once a block.
+// is worked on, its checkpoint from the last piece on; every warp stages its own
+// channels, one channel a lane, so that the warps meet only at the sums of dB
+// and dC, once a block.
 //
 // Parallelism over tokens as in the forward: segments of equal length; a first
 // launch runs each segment's part of the sequence that came in from the segment
 // before, backwards from zero (or from dh_final where the sequence ends in it),
 // and a block of the main launch folds the segments behind its own.
 //
-// What bounds it: issue slots.  Per token and 32 channels about 120 two-wide
-// operations (two slots each), 28 exponentials, 100 instructions of exchanges and
-// shared memory traffic and 70 for the element-wise parts.
+// What bounds it: issue slots and the latencies that three warps a scheduler do
+// not cover.  Per token and 32 channels 120 two-wide operations (two slots each),
+// 33 of the special function unit, 60 of shared memory and exchanges, 500
+// instructions in all, in about 900 cycles.
 #include "chunk_common.cuh"
 #include "ssm_scan.cuh"
 
@@ -43,10 +49,12 @@ namespace gdn {
 namespace {
 
 constexpr int BT = kCkpt;  // tokens per block
-constexpr int Q = 4;       // tokens per piece
+constexpr int Q = 2;       // tokens per piece
 constexpr int NS = 4;      // states per lane and channel
-constexpr int NC = 4;      // channels per lane
+constexpr int P = 2;       // channel pairs per lane
+constexpr int NC = 2 * P;  // channels per lane
 constexpr int NW = 4;      // warps per block
+constexpr int OCC = 3;     // blocks per SM: 168 registers a thread
 constexpr int NT = 32 * NW;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -72,12 +80,13 @@ struct BShape {
     static constexpr int WC = NC * 32 / K;  // channels per warp
     static constexpr int CH = NW * WC;      // channels per block
     static constexpr int NP = NS * K;       // padded states
-    // a warp's floats: delta, u, ds, slope, q1, x [BT][WC] each; the states before each piece [BT / Q][NC][32] float4
+    // a warp's floats: delta, u, ds, slope, q1, x [BT][WC] each; the block's checkpoint and the states before its
+    // other pieces [BT / Q][NC][32] float4
     static constexpr int AR = BT * WC;
     static constexpr int WARP = 6 * AR + BT / Q * NC * 32 * 4;
     static constexpr size_t raw_bytes = sizeof(E) * 4 * BT * CH;  // x, dt, dy, z as they come
-    // B and C of two blocks [2][BT][2 NP]; the warps' dB and dC [NW][BT][2 NP]
-    static constexpr size_t smem = 4 * (size_t)(NW * WARP + 2 * BT * 2 * NP + NW * BT * 2 * NP) + raw_bytes;
+    // B and C of two blocks, every value twice, [2][BT][4 NP]; the warps' dB and dC [NW][BT][2 NP]
+    static constexpr size_t smem = 4 * (size_t)(NW * WARP + 2 * BT * 4 * NP + NW * BT * 2 * NP) + raw_bytes;
 };
 
 // Sums over a channel's K adjacent lanes of the lane's four channels; lane k ends
@@ -123,70 +132,92 @@ __device__ __forceinline__ void sum_channels8(float (&v)[8], int lane, int& firs
     }
 }
 
-__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+// the lane's channels, in pairs
+__device__ __forceinline__ void lds_pairs(F2 (&f)[P], const float* p) {
+    f2_load2(p, f[0], f[1]);
+}
+// four values that lie there twice each
+__device__ __forceinline__ void lds_dup(F2 (&f)[4], const float* p) {
+    f2_load2(p, f[0], f[1]);
+    f2_load2(p + 4, f[2], f[3]);
+}
 
 template <typename E, int K>
-__global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) {
+__global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p) {
     using Sh = BShape<E, K>;
     constexpr int WC = Sh::WC, CH = Sh::CH, NP = Sh::NP, AR = Sh::AR;
     constexpr int TPS = 32 / WC;  // tokens that a warp stages at a time, a channel a lane
-    constexpr int VEC = 16 / sizeof(E), VR = WC / VEC;
-    static_assert(K >= 4 && K <= 16, "a lane's four channels spread over four lanes at least");
+    constexpr int VEC = 16 / sizeof(E), VR = WC / VEC;  // 16-byte vectors a row
+    static_assert(K >= 4 && K <= 16 && NC == 4, "a lane's four channels spread over four lanes at least");
     extern __shared__ float4 smem4[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = lane % K, cg = lane / K;
     float* wb = reinterpret_cast<float*>(smem4) + warp * Sh::WARP;
     float *dl = wb, *uu = wb + AR, *dsv = wb + 2 * AR, *slope = wb + 3 * AR, *q1 = wb + 4 * AR, *xx = wb + 5 * AR;
     float4* hs = reinterpret_cast<float4*>(wb + 6 * AR);                       // [BT / Q][NC][32]
-    float* bcs = reinterpret_cast<float*>(smem4) + NW * Sh::WARP;              // [2][BT][2 NP]
-    float* slab = bcs + 2 * BT * 2 * NP;                                       // [NW][BT][2 NP]
+    float* bcs = reinterpret_cast<float*>(smem4) + NW * Sh::WARP;              // [2][BT][4 NP]
+    float* slab = bcs + 2 * BT * 4 * NP;                                       // [NW][BT][2 NP]
     E* raw = reinterpret_cast<E*>(slab + NW * BT * 2 * NP) + warp * 4 * BT * WC;  // [x, dt, dy, z][BT][WC]
     const int grp = blockIdx.x / p.tiles, cend = (grp + 1) * p.per;
     const int wc0 = grp * p.per + (blockIdx.x % p.tiles) * CH + warp * WC;  // the warp's first channel
     const int c4 = wc0 + cg * NC;                                          // the lane's first channel
     const int s = blockIdx.y, t0 = s * p.seg, te = min(p.T, t0 + p.seg);
 
-    F2 A2[NC][2], dh[NC][2], h[NC][2], dA[NC][2];
-    auto load_state = [&](F2 (&f)[NC][2], const float* src, int64_t row) {  // src [rows, ch, N] or null
+    // two channels side by side: delta, u and ds of both are one operand as they are read
+    F2 A2[P][NS], dh[P][NS], h[P][NS], dA[P][NS];
+    const bool vec = p.N % 4 == 0;
+    auto load_state = [&](F2 (&f)[P][NS], const float* src, int64_t row) {  // src [rows, ch, N] or null
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            float* q = reinterpret_cast<float*>(f[i]);
-            const bool ok = src && c4 + i < cend;
-            const float* g = src + (row * p.ch + c4 + i) * p.N + k * NS;
-            if (p.N % 4 == 0) {
-                const float4 v = ok && k * NS < p.N ? __ldg(reinterpret_cast<const float4*>(g)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
+        for (int i = 0; i < P; ++i) {
+            const int c = c4 + 2 * i;
+            const bool in0 = src && c < cend, in1 = src && c + 1 < cend;
+            const float* g = src + (row * p.ch + c) * p.N + k * NS;
+            if (vec) {
+                const bool ok = k * NS < p.N;
+                const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 v0 = ok && in0 ? __ldg(reinterpret_cast<const float4*>(g)) : z4;
+                const float4 v1 = ok && in1 ? __ldg(reinterpret_cast<const float4*>(g + p.N)) : z4;
+                f[i][0] = f2(v0.x, v1.x);
+                f[i][1] = f2(v0.y, v1.y);
+                f[i][2] = f2(v0.z, v1.z);
+                f[i][3] = f2(v0.w, v1.w);
             } else {
 #pragma unroll
-                for (int n = 0; n < NS; ++n) q[n] = ok && k * NS + n < p.N ? __ldg(g + n) : 0.f;
+                for (int n = 0; n < NS; ++n) {
+                    const bool ok = k * NS + n < p.N;
+                    f[i][n] = f2(ok && in0 ? __ldg(g + n) : 0.f, ok && in1 ? __ldg(g + p.N + n) : 0.f);
+                }
             }
         }
     };
-    auto store_state = [&](float* dst, int64_t row, const F2 (&f)[NC][2]) {
+    auto store_state = [&](float* dst, int64_t row, const F2 (&f)[P][NS]) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const float* q = reinterpret_cast<const float*>(f[i]);
-            if (c4 + i < cend)
+        for (int i = 0; i < P; ++i) {
+            const int c = c4 + 2 * i;
+            float* g = dst + (row * p.ch + c) * p.N + k * NS;
 #pragma unroll
-                for (int n = 0; n < NS; ++n)
-                    if (k * NS + n < p.N) dst[(row * p.ch + c4 + i) * p.N + k * NS + n] = q[n];
+            for (int n = 0; n < NS; ++n)
+                if (k * NS + n < p.N) {
+                    if (c < cend) g[n] = f[i][n].x();
+                    if (c + 1 < cend) g[p.N + n] = f[i][n].y();
+                }
         }
     };
     auto pass_empty = [&](int m) {  // an empty sequence's final state is its initial one
         if (!p.dh0) return;
-        F2 f[NC][2];
+        F2 f[P][NS];
         load_state(f, p.dhf, m);
         store_state(p.dh0, m, f);
     };
     load_state(A2, p.A_log, 0);
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int st = k * NS + 2 * q;
-            const bool ok = c4 + i < cend;
-            A2[i][q].x = ok && st < p.N ? -expf(A2[i][q].x) * kLog2e : 0.f;
-            A2[i][q].y = ok && st + 1 < p.N ? -expf(A2[i][q].y) * kLog2e : 0.f;
-            dh[i][q] = h[i][q] = dA[i][q] = F2{0.f, 0.f};
+        for (int n = 0; n < NS; ++n) {
+            const bool ok = k * NS + n < p.N;
+            const int c = c4 + 2 * i;
+            A2[i][n] = f2(ok && c < cend ? -expf(A2[i][n].x()) * kLog2e : 0.f,
+                          ok && c + 1 < cend ? -expf(A2[i][n].y()) * kLog2e : 0.f);
+            dh[i][n] = h[i][n] = dA[i][n] = f2_dup(0.f);
         }
     // the gradient of the state behind the segment's last token
     if (p.T > 0) {
@@ -198,13 +229,15 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) 
             const int je = (min(end, p.T) - 1) / p.seg;
             load_state(dh, p.G, je);
             for (int j = je - 1; j > s; --j) {
-                F2 g[NC][2];
+                F2 g[P][NS];
                 load_state(g, p.G, j);
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const F2 d = f2_dup(c4 + i < cend ? __ldg(p.sd + (int64_t)j * p.ch + c4 + i) : 0.f);
+                for (int i = 0; i < P; ++i) {
+                    const int c = c4 + 2 * i;
+                    const float* sd = p.sd + (int64_t)j * p.ch + c;
+                    const F2 d = f2(c < cend ? __ldg(sd) : 0.f, c + 1 < cend ? __ldg(sd + 1) : 0.f);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) dh[i][q] = f2_fma(f2_exp2(f2_mul(d, A2[i][q])), dh[i][q], g[i][q]);
+                    for (int q = 0; q < NS; ++q) dh[i][q] = f2_fma(f2_exp2(f2_mul(d, A2[i][q])), dh[i][q], g[i][q]);
                 }
             }
         }
@@ -220,10 +253,8 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) 
     const float sbias = p.dt_bias && wc0 + sch < cend ? __ldg(p.dt_bias + wc0 + sch) : 0.f;
     const float Do = p.D && wc0 + och < cend ? __ldg(p.D + wc0 + och) : 0.f;
     float aD = 0.f, aT = 0.f;
-    E* dxp = static_cast<E*>(p.dx) + wc0 + och;
-    E* dtp = static_cast<E*>(p.ddt) + wc0 + och;
-    E* dzp = static_cast<E*>(p.dz) + wc0 + och;
 
+    int cks = 0;  // the checkpoint that is in place
     auto copy = [&](int tb) {
 #pragma unroll
         for (int it = lane; it < BT * VR; it += 32) {
@@ -240,6 +271,30 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) 
         }
         cp_async_commit();
     };
+    // the checkpoint before a block: each lane copies its own channels' states and reads them back
+    const int ckq = c4 + NC <= cend ? NC : (c4 < cend ? cend - c4 : 0);  // its channels that exist
+    auto fetch_state = [&](int tb) {
+        if (vec) {
+            const float* g = p.ckpt + ((int64_t)(tb / BT) * p.ch + (ckq ? c4 : 0)) * p.N;
+            const bool ok = k * NS < p.N;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                cp_async16(hs + i * 32 + lane, g + (i < ckq ? (int64_t)i * p.N : 0) + (ok ? k * NS : 0), ok && i < ckq ? 16 : 0);
+        }
+        cp_async_commit();
+        cks = tb / BT;
+    };
+    auto block_state = [&]() {
+        if (!vec) return load_state(h, p.ckpt, cks);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float4 v0 = hs[2 * i * 32 + lane], v1 = hs[(2 * i + 1) * 32 + lane];
+            h[i][0] = f2(v0.x, v1.x);
+            h[i][1] = f2(v0.y, v1.y);
+            h[i][2] = f2(v0.z, v1.z);
+            h[i][3] = f2(v0.w, v1.w);
+        }
+    };
     constexpr int PER = BT * 2 * NP / NT;
     E bc[PER];
     auto fetch_bc = [&](int tb) {
@@ -254,25 +309,47 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) 
     };
     auto put_bc = [&](int b) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) bcs[b * BT * 2 * NP + tid + i * NT] = Elem<E>::to_f(bc[i]);
+        for (int i = 0; i < PER; ++i) {
+            const float v = Elem<E>::to_f(bc[i]);
+            reinterpret_cast<float2*>(bcs)[b * BT * 2 * NP + tid + i * NT] = make_float2(v, v);
+        }
+    };
+
+    // the outputs of the lane's channel at row r of the block, from its sums over the states
+    auto outputs = [&](int r, int tb, float dus, float dds, float y) {
+        const int i = r * WC + och;
+        if (writer && tb + r < te) {
+            const int64_t off = (int64_t)(tb + r) * p.ch + wc0 + och;
+            const float g = dsv[i], xv = xx[i];
+            const float gd = fmaf(kLn2, dds, dus * xv) * slope[i];
+            static_cast<E*>(p.dx)[off] = Elem<E>::from_f(fmaf(dus, dl[i], Do * g));
+            static_cast<E*>(p.ddt)[off] = Elem<E>::from_f(gd);
+            if (p.z) static_cast<E*>(p.dz)[off] = Elem<E>::from_f(fmaf(Do, xv, y) * q1[i]);
+            aD = fmaf(g, xv, aD);
+            aT += gd;
+        }
     };
 
     const int nblk = (te - t0 + BT - 1) / BT;
     if (nblk > 0) {
         copy(t0 + (nblk - 1) * BT);
+        fetch_state(t0 + (nblk - 1) * BT);
         fetch_bc(t0 + (nblk - 1) * BT);
         put_bc(0);
         __syncthreads();
     }
     int buf = 0;
+    // the sequence that the walk is in, and its start
+    int sq = nblk > 0 ? seq_of(p.cu, p.num_seqs, te - 1) : 0;
+    int cur = nblk > 0 ? min(__ldg(p.cu + sq), te - 1) : -1;
     for (int b = nblk - 1; b >= 0; --b, buf ^= 1) {
         const int tb = t0 + b * BT;
-        load_state(h, p.ckpt, tb / BT);
         uint32_t starts = 0;  // which of the block's tokens start a sequence
-        {
-            const int t = tb + lane;
-            const bool st = lane < BT && t < te && __ldg(p.cu + seq_of(p.cu, p.num_seqs, t)) == t;
-            starts = __ballot_sync(0xffffffffu, st);
+        while (cur >= tb) {
+            if (cur < te) starts |= 1u << (cur - tb);
+            do --sq;
+            while (sq >= 0 && __ldg(p.cu + sq) == cur);
+            cur = sq >= 0 ? min(__ldg(p.cu + sq), cur - 1) : -1;
         }
         cp_async_wait_all();
         __syncwarp();
@@ -301,71 +378,75 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) 
             copy(tb - BT);
             fetch_bc(tb - BT);
         }
-        const float* bcb = bcs + buf * BT * 2 * NP + k * NS;
+        block_state();
+        const float* bcb = bcs + buf * BT * 4 * NP + 2 * k * NS;
         const int co = cg * NC;
         // forward: the state before every piece
 #pragma unroll 1
-        for (int q = 0; q < BT / Q; ++q) {
-#pragma unroll
-            for (int i = 0; i < NC; ++i) hs[(q * NC + i) * 32 + lane] = make_float4(h[i][0].x, h[i][0].y, h[i][1].x, h[i][1].y);
-            if (q == BT / Q - 1) break;
+        for (int q = 0; q < BT / Q - 1; ++q) {
+            const bool any = starts >> (q * Q) & (1u << Q) - 1;
 #pragma unroll
             for (int e = 0; e < Q; ++e) {
                 const int r = q * Q + e;
-                if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
-                const float4 d4 = lds4(dl + r * WC + co), u4 = lds4(uu + r * WC + co), b4 = lds4(bcb + r * 2 * NP);
-                const float d_[4] = {d4.x, d4.y, d4.z, d4.w}, u_[4] = {u4.x, u4.y, u4.z, u4.w};
-                const F2 bb[2] = {{b4.x, b4.y}, {b4.z, b4.w}};
+                if (any)
+                    if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
+                F2 d[P], u[P], bb[NS];
+                lds_pairs(d, dl + r * WC + co);
+                lds_pairs(u, uu + r * WC + co);
+                lds_dup(bb, bcb + r * 4 * NP);
 #pragma unroll
-                for (int i = 0; i < NC; ++i)
+                for (int i = 0; i < P; ++i)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        h[i][j] = f2_fma(f2_dup(u_[i]), bb[j], f2_mul(f2_decay(f2_dup(d_[i]), A2[i][j]), h[i][j]));
+                    for (int n = 0; n < NS; ++n) h[i][n] = f2_fma(u[i], bb[n], f2_mul(f2_decay(d[i], A2[i][n]), h[i][n]));
             }
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                f2_store2(hs + ((q + 1) * NC + i) * 32 + lane, h[i >> 1][(i & 1) * 2], h[i >> 1][(i & 1) * 2 + 1]);
         }
         // the pieces, last to first
 #pragma unroll 1
         for (int q = BT / Q - 1; q >= 0; --q) {
-            F2 a[Q][NC][2], w[Q][NC][2];
+            const bool any = starts >> (q * Q) & (1u << Q) - 1;
+            F2 a[Q][P][NS], w[Q][P][NS];
             float ys[Q];
+            if (q) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                const float4 v = hs[(q * NC + i) * 32 + lane];
-                h[i][0] = F2{v.x, v.y};
-                h[i][1] = F2{v.z, v.w};
+                for (int i = 0; i < NC; ++i)
+                    f2_load2(reinterpret_cast<const float*>(hs + (q * NC + i) * 32 + lane), h[i >> 1][(i & 1) * 2],
+                             h[i >> 1][(i & 1) * 2 + 1]);
+            } else {
+                block_state();
+                if (b > 0) fetch_state(tb - BT);  // the slot is free, and the piece's work lies before the next block
             }
             float* sl = slab + warp * BT * 2 * NP + k * NS;
 #pragma unroll
             for (int e2 = 0; e2 < Q; e2 += 2) {
                 float v8[8];
+                F2 yv[2][P];
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
                     const int e = e2 + o, r = q * Q + e;
-                    if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
-                    const float4 d4 = lds4(dl + r * WC + co), u4 = lds4(uu + r * WC + co), g4 = lds4(dsv + r * WC + co);
-                    const float4 b4 = lds4(bcb + r * 2 * NP), c4v = lds4(bcb + r * 2 * NP + NP);
-                    const float d_[4] = {d4.x, d4.y, d4.z, d4.w}, u_[4] = {u4.x, u4.y, u4.z, u4.w};
-                    const float g_[4] = {g4.x, g4.y, g4.z, g4.w};
-                    const F2 bb[2] = {{b4.x, b4.y}, {b4.z, b4.w}}, cc[2] = {{c4v.x, c4v.y}, {c4v.z, c4v.w}};
-                    F2 dc[2];
-                    float yv[NC];
+                    if (any)
+                        if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
+                    F2 d[P], u[P], g[P], bb[NS], cc[NS], t[NS];
+                    lds_pairs(d, dl + r * WC + co);
+                    lds_pairs(u, uu + r * WC + co);
+                    lds_pairs(g, dsv + r * WC + co);
+                    lds_dup(bb, bcb + r * 4 * NP);
+                    lds_dup(cc, bcb + r * 4 * NP + 2 * NP);
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) {
+                    for (int i = 0; i < P; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            a[e][i][j] = f2_decay(f2_dup(d_[i]), A2[i][j]);
-                            w[e][i][j] = f2_mul(a[e][i][j], h[i][j]);
-                            h[i][j] = f2_fma(f2_dup(u_[i]), bb[j], w[e][i][j]);
-                            dc[j] = i ? f2_fma(f2_dup(g_[i]), h[i][j], dc[j]) : f2_mul(f2_dup(g_[i]), h[i][j]);
+                        for (int n = 0; n < NS; ++n) {
+                            a[e][i][n] = f2_decay(d[i], A2[i][n]);
+                            w[e][i][n] = f2_mul(a[e][i][n], h[i][n]);
+                            h[i][n] = f2_fma(u[i], bb[n], w[e][i][n]);
+                            t[n] = i ? f2_fma(g[i], h[i][n], t[n]) : f2_mul(g[i], h[i][n]);
+                            yv[o][i] = n ? f2_fma(h[i][n], cc[n], yv[o][i]) : f2_mul(h[i][n], cc[n]);
                         }
-                        const F2 t = f2_fma(h[i][1], cc[1], f2_mul(h[i][0], cc[0]));
-                        yv[i] = t.x + t.y;
-                    }
-                    ys[e] = sum_states<K>(yv[0], yv[1], yv[2], yv[3], k);
-                    v8[4 * o] = dc[0].x;
-                    v8[4 * o + 1] = dc[0].y;
-                    v8[4 * o + 2] = dc[1].x;
-                    v8[4 * o + 3] = dc[1].y;
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) v8[4 * o + n] = f2_sum(t[n]);
+                    ys[e] = sum_states<K>(yv[o][0].x(), yv[o][0].y(), yv[o][1].x(), yv[o][1].y(), k);
                 }
                 int first;
                 sum_channels8<K>(v8, lane, first);
@@ -376,57 +457,39 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) 
 #pragma unroll
             for (int e2 = Q - 2; e2 >= 0; e2 -= 2) {
                 float v8[8];
+                F2 du[2][P], dd[2][P];
 #pragma unroll
                 for (int o = 1; o >= 0; --o) {
                     const int e = e2 + o, r = q * Q + e, t = tb + r;
-                    const float4 d4 = lds4(dl + r * WC + co), u4 = lds4(uu + r * WC + co), g4 = lds4(dsv + r * WC + co);
-                    const float4 b4 = lds4(bcb + r * 2 * NP), c4v = lds4(bcb + r * 2 * NP + NP);
-                    const float d_[4] = {d4.x, d4.y, d4.z, d4.w}, u_[4] = {u4.x, u4.y, u4.z, u4.w};
-                    const float g_[4] = {g4.x, g4.y, g4.z, g4.w};
-                    const F2 bb[2] = {{b4.x, b4.y}, {b4.z, b4.w}}, cc[2] = {{c4v.x, c4v.y}, {c4v.z, c4v.w}};
-                    F2 db[2];
-                    float du[NC], dd[NC];
+                    F2 d[P], u[P], g[P], bb[NS], cc[NS], tt[NS];
+                    lds_pairs(d, dl + r * WC + co);
+                    lds_pairs(u, uu + r * WC + co);
+                    lds_pairs(g, dsv + r * WC + co);
+                    lds_dup(bb, bcb + r * 4 * NP);
+                    lds_dup(cc, bcb + r * 4 * NP + 2 * NP);
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        F2 m[2];
+                    for (int i = 0; i < P; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            dh[i][j] = f2_fma(f2_dup(g_[i]), cc[j], dh[i][j]);
-                            db[j] = i ? f2_fma(f2_dup(u_[i]), dh[i][j], db[j]) : f2_mul(f2_dup(u_[i]), dh[i][j]);
-                            m[j] = f2_mul(dh[i][j], w[e][i][j]);
-                            dA[i][j] = f2_fma(f2_dup(d_[i]), m[j], dA[i][j]);
+                        for (int n = 0; n < NS; ++n) {
+                            dh[i][n] = f2_fma(g[i], cc[n], dh[i][n]);
+                            tt[n] = i ? f2_fma(u[i], dh[i][n], tt[n]) : f2_mul(u[i], dh[i][n]);
+                            du[o][i] = n ? f2_fma(dh[i][n], bb[n], du[o][i]) : f2_mul(dh[i][n], bb[n]);
+                            const F2 m = f2_mul(dh[i][n], w[e][i][n]);
+                            dA[i][n] = f2_fma(d[i], m, dA[i][n]);
+                            dd[o][i] = n ? f2_fma(m, A2[i][n], dd[o][i]) : f2_mul(m, A2[i][n]);
+                            dh[i][n] = f2_mul(dh[i][n], a[e][i][n]);
                         }
-                        const F2 t1 = f2_fma(dh[i][1], bb[1], f2_mul(dh[i][0], bb[0]));
-                        const F2 t2 = f2_fma(m[1], A2[i][1], f2_mul(m[0], A2[i][0]));
-                        du[i] = t1.x + t1.y;
-                        dd[i] = t2.x + t2.y;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) dh[i][j] = f2_mul(dh[i][j], a[e][i][j]);
-                    }
-                    v8[4 * o] = db[0].x;
-                    v8[4 * o + 1] = db[0].y;
-                    v8[4 * o + 2] = db[1].x;
-                    v8[4 * o + 3] = db[1].y;
-                    const float dus = sum_states<K>(du[0], du[1], du[2], du[3], k);
-                    const float dds = sum_states<K>(dd[0], dd[1], dd[2], dd[3], k);
-                    if (starts >> r & 1) {  // the token starts a sequence: dh is the gradient of its h0
+                    for (int n = 0; n < NS; ++n) v8[4 * o + n] = f2_sum(tt[n]);
+                    if (any && (starts >> r & 1)) {  // the token starts a sequence: dh is the gradient of its h0
                         const int n = seq_of(p.cu, p.num_seqs, t);
                         if (p.dh0) store_state(p.dh0, n, dh);
                         int m = n - 1;
                         while (m >= 0 && __ldg(p.cu + m) == t) pass_empty(m--);
                         load_state(dh, m >= 0 ? p.dhf : nullptr, m >= 0 ? m : 0);
                     }
-                    // the outputs of the lane's channel
-                    const int i = r * WC + och;
-                    if (writer && t < te) {
-                        const float g = dsv[i], xv = xx[i];
-                        const float gd = fmaf(kLn2, dds, dus * xv) * slope[i];
-                        dxp[(int64_t)t * p.ch] = Elem<E>::from_f(fmaf(dus, dl[i], Do * g));
-                        dtp[(int64_t)t * p.ch] = Elem<E>::from_f(gd);
-                        if (p.z) dzp[(int64_t)t * p.ch] = Elem<E>::from_f(fmaf(Do, xv, ys[e]) * q1[i]);
-                        aD = fmaf(g, xv, aD);
-                        aT += gd;
-                    }
+                    outputs(r, tb, sum_states<K>(du[o][0].x(), du[o][0].y(), du[o][1].x(), du[o][1].y(), k),
+                            sum_states<K>(dd[o][0].x(), dd[o][0].y(), dd[o][1].x(), dd[o][1].y(), k), ys[e]);
                 }
                 int first;
                 sum_channels8<K>(v8, lane, first);
@@ -448,15 +511,15 @@ __global__ void __launch_bounds__(NT, 2) scan_bwd_kernel(const ScanBwdParams p) 
         __syncthreads();  // the slabs are read
     }
     // the parameters' partial gradients of this segment
-    float* par = p.par + (int64_t)s * p.ch * (p.N + 2);
+    float* pg = p.par + (int64_t)s * p.ch * (p.N + 2);
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < P; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) dA[i][j] = f2_mul(f2_mul(dA[i][j], A2[i][j]), f2_dup(kLn2));
-    store_state(par, 0, dA);
+        for (int n = 0; n < NS; ++n) dA[i][n] = f2_mul(f2_mul(dA[i][n], A2[i][n]), f2_dup(kLn2));
+    store_state(pg, 0, dA);
     if (writer) {
-        par[(int64_t)p.ch * p.N + wc0 + och] = aD;
-        par[(int64_t)p.ch * p.N + p.ch + wc0 + och] = aT;
+        pg[(int64_t)p.ch * p.N + wc0 + och] = aD;
+        pg[(int64_t)p.ch * p.N + p.ch + wc0 + och] = aT;
     }
 }
 
@@ -481,11 +544,12 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const float* bc, int T, in
 int lanes_of(int N) { return N <= 16 ? 4 : (N <= 32 ? 8 : 16); }
 int block_channels(int N) { return NW * NC * 32 / lanes_of(N); }
 
-// Segments: enough blocks for two resident ones an SM, 64 tokens or more.
+// Segments: two waves of resident blocks (one wave leaves the launch before, whose
+// blocks cover more channels, too few blocks to fill the SMs), 64 tokens or more.
 void segments(int T, int ch, int N, int groups, int& tiles, int& seg, int& S) {
     const int per = ch / groups, cb = block_channels(N);
     tiles = (per + cb - 1) / cb;
-    int64_t want = (int64_t)device_sm_count() * 2 / ((int64_t)groups * tiles);
+    int64_t want = (int64_t)device_sm_count() * OCC * 2 / ((int64_t)groups * tiles);
     const int64_t most = (T + 63) / 64;
     if (want > most) want = most;
     if (want < 1) want = 1;

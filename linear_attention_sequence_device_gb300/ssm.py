@@ -183,8 +183,8 @@ def _scan_args(x, dt, A_log, B, C, D, z, dt_bias):
 
 
 def ssm_scan_ckpt_shape(T, channels, d_state):
-    """Shape of the forward's checkpoints: the states before every 16th token."""
-    return ((T + 15) // 16, channels, d_state)
+    """Shape of the forward's checkpoints: the states before every 8th token."""
+    return ((T + 7) // 8, channels, d_state)
 
 
 def ssm_scan_workspace_size(T, channels, d_state, groups=1) -> int:

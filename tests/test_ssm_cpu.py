@@ -127,7 +127,7 @@ def test_conv_refusals(lib):
 def test_scan_refusals(lib):
     need = lib.gdn_ssm_scan_workspace_size(128, 64, 16, 2)
     assert need > 0 and need % 256 == 0
-    assert lib.gdn_ssm_scan_ckpt_floats(65, 64, 16) == 5 * 64 * 16 and lib.gdn_ssm_scan_ckpt_floats(0, 64, 16) == 0
+    assert lib.gdn_ssm_scan_ckpt_floats(65, 64, 16) == 9 * 64 * 16 and lib.gdn_ssm_scan_ckpt_floats(0, 64, 16) == 0
     for bad in ((128, 64, 65, 2), (128, 64, 0, 2), (128, 24, 16, 2), (128, 64, 16, 3), (-1, 64, 16, 2)):
         assert lib.gdn_ssm_scan_workspace_size(*bad) == 0 and lib.gdn_ssm_scan_bwd_workspace_size(*bad) == 0
 
