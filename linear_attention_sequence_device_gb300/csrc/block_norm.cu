@@ -8,14 +8,27 @@
 //   dp   = dr scale sigmoid(gate),  dgate = dr scale p sg (1 - sg),  dscale = sum dr sg p
 //   do   = (w_post dp - o^ mean(w_post dp o^)) / rms(o)
 //   dw_pre = sum dy r^,  dw_post = sum dp o^
+// The mean in do needs dr, which needs the mean of the pre norm: its sum is taken
+// apart into three that do not, so that a row has one reduction:
+//   sum_i q_i dr_i = sum q dr' + (sum q w_pre dy - mean(w_pre dy r^) sum q r^) / rms(r'),
+//   q = w_post scale sg o^.
+//
 // HBM-bound: each array is read or written once.  A block works on one row at a
-// time, eight columns per thread and vector, and keeps the row in registers
-// between the two reductions; the blocks are persistent, so that the backward's
-// column sums stay in registers over all of a block's rows and leave as one
-// partial row per block, summed in block order by a second kernel.
+// time, eight columns per thread and vector, and the forward
+// keeps the row in registers between its reductions.  The blocks of the backward
+// are persistent, so that its column sums stay in registers over all of a block's
+// rows and leave as one partial row per block, summed in block order by a second
+// kernel; its rows come by asynchronous copies into a ring in shared memory that
+// every thread fills and reads alone, once before and once behind the reduction.
+#include "chunk_common.cuh"
 #include "ssm_common.cuh"
 
+#include <type_traits>
+
 namespace gdn {
+
+gdn_status set_smem_attr(const void* func, size_t bytes);
+
 namespace {
 
 struct NormParams {
@@ -30,31 +43,61 @@ struct NormParams {
     void* d_o; void* dgate; void* dres; float* part;
 };
 
-// Sums over the block; the scratch alternates so that one barrier a call is enough.
-template <int NV>
-__device__ __forceinline__ void block_sum(float (&v)[NV], float* scratch) {
+// A sum over the block, in one order for all threads: lane w of every warp takes
+// warp w's sum, then the lanes are added.  Callers alternate the scratch [32], so
+// that one barrier a call is enough.
+__device__ __forceinline__ float block_sum(float v, float* scratch) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int off = 16; off; off >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
+    for (int off = 16; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-        for (int i = 0; i < NV; ++i) scratch[w * NV + i] = v[i];
+    if (nw == 1) return v;
+    if (lane == 0) scratch[w] = v;
     __syncthreads();
+    v = lane < nw ? scratch[lane] : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float s = 0.f;
-        for (int k = 0; k < nw; ++k) s += scratch[k * NV + i];
-        v[i] = s;
+    for (int off = 8; off; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// Eight sums over the block's at most 16 warps, likewise.  Halving exchanges leave
+// each lane with the value of its three low bits (seven exchanges instead of the
+// forty that whole sums of eight values would take); scratch [16][8].
+__device__ __forceinline__ void block_sum8(float (&v)[8], float* scratch) {
+    const int nw = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 1, cnt = 4; m < 8; m <<= 1, cnt >>= 1) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < cnt) {
+                const float snd = up ? v[2 * i] : v[2 * i + 1], kp = up ? v[2 * i + 1] : v[2 * i];
+                v[i] = kp + __shfl_xor_sync(0xffffffffu, snd, m);
+            }
     }
+    float t = v[0];
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    if (nw > 1) {
+        if (lane < 8) scratch[w * 8 + lane] = t;
+        __syncthreads();
+        t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int u = 4 * i + (lane >> 3);
+            if (u < nw) t += scratch[u * 8 + (lane & 7)];
+        }
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, t, i);
 }
 
 constexpr int kMaxThreads = 512;
 
 template <typename E, typename R, int VPT>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams p) {
-    __shared__ float red[2][kMaxThreads / 32];
+    __shared__ float red[2][32];
     const int nv = p.W >> 3;
     const float inv = 1.f / (float)p.W;
     const E* wpost = static_cast<const E*>(p.w_post);
@@ -64,7 +107,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams 
         const E* g = p.gate ? static_cast<const E*>(p.gate) + (int64_t)row * p.ldg : nullptr;
         const R* r = static_cast<const R*>(p.res) + (int64_t)row * p.W;
         float b[VPT][8], rv[VPT][8];
-        float ss[1] = {0.f};
+        float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
@@ -72,15 +115,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams 
                 load8(o + 8 * v, b[j]);
                 load8_rw(r + 8 * v, rv[j]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss[0] = fmaf(b[j][i], b[j][i], ss[0]);
+                for (int i = 0; i < 8; ++i) ss = fmaf(b[j][i], b[j][i], ss);
             }
         }
         float r1 = 1.f;
         if (wpost) {
-            block_sum<1>(ss, red[0]);
-            r1 = 1.f / sqrtf(ss[0] * inv + p.eps);
+            r1 = 1.f / sqrtf(block_sum(ss, red[0]) * inv + p.eps);
         }
-        float sr[1] = {0.f};
+        float sr = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
@@ -104,13 +146,12 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams 
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     rv[j][i] += b[j][i];
-                    sr[0] = fmaf(rv[j][i], rv[j][i], sr[0]);
+                    sr = fmaf(rv[j][i], rv[j][i], sr);
                 }
                 store8(static_cast<R*>(p.res_out) + (int64_t)row * p.W + 8 * v, rv[j]);
             }
         }
-        block_sum<1>(sr, red[1]);
-        const float r2 = 1.f / sqrtf(sr[0] * inv + p.eps);
+        const float r2 = 1.f / sqrtf(block_sum(sr, red[1]) * inv + p.eps);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
@@ -126,119 +167,204 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams 
     }
 }
 
+// What the backward reads of a row: res_out, dres_out (R), dy, o, gate (E).
 template <typename E, typename R, int VPT>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams p) {
-    __shared__ float red[2][3 * kMaxThreads / 32];
-    const int nv = p.W >> 3;
+constexpr size_t row_bytes(int threads) {
+    return (size_t)threads * VPT * (2 * 8 * sizeof(R) + 3 * 8 * sizeof(E));
+}
+constexpr size_t kRingBytes = 200 << 10;  // of an SM's shared memory, for the rings of its blocks
+constexpr int kMaxStages = 4;
+
+// RING: rows come through the ring of `stages` rows; else (rows too wide for two
+// of them) they are read where they are used.
+template <typename E, typename R, int VPT, bool RING>
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams p, int stages) {
+    extern __shared__ uint4 ring[];
+    __shared__ float red[2][16 * 8];
+    constexpr int VE = 8 * sizeof(E) / 16, VRS = 8 * sizeof(R) / 16;  // 16-byte pieces of eight elements
+    const int nv = p.W >> 3, nt = blockDim.x, tid = threadIdx.x;
     const float inv = 1.f / (float)p.W;
     const E* wpost = static_cast<const E*>(p.w_post);
     const E* wpre = static_cast<const E*>(p.w_pre);
-    float a_pre[VPT][8], a_post[VPT][8], a_sc[VPT][8];
+    const R* res = static_cast<const R*>(p.res);
+    const R* dro = static_cast<const R*>(p.dres_out);
+    const E* dy = static_cast<const E*>(p.dy);
+    const E* o = static_cast<const E*>(p.o);
+    const E* gate = static_cast<const E*>(p.gate);
+    constexpr int PIECES = VPT * (2 * VRS + 3 * VE);
+    auto piece = [&](int st, int q) { return ring + ((size_t)st * PIECES + q) * nt + tid; };
+    auto copy8 = [&](int st, int q, const void* src, int pieces) {
+        for (int i = 0; i < pieces; ++i) cp_async16(piece(st, q + i), static_cast<const uint4*>(src) + i, 16);
+    };
+    auto fetch = [&](int64_t row, int st) {
+        if (row < p.T)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = tid + j * nt, q = j * (2 * VRS + 3 * VE);
+                if (v < nv) {
+                    copy8(st, q, res + row * p.W + 8 * v, VRS);
+                    if (dro) copy8(st, q + VRS, dro + row * p.W + 8 * v, VRS);
+                    copy8(st, q + 2 * VRS, dy + row * p.W + 8 * v, VE);
+                    copy8(st, q + 2 * VRS + VE, o + row * p.ldo + 8 * v, VE);
+                    if (gate) copy8(st, q + 2 * VRS + 2 * VE, gate + row * p.ldg + 8 * v, VE);
+                }
+            }
+        cp_async_commit();
+    };
+    auto take = [&](auto* src, int st, int q, F2 (&f)[4]) {
+        using X = typename std::remove_const<typename std::remove_pointer<decltype(src)>::type>::type;
+        if constexpr (RING) {
+            uint4 raw[8 * sizeof(X) / 16];
+#pragma unroll
+            for (int i = 0; i < (int)(8 * sizeof(X) / 16); ++i) raw[i] = *piece(st, q + i);
+            f2_load8(reinterpret_cast<const X*>(raw), f);
+        } else {
+            f2_load8(src, f);
+        }
+    };
+    // w_pre and f = w_post scale of vector v (1 where missing)
+    auto weights = [&](int v, F2 (&w)[4], F2 (&f)[4]) {
+        f2_load8(wpre + 8 * v, w);
+        if (wpost) f2_load8(wpost + 8 * v, f);
+        if (p.scale) {
+            F2 t[4];
+            f2_load8(p.scale + 8 * v, t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = wpost ? f2_mul(f[i], t[i]) : t[i];
+        } else if (!wpost) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = f2_dup(1.f);
+        }
+    };
+    constexpr bool KEEP = VPT == 1;  // a row's vector and the weights stay in registers; else they are read twice
+    F2 kw[4], kf[4], kr[5][4];  // used with KEEP
+    if (KEEP && tid < nv) weights(tid, kw, kf);
+    // sums over the rows: dy r^, and dr sg o^, of which dw_post and dscale are multiples by column
+    F2 a_pre[VPT][4], a_br[VPT][4];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a_pre[j][i] = a_post[j][i] = a_sc[j][i] = 0.f;
-    for (int row = blockIdx.x; row < p.T; row += gridDim.x) {
-        const int64_t base = (int64_t)row * p.W;
-        const E* o = static_cast<const E*>(p.o) + (int64_t)row * p.ldo;
-        const E* g = p.gate ? static_cast<const E*>(p.gate) + (int64_t)row * p.ldg : nullptr;
-        float ov[VPT][8], rv[VPT][8], gy[VPT][8];
-        float s3[3] = {0.f, 0.f, 0.f};  // sum r'^2, sum w_pre dy r', sum o^2
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < nv) {
-                float w[8];
-                load8(static_cast<const R*>(p.res) + base + 8 * v, rv[j]);
-                load8(static_cast<const E*>(p.dy) + base + 8 * v, gy[j]);
-                load8(o + 8 * v, ov[j]);
-                load8(wpre + 8 * v, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s3[0] = fmaf(rv[j][i], rv[j][i], s3[0]);
-                    s3[1] = fmaf(w[i] * gy[j][i], rv[j][i], s3[1]);
-                    s3[2] = fmaf(ov[j][i], ov[j][i], s3[2]);
-                }
-            }
+        for (int i = 0; i < 4; ++i) a_pre[j][i] = a_br[j][i] = f2_dup(0.f);
+    int st = 0, par = 0;
+    if (RING)
+        for (int i = 0; i < stages - 1; ++i) fetch((int64_t)blockIdx.x + (int64_t)i * gridDim.x, i);
+    for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x, par ^= 1) {
+        const int64_t base = row * p.W;
+        if (RING) {
+            fetch(row + (int64_t)(stages - 1) * gridDim.x, st == 0 ? stages - 1 : st - 1);
+            if (stages == 4) cp_async_wait<3>();
+            else if (stages == 3) cp_async_wait<2>();
+            else cp_async_wait<1>();
         }
-        block_sum<3>(s3, red[0]);
-        const float r2 = 1.f / sqrtf(s3[0] * inv + p.eps);
-        const float r1 = 1.f / sqrtf(s3[2] * inv + p.eps);
-        const float m2 = s3[1] * r2 * inv;  // mean(w_pre dy r^)
-        float s1[1] = {0.f};
-        float dp[VPT][8];
+        // x: res_out, dres_out, dy, o, sigmoid(gate)
+        auto row_vec = [&](int j, F2 (&x)[5][4]) {
+            const int q = j * (2 * VRS + 3 * VE), v = tid + j * nt;
+            take(res + base + 8 * v, st, q, x[0]);
+            if (dro) take(dro + base + 8 * v, st, q + VRS, x[1]);
+            else
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[1][i] = f2_dup(0.f);
+            take(dy + base + 8 * v, st, q + 2 * VRS, x[2]);
+            take(o + row * p.ldo + 8 * v, st, q + 2 * VRS + VE, x[3]);
+            if (gate) {
+                take(gate + row * p.ldg + 8 * v, st, q + 2 * VRS + 2 * VE, x[4]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4][i] = f2_sigmoid(x[4][i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4][i] = f2_dup(1.f);
+            }
+        };
+        // sums: r'^2, w_pre dy r', o^2, and of q = f sg o: q dr', q w_pre dy, q r'
+        F2 s6[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) s6[i] = f2_dup(0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < nv) {
-                float w[8], dr[8], sg[8], pv[8], t[8];
-                load8(wpre + 8 * v, w);
-                if (p.dres_out) load8_rw(static_cast<const R*>(p.dres_out) + base + 8 * v, dr);
-                else
+            if (tid + j * nt < nv) {
+                F2 x[5][4], w[4], f[4];
+                row_vec(j, x);
+                if constexpr (!KEEP) weights(tid + j * nt, w, f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dr[i] = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float rh = rv[j][i] * r2;
-                    a_pre[j][i] = fmaf(gy[j][i], rh, a_pre[j][i]);
-                    dr[i] += r2 * (w[i] * gy[j][i] - rh * m2);
-                }
-                store8(static_cast<R*>(p.dres) + base + 8 * v, dr);
-                if (g) {
-                    load8(g + 8 * v, t);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sg[i] = sigmoid_fast(t[i]);
-                }
-                if (wpost) load8(wpost + 8 * v, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) pv[i] = wpost ? ov[j][i] * r1 * w[i] : ov[j][i];
-                if (p.scale) {
-                    load8(p.scale + 8 * v, t);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        a_sc[j][i] = fmaf(g ? dr[i] * sg[i] : dr[i], pv[i], a_sc[j][i]);
-                        dr[i] *= t[i];
-                    }
-                }
-                if (g) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) t[i] = dr[i] * pv[i] * sg[i] * (1.f - sg[i]);
-                    store8(static_cast<E*>(p.dgate) + base + 8 * v, t);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dp[j][i] = g ? dr[i] * sg[i] : dr[i];
+                for (int i = 0; i < 4; ++i) {
+                    const F2 wd = f2_mul(KEEP ? kw[i] : w[i], x[2][i]);
+                    s6[0] = f2_fma(x[0][i], x[0][i], s6[0]);
+                    s6[1] = f2_fma(wd, x[0][i], s6[1]);
                     if (wpost) {
-                        const float oh = ov[j][i] * r1;
-                        a_post[j][i] = fmaf(dp[j][i], oh, a_post[j][i]);
-                        dp[j][i] *= w[i];
-                        s1[0] = fmaf(dp[j][i], oh, s1[0]);
-                        ov[j][i] = oh;
+                        const F2 fo = f2_mul(KEEP ? kf[i] : f[i], x[3][i]), qv = gate ? f2_mul(fo, x[4][i]) : fo;
+                        s6[2] = f2_fma(x[3][i], x[3][i], s6[2]);
+                        s6[3] = f2_fma(qv, x[1][i], s6[3]);
+                        s6[4] = f2_fma(qv, wd, s6[4]);
+                        s6[5] = f2_fma(qv, x[0][i], s6[5]);
                     }
                 }
+                if constexpr (KEEP)
+#pragma unroll
+                    for (int a = 0; a < 5; ++a)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) kr[a][i] = x[a][i];
             }
         }
-        block_sum<1>(s1, red[1]);
-        const float m1 = s1[0] * inv;
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = i < 6 ? f2_sum(s6[i]) : 0.f;
+        block_sum8(s, red[par]);
+        const float r2 = 1.f / sqrtf(s[0] * inv + p.eps);
+        const float r1 = wpost ? 1.f / sqrtf(s[2] * inv + p.eps) : 1.f;
+        const float m2 = s[1] * r2 * inv;                                            // mean(w_pre dy r^)
+        const float m1 = wpost ? r1 * inv * (s[3] + r2 * (s[4] - m2 * r2 * s[5])) : 0.f;  // mean(w_post dp o^)
+        const F2 R2 = f2_dup(r2), R1 = f2_dup(r1), M2 = f2_dup(-m2), M1 = f2_dup(-m1), one = f2_dup(1.f), neg = f2_dup(-1.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = tid + j * nt;
             if (v < nv) {
-                if (wpost)
+                F2 x[5][4], w[4], f[4], t[4], dp[4], dr[4];
+                if constexpr (KEEP) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) dp[j][i] = r1 * (dp[j][i] - ov[j][i] * m1);
-                store8(static_cast<E*>(p.d_o) + base + 8 * v, dp[j]);
+                    for (int a = 0; a < 5; ++a)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[a][i] = kr[a][i];
+                } else {
+                    row_vec(j, x);
+                    weights(v, w, f);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const F2 rh = f2_mul(x[0][i], R2), wi = KEEP ? kw[i] : w[i], fi = KEEP ? kf[i] : f[i];
+                    a_pre[j][i] = f2_fma(x[2][i], rh, a_pre[j][i]);
+                    dr[i] = f2_fma(R2, f2_fma(wi, x[2][i], f2_mul(rh, M2)), x[1][i]);
+                    const F2 oh = f2_mul(x[3][i], R1), dg = gate ? f2_mul(dr[i], x[4][i]) : dr[i];
+                    a_br[j][i] = f2_fma(dg, oh, a_br[j][i]);
+                    const F2 df = f2_mul(dg, fi);
+                    if (gate) t[i] = f2_mul(f2_mul(df, oh), f2_fma(x[4][i], neg, one));
+                    dp[i] = wpost ? f2_mul(R1, f2_fma(oh, M1, df)) : df;
+                }
+                f2_store8(static_cast<R*>(p.dres) + base + 8 * v, dr);
+                if (gate) f2_store8(static_cast<E*>(p.dgate) + base + 8 * v, t);
+                f2_store8(static_cast<E*>(p.d_o) + base + 8 * v, dp);
             }
         }
+        st = st == stages - 1 ? 0 : st + 1;
     }
+    if (RING) cp_async_wait<0>();
     float* part = p.part + (int64_t)blockIdx.x * 3 * p.W;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
+        const int v = tid + j * nt;
         if (v < nv) {
-            store8(part + 8 * v, a_pre[j]);
-            store8(part + p.W + 8 * v, a_post[j]);
-            store8(part + 2 * (int64_t)p.W + 8 * v, a_sc[j]);
+            f2_store8(part + 8 * v, a_pre[j]);
+            F2 c[4], d[4];
+            if (p.scale) {
+                f2_load8(p.scale + 8 * v, c);
+                if (wpost) f2_load8(wpost + 8 * v, d);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = p.scale ? f2_mul(a_br[j][i], c[i]) : a_br[j][i];                // dw_post
+                d[i] = p.scale && wpost ? f2_mul(a_br[j][i], d[i]) : a_br[j][i];       // dscale
+            }
+            f2_store8(part + p.W + 8 * v, c);
+            f2_store8(part + 2 * (int64_t)p.W + 8 * v, d);
         }
     }
 }
@@ -282,12 +408,29 @@ void norm_shape(int W, int& threads, int& vpt) {
     threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
 }
 
+// 128 registers a thread: 512 threads fill an SM
+int bwd_per_sm(int threads) { return threads >= 512 ? 1 : (512 / threads > 8 ? 8 : 512 / threads); }
 int bwd_blocks(int T, int W) {
     int threads, vpt;
     norm_shape(W, threads, vpt);
-    const int per = threads >= 512 ? 1 : 512 / threads;  // 128 registers a thread: 512 threads fill an SM
-    const int n = device_sm_count() * (per > 8 ? 8 : per);
+    const int n = device_sm_count() * bwd_per_sm(threads);
     return T < n ? (T > 0 ? T : 1) : n;
+}
+
+template <typename E, typename R, int VPT>
+gdn_status run_bwd(const NormParams& p, int threads, cudaStream_t s) {
+    const int grid = bwd_blocks(p.T, p.W);
+    const size_t row = row_bytes<E, R, VPT>(threads);
+    int stages = (int)(kRingBytes / bwd_per_sm(threads) / row);
+    if (stages > kMaxStages) stages = kMaxStages;
+    if (stages < 2) {
+        norm_bwd_kernel<E, R, VPT, false><<<grid, threads, 0, s>>>(p, 1);
+        return check_launch("norm_bwd_kernel");
+    }
+    const gdn_status st = set_smem_attr((const void*)norm_bwd_kernel<E, R, VPT, true>, kRingBytes);
+    if (st != GDN_OK) return st;
+    norm_bwd_kernel<E, R, VPT, true><<<grid, threads, stages * row, s>>>(p, stages);
+    return check_launch("norm_bwd_kernel");
 }
 
 template <typename E, typename R>
@@ -303,11 +446,9 @@ gdn_status run_norm(const NormParams& p, bool bwd, cudaStream_t s) {
         else norm_fwd_kernel<E, R, 4><<<grid, threads, 0, s>>>(p);
         return check_launch("norm_fwd_kernel");
     }
-    const int grid = bwd_blocks(p.T, p.W);
-    if (vpt == 1) norm_bwd_kernel<E, R, 1><<<grid, threads, 0, s>>>(p);
-    else if (vpt == 2) norm_bwd_kernel<E, R, 2><<<grid, threads, 0, s>>>(p);
-    else norm_bwd_kernel<E, R, 4><<<grid, threads, 0, s>>>(p);
-    return check_launch("norm_bwd_kernel");
+    if (vpt == 1) return run_bwd<E, R, 1>(p, threads, s);
+    if (vpt == 2) return run_bwd<E, R, 2>(p, threads, s);
+    return run_bwd<E, R, 4>(p, threads, s);
 }
 
 gdn_status dispatch_norm(const NormParams& p, bool bwd, gdn_dtype dt, gdn_dtype rdt, cudaStream_t s) {

@@ -141,6 +141,34 @@ __device__ __forceinline__ F2 f2_exp2(F2 a) {
 __device__ __forceinline__ F2 f2_dup(float v) { return f2(v, v); }
 __device__ __forceinline__ F2 f2_decay(F2 d, F2 A2) { return f2_exp2(f2_fma(d, A2, f2_dup(kDecayBias))); }
 __device__ __forceinline__ float f2_sum(F2 a) { return a.x() + a.y(); }
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
+    return r;
+}
+__device__ __forceinline__ F2 f2_sigmoid(F2 v) { return f2(sigmoid_fast(v.x()), sigmoid_fast(v.y())); }
+// eight consecutive elements (16-byte aligned) as four pairs
+__device__ __forceinline__ void f2_load8(const __nv_bfloat16* p, F2 (&f)[4]) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void f2_load8(const float* p, F2 (&f)[4]) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0], b = reinterpret_cast<const ulonglong2*>(p)[1];
+    f[0].b = a.x; f[1].b = a.y; f[2].b = b.x; f[3].b = b.y;
+}
+__device__ __forceinline__ void f2_store8(__nv_bfloat16* p, const F2 (&f)[4]) {
+    uint4 raw;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&raw);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[i].x(), f[i].y());
+    *reinterpret_cast<uint4*>(p) = raw;
+}
+__device__ __forceinline__ void f2_store8(float* p, const F2 (&f)[4]) {
+    reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0].b, f[1].b);
+    reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2].b, f[3].b);
+}
 // one pair, or two, from shared memory
 __device__ __forceinline__ F2 f2_load(const float* p) { return F2{*reinterpret_cast<const unsigned long long*>(p)}; }
 __device__ __forceinline__ void f2_load2(const float* p, F2& a, F2& b) {
