@@ -16,31 +16,28 @@ constexpr int NT = 128;
 constexpr int CV = 4;   // channels per thread of the backward
 constexpr int RB = 4;   // rows loaded ahead
 
+// four channels as they come, and as two pairs
 template <typename T> struct Raw4;
 template <> struct Raw4<__nv_bfloat16> {
     uint2 v;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
-    __device__ __forceinline__ void unpack(float (&f)[4]) const {
-        f[0] = __uint_as_float(v.x << 16);
-        f[1] = __uint_as_float(v.x & 0xffff0000u);
-        f[2] = __uint_as_float(v.y << 16);
-        f[3] = __uint_as_float(v.y & 0xffff0000u);
+    __device__ __forceinline__ void unpack(F2 (&f)[2]) const {
+        f[0] = f2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+        f[1] = f2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[4]) {
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const F2 (&f)[2]) {
         uint2 r;
         __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&r);
-        h[0] = __floats2bfloat162_rn(f[0], f[1]);
-        h[1] = __floats2bfloat162_rn(f[2], f[3]);
+        h[0] = __floats2bfloat162_rn(f[0].x(), f[0].y());
+        h[1] = __floats2bfloat162_rn(f[1].x(), f[1].y());
         *reinterpret_cast<uint2*>(p) = r;
     }
 };
 template <> struct Raw4<float> {
-    float4 v;
-    __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
-    __device__ __forceinline__ void unpack(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
-    static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
-        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    }
+    ulonglong2 v;
+    __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const ulonglong2*>(p)); }
+    __device__ __forceinline__ void unpack(F2 (&f)[2]) const { f[0].b = v.x; f[1].b = v.y; }
+    static __device__ __forceinline__ void store(float* p, const F2 (&f)[2]) { f2_store2(p, f[0], f[1]); }
 };
 
 struct ConvBwdParams {
@@ -60,9 +57,12 @@ struct ConvBwdParams {
 // strip of rows and walks down it with a window of the last K - 1 inputs and of
 // the K - 1 rows whose dx is not complete yet.  A strip runs K - 1 rows past
 // its end (within the sequence) for the dx of its own last rows; those rows'
-// dw and db belong to the next strip.
+// dw and db belong to the next strip.  Groups of four rows that touch no sequence's
+// end and no strip's edge, all but a few, run without a check.  Channels go in
+// pairs through the two-wide instructions: about 26 issue slots an element where
+// single ones took 44, which at four blocks an SM had bounded it.
 template <typename T, int K>
-__global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
+__global__ void __launch_bounds__(NT, 4) conv_bwd_kernel(const ConvBwdParams p) {
     constexpr int H = K > 1 ? K - 1 : 1;
     const int c0 = (blockIdx.x * NT + threadIdx.x) * CV;
     if (c0 >= p.C) return;
@@ -72,36 +72,41 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
     const T* dy = static_cast<const T*>(p.dy) + c0;
     T* dx = static_cast<T*>(p.dx) + c0;
 
-    auto end_grad = [&](int seq, int j, float (&f)[4]) {  // dstate_out row j
+    auto end_grad = [&](int seq, int j, F2 (&f)[2]) {  // dstate_out row j
         if (p.dso) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p.dso + ((int64_t)seq * (K - 1) + j) * p.C + c0));
-            f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+            Raw4<float> r;
+            r.load(p.dso + ((int64_t)seq * (K - 1) + j) * p.C + c0);
+            r.unpack(f);
         } else {
-            f[0] = f[1] = f[2] = f[3] = 0.f;
+            f[0] = f[1] = f2_dup(0.f);
         }
     };
-    auto put_state = [&](int seq, int j, const float (&f)[4]) {
+    auto put_state = [&](int seq, int j, const F2 (&f)[2]) {
         if (p.dstate) Raw4<float>::store(p.dstate + ((int64_t)seq * (K - 1) + j) * p.C + c0, f);
     };
     auto pass_empty = [&](int seq) {  // its final state is its initial one
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
-            float f[4];
+            F2 f[2];
             end_grad(seq, j, f);
             put_state(seq, j, f);
         }
     };
 
-    float w[K][4], b[4], dw[K][4], db[4];
+    F2 w[K][2], b[2], dw[K][2], db[2];
+    const F2 zero = f2_dup(0.f), one = f2_dup(1.f), neg = f2_dup(-1.f);
+    {
+        const T *wp = static_cast<const T*>(p.w) + (int64_t)c0 * K, *bp = static_cast<const T*>(p.b) + c0;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) {
-            w[j][c] = Elem<T>::to_f(static_cast<const T*>(p.w)[(int64_t)(c0 + c) * K + j]);
-            dw[j][c] = 0.f;
+            for (int j = 0; j < K; ++j) {
+                w[j][h] = f2(Elem<T>::to_f(wp[2 * h * K + j]), Elem<T>::to_f(wp[(2 * h + 1) * K + j]));
+                dw[j][h] = zero;
+            }
+            b[h] = p.b ? f2(Elem<T>::to_f(bp[2 * h]), Elem<T>::to_f(bp[2 * h + 1])) : zero;
+            db[h] = zero;
         }
-        b[c] = p.b ? Elem<T>::to_f(static_cast<const T*>(p.b)[c0 + c]) : 0.f;
-        db[c] = 0.f;
     }
     const int lt0 = blockIdx.y * p.rows, lt1 = min(p.T, lt0 + p.rows);
     if (p.T == 0) {
@@ -112,20 +117,20 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
         int start = __ldg(cu + seg), next = __ldg(cu + seg + 1);
         if (start == lt0)  // empty sequences that end where this strip starts
             for (int m = seg - 1; m >= 0 && __ldg(cu + m) == lt0; --m) pass_empty(m);
-        float win[H][4], acc[H][4];
-        auto load_state = [&](int j, float (&f)[4]) {
+        F2 win[H][2], acc[H][2];
+        auto load_state = [&](int j, F2 (&f)[2]) {
             if (p.state) {
                 Raw4<T> r;
                 r.load(static_cast<const T*>(p.state) + ((int64_t)seg * (K - 1) + j) * p.C + c0);
                 r.unpack(f);
             } else {
-                f[0] = f[1] = f[2] = f[3] = 0.f;
+                f[0] = f[1] = zero;
             }
         };
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) {
             const int row = lt0 - (K - 1) + j, m = K - 1 - (start - row);
-            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+            acc[j][0] = acc[j][1] = zero;
             if (row >= start && row >= 0) {
                 Raw4<T> r;
                 r.load(x + (int64_t)row * p.ldx);
@@ -133,15 +138,46 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
             } else if (m >= 0 && m < K - 1) {
                 load_state(m, win[j]);
             } else {
-                win[j][0] = win[j][1] = win[j][2] = win[j][3] = 0.f;
+                win[j][0] = win[j][1] = zero;
             }
         }
-        auto emit = [&](int row, const float (&f)[4]) {
+        auto emit = [&](int row, const F2 (&f)[2]) {
             if (row >= start) {
                 if (row >= lt0 && row < lt1) Raw4<T>::store(dx + (int64_t)row * p.lddx, f);
             } else if (start >= lt0) {
                 const int m = K - 1 - (start - row);
                 if (m >= 0 && m < K - 1) put_state(seg, m, f);
+            }
+        };
+        // one row: ds, the sums, and the dx that it completes (of the row K - 1 before it)
+        auto step = [&](const Raw4<T>& rx, const Raw4<T>& ry, bool own, F2 (&first)[2]) {
+            F2 xv[2], g[2];
+            rx.unpack(xv);
+            ry.unpack(g);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                F2 pre = b[h];
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) pre = f2_fma(w[j][h], win[j][h], pre);
+                pre = f2_fma(w[K - 1][h], xv[h], pre);
+                const F2 sg = f2_sigmoid(pre);
+                const F2 ds = f2_mul(f2_mul(g[h], sg), f2_fma(pre, f2_fma(sg, neg, one), one));
+                if (own) {
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) dw[j][h] = f2_fma(ds, win[j][h], dw[j][h]);
+                    dw[K - 1][h] = f2_fma(ds, xv[h], dw[K - 1][h]);
+                    db[h] = f2_add(db[h], ds);
+                }
+                first[h] = K > 1 ? f2_fma(w[0][h], ds, acc[0][h]) : f2_mul(w[0][h], ds);
+#pragma unroll
+                for (int j = 0; j + 1 < K - 1; ++j) {
+                    acc[j][h] = f2_fma(w[j + 1][h], ds, acc[j + 1][h]);
+                    win[j][h] = win[j + 1][h];
+                }
+                if (K > 1) {
+                    acc[H - 1][h] = f2_mul(w[K - 1][h], ds);
+                    win[H - 1][h] = xv[h];
+                }
             }
         };
         const int tend = min(p.T, lt1 + K - 1);
@@ -164,6 +200,16 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
                 cy[u] = ny[u];
             }
             if (tb + RB < tend) fetch(tb + RB);
+            if (tb + RB <= lt1 && next > tb + RB && tb - (K - 1) >= max(start, lt0)) {
+                T* out = dx + (int64_t)(tb - (K - 1)) * p.lddx;
+#pragma unroll
+                for (int u = 0; u < RB; ++u) {
+                    F2 first[2];
+                    step(cx[u], cy[u], true, first);
+                    Raw4<T>::store(out + u * p.lddx, first);
+                }
+                continue;
+            }
 #pragma unroll
             for (int u = 0; u < RB; ++u) {
                 const int t = tb + u;
@@ -180,48 +226,21 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
 #pragma unroll
                         for (int j = 0; j < K - 1; ++j) {
                             load_state(j, win[j]);
-                            acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+                            acc[j][0] = acc[j][1] = zero;
                         }
                     }
                 }
                 if (done || t >= tend) continue;
-                float xv[4], g[4];
-                cx[u].unpack(xv);
-                cy[u].unpack(g);
-                const bool own = t < lt1;
-                float first[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float pre = b[c];
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) pre = fmaf(w[j][c], win[j][c], pre);
-                    pre = fmaf(w[K - 1][c], xv[c], pre);
-                    const float s = sigmoid_fast(pre);
-                    const float ds = g[c] * s * fmaf(pre, 1.f - s, 1.f);
-                    const float dsw = own ? ds : 0.f;
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) dw[j][c] = fmaf(dsw, win[j][c], dw[j][c]);
-                    dw[K - 1][c] = fmaf(dsw, xv[c], dw[K - 1][c]);
-                    db[c] += dsw;
-                    first[c] = fmaf(w[0][c], ds, K > 1 ? acc[0][c] : 0.f);
-#pragma unroll
-                    for (int j = 0; j + 1 < K - 1; ++j) {
-                        acc[j][c] = fmaf(w[j + 1][c], ds, acc[j + 1][c]);
-                        win[j][c] = win[j + 1][c];
-                    }
-                    if (K > 1) {
-                        acc[H - 1][c] = w[K - 1][c] * ds;
-                        win[H - 1][c] = xv[c];
-                    }
-                }
+                F2 first[2];
+                step(cx[u], cy[u], t < lt1, first);
                 emit(t - (K - 1), first);
                 if (t + 1 == next) {  // the sequence ends: its last rows are complete
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j) {
-                        float f[4];
+                        F2 f[2];
                         end_grad(seg, j, f);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) f[c] += acc[j][c];
+                        f[0] = f2_add(f[0], acc[j][0]);
+                        f[1] = f2_add(f[1], acc[j][1]);
                         emit(t - (K - 1) + 1 + j, f);
                     }
                 }
@@ -232,49 +251,68 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwdParams p) {
     }
     float* part = p.part + (int64_t)blockIdx.y * p.C * (K + 1);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < K; ++j) part[(int64_t)(c0 + c) * K + j] = dw[j][c];
+        for (int j = 0; j < K; ++j) {
+            part[(int64_t)(c0 + 2 * h) * K + j] = dw[j][h].x();
+            part[(int64_t)(c0 + 2 * h + 1) * K + j] = dw[j][h].y();
+        }
     Raw4<float>::store(part + (int64_t)p.C * K + c0, db);
 }
 
 // One token per request: read K - 1 state rows, write K - 1 (shifted) and y.
-// Bound by those bytes (or, for a few requests, by the launch).
+// Bound by those bytes (or, for a few requests, by the launch): a thread holds the
+// weights of eight channels and takes the requests gridDim.y apart.
 template <typename T, int K>
-__global__ void __launch_bounds__(NT) conv_step_kernel(const T* x, int64_t ldx, int C, const T* w, const T* bias,
-                                                       T* states, int num_slots, const int32_t* src,
+__global__ void __launch_bounds__(NT) conv_step_kernel(const T* x, int64_t ldx, int batch, int C, const T* w,
+                                                       const T* bias, T* states, int num_slots, const int32_t* src,
                                                        const int32_t* dst, T* y, int64_t ldy) {
-    const int c0 = (blockIdx.x * NT + threadIdx.x) * 8, r = blockIdx.y;
+    const int c0 = (blockIdx.x * NT + threadIdx.x) * 8;
     if (c0 >= C) return;
-    int from = src ? __ldg(src + r) : r, to = dst ? __ldg(dst + r) : r;
-    if (from >= num_slots) from = -1;
-    float f[8];
-    T* yr = y + (int64_t)r * ldy + c0;
-    if (to < 0 || to >= num_slots) {  // a padded row
+    float wv[8 * K], b[8];
+    const T* wp = w + (int64_t)c0 * K;
+    if ((reinterpret_cast<uintptr_t>(w) & 15u) == 0) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) f[c] = 0.f;
+        for (int j = 0; j < K; ++j) load8(wp + 8 * j, *reinterpret_cast<float(*)[8]>(wv + 8 * j));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) wv[i] = Elem<T>::to_f(wp[i]);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) b[c] = bias ? Elem<T>::to_f(bias[c0 + c]) : 0.f;
+    for (int r = blockIdx.y; r < batch; r += gridDim.y) {
+        int from = src ? __ldg(src + r) : r;
+        const int to = dst ? __ldg(dst + r) : r;
+        if (from >= num_slots) from = -1;
+        T* yr = y + (int64_t)r * ldy + c0;
+        float rows[K][8], f[8];
+        if (to < 0 || to >= num_slots) {  // a padded row
+#pragma unroll
+            for (int c = 0; c < 8; ++c) f[c] = 0.f;
+            store8(yr, f);
+            continue;
+        }
+        const T* in = states + (int64_t)from * (K - 1) * C + c0;
+        T* out = states + (int64_t)to * (K - 1) * C + c0;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            if (from >= 0) load8_rw(in + (int64_t)j * C, rows[j]);
+            else
+#pragma unroll
+                for (int c = 0; c < 8; ++c) rows[j][c] = 0.f;
+        }
+        load8(x + (int64_t)r * ldx + c0, rows[K - 1]);
+#pragma unroll
+        for (int j = 1; j < K; ++j) store8(out + (int64_t)(j - 1) * C, rows[j]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            float acc = b[c];
+#pragma unroll
+            for (int j = 0; j < K; ++j) acc = fmaf(wv[c * K + j], rows[j][c], acc);
+            f[c] = silu_fast(acc);
+        }
         store8(yr, f);
-        return;
     }
-    float acc[8], row[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] = bias ? Elem<T>::to_f(bias[c0 + c]) : 0.f;
-    T* out = states + (int64_t)to * (K - 1) * C + c0;
-    const T* in = states + (int64_t)from * (K - 1) * C + c0;
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-        if (j == K - 1) load8(x + (int64_t)r * ldx + c0, row);
-        else if (from >= 0) load8_rw(in + (int64_t)j * C, row);
-        else
-#pragma unroll
-            for (int c = 0; c < 8; ++c) row[c] = 0.f;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = fmaf(Elem<T>::to_f(w[(int64_t)(c0 + c) * K + j]), row[c], acc[c]);
-        if (j > 0) store8(out + (int64_t)(j - 1) * C, row);
-    }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) f[c] = silu_fast(acc[c]);
-    store8(yr, f);
 }
 
 // Strips of the backward: enough blocks for four resident ones an SM, strips of
@@ -305,14 +343,15 @@ gdn_status run_bwd(ConvBwdParams p, int K, cudaStream_t s) {
 template <typename T>
 gdn_status run_step(const void* x, int64_t ldx, int batch, int C, const void* w, const void* bias, int K, void* states,
                     int num_slots, const int32_t* src, const int32_t* dst, void* y, int64_t ldy, cudaStream_t s) {
-    const dim3 grid((C / 8 + NT - 1) / NT, batch);
+    const int nx = (C / 8 + NT - 1) / NT, most = (device_sm_count() * 12 + nx - 1) / nx;  // about 12 blocks an SM
+    const dim3 grid(nx, batch < most ? batch : most);
     const T *xt = static_cast<const T*>(x), *wt = static_cast<const T*>(w), *bt = static_cast<const T*>(bias);
     T *st = static_cast<T*>(states), *yt = static_cast<T*>(y);
     switch (K) {
-        case 1: conv_step_kernel<T, 1><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
-        case 2: conv_step_kernel<T, 2><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
-        case 3: conv_step_kernel<T, 3><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
-        default: conv_step_kernel<T, 4><<<grid, NT, 0, s>>>(xt, ldx, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+        case 1: conv_step_kernel<T, 1><<<grid, NT, 0, s>>>(xt, ldx, batch, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+        case 2: conv_step_kernel<T, 2><<<grid, NT, 0, s>>>(xt, ldx, batch, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+        case 3: conv_step_kernel<T, 3><<<grid, NT, 0, s>>>(xt, ldx, batch, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
+        default: conv_step_kernel<T, 4><<<grid, NT, 0, s>>>(xt, ldx, batch, C, wt, bt, st, num_slots, src, dst, yt, ldy); break;
     }
     return check_launch("conv_step_kernel");
 }

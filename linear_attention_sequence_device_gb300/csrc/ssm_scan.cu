@@ -297,66 +297,93 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
 }
 
 // One token per request.  Bound by the states, read and written once (for a few
-// requests by the launch): one thread per channel and four states, K lanes a channel.
-template <typename E, int K>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p, float* states, int num_slots,
+// requests by the launch): a thread holds four states' decay rates of one channel,
+// K lanes a channel, and takes the requests gridDim.y apart, the next one's state
+// under way meanwhile.  N above 4 K: the lanes go round (RND times).
+template <typename E, int K, int RND>
+__global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p, int batch, float* states, int num_slots,
                                                         const int32_t* src, const int32_t* dst) {
-    const int r = blockIdx.y, lane_k = threadIdx.x % K;
-    const int c = (blockIdx.x * 256 + threadIdx.x) / K;
-    int from = src ? __ldg(src + r) : r;
-    const int to = dst ? __ldg(dst + r) : r;
-    if (from >= num_slots) from = -1;
-    const bool pad = to < 0 || to >= num_slots;
-    const bool in = c < p.ch;
-    float acc = 0.f, xv = 0.f;
-    if (in && !pad) {
-        xv = Elem<E>::load(static_cast<const E*>(p.x) + (int64_t)r * p.ldx + c);
-        const float dl = softplus_f(Elem<E>::load(static_cast<const E*>(p.dt) + (int64_t)r * p.lddt + c) +
-                                    (p.dt_bias ? __ldg(p.dt_bias + c) : 0.f));
-        const float u = dl * xv;
-        const int grp = c / p.per;
-        const E* B = static_cast<const E*>(p.B) + (int64_t)r * p.ldb + (int64_t)grp * p.N;
-        const E* C = static_cast<const E*>(p.C) + (int64_t)r * p.ldc + (int64_t)grp * p.N;
-        for (int n0 = 4 * lane_k; n0 < p.N; n0 += 4 * K) {
-            float h[4] = {0.f, 0.f, 0.f, 0.f}, a[4];
-            const int64_t off = (int64_t)c * p.N + n0;
-            const float* in_p = states + (int64_t)from * p.ch * p.N + off;
-            float* out_p = states + (int64_t)to * p.ch * p.N + off;
-            if (p.N % 4 == 0) {
-                if (from >= 0) {
-                    const float4 v = *reinterpret_cast<const float4*>(in_p);
-                    h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
-                }
-                const float4 v = __ldg(reinterpret_cast<const float4*>(p.A_log + off));
-                a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+    const int k = threadIdx.x % K, c = (blockIdx.x * 256 + threadIdx.x) / K;
+    const bool in = c < p.ch, vec = p.N % 4 == 0;
+    const int cc = in ? c : 0;
+    float A2[RND][4];
+#pragma unroll
+    for (int q = 0; q < RND; ++q)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int st = 4 * (k + q * K) + n;
+            A2[q][n] = st < p.N ? -expf(__ldg(p.A_log + (int64_t)cc * p.N + st)) * kLog2e : 0.f;
+        }
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + cc) : 0.f, Dc = p.D ? __ldg(p.D + cc) : 0.f;
+    const int64_t goff = (int64_t)(cc / p.per) * p.N;
+    struct Row {
+        int to;
+        float x, dt, z, h[RND][4], B[RND][4], C[RND][4];
+    };
+    auto fetch = [&](int r, Row& w) {
+        int from = src ? __ldg(src + r) : r;
+        w.to = dst ? __ldg(dst + r) : r;
+        if (from >= num_slots) from = -1;
+        if (w.to >= num_slots || !in) w.to = -1;
+        w.x = Elem<E>::load(static_cast<const E*>(p.x) + (int64_t)r * p.ldx + cc);
+        w.dt = Elem<E>::load(static_cast<const E*>(p.dt) + (int64_t)r * p.lddt + cc);
+        w.z = p.z ? Elem<E>::load(static_cast<const E*>(p.z) + (int64_t)r * p.ldz + cc) : 0.f;
+        const E* B = static_cast<const E*>(p.B) + (int64_t)r * p.ldb + goff;
+        const E* C = static_cast<const E*>(p.C) + (int64_t)r * p.ldc + goff;
+        const bool have = from >= 0 && w.to >= 0;
+        const float* g = states + ((int64_t)(have ? from : 0) * p.ch + cc) * p.N;
+#pragma unroll
+        for (int q = 0; q < RND; ++q) {
+            const int st = 4 * (k + q * K);
+            if (vec && have && st < p.N) {
+                const float4 v = *reinterpret_cast<const float4*>(g + st);
+                w.h[q][0] = v.x; w.h[q][1] = v.y; w.h[q][2] = v.z; w.h[q][3] = v.w;
             } else {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const bool ok = n0 + n < p.N;
-                    if (ok && from >= 0) h[n] = in_p[n];
-                    a[n] = ok ? __ldg(p.A_log + off + n) : 0.f;
-                }
+                for (int n = 0; n < 4; ++n) w.h[q][n] = !vec && have && st + n < p.N ? g[st + n] : 0.f;
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                if (n0 + n < p.N) {
-                    h[n] = fmaf(decay_fast(dl, -expf(a[n]) * kLog2e), h[n], u * Elem<E>::load(B + n0 + n));
-                    acc = fmaf(h[n], Elem<E>::load(C + n0 + n), acc);
+                w.B[q][n] = st + n < p.N ? Elem<E>::load(B + st + n) : 0.f;
+                w.C[q][n] = st + n < p.N ? Elem<E>::load(C + st + n) : 0.f;
+            }
+        }
+    };
+    Row cur, nxt;
+    int r = blockIdx.y;
+    fetch(r, cur);
+    for (; r < batch; r += gridDim.y) {
+        const bool more = r + (int)gridDim.y < batch;
+        if (more) fetch(r + gridDim.y, nxt);
+        const float dl = softplus_f(cur.dt + bias), u = dl * cur.x;
+        float acc = 0.f;
+#pragma unroll
+        for (int q = 0; q < RND; ++q) {
+            const int st = 4 * (k + q * K);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                cur.h[q][n] = fmaf(decay_fast(dl, A2[q][n]), cur.h[q][n], u * cur.B[q][n]);
+                acc = fmaf(cur.h[q][n], cur.C[q][n], acc);
+            }
+            if (cur.to >= 0) {
+                float* g = states + ((int64_t)cur.to * p.ch + cc) * p.N + st;
+                if (vec) {
+                    if (st < p.N) *reinterpret_cast<float4*>(g) = make_float4(cur.h[q][0], cur.h[q][1], cur.h[q][2], cur.h[q][3]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (st + n < p.N) g[n] = cur.h[q][n];
                 }
             }
-            if (p.N % 4 == 0) *reinterpret_cast<float4*>(out_p) = make_float4(h[0], h[1], h[2], h[3]);
-            else
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    if (n0 + n < p.N) out_p[n] = h[n];
         }
-    }
 #pragma unroll
-    for (int off = 1; off < K; off <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (in && lane_k == 0) {
-        if (p.D) acc = fmaf(__ldg(p.D + c), xv, acc);
-        if (p.z && !pad) acc *= silu_fast(Elem<E>::load(static_cast<const E*>(p.z) + (int64_t)r * p.ldz + c));
-        static_cast<E*>(p.y)[(int64_t)r * p.ldy + c] = Elem<E>::from_f(pad ? 0.f : acc);
+        for (int off = 1; off < K; off <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        if (in && k == 0) {
+            acc = fmaf(Dc, cur.x, acc);
+            if (p.z) acc *= silu_fast(cur.z);
+            static_cast<E*>(p.y)[(int64_t)r * p.ldy + c] = Elem<E>::from_f(cur.to < 0 ? 0.f : acc);
+        }
+        if (more) cur = nxt;
     }
 }
 
@@ -425,10 +452,13 @@ template <typename E>
 gdn_status run_step(const ScanParams& p, int batch, float* states, int num_slots, const int32_t* src,
                     const int32_t* dst, cudaStream_t s) {
     const int K = lanes_of(p.N);
-    const dim3 grid((unsigned)(((int64_t)p.ch * K + 255) / 256), batch);
-    if (K == 1) scan_step_kernel<E, 1><<<grid, 256, 0, s>>>(p, states, num_slots, src, dst);
-    else if (K == 2) scan_step_kernel<E, 2><<<grid, 256, 0, s>>>(p, states, num_slots, src, dst);
-    else scan_step_kernel<E, 4><<<grid, 256, 0, s>>>(p, states, num_slots, src, dst);
+    const int nx = (int)(((int64_t)p.ch * K + 255) / 256), most = (device_sm_count() * 8 + nx - 1) / nx;  // 8 blocks an SM
+    const dim3 grid(nx, batch < most ? batch : most);
+    if (K == 1) scan_step_kernel<E, 1, 1><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
+    else if (K == 2) scan_step_kernel<E, 2, 1><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
+    else if (p.N <= 16) scan_step_kernel<E, 4, 1><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
+    else if (p.N <= 32) scan_step_kernel<E, 4, 2><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
+    else scan_step_kernel<E, 4, 4><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
     return check_launch("scan_step_kernel");
 }
 
