@@ -296,100 +296,168 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
     }
 }
 
+constexpr int STG = 4;     // requests whose states are in flight or in use (step)
+
 // One token per request.  Bound by the states, read and written once (for a few
-// requests by the launch): a thread holds four states' decay rates of one channel,
-// K lanes a channel, and takes the requests gridDim.y apart, the next one's state
-// under way meanwhile.  N above 4 K: the lanes go round (RND times).
-template <typename E, int K, int RND>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p, int batch, float* states, int num_slots,
-                                                        const int32_t* src, const int32_t* dst) {
-    const int k = threadIdx.x % K, c = (blockIdx.x * 256 + threadIdx.x) / K;
-    const bool in = c < p.ch, vec = p.N % 4 == 0;
-    const int cc = in ? c : 0;
-    float A2[RND][4];
+// requests by the launch).  As in the prompt's kernel a lane holds up to 16 states
+// of one channel (four lanes a channel and four states, which reads states
+// directly, took 272 instructions for 8 channels and was bound by them at 70 us
+// for 256 requests of 4096 channels); a warp's channels are one contiguous piece
+// of a slot, which comes by 16-byte asynchronous copies into the warp's ring and
+// goes back from there, both in full lines.  A warp takes the requests gridDim.y
+// apart, three of them under way.  FULL: N is all of a lane's states and the warp's
+// channels exist, so that the copies' counts are known.
+template <typename E, int K, int NS, bool FULL>
+__global__ void __launch_bounds__(NTH, 4) scan_step_kernel(const ScanParams p, int batch, float* states, int num_slots,
+                                                           const int32_t* src, const int32_t* dst) {
+    constexpr int NP = K * NS, NBC = (2 * NP + 31) / 32;  // padded states; values of B and C per lane
+    constexpr int WC = 32 / K;  // channels per warp
+    extern __shared__ float4 smem4[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = lane % K, G = gridDim.y;
+    const int grp = blockIdx.x / p.tiles, cend = (grp + 1) * p.per;
+    const int c0 = grp * p.per + (blockIdx.x % p.tiles) * (NTH / K) + warp * WC;  // the warp's first channel
+    if (c0 >= cend) return;
+    const int c = c0 + lane / K;
+    const bool in = c < cend, vec = FULL || p.N % 4 == 0;
+    const int cc = in ? c : c0, N = FULL ? NP : p.N;
+    const int tile = WC * N, chunks = FULL ? WC * NP / 4 : min(WC, cend - c0) * N / 4;  // floats; 16-byte pieces that exist
+    float* ring = reinterpret_cast<float*>(smem4) + warp * (STG * tile + 4 * NP);
+    float* bcs = ring + STG * tile;  // [2][B, C][NP]
+    F2 A2[NS / 2];
 #pragma unroll
-    for (int q = 0; q < RND; ++q)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int st = 4 * (k + q * K) + n;
-            A2[q][n] = st < p.N ? -expf(__ldg(p.A_log + (int64_t)cc * p.N + st)) * kLog2e : 0.f;
-        }
+    for (int q = 0; q < NS / 2; ++q) {
+        const int st = k * NS + 2 * q;
+        const float* g = p.A_log + (int64_t)cc * p.N + st;
+        A2[q] = f2(st < p.N ? -expf(__ldg(g)) * kLog2e : 0.f, st + 1 < p.N ? -expf(__ldg(g + 1)) * kLog2e : 0.f);
+    }
     const float bias = p.dt_bias ? __ldg(p.dt_bias + cc) : 0.f, Dc = p.D ? __ldg(p.D + cc) : 0.f;
-    const int64_t goff = (int64_t)(cc / p.per) * p.N;
+    // four-state pieces of 16 lie 64 bytes apart between lanes: their order within a channel turns with the lane,
+    // so that eight lanes' reads meet all banks
+    constexpr bool TURN = FULL && NS == 16 && K == 1;
+    const int turn = TURN ? lane >> 1 & 3 : 0;
+    // the slots that request r reads (-1: none) and writes (-1: a padded row)
+    auto slots = [&](int r, int& from, int& to) {
+        from = to = -1;
+        if (r < batch) {
+            from = src ? __ldg(src + r) : r;
+            to = dst ? __ldg(dst + r) : r;
+            if (to >= num_slots) to = -1;
+            if (from >= num_slots || to < 0) from = -1;
+        }
+    };
+    auto piece = [&](int t) {  // where 16-byte piece t of the tile lies
+        return TURN ? (t & ~3) | ((t & 3) ^ (t >> 3 & 3)) : t;
+    };
+    auto copy = [&](int from, int stage) {
+        const float* g = states + ((int64_t)(from < 0 ? 0 : from) * p.ch + c0) * p.N;
+        float* d = ring + stage * tile;
+        if constexpr (FULL && WC * NP / 4 % 32 == 0) {
+#pragma unroll
+            for (int i = 0; i < WC * NP / 128; ++i)
+                cp_async16(d + 4 * piece(lane + 32 * i), g + 4 * (lane + 32 * i), from < 0 ? 0 : 16);
+        } else {
+            for (int t = lane; t < chunks; t += 32) cp_async16(d + 4 * piece(t), g + 4 * t, from < 0 ? 0 : 16);
+        }
+        cp_async_commit();
+    };
     struct Row {
-        int to;
-        float x, dt, z, h[RND][4], B[RND][4], C[RND][4];
+        E x, dt, z, bc[NBC];
     };
     auto fetch = [&](int r, Row& w) {
-        int from = src ? __ldg(src + r) : r;
-        w.to = dst ? __ldg(dst + r) : r;
-        if (from >= num_slots) from = -1;
-        if (w.to >= num_slots || !in) w.to = -1;
-        w.x = Elem<E>::load(static_cast<const E*>(p.x) + (int64_t)r * p.ldx + cc);
-        w.dt = Elem<E>::load(static_cast<const E*>(p.dt) + (int64_t)r * p.lddt + cc);
-        w.z = p.z ? Elem<E>::load(static_cast<const E*>(p.z) + (int64_t)r * p.ldz + cc) : 0.f;
-        const E* B = static_cast<const E*>(p.B) + (int64_t)r * p.ldb + goff;
-        const E* C = static_cast<const E*>(p.C) + (int64_t)r * p.ldc + goff;
-        const bool have = from >= 0 && w.to >= 0;
-        const float* g = states + ((int64_t)(have ? from : 0) * p.ch + cc) * p.N;
+        w.x = __ldg(static_cast<const E*>(p.x) + (int64_t)r * p.ldx + cc);
+        w.dt = __ldg(static_cast<const E*>(p.dt) + (int64_t)r * p.lddt + cc);
+        if (p.z) w.z = __ldg(static_cast<const E*>(p.z) + (int64_t)r * p.ldz + cc);
 #pragma unroll
-        for (int q = 0; q < RND; ++q) {
-            const int st = 4 * (k + q * K);
-            if (vec && have && st < p.N) {
-                const float4 v = *reinterpret_cast<const float4*>(g + st);
-                w.h[q][0] = v.x; w.h[q][1] = v.y; w.h[q][2] = v.z; w.h[q][3] = v.w;
-            } else {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) w.h[q][n] = !vec && have && st + n < p.N ? g[st + n] : 0.f;
-            }
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                w.B[q][n] = st + n < p.N ? Elem<E>::load(B + st + n) : 0.f;
-                w.C[q][n] = st + n < p.N ? Elem<E>::load(C + st + n) : 0.f;
-            }
+        for (int i = 0; i < NBC; ++i) {
+            const int j = lane + 32 * i, n = j % NP;
+            const E* q = j < NP ? static_cast<const E*>(p.B) + (int64_t)r * p.ldb : static_cast<const E*>(p.C) + (int64_t)r * p.ldc;
+            w.bc[i] = j < 2 * NP && n < N ? __ldg(q + (int64_t)grp * N + n) : Elem<E>::from_f(0.f);
         }
     };
+    int from[STG], to[STG];  // of this request and the next ones
+#pragma unroll
+    for (int i = 0; i < STG; ++i) slots(blockIdx.y + i * G, from[i], to[i]);
+#pragma unroll
+    for (int i = 0; i < STG - 1; ++i) copy(from[i], i);
     Row cur, nxt;
-    int r = blockIdx.y;
-    fetch(r, cur);
-    for (; r < batch; r += gridDim.y) {
-        const bool more = r + (int)gridDim.y < batch;
-        if (more) fetch(r + gridDim.y, nxt);
-        const float dl = softplus_f(cur.dt + bias), u = dl * cur.x;
-        float acc = 0.f;
+    int stage = 0, par = 0;
+    fetch(blockIdx.y, cur);
+    for (int r = blockIdx.y; r < batch; r += G, par ^= 1) {
+        copy(from[STG - 1], stage == 0 ? STG - 1 : stage - 1);
+        if (r + G < batch) fetch(r + G, nxt);
+        const int out = to[0];
 #pragma unroll
-        for (int q = 0; q < RND; ++q) {
-            const int st = 4 * (k + q * K);
+        for (int i = 0; i < STG - 1; ++i) {
+            from[i] = from[i + 1];
+            to[i] = to[i + 1];
+        }
+        slots(r + STG * G, from[STG - 1], to[STG - 1]);
+        float* bcw = bcs + par * 2 * NP;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                cur.h[q][n] = fmaf(decay_fast(dl, A2[q][n]), cur.h[q][n], u * cur.B[q][n]);
-                acc = fmaf(cur.h[q][n], cur.C[q][n], acc);
+        for (int i = 0; i < NBC; ++i)
+            if (lane + 32 * i < 2 * NP) bcw[lane + 32 * i] = Elem<E>::to_f(cur.bc[i]);
+        const float xv = Elem<E>::to_f(cur.x), dlt = softplus_f(Elem<E>::to_f(cur.dt) + bias);
+        const F2 d = f2_dup(dlt), u = f2_dup(dlt * xv);
+        F2 acc = f2_dup(0.f);
+        cp_async_wait<STG - 1>();
+        __syncwarp();
+        float* own = ring + stage * tile + (lane / K) * N + k * NS;
+#pragma unroll
+        for (int q = 0; q < NS / 4; ++q) {
+            const int left = N - (k * NS + 4 * q);
+            float* g = own + 4 * (q ^ turn);
+            F2 h0, h1, b0, b1, d0, d1;
+            if (vec) {
+                if (left > 0) f2_load2(g, h0, h1);
+                else h0 = h1 = f2_dup(0.f);
+            } else {
+                h0 = f2(left > 0 ? g[0] : 0.f, left > 1 ? g[1] : 0.f);
+                h1 = f2(left > 2 ? g[2] : 0.f, left > 3 ? g[3] : 0.f);
             }
-            if (cur.to >= 0) {
-                float* g = states + ((int64_t)cur.to * p.ch + cc) * p.N + st;
-                if (vec) {
-                    if (st < p.N) *reinterpret_cast<float4*>(g) = make_float4(cur.h[q][0], cur.h[q][1], cur.h[q][2], cur.h[q][3]);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        if (st + n < p.N) g[n] = cur.h[q][n];
-                }
+            f2_load2(bcw + k * NS + 4 * q, b0, b1);
+            f2_load2(bcw + NP + k * NS + 4 * q, d0, d1);
+            h0 = f2_fma(f2_decay(d, A2[2 * q]), h0, f2_mul(u, b0));
+            h1 = f2_fma(f2_decay(d, A2[2 * q + 1]), h1, f2_mul(u, b1));
+            acc = f2_fma(h0, d0, acc);
+            acc = f2_fma(h1, d1, acc);
+            if (vec) {
+                if (left > 0) f2_store2(g, h0, h1);
+            } else {
+                if (left > 0) g[0] = h0.x();
+                if (left > 1) g[1] = h0.y();
+                if (left > 2) g[2] = h1.x();
+                if (left > 3) g[3] = h1.y();
             }
         }
+        float o = f2_sum(acc);
 #pragma unroll
-        for (int off = 1; off < K; off <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+        for (int off = 1; off < K; off <<= 1) o += __shfl_xor_sync(0xffffffffu, o, off);
         if (in && k == 0) {
-            acc = fmaf(Dc, cur.x, acc);
-            if (p.z) acc *= silu_fast(cur.z);
-            static_cast<E*>(p.y)[(int64_t)r * p.ldy + c] = Elem<E>::from_f(cur.to < 0 ? 0.f : acc);
+            o = fmaf(Dc, xv, o);
+            if (p.z) o *= silu_fast(Elem<E>::to_f(cur.z));
+            static_cast<E*>(p.y)[(int64_t)r * p.ldy + c] = Elem<E>::from_f(out < 0 ? 0.f : o);
         }
-        if (more) cur = nxt;
+        __syncwarp();
+        if (out >= 0) {
+            float4* g = reinterpret_cast<float4*>(states + ((int64_t)out * p.ch + c0) * p.N);
+            const float* sm = ring + stage * tile;
+            if constexpr (FULL && WC * NP / 4 % 32 == 0) {
+#pragma unroll
+                for (int i = 0; i < WC * NP / 128; ++i)
+                    g[lane + 32 * i] = *reinterpret_cast<const float4*>(sm + 4 * piece(lane + 32 * i));
+            } else {
+                for (int t = lane; t < chunks; t += 32) g[t] = *reinterpret_cast<const float4*>(sm + 4 * piece(t));
+            }
+        }
+        __syncwarp();  // the stage is read before it is copied into again
+        cur = nxt;
+        stage = stage == STG - 1 ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
 }
 
 // ---- host ----------------------------------------------------------------------
 
-int lanes_of(int N) { return N <= 4 ? 1 : (N <= 8 ? 2 : 4); }  // of the step: four states each
 int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH / 4); }
 
 // Segments of a call: enough blocks for four resident ones an SM, of 64 tokens
@@ -448,18 +516,34 @@ gdn_status dispatch_scan(const ScanParams& p, int groups, bool grad, cudaStream_
     return run_scan<E, 4, 16>(p, groups, grad, s);
 }
 
-template <typename E>
-gdn_status run_step(const ScanParams& p, int batch, float* states, int num_slots, const int32_t* src,
-                    const int32_t* dst, cudaStream_t s) {
-    const int K = lanes_of(p.N);
-    const int nx = (int)(((int64_t)p.ch * K + 255) / 256), most = (device_sm_count() * 8 + nx - 1) / nx;  // 8 blocks an SM
+template <typename E, int K, int NS>
+gdn_status run_step_k(ScanParams p, int groups, int batch, float* states, int num_slots, const int32_t* src,
+                      const int32_t* dst, cudaStream_t s) {
+    const size_t smem = sizeof(float) * (STG * (NTH / K) * p.N + NTH / 32 * 4 * K * NS);  // 36 KB at most
+    p.tiles = (p.per + NTH / K - 1) / (NTH / K);
+    const int nx = groups * p.tiles, most = (device_sm_count() * 4 + nx - 1) / nx;
     const dim3 grid(nx, batch < most ? batch : most);
-    if (K == 1) scan_step_kernel<E, 1, 1><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
-    else if (K == 2) scan_step_kernel<E, 2, 1><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
-    else if (p.N <= 16) scan_step_kernel<E, 4, 1><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
-    else if (p.N <= 32) scan_step_kernel<E, 4, 2><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
-    else scan_step_kernel<E, 4, 4><<<grid, 256, 0, s>>>(p, batch, states, num_slots, src, dst);
+    if (p.N == K * NS && p.per % (32 / K) == 0)
+        scan_step_kernel<E, K, NS, true><<<grid, NTH, smem, s>>>(p, batch, states, num_slots, src, dst);
+    else
+        scan_step_kernel<E, K, NS, false><<<grid, NTH, smem, s>>>(p, batch, states, num_slots, src, dst);
     return check_launch("scan_step_kernel");
+}
+
+template <typename E>
+gdn_status run_step(const ScanParams& p, int groups, int batch, float* states, int num_slots, const int32_t* src,
+                    const int32_t* dst, cudaStream_t s) {
+    if (p.N <= 4) return run_step_k<E, 1, 4>(p, groups, batch, states, num_slots, src, dst, s);
+    if (p.N <= 8) return run_step_k<E, 1, 8>(p, groups, batch, states, num_slots, src, dst, s);
+    if (p.N <= 16) {
+        // below three warps a scheduler the latency of a lane's 16 states counts: four lanes a channel then, each with
+        // a quarter of them (4096 channels: 1 request 2.4 against 3.0 us, 16 4.7 against 5.4, 64 10.8 against 8.0)
+        if ((int64_t)batch * p.ch <= (int64_t)device_sm_count() * 4 * 32 * 3)
+            return run_step_k<E, 4, 4>(p, groups, batch, states, num_slots, src, dst, s);
+        return run_step_k<E, 1, 16>(p, groups, batch, states, num_slots, src, dst, s);
+    }
+    if (p.N <= 32) return run_step_k<E, 2, 16>(p, groups, batch, states, num_slots, src, dst, s);
+    return run_step_k<E, 4, 16>(p, groups, batch, states, num_slots, src, dst, s);
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -575,8 +659,8 @@ gdn_status gdn_ssm_scan_step(const void* x, int64_t ldx, const void* dt, int64_t
     p.A_log = A_log; p.D = D; p.dt_bias = dt_bias; p.ch = channels; p.N = d_state; p.per = channels / groups; p.y = y;
     p.ldy = ldy;
     cudaStream_t s = (cudaStream_t)stream;
-    return dtype == GDN_BF16 ? run_step<__nv_bfloat16>(p, batch, states, num_slots, src, dst, s)
-                             : run_step<float>(p, batch, states, num_slots, src, dst, s);
+    return dtype == GDN_BF16 ? run_step<__nv_bfloat16>(p, groups, batch, states, num_slots, src, dst, s)
+                             : run_step<float>(p, groups, batch, states, num_slots, src, dst, s);
 }
 
 }  // extern "C"
