@@ -13,11 +13,6 @@
 // what it copied itself, no block-level synchronisation is needed.
 // Grid: (channel blocks, strips per shard, shards), with the strip length
 // chosen at launch so that all CTAs fit in one wave of resident blocks.
-// The STATE instances (one shard) give every sequence its own history rows
-// instead of zeros and write each sequence's last conv_k - 1 input rows: the
-// window at a sequence's start is loaded from its state, and the window after
-// its last row is its final state.  Their SiLU is a / (1 + e^-a) for both
-// types, so that a bf16 result is off by its own rounding only.
 #include "chunk_common.cuh"
 
 namespace gdn {
@@ -36,7 +31,6 @@ struct ConvParams {
     const void* halo; int halo_len;    // explicit mode
     const int32_t* plan; int P;        // shard mode
     int rows;                          // rows per strip (a multiple of RB)
-    const void* state; void* state_out;  // STATE: [num_seqs, Kc - 1, C] each, or null
 };
 
 template <typename T> struct Vec8;
@@ -109,35 +103,7 @@ __device__ __forceinline__ float silu<float>(float a) {
     return __fdividef(a, 1.f + __expf(fminf(-a, 80.f)));
 }
 
-// STATE: the window before a sequence's first row, and its rows after the last
-// one (exact: fp32 holds the loaded values).
 template <typename T, int KC>
-__device__ __forceinline__ void load_history(const ConvParams& p, int seq, int c0, float (&win)[KC > 1 ? KC - 1 : 1][8]) {
-#pragma unroll
-    for (int j = 0; j < KC - 1; ++j) {
-        if (p.state) Vec8<T>::load(static_cast<const T*>(p.state) + ((int64_t)seq * (KC - 1) + j) * p.C + c0, win[j]);
-        else
-#pragma unroll
-            for (int c = 0; c < 8; ++c) win[j][c] = 0.f;
-    }
-}
-template <typename T, int KC>
-__device__ __forceinline__ void store_history(const ConvParams& p, int seq, int c0,
-                                              const float (&win)[KC > 1 ? KC - 1 : 1][8]) {
-    if (!p.state_out) return;
-#pragma unroll
-    for (int j = 0; j < KC - 1; ++j)
-        Vec8<T>::store(static_cast<T*>(p.state_out) + ((int64_t)seq * (KC - 1) + j) * p.C + c0, win[j]);
-}
-// STATE: an empty sequence's final state is its initial one
-template <typename T, int KC>
-__device__ __forceinline__ void pass_history(const ConvParams& p, int seq, int c0) {
-    float h[KC > 1 ? KC - 1 : 1][8];
-    load_history<T, KC>(p, seq, c0, h);
-    store_history<T, KC>(p, seq, c0, h);
-}
-
-template <typename T, int KC, bool STATE>
 __global__ void __launch_bounds__(NT) conv_kernel(const ConvParams p) {
     const int c0 = (blockIdx.x * NT + threadIdx.x) * 8;
     if (c0 >= p.C) return;
@@ -193,10 +159,6 @@ __global__ void __launch_bounds__(NT) conv_kernel(const ConvParams p) {
         if (lrow >= seg_start && lrow >= 0) {
             have = true;
             src = x + (int64_t)(rs + lrow) * p.ldx + c0;
-        } else if (STATE) {
-            const int m = KC - 1 - (seg_start - lrow);  // row of the sequence's state
-            have = p.state != nullptr && m >= 0 && m < KC - 1;
-            if (have) src = static_cast<const T*>(p.state) + ((int64_t)seg * (KC - 1) + m) * p.C + c0;
         } else if (seg == 0 && seg_start - lrow <= hlen) {
             const int m = seg_start - lrow;  // rows before the shard start (1 = adjacent)
             have = true;
@@ -209,8 +171,6 @@ __global__ void __launch_bounds__(NT) conv_kernel(const ConvParams p) {
             for (int c = 0; c < 8; ++c) win[j][c] = 0.f;
         }
     }
-    if (STATE && lt0 == seg_start)  // empty sequences that end where this strip starts
-        for (int m = seg - 1; m >= 0 && lc[m] == lt0; --m) pass_history<T, KC>(p, m, c0);
     // ring of NSTAGE batches: stage b holds rows [lt0 + RB b, lt0 + RB (b + 1))
     constexpr int VEC = sizeof(T) * 8 / 16;  // 16-byte vectors per row and thread
     extern __shared__ uint4 ring[];          // [NSTAGE][RB][VEC][NT]
@@ -241,22 +201,12 @@ __global__ void __launch_bounds__(NT) conv_kernel(const ConvParams p) {
             const int t = lt0 + RB * b + u;
             if (t >= lt1) break;
             while (t == next) {  // a new sequence starts: no history
-                if constexpr (STATE) {
-                    store_history<T, KC>(p, seg, c0, win);
-                    if (++seg >= nloc) {  // malformed cu
-                        next = part;
-                    } else {
-                        load_history<T, KC>(p, seg, c0, win);
-                        next = lc[seg + 1];
-                    }
-                } else {
 #pragma unroll
-                    for (int j = 0; j < KC - 1; ++j)
+                for (int j = 0; j < KC - 1; ++j)
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) win[j][c] = 0.f;
-                    ++seg;
-                    next = seg + 1 <= nloc ? lc[seg + 1] : part;
-                }
+                    for (int c = 0; c < 8; ++c) win[j][c] = 0.f;
+                ++seg;
+                next = seg + 1 <= nloc ? lc[seg + 1] : part;
             }
             float cur[8], out[8];
             uint4 rv[VEC];
@@ -269,7 +219,7 @@ __global__ void __launch_bounds__(NT) conv_kernel(const ConvParams p) {
 #pragma unroll
                 for (int j = 0; j < KC - 1; ++j) acc = fmaf(wr[j][c], win[j][c], acc);
                 acc = fmaf(wr[KC - 1][c], cur[c], acc);
-                out[c] = STATE ? silu<float>(acc) : silu<T>(acc);
+                out[c] = silu<T>(acc);
             }
             Vec8<T>::store(y + (int64_t)(rs + t) * p.ldy + c0, out);
 #pragma unroll
@@ -282,19 +232,6 @@ __global__ void __launch_bounds__(NT) conv_kernel(const ConvParams p) {
             }
         }
     }
-    if (STATE && next == lt1 && seg < nloc) {  // the sequence ends with the strip
-        store_history<T, KC>(p, seg, c0, win);
-        if (lt1 == part)  // empty sequences behind the last token
-            for (int m = seg + 1; m < nloc; ++m) pass_history<T, KC>(p, m, c0);
-    }
-}
-
-// STATE with no rows at all: every sequence is empty
-template <typename T, int KC>
-__global__ void __launch_bounds__(NT) conv_pass_state_kernel(const ConvParams p) {
-    const int c0 = (blockIdx.x * NT + threadIdx.x) * 8;
-    if (c0 >= p.C) return;
-    for (int m = blockIdx.y; m < p.num_seqs; m += gridDim.y) pass_history<T, KC>(p, m, c0);
 }
 
 }  // namespace
@@ -304,7 +241,7 @@ gdn_status set_smem_attr(const void* func, size_t bytes);
 namespace {
 
 // Resident CTAs of the instance on the current device (cached per device).
-template <typename T, int KC, bool STATE>
+template <typename T, int KC>
 int resident_slots(size_t smem) {
     static int cache[64];
     int dev = 0;
@@ -312,21 +249,21 @@ int resident_slots(size_t smem) {
     if (cache[dev] > 0) return cache[dev];
     int sms = 0, per = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, conv_kernel<T, KC, STATE>, NT, smem) != cudaSuccess)
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, conv_kernel<T, KC>, NT, smem) != cudaSuccess)
         return 0;
     return cache[dev] = sms * per;
 }
 
-template <typename T, int KC, bool STATE>
+template <typename T, int KC>
 gdn_status launch_tk(ConvParams p, dim3 grid, cudaStream_t s) {
     const size_t smem = (size_t)NSTAGE * RB * (sizeof(T) * 8 / 16) * NT * 16;
-    gdn_status st = set_smem_attr((const void*)conv_kernel<T, KC, STATE>, smem);
+    gdn_status st = set_smem_attr((const void*)conv_kernel<T, KC>, smem);
     if (st != GDN_OK) return st;
     // strips per shard: the CTAs fill whole waves of resident slots (a partly
     // filled last wave moves its bytes at a fraction of the bandwidth), with
     // strips of at least 64 rows so that the K-1 halo rows stay a small overhead
     const int part = p.T / p.P;
-    const int slots = resident_slots<T, KC, STATE>(smem);
+    const int slots = resident_slots<T, KC>(smem);
     const int per = (int)grid.x * p.P;
     const int nmax = max(1, part / 64);
     int n = (part + 127) / 128;
@@ -347,17 +284,17 @@ gdn_status launch_tk(ConvParams p, dim3 grid, cudaStream_t s) {
     int rows = (part + n - 1) / n;
     p.rows = (rows + RB - 1) / RB * RB;
     grid.y = (part + p.rows - 1) / p.rows;
-    conv_kernel<T, KC, STATE><<<grid, NT, smem, s>>>(p);
+    conv_kernel<T, KC><<<grid, NT, smem, s>>>(p);
     return check_launch("conv_kernel");
 }
 
-template <typename T, bool STATE>
+template <typename T>
 gdn_status launch_t(const ConvParams& p, dim3 grid, cudaStream_t s) {
     switch (p.Kc) {
-        case 1: return launch_tk<T, 1, STATE>(p, grid, s);
-        case 2: return launch_tk<T, 2, STATE>(p, grid, s);
-        case 3: return launch_tk<T, 3, STATE>(p, grid, s);
-        case 4: return launch_tk<T, 4, STATE>(p, grid, s);
+        case 1: return launch_tk<T, 1>(p, grid, s);
+        case 2: return launch_tk<T, 2>(p, grid, s);
+        case 3: return launch_tk<T, 3>(p, grid, s);
+        case 4: return launch_tk<T, 4>(p, grid, s);
     }
     return fail(GDN_ERR_UNSUPPORTED_SHAPE, "conv_k=%d not in 1..4", p.Kc);
 }
@@ -368,31 +305,11 @@ gdn_status launch_conv(const void* x, int64_t ldx, gdn_dtype dt, int T, int C, c
                        const void* b, int Kc, const int32_t* cu, int num_seqs, const void* halo,
                        int halo_len, void* y, int64_t ldy, const int32_t* plan, int P,
                        cudaStream_t s) {
-    ConvParams p{x, ldx, y, ldy, w, b, T, C, Kc, cu, num_seqs, halo, halo_len, plan, plan ? P : 1, 128, nullptr, nullptr};
+    ConvParams p{x, ldx, y, ldy, w, b, T, C, Kc, cu, num_seqs, halo, halo_len, plan, plan ? P : 1, 128};
     const int part = T / p.P;
     dim3 grid((C / 8 + NT - 1) / NT, 1, p.P);
     if (part <= 0) return GDN_OK;
-    return dt == GDN_BF16 ? launch_t<__nv_bfloat16, false>(p, grid, s) : launch_t<float, false>(p, grid, s);
-}
-
-gdn_status launch_conv_state(const void* x, int64_t ldx, gdn_dtype dt, int T, int C, const void* w, const void* b,
-                             int Kc, const int32_t* cu, int num_seqs, const void* state, void* state_out, void* y,
-                             int64_t ldy, cudaStream_t s) {
-    ConvParams p{x, ldx, y, ldy, w, b, T, C, Kc, cu, num_seqs, nullptr, 0, nullptr, 1, 128, state, state_out};
-    dim3 grid((C / 8 + NT - 1) / NT, 1, 1);
-    if (T > 0) return dt == GDN_BF16 ? launch_t<__nv_bfloat16, true>(p, grid, s) : launch_t<float, true>(p, grid, s);
-    if (!state_out || Kc == 1) return GDN_OK;
-    grid.y = num_seqs < 1024 ? num_seqs : 1024;
-    if (dt == GDN_BF16) {
-        if (Kc == 2) conv_pass_state_kernel<__nv_bfloat16, 2><<<grid, NT, 0, s>>>(p);
-        else if (Kc == 3) conv_pass_state_kernel<__nv_bfloat16, 3><<<grid, NT, 0, s>>>(p);
-        else conv_pass_state_kernel<__nv_bfloat16, 4><<<grid, NT, 0, s>>>(p);
-    } else {
-        if (Kc == 2) conv_pass_state_kernel<float, 2><<<grid, NT, 0, s>>>(p);
-        else if (Kc == 3) conv_pass_state_kernel<float, 3><<<grid, NT, 0, s>>>(p);
-        else conv_pass_state_kernel<float, 4><<<grid, NT, 0, s>>>(p);
-    }
-    return check_launch("conv_pass_state_kernel");
+    return dt == GDN_BF16 ? launch_t<__nv_bfloat16>(p, grid, s) : launch_t<float>(p, grid, s);
 }
 
 }  // namespace gdn

@@ -391,10 +391,6 @@ gdn_status launch_conv(const void* x, int64_t ldx, gdn_dtype dt, int T, int C, c
                        const void* b, int Kc, const int32_t* cu, int num_seqs, const void* halo,
                        int halo_len, void* y, int64_t ldy, const int32_t* plan, int P,
                        cudaStream_t s);
-// conv.cu: one shard, with a state per sequence
-gdn_status launch_conv_state(const void* x, int64_t ldx, gdn_dtype dt, int T, int C, const void* w, const void* b,
-                             int Kc, const int32_t* cu, int num_seqs, const void* state, void* state_out, void* y,
-                             int64_t ldy, cudaStream_t s);
 // block_norm.cu: sums over the rows of a [rows, stride] fp32 array in a fixed
 // order; columns below n0 go to out0, below n1 to out1, the rest to out2
 gdn_status launch_column_sum(const float* part, int rows, int64_t stride, int64_t n0, int64_t n1, float* out0,

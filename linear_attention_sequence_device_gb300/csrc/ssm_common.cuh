@@ -146,7 +146,11 @@ __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.b) : "l"(a.b), "l"(b.b));
     return r;
 }
-__device__ __forceinline__ F2 f2_sigmoid(F2 v) { return f2(sigmoid_fast(v.x()), sigmoid_fast(v.y())); }
+__device__ __forceinline__ F2 f2_sigmoid(F2 v) {
+    const F2 e = f2_add(f2_exp2(f2_mul(v, f2_dup(-kLog2e))), f2_dup(1.f));
+    return f2(rcp_fast(e.x()), rcp_fast(e.y()));
+}
+__device__ __forceinline__ F2 f2_silu(F2 v) { return f2_mul(v, f2_sigmoid(v)); }
 // eight consecutive elements (16-byte aligned) as four pairs
 __device__ __forceinline__ void f2_load8(const __nv_bfloat16* p, F2 (&f)[4]) {
     const uint4 r = *reinterpret_cast<const uint4*>(p);

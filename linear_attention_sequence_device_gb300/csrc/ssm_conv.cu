@@ -1,5 +1,5 @@
-// The selective scan layer's short convolution: its gradient, its single-token
-// form and the C entry points (the prompt's forward is conv.cu's STATE form).
+// The selective scan layer's short convolution over packed sequences, each with
+// its own state: forward, gradient, single-token form and the C entry points.
 //
 // Forward: pre[t] = b + sum_j w[j] x'[t - K + 1 + j], y = pre s(pre), s the
 // logistic function.  Backward, with ds[t] = dy s (1 + pre (1 - s)):
@@ -7,14 +7,18 @@
 //   dw[j] = sum_t ds[t] x'[t - K + 1 + j],  db = sum_t ds[t];
 // the gradients of the K - 1 rows before a sequence's start are its state's,
 // and dstate_out adds to the last K - 1 rows.
+#include "chunk_common.cuh"
 #include "ssm_common.cuh"
 
 namespace gdn {
+
+gdn_status set_smem_attr(const void* func, size_t bytes);
+
 namespace {
 
 constexpr int NT = 128;
 constexpr int CV = 4;   // channels per thread of the backward
-constexpr int RB = 4;   // rows loaded ahead
+constexpr int RB = 4;   // rows per batch
 
 // four channels as they come, and as two pairs
 template <typename T> struct Raw4;
@@ -39,6 +43,160 @@ template <> struct Raw4<float> {
     __device__ __forceinline__ void unpack(F2 (&f)[2]) const { f[0].b = v.x; f[1].b = v.y; }
     static __device__ __forceinline__ void store(float* p, const F2 (&f)[2]) { f2_store2(p, f[0], f[1]); }
 };
+
+struct ConvParams {
+    const void* x; int64_t ldx;
+    const void* w; const void* b;
+    int T, C;
+    const int32_t* cu; int num_seqs;
+    const void* state; void* state_out;
+    void* y; int64_t ldy;
+    int rows;  // rows per strip, a multiple of RB
+};
+
+// weights of N channels from c0 on, as pairs of channels
+template <typename T, int K, int N>
+__device__ __forceinline__ void load_weights(const void* w, const void* b, int c0, F2 (&wv)[K][N / 2], F2 (&bv)[N / 2]) {
+    const T *wp = static_cast<const T*>(w) + (int64_t)c0 * K, *bp = static_cast<const T*>(b) + c0;
+#pragma unroll
+    for (int h = 0; h < N / 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            wv[j][h] = f2(Elem<T>::to_f(wp[2 * h * K + j]), Elem<T>::to_f(wp[(2 * h + 1) * K + j]));
+        bv[h] = b ? f2(Elem<T>::to_f(bp[2 * h]), Elem<T>::to_f(bp[2 * h + 1])) : f2_dup(0.f);
+    }
+}
+
+// Forward.  HBM-bound: x in, y out, each once.  A thread owns eight channels of a
+// strip of rows and walks down it with a window of the last K - 1 inputs; rows come
+// by asynchronous copies into a ring of NSTAGE batches of RB rows that it fills and
+// reads alone.  A batch that no sequence starts in, all but a few, runs without a
+// check, which also lets the window stay where it is instead of moving up row by
+// row.  The SiLU is a / (1 + e^-a) for both types, so that a bf16 result is off by
+// its own rounding only; in pairs that is 3 issue slots an element.
+constexpr int NSTAGE = 4;
+template <typename T, int K>
+__global__ void __launch_bounds__(NT, 4) conv_fwd_kernel(const ConvParams p) {
+    constexpr int H = K > 1 ? K - 1 : 1, VEC = sizeof(T) * 8 / 16;
+    const int c0 = (blockIdx.x * NT + threadIdx.x) * 8;
+    if (c0 >= p.C) return;
+    const int nseq = p.num_seqs, tid = threadIdx.x;
+    const int32_t* cu = p.cu;
+    const T* x = static_cast<const T*>(p.x) + c0;
+    T* y = static_cast<T*>(p.y) + c0;
+    F2 win[H][4];
+    auto load_state = [&](int seq) {
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            if (p.state) f2_load8(static_cast<const T*>(p.state) + ((int64_t)seq * (K - 1) + j) * p.C + c0, win[j]);
+            else
+#pragma unroll
+                for (int i = 0; i < 4; ++i) win[j][i] = f2_dup(0.f);
+        }
+    };
+    auto store_state = [&](int seq) {  // exact: the window holds the values as loaded
+        if (p.state_out)
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+                f2_store8(static_cast<T*>(p.state_out) + ((int64_t)seq * (K - 1) + j) * p.C + c0, win[j]);
+    };
+    auto pass_empty = [&](int seq) {  // its final state is its initial one
+        load_state(seq);
+        store_state(seq);
+    };
+    if (p.T == 0) {
+        if (blockIdx.y == 0)
+            for (int m = 0; m < nseq; ++m) pass_empty(m);
+        return;
+    }
+    const int lt0 = blockIdx.y * p.rows, lt1 = min(p.T, lt0 + p.rows);
+    if (lt0 >= p.T) return;
+    int seg = seq_of(cu, nseq, lt0);
+    const int start = __ldg(cu + seg);
+    int next = __ldg(cu + seg + 1);
+    if (start == lt0)  // empty sequences that end where this strip starts
+        for (int m = seg - 1; m >= 0 && __ldg(cu + m) == lt0; --m) pass_empty(m);
+
+    extern __shared__ uint4 ring[];  // [NSTAGE][RB][VEC][NT]
+    const int nb = (lt1 - lt0 + RB - 1) / RB;
+    auto issue = [&](int b) {
+        if (b < nb) {
+            uint4* st = ring + (size_t)(b % NSTAGE) * RB * VEC * NT + tid;
+#pragma unroll
+            for (int u = 0; u < RB; ++u) {
+                const int t = lt0 + RB * b + u;
+                const T* src = x + (int64_t)min(t, lt1 - 1) * p.ldx;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    cp_async16(st + (u * VEC + v) * NT, reinterpret_cast<const uint4*>(src) + v, t < lt1 ? 16 : 0);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int b = 0; b < NSTAGE - 1; ++b) issue(b);
+
+    F2 w[K][4], b[4];
+    load_weights<T, K, 8>(p.w, p.b, c0, w, b);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        const int row = lt0 - (K - 1) + j, m = K - 1 - (start - row);  // m: its row of the state
+        if (row >= start && row >= 0) f2_load8(x + (int64_t)row * p.ldx, win[j]);
+        else if (p.state && m >= 0 && m < K - 1)
+            f2_load8(static_cast<const T*>(p.state) + ((int64_t)seg * (K - 1) + m) * p.C + c0, win[j]);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i) win[j][i] = f2_dup(0.f);
+    }
+    for (int bt = 0; bt < nb; ++bt) {
+        issue(bt + NSTAGE - 1);
+        cp_async_wait<NSTAGE - 1>();
+        const uint4* st = ring + (size_t)(bt % NSTAGE) * RB * VEC * NT + tid;
+        const int tb = lt0 + RB * bt;
+        auto row = [&](int u) {
+            uint4 raw[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) raw[v] = st[(u * VEC + v) * NT];
+            F2 cur[4], out[4];
+            f2_load8(reinterpret_cast<const T*>(raw), cur);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                F2 a = b[i];
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) a = f2_fma(w[j][i], win[j][i], a);
+                out[i] = f2_silu(f2_fma(w[K - 1][i], cur[i], a));
+#pragma unroll
+                for (int j = 0; j + 1 < K - 1; ++j) win[j][i] = win[j + 1][i];
+                if (K > 1) win[H - 1][i] = cur[i];
+            }
+            f2_store8(y + (int64_t)(tb + u) * p.ldy, out);
+        };
+        if (tb + RB <= lt1 && next >= tb + RB) {
+#pragma unroll
+            for (int u = 0; u < RB; ++u) row(u);
+        } else {
+#pragma unroll 1
+            for (int u = 0; u < RB && tb + u < lt1; ++u) {
+                while (tb + u == next) {  // a sequence ends and the next one starts
+                    store_state(seg);
+                    if (++seg >= nseq) {
+                        next = p.T;  // malformed cu
+                    } else {
+                        load_state(seg);
+                        next = __ldg(cu + seg + 1);
+                    }
+                }
+                row(u);
+            }
+        }
+    }
+    cp_async_wait<0>();
+    if (next == lt1 && seg < nseq) {  // the sequence ends with the strip
+        store_state(seg);
+        if (lt1 == p.T)  // empty sequences behind the last token
+            for (int m = seg + 1; m < nseq; ++m) pass_empty(m);
+    }
+}
 
 struct ConvBwdParams {
     const void* dy; int64_t lddy;
@@ -95,18 +253,12 @@ __global__ void __launch_bounds__(NT, 4) conv_bwd_kernel(const ConvBwdParams p) 
 
     F2 w[K][2], b[2], dw[K][2], db[2];
     const F2 zero = f2_dup(0.f), one = f2_dup(1.f), neg = f2_dup(-1.f);
-    {
-        const T *wp = static_cast<const T*>(p.w) + (int64_t)c0 * K, *bp = static_cast<const T*>(p.b) + c0;
+    load_weights<T, K, 4>(p.w, p.b, c0, w, b);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < K; ++j) {
-                w[j][h] = f2(Elem<T>::to_f(wp[2 * h * K + j]), Elem<T>::to_f(wp[(2 * h + 1) * K + j]));
-                dw[j][h] = zero;
-            }
-            b[h] = p.b ? f2(Elem<T>::to_f(bp[2 * h]), Elem<T>::to_f(bp[2 * h + 1])) : zero;
-            db[h] = zero;
-        }
+        for (int j = 0; j < K; ++j) dw[j][h] = zero;
+        db[h] = zero;
     }
     const int lt0 = blockIdx.y * p.rows, lt1 = min(p.T, lt0 + p.rows);
     if (p.T == 0) {
@@ -326,6 +478,34 @@ int bwd_strips(int T, int C) {
     return n < 1 ? 1 : n;
 }
 
+template <typename T, int K>
+gdn_status run_fwd_k(ConvParams p, cudaStream_t s) {
+    constexpr size_t smem = (size_t)NSTAGE * RB * sizeof(T) * 8 * NT;
+    if (smem > (48 << 10)) {
+        const gdn_status st = set_smem_attr((const void*)conv_fwd_kernel<T, K>, smem);
+        if (st != GDN_OK) return st;
+    }
+    // strips: one wave of four blocks an SM, of 64 rows at least
+    const int nx = (p.C / 8 + NT - 1) / NT;
+    int n = device_sm_count() * 4 / nx;
+    if (n > p.T / 64) n = p.T / 64;
+    if (n > 65535) n = 65535;
+    if (n < 1) n = 1;
+    p.rows = p.T > 0 ? ((p.T + n - 1) / n + RB - 1) / RB * RB : RB;
+    const int strips = p.T > 0 ? (p.T + p.rows - 1) / p.rows : 1;
+    conv_fwd_kernel<T, K><<<dim3(nx, strips), NT, smem, s>>>(p);
+    return check_launch("conv_fwd_kernel");
+}
+template <typename T>
+gdn_status run_fwd(const ConvParams& p, int K, cudaStream_t s) {
+    switch (K) {
+        case 1: return run_fwd_k<T, 1>(p, s);
+        case 2: return run_fwd_k<T, 2>(p, s);
+        case 3: return run_fwd_k<T, 3>(p, s);
+        default: return run_fwd_k<T, 4>(p, s);
+    }
+}
+
 template <typename T>
 gdn_status run_bwd(ConvBwdParams p, int K, cudaStream_t s) {
     const int strips = bwd_strips(p.T, p.C);
@@ -395,8 +575,9 @@ gdn_status gdn_ssm_conv_fwd(const void* x, int64_t ldx, gdn_dtype dtype, int32_t
         if ((st = check_rows(x, ldx, channels, "x")) != GDN_OK) return st;
         if ((st = check_rows(y, ldy, channels, "y")) != GDN_OK) return st;
     }
-    return launch_conv_state(x, ldx, dtype, T, channels, w, bias, conv_k, cu_seqlens, num_seqs, state, state_out, y,
-                             ldy, (cudaStream_t)stream);
+    ConvParams p{x, ldx, w, bias, T, channels, cu_seqlens, num_seqs, state, state_out, y, ldy, 0};
+    cudaStream_t s = (cudaStream_t)stream;
+    return dtype == GDN_BF16 ? run_fwd<__nv_bfloat16>(p, conv_k, s) : run_fwd<float>(p, conv_k, s);
 }
 
 size_t gdn_ssm_conv_bwd_workspace_size(int32_t T, int32_t channels, int32_t conv_k) {
