@@ -25,6 +25,7 @@ template <typename T> struct Raw4;
 template <> struct Raw4<__nv_bfloat16> {
     uint2 v;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void take(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
     __device__ __forceinline__ void unpack(F2 (&f)[2]) const {
         f[0] = f2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
         f[1] = f2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
@@ -40,6 +41,7 @@ template <> struct Raw4<__nv_bfloat16> {
 template <> struct Raw4<float> {
     ulonglong2 v;
     __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const ulonglong2*>(p)); }
+    __device__ __forceinline__ void take(const float* p) { v = *reinterpret_cast<const ulonglong2*>(p); }
     __device__ __forceinline__ void unpack(F2 (&f)[2]) const { f[0].b = v.x; f[1].b = v.y; }
     static __device__ __forceinline__ void store(float* p, const F2 (&f)[2]) { f2_store2(p, f[0], f[1]); }
 };
@@ -198,6 +200,12 @@ __global__ void __launch_bounds__(NT, 4) conv_fwd_kernel(const ConvParams p) {
     }
 }
 
+// four channels' copy, 8 or 16 bytes
+__device__ __forceinline__ void copy4(__nv_bfloat16* dst, const __nv_bfloat16* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src));
+}
+__device__ __forceinline__ void copy4(float* dst, const float* src) { cp_async16(dst, src, 16); }
+
 struct ConvBwdParams {
     const void* dy; int64_t lddy;
     const void* x; int64_t ldx;
@@ -217,8 +225,9 @@ struct ConvBwdParams {
 // its end (within the sequence) for the dx of its own last rows; those rows'
 // dw and db belong to the next strip.  Groups of four rows that touch no sequence's
 // end and no strip's edge, all but a few, run without a check.  Channels go in
-// pairs through the two-wide instructions: about 26 issue slots an element where
-// single ones took 44, which at four blocks an SM had bounded it.
+// pairs through the two-wide instructions: single ones took 44 issue slots an
+// element, which bounded it at 290 us for 65536 x 2048.  x and dy come through a ring
+// as in the forward.
 template <typename T, int K>
 __global__ void __launch_bounds__(NT, 4) conv_bwd_kernel(const ConvBwdParams p) {
     constexpr int H = K > 1 ? K - 1 : 1;
@@ -332,26 +341,34 @@ __global__ void __launch_bounds__(NT, 4) conv_bwd_kernel(const ConvBwdParams p) 
                 }
             }
         };
-        const int tend = min(p.T, lt1 + K - 1);
-        Raw4<T> nx[RB], ny[RB];
-        auto fetch = [&](int t) {
-#pragma unroll
-            for (int u = 0; u < RB; ++u) {
-                const int r = min(t + u, p.T - 1);
-                nx[u].load(x + (int64_t)r * p.ldx);
-                ny[u].load(dy + (int64_t)r * p.lddy);
-            }
+        const int tend = min(p.T, lt1 + K - 1), nb = (tend - lt0 + RB - 1) / RB;
+        extern __shared__ uint4 ring[];  // [NSTAGE][RB][x, dy][NT][CV] elements
+        auto slot = [&](int b, int u, int a) {
+            return reinterpret_cast<T*>(ring) + (((b % NSTAGE * RB + u) * 2 + a) * NT + threadIdx.x) * CV;
         };
-        fetch(lt0);
+        auto issue = [&](int b) {
+            if (b < nb)
+#pragma unroll
+                for (int u = 0; u < RB; ++u) {
+                    const int r = min(lt0 + RB * b + u, tend - 1);
+                    copy4(slot(b, u, 0), x + (int64_t)r * p.ldx);
+                    copy4(slot(b, u, 1), dy + (int64_t)r * p.lddy);
+                }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < NSTAGE - 1; ++i) issue(i);
         bool done = false;
-        for (int tb = lt0; tb < tend && !done; tb += RB) {
+        for (int bt = 0; bt < nb && !done; ++bt) {
+            const int tb = lt0 + RB * bt;
+            issue(bt + NSTAGE - 1);
+            cp_async_wait<NSTAGE - 1>();
             Raw4<T> cx[RB], cy[RB];
 #pragma unroll
             for (int u = 0; u < RB; ++u) {
-                cx[u] = nx[u];
-                cy[u] = ny[u];
+                cx[u].take(slot(bt, u, 0));
+                cy[u].take(slot(bt, u, 1));
             }
-            if (tb + RB < tend) fetch(tb + RB);
             if (tb + RB <= lt1 && next > tb + RB && tb - (K - 1) >= max(start, lt0)) {
                 T* out = dx + (int64_t)(tb - (K - 1)) * p.lddx;
 #pragma unroll
@@ -398,6 +415,7 @@ __global__ void __launch_bounds__(NT, 4) conv_bwd_kernel(const ConvBwdParams p) 
                 }
             }
         }
+        cp_async_wait<0>();
         if (lt1 == p.T && next == p.T)
             for (int m = seg + 1; m < nseq; ++m) pass_empty(m);
     }
@@ -506,18 +524,27 @@ gdn_status run_fwd(const ConvParams& p, int K, cudaStream_t s) {
     }
 }
 
+template <typename T, int K>
+gdn_status run_bwd_k(const ConvBwdParams& p, dim3 grid, cudaStream_t s) {
+    constexpr size_t smem = (size_t)NSTAGE * RB * 2 * NT * CV * sizeof(T);
+    if (smem > (48 << 10)) {
+        const gdn_status st = set_smem_attr((const void*)conv_bwd_kernel<T, K>, smem);
+        if (st != GDN_OK) return st;
+    }
+    conv_bwd_kernel<T, K><<<grid, NT, smem, s>>>(p);
+    return check_launch("conv_bwd_kernel");
+}
 template <typename T>
 gdn_status run_bwd(ConvBwdParams p, int K, cudaStream_t s) {
     const int strips = bwd_strips(p.T, p.C);
     p.rows = p.T > 0 ? (p.T + strips - 1) / strips : 1;
     const dim3 grid((p.C / CV + NT - 1) / NT, strips);
     switch (K) {
-        case 1: conv_bwd_kernel<T, 1><<<grid, NT, 0, s>>>(p); break;
-        case 2: conv_bwd_kernel<T, 2><<<grid, NT, 0, s>>>(p); break;
-        case 3: conv_bwd_kernel<T, 3><<<grid, NT, 0, s>>>(p); break;
-        default: conv_bwd_kernel<T, 4><<<grid, NT, 0, s>>>(p); break;
+        case 1: return run_bwd_k<T, 1>(p, grid, s);
+        case 2: return run_bwd_k<T, 2>(p, grid, s);
+        case 3: return run_bwd_k<T, 3>(p, grid, s);
+        default: return run_bwd_k<T, 4>(p, grid, s);
     }
-    return check_launch("conv_bwd_kernel");
 }
 
 template <typename T>
