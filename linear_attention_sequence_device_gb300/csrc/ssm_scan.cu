@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
                     store_state(p.h_final, m);
                 }
             load_state(p.h0, n);
+        } else if (p.folded) {
+            load_state(p.H, s - 1);
         } else {
             const int j0 = max(start, 0) / p.seg;
             load_state(p.H, j0);
@@ -296,6 +298,52 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
     }
 }
 
+// The fold of the segments' own ends (REV: start gradients) into the states at the
+// segments' starts (the gradients behind their ends), in place: row s - 1 becomes
+// the state at segment s's start (row s + 1 the gradient behind segment s), for
+// segments in the middle of a sequence.  One thread per channel and state.
+constexpr int FTH = 256;
+template <bool REV>
+__global__ void __launch_bounds__(FTH) scan_fold_kernel(const ScanParams p) {
+    extern __shared__ unsigned char kind[];  // [S]: 0 no fold ends here, 1 the row as it is, 2 folded with the one before
+    for (int s = threadIdx.x; s < p.S; s += FTH) {
+        int kd = 0;
+        if (!REV && s > 0) {
+            const int t0 = s * p.seg, start = max(__ldg(p.cu + seq_of(p.cu, p.num_seqs, t0)), 0);
+            if (start < t0) kd = start / p.seg == s - 1 ? 1 : 2;
+        } else if (REV && s < p.S - 1) {
+            const int te = (s + 1) * p.seg, end = min(__ldg(p.cu + seq_of(p.cu, p.num_seqs, te - 1) + 1), p.T);
+            if (end > te) kd = (end - 1) / p.seg == s + 1 ? 1 : 2;
+        }
+        kind[s] = kd;
+    }
+    __syncthreads();
+    const int64_t i = (int64_t)blockIdx.x * FTH + threadIdx.x;
+    if (i >= (int64_t)p.ch * p.N) return;
+    const float A2 = -expf(__ldg(p.A_log + i)) * kLog2e;
+    const int c = (int)(i / p.N);
+    float v = 0.f;
+    constexpr int U = 16;  // rows loaded at a time: the walk is bound by their latency
+    for (int b = 1; b < p.S; b += U) {
+        float Hr[U], d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = min(b + u, p.S - 1), row = REV ? p.S - q : q - 1;
+            Hr[u] = p.H[(int64_t)row * p.ch * p.N + i];
+            d[u] = p.sd[(int64_t)row * p.ch + c];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = b + u, row = REV ? p.S - q : q - 1;
+            if (q >= p.S) break;
+            const int kd = kind[REV ? p.S - 1 - q : q];
+            if (kd == 0) continue;
+            v = kd == 1 ? Hr[u] : fmaf(exp2_fast(d[u] * A2), v, Hr[u]);
+            if (kd == 2) p.H[(int64_t)row * p.ch * p.N + i] = v;
+        }
+    }
+}
+
 constexpr int STG = 4;     // requests whose states are in flight or in use (step)
 
 // One token per request.  Bound by the states, read and written once (for a few
@@ -460,12 +508,15 @@ __global__ void __launch_bounds__(NTH, 4) scan_step_kernel(const ScanParams p, i
 
 int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH / 4); }
 
-// Segments of a call: enough blocks for four resident ones an SM, of 64 tokens
-// or more; multiples of 64 so that the checkpoints fall on tile starts.
+// Segments of a call: one wave of four resident blocks an SM, two where that
+// leaves segments of 512 tokens or more (the last blocks' idle time halves: 2.05 ->
+// 1.99 ms on 131072 tokens of 2048 channels), of 64 tokens or more; multiples of 64
+// so that the checkpoints fall on tile starts.
 void segments(int T, int ch, int N, int groups, int& seg, int& S) {
     const int per = ch / groups, cb = channels_per_block(N);
     const int64_t blocks = (int64_t)groups * ((per + cb - 1) / cb);
     int64_t want = (int64_t)device_sm_count() * 4 / blocks;
+    if (T >= 2 * want * 512) want *= 2;
     if (want < 1) want = 1;
     const int64_t most = (T + 63) / 64;
     if (want > most) want = most;
@@ -495,14 +546,27 @@ gdn_status run_mode(const ScanParams& p, dim3 grid, cudaStream_t s) {
     return check_launch("scan_kernel");
 }
 
+template <bool REV>
+gdn_status run_fold(const ScanParams& p, cudaStream_t s) {
+    const int64_t n = (int64_t)p.ch * p.N;
+    scan_fold_kernel<REV><<<(unsigned)((n + FTH - 1) / FTH), FTH, p.S, s>>>(p);
+    return check_launch("scan_fold_kernel");
+}
+
 template <typename E, int K, int NS>
 gdn_status run_scan(ScanParams p, int groups, bool grad, cudaStream_t s) {
     p.tiles = (p.per + NTH / K - 1) / (NTH / K);
     const dim3 all(groups * p.tiles, p.S), joints(groups * p.tiles, p.S - 1);
-    if (grad) return p.S > 1 ? run_mode<E, K, NS, SCAN_START_GRAD>(p, joints, s) : GDN_OK;
+    gdn_status st;
+    if (grad) {
+        if (p.S == 1) return GDN_OK;
+        if ((st = run_mode<E, K, NS, SCAN_START_GRAD>(p, joints, s)) != GDN_OK) return st;
+        return p.S > kFoldSegments ? run_fold<true>(p, s) : GDN_OK;
+    }
     if (p.S > 1) {
-        const gdn_status st = run_mode<E, K, NS, SCAN_END>(p, joints, s);
-        if (st != GDN_OK) return st;
+        if ((st = run_mode<E, K, NS, SCAN_END>(p, joints, s)) != GDN_OK) return st;
+        p.folded = p.S > kFoldSegments;
+        if (p.folded && (st = run_fold<false>(p, s)) != GDN_OK) return st;
     }
     return run_mode<E, K, NS, SCAN_FULL>(p, all, s);
 }

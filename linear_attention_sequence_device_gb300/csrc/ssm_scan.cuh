@@ -21,6 +21,7 @@ struct ScanParams {
     float* h_final; float* ckpt;     // ckpt [ceil(T / kCkpt), ch, N]
     int seg, S;                      // tokens per segment, segments
     float* H; float* sd;             // [S, ch, N], [S, ch]
+    bool folded;                     // H's row s - 1 holds the state at segment s's start already
 };
 
 // Which part of a segment a scan_kernel launch runs: the outputs; only the end
@@ -29,6 +30,9 @@ struct ScanParams {
 // sends to the state before it (x, B and h0 are then dy, C and dh_final).
 enum ScanMode : int { SCAN_FULL = 0, SCAN_END = 1, SCAN_START_GRAD = 2 };
 
+// Segments above which the rows of H are folded once by a launch of their own
+// instead of by every block for its own channels.
+constexpr int kFoldSegments = 4;
 gdn_status launch_scan_start_grad(const ScanParams& p, gdn_dtype dtype, int groups, cudaStream_t s);
 
 // argument checks (ssm_scan.cu)

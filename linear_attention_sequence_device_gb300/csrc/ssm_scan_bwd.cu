@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
         if (end <= te) {
             load_state(dh, p.dhf, n);
         } else {
-            const int je = (min(end, p.T) - 1) / p.seg;
+            const int je = p.S > kFoldSegments ? s + 1 : (min(end, p.T) - 1) / p.seg;  // folded: the next row is all
             load_state(dh, p.G, je);
             for (int j = je - 1; j > s; --j) {
                 F2 g[P][NS];
