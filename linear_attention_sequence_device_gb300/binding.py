@@ -130,8 +130,18 @@ def _check(st: int):
         raise GdnError(st, load().gdn_last_error().decode())
 
 
+class _Pointer(ctypes.c_void_p):
+    """A device address that keeps its tensor: several arguments may be
+    contiguous copies made for the call, and one that was freed before the next
+    is made would give that one its memory."""
+
+
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    if t is None:
+        return None
+    p = _Pointer(t.data_ptr())
+    p.tensor = t
+    return p
 
 
 def _stream():
