@@ -92,7 +92,9 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
     };
     // the sequence at the first token, and the state there
     int next = 0x7fffffff;  // first token of the next sequence
-    float dsum = 0.f;
+    // sum of delta: a tile's, and all before it with what its additions lost, since an exponent made of thousands of
+    // terms added one by one would be off by a few of its last digits
+    float dsum = 0.f, dall = 0.f, dlost = 0.f;
     if (REV) {
         const int n = seq_of(p.cu, p.num_seqs, t0);
         if (__ldg(p.cu + n) >= t0) return;  // nothing came in
@@ -282,11 +284,17 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
             }
         }
         if (more) put_bc(buf ^ 1);
+        if (LAST) {
+            const float t = __fadd_rn(dall, dsum);
+            dlost = __fadd_rn(dlost, __fadd_rn(dsum, -__fadd_rn(t, -dall)));
+            dall = t;
+            dsum = 0.f;
+        }
     }
     cp_async_wait<0>();
     if (LAST) {
         store_state(p.H, s);
-        if (k == 0 && in) p.sd[(int64_t)s * p.ch + c] = dsum;
+        if (k == 0 && in) p.sd[(int64_t)s * p.ch + c] = dall + dlost;
     } else if (p.h_final && next <= te) {  // the sequence ends with the segment
         const int m = seq_of(p.cu, p.num_seqs, te - 1);
         store_state(p.h_final, m);

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
     const bool writer = k < 4 && wc0 + och < cend;
     const float sbias = p.dt_bias && wc0 + sch < cend ? __ldg(p.dt_bias + wc0 + sch) : 0.f;
     const float Do = p.D && wc0 + och < cend ? __ldg(p.D + wc0 + och) : 0.f;
-    float aD = 0.f, aT = 0.f;
+    float aD = 0.f, aT = 0.f, bD = 0.f, bT = 0.f;  // a block's sums b, added to the segment's: fewer terms in a row
 
     int cks = 0;  // the checkpoint that is in place
     auto copy = [&](int tb) {
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
             static_cast<E*>(p.dx)[off] = Elem<E>::from_f(fmaf(dus, dl[i], Do * g));
             static_cast<E*>(p.ddt)[off] = Elem<E>::from_f(gd);
             if (p.z) static_cast<E*>(p.dz)[off] = Elem<E>::from_f(fmaf(Do, xv, y) * q1[i]);
-            aD = fmaf(g, xv, aD);
-            aT += gd;
+            bD = fmaf(g, xv, bD);
+            bT += gd;
         }
     };
 
@@ -509,6 +509,9 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
             if (tb + r < te && n < p.N) p.bc[(((int64_t)blockIdx.x * p.T + tb + r) * 2 + which) * p.N + n] = sum;
         }
         __syncthreads();  // the slabs are read
+        aD += bD;
+        aT += bT;
+        bD = bT = 0.f;
     }
     // the parameters' partial gradients of this segment
     float* pg = p.par + (int64_t)s * p.ch * (p.N + 2);
