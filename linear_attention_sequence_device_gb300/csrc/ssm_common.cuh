@@ -100,15 +100,26 @@ __device__ __forceinline__ float softplus_f(float v) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(v), "f"(0.f));
     return fmaf(t, q, m);
 }
-// The decay 2^(d A2) of a step.  The special function unit's results for
-// arguments in [-1, 0] lie below the value on average, by 0.6e-8 above -1e-3 and
-// by 1.7e-8 to 2.8e-8 (up to half of half a step) below, which a state multiplied
-// a thousand times adds up; the constant in the argument, which costs nothing
-// inside the product, takes most of that back.  Against 64 bits on 32768 tokens the
-// gradient of the initial states is off by 1.1e-6 of its norm with it, 2.2e-6
-// without.
+// The decay 2^(d A2) of a step.  The special function unit's results lie below the
+// value on average, by 0.6e-8 to 3.5e-8 with the argument's place in cells of 1/64
+// (half a step is 3e-8 there), and a state multiplied a thousand times by the decay
+// of its channel, whose arguments stay in a few cells, adds that up.  Two remedies
+// that cost no operation per state:
+//  - a constant in the argument, inside the product;
+//  - shifts: tokens go in pairs, of which the first takes its decays 2^s too large
+//    and the second 2^s too small, so that the state is 2^s times its value between
+//    the two.  What enters and leaves there is scaled by 2^s per token, not per state.
+//    Eight pairs' shifts spread the arguments over sixteen places in eight cells, on
+//    average over which the error is between -0.8e-8 (arguments near 0) and -2.8e-8
+//    (near -0.07); the constant takes back 1.1e-8.
+// Measured on sequences of 50 to 200 tokens with a carried state: the final state is
+// off by 4.5e-7 of its norm, 1.6e-8 of that in one direction where the carried state
+// rules; without the shifts by 9e-7, of which 5e-7 in one direction.
 constexpr float kDecayBias = 1.6e-8f;
-__device__ __forceinline__ float decay_fast(float d, float A2) { return exp2_fast(fmaf(d, A2, kDecayBias)); }
+constexpr int kShifts = 8;
+__constant__ const float kShift[kShifts] = {0.00439453125f, 0.0131835938f, 0.0219726562f, 0.0307617188f, 0.0395507812f, 0.0483398438f, 0.0571289062f, 0.0659179688f};
+__constant__ const float kShiftUp[kShifts] = {1.00305068f, 1.00918007f, 1.01534688f, 1.02155137f, 1.02779377f, 1.03407431f, 1.04039323f, 1.04675078f};  // 2^s
+__constant__ const float kShiftDown[kShifts] = {0.996958554f, 0.990903437f, 0.984885097f, 0.978903294f, 0.97295785f, 0.967048526f, 0.961175025f, 0.955337226f};  // 2^-s
 
 // Two fp32 values in a register pair, for the two-wide instructions: the pipe's
 // rate is the same, the instructions are half.  Kept as 64 bits, so that the pair
@@ -142,7 +153,7 @@ __device__ __forceinline__ F2 f2_exp2(F2 a) {
     return r;
 }
 __device__ __forceinline__ F2 f2_dup(float v) { return f2(v, v); }
-__device__ __forceinline__ F2 f2_decay(F2 d, F2 A2) { return f2_exp2(f2_fma(d, A2, f2_dup(kDecayBias))); }
+__device__ __forceinline__ F2 f2_decay(F2 d, F2 A2, F2 bias) { return f2_exp2(f2_fma(d, A2, bias)); }
 __device__ __forceinline__ float f2_sum(F2 a) { return a.x() + a.y(); }
 __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
     F2 r;

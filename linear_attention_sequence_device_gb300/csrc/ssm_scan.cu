@@ -37,7 +37,7 @@ gdn_status set_smem_attr(const void* func, size_t bytes);
 namespace {
 
 constexpr int TT = 16;     // tokens per tile
-constexpr int UN = 4;      // tokens handled together
+constexpr int UN = 4;      // tokens handled together (pairs of them, see kShift)
 constexpr int NST = 3;     // tiles of x, dt and z in flight or in use
 constexpr int NTH = 128;   // threads per block
 
@@ -195,20 +195,20 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
             if (it < TT * NB) bcs[b * TT * NB + it] = Elem<E>::to_f(bc[i]);
         }
     };
-    // one token: state and y
-    auto token = [&](const float* row, float dlt, float u, float xv, float sil, E* yo) {
-        const F2 d = f2_dup(dlt), uu = f2_dup(u);
+    // one token: state and y; shift: of its decays; u and the sum that makes y come scaled to what the state is
+    auto token = [&](const float* row, float dlt, float u, float xv, float sil, float shift, float down, E* yo) {
+        const F2 d = f2_dup(dlt), uu = f2_dup(u), bi = f2_dup(shift);
         F2 acc[2];
 #pragma unroll
         for (int q = 0; q < NS / 2; q += 2) {
             F2 b0, b1;
             f2_load2(row + 2 * q, b0, b1);
             if (REV) {
-                h[q] = f2_mul(f2_decay(d, A2[q]), f2_fma(uu, b0, h[q]));
-                h[q + 1] = f2_mul(f2_decay(d, A2[q + 1]), f2_fma(uu, b1, h[q + 1]));
+                h[q] = f2_mul(f2_decay(d, A2[q], bi), f2_fma(uu, b0, h[q]));
+                h[q + 1] = f2_mul(f2_decay(d, A2[q + 1], bi), f2_fma(uu, b1, h[q + 1]));
             } else {
-                h[q] = f2_fma(f2_decay(d, A2[q]), h[q], f2_mul(uu, b0));
-                h[q + 1] = f2_fma(f2_decay(d, A2[q + 1]), h[q + 1], f2_mul(uu, b1));
+                h[q] = f2_fma(f2_decay(d, A2[q], bi), h[q], f2_mul(uu, b0));
+                h[q + 1] = f2_fma(f2_decay(d, A2[q + 1], bi), h[q + 1], f2_mul(uu, b1));
             }
             if (!LAST) {
                 F2 c0, c1;
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
             float o = f2_sum(acc[0]) + f2_sum(acc[1]);
 #pragma unroll
             for (int m = 1; m < K; m <<= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
-            o = fmaf(Dc, xv, o);
+            o = fmaf(o, down, Dc * xv);
             if (gate) o *= sil;
             if (in && k == 0) *yo = Elem<E>::from_f(o);
         }
@@ -256,8 +256,13 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
                 for (int u = 0; u < UN; ++u) sil[u] = gate ? silu_fast(Elem<E>::to_f(xg[(2 * TT + u) * CH])) : 1.f;
 #pragma unroll
                 for (int u = 0; u < UN; ++u) {
+                    // pairs: the state is 2^s times its value behind the first token (kShift)
+                    const int pr = (r0 + u) / 2 % kShifts;
                     const float xv = Elem<E>::to_f(xg[u * CH]);
-                    token(row + u * NB, dl[u], (REV ? sil[u] : dl[u]) * xv, xv, sil[u], yo + u * p.ldy);
+                    float ut = (REV ? sil[u] : dl[u]) * xv;
+                    if ((u & 1) == (REV ? 1 : 0)) ut *= kShiftUp[pr];  // backwards it enters before the decay
+                    token(row + u * NB, dl[u], ut, xv, sil[u], (u & 1 ? -kShift[pr] : kShift[pr]) + kDecayBias,
+                          u & 1 ? 1.f : kShiftDown[pr], yo + u * p.ldy);
                 }
             } else {  // a sequence's end or the segment's is near: one by one
 #pragma unroll 1
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
                     const float xv = Elem<E>::to_f(xg[u * CH]);
                     const float d = softplus_f(Elem<E>::to_f(xg[(TT + u) * CH]) + bias);
                     const float sl = gate ? silu_fast(Elem<E>::to_f(xg[(2 * TT + u) * CH])) : 1.f;
-                    token(row + u * NB, d, (REV ? sl : d) * xv, xv, sl, yo + u * p.ldy);
+                    token(row + u * NB, d, (REV ? sl : d) * xv, xv, sl, kDecayBias, 1.f, yo + u * p.ldy);
                 }
             }
         }
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(NTH, 4) scan_step_kernel(const ScanParams p, i
         for (int i = 0; i < NBC; ++i)
             if (lane + 32 * i < 2 * NP) bcw[lane + 32 * i] = Elem<E>::to_f(cur.bc[i]);
         const float xv = Elem<E>::to_f(cur.x), dlt = softplus_f(Elem<E>::to_f(cur.dt) + bias);
-        const F2 d = f2_dup(dlt), u = f2_dup(dlt * xv);
+        const F2 d = f2_dup(dlt), u = f2_dup(dlt * xv), bi = f2_dup(kDecayBias);
         F2 acc = f2_dup(0.f);
         cp_async_wait<STG - 1>();
         __syncwarp();
@@ -472,8 +477,8 @@ __global__ void __launch_bounds__(NTH, 4) scan_step_kernel(const ScanParams p, i
             }
             f2_load2(bcw + k * NS + 4 * q, b0, b1);
             f2_load2(bcw + NP + k * NS + 4 * q, d0, d1);
-            h0 = f2_fma(f2_decay(d, A2[2 * q]), h0, f2_mul(u, b0));
-            h1 = f2_fma(f2_decay(d, A2[2 * q + 1]), h1, f2_mul(u, b1));
+            h0 = f2_fma(f2_decay(d, A2[2 * q], bi), h0, f2_mul(u, b0));
+            h1 = f2_fma(f2_decay(d, A2[2 * q + 1], bi), h1, f2_mul(u, b1));
             acc = f2_fma(h0, d0, acc);
             acc = f2_fma(h1, d1, acc);
             if (vec) {

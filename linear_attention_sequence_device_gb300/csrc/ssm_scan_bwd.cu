@@ -56,6 +56,7 @@ constexpr int NC = 2 * P;  // channels per lane
 constexpr int NW = 4;      // warps per block
 constexpr int OCC = 3;     // blocks per SM: 168 registers a thread
 constexpr int NT = 32 * NW;
+static_assert(Q == 2 && kShifts % (BT / 2) == 0, "pieces are pairs of shifted decays");
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct ScanBwdParams {
@@ -202,6 +203,12 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
                 }
         }
     };
+    auto scale_state = [&](F2 (&f)[P][NS], float v) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+            for (int n = 0; n < NS; ++n) f[i][n] = f2_mul(f[i][n], f2_dup(v));
+    };
     auto pass_empty = [&](int m) {  // an empty sequence's final state is its initial one
         if (!p.dh0) return;
         F2 f[P][NS];
@@ -315,12 +322,20 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
         }
     };
 
+    // a sequence starts at row r of the block: its initial state, scaled to where in a pair that is
+    auto start_state = [&](int r, int tb, float up) {
+        load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
+        scale_state(h, up);
+    };
     // the outputs of the lane's channel at row r of the block, from its sums over the states
-    auto outputs = [&](int r, int tb, float dus, float dds, float y) {
+    // (up, down: 2^s and 2^-s in the first rows of pairs)
+    auto outputs = [&](int r, int tb, float dus, float dds, float y, float up, float down) {
         const int i = r * WC + och;
         if (writer && tb + r < te) {
             const int64_t off = (int64_t)(tb + r) * p.ch + wc0 + och;
-            const float g = dsv[i], xv = xx[i];
+            dus *= up;
+            y *= down;
+            const float g = dsv[i] * up, xv = xx[i];
             const float gd = fmaf(kLn2, dds, dus * xv) * slope[i];
             static_cast<E*>(p.dx)[off] = Elem<E>::from_f(fmaf(dus, dl[i], Do * g));
             static_cast<E*>(p.ddt)[off] = Elem<E>::from_f(gd);
@@ -351,6 +366,7 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
             while (sq >= 0 && __ldg(p.cu + sq) == cur);
             cur = sq >= 0 ? min(__ldg(p.cu + sq), cur - 1) : -1;
         }
+        const int shift0 = tb / BT % (kShifts / (BT / 2)) * (BT / 2);  // the block's pairs' first shift
         cp_async_wait_all();
         __syncwarp();
 #pragma unroll 4
@@ -366,9 +382,12 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
                 g = gy * (zv * sg);
                 qv = gy * sg * fmaf(zv, 1.f - sg, 1.f);
             }
+            // the first rows of pairs, between whose tokens the state is 2^s times its value: u and ds to match
+            const int row = r0 + lane / WC, pr = shift0 + row / 2;
+            const float up = row & 1 ? 1.f : kShiftUp[pr], down = row & 1 ? 1.f : kShiftDown[pr];
             dl[i] = ok ? d : 0.f;
-            uu[i] = ok ? d * xv : 0.f;
-            dsv[i] = ok ? g : 0.f;
+            uu[i] = ok ? d * xv * up : 0.f;
+            dsv[i] = ok ? g * down : 0.f;
             slope[i] = v > 20.f ? 1.f : sigmoid_fast(v);
             q1[i] = qv;
             xx[i] = xv;
@@ -385,11 +404,13 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
 #pragma unroll 1
         for (int q = 0; q < BT / Q - 1; ++q) {
             const bool any = starts >> (q * Q) & (1u << Q) - 1;
+            const float sh = kShift[shift0 + q], up = kShiftUp[shift0 + q];
 #pragma unroll
             for (int e = 0; e < Q; ++e) {
                 const int r = q * Q + e;
                 if (any)
-                    if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
+                    if (starts >> r & 1) start_state(r, tb, e ? up : 1.f);
+                const F2 bi = f2_dup((e ? -sh : sh) + kDecayBias);
                 F2 d[P], u[P], bb[NS];
                 lds_pairs(d, dl + r * WC + co);
                 lds_pairs(u, uu + r * WC + co);
@@ -397,7 +418,7 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
 #pragma unroll
                 for (int i = 0; i < P; ++i)
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) h[i][n] = f2_fma(u[i], bb[n], f2_mul(f2_decay(d[i], A2[i][n]), h[i][n]));
+                    for (int n = 0; n < NS; ++n) h[i][n] = f2_fma(u[i], bb[n], f2_mul(f2_decay(d[i], A2[i][n], bi), h[i][n]));
             }
 #pragma unroll
             for (int i = 0; i < NC; ++i)
@@ -407,6 +428,7 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
 #pragma unroll 1
         for (int q = BT / Q - 1; q >= 0; --q) {
             const bool any = starts >> (q * Q) & (1u << Q) - 1;
+            const float sh = kShift[shift0 + q], up = kShiftUp[shift0 + q], down = kShiftDown[shift0 + q];
             F2 a[Q][P][NS], w[Q][P][NS];
             float ys[Q];
             if (q) {
@@ -427,7 +449,8 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
                 for (int o = 0; o < 2; ++o) {
                     const int e = e2 + o, r = q * Q + e;
                     if (any)
-                        if (starts >> r & 1) load_state(h, p.h0, seq_of(p.cu, p.num_seqs, tb + r));
+                        if (starts >> r & 1) start_state(r, tb, e ? up : 1.f);
+                    const F2 bi = f2_dup((e ? -sh : sh) + kDecayBias);
                     F2 d[P], u[P], g[P], bb[NS], cc[NS], t[NS];
                     lds_pairs(d, dl + r * WC + co);
                     lds_pairs(u, uu + r * WC + co);
@@ -438,7 +461,7 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
                     for (int i = 0; i < P; ++i)
 #pragma unroll
                         for (int n = 0; n < NS; ++n) {
-                            a[e][i][n] = f2_decay(d[i], A2[i][n]);
+                            a[e][i][n] = f2_decay(d[i], A2[i][n], bi);
                             w[e][i][n] = f2_mul(a[e][i][n], h[i][n]);
                             h[i][n] = f2_fma(u[i], bb[n], w[e][i][n]);
                             t[n] = i ? f2_fma(g[i], h[i][n], t[n]) : f2_mul(g[i], h[i][n]);
@@ -483,13 +506,16 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
                     for (int n = 0; n < NS; ++n) v8[4 * o + n] = f2_sum(tt[n]);
                     if (any && (starts >> r & 1)) {  // the token starts a sequence: dh is the gradient of its h0
                         const int n = seq_of(p.cu, p.num_seqs, t);
+                        if (e) scale_state(dh, up);
                         if (p.dh0) store_state(p.dh0, n, dh);
                         int m = n - 1;
                         while (m >= 0 && __ldg(p.cu + m) == t) pass_empty(m--);
                         load_state(dh, m >= 0 ? p.dhf : nullptr, m >= 0 ? m : 0);
+                        if (e) scale_state(dh, down);
                     }
                     outputs(r, tb, sum_states<K>(du[o][0].x(), du[o][0].y(), du[o][1].x(), du[o][1].y(), k),
-                            sum_states<K>(dd[o][0].x(), dd[o][0].y(), dd[o][1].x(), dd[o][1].y(), k), ys[e]);
+                            sum_states<K>(dd[o][0].x(), dd[o][0].y(), dd[o][1].x(), dd[o][1].y(), k), ys[e], e ? 1.f : up,
+                            e ? 1.f : down);
                 }
                 int first;
                 sum_channels8<K>(v8, lane, first);
