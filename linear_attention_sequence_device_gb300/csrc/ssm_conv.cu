@@ -71,14 +71,16 @@ __device__ __forceinline__ void load_weights(const void* w, const void* b, int c
 
 // Forward.  HBM-bound: x in, y out, each once.  A thread owns eight channels of a
 // strip of rows and walks down it with a window of the last K - 1 inputs; rows come
-// by asynchronous copies into a ring of NSTAGE batches of RB rows that it fills and
+// by asynchronous copies into a ring of kStages batches of RB rows that it fills and
 // reads alone.  A batch that no sequence starts in, all but a few, runs without a
 // check, which also lets the window stay where it is instead of moving up row by
 // row.  The SiLU is a / (1 + e^-a) for both types, so that a bf16 result is off by
 // its own rounding only; in pairs that is 3 issue slots an element.
-constexpr int NSTAGE = 4;
+template <typename T>
+constexpr int kStages = sizeof(T) == 4 ? 3 : 4;  // four blocks' rings fit an SM (fp32, 30038 x 2112: 172 us with 4)
 template <typename T, int K>
 __global__ void __launch_bounds__(NT, 4) conv_fwd_kernel(const ConvParams p) {
+    constexpr int NST = kStages<T>;
     constexpr int H = K > 1 ? K - 1 : 1, VEC = sizeof(T) * 8 / 16;
     const int c0 = (blockIdx.x * NT + threadIdx.x) * 8;
     if (c0 >= p.C) return;
@@ -119,11 +121,11 @@ __global__ void __launch_bounds__(NT, 4) conv_fwd_kernel(const ConvParams p) {
     if (start == lt0)  // empty sequences that end where this strip starts
         for (int m = seg - 1; m >= 0 && __ldg(cu + m) == lt0; --m) pass_empty(m);
 
-    extern __shared__ uint4 ring[];  // [NSTAGE][RB][VEC][NT]
+    extern __shared__ uint4 ring[];  // [NST][RB][VEC][NT]
     const int nb = (lt1 - lt0 + RB - 1) / RB;
     auto issue = [&](int b) {
         if (b < nb) {
-            uint4* st = ring + (size_t)(b % NSTAGE) * RB * VEC * NT + tid;
+            uint4* st = ring + (size_t)(b % NST) * RB * VEC * NT + tid;
 #pragma unroll
             for (int u = 0; u < RB; ++u) {
                 const int t = lt0 + RB * b + u;
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(NT, 4) conv_fwd_kernel(const ConvParams p) {
         cp_async_commit();
     };
 #pragma unroll
-    for (int b = 0; b < NSTAGE - 1; ++b) issue(b);
+    for (int b = 0; b < NST - 1; ++b) issue(b);
 
     F2 w[K][4], b[4];
     load_weights<T, K, 8>(p.w, p.b, c0, w, b);
@@ -151,9 +153,9 @@ __global__ void __launch_bounds__(NT, 4) conv_fwd_kernel(const ConvParams p) {
             for (int i = 0; i < 4; ++i) win[j][i] = f2_dup(0.f);
     }
     for (int bt = 0; bt < nb; ++bt) {
-        issue(bt + NSTAGE - 1);
-        cp_async_wait<NSTAGE - 1>();
-        const uint4* st = ring + (size_t)(bt % NSTAGE) * RB * VEC * NT + tid;
+        issue(bt + NST - 1);
+        cp_async_wait<NST - 1>();
+        const uint4* st = ring + (size_t)(bt % NST) * RB * VEC * NT + tid;
         const int tb = lt0 + RB * bt;
         auto row = [&](int u) {
             uint4 raw[VEC];
@@ -228,6 +230,7 @@ struct ConvBwdParams {
 // pairs through the two-wide instructions: single ones took 44 issue slots an
 // element, which bounded it at 290 us for 65536 x 2048.  x and dy come through a ring
 // as in the forward.
+constexpr int NSTAGE = 4;
 template <typename T, int K>
 __global__ void __launch_bounds__(NT, 4) conv_bwd_kernel(const ConvBwdParams p) {
     constexpr int H = K > 1 ? K - 1 : 1;
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const T* x, int64_t ldx, 
 int bwd_strips(int T, int C) {
     const int nx = (C / CV + NT - 1) / NT;
     int n = device_sm_count() * 4 / nx;
-    const int most = T / 64;
+    const int most = T / 16;  // 104 rows: 13 us, 23 with strips of 64
     if (n > most) n = most;
     if (n > 65535) n = 65535;
     return n < 1 ? 1 : n;
@@ -498,15 +501,13 @@ int bwd_strips(int T, int C) {
 
 template <typename T, int K>
 gdn_status run_fwd_k(ConvParams p, cudaStream_t s) {
-    constexpr size_t smem = (size_t)NSTAGE * RB * sizeof(T) * 8 * NT;
-    if (smem > (48 << 10)) {
-        const gdn_status st = set_smem_attr((const void*)conv_fwd_kernel<T, K>, smem);
-        if (st != GDN_OK) return st;
-    }
-    // strips: one wave of four blocks an SM, of 64 rows at least
+    constexpr size_t smem = (size_t)kStages<T> * RB * sizeof(T) * 8 * NT;
+    static_assert(smem <= (48 << 10), "dynamic shared memory that needs no attribute");
+    // Strips: one wave of four blocks an SM, of 8 rows at least: the K - 1 rows before a strip
+    // are read twice, but a strip's rows follow one another (104 rows: 23 us at 64, 9 at 8).
     const int nx = (p.C / 8 + NT - 1) / NT;
     int n = device_sm_count() * 4 / nx;
-    if (n > p.T / 64) n = p.T / 64;
+    if (n > p.T / 8) n = p.T / 8;
     if (n > 65535) n = 65535;
     if (n < 1) n = 1;
     p.rows = p.T > 0 ? ((p.T + n - 1) / n + RB - 1) / RB * RB : RB;

@@ -26,7 +26,9 @@
 // from h0 where the sequence starts in it), keeping only the end state H and
 // the sum of delta; from the first token of a segment that continues a
 // sequence, the state is the fold  h <- 2^(A2 sum delta_j) h + H_j  over the
-// segments before it, which each block does for its own channels.
+// segments before it.  Up to kFoldSegments segments each block of the main launch
+// folds for its own channels; above, a launch between the two does, one thread a
+// channel and state.
 #include "chunk_common.cuh"
 #include "ssm_scan.cuh"
 
@@ -523,19 +525,20 @@ int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH 
 
 // Segments of a call: one wave of four resident blocks an SM, two where that
 // leaves segments of 512 tokens or more (the last blocks' idle time halves: 2.05 ->
-// 1.99 ms on 131072 tokens of 2048 channels), of 64 tokens or more; multiples of 64
-// so that the checkpoints fall on tile starts.
+// 1.99 ms on 131072 tokens of 2048 channels); whole tiles, on whose starts the
+// checkpoints fall, down to one: few tokens are a walk, and a shorter one costs only
+// a fold (207 tokens of 88 channels: 19 us, 27 with segments of 64).
 void segments(int T, int ch, int N, int groups, int& seg, int& S) {
     const int per = ch / groups, cb = channels_per_block(N);
     const int64_t blocks = (int64_t)groups * ((per + cb - 1) / cb);
     int64_t want = (int64_t)device_sm_count() * 4 / blocks;
     if (T >= 2 * want * 512) want *= 2;
     if (want < 1) want = 1;
-    const int64_t most = (T + 63) / 64;
+    const int64_t least = TT, most = (T + least - 1) / least;
     if (want > most) want = most;
     if (want < 1) want = 1;
-    seg = (int)(((T + want - 1) / want + 63) / 64 * 64);
-    if (seg < 64) seg = 64;
+    seg = (int)(((T + want - 1) / want + TT - 1) / TT * TT);
+    if (seg < least) seg = least;
     S = (T + seg - 1) / seg;
     if (S < 1) S = 1;
 }
