@@ -24,7 +24,7 @@
 // registers over all of a block's rows and leave as one partial row per block,
 // summed in block order by a second kernel; its rows come by asynchronous copies
 // into a ring in shared memory that every thread fills and reads alone, once before
-// and once behind the reduction (32768 rows of 4096 in bf16: 447 us, 4.8 TB/s; 512
+// and once behind the reduction (32768 rows of 4096 in bf16: 381 us, 5.6 TB/s; 512
 // threads of 128 registers are one block an SM, whose reduction nothing covers).
 #include "chunk_common.cuh"
 #include "ssm_common.cuh"
@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams 
                 for (int i = 0; i < 4; ++i) x[4][i] = f2_dup(1.f);
             }
         };
-        // sums: r'^2, w_pre dy r', o^2, and of q = f sg o: q dr', q w_pre dy, q r'
+        // sums: r'^2, w_pre dy r', o^2, and of q = f sg o: q dr', q w_pre dy, q r' (the last four used with
+        // w_post; without it r1 is 1 and m1 is 0, without a gate sg is 1: choices cost more here than products)
         F2 s6[6];
 #pragma unroll
         for (int i = 0; i < 6; ++i) s6[i] = f2_dup(0.f);
@@ -324,13 +325,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams 
                     const F2 wd = f2_mul(KEEP ? kw[i] : w[i], x[2][i]);
                     s6[0] = f2_fma(x[0][i], x[0][i], s6[0]);
                     s6[1] = f2_fma(wd, x[0][i], s6[1]);
-                    if (wpost) {
-                        const F2 fo = f2_mul(KEEP ? kf[i] : f[i], x[3][i]), qv = gate ? f2_mul(fo, x[4][i]) : fo;
-                        s6[2] = f2_fma(x[3][i], x[3][i], s6[2]);
-                        s6[3] = f2_fma(qv, x[1][i], s6[3]);
-                        s6[4] = f2_fma(qv, wd, s6[4]);
-                        s6[5] = f2_fma(qv, x[0][i], s6[5]);
-                    }
+                    const F2 qv = f2_mul(f2_mul(KEEP ? kf[i] : f[i], x[3][i]), x[4][i]);
+                    s6[2] = f2_fma(x[3][i], x[3][i], s6[2]);
+                    s6[3] = f2_fma(qv, x[1][i], s6[3]);
+                    s6[4] = f2_fma(qv, wd, s6[4]);
+                    s6[5] = f2_fma(qv, x[0][i], s6[5]);
                 }
                 if constexpr (KEEP)
 #pragma unroll
@@ -367,11 +366,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams 
                     const F2 rh = f2_mul(x[0][i], R2), wi = KEEP ? kw[i] : w[i], fi = KEEP ? kf[i] : f[i];
                     a_pre[j][i] = f2_fma(x[2][i], rh, a_pre[j][i]);
                     dr[i] = f2_fma(R2, f2_fma(wi, x[2][i], f2_mul(rh, M2)), x[1][i]);
-                    const F2 oh = f2_mul(x[3][i], R1), dg = gate ? f2_mul(dr[i], x[4][i]) : dr[i];
+                    const F2 oh = f2_mul(x[3][i], R1), dg = f2_mul(dr[i], x[4][i]);
                     a_br[j][i] = f2_fma(dg, oh, a_br[j][i]);
                     const F2 df = f2_mul(dg, fi);
-                    if (gate) t[i] = f2_mul(f2_mul(df, oh), f2_fma(x[4][i], neg, one));
-                    dp[i] = wpost ? f2_mul(R1, f2_fma(oh, M1, df)) : df;
+                    t[i] = f2_mul(f2_mul(df, oh), f2_fma(x[4][i], neg, one));
+                    dp[i] = f2_mul(R1, f2_fma(oh, M1, df));
                 }
                 f2_store8(static_cast<R*>(p.dres) + base + 8 * v, dr);
                 if (gate) f2_store8(static_cast<E*>(p.dgate) + base + 8 * v, t);
