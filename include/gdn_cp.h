@@ -22,9 +22,9 @@
  *
  * Conventions shared by every entry point
  *   - Pointers marked "device" must be CUDA device (or managed) memory; the
- *     caller allocates and owns every buffer.  Except for the workspaces of
- *     gdn_shard_fwd (required) and gdn_chunk_fwd (optional), no entry point
- *     needs scratch memory, and none allocates.
+ *     caller allocates and owns every buffer.  Scratch memory is the
+ *     workspace argument of the entry points that have one (required but in
+ *     gdn_chunk_fwd); none allocates.
  *   - All work is enqueued on `stream` (a cudaStream_t passed as void*; NULL
  *     = the legacy default stream).  No entry point synchronises the host.
  *   - Tokens are packed, batch 1: a token-major [T, ...] layout with

@@ -165,6 +165,32 @@ __device__ __forceinline__ F2 f2_sigmoid(F2 v) {
     return f2(rcp_fast(e.x()), rcp_fast(e.y()));
 }
 __device__ __forceinline__ F2 f2_silu(F2 v) { return f2_mul(v, f2_sigmoid(v)); }
+__device__ __forceinline__ F2 f2_max0(F2 v) {
+    float x, y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(v.x()), "f"(0.f));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(v.y()), "f"(0.f));
+    return f2(x, y);
+}
+// softplus_f of pairs, step by step together: a coefficient is made once for all
+template <int M>
+__device__ __forceinline__ void f2_softplus(F2 (&v)[M]) {
+    constexpr float c[9] = {0.019542526453733444f, -0.056373611092567444f, 0.10543623566627502f, -0.1526966691017151f,
+                            0.1966327428817749f, -0.24951615929603577f, 0.33329710364341736f, -0.49999892711639404f, 1.f};
+    F2 t[M], q[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        t[i] = f2(exp2_fast(-fabsf(v[i].x()) * kLog2e), exp2_fast(-fabsf(v[i].y()) * kLog2e));
+        q[i] = f2_dup(-0.0031760570127516985f);
+    }
+#pragma unroll
+    for (int k = 0; k < 9; ++k) {
+        const F2 ck = f2_dup(c[k]);
+#pragma unroll
+        for (int i = 0; i < M; ++i) q[i] = f2_fma(q[i], t[i], ck);
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = f2_fma(t[i], q[i], f2_max0(v[i]));
+}
 // eight consecutive elements (16-byte aligned) as four pairs
 __device__ __forceinline__ void f2_load8(const __nv_bfloat16* p, F2 (&f)[4]) {
     const uint4 r = *reinterpret_cast<const uint4*>(p);

@@ -14,11 +14,15 @@
 // under way without holding registers; B and C, which all channels of a group
 // read, are laid beside them as fp32 and come back as broadcasts.
 //
-// What bounds it: the 16 exponentials a token and channel (the special function
-// unit: 4 cycles a warp each) and as many cycles of the FMA pipe (four
-// operations a state), with about 95 issue slots against 64 + 16 cycles of
-// either.  Pairs of states go through the two-wide fp32 instructions, without
-// which the issue slots would come first.
+// What bounds it: issue slots.  A token of 32 channels takes 124 of them (76 in the
+// launch that keeps end states only): 32 two-wide operations, which hold the FMA pipe
+// for two cycles each, 19 of the special function unit (16 decays; 4 cycles each), 13
+// loads and stores, and delta, u and the SiLU.  63 % of the slots are used with the
+// four warps a scheduler that 128 registers allow.  Pairs of states, and of tokens'
+// deltas, go through the two-wide fp32 instructions, without which the slots would be
+// 36 more.  32768 tokens of 4096 channels in prompts of 512 to 8192: 1.03 ms, of which
+// the first launch 0.39 and the main one 0.63; two channels a lane, more tokens at a
+// time or pairs in the SiLU and u too (registers) were no faster.
 //
 // Parallelism over tokens.  The packed tokens are cut into S segments of equal
 // length, whatever the sequences' lengths.  A first launch runs each segment's
@@ -252,8 +256,13 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
             E* yo = yp + (int64_t)tg * p.ldy;
             if (jg + UN <= len && next >= tg + UN) {
                 float dl[UN], sil[UN];
+                F2 dp[UN / 2];
 #pragma unroll
-                for (int u = 0; u < UN; ++u) dl[u] = softplus_f(Elem<E>::to_f(xg[(TT + u) * CH]) + bias);
+                for (int u = 0; u < UN; u += 2)
+                    dp[u / 2] = f2(Elem<E>::to_f(xg[(TT + u) * CH]) + bias, Elem<E>::to_f(xg[(TT + u + 1) * CH]) + bias);
+                f2_softplus(dp);
+#pragma unroll
+                for (int u = 0; u < UN; ++u) dl[u] = u & 1 ? dp[u / 2].y() : dp[u / 2].x();
 #pragma unroll
                 for (int u = 0; u < UN; ++u) sil[u] = gate ? silu_fast(Elem<E>::to_f(xg[(2 * TT + u) * CH])) : 1.f;
 #pragma unroll

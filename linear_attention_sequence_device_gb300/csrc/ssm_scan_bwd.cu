@@ -36,12 +36,12 @@
 // Parallelism over tokens as in the forward: segments of equal length; a first
 // launch runs each segment's part of the sequence that came in from the segment
 // before, backwards from zero (or from dh_final where the sequence ends in it),
-// and a block of the main launch folds the segments behind its own.
+// and the segments behind a block's own are folded by the block or by a launch.
 //
-// What bounds it: issue slots and the latencies that three warps a scheduler do
-// not cover.  Per token and 32 channels 120 two-wide operations (two slots each),
-// 33 of the special function unit, 60 of shared memory and exchanges, 500
-// instructions in all, in about 900 cycles.
+// What bounds it: issue slots, 520 a token of 32 channels (114 two-wide operations
+// that hold the FMA pipe for two cycles, 34 of the special function unit, 62 loads,
+// stores and exchanges), of which 62 % are used with the three warps a scheduler
+// that 168 registers allow.  32768 tokens of 4096 channels: 2.82 ms.
 #include "chunk_common.cuh"
 #include "ssm_scan.cuh"
 
@@ -369,28 +369,40 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
         const int shift0 = tb / BT % (kShifts / (BT / 2)) * (BT / 2);  // the block's pairs' first shift
         cp_async_wait_all();
         __syncwarp();
-#pragma unroll 4
-        for (int r0 = 0; r0 < BT; r0 += TPS) {
-            const int i = r0 * WC + lane;  // token r0 + lane / WC, channel sch
-            const bool ok = tb + r0 + lane / WC < te;
-            const float xv = Elem<E>::to_f(raw[i]), gy = Elem<E>::to_f(raw[2 * BT * WC + i]);
-            const float v = Elem<E>::to_f(raw[BT * WC + i]) + sbias;
-            const float d = softplus_f(v);
-            float g = gy, qv = 0.f;
-            if (p.z) {
-                const float zv = Elem<E>::to_f(raw[3 * BT * WC + i]), sg = sigmoid_fast(zv);
-                g = gy * (zv * sg);
-                qv = gy * sg * fmaf(zv, 1.f - sg, 1.f);
+        constexpr int SG = BT / TPS < 4 ? 2 : 4;  // a lane's tokens staged together
+#pragma unroll
+        for (int g0 = 0; g0 < BT; g0 += SG * TPS) {
+            F2 vp[SG / 2], dp[SG / 2], lp[SG / 2];  // dt + bias, delta, its slope
+#pragma unroll
+            for (int m = 0; m < SG; m += 2) {
+                const int i = (g0 + m * TPS) * WC + lane;
+                vp[m / 2] = f2(Elem<E>::to_f(raw[BT * WC + i]) + sbias, Elem<E>::to_f(raw[BT * WC + i + 32]) + sbias);
+                dp[m / 2] = vp[m / 2];
+                lp[m / 2] = f2_sigmoid(vp[m / 2]);
             }
-            // the first rows of pairs, between whose tokens the state is 2^s times its value: u and ds to match
-            const int row = r0 + lane / WC, pr = shift0 + row / 2;
-            const float up = row & 1 ? 1.f : kShiftUp[pr], down = row & 1 ? 1.f : kShiftDown[pr];
-            dl[i] = ok ? d : 0.f;
-            uu[i] = ok ? d * xv * up : 0.f;
-            dsv[i] = ok ? g * down : 0.f;
-            slope[i] = v > 20.f ? 1.f : sigmoid_fast(v);
-            q1[i] = qv;
-            xx[i] = xv;
+            f2_softplus(dp);
+#pragma unroll
+            for (int m = 0; m < SG; ++m) {
+                const int i = (g0 + m * TPS) * WC + lane, row = g0 + m * TPS + lane / WC;  // token row, channel sch
+                const bool ok = tb + row < te;
+                auto of = [&](const F2 (&f)[SG / 2]) { return m & 1 ? f[m / 2].y() : f[m / 2].x(); };
+                const float xv = Elem<E>::to_f(raw[i]), gy = Elem<E>::to_f(raw[2 * BT * WC + i]), d = of(dp);
+                float g = gy, qv = 0.f;
+                if (p.z) {
+                    const float zv = Elem<E>::to_f(raw[3 * BT * WC + i]), sg = sigmoid_fast(zv);
+                    g = gy * (zv * sg);
+                    qv = gy * sg * fmaf(zv, 1.f - sg, 1.f);
+                }
+                // the first rows of pairs, between whose tokens the state is 2^s times its value: u and ds to match
+                const int pr = shift0 + row / 2;
+                const float up = row & 1 ? 1.f : kShiftUp[pr], down = row & 1 ? 1.f : kShiftDown[pr];
+                dl[i] = ok ? d : 0.f;
+                uu[i] = ok ? d * xv * up : 0.f;
+                dsv[i] = ok ? g * down : 0.f;
+                slope[i] = of(vp) > 20.f ? 1.f : of(lp);
+                q1[i] = qv;
+                xx[i] = xv;
+            }
         }
         __syncwarp();
         if (b > 0) {
