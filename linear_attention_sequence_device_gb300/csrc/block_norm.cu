@@ -24,8 +24,10 @@
 // registers over all of a block's rows and leave as one partial row per block,
 // summed in block order by a second kernel; its rows come by asynchronous copies
 // into a ring in shared memory that every thread fills and reads alone, once before
-// and once behind the reduction (32768 rows of 4096 in bf16: 381 us, 5.6 TB/s; 512
-// threads of 128 registers are one block an SM, whose reduction nothing covers).
+// and once behind the reduction (32768 rows of 4096 in bf16: 374 us, 5.7 TB/s; 512
+// threads of 128 registers fill an SM, so that little covers a reduction).  Up to two
+// vectors a thread the weights stay in registers: read twice a row they cost half as
+// much again (8192 rows of 5120: 280 us, 164 kept).
 #include "chunk_common.cuh"
 #include "ssm_common.cuh"
 
@@ -270,9 +272,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams 
             for (int i = 0; i < 4; ++i) f[i] = f2_dup(1.f);
         }
     };
-    constexpr bool KEEP = VPT == 1;  // a row's vector and the weights stay in registers; else they are read twice
-    F2 kw[4], kf[4], kr[5][4];  // used with KEEP
-    if (KEEP && tid < nv) weights(tid, kw, kf);
+    constexpr bool KEEP = VPT == 1;   // a row's vector stays in registers; else it is read twice
+    constexpr bool KEEPW = VPT <= 2;  // so do the weights
+    F2 kw[KEEPW ? VPT : 1][4], kf[KEEPW ? VPT : 1][4], kr[5][4];
+    if (KEEPW)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (tid + j * nt < nv) weights(tid + j * nt, kw[j], kf[j]);
     // sums over the rows: dy r^, and dr sg o^, of which dw_post and dscale are multiples by column
     F2 a_pre[VPT][4], a_br[VPT][4];
 #pragma unroll
@@ -319,13 +325,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams 
             if (tid + j * nt < nv) {
                 F2 x[5][4], w[4], f[4];
                 row_vec(j, x);
-                if constexpr (!KEEP) weights(tid + j * nt, w, f);
+                if constexpr (!KEEPW) weights(tid + j * nt, w, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const F2 wd = f2_mul(KEEP ? kw[i] : w[i], x[2][i]);
+                    const F2 wd = f2_mul(KEEPW ? kw[KEEPW ? j : 0][i] : w[i], x[2][i]);
                     s6[0] = f2_fma(x[0][i], x[0][i], s6[0]);
                     s6[1] = f2_fma(wd, x[0][i], s6[1]);
-                    const F2 qv = f2_mul(f2_mul(KEEP ? kf[i] : f[i], x[3][i]), x[4][i]);
+                    const F2 qv = f2_mul(f2_mul(KEEPW ? kf[KEEPW ? j : 0][i] : f[i], x[3][i]), x[4][i]);
                     s6[2] = f2_fma(x[3][i], x[3][i], s6[2]);
                     s6[3] = f2_fma(qv, x[1][i], s6[3]);
                     s6[4] = f2_fma(qv, wd, s6[4]);
@@ -359,11 +365,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormParams 
                         for (int i = 0; i < 4; ++i) x[a][i] = kr[a][i];
                 } else {
                     row_vec(j, x);
-                    weights(v, w, f);
+                    if constexpr (!KEEPW) weights(v, w, f);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const F2 rh = f2_mul(x[0][i], R2), wi = KEEP ? kw[i] : w[i], fi = KEEP ? kf[i] : f[i];
+                    const F2 rh = f2_mul(x[0][i], R2), wi = KEEPW ? kw[KEEPW ? j : 0][i] : w[i], fi = KEEPW ? kf[KEEPW ? j : 0][i] : f[i];
                     a_pre[j][i] = f2_fma(x[2][i], rh, a_pre[j][i]);
                     dr[i] = f2_fma(R2, f2_fma(wi, x[2][i], f2_mul(rh, M2)), x[1][i]);
                     const F2 oh = f2_mul(x[3][i], R1), dg = f2_mul(dr[i], x[4][i]);
@@ -441,18 +447,28 @@ void norm_shape(int W, int& threads, int& vpt) {
     threads = ((nv + vpt - 1) / vpt + 31) / 32 * 32;
 }
 
+// Of the backward: two vectors where the types are the same, and bf16 rows wider
+// than 2048 (bf16, 16384 rows of 2560: 129 us, 161 with one; 32768 of 4096: 374 and
+// 381; 32768 of 1024: 103 and 96; fp32, 8192 of 4096: 212 and 280), one where the
+// stream is fp32 beside bf16 (32768 of 4096: 633 us, 693 with two).
+void bwd_shape(int W, bool mixed, bool f32, int& threads, int& vpt) {
+    norm_shape(W, threads, vpt);
+    const int nv = W / 8;
+    if (vpt == 1 && !mixed && nv > (f32 ? 32 : 256)) {
+        vpt = 2;
+        threads = ((nv + 1) / 2 + 31) / 32 * 32;
+    }
+}
 // 128 registers a thread: 512 threads fill an SM
 int bwd_per_sm(int threads) { return threads >= 512 ? 1 : 512 / threads; }
-int bwd_blocks(int T, int W) {
-    int threads, vpt;
-    norm_shape(W, threads, vpt);
+int bwd_blocks(int T, int threads) {
     const int n = device_sm_count() * bwd_per_sm(threads);
     return T < n ? (T > 0 ? T : 1) : n;
 }
 
 template <typename E, typename R, int VPT>
 gdn_status run_bwd(const NormParams& p, int threads, cudaStream_t s) {
-    const int grid = bwd_blocks(p.T, p.W);
+    const int grid = bwd_blocks(p.T, threads);
     const size_t row = row_bytes<E, R, VPT>(threads);
     int stages = (int)(kRingBytes / bwd_per_sm(threads) / row);
     if (stages > kMaxStages) stages = kMaxStages;
@@ -489,6 +505,7 @@ gdn_status run_norm(const NormParams& p, bool bwd, cudaStream_t s) {
         else norm_fwd_kernel<E, R, 4><<<grid, threads, 0, s>>>(p);
         return check_launch("norm_fwd_kernel");
     }
+    bwd_shape(p.W, sizeof(E) != sizeof(R), sizeof(E) == 4, threads, vpt);
     if (vpt == 1) return run_bwd<E, R, 1>(p, threads, s);
     if (vpt == 2) return run_bwd<E, R, 2>(p, threads, s);
     return run_bwd<E, R, 4>(p, threads, s);
@@ -546,7 +563,13 @@ gdn_status gdn_block_norm_fwd(const void* o, int64_t ldo, const void* gate, int6
 
 size_t gdn_block_norm_bwd_workspace_size(int32_t T, int32_t width) {
     if (T < 0 || width < 1 || width % 8 != 0 || width > 16384) return 0;
-    return (sizeof(float) * 3 * (size_t)width * bwd_blocks(T, width) + 255) & ~size_t(255);
+    int blocks = 0;
+    for (int i = 0; i < 3; ++i) {  // whatever the types
+        int threads, vpt;
+        bwd_shape(width, i == 2, i == 1, threads, vpt);
+        blocks = max(blocks, bwd_blocks(T, threads));
+    }
+    return (sizeof(float) * 3 * (size_t)width * blocks + 255) & ~size_t(255);
 }
 
 gdn_status gdn_block_norm_bwd(const void* dy, const void* dres_out, const void* o, int64_t ldo, const void* gate,
@@ -575,7 +598,9 @@ gdn_status gdn_block_norm_bwd(const void* dy, const void* dres_out, const void* 
     p.dgate = dgate; p.dres = dres; p.part = static_cast<float*>(workspace);
     cudaStream_t s = (cudaStream_t)stream;
     if ((st = dispatch_norm(p, true, dtype, res_dtype, s)) != GDN_OK) return st;  // T == 0: zero partial sums
-    return launch_column_sum(p.part, bwd_blocks(T, width), 3 * (int64_t)width, width, 2 * width, dw_pre,
+    int threads, vpt;
+    bwd_shape(width, res_dtype != dtype, dtype == GDN_F32, threads, vpt);
+    return launch_column_sum(p.part, bwd_blocks(T, threads), 3 * (int64_t)width, width, 2 * width, dw_pre,
                              w_post ? dw_post : nullptr, scale ? dscale : nullptr, s);
 }
 
