@@ -435,9 +435,13 @@ __global__ void __launch_bounds__(NT, 4) conv_bwd_kernel(const ConvBwdParams p) 
 
 // One token per request: read K - 1 state rows, write K - 1 (shifted) and y.
 // Bound by those bytes (or, for a few requests, by the launch): a thread holds the
-// weights of eight channels and takes the requests gridDim.y apart.
+// weights of eight channels and takes the requests gridDim.y apart, the next one's
+// rows on their way while it works on one (256 requests of 8192 channels in bf16,
+// states in L2: 5.8 us, 7.7 without).
+template <typename T>
+constexpr int kStepBlocks = sizeof(T) == 4 ? 3 : 4;  // resident on an SM
 template <typename T, int K>
-__global__ void __launch_bounds__(NT) conv_step_kernel(const T* x, int64_t ldx, int batch, int C, const T* w,
+__global__ void __launch_bounds__(NT, kStepBlocks<T>) conv_step_kernel(const T* x, int64_t ldx, int batch, int C, const T* w,
                                                        const T* bias, T* states, int num_slots, const int32_t* src,
                                                        const int32_t* dst, T* y, int64_t ldy) {
     const int c0 = (blockIdx.x * NT + threadIdx.x) * 8;
@@ -453,38 +457,57 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const T* x, int64_t ldx, 
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c) b[c] = bias ? Elem<T>::to_f(bias[c0 + c]) : 0.f;
+    constexpr int VEC = sizeof(T) * 8 / 16;
+    struct Raw {
+        uint4 v[K][VEC];  // the state's rows and x, as they lie in memory
+        int from, to;     // slots read (-1: none) and written (-1: a padded row)
+    };
+    auto fetch = [&](int r, Raw& w) {
+        w.from = w.to = -1;
+        if (r >= batch) return;
+        w.to = dst ? __ldg(dst + r) : r;
+        w.from = src ? __ldg(src + r) : r;
+        if (w.to >= num_slots) w.to = -1;
+        if (w.to < 0) return;
+        if (w.from >= num_slots) w.from = -1;
+        const T* in = states + (int64_t)w.from * (K - 1) * C + c0;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+                w.v[j][v] = w.from >= 0 ? reinterpret_cast<const uint4*>(in + (int64_t)j * C)[v] : make_uint4(0, 0, 0, 0);
+            w.v[K - 1][v] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)r * ldx + c0) + v);
+        }
+    };
+    Raw cur, nxt;
+    fetch(blockIdx.y, cur);
     for (int r = blockIdx.y; r < batch; r += gridDim.y) {
-        int from = src ? __ldg(src + r) : r;
-        const int to = dst ? __ldg(dst + r) : r;
-        if (from >= num_slots) from = -1;
+        fetch(r + gridDim.y, nxt);
         T* yr = y + (int64_t)r * ldy + c0;
-        float rows[K][8], f[8];
-        if (to < 0 || to >= num_slots) {  // a padded row
+        float f[8];
+        if (cur.to < 0) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) f[c] = 0.f;
-            store8(yr, f);
-            continue;
-        }
-        const T* in = states + (int64_t)from * (K - 1) * C + c0;
-        T* out = states + (int64_t)to * (K - 1) * C + c0;
+        } else {
+            T* out = states + (int64_t)cur.to * (K - 1) * C + c0;
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) {
-            if (from >= 0) load8_rw(in + (int64_t)j * C, rows[j]);
-            else
+            for (int j = 1; j < K; ++j)
 #pragma unroll
-                for (int c = 0; c < 8; ++c) rows[j][c] = 0.f;
-        }
-        load8(x + (int64_t)r * ldx + c0, rows[K - 1]);
+                for (int v = 0; v < VEC; ++v) reinterpret_cast<uint4*>(out + (int64_t)(j - 1) * C)[v] = cur.v[j][v];
 #pragma unroll
-        for (int j = 1; j < K; ++j) store8(out + (int64_t)(j - 1) * C, rows[j]);
+            for (int c = 0; c < 8; ++c) f[c] = b[c];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            float acc = b[c];
+            for (int j = 0; j < K; ++j) {
+                float row[8];
+                load8_rw(reinterpret_cast<const T*>(cur.v[j]), row);
 #pragma unroll
-            for (int j = 0; j < K; ++j) acc = fmaf(wv[c * K + j], rows[j][c], acc);
-            f[c] = silu_fast(acc);
+                for (int c = 0; c < 8; ++c) f[c] = fmaf(wv[c * K + j], row[c], f[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) f[c] = silu_fast(f[c]);
         }
         store8(yr, f);
+        cur = nxt;
     }
 }
 
@@ -551,7 +574,7 @@ gdn_status run_bwd(ConvBwdParams p, int K, cudaStream_t s) {
 template <typename T>
 gdn_status run_step(const void* x, int64_t ldx, int batch, int C, const void* w, const void* bias, int K, void* states,
                     int num_slots, const int32_t* src, const int32_t* dst, void* y, int64_t ldy, cudaStream_t s) {
-    const int nx = (C / 8 + NT - 1) / NT, most = (device_sm_count() * 12 + nx - 1) / nx;  // about 12 blocks an SM
+    const int nx = (C / 8 + NT - 1) / NT, most = (device_sm_count() * kStepBlocks<T> + nx - 1) / nx;  // one wave
     const dim3 grid(nx, batch < most ? batch : most);
     const T *xt = static_cast<const T*>(x), *wt = static_cast<const T*>(w), *bt = static_cast<const T*>(bias);
     T *st = static_cast<T*>(states), *yt = static_cast<T*>(y);
