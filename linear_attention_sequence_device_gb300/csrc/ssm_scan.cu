@@ -536,8 +536,9 @@ int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH 
 // leaves segments of 512 tokens or more (the last blocks' idle time halves: 2.05 ->
 // 1.99 ms on 131072 tokens of 2048 channels); whole tiles, on whose starts the
 // checkpoints fall, down to one: few tokens are a walk, and a shorter one costs only
-// a fold (207 tokens of 88 channels: 19 us, 27 with segments of 64).
-void segments(int T, int ch, int N, int groups, int& seg, int& S) {
+// a fold (207 tokens of 88 channels: 19 us, 27 with segments of 64).  Returns the most
+// segments that a call of up to T tokens has, which the workspace is for.
+int segments(int T, int ch, int N, int groups, int& seg, int& S) {
     const int per = ch / groups, cb = channels_per_block(N);
     const int64_t blocks = (int64_t)groups * ((per + cb - 1) / cb);
     int64_t want = (int64_t)device_sm_count() * 4 / blocks;
@@ -550,6 +551,7 @@ void segments(int T, int ch, int N, int groups, int& seg, int& S) {
     if (seg < least) seg = least;
     S = (T + seg - 1) / seg;
     if (S < 1) S = 1;
+    return (int)want;
 }
 
 constexpr size_t kSmemPlain = 48 << 10;  // dynamic shared memory that needs no attribute
@@ -688,8 +690,8 @@ size_t gdn_ssm_scan_workspace_size(int32_t T, int32_t channels, int32_t d_state,
         d_state > 64)
         return 0;
     int seg, S;
-    segments(T, channels, d_state, groups, seg, S);
-    return (sizeof(float) * (size_t)S * channels * (d_state + 1) + 255) & ~size_t(255);
+    const int most = segments(T, channels, d_state, groups, seg, S);
+    return (sizeof(float) * (size_t)most * channels * (d_state + 1) + 255) & ~size_t(255);
 }
 
 gdn_status gdn_ssm_scan_fwd(const void* x, int64_t ldx, const void* dt, int64_t lddt, const void* z, int64_t ldz,

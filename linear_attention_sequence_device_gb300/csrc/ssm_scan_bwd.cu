@@ -588,7 +588,8 @@ int block_channels(int N) { return NW * NC * 32 / lanes_of(N); }
 // Segments: two waves of resident blocks (one wave leaves the launch before, whose
 // blocks cover more channels, too few blocks to fill the SMs), of whole pairs of
 // token blocks (71 tokens of 3584 channels: 54 us for both passes, 94 with segments of 64).
-void segments(int T, int ch, int N, int groups, int& tiles, int& seg, int& S) {
+// Returns the most segments that a call of up to T tokens has.
+int segments(int T, int ch, int N, int groups, int& tiles, int& seg, int& S) {
     const int per = ch / groups, cb = block_channels(N);
     tiles = (per + cb - 1) / cb;
     int64_t want = (int64_t)device_sm_count() * OCC * 2 / ((int64_t)groups * tiles);
@@ -599,6 +600,7 @@ void segments(int T, int ch, int N, int groups, int& tiles, int& seg, int& S) {
     if (seg < least) seg = least;
     S = (T + seg - 1) / seg;
     if (S < 1) S = 1;
+    return (int)want;
 }
 
 struct Layout {
@@ -606,14 +608,14 @@ struct Layout {
 };
 Layout layout(int T, int ch, int N, int groups) {
     int tiles, seg, S;
-    segments(T, ch, N, groups, tiles, seg, S);
+    const int most = segments(T, ch, N, groups, tiles, seg, S);
     auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
     Layout L{};
     size_t o = 0;
-    L.G = o; o += up(sizeof(float) * (size_t)S * ch * N);
-    L.sd = o; o += up(sizeof(float) * (size_t)S * ch);
+    L.G = o; o += up(sizeof(float) * (size_t)most * ch * N);
+    L.sd = o; o += up(sizeof(float) * (size_t)most * ch);
     L.bc = o; o += up(sizeof(float) * (size_t)groups * tiles * T * 2 * N);
-    L.par = o; o += up(sizeof(float) * (size_t)S * ch * (N + 2));
+    L.par = o; o += up(sizeof(float) * (size_t)most * ch * (N + 2));
     L.total = o;
     return L;
 }

@@ -191,3 +191,15 @@ def test_norm_refusals(lib):
     assert bwd(dy=None) == 1 and bwd(do=ODD) == 1 and bwd(dwp=None) == 1
     assert bwd(g=FAKE) == 1 and bwd(wq=FAKE) == 1 and bwd(sc=FAKE) == 1  # an input without its gradient
     assert bwd(wb=need - 1) == 9 and bwd(ws=None) == 9
+
+
+@pytest.mark.parametrize("ch,N,G", [(8, 16, 1), (152, 12, 1), (1024, 16, 4), (1536, 5, 2), (4096, 16, 1), (8192, 64, 8)])
+def test_workspace_sizes_do_not_fall(lib, ch, N, G):
+    """A workspace for a long call serves every shorter one."""
+    lens = sorted({int(1.17 ** i) + j for i in range(80) for j in (0, 1, 7)})
+    for size in (lambda T: lib.gdn_ssm_scan_workspace_size(T, ch, N, G),
+                 lambda T: lib.gdn_ssm_scan_bwd_workspace_size(T, ch, N, G),
+                 lambda T: lib.gdn_ssm_conv_bwd_workspace_size(T, ch, 4),
+                 lambda T: lib.gdn_block_norm_bwd_workspace_size(T, ch)):
+        s = [size(T) for T in lens]
+        assert all(a <= b for a, b in zip(s, s[1:])) and s[0] > 0
