@@ -43,34 +43,45 @@ def _lead(t, name):
     return dev, code
 
 
-def _ptr(t, name, dtype, dev, shape):
-    """Address of t (None: none), after its dtype, device and shape."""
-    if t is None:
-        return None
+def _wrong(t, name, dtype, dev, shape):
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on CUDA device {dev}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _ptr(t, name, dtype, dev, shape):
+    """Address of t (None: none), after its dtype, device and shape."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _wrong(t, name, dtype, dev, shape)
     return t.data_ptr()
 
 
 def _dense(t, name, dtype, dev, shape):
     """The same for an array that is read or written in place, which has to be contiguous."""
-    p = _ptr(t, name, dtype, dev, shape)
-    if p is not None and not t.is_contiguous():
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _wrong(t, name, dtype, dev, shape)
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return p
+    return t.data_ptr()
 
 
-def _row(t, name):
-    """Row stride of a [T, C] view with unit column stride."""
+def _rows(t, name, dtype, dev, shape):
+    """Address and row stride of a [T, C] view with unit column stride (None: none)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _wrong(t, name, dtype, dev, shape)
     s0, s1 = t.stride()
-    if s1 != 1 and t.shape[1] > 1:
+    if s1 != 1 and shape[1] > 1:
         raise ValueError(f"{name} must be a 2-d view with unit column stride")
     # a single row's stride is free: any valid one will do
-    return s0 if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+    return t.data_ptr(), s0 if shape[0] > 1 else (shape[1] + 7) // 8 * 8
 
 
 def _c(t):
@@ -111,10 +122,10 @@ def gdn_ssm_conv_fwd(x, w, bias, cu_seqlens, state=None, output_state=True, out=
     cu, n = _lens(cu_seqlens, dev)
     y = torch.empty_like(x) if out is None else out
     st = _new_like(state, (n, K - 1, C), dt, dev) if output_state else None
-    _run(_lib().gdn_ssm_conv_fwd(x.data_ptr(), _row(x, "x"), code, T, C, _ptr(w, "w", dt, dev, (C, K)),
+    _run(_lib().gdn_ssm_conv_fwd(*_rows(x, "x", dt, dev, (T, C)), code, T, C, _ptr(w, "w", dt, dev, (C, K)),
                                  _ptr(bias, "bias", dt, dev, (C,)), K, cu, n,
                                  _ptr(state, "state", dt, dev, (n, K - 1, C)), None if st is None else st.data_ptr(),
-                                 _ptr(y, "out", dt, dev, (T, C)), _row(y, "out"), _raw_stream(dev)))
+                                 *_rows(y, "out", dt, dev, (T, C)), _raw_stream(dev)))
     return y, st
 
 
@@ -131,11 +142,12 @@ def gdn_ssm_conv_bwd(dy, x, w, bias, cu_seqlens, state=None, dstate_out=None, wo
     r = dict(dx=torch.empty_like(x), dw=torch.empty((C, K), dtype=_F32, device=dev),
              dbias=None if bias is None else torch.empty((C,), dtype=_F32, device=dev),
              dstate=_new_like(dstate_out, (n, K - 1, C), _F32, dev))
-    _run(lib.gdn_ssm_conv_bwd(_ptr(dy, "dy", dt, dev, (T, C)), _row(dy, "dy"), x.data_ptr(), _row(x, "x"), code, T, C,
+    _run(lib.gdn_ssm_conv_bwd(*_rows(dy, "dy", dt, dev, (T, C)), *_rows(x, "x", dt, dev, (T, C)), code, T, C,
                               _ptr(w, "w", dt, dev, (C, K)), _ptr(bias, "bias", dt, dev, (C,)), K, cu, n,
                               _ptr(state, "state", dt, dev, (n, K - 1, C)),
-                              _ptr(dstate_out, "dstate_out", _F32, dev, (n, K - 1, C)), r["dx"].data_ptr(),
-                              _row(r["dx"], "dx"), r["dw"].data_ptr(), None if bias is None else r["dbias"].data_ptr(),
+                              _ptr(dstate_out, "dstate_out", _F32, dev, (n, K - 1, C)),
+                              *_rows(r["dx"], "dx", dt, dev, (T, C)), r["dw"].data_ptr(),
+                              None if bias is None else r["dbias"].data_ptr(),
                               r["dstate"].data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return r
 
@@ -149,11 +161,11 @@ def gdn_ssm_conv_step(x, w, bias, states, src=None, dst=None, out=None):
     dt, (B, C), K, n = x.dtype, x.shape, w.shape[-1], states.shape[0]
     w, bias = _c(w), _c(bias)
     y = torch.empty_like(x) if out is None else out
-    _run(_lib().gdn_ssm_conv_step(x.data_ptr(), _row(x, "x"), code, B, C, _ptr(w, "w", dt, dev, (C, K)),
+    _run(_lib().gdn_ssm_conv_step(*_rows(x, "x", dt, dev, (B, C)), code, B, C, _ptr(w, "w", dt, dev, (C, K)),
                                   _ptr(bias, "bias", dt, dev, (C,)), K,
                                   _dense(states, "states", dt, dev, (n, K - 1, C)), n,
                                   _dense(src, "src", _I32, dev, (B,)), _dense(dst, "dst", _I32, dev, (B,)),
-                                  _ptr(y, "out", dt, dev, (B, C)), _row(y, "out"), _raw_stream(dev)))
+                                  *_rows(y, "out", dt, dev, (B, C)), _raw_stream(dev)))
     return y
 
 
@@ -174,9 +186,9 @@ def _scan_args(x, dt, A_log, B, C, D, z, dt_bias):
         if (s[-1] != 1 and N > 1) or (G > 1 and s[-2] != N):
             raise ValueError(f"{name} must be a [T, groups, N] view with a dense (groups, N) part")
         ld.append(s[0] if T > 1 else G * N)
-    lead = (x.data_ptr(), _row(x, "x"), _ptr(dt, "dt", e, dev, (T, ch)), _row(dt, "dt"),
-            _ptr(z, "z", e, dev, (T, ch)), 0 if z is None else _row(z, "z"), _ptr(B, "B", e, dev, (T, G, N)), ld[0],
-            _ptr(C, "C", e, dev, (T, G, N)), ld[1], code)
+    tc, tgn = (T, ch), (T, G, N)
+    lead = (*_rows(x, "x", e, dev, tc), *_rows(dt, "dt", e, dev, tc), *_rows(z, "z", e, dev, tc),
+            _ptr(B, "B", e, dev, tgn), ld[0], _ptr(C, "C", e, dev, tgn), ld[1], code)
     par = [_c(A_log), _c(D), _c(dt_bias)]  # kept by the caller until its launch
     pp = (_ptr(par[0], "A_log", _F32, dev, (ch, N)), _ptr(par[1], "D", _F32, dev, (ch,)),
           _ptr(par[2], "dt_bias", _F32, dev, (ch,)))
@@ -212,7 +224,7 @@ def gdn_ssm_scan_fwd(x, dt, A_log, B, C, cu_seqlens, D=None, z=None, dt_bias=Non
     ck = torch.empty(ssm_scan_ckpt_shape(T, ch, N), dtype=_F32, device=dev) if checkpoints else None
     ws = _workspace(lib.gdn_ssm_scan_workspace_size(T, ch, N, G), workspace, dev)
     _run(lib.gdn_ssm_scan_fwd(*lead, *pp, _ptr(h0, "h0", _F32, dev, (n, ch, N)), cu, n, T, ch, N, G,
-                              _ptr(y, "out", x.dtype, dev, (T, ch)), _row(y, "out"),
+                              *_rows(y, "out", x.dtype, dev, (T, ch)),
                               None if hf is None else hf.data_ptr(), None if ck is None else ck.data_ptr(),
                               ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return y, hf, ck
@@ -236,7 +248,7 @@ def gdn_ssm_scan_bwd(dy, x, dt, A_log, B, C, cu_seqlens, ckpt, D=None, z=None, d
              dD=None if D is None else new((ch,), _F32), ddt_bias=None if dt_bias is None else new((ch,), _F32),
              dh0=_new_like(h0, (n, ch, N), _F32, dev))
     ws = _workspace(lib.gdn_ssm_scan_bwd_workspace_size(T, ch, N, G), workspace, dev)
-    _run(lib.gdn_ssm_scan_bwd(_ptr(dy, "dy", e, dev, (T, ch)), _row(dy, "dy"), *lead, *pp,
+    _run(lib.gdn_ssm_scan_bwd(*_rows(dy, "dy", e, dev, (T, ch)), *lead, *pp,
                               _ptr(h0, "h0", _F32, dev, (n, ch, N)),
                               _dense(ckpt, "ckpt", _F32, dev, ssm_scan_ckpt_shape(T, ch, N)),
                               _ptr(dh_final, "dh_final", _F32, dev, (n, ch, N)), cu, n, T, ch, N, G,
@@ -254,7 +266,7 @@ def gdn_ssm_scan_step(x, dt, A_log, B, C, states, D=None, z=None, dt_bias=None, 
     y = torch.empty_like(x) if out is None else out
     _run(_lib().gdn_ssm_scan_step(*lead, *pp, Bt, ch, N, G, _dense(states, "states", _F32, dev, (n, ch, N)), n,
                                   _dense(src, "src", _I32, dev, (Bt,)), _dense(dst, "dst", _I32, dev, (Bt,)),
-                                  _ptr(y, "out", x.dtype, dev, (Bt, ch)), _row(y, "out"), _raw_stream(dev)))
+                                  *_rows(y, "out", x.dtype, dev, (Bt, ch)), _raw_stream(dev)))
     return y
 
 
@@ -276,9 +288,9 @@ def gdn_block_norm_fwd(o, res, w_pre, w_post=None, gate=None, scale=None, eps=1e
     w_pre, w_post, scale = _c(w_pre), _c(w_post), _c(scale)
     y = torch.empty_like(o) if out is None else out
     r = torch.empty_like(res) if res_out is None else res_out
-    _run(_lib().gdn_block_norm_fwd(o.data_ptr(), _row(o, "o"), _ptr(gate, "gate", e, dev, TW),
-                                   0 if gate is None else _row(gate, "gate"), code, _dense(res, "res", rt, dev, TW),
-                                   _CODE[rt], _ptr(w_post, "w_post", e, dev, (W,)), _ptr(w_pre, "w_pre", e, dev, (W,)),
+    _run(_lib().gdn_block_norm_fwd(*_rows(o, "o", e, dev, TW), *_rows(gate, "gate", e, dev, TW), code,
+                                   _dense(res, "res", rt, dev, TW), _CODE[rt],
+                                   _ptr(w_post, "w_post", e, dev, (W,)), _ptr(w_pre, "w_pre", e, dev, (W,)),
                                    _ptr(scale, "scale", _F32, dev, (W,)), eps, T, W,
                                    _dense(r, "res_out", rt, dev, TW), _dense(y, "out", e, dev, TW), _raw_stream(dev)))
     return y, r
@@ -301,9 +313,9 @@ def gdn_block_norm_bwd(dy, dres_out, o, res_out, w_pre, w_post=None, gate=None, 
     r = dict(do=torch.empty_like(o), dgate=None if gate is None else torch.empty_like(o),
              dres=torch.empty_like(res_out), dw_pre=new((W,), _F32),
              dw_post=None if w_post is None else new((W,), _F32), dscale=None if scale is None else new((W,), _F32))
-    _run(lib.gdn_block_norm_bwd(_ptr(dy, "dy", e, dev, TW), _ptr(dres_out, "dres_out", rt, dev, TW), o.data_ptr(),
-                                _row(o, "o"), _ptr(gate, "gate", e, dev, TW), 0 if gate is None else _row(gate, "gate"),
-                                code, _dense(res_out, "res_out", rt, dev, TW), _CODE[rt],
+    _run(lib.gdn_block_norm_bwd(_ptr(dy, "dy", e, dev, TW), _ptr(dres_out, "dres_out", rt, dev, TW),
+                                *_rows(o, "o", e, dev, TW), *_rows(gate, "gate", e, dev, TW), code,
+                                _dense(res_out, "res_out", rt, dev, TW), _CODE[rt],
                                 _ptr(w_post, "w_post", e, dev, (W,)), _ptr(w_pre, "w_pre", e, dev, (W,)),
                                 _ptr(scale, "scale", _F32, dev, (W,)), eps, T, W,
                                 *(None if t is None else t.data_ptr() for t in r.values()), ws.data_ptr(), ws.numel(),
