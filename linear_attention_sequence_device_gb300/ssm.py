@@ -93,6 +93,11 @@ def _new_like(t, shape, dtype, dev):
     return torch.empty(shape, dtype=dtype, device=dev) if t is None else torch.empty_like(t)
 
 
+def _f32_like(t):
+    """A new fp32 array of the shape of a contiguous t (None: none)."""
+    return t if t is None else torch.empty_like(t) if t.dtype is _F32 else torch.empty_like(t, dtype=_F32)
+
+
 def _lens(cu, dev):
     """Address of cu_seqlens and the number of sequences."""
     if cu.dim() != 1 or cu.shape[0] < 2:
@@ -139,8 +144,7 @@ def gdn_ssm_conv_bwd(dy, x, w, bias, cu_seqlens, state=None, dstate_out=None, wo
     cu, n = _lens(cu_seqlens, dev)
     lib = _lib()
     ws = _workspace(lib.gdn_ssm_conv_bwd_workspace_size(T, C, K), workspace, dev)
-    r = dict(dx=torch.empty_like(x), dw=torch.empty((C, K), dtype=_F32, device=dev),
-             dbias=None if bias is None else torch.empty((C,), dtype=_F32, device=dev),
+    r = dict(dx=torch.empty_like(x), dw=_f32_like(w), dbias=_f32_like(bias),
              dstate=_new_like(dstate_out, (n, K - 1, C), _F32, dev))
     _run(lib.gdn_ssm_conv_bwd(*_rows(dy, "dy", dt, dev, (T, C)), *_rows(x, "x", dt, dev, (T, C)), code, T, C,
                               _ptr(w, "w", dt, dev, (C, K)), _ptr(bias, "bias", dt, dev, (C,)), K, cu, n,
@@ -242,11 +246,10 @@ def gdn_ssm_scan_bwd(dy, x, dt, A_log, B, C, cu_seqlens, ckpt, D=None, z=None, d
     h0, dh_final = _c(h0), _c(dh_final)
     lib = _lib()
     e = x.dtype
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
     r = dict(dx=torch.empty_like(x), ddt=torch.empty_like(x), dz=None if z is None else torch.empty_like(x),
-             dB=new((T, G, N), e), dC=new((T, G, N), e), dA_log=new((ch, N), _F32),
-             dD=None if D is None else new((ch,), _F32), ddt_bias=None if dt_bias is None else new((ch,), _F32),
-             dh0=_new_like(h0, (n, ch, N), _F32, dev))
+             dB=torch.empty_like(B, memory_format=torch.contiguous_format),
+             dC=torch.empty_like(C, memory_format=torch.contiguous_format), dA_log=_f32_like(keep[0]),
+             dD=_f32_like(keep[1]), ddt_bias=_f32_like(keep[2]), dh0=_new_like(h0, (n, ch, N), _F32, dev))
     ws = _workspace(lib.gdn_ssm_scan_bwd_workspace_size(T, ch, N, G), workspace, dev)
     _run(lib.gdn_ssm_scan_bwd(*_rows(dy, "dy", e, dev, (T, ch)), *lead, *pp,
                               _ptr(h0, "h0", _F32, dev, (n, ch, N)),
@@ -309,10 +312,8 @@ def gdn_block_norm_bwd(dy, dres_out, o, res_out, w_pre, w_post=None, gate=None, 
     dy, dres_out, w_pre, w_post, scale = _c(dy), _c(dres_out), _c(w_pre), _c(w_post), _c(scale)
     lib = _lib()
     ws = _workspace(lib.gdn_block_norm_bwd_workspace_size(T, W), workspace, dev)
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
     r = dict(do=torch.empty_like(o), dgate=None if gate is None else torch.empty_like(o),
-             dres=torch.empty_like(res_out), dw_pre=new((W,), _F32),
-             dw_post=None if w_post is None else new((W,), _F32), dscale=None if scale is None else new((W,), _F32))
+             dres=torch.empty_like(res_out), dw_pre=_f32_like(w_pre), dw_post=_f32_like(w_post), dscale=_f32_like(scale))
     _run(lib.gdn_block_norm_bwd(_ptr(dy, "dy", e, dev, TW), _ptr(dres_out, "dres_out", rt, dev, TW),
                                 *_rows(o, "o", e, dev, TW), *_rows(gate, "gate", e, dev, TW), code,
                                 _dense(res_out, "res_out", rt, dev, TW), _CODE[rt],
