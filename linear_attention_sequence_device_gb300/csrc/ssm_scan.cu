@@ -20,8 +20,8 @@
 // loads and stores, and delta, u and the SiLU.  63 % of the slots are used with the
 // four warps a scheduler that 128 registers allow.  Pairs of states, and of tokens'
 // deltas, go through the two-wide fp32 instructions, without which the slots would be
-// 36 more.  32768 tokens of 4096 channels in prompts of 512 to 8192: 1.03 ms, of which
-// the first launch 0.39 and the main one 0.63; two channels a lane, more tokens at a
+// 36 more.  32768 tokens of 4096 channels in prompts of 512 to 8192: 0.98 ms, of which
+// the first launch 0.36 and the main one 0.61; two channels a lane, more tokens at a
 // time or pairs in the SiLU and u too (registers) were no faster.
 //
 // Parallelism over tokens.  The packed tokens are cut into S segments of equal
@@ -63,6 +63,60 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
     const int cc = in ? c : cend - 1;  // a channel to read for lanes without one
     const int s = REV ? blockIdx.y + 1 : blockIdx.y;
     int t0 = s * p.seg, te = min(p.T, t0 + p.seg);
+    E* yp = static_cast<E*>(p.y) + cc;
+    const bool gate = MODE != SCAN_END && p.z;
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + cc) : 0.f, Dc = p.D ? __ldg(p.D + cc) : 0.f;
+    // the ring: [NST][x, dt, z][TT][CH]
+    E* ring = reinterpret_cast<E*>(smem4);
+    float* bcs = reinterpret_cast<float*>(ring + NST * NA * TT * CH);  // [2][TT][NB]
+    constexpr int VEC = 16 / sizeof(E), VR = CH / VEC;  // 16-byte vectors a row
+    const int c0 = grp * p.per + (blockIdx.x % p.tiles) * CH;
+    // row j of the walk is token t0 + j, or te - 1 - j backwards
+    int len = te - t0;
+    auto tok = [&](int j) { return (int64_t)(REV ? te - 1 - j : t0 + j); };
+    auto copy = [&](int jb, int st) {
+        if (jb < len) {
+#pragma unroll
+            for (int it = tid; it < TT * VR; it += NTH) {
+                const int r = it / VR, v = it - r * VR;
+                const bool ok = jb + r < len && c0 + v * VEC < cend;
+                const int64_t t = ok ? tok(jb + r) : t0;
+                const int cv = ok ? c0 + v * VEC : c0;
+                E* d = ring + (st * NA * TT + r) * CH + v * VEC;
+                const int bytes = ok ? 16 : 0;
+                cp_async16(d, static_cast<const E*>(p.x) + t * p.ldx + cv, bytes);
+                cp_async16(d + TT * CH, static_cast<const E*>(p.dt) + t * p.lddt + cv, bytes);
+                if (gate) cp_async16(d + 2 * TT * CH, static_cast<const E*>(p.z) + t * p.ldz + cv, bytes);
+            }
+        }
+        cp_async_commit();
+    };
+    E bc[PER];
+    const int64_t goff = (int64_t)grp * p.N;
+    auto fetch_bc = [&](int jb) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int it = tid + i * NTH, r = it / NB, j = it % NB, n = j % NP;
+            const int64_t t = tok(min(jb + r, len - 1));
+            const E* q = (j < NP ? static_cast<const E*>(p.B) + t * p.ldb : static_cast<const E*>(p.C) + t * p.ldc) + goff;
+            bc[i] = it < TT * NB && n < p.N ? load_now(q + n) : Elem<E>::from_f(0.f);
+        }
+    };
+    auto put_bc = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int it = tid + i * NTH;
+            if (it < TT * NB) bcs[b * TT * NB + it] = Elem<E>::to_f(bc[i]);
+        }
+    };
+    // the first tiles' copies start here, before the loads that the state's start needs; a launch for the segments'
+    // ends learns there where it begins
+    auto first_tiles = [&]() {
+        fetch_bc(0);
+#pragma unroll
+        for (int i = 0; i < NST - 1; ++i) copy(i * TT, i);
+    };
+    if (!LAST && p.T > 0) first_tiles();
     F2 A2[NS / 2], h[NS / 2];
 #pragma unroll
     for (int q = 0; q < NS / 2; ++q) {
@@ -155,52 +209,6 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
         }
     }
 
-    E* yp = static_cast<E*>(p.y) + cc;
-    const bool gate = MODE != SCAN_END && p.z;
-    const float bias = p.dt_bias ? __ldg(p.dt_bias + cc) : 0.f, Dc = p.D ? __ldg(p.D + cc) : 0.f;
-    // the ring: [NST][x, dt, z][TT][CH]
-    E* ring = reinterpret_cast<E*>(smem4);
-    float* bcs = reinterpret_cast<float*>(ring + NST * NA * TT * CH);  // [2][TT][NB]
-    constexpr int VEC = 16 / sizeof(E), VR = CH / VEC;  // 16-byte vectors a row
-    const int c0 = grp * p.per + (blockIdx.x % p.tiles) * CH;
-    // row j of the walk is token t0 + j, or te - 1 - j backwards
-    const int len = te - t0;
-    auto tok = [&](int j) { return (int64_t)(REV ? te - 1 - j : t0 + j); };
-    auto copy = [&](int jb, int st) {
-        if (jb < len) {
-#pragma unroll
-            for (int it = tid; it < TT * VR; it += NTH) {
-                const int r = it / VR, v = it - r * VR;
-                const bool ok = jb + r < len && c0 + v * VEC < cend;
-                const int64_t t = ok ? tok(jb + r) : t0;
-                const int cv = ok ? c0 + v * VEC : c0;
-                E* d = ring + (st * NA * TT + r) * CH + v * VEC;
-                const int bytes = ok ? 16 : 0;
-                cp_async16(d, static_cast<const E*>(p.x) + t * p.ldx + cv, bytes);
-                cp_async16(d + TT * CH, static_cast<const E*>(p.dt) + t * p.lddt + cv, bytes);
-                if (gate) cp_async16(d + 2 * TT * CH, static_cast<const E*>(p.z) + t * p.ldz + cv, bytes);
-            }
-        }
-        cp_async_commit();
-    };
-    E bc[PER];
-    const int64_t goff = (int64_t)grp * p.N;
-    auto fetch_bc = [&](int jb) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int it = tid + i * NTH, r = it / NB, j = it % NB, n = j % NP;
-            const int64_t t = tok(min(jb + r, len - 1));
-            const E* q = (j < NP ? static_cast<const E*>(p.B) + t * p.ldb : static_cast<const E*>(p.C) + t * p.ldc) + goff;
-            bc[i] = it < TT * NB && n < p.N ? load_now(q + n) : Elem<E>::from_f(0.f);
-        }
-    };
-    auto put_bc = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int it = tid + i * NTH;
-            if (it < TT * NB) bcs[b * TT * NB + it] = Elem<E>::to_f(bc[i]);
-        }
-    };
     // one token: state and y; shift: of its decays; u and the sum that makes y come scaled to what the state is
     auto token = [&](const float* row, float dlt, float u, float xv, float sil, float shift, float down, E* yo) {
         const F2 d = f2_dup(dlt), uu = f2_dup(u), bi = f2_dup(shift);
@@ -234,10 +242,11 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
             if (in && k == 0) *yo = Elem<E>::from_f(o);
         }
     };
-    fetch_bc(0);
+    if (LAST) {
+        len = te - t0;
+        first_tiles();
+    }
     put_bc(0);
-#pragma unroll
-    for (int i = 0; i < NST - 1; ++i) copy(i * TT, i);
     int buf = 0, st = 0;
     for (int jb = 0; jb < len; jb += TT, buf ^= 1, st = st == NST - 1 ? 0 : st + 1) {
         cp_async_wait<NST - 2>();
