@@ -14,15 +14,15 @@
 // under way without holding registers; B and C, which all channels of a group
 // read, are laid beside them as fp32 and come back as broadcasts.
 //
-// What bounds it: issue slots.  A token of 32 channels takes 124 of them (76 in the
-// launch that keeps end states only): 32 two-wide operations, which hold the FMA pipe
-// for two cycles each, 19 of the special function unit (16 decays; 4 cycles each), 13
-// loads and stores, and delta, u and the SiLU.  63 % of the slots are used with the
-// four warps a scheduler that 128 registers allow.  Pairs of states, and of tokens'
-// deltas, go through the two-wide fp32 instructions, without which the slots would be
-// 36 more.  32768 tokens of 4096 channels in prompts of 512 to 8192: 0.98 ms, of which
-// the first launch 0.36 and the main one 0.61; two channels a lane, more tokens at a
-// time or pairs in the SiLU and u too (registers) were no faster.
+// What bounds it: issue slots and the FMA pipe.  A token of 32 channels takes 107
+// slots (69 in the launch that keeps end states only): 37 two-wide operations, which
+// hold the FMA pipe for two cycles each, 19 of the special function unit (16 decays; 4
+// cycles each), 13 loads and stores, and the rest of delta, u and the SiLU.  63 % of
+// the slots are used with the four warps a scheduler that 128 registers allow.  Pairs
+// of states, and of tokens in delta and the SiLU, go through the two-wide fp32
+// instructions, without which the slots would be 37 more.  32768 tokens of 4096
+// channels in prompts of 512 to 8192: 0.89 ms, of which the first launch 0.33 and the
+// main one 0.54; two channels a lane were no faster.
 //
 // Parallelism over tokens.  The packed tokens are cut into S segments of equal
 // length, whatever the sequences' lengths.  A first launch runs each segment's
