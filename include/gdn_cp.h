@@ -26,7 +26,8 @@
  *     workspace argument of the entry points that have one (required but in
  *     gdn_chunk_fwd); none allocates.
  *   - All work is enqueued on `stream` (a cudaStream_t passed as void*; NULL
- *     = the legacy default stream).  No entry point synchronises the host.
+ *     = the legacy default stream) of the current device, which has to be the
+ *     one that the buffers are on.  No entry point synchronises the host.
  *   - Tokens are packed, batch 1: a token-major [T, ...] layout with
  *     sequence boundaries in cu_seqlens (int32, device, [num_seqs + 1],
  *     cu_seqlens[0] = 0, non-decreasing, cu_seqlens[num_seqs] = T).

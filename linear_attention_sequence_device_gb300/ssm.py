@@ -33,10 +33,14 @@ def _run(status):
 
 
 def _lead(t, name):
-    """Device and dtype code of the tensor that the others have to match."""
+    """Device and dtype code of the tensor that the others have to match.  The
+    library launches on the current device, whatever the stream."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on CUDA device {dev}, which is not the current device "
+                         f"({torch.cuda.current_device()}): make the call under torch.cuda.device({dev})")
     code = _CODE.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
