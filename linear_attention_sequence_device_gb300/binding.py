@@ -161,6 +161,9 @@ def _need(t, name, dtype=None):
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():  # where the library launches
+        raise ValueError(f"{name} is on CUDA device {t.get_device()}, which is not the current device "
+                         f"({torch.cuda.current_device()})")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 

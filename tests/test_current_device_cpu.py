@@ -46,3 +46,21 @@ def test_scan_layer_and_block_norm(name):
 def test_on_the_current_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     assert ssm._lead(X, "x") == (1, g.binding.GDN_BF16)
+
+
+LAYER = dict(chunk_fwd=lambda: g.gdn_chunk_fwd(X, X, X, X, X, X), chunk_bwd=lambda: g.gdn_chunk_bwd(X, X, X, X, X, X, X),
+             chunk_heads=lambda: g.binding.gdn_chunk_fwd_heads(X, X, X, X, X, X),
+             summary=lambda: g.gdn_chunk_summary(X, X, X, X, X), conv=lambda: g.gdn_conv_silu(X, X, None, X),
+             plan=lambda: g.gdn_cp_plan(X, 2), combine=lambda: g.gdn_state_combine(X, X),
+             shard=lambda: g.gdn_shard_fwd(X, X, None, X, X, X, 1, 1, 32, 32, 2),
+             noalloc=lambda: g.binding.gdn_shard_fwd_noalloc(X, X, None, X, X, X, 1, 1, 32, 32, 2),
+             layer=lambda: g.gdn_layer_fwd(X, X, None, X, X, X, X, X, X, X, 1, 1, 32, 32, 2),
+             head_major=lambda: g.binding.to_head_major(X), token_major=lambda: g.binding.to_token_major(X))
+
+
+@pytest.mark.parametrize("name", LAYER)
+def test_gated_delta_net_layer(name, monkeypatch):
+    # the first argument of most is of the element type, of two of another
+    monkeypatch.setattr(Elsewhere, "dtype", dict(plan=torch.int32, combine=torch.float32).get(name, torch.bfloat16))
+    with pytest.raises(ValueError, match="current device"):
+        LAYER[name]()
