@@ -486,8 +486,9 @@ gdn_status gdn_shard_fwd_noalloc(const void *x, const void *conv_w, const void *
  * 16-byte aligned x, y, state and state_out.  fp32 accumulation.  The SiLU is
  * a / (1 + e^-a) for both types (gdn_conv_silu takes a hardware tanh for
  * bf16).  The sizes of the workspaces from here on do not fall with T: one
- * for the longest call serves shorter ones.  A malformed cu_seqlens gives unspecified results, never an access
- * outside the arrays (this holds for every entry point below).
+ * for the longest call serves shorter ones.  T is at most 2^31 - 1 - 2^20, and a
+ * malformed cu_seqlens gives unspecified results, never an access outside the
+ * arrays (both hold for every entry point below).
  *
  * gdn_ssm_conv_bwd: gradients of the above for dy and dstate_out
  *   dy         device [T, channels] dtype, row stride lddy

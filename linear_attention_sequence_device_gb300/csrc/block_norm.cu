@@ -524,6 +524,7 @@ gdn_status check_norm(gdn_dtype dt, gdn_dtype rdt, int T, int W, const void* o, 
     if (dt != GDN_F32 && dt != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dt);
     if (rdt != GDN_F32 && rdt != dt) return fail(GDN_ERR_DTYPE, "res_dtype %d must be fp32 or the dtype", (int)rdt);
     if (T < 0 || W < 1) return fail(GDN_ERR_INVALID_ARG, "T=%d width=%d", T, W);
+    if (T > kMaxTokens) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%d tokens, more than %d", T, kMaxTokens);
     if (W % 8 != 0 || W > 16384)
         return fail(GDN_ERR_UNSUPPORTED_SHAPE, "width=%d must be a multiple of 8 up to 16384", W);
     if (!(eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "eps must not be negative");
@@ -562,7 +563,7 @@ gdn_status gdn_block_norm_fwd(const void* o, int64_t ldo, const void* gate, int6
 }
 
 size_t gdn_block_norm_bwd_workspace_size(int32_t T, int32_t width) {
-    if (T < 0 || width < 1 || width % 8 != 0 || width > 16384) return 0;
+    if (T < 0 || T > kMaxTokens || width < 1 || width % 8 != 0 || width > 16384) return 0;
     int blocks = 0;
     for (int i = 0; i < 3; ++i) {  // whatever the types
         int threads, vpt;

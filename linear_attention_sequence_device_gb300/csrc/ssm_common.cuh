@@ -7,6 +7,11 @@ namespace gdn {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The most tokens of a call.  Rows are counted in 32 bits, and a strip's, a segment's
+// or a grid's step beyond the last row stays below 2^31 with this much to spare (strips:
+// 65535 of them, each rounded up to four rows).
+constexpr int kMaxTokens = 0x7fffffff - (1 << 20);
+
 // eight consecutive elements (16-byte aligned) <-> fp32
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
     const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));

@@ -592,6 +592,7 @@ bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 gdn_status check_conv(gdn_dtype dtype, int rows, int channels, const void* w, int conv_k) {
     if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dtype);
     if (rows < 0 || channels < 1) return fail(GDN_ERR_INVALID_ARG, "rows=%d channels=%d", rows, channels);
+    if (rows > kMaxTokens) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%d tokens, more than %d", rows, kMaxTokens);
     if (channels % 8 != 0) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "channels=%d not a multiple of 8", channels);
     if (conv_k < 1 || conv_k > 4) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "conv_k=%d not in 1..4", conv_k);
     if (!w) return fail(GDN_ERR_INVALID_ARG, "w is NULL");
@@ -632,7 +633,7 @@ gdn_status gdn_ssm_conv_fwd(const void* x, int64_t ldx, gdn_dtype dtype, int32_t
 }
 
 size_t gdn_ssm_conv_bwd_workspace_size(int32_t T, int32_t channels, int32_t conv_k) {
-    if (T < 0 || channels < 1 || channels % 8 != 0 || conv_k < 1 || conv_k > 4) return 0;
+    if (T < 0 || T > kMaxTokens || channels < 1 || channels % 8 != 0 || conv_k < 1 || conv_k > 4) return 0;
     return (sizeof(float) * (size_t)channels * (conv_k + 1) * bwd_strips(T, channels) + 255) & ~size_t(255);
 }
 

@@ -664,6 +664,7 @@ gdn_status check_scan_shape(gdn_dtype dtype, int rows, int ch, int N, int groups
     if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dtype);
     if (rows < 0 || ch < 1 || groups < 1)
         return fail(GDN_ERR_INVALID_ARG, "rows=%d channels=%d groups=%d", rows, ch, groups);
+    if (rows > kMaxTokens) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%d tokens, more than %d", rows, kMaxTokens);
     if (ch % groups != 0 || (ch / groups) % 8 != 0)
         return fail(GDN_ERR_UNSUPPORTED_SHAPE, "channels=%d per group of %d must be a multiple of 8", ch, groups);
     if (N < 1 || N > 64) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "d_state=%d not in 1..64", N);
@@ -696,13 +697,13 @@ using namespace gdn;
 extern "C" {
 
 size_t gdn_ssm_scan_ckpt_floats(int32_t T, int32_t channels, int32_t d_state) {
-    if (T < 0 || channels < 1 || d_state < 1) return 0;
+    if (T < 0 || T > kMaxTokens || channels < 1 || d_state < 1) return 0;
     return (size_t)((T + kCkpt - 1) / kCkpt) * channels * d_state;
 }
 
 size_t gdn_ssm_scan_workspace_size(int32_t T, int32_t channels, int32_t d_state, int32_t groups) {
-    if (T < 0 || channels < 1 || groups < 1 || channels % groups || (channels / groups) % 8 || d_state < 1 ||
-        d_state > 64)
+    if (T < 0 || T > kMaxTokens || channels < 1 || groups < 1 || channels % groups || (channels / groups) % 8 ||
+        d_state < 1 || d_state > 64)
         return 0;
     int seg, S;
     const int most = segments(T, channels, d_state, groups, seg, S);

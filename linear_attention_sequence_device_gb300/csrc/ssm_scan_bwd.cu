@@ -660,8 +660,8 @@ using namespace gdn;
 extern "C" {
 
 size_t gdn_ssm_scan_bwd_workspace_size(int32_t T, int32_t channels, int32_t d_state, int32_t groups) {
-    if (T < 0 || channels < 1 || groups < 1 || channels % groups || (channels / groups) % 8 || d_state < 1 ||
-        d_state > 64)
+    if (T < 0 || T > kMaxTokens || channels < 1 || groups < 1 || channels % groups || (channels / groups) % 8 ||
+        d_state < 1 || d_state > 64)
         return 0;
     return layout(T, channels, d_state, groups).total;
 }
