@@ -494,6 +494,7 @@ gdn_status gdn_shard_fwd_noalloc(const void *x, const void *conv_w, const void *
  *   dy         device [T, channels] dtype, row stride lddy
  *   dstate_out device [num_seqs, conv_k - 1, channels] fp32, or NULL (zero)
  *   dx         device [T, channels] dtype, row stride lddx
+ *              (dy, dx, dstate_out and dstate 16-byte aligned)
  *   dw         device [channels, conv_k] fp32;  dbias device [channels] fp32
  *              or NULL;  dstate device [num_seqs, conv_k - 1, channels] fp32
  *              or NULL
@@ -552,7 +553,8 @@ gdn_status gdn_ssm_conv_step(const void *x, int64_t ldx, gdn_dtype dtype, int32_
  *   workspace device, >= gdn_ssm_scan_workspace_size(...) bytes, 256-byte
  *           aligned, contents on entry irrelevant
  * Needs channels / groups a multiple of 8, N in 1..64, row strides of x, dt,
- * z, y multiples of 8 and those arrays 16-byte aligned.  All arithmetic in
+ * z, y multiples of 8 and those arrays, h_final and ckpt 16-byte aligned (here
+ * and below; A_log, D, dt_bias, h0 and dh_final: as their type).  All arithmetic in
  * fp32 whatever the dtype; y is rounded once.  The packed tokens are cut into
  * segments that run at the same time; a first pass gives each segment's own
  * end state where the next one continues its sequence.
@@ -563,6 +565,7 @@ gdn_status gdn_ssm_conv_step(const void *x, int64_t ldx, gdn_dtype dtype, int32_
  *   dB, dC       device [T, groups, N] dtype, dense
  *   dA_log       device [channels, N] fp32;  dD, ddt_bias device [channels]
  *                fp32 or NULL;  dh0 device [num_seqs, channels, N] fp32 or NULL
+ *                (dy, dx, ddt, dz 16-byte aligned)
  *   workspace    device, >= gdn_ssm_scan_bwd_workspace_size(...) bytes,
  *                256-byte aligned, contents on entry irrelevant
  * Sums are taken in a fixed order: equal calls give equal bits.

@@ -759,8 +759,7 @@ gdn_status gdn_ssm_scan_step(const void* x, int64_t ldx, const void* dt, int64_t
     if ((st = check_scan_inputs(x, ldx, dt, lddt, z, ldz, B, ldb, C, ldc, A_log, channels, d_state, groups)) != GDN_OK)
         return st;
     if ((st = check_scan_row(y, ldy, channels, "y")) != GDN_OK) return st;
-    if (!states || !al16(states) || !al16(A_log))
-        return fail(GDN_ERR_INVALID_ARG, "states and A_log must be 16-byte aligned and states not NULL");
+    if (!states || !al16(states)) return fail(GDN_ERR_INVALID_ARG, "states must be 16-byte aligned and not NULL");
     ScanParams p{};
     p.x = x; p.ldx = ldx; p.dt = dt; p.lddt = lddt; p.z = z; p.ldz = ldz; p.B = B; p.ldb = ldb; p.C = C; p.ldc = ldc;
     p.A_log = A_log; p.D = D; p.dt_bias = dt_bias; p.ch = channels; p.N = d_state; p.per = channels / groups; p.y = y;

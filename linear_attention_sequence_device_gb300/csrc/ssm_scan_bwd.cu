@@ -69,6 +69,7 @@ struct ScanBwdParams {
     const float* A_log; const float* D; const float* dt_bias; const float* h0; const float* ckpt; const float* dhf;
     const int32_t* cu;
     int num_seqs, T, ch, N, per, tiles;
+    bool vec;  // states in pieces of four: N is a multiple of it and the caller's arrays are 16-byte aligned
     void* dx; void* ddt; void* dz; float* dh0;
     int seg, S;
     float* G; float* sd;   // [S, ch, N], [S, ch]: the segments' own start gradients and sums of delta
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
 
     // two channels side by side: delta, u and ds of both are one operand as they are read
     F2 A2[P][NS], dh[P][NS], h[P][NS], dA[P][NS];
-    const bool vec = p.N % 4 == 0;
+    const bool vec = p.vec;
     auto load_state = [&](F2 (&f)[P][NS], const float* src, int64_t row) {  // src [rows, ch, N] or null
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -686,8 +687,7 @@ gdn_status gdn_ssm_scan_bwd(const void* dy, int64_t lddy, const void* x, int64_t
         if (!al16(dx) || !al16(ddt) || !al16(dz))
             return fail(GDN_ERR_INVALID_ARG, "dx, ddt and dz must be 16-byte aligned");
     }
-    if (!al16(A_log) || !al16(h0) || !al16(ckpt) || !al16(dh_final))
-        return fail(GDN_ERR_INVALID_ARG, "A_log, h0, ckpt and dh_final must be 16-byte aligned");
+    if (!al16(ckpt)) return fail(GDN_ERR_INVALID_ARG, "ckpt must be 16-byte aligned");
     if (dh_final && dh_final == dh0) return fail(GDN_ERR_INVALID_ARG, "dh0 must not be dh_final");
     const Layout L = layout(T, channels, d_state, groups);
     if (!workspace || workspace_bytes < L.total)
@@ -701,6 +701,7 @@ gdn_status gdn_ssm_scan_bwd(const void* dy, int64_t lddy, const void* x, int64_t
     p.C = C; p.ldc = ldc; p.A_log = A_log; p.D = D; p.dt_bias = dt_bias; p.h0 = h0; p.ckpt = ckpt; p.dhf = dh_final;
     p.cu = cu_seqlens; p.num_seqs = num_seqs; p.T = T; p.ch = channels; p.N = d_state; p.per = channels / groups;
     p.dx = dx; p.ddt = ddt; p.dz = dz; p.dh0 = dh0;
+    p.vec = d_state % 4 == 0 && al16(A_log) && al16(h0) && al16(dh_final);
     segments(T, channels, d_state, groups, p.tiles, p.seg, p.S);
     p.G = reinterpret_cast<float*>(ws + L.G);
     p.sd = reinterpret_cast<float*>(ws + L.sd);
