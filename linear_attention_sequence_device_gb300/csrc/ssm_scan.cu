@@ -266,11 +266,11 @@ __global__ void __launch_bounds__(NTH, 4) scan_kernel(const ScanParams p) {
             E* yo = yp + (int64_t)tg * p.ldy;
             if (jg + UN <= len && next >= tg + UN) {
                 float dl[UN], sil[UN];
-                F2 dp[UN / 2];
+                F2 dp[UN / 2], et[UN / 2];
 #pragma unroll
                 for (int u = 0; u < UN; u += 2)
                     dp[u / 2] = f2(Elem<E>::to_f(xg[(TT + u) * CH]) + bias, Elem<E>::to_f(xg[(TT + u + 1) * CH]) + bias);
-                f2_softplus(dp);
+                f2_softplus(dp, et);
 #pragma unroll
                 for (int u = 0; u < UN; ++u) dl[u] = u & 1 ? dp[u / 2].y() : dp[u / 2].x();
 #pragma unroll

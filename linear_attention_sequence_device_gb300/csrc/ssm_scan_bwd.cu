@@ -373,15 +373,14 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
         constexpr int SG = BT / TPS < 4 ? 2 : 4;  // a lane's tokens staged together
 #pragma unroll
         for (int g0 = 0; g0 < BT; g0 += SG * TPS) {
-            F2 vp[SG / 2], dp[SG / 2], lp[SG / 2];  // dt + bias, delta, its slope
+            F2 vp[SG / 2], dp[SG / 2], et[SG / 2];  // v = dt + bias, delta, e^-|v|
 #pragma unroll
             for (int m = 0; m < SG; m += 2) {
                 const int i = (g0 + m * TPS) * WC + lane;
                 vp[m / 2] = f2(Elem<E>::to_f(raw[BT * WC + i]) + sbias, Elem<E>::to_f(raw[BT * WC + i + 32]) + sbias);
                 dp[m / 2] = vp[m / 2];
-                lp[m / 2] = f2_sigmoid(vp[m / 2]);
             }
-            f2_softplus(dp);
+            f2_softplus(dp, et);
 #pragma unroll
             for (int m = 0; m < SG; ++m) {
                 const int i = (g0 + m * TPS) * WC + lane, row = g0 + m * TPS + lane / WC;  // token row, channel sch
@@ -400,7 +399,8 @@ __global__ void __launch_bounds__(NT, OCC) scan_bwd_kernel(const ScanBwdParams p
                 dl[i] = ok ? d : 0.f;
                 uu[i] = ok ? d * xv * up : 0.f;
                 dsv[i] = ok ? g * down : 0.f;
-                slope[i] = of(vp) > 20.f ? 1.f : of(lp);
+                const float v = of(vp), t = of(et);
+                slope[i] = v > 20.f ? 1.f : (v < 0.f ? t : 1.f) * rcp_fast(1.f + t);  // the logistic function of v
                 q1[i] = qv;
                 xx[i] = xv;
             }
