@@ -463,7 +463,7 @@ void bwd_shape(int W, bool mixed, bool f32, int& threads, int& vpt) {
 int bwd_per_sm(int threads) { return threads >= 512 ? 1 : 512 / threads; }
 int bwd_blocks(int T, int threads) {
     const int n = device_sm_count() * bwd_per_sm(threads);
-    return T < n ? (T > 0 ? T : 1) : n;
+    return T < n ? (T > 0 ? T : 1) : (int)blocks_for_sum(T, n);
 }
 
 template <typename E, typename R, int VPT>

@@ -142,6 +142,16 @@ __constant__ const float kShift[kShifts] = {0.00439453125f, 0.0131835938f, 0.021
 __constant__ const float kShiftUp[kShifts] = {1.00305068f, 1.00918007f, 1.01534688f, 1.02155137f, 1.02779377f, 1.03407431f, 1.04039323f, 1.04675078f};  // 2^s
 __constant__ const float kShiftDown[kShifts] = {0.996958554f, 0.990903437f, 0.984885097f, 0.978903294f, 0.97295785f, 0.967048526f, 0.961175025f, 0.955337226f};  // 2^-s
 
+// Gradients that are sums over all tokens are added one by one within a block, in fp32,
+// and the blocks' partial sums behind it; terms that are alike then put the sum off by up
+// to half a step for every two of a block's.  So a block has this many tokens at most:
+// above, `wave` blocks side by side become whole multiples of that many.
+constexpr int kLongestSum = 1024;
+inline int64_t blocks_for_sum(int64_t tokens, int64_t wave) {
+    const int64_t least = (tokens + kLongestSum - 1) / kLongestSum;
+    return wave >= least ? wave : (least + wave - 1) / wave * wave;
+}
+
 // Two fp32 values in a register pair, for the two-wide instructions: the pipe's
 // rate is the same, the instructions are half.  Kept as 64 bits, so that the pair
 // is not taken apart and put together again between operations.

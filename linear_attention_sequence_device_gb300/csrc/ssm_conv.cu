@@ -511,15 +511,14 @@ __global__ void __launch_bounds__(NT, kStepBlocks<T>) conv_step_kernel(const T* 
     }
 }
 
-// Strips of the backward: enough blocks for four resident ones an SM, strips of
-// 64 rows at least.
+// Strips of the backward: one wave of four resident blocks an SM, of 16 rows at least
+// (104 rows: 13 us, 23 with 64), whole waves of kLongestSum rows at most.
 int bwd_strips(int T, int C) {
-    const int nx = (C / CV + NT - 1) / NT;
-    int n = device_sm_count() * 4 / nx;
-    const int most = T / 16;  // 104 rows: 13 us, 23 with strips of 64
+    const int nx = (C / CV + NT - 1) / NT, wave = device_sm_count() * 4 / nx, most = T / 16;
+    int64_t n = blocks_for_sum(T, wave > 1 ? wave : 1);
     if (n > most) n = most;
     if (n > 65535) n = 65535;
-    return n < 1 ? 1 : n;
+    return n < 1 ? 1 : (int)n;
 }
 
 template <typename T, int K>

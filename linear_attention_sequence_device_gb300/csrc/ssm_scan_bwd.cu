@@ -586,16 +586,21 @@ __global__ void __launch_bounds__(256) scan_bc_kernel(const float* bc, int T, in
 int lanes_of(int N) { return N <= 16 ? 4 : (N <= 32 ? 8 : 16); }
 int block_channels(int N) { return NW * NC * 32 / lanes_of(N); }
 
+constexpr int64_t kMostSegments = 32768;  // a byte each in the fold's shared memory
+
 // Segments: two waves of resident blocks (one wave leaves the launch before, whose
 // blocks cover more channels, too few blocks to fill the SMs), of whole pairs of
-// token blocks (71 tokens of 3584 channels: 54 us for both passes, 94 with segments of 64).
+// token blocks (71 tokens of 3584 channels: 54 us for both passes, 94 with segments of 64);
+// more where they would be longer than kLongestSum.
 // Returns the most segments that a call of up to T tokens has.
 int segments(int T, int ch, int N, int groups, int& tiles, int& seg, int& S) {
     const int per = ch / groups, cb = block_channels(N);
     tiles = (per + cb - 1) / cb;
-    int64_t want = (int64_t)device_sm_count() * OCC * 2 / ((int64_t)groups * tiles);
+    const int64_t waves = (int64_t)device_sm_count() * OCC * 2 / ((int64_t)groups * tiles);
     const int64_t least = 2 * BT, most = (T + least - 1) / least;
+    int64_t want = blocks_for_sum(T, waves > 1 ? waves : 1);
     if (want > most) want = most;
+    if (want > kMostSegments) want = kMostSegments;
     if (want < 1) want = 1;
     seg = (int)(((T + want - 1) / want + 2 * BT - 1) / (2 * BT) * (2 * BT));
     if (seg < least) seg = least;
