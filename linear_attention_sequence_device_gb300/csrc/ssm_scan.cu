@@ -642,9 +642,12 @@ gdn_status run_step(const ScanParams& p, int groups, int batch, float* states, i
     if (p.N <= 4) return run_step_k<E, 1, 4>(p, groups, batch, states, num_slots, src, dst, s);
     if (p.N <= 8) return run_step_k<E, 1, 8>(p, groups, batch, states, num_slots, src, dst, s);
     if (p.N <= 16) {
-        // below three warps a scheduler the latency of a lane's 16 states counts: four lanes a channel then, each with
-        // a quarter of them (4096 channels: 1 request 2.4 against 3.0 us, 16 4.7 against 5.4, 64 10.8 against 8.0)
-        if ((int64_t)batch * p.ch <= (int64_t)device_sm_count() * 4 * 32 * 3)
+        // few warps a scheduler: the latency of a lane's 16 states counts, and four lanes a channel take a quarter of
+        // them each.  With all 16 that pays below three warps of one lane a channel (4096 channels in us, four lanes
+        // against one: 2 requests 2.3, 2.9; 8 3.5, 3.8; 12 4.4, 4.6; 16 5.1, 5.3; 20 5.6, 5.6; 8192 channels: 3 requests
+        // 3.5, 3.5; 6 5.0, 4.6); with fewer, whose pieces are not the copies' whole rows, below one (12 states, 4096
+        // channels: 2 requests 2.7, 2.9; 4 2.9, 3.0; 6 4.3, 3.3; 12 6.1, 3.9)
+        if ((int64_t)batch * p.ch <= (int64_t)device_sm_count() * 4 * 32 * (p.N == 16 ? 3 : 1))
             return run_step_k<E, 4, 4>(p, groups, batch, states, num_slots, src, dst, s);
         return run_step_k<E, 1, 16>(p, groups, batch, states, num_slots, src, dst, s);
     }

@@ -172,7 +172,7 @@ STEP = [(130, 4096, 16, 1, BF, "Dzb"), (130, 4096, 16, 2, F32, "Dzb"), (130, 407
         (130, 4096, 12, 1, F32, "Db"), (130, 4056, 13, 1, BF, "zb"), (900, 64, 16, 1, F32, "Dzb"), (110, 512, 11, 1, BF, "Dz"),
         (130, 4096, 8, 1, BF, "Dzb"), (130, 4072, 7, 1, F32, "Dzb"), (130, 4096, 4, 1, F32, "zb"),
         (130, 2048, 32, 1, BF, "Dzb"), (130, 2040, 24, 1, F32, "Dzb"), (130, 1024, 64, 2, F32, "Dzb"),
-        (130, 1016, 50, 1, BF, "Dzb")]
+        (130, 1016, 50, 1, BF, "Dzb"), (2000, 8, 11, 1, F32, "Dzb"), (1200, 16, 13, 2, BF, "zb")]
 
 
 @pytest.mark.parametrize("batch,ch,N,G,dtype,opts", STEP)
