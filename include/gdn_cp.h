@@ -494,7 +494,8 @@ gdn_status gdn_shard_fwd_noalloc(const void *x, const void *conv_w, const void *
  *   dy         device [T, channels] dtype, row stride lddy
  *   dstate_out device [num_seqs, conv_k - 1, channels] fp32, or NULL (zero)
  *   dx         device [T, channels] dtype, row stride lddx
- *              (dy, dx, dstate_out and dstate 16-byte aligned)
+ *              (dy, dx, dstate_out and dstate 16-byte aligned; dx overlaps
+ *              neither x nor dy)
  *   dw         device [channels, conv_k] fp32;  dbias device [channels] fp32
  *              or NULL;  dstate device [num_seqs, conv_k - 1, channels] fp32
  *              or NULL

@@ -625,6 +625,7 @@ gdn_status gdn_ssm_conv_fwd(const void* x, int64_t ldx, gdn_dtype dtype, int32_t
     if (T > 0) {
         if ((st = check_rows(x, ldx, channels, "x")) != GDN_OK) return st;
         if ((st = check_rows(y, ldy, channels, "y")) != GDN_OK) return st;
+        if (x == y) return fail(GDN_ERR_INVALID_ARG, "y must not be x");
     }
     ConvParams p{x, ldx, w, bias, T, channels, cu_seqlens, num_seqs, state, state_out, y, ldy, 0};
     cudaStream_t s = (cudaStream_t)stream;
@@ -657,6 +658,7 @@ gdn_status gdn_ssm_conv_bwd(const void* dy, int64_t lddy, const void* x, int64_t
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes < required %zu", workspace ? workspace_bytes : 0, need);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (T > 0 && (dx == x || dx == dy)) return fail(GDN_ERR_INVALID_ARG, "dx must not be x or dy");
     ConvBwdParams p{dy, lddy, x, ldx, w, bias, T, channels, cu_seqlens, num_seqs, state, dstate_out, dx, lddx, dstate,
                     static_cast<float*>(workspace), 0};
     cudaStream_t s = (cudaStream_t)stream;

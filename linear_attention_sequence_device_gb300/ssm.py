@@ -123,8 +123,8 @@ def _workspace(need, given, dev):
 def gdn_ssm_conv_fwd(x, w, bias, cu_seqlens, state=None, output_state=True, out=None):
     """Causal depthwise conv1d + SiLU over packed sequences; x [T, C] (a
     row-strided view will do), w [C, K], bias [C] or None, state [N, K - 1, C]:
-    the rows before each sequence (None: zeros).  Returns (y [T, C], the state
-    after each sequence or None)."""
+    the rows before each sequence (None: zeros).  out must not overlap x.
+    Returns (y [T, C], the state after each sequence or None)."""
     dev, code = _lead(x, "x")
     dt, (T, C), K = x.dtype, x.shape, w.shape[-1]
     w, bias, state = _c(w), _c(bias), _c(state)

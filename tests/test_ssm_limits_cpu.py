@@ -52,3 +52,14 @@ def test_sizes(lib):
                  lambda T: lib.gdn_ssm_scan_bwd_workspace_size(T, 8, 1, 1), lambda T: lib.gdn_block_norm_bwd_workspace_size(T, 8)):
         assert size(MOST) > 0 and all(size(T) == 0 for T in OVER)
     assert lib.gdn_ssm_scan_ckpt_floats(MOST, 8, 1) == 8 * ((MOST + 7) // 8)
+
+
+def test_conv_results_over_its_inputs(lib):
+    """Strips read rows of their neighbours, so that a result in an input's place would be read as one."""
+    other, ws = ctypes.c_void_p(8192), (FAKE, 1 << 62)
+    assert lib.gdn_ssm_conv_fwd(FAKE, 8, 1, 100, 8, FAKE, None, 4, FAKE, 1, None, None, FAKE, 8, None) == 1
+    assert b"y" in lib.gdn_last_error()
+    for dy, x in ((FAKE, other), (other, FAKE)):
+        assert lib.gdn_ssm_conv_bwd(dy, 8, x, 8, 1, 100, 8, FAKE, None, 4, FAKE, 1, None, None, FAKE, 8, FAKE, None, None,
+                                    *ws, None) == 1
+        assert b"dx" in lib.gdn_last_error()
