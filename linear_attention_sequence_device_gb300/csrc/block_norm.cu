@@ -28,6 +28,9 @@
 // threads of 128 registers fill an SM, so that little covers a reduction).  Up to two
 // vectors a thread the weights stay in registers: read twice a row they cost half as
 // much again (8192 rows of 5120: 280 us, 164 kept).
+// Rows of which a block's share of shared memory holds fewer than two are read where
+// they are used: fp32 of 264 to 4096 columns and above 5120, bf16 above 10240, bf16
+// with an fp32 stream above 7168.
 #include "chunk_common.cuh"
 #include "ssm_common.cuh"
 
@@ -460,25 +463,40 @@ void bwd_shape(int W, bool mixed, bool f32, int& threads, int& vpt) {
     }
 }
 // 128 registers a thread: 512 threads fill an SM
-int bwd_per_sm(int threads) { return threads >= 512 ? 1 : 512 / threads; }
+constexpr int bwd_per_sm(int threads) { return threads >= 512 ? 1 : 512 / threads; }
 int bwd_blocks(int T, int threads) {
     const int n = device_sm_count() * bwd_per_sm(threads);
     return T < n ? (T > 0 ? T : 1) : (int)blocks_for_sum(T, n);
 }
 
+// Rows that a block's ring holds; below two there is none.
+template <typename E, typename R, int VPT>
+constexpr int ring_stages(int threads) {
+    const int n = (int)(kRingBytes / bwd_per_sm(threads) / row_bytes<E, R, VPT>(threads));
+    return n < kMaxStages ? n : kMaxStages;
+}
+// whether blocks of some size have a ring (or none)
+template <typename E, typename R, int VPT>
+constexpr bool some_block(bool ring) {
+    for (int threads = 32; threads <= kMaxThreads; threads += 32)
+        if ((ring_stages<E, R, VPT>(threads) >= 2) == ring) return true;
+    return false;
+}
+
 template <typename E, typename R, int VPT>
 gdn_status run_bwd(const NormParams& p, int threads, cudaStream_t s) {
-    const int grid = bwd_blocks(p.T, threads);
-    const size_t row = row_bytes<E, R, VPT>(threads);
-    int stages = (int)(kRingBytes / bwd_per_sm(threads) / row);
-    if (stages > kMaxStages) stages = kMaxStages;
-    if (stages < 2) {
-        norm_bwd_kernel<E, R, VPT, false><<<grid, threads, 0, s>>>(p, 1);
-        return check_launch("norm_bwd_kernel");
+    const int grid = bwd_blocks(p.T, threads), stages = ring_stages<E, R, VPT>(threads);
+    if constexpr (some_block<E, R, VPT>(false)) {
+        if (stages < 2) {
+            norm_bwd_kernel<E, R, VPT, false><<<grid, threads, 0, s>>>(p, 1);
+            return check_launch("norm_bwd_kernel");
+        }
     }
-    const gdn_status st = set_smem_attr((const void*)norm_bwd_kernel<E, R, VPT, true>, kRingBytes);
-    if (st != GDN_OK) return st;
-    norm_bwd_kernel<E, R, VPT, true><<<grid, threads, stages * row, s>>>(p, stages);
+    if constexpr (some_block<E, R, VPT>(true)) {
+        const gdn_status st = set_smem_attr((const void*)norm_bwd_kernel<E, R, VPT, true>, kRingBytes);
+        if (st != GDN_OK) return st;
+        norm_bwd_kernel<E, R, VPT, true><<<grid, threads, stages * row_bytes<E, R, VPT>(threads), s>>>(p, stages);
+    }
     return check_launch("norm_bwd_kernel");
 }
 

@@ -248,8 +248,7 @@ __device__ __forceinline__ void f2_store8(float* p, const F2 (&f)[4]) {
     reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0].b, f[1].b);
     reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2].b, f[3].b);
 }
-// one pair, or two, from shared memory
-__device__ __forceinline__ F2 f2_load(const float* p) { return F2{*reinterpret_cast<const unsigned long long*>(p)}; }
+// two pairs from shared memory
 __device__ __forceinline__ void f2_load2(const float* p, F2& a, F2& b) {
     const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
     a.b = v.x;
