@@ -274,8 +274,9 @@ def _own_conv_fwd(s):
 
 
 def _own_conv_bwd(s):
-    r = _pkg().gdn_ssm_conv_bwd(s["dy"], s["x"], s["w"], s["b"], s["cu"], state=s["state"],
-                                dstate_out=s["dstate_out"])
+    # the gradient of a bias of zeros is among the outputs where there is none
+    b = s["b"] if s["b"] is not None else torch.zeros_like(s["w"][:, 0])
+    r = _pkg().gdn_ssm_conv_bwd(s["dy"], s["x"], s["w"], b, s["cu"], state=s["state"], dstate_out=s["dstate_out"])
     return {k: r[k] for k in ("dx", "dw", "dbias", "dstate")}
 
 
