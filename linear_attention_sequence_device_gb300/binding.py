@@ -156,14 +156,18 @@ def _dt(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
+# a tenth of a microsecond; torch.cuda.current_device() takes twice that
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _need(t, name, dtype=None):
     if t is None:
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():  # where the library launches
+    if t.get_device() != _current_device():  # where the library launches
         raise ValueError(f"{name} is on CUDA device {t.get_device()}, which is not the current device "
-                         f"({torch.cuda.current_device()})")
+                         f"({_current_device()})")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 

@@ -38,9 +38,9 @@ def _lead(t, name):
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
+    if dev != binding._current_device():
         raise ValueError(f"{name} is on CUDA device {dev}, which is not the current device "
-                         f"({torch.cuda.current_device()}): make the call under torch.cuda.device({dev})")
+                         f"({binding._current_device()}): make the call under torch.cuda.device({dev})")
     code = _CODE.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")

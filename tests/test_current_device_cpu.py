@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import linear_attention_sequence_device_gb300 as g
-from linear_attention_sequence_device_gb300 import ssm
+from linear_attention_sequence_device_gb300 import binding, ssm
 
 
 class Elsewhere:
@@ -19,7 +19,7 @@ class Elsewhere:
 
 @pytest.fixture(autouse=True)
 def device_0(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
 
     def used(*a, **kw):
         raise AssertionError("allocated or launched")
@@ -44,18 +44,18 @@ def test_scan_layer_and_block_norm(name):
 
 
 def test_on_the_current_device(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    assert ssm._lead(X, "x") == (1, g.binding.GDN_BF16)
+    monkeypatch.setattr(binding, "_current_device", lambda: 1)
+    assert ssm._lead(X, "x") == (1, binding.GDN_BF16)
 
 
 LAYER = dict(chunk_fwd=lambda: g.gdn_chunk_fwd(X, X, X, X, X, X), chunk_bwd=lambda: g.gdn_chunk_bwd(X, X, X, X, X, X, X),
-             chunk_heads=lambda: g.binding.gdn_chunk_fwd_heads(X, X, X, X, X, X),
+             chunk_heads=lambda: binding.gdn_chunk_fwd_heads(X, X, X, X, X, X),
              summary=lambda: g.gdn_chunk_summary(X, X, X, X, X), conv=lambda: g.gdn_conv_silu(X, X, None, X),
              plan=lambda: g.gdn_cp_plan(X, 2), combine=lambda: g.gdn_state_combine(X, X),
              shard=lambda: g.gdn_shard_fwd(X, X, None, X, X, X, 1, 1, 32, 32, 2),
-             noalloc=lambda: g.binding.gdn_shard_fwd_noalloc(X, X, None, X, X, X, 1, 1, 32, 32, 2),
+             noalloc=lambda: binding.gdn_shard_fwd_noalloc(X, X, None, X, X, X, 1, 1, 32, 32, 2),
              layer=lambda: g.gdn_layer_fwd(X, X, None, X, X, X, X, X, X, X, 1, 1, 32, 32, 2),
-             head_major=lambda: g.binding.to_head_major(X), token_major=lambda: g.binding.to_token_major(X))
+             head_major=lambda: binding.to_head_major(X), token_major=lambda: binding.to_token_major(X))
 
 
 @pytest.mark.parametrize("name", LAYER)
