@@ -133,9 +133,12 @@ __device__ __forceinline__ float softplus_f(float v) {
 //    Eight pairs' shifts spread the arguments over sixteen places in eight cells, on
 //    average over which the error is between -0.8e-8 (arguments near 0) and -2.8e-8
 //    (near -0.07); the constant takes back 1.1e-8.
-// Measured on sequences of 50 to 200 tokens with a carried state: the final state is
-// off by 4.5e-7 of its norm, 1.6e-8 of that in one direction where the carried state
-// rules; without the shifts by 9e-7, of which 5e-7 in one direction.
+// Measured on sequences of 8 to 1200 tokens with carried states (4096 channels of 16
+// states, segments of 256 tokens), error in norm and of that in one direction: final
+// states 3.4e-7 and -0.2e-7, A_log's gradient 5.2e-7 and -0.5e-7; without the constant
+// 7.9e-7 and -4.8e-7, 15e-7 and -11e-7; without the shifts 6.0e-7 and -2.3e-7, 13e-7 and
+// -8e-7; with a constant of 1.3e-8 3.3e-7 and -1.0e-7, 5.6e-7 and -2.6e-7, of 2.0e-8
+// 4.5e-7 and 1.1e-7, 7.1e-7 and 2.4e-7.
 constexpr float kDecayBias = 1.6e-8f;
 constexpr int kShifts = 8;
 __constant__ const float kShift[kShifts] = {0.00439453125f, 0.0131835938f, 0.0219726562f, 0.0307617188f, 0.0395507812f, 0.0483398438f, 0.0571289062f, 0.0659179688f};

@@ -74,7 +74,9 @@ __device__ __forceinline__ void load_weights(const void* w, const void* b, int c
 // by asynchronous copies into a ring of kStages batches of RB rows that it fills and
 // reads alone.  A batch that no sequence starts in, all but a few, runs without a
 // check, which also lets the window stay where it is instead of moving up row by
-// row.  The SiLU is a / (1 + e^-a) for both types, so that a bf16 result is off by
+// row.  A block's threads cover 1024 channels, so that of 2112 channels the third
+// block has 8 threads at work and holds a slot all the same (fp32, 30038 rows: 138 us
+// for 75 us of bytes; 4096 channels, 32768 rows: 245 for 159).  The SiLU is a / (1 + e^-a) for both types, so that a bf16 result is off by
 // its own rounding only; in pairs that is 3 issue slots an element.
 template <typename T>
 constexpr int kStages = sizeof(T) == 4 ? 3 : 4;  // four blocks' rings fit an SM (fp32, 30038 x 2112: 172 us with 4)

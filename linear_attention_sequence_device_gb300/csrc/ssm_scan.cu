@@ -14,15 +14,17 @@
 // under way without holding registers; B and C, which all channels of a group
 // read, are laid beside them as fp32 and come back as broadcasts.
 //
-// What bounds it: issue slots and the FMA pipe.  A token of 32 channels takes 107
-// slots (69 in the launch that keeps end states only): 37 two-wide operations, which
+// What bounds it: issue slots and the FMA pipe.  A token of 32 channels takes 108
+// slots (70 in the launch that keeps end states only): 37 two-wide operations, which
 // hold the FMA pipe for two cycles each, 19 of the special function unit (16 decays; 4
 // cycles each), 13 loads and stores, and the rest of delta, u and the SiLU.  63 % of
-// the slots are used with the four warps a scheduler that 128 registers allow.  Pairs
+// the slots are used with the four warps a scheduler that 128 registers allow (fp32:
+// the ring leaves room for two blocks an SM with 9 to 16 states, three below).  Pairs
 // of states, and of tokens in delta and the SiLU, go through the two-wide fp32
 // instructions, without which the slots would be 37 more.  32768 tokens of 4096
-// channels in prompts of 512 to 8192: 0.89 ms, of which the first launch 0.33 and the
-// main one 0.54; two channels a lane were no faster.
+// channels in prompts of 512 to 8192: 0.90 ms, of which the first launch 0.34 and the
+// main one 0.55; two channels a lane were no faster.  In fp32 1.05 ms (0.37 and 0.66).
+// As many states in wider ones: 2048 channels of 32 states 1.03 ms, 1024 of 64 1.63.
 //
 // Parallelism over tokens.  The packed tokens are cut into S segments of equal
 // length, whatever the sequences' lengths.  A first launch runs each segment's
@@ -547,7 +549,8 @@ __global__ void __launch_bounds__(NTH, 4) scan_step_kernel(const ScanParams p, i
 
 int channels_per_block(int N) { return N <= 16 ? NTH : (N <= 32 ? NTH / 2 : NTH / 4); }
 
-// Segments of a call: one wave of four resident blocks an SM, two where that
+// Segments of a call: one wave of four resident blocks an SM (of the outputs' launch in
+// fp32 fewer fit, so that there it is two waves or one and a half), two where that
 // leaves segments of 512 tokens or more (the last blocks' idle time halves: 2.05 ->
 // 1.99 ms on 131072 tokens of 2048 channels); whole tiles, on whose starts the
 // checkpoints fall, down to one: few tokens are a walk, and a shorter one costs only

@@ -38,10 +38,12 @@
 // before, backwards from zero (or from dh_final where the sequence ends in it),
 // and the segments behind a block's own are folded by the block or by a launch.
 //
-// What bounds it: issue slots, 520 a token of 32 channels (114 two-wide operations
-// that hold the FMA pipe for two cycles, 34 of the special function unit, 62 loads,
+// What bounds it: issue slots, 526 a token of 32 channels (114 two-wide operations
+// that hold the FMA pipe for two cycles, 32 of the special function unit, 62 loads,
 // stores and exchanges), of which 62 % are used with the three warps a scheduler
-// that 168 registers allow.  32768 tokens of 4096 channels: 2.82 ms.
+// that 168 registers allow.  32768 tokens of 4096 channels: 2.82 ms; in fp32, whose
+// 80 KB of shared memory a block leave room for two blocks, 3.38.  As many states in
+// wider channels: 2048 of 32 3.04 ms, 1024 of 64 3.11.
 #include "chunk_common.cuh"
 #include "ssm_scan.cuh"
 
@@ -54,7 +56,7 @@ constexpr int NS = 4;      // states per lane and channel
 constexpr int P = 2;       // channel pairs per lane
 constexpr int NC = 2 * P;  // channels per lane
 constexpr int NW = 4;      // warps per block
-constexpr int OCC = 3;     // blocks per SM: 168 registers a thread
+constexpr int OCC = 3;     // blocks per SM: 168 registers a thread (fp32 up to 16 states: two, by shared memory)
 constexpr int NT = 32 * NW;
 static_assert(Q == 2 && kShifts % (BT / 2) == 0, "pieces are pairs of shifted decays");
 constexpr float kLn2 = 0.6931471805599453f;

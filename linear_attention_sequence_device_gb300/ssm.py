@@ -3,8 +3,10 @@ the short causal convolution with a state per sequence, the selective state
 space scan and the norms between two blocks, each with its gradient, and the
 single-token forms over a cache of states.
 
-Argument marshalling only, on the current stream; wrong arguments raise before
-anything is launched.  A single-token call's kernel takes a few microseconds, so
+Argument marshalling only, on the current stream of the current device, which has
+to be the tensors'; wrong arguments raise before anything is launched.  Results have
+no autograd history: gradients are calls of their own, from which
+examples/hybrid_lm.py makes autograd functions.  A single-token call's kernel takes a few microseconds, so
 the checks look at each tensor once and hand plain integers to the library, and
 results are made like an input (2.4 us between two launches; from a shape, a type
 and a device 4.8).  Rows with a stride of their own give dense results: an array
