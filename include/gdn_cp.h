@@ -36,7 +36,7 @@
  *     head h reads query/key head h / (Hv / Hk) (repeat_interleave on the
  *     head dimension, [HP-CP] the P2P wrapper's forward).
  *   - Supported: dk, dv in {32, 64, 128}; conv kernel size 1..4; chunk 64.
- *     (The selective scan layer and the block norm, at the end, state their own.)
+ *     (The entry points from the selective scan layer on state their own.)
  *   - dtype GDN_BF16: q/k/v/x/beta/o/conv weights in bf16, arithmetic and
  *     the state in fp32.  GDN_F32: everything fp32.  g is always fp32.
  *   - Errors detectable on the host return a non-OK status before anything
@@ -642,6 +642,117 @@ gdn_status gdn_block_norm_bwd(const void *dy, const void *dres_out, const void *
                               int32_t width, void *d_o, void *dgate, void *dres, float *dw_pre,
                               float *dw_post, float *dscale, void *workspace,
                               size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The gated delta rule for one token of `batch` requests over a cache of
+ * states, per value head h (query/key head h / (Hv / Hk)):
+ *
+ *   S' = e^g S[src],  u = v - S'^T k,  S = S' + beta k u^T,
+ *   o = S^T (scale q),  S[dst] = S
+ *
+ *   q, k    device [batch, Hk, dk] dtype, row strides ldq, ldk
+ *   v       device [batch, Hv, dv] dtype, row stride ldv
+ *   g       device [batch, Hv] fp32;  beta device [batch, Hv] dtype
+ *   states  device [num_slots, Hv, dk, dv] fp32, 16-byte aligned
+ *   src, dst  as for gdn_ssm_conv_step
+ *   o       device [batch, Hv, dv] dtype
+ * flags: GDN_QK_L2NORM as for gdn_chunk_fwd.  dk, dv in {32, 64, 128}; batch *
+ * Hv below 2^31; every array but states at any alignment of its type.  fp32
+ * arithmetic; o is rounded once.
+ *
+ * gdn_layer_step: the same behind the short conv of a layer, as gdn_layer_fwd
+ *   x       device [batch, 2 Hk dk + Hv dv] dtype, row stride ldx: the conv's
+ *           output (gdn_ssm_conv_step), channels [Q | K | V]; q and k are
+ *           divided by their norms
+ *   a, b    device [batch, Hv] dtype, row strides lda, ldb: g = -exp(A_log)
+ *           softplus(a + dt_bias), beta = sigmoid(b), both in fp32
+ *   z       device [batch, Hv, dv] dtype, row stride ldz, or NULL: then
+ *           y = norm_w * o / sqrt(mean(o^2) + norm_eps) * silu(z), of the
+ *           unrounded o;  norm_w device [dv] dtype
+ * ---------------------------------------------------------------------- */
+gdn_status gdn_chunk_step(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk,
+                          int64_t ldv, gdn_dtype dtype, const float *g, const void *beta,
+                          int32_t batch, int32_t Hk, int32_t Hv, int32_t dk, int32_t dv,
+                          float scale, uint32_t flags, float *states, int32_t num_slots,
+                          const int32_t *src, const int32_t *dst, void *o, void *stream);
+gdn_status gdn_layer_step(const void *x, int64_t ldx, const void *a, int64_t lda, const void *b,
+                          int64_t ldb, gdn_dtype dtype, const float *A_log, const float *dt_bias,
+                          const void *z, int64_t ldz, const void *norm_w, float norm_eps,
+                          int32_t batch, int32_t Hk, int32_t Hv, int32_t dk, int32_t dv,
+                          float scale, float *states, int32_t num_slots, const int32_t *src,
+                          const int32_t *dst, void *y, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Embedding:  y_t = scale table[token_t]
+ *
+ *   tokens  device [T] int32 or int64 (index_bits 32 or 64); a token outside
+ *           [0, vocab) is a padded one: a row of zeros, no gradient
+ *   table   device [vocab, width] dtype, row stride ldt
+ *   y       device [T, width] dtype, row stride ldy; must not overlap table
+ * Any width up to 2^20 and any alignment; 16-byte accesses where the width, the
+ * strides and the arrays allow them.
+ *
+ * gdn_embed_bwd: dtable[v] = scale * (sum of dy_t over the tokens v, in the
+ * tokens' order), added in fp32 and rounded once; with accumulate != 0 it is
+ * added to what dtable holds, and only the rows of tokens that occur are
+ * touched.  Equal calls give equal bits.
+ *   dy      device [T, width] dtype, row stride lddy
+ *   dtable  device [vocab, width] dtype, row stride ldd; must not overlap dy
+ *   workspace  device, >= gdn_embed_bwd_workspace_size(...) bytes, 256-byte
+ *           aligned, contents on entry irrelevant
+ * ---------------------------------------------------------------------- */
+gdn_status gdn_embed_fwd(const void *tokens, int32_t index_bits, const void *table, int64_t ldt,
+                         gdn_dtype dtype, int32_t vocab, int32_t T, int32_t width, float scale,
+                         void *y, int64_t ldy, void *stream);
+size_t gdn_embed_bwd_workspace_size(int32_t T, int32_t width);
+gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const void *tokens,
+                         int32_t index_bits, int32_t vocab, int32_t T, int32_t width, float scale,
+                         int32_t accumulate, void *dtable, int64_t ldd, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Softmax cross entropy over a vocabulary from hidden states and output
+ * weights; the logits x_tv = scale h_t . w_v never exist as an array:
+ *
+ *   lse_t = log sum_v e^{x_tv},  loss_t = lse_t - x_{t, target_t}
+ *
+ *   h       device [T, width] dtype, row stride ldh
+ *   w       device [vocab, width] dtype, row stride ldw
+ *   targets device [T] int32 or int64 (index_bits 32 or 64).  Negative: the
+ *           token is left out (loss 0, no gradient, whatever its h holds).
+ *           vocab or more: loss NaN, and NaN in what its gradient reaches.
+ *   loss, lse  device [T] fp32
+ * Any width up to 2^20, T and vocab up to 2^28.  bf16 rows of a multiple of 8
+ * elements are read in place, so that h and w then have to be 16-byte aligned
+ * with row strides that are multiples of 8; other widths and fp32 are read at
+ * any alignment, into a copy in the workspace.  Products of bf16 inputs are
+ * exact and added in fp32; fp32 inputs are split into three bf16 parts each,
+ * of whose nine products the six that count are added in fp32.
+ *
+ * gdn_vocab_loss_bwd: gradients of the above for dloss, from the forward's lse
+ *   dloss   device [T] fp32
+ *   dh      device [T, width] dtype, row stride lddh;  dw device [vocab,
+ *           width] dtype, row stride lddw; neither overlaps an input
+ * dh and dw are products with P_tv = scale dloss_t (softmax - one hot), which
+ * is rounded to bf16 for bf16 inputs and split like them for fp32.  The
+ * vocabulary is taken in pieces; the workspace holds one piece's P (half a
+ * gigabyte at most, or 1024 columns), and dh in fp32.
+ *   workspace  device, >= the _workspace_size(...) bytes of the call, 256-byte
+ *           aligned, contents on entry irrelevant
+ * Equal calls give equal bits.
+ * ---------------------------------------------------------------------- */
+size_t gdn_vocab_loss_fwd_workspace_size(int32_t T, int32_t vocab, int32_t width, gdn_dtype dtype);
+gdn_status gdn_vocab_loss_fwd(const void *h, int64_t ldh, const void *w, int64_t ldw,
+                              gdn_dtype dtype, const void *targets, int32_t index_bits, int32_t T,
+                              int32_t vocab, int32_t width, float scale, float *loss, float *lse,
+                              void *workspace, size_t workspace_bytes, void *stream);
+size_t gdn_vocab_loss_bwd_workspace_size(int32_t T, int32_t vocab, int32_t width, gdn_dtype dtype);
+gdn_status gdn_vocab_loss_bwd(const float *dloss, const void *h, int64_t ldh, const void *w,
+                              int64_t ldw, gdn_dtype dtype, const void *targets,
+                              int32_t index_bits, const float *lse, int32_t T, int32_t vocab,
+                              int32_t width, float scale, void *dh, int64_t lddh, void *dw,
+                              int64_t lddw, void *workspace, size_t workspace_bytes,
+                              void *stream);
 
 #ifdef __cplusplus
 }

@@ -95,6 +95,21 @@ SIGNATURES = {
     "gdn_block_norm_bwd_workspace_size": (_sz, [_i32, _i32]),
     "gdn_block_norm_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
                                           _vp, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    # single tokens of the gated delta rule, the embedding and the vocabulary's loss (front end: lm.py)
+    "gdn_chunk_step": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, _vp, _vp, _i32, _i32, _i32, _i32,
+                                      _i32, _f32, _u32, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "gdn_layer_step": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _vp, _vp, _i64, _vp, _f32,
+                                      _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "gdn_embed_fwd": (ctypes.c_int, [_vp, _i32, _vp, _i64, ctypes.c_int, _i32, _i32, _i32, _f32, _vp, _i64, _vp]),
+    "gdn_embed_bwd_workspace_size": (_sz, [_i32, _i32]),
+    "gdn_embed_bwd": (ctypes.c_int, [_vp, _i64, ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _i64, _vp,
+                                     _sz, _vp]),
+    "gdn_vocab_loss_fwd_workspace_size": (_sz, [_i32, _i32, _i32, ctypes.c_int]),
+    "gdn_vocab_loss_fwd": (ctypes.c_int, [_vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _f32, _vp,
+                                          _vp, _vp, _sz, _vp]),
+    "gdn_vocab_loss_bwd_workspace_size": (_sz, [_i32, _i32, _i32, ctypes.c_int]),
+    "gdn_vocab_loss_bwd": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i32, _vp, _i32, _i32, _i32,
+                                          _f32, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 32 << 20
 

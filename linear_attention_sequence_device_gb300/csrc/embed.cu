@@ -1,0 +1,581 @@
+// Embedding lookup with a scale, and its gradient by sorted tokens.
+//
+//   y_t = scale table[token_t]           dtable[v] = scale sum_{t : token_t = v} dy_t
+//
+// A token outside [0, vocab) is a padded one: a row of zeros, and no gradient.
+//
+// The lookup is a copy of rows; what bounds it is DRAM.
+//
+// The gradient sorts the tokens' positions by token (a stable radix sort, so that a
+// token's rows are added in their order and equal calls give equal bits), walks the
+// sorted rows in pieces of `piece` rows, and fills the rows of tokens that do not occur
+// with zeros.  A piece adds up the rows of one token after the other in registers, its
+// loads ahead, and writes a token's sum where all its rows are in the piece; the parts
+// of a token that several pieces hold go to the workspace in fp32 and are added, in the
+// pieces' order, by a second launch.  So a token that fills a twentieth of a batch costs no
+// more than the others.  What bounds it: dy read once, the table's gradient written once.
+#include "ssm_common.cuh"
+
+namespace gdn {
+namespace {
+
+// ---- vectors ---------------------------------------------------------------
+
+// VEC consecutive elements: 8 (bf16) or 4 (fp32) in 16-byte accesses, or one
+template <typename E, int VEC> struct Vec;
+template <> struct Vec<__nv_bfloat16, 8> {
+    using raw = uint4;
+    static __device__ __forceinline__ void to_f(const uint4& r, float (&f)[8]) {
+        const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 from_f(const float (&f)[8]) {
+        uint4 r;
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        return r;
+    }
+};
+template <> struct Vec<float, 4> {
+    using raw = float4;
+    static __device__ __forceinline__ void to_f(const float4& r, float (&f)[4]) {
+        f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
+    }
+    static __device__ __forceinline__ float4 from_f(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <> struct Vec<__nv_bfloat16, 1> {
+    using raw = __nv_bfloat16;
+    static __device__ __forceinline__ void to_f(raw r, float (&f)[1]) { f[0] = __bfloat162float(r); }
+    static __device__ __forceinline__ raw from_f(const float (&f)[1]) { return __float2bfloat16_rn(f[0]); }
+};
+template <> struct Vec<float, 1> {
+    using raw = float;
+    static __device__ __forceinline__ void to_f(raw r, float (&f)[1]) { f[0] = r; }
+    static __device__ __forceinline__ raw from_f(const float (&f)[1]) { return f[0]; }
+};
+
+template <typename I>
+__device__ __forceinline__ int token_of(const I* tokens, int64_t t, int vocab) {
+    const I v = __ldg(tokens + t);
+    return v < 0 || v >= (I)vocab ? -1 : (int)v;
+}
+
+// ---- lookup ----------------------------------------------------------------
+
+constexpr int FT = 256;  // threads of a block
+constexpr int FU = 4;    // vectors of a thread, loaded together
+
+// vector i of the output: row i / nv, vector i % nv of it
+template <typename E, int VEC, typename I>
+__global__ void __launch_bounds__(FT) embed_fwd_kernel(const I* __restrict__ tokens, const E* __restrict__ table,
+                                                       int64_t ldt, int vocab, int64_t T, int nv, float scale,
+                                                       E* __restrict__ y, int64_t ldy) {
+    using V = Vec<E, VEC>;
+    using R = typename V::raw;
+    const int64_t n = T * nv, first = (int64_t)blockIdx.x * (FT * FU) + threadIdx.x;
+    R r[FU];
+    int64_t at[FU];
+    bool real[FU];
+#pragma unroll
+    for (int u = 0; u < FU; ++u) {
+        const int64_t i = first + u * FT;
+        real[u] = false;
+        at[u] = -1;
+        if (i < n) {
+            const int64_t t = (n >> 31) ? i / nv : (int64_t)((unsigned)i / (unsigned)nv);
+            const int c = (int)(i - t * nv);
+            at[u] = t * ldy + (int64_t)c * VEC;
+            const int v = token_of(tokens, t, vocab);
+            real[u] = v >= 0;
+            if (real[u]) r[u] = __ldg(reinterpret_cast<const R*>(table + (int64_t)v * ldt + (int64_t)c * VEC));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < FU; ++u) {
+        if (at[u] < 0) continue;
+        float f[VEC];
+        if (real[u]) {
+            V::to_f(r[u], f);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[j] *= scale;
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[j] = 0.f;
+        }
+        *reinterpret_cast<R*>(y + at[u]) = V::from_f(f);
+    }
+}
+
+// ---- sort ------------------------------------------------------------------
+
+// Keys are the tokens, `vocab` for a padded one, which ends up behind the others.  A pass
+// sorts by up to 9 bits, low ones first: the blocks' counts of digits, then the
+// places.  Block b takes the rows [b per, (b + 1) per) of the order so far.
+constexpr int SW = 8;               // warps of a block
+constexpr int ST = SW * 32;
+constexpr int SI = 4;               // rows of a lane in one step
+constexpr int STILE = ST * SI;      // rows of a step
+constexpr int kBits = 9, kBins = 1 << kBits;
+constexpr int kMaxSortBlocks = 128;
+
+struct SortArgs {
+    const void* tokens;    // the first pass's input
+    const int* key_in; const int* pos_in;
+    int* key_out; int* pos_out;
+    int* count;            // [blocks][kBins] counts of this pass
+    int T, vocab, per, shift;
+};
+
+template <typename I>
+__device__ __forceinline__ int sort_key(const SortArgs& a, int i) {
+    if (a.key_in) return a.key_in[i];
+    const int v = token_of(static_cast<const I*>(a.tokens), i, a.vocab);
+    return v < 0 ? a.vocab : v;
+}
+
+template <typename I>
+__global__ void __launch_bounds__(ST) sort_count_kernel(const SortArgs a) {
+    __shared__ int hist[kBins];
+    for (int i = threadIdx.x; i < kBins; i += ST) hist[i] = 0;
+    __syncthreads();
+    const int lo = blockIdx.x * a.per, hi = min(a.T, lo + a.per);
+    for (int i = lo + threadIdx.x; i < hi; i += ST) atomicAdd(&hist[(sort_key<I>(a, i) >> a.shift) & (kBins - 1)], 1);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += ST) a.count[blockIdx.x * kBins + i] = hist[i];
+}
+
+// Sum of v over the threads below, for one value a thread; all ST threads
+__device__ __forceinline__ int exclusive_sum(int v, int* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, m);
+        if (lane >= m) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < SW; ++w) before += w < warp ? warp_sums[w] : 0;
+    __syncthreads();
+    return before + x - v;
+}
+
+template <typename I>
+__global__ void __launch_bounds__(ST) sort_place_kernel(const SortArgs a) {
+    __shared__ int base[kBins];       // where this block's next row of a digit goes
+    __shared__ int wc[SW][kBins];     // a warp's rows of a digit in this step, then where they begin
+    __shared__ int warp_sums[SW];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // rows of smaller digits anywhere, and of the same digit in the blocks before
+    {
+        int all[kBins / ST], mine[kBins / ST], sum = 0;
+#pragma unroll
+        for (int j = 0; j < kBins / ST; ++j) {
+            const int d = tid * (kBins / ST) + j;
+            all[j] = mine[j] = 0;
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int c = __ldg(a.count + b * kBins + d);
+                all[j] += c;
+                mine[j] += b < (int)blockIdx.x ? c : 0;
+            }
+            sum += all[j];
+        }
+        int at = exclusive_sum(sum, warp_sums);
+#pragma unroll
+        for (int j = 0; j < kBins / ST; ++j) {
+            base[tid * (kBins / ST) + j] = at + mine[j];
+            at += all[j];
+        }
+    }
+    const int lo = blockIdx.x * a.per, hi = min(a.T, lo + a.per);
+    for (int t0 = lo; t0 < hi; t0 += STILE) {
+        for (int i = lane; i < kBins; i += 32) wc[warp][i] = 0;
+        __syncwarp();
+        int key[SI], pos[SI], rank[SI];
+#pragma unroll
+        for (int j = 0; j < SI; ++j) {
+            const int i = t0 + warp * (32 * SI) + j * 32 + lane;
+            key[j] = i < hi ? sort_key<I>(a, i) : -1;
+            pos[j] = i < hi ? (a.pos_in ? a.pos_in[i] : i) : 0;
+        }
+#pragma unroll
+        for (int j = 0; j < SI; ++j) {
+            const int d = key[j] < 0 ? kBins : (key[j] >> a.shift) & (kBins - 1);
+            const unsigned same = __match_any_sync(0xffffffffu, d);
+            const int before = d < kBins ? wc[warp][d] : 0;
+            rank[j] = before + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (d < kBins && lane == __ffs(same) - 1) wc[warp][d] = before + __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int d = tid; d < kBins; d += ST) {  // where each warp's rows of digit d begin
+            int at = base[d];
+#pragma unroll
+            for (int w = 0; w < SW; ++w) {
+                const int c = wc[w][d];
+                wc[w][d] = at;
+                at += c;
+            }
+            base[d] = at;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < SI; ++j)
+            if (key[j] >= 0) {
+                const int to = wc[warp][(key[j] >> a.shift) & (kBins - 1)] + rank[j];
+                a.key_out[to] = key[j];
+                a.pos_out[to] = pos[j];
+            }
+        __syncwarp();  // a warp clears only its own counts
+    }
+}
+
+// ---- sums of sorted rows ---------------------------------------------------
+
+constexpr int PT = 128;       // threads of a block, a vector of columns each
+constexpr int kMaxPiece = 256;
+
+struct SumArgs {
+    const int* key; const int* pos;
+    int T, vocab, W, piece, pieces, zrows;
+    int64_t lddy, ldo;
+    const void* dy;
+    float scale;
+    void* out;
+    int into;           // add to what is there
+    float* part;        // [pieces][2][W]: a piece's first token's part, its last one's
+};
+
+// first i with key[i] >= v
+__device__ __forceinline__ int first_at(const int* key, int T, int v) {
+    int lo = 0, hi = T;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(key + mid) < v) lo = mid + 1; else hi = mid;
+    }
+    return lo;
+}
+
+template <typename O, int VEC>
+__device__ __forceinline__ void put_row(const SumArgs& a, int v, int c, const float (&acc)[VEC]) {
+    O* o = static_cast<O*>(a.out) + (int64_t)v * a.ldo + c;
+    if constexpr (VEC == 1) {
+        float f = acc[0] * a.scale;
+        if (a.into) f += Elem<O>::to_f(*o);
+        *o = Elem<O>::from_f(f);
+    } else {
+        constexpr int N = 16 / sizeof(O);  // elements of a 16-byte access
+#pragma unroll
+        for (int b = 0; b < VEC; b += N) {
+            using V = Vec<O, N>;
+            float f[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) f[j] = acc[b + j] * a.scale;
+            typename V::raw* q = reinterpret_cast<typename V::raw*>(o + b);
+            if (a.into) {
+                float old[N];
+                V::to_f(*q, old);
+#pragma unroll
+                for (int j = 0; j < N; ++j) f[j] += old[j];
+            }
+            *q = V::from_f(f);
+        }
+    }
+}
+
+// Blocks [0, pieces) walk a piece of the sorted rows each; the others fill the rows of
+// tokens that do not occur, zrows each.  blockIdx.y: PT * VEC columns.
+template <typename E, int VEC>
+__global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
+    using V = Vec<E, VEC>;
+    using R = typename V::raw;
+    const int c = (blockIdx.y * PT + threadIdx.x) * VEC;
+    const bool live = c < a.W;
+    if ((int)blockIdx.x >= a.pieces) {
+        __shared__ unsigned hit[kMaxPiece / 32];
+        const int v0 = ((int)blockIdx.x - a.pieces) * a.zrows, v1 = min(a.vocab, v0 + a.zrows);
+        for (int i = threadIdx.x; i < kMaxPiece / 32; i += PT) hit[i] = 0;
+        __syncthreads();
+        const int lo = first_at(a.key, a.T, v0), hi = first_at(a.key, a.T, v1);
+        // a token's rows lie together: only its first one counts
+        for (int i = lo + threadIdx.x; i < hi; i += PT) {
+            const int v = __ldg(a.key + i);
+            if (i == lo || __ldg(a.key + i - 1) != v) atomicOr(&hit[(v - v0) >> 5], 1u << ((v - v0) & 31));
+        }
+        __syncthreads();
+        if (!live) return;
+        float zero[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) zero[j] = 0.f;
+        for (int v = v0; v < v1; ++v)
+            if (!(hit[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)) put_row<E, VEC>(a, v, c, zero);
+        return;
+    }
+    __shared__ int key[kMaxPiece + 2];  // with the rows on either side
+    __shared__ int pos[kMaxPiece];
+    const int r0 = blockIdx.x * a.piece, n = min(a.piece, a.T - r0);
+    for (int i = threadIdx.x; i < n + 2; i += PT) {
+        const int r = r0 + i - 1;
+        key[i] = r < 0 || r >= a.T ? -1 : __ldg(a.key + r);
+        if (i > 0 && i <= n) pos[i - 1] = __ldg(a.pos + r);
+    }
+    __syncthreads();
+    if (!live) return;
+    const E* dy = static_cast<const E*>(a.dy) + c;
+    constexpr int AHEAD = 8;
+    R row[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+        if (u < n && key[u + 1] < a.vocab) row[u] = __ldg(reinterpret_cast<const R*>(dy + pos[u] * a.lddy));
+    float acc[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+    bool whole = key[0] != key[1];  // the token began in this piece
+    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int i = i0 + u;
+            if (i >= n) break;
+            const int v = key[i + 1];
+            if (v >= a.vocab) return;  // padded tokens are behind all others
+            float f[VEC];
+            V::to_f(row[u], f);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) acc[j] += f[j];
+            const int nx = i + AHEAD;
+            if (nx < n && key[nx + 1] < a.vocab) row[u] = __ldg(reinterpret_cast<const R*>(dy + pos[nx] * a.lddy));
+            if (key[i + 2] != v) {
+                if (whole) put_row<E, VEC>(a, v, c, acc);
+                else {
+                    float* w = a.part + (int64_t)blockIdx.x * 2 * a.W + c;
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) w[j] = acc[j];
+                }
+                whole = true;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+            } else if (i == n - 1) {  // goes on in the next piece
+                float* w = a.part + ((int64_t)blockIdx.x * 2 + 1) * a.W + c;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) w[j] = acc[j];
+            }
+        }
+    }
+}
+
+// Block b adds up the token that begins in piece b and goes on in the next ones: the last
+// part of piece b, the last parts of the pieces that it fills, and the first part of the
+// one that it ends in (of which the last part when it fills that too and ends there is
+// written as the first).
+template <typename E, int VEC>
+__global__ void __launch_bounds__(PT) embed_join_kernel(const SumArgs a) {
+    const int b = blockIdx.x, last = (b + 1) * a.piece - 1;  // the piece is full: another follows
+    const int v = __ldg(a.key + last);
+    if (v >= a.vocab || __ldg(a.key + last + 1) != v) return;                     // does not go on
+    if (b > 0 && __ldg(a.key + b * a.piece - 1) == v) return;                     // began earlier
+    const int c = (blockIdx.y * PT + threadIdx.x) * VEC;
+    if (c >= a.W) return;
+    const int end = first_at(a.key, a.T, v + 1);  // behind the token's last row
+    const int pe = (end - 1) / a.piece;           // the piece that it ends in
+    float acc[VEC];
+    const float* w = a.part + ((int64_t)b * 2 + 1) * a.W + c;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[j] = w[j];
+#pragma unroll 4
+    for (int p = b + 1; p < pe; ++p) {
+        const float* x = a.part + ((int64_t)p * 2 + 1) * a.W + c;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] += x[j];
+    }
+    const float* x = a.part + (int64_t)pe * 2 * a.W + c;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc[j] += x[j];
+    put_row<E, VEC>(a, v, c, acc);
+}
+
+// ---- host ------------------------------------------------------------------
+
+int sort_blocks(int64_t T) {
+    const int64_t n = (T + STILE - 1) / STILE;
+    return (int)(n < 1 ? 1 : n > kMaxSortBlocks ? kMaxSortBlocks : n);
+}
+// Rows of a piece: enough pieces for the GPU, and few parts of a token that fills many
+constexpr int kPieces = 2048;
+int piece_rows(int64_t T) {
+    int p = 16;
+    while (p < kMaxPiece && T / p > kPieces) p *= 2;
+    return p;
+}
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+struct Layout {
+    size_t key[2], pos[2], count, part, total;
+};
+Layout layout(int64_t T, int W) {
+    Layout l{};
+    size_t at = 0;
+    const size_t row = round256(4 * (size_t)T);
+    for (int i = 0; i < 2; ++i) {
+        l.key[i] = at; at += row;
+        l.pos[i] = at; at += row;
+    }
+    l.count = at; at += round256(sizeof(int) * (size_t)kMaxSortBlocks * kBins);
+    // the most pieces of any call of up to T rows
+    int64_t pieces = (T + 15) / 16;
+    if (pieces > kPieces + 1) pieces = kPieces + 1;
+    if (pieces < T / kMaxPiece + 1) pieces = T / kMaxPiece + 1;
+    l.part = at; at += round256(sizeof(float) * 2 * (size_t)pieces * W);
+    l.total = at;
+    return l;
+}
+
+template <typename I>
+gdn_status sort_tokens(const void* tokens, int T, int vocab, char* ws, const Layout& l, int& which, cudaStream_t s) {
+    int bits = 1;
+    while (bits < 31 && ((int64_t)1 << bits) <= vocab) ++bits;  // keys up to vocab
+    SortArgs a{};
+    a.tokens = tokens;
+    a.T = T;
+    a.vocab = vocab;
+    const int blocks = sort_blocks(T);
+    a.per = (T + blocks - 1) / blocks;
+    a.count = reinterpret_cast<int*>(ws + l.count);
+    which = 0;
+    for (int shift = 0; shift < bits; shift += kBits) {
+        a.shift = shift;
+        a.key_out = reinterpret_cast<int*>(ws + l.key[which]);
+        a.pos_out = reinterpret_cast<int*>(ws + l.pos[which]);
+        sort_count_kernel<I><<<blocks, ST, 0, s>>>(a);
+        sort_place_kernel<I><<<blocks, ST, 0, s>>>(a);
+        a.key_in = a.key_out;
+        a.pos_in = a.pos_out;
+        which ^= 1;
+    }
+    which ^= 1;
+    return check_launch("sort kernels");
+}
+
+template <typename E, int VEC>
+gdn_status run_sum(const SumArgs& a, cudaStream_t s) {
+    const unsigned ny = (unsigned)((a.W + PT * VEC - 1) / (PT * VEC));
+    const unsigned zeros = a.into ? 0u : (unsigned)((a.vocab + a.zrows - 1) / a.zrows);
+    if ((unsigned)a.pieces + zeros > 0) {
+        embed_sum_kernel<E, VEC><<<dim3(a.pieces + zeros, ny), PT, 0, s>>>(a);
+        gdn_status st = check_launch("embed_sum_kernel");
+        if (st != GDN_OK) return st;
+    }
+    if (a.pieces > 1) {
+        embed_join_kernel<E, VEC><<<dim3(a.pieces - 1, ny), PT, 0, s>>>(a);
+        return check_launch("embed_join_kernel");
+    }
+    return GDN_OK;
+}
+
+bool al(const void* p, int64_t ld, size_t e) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * (int64_t)e) % 16 == 0;
+}
+
+template <typename E, int VEC, typename I>
+gdn_status run_fwd_i(const void* tokens, const void* table, int64_t ldt, int vocab, int T, int W, float scale, void* y,
+                     int64_t ldy, cudaStream_t s) {
+    const int64_t n = (int64_t)T * (W / VEC), blocks = (n + FT * FU - 1) / (FT * FU);
+    if (blocks > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows of %d elements", T, W);
+    embed_fwd_kernel<E, VEC, I><<<(unsigned)blocks, FT, 0, s>>>(static_cast<const I*>(tokens),
+                                                                static_cast<const E*>(table), ldt, vocab, T, W / VEC,
+                                                                scale, static_cast<E*>(y), ldy);
+    return check_launch("embed_fwd_kernel");
+}
+template <typename E, int VEC>
+gdn_status run_fwd(int wide, const void* tokens, const void* table, int64_t ldt, int vocab, int T, int W, float scale,
+                   void* y, int64_t ldy, cudaStream_t s) {
+    return wide ? run_fwd_i<E, VEC, int64_t>(tokens, table, ldt, vocab, T, W, scale, y, ldy, s)
+                : run_fwd_i<E, VEC, int32_t>(tokens, table, ldt, vocab, T, W, scale, y, ldy, s);
+}
+
+gdn_status check_embed(gdn_dtype dtype, int32_t index_bits, int T, int W, int vocab, const void* tokens) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+    if (index_bits != 32 && index_bits != 64) return fail(GDN_ERR_DTYPE, "tokens of %d bits", index_bits);
+    if (T < 0 || W < 1 || vocab < 0) return fail(GDN_ERR_INVALID_ARG, "T=%d width=%d vocab=%d", T, W, vocab);
+    if (T > kMaxTokens) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%d tokens, more than %d", T, kMaxTokens);
+    if (W > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "width=%d above 2^20", W);
+    if (vocab > (1 << 30)) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "vocab=%d above 2^30", vocab);
+    if (T > 0 && !tokens) return fail(GDN_ERR_INVALID_ARG, "tokens is NULL");
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_embed_fwd(const void* tokens, int32_t index_bits, const void* table, int64_t ldt, gdn_dtype dtype,
+                         int32_t vocab, int32_t T, int32_t width, float scale, void* y, int64_t ldy, void* stream) {
+    gdn_status st = check_embed(dtype, index_bits, T, width, vocab, tokens);
+    if (st != GDN_OK) return st;
+    if (T == 0) return GDN_OK;
+    if (!y || (vocab > 0 && !table)) return fail(GDN_ERR_INVALID_ARG, "table or y is NULL");
+    if (ldt < width || ldy < width)
+        return fail(GDN_ERR_INVALID_ARG, "row strides of table and y must be >= width=%d", width);
+    cudaStream_t s = (cudaStream_t)stream;
+    const int w64 = index_bits == 64;
+    if (dtype == GDN_BF16)
+        return width % 8 == 0 && al(table, ldt, 2) && al(y, ldy, 2)
+                   ? run_fwd<__nv_bfloat16, 8>(w64, tokens, table, ldt, vocab, T, width, scale, y, ldy, s)
+                   : run_fwd<__nv_bfloat16, 1>(w64, tokens, table, ldt, vocab, T, width, scale, y, ldy, s);
+    return width % 4 == 0 && al(table, ldt, 4) && al(y, ldy, 4)
+               ? run_fwd<float, 4>(w64, tokens, table, ldt, vocab, T, width, scale, y, ldy, s)
+               : run_fwd<float, 1>(w64, tokens, table, ldt, vocab, T, width, scale, y, ldy, s);
+}
+
+size_t gdn_embed_bwd_workspace_size(int32_t T, int32_t width) {
+    if (T < 0 || T > kMaxTokens || width < 1 || width > (1 << 20)) return 0;
+    return layout(T, width).total;
+}
+
+gdn_status gdn_embed_bwd(const void* dy, int64_t lddy, gdn_dtype dtype, const void* tokens, int32_t index_bits,
+                         int32_t vocab, int32_t T, int32_t width, float scale, int32_t accumulate, void* dtable,
+                         int64_t ldd, void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status st = check_embed(dtype, index_bits, T, width, vocab, tokens);
+    if (st != GDN_OK) return st;
+    if (vocab == 0) return GDN_OK;
+    if (!dtable || (T > 0 && !dy)) return fail(GDN_ERR_INVALID_ARG, "dy or dtable is NULL");
+    if (ldd < width || (T > 0 && lddy < width))
+        return fail(GDN_ERR_INVALID_ARG, "row strides of dy and dtable must be >= width=%d", width);
+    const Layout l = layout(T, width);
+    if (!workspace || workspace_bytes < l.total)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes < required %zu", workspace ? workspace_bytes : 0, l.total);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    cudaStream_t s = (cudaStream_t)stream;
+    char* ws = static_cast<char*>(workspace);
+    int which = 0;
+    if (T > 0) {
+        st = index_bits == 64 ? sort_tokens<int64_t>(tokens, T, vocab, ws, l, which, s)
+                              : sort_tokens<int32_t>(tokens, T, vocab, ws, l, which, s);
+        if (st != GDN_OK) return st;
+    }
+    SumArgs a{};
+    a.key = reinterpret_cast<int*>(ws + l.key[which]);
+    a.pos = reinterpret_cast<int*>(ws + l.pos[which]);
+    a.T = T; a.vocab = vocab; a.W = width; a.piece = piece_rows(T);
+    a.pieces = (T + a.piece - 1) / a.piece;
+    a.zrows = vocab > 1 << 20 ? kMaxPiece : 32;
+    a.dy = dy; a.lddy = lddy; a.ldo = ldd; a.scale = scale; a.out = dtable; a.into = accumulate != 0;
+    a.part = reinterpret_cast<float*>(ws + l.part);
+    if (dtype == GDN_BF16)
+        return width % 8 == 0 && al(dy, lddy, 2) && al(dtable, ldd, 2) ? run_sum<__nv_bfloat16, 8>(a, s)
+                                                                       : run_sum<__nv_bfloat16, 1>(a, s);
+    return width % 4 == 0 && al(dy, lddy, 4) && al(dtable, ldd, 4) ? run_sum<float, 4>(a, s) : run_sum<float, 1>(a, s);
+}
+
+}  // extern "C"

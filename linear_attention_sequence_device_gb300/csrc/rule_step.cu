@@ -1,0 +1,266 @@
+// The gated delta rule for one token of each request, over a cache of states:
+//
+//   S' = e^g S,  u = v - S'^T k,  S <- S' + beta k u^T,  o = S^T (scale q)
+//      = S'^T (scale q) + beta scale (k.q) u
+//
+// so both column sums, S'^T k and S'^T q, come from one sweep over the state, which is
+// read once and written once.  q and k are read as they come, or divided by their
+// norms; the gates come ready or from the raw projections; the gated RMS norm of the
+// layer's output is taken from the sums in fp32, before anything is rounded.
+//
+// What bounds it: 8 dk dv bytes of state a head.  A block holds a whole head in
+// registers, 32 values a thread as eight 16-byte pieces of eight rows, all of whose
+// loads are in flight before the first sum; a warp covers whole lines of 1024 / dv rows.  The
+// sums over rows end in shared memory (two barriers); every warp forms the norms and
+// k.q by itself, which takes no barrier.
+#include "ssm_common.cuh"
+
+namespace gdn {
+namespace {
+
+struct StepParams {
+    const void* q; const void* k; const void* v;  // head h of request b at + b * ld + h * d
+    int64_t ldq, ldk, ldv;
+    const void* g;      // fp32 [batch, Hv], or with A_log the raw projection a
+    const void* beta;   // [batch, Hv], or with A_log the raw projection b
+    int64_t ldg, ldb;
+    const float* A_log; const float* dt_bias;
+    const void* z; int64_t ldz;  // gated norm of the output, or null
+    const void* norm_w;
+    float eps, scale;
+    int l2norm;
+    float* states;
+    const int32_t* src; const int32_t* dst;
+    int num_slots, Hk, Hv, group;
+    void* o;
+};
+
+template <typename E, int DK, int DV>
+__global__ void __launch_bounds__(DK * DV / 32, 1024 / (DK * DV / 32)) rule_step_kernel(const StepParams p) {
+    constexpr int NT = DK * DV / 32, NW = NT / 32;
+    constexpr int LPR = DV / 4;      // lanes of a row
+    constexpr int RPW = 32 / LPR;    // rows of a warp's one load
+    constexpr int KP = DK / 32;      // elements of q and k a lane
+    __shared__ float part[NW][2][DV];
+    __shared__ float sums[2][DV];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int b = blockIdx.x / p.Hv, hv = blockIdx.x % p.Hv, hk = hv / p.group;
+    int slot = p.src ? __ldg(p.src + b) : b;
+    const int to = p.dst ? __ldg(p.dst + b) : b;
+    E* const out = static_cast<E*>(p.o) + ((int64_t)b * p.Hv + hv) * DV;
+    if (to < 0 || to >= p.num_slots) {  // a padded row
+        for (int c = tid; c < DV; c += NT) out[c] = Elem<E>::from_f(0.f);
+        return;
+    }
+    const int row0 = warp * (8 * RPW) + lane / LPR, col = (lane % LPR) * 4;
+    const int64_t head = (int64_t)DK * DV;
+    float4 S[8];
+    if (slot >= 0 && slot < p.num_slots) {
+        const float* s = p.states + ((int64_t)slot * p.Hv + hv) * head + (int64_t)row0 * DV + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) S[i] = __ldcs(reinterpret_cast<const float4*>(s + i * RPW * DV));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const E* q = static_cast<const E*>(p.q) + (int64_t)b * p.ldq + hk * DK;
+    const E* k = static_cast<const E*>(p.k) + (int64_t)b * p.ldk + hk * DK;
+    const E* v = static_cast<const E*>(p.v) + (int64_t)b * p.ldv + hv * DV + col;
+    float kr[8], qr[8], vc[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        kr[i] = Elem<E>::load(k + row0 + i * RPW);
+        qr[i] = Elem<E>::load(q + row0 + i * RPW);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vc[j] = Elem<E>::load(v + j);
+    float qq = 0.f, kk = 0.f, kq = 0.f;
+#pragma unroll
+    for (int j = 0; j < KP; ++j) {
+        const float a = Elem<E>::load(q + lane + 32 * j), c = Elem<E>::load(k + lane + 32 * j);
+        qq = fmaf(a, a, qq);
+        kk = fmaf(c, c, kk);
+        kq = fmaf(a, c, kq);
+    }
+    float g, beta;
+    if (p.A_log) {
+        const float x = Elem<E>::load(static_cast<const E*>(p.g) + (int64_t)b * p.ldg + hv) + __ldg(p.dt_bias + hv);
+        g = -expf(__ldg(p.A_log + hv)) * (x > 20.f ? x : log1pf(expf(x)));
+        beta = 1.f / (1.f + expf(-Elem<E>::load(static_cast<const E*>(p.beta) + (int64_t)b * p.ldb + hv)));
+    } else {
+        g = __ldg(static_cast<const float*>(p.g) + (int64_t)b * p.ldg + hv);
+        beta = Elem<E>::load(static_cast<const E*>(p.beta) + (int64_t)b * p.ldb + hv);
+    }
+    const float decay = expf(g);
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+        qq += __shfl_xor_sync(0xffffffffu, qq, m);
+        kk += __shfl_xor_sync(0xffffffffu, kk, m);
+        kq += __shfl_xor_sync(0xffffffffu, kq, m);
+    }
+    const float nk = p.l2norm ? rsqrtf(kk + 1e-6f) : 1.f;
+    const float nq = p.scale * (p.l2norm ? rsqrtf(qq + 1e-6f) : 1.f);
+    float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float s[4] = {S[i].x, S[i].y, S[i].z, S[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sk[j] = fmaf(s[j], kr[i], sk[j]);
+            sq[j] = fmaf(s[j], qr[i], sq[j]);
+        }
+    }
+#pragma unroll
+    for (int m = LPR; m < 32; m <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sk[j] += __shfl_xor_sync(0xffffffffu, sk[j], m);
+            sq[j] += __shfl_xor_sync(0xffffffffu, sq[j], m);
+        }
+    if (lane < LPR) {
+        *reinterpret_cast<float4*>(&part[warp][0][col]) = make_float4(sk[0], sk[1], sk[2], sk[3]);
+        *reinterpret_cast<float4*>(&part[warp][1][col]) = make_float4(sq[0], sq[1], sq[2], sq[3]);
+    }
+    __syncthreads();
+    for (int c = tid; c < 2 * DV; c += NT) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) t += (&part[w][0][0])[c];
+        (&sums[0][0])[c] = t;
+    }
+    __syncthreads();
+    const float dk_ = decay * nk;
+    float bu[4];  // beta |k|^-1 u
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bu[j] = beta * nk * (vc[j] - dk_ * sums[0][col + j]);
+    float* d = p.states + ((int64_t)to * p.Hv + hv) * head + (int64_t)row0 * DV + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float4 r;
+        r.x = fmaf(kr[i], bu[0], decay * S[i].x);
+        r.y = fmaf(kr[i], bu[1], decay * S[i].y);
+        r.z = fmaf(kr[i], bu[2], decay * S[i].z);
+        r.w = fmaf(kr[i], bu[3], decay * S[i].w);
+        __stcs(reinterpret_cast<float4*>(d + i * RPW * DV), r);
+    }
+    if (warp == 0) {
+        float o[4], ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            o[j] = nq * fmaf(kq, bu[j], decay * sums[1][col + j]);
+            ss = fmaf(o[j], o[j], ss);
+        }
+        if (p.z) {
+#pragma unroll
+            for (int m = LPR / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+            const float r = 1.f / sqrtf(ss * (1.f / DV) + p.eps);
+            const E* z = static_cast<const E*>(p.z) + (int64_t)b * p.ldz + (int64_t)hv * DV + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float zz = Elem<E>::load(z + j);
+                o[j] *= r * Elem<E>::load(static_cast<const E*>(p.norm_w) + col + j) * (zz / (1.f + expf(-zz)));
+            }
+        }
+        if (lane < LPR) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) out[col + j] = Elem<E>::from_f(o[j]);
+        }
+    }
+}
+
+template <typename E, int DK>
+void run_dv(const StepParams& p, int dv, unsigned blocks, cudaStream_t s) {
+    if (dv == 32) rule_step_kernel<E, DK, 32><<<blocks, DK, 0, s>>>(p);
+    else if (dv == 64) rule_step_kernel<E, DK, 64><<<blocks, DK * 2, 0, s>>>(p);
+    else rule_step_kernel<E, DK, 128><<<blocks, DK * 4, 0, s>>>(p);
+}
+
+template <typename E>
+gdn_status run_step(const StepParams& p, int batch, int dk, int dv, cudaStream_t s) {
+    const unsigned blocks = (unsigned)batch * (unsigned)p.Hv;
+    if (dk == 32) run_dv<E, 32>(p, dv, blocks, s);
+    else if (dk == 64) run_dv<E, 64>(p, dv, blocks, s);
+    else run_dv<E, 128>(p, dv, blocks, s);
+    return check_launch("rule_step_kernel");
+}
+
+bool head_size(int d) { return d == 32 || d == 64 || d == 128; }
+
+gdn_status check_step(gdn_dtype dtype, int batch, int Hk, int Hv, int dk, int dv, const float* states, int num_slots,
+                      const int32_t* src, const int32_t* dst) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+    if (batch < 0 || Hk < 1 || Hv < 1 || num_slots < 0)
+        return fail(GDN_ERR_INVALID_ARG, "batch=%d Hk=%d Hv=%d num_slots=%d", batch, Hk, Hv, num_slots);
+    if (!head_size(dk) || !head_size(dv))
+        return fail(GDN_ERR_UNSUPPORTED_SHAPE, "dk=%d, dv=%d must be 32, 64 or 128", dk, dv);
+    if (Hv % Hk != 0) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "Hv=%d must be a multiple of Hk=%d", Hv, Hk);
+    if ((int64_t)batch * Hv > 0x7fffffff)
+        return fail(GDN_ERR_UNSUPPORTED_SHAPE, "batch * Hv = %lld above 2^31 - 1", (long long)batch * Hv);
+    if ((int64_t)Hv * 128 > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "Hv=%d", Hv);
+    if ((!src || !dst) && num_slots < batch)
+        return fail(GDN_ERR_INVALID_ARG, "num_slots=%d < batch=%d without slot numbers", num_slots, batch);
+    if (batch > 0 && (!states || (reinterpret_cast<uintptr_t>(states) & 15u)))
+        return fail(GDN_ERR_INVALID_ARG, "states must be 16-byte aligned and not NULL");
+    return GDN_OK;
+}
+
+gdn_status check_ld(const void* p, int64_t ld, int64_t least, const char* name) {
+    if (!p) return fail(GDN_ERR_INVALID_ARG, "%s is NULL", name);
+    if (ld < least)
+        return fail(GDN_ERR_INVALID_ARG, "row stride of %s (%lld) must be >= %lld", name, (long long)ld, (long long)least);
+    return GDN_OK;
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_chunk_step(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
+                          gdn_dtype dtype, const float* g, const void* beta, int32_t batch, int32_t Hk, int32_t Hv,
+                          int32_t dk, int32_t dv, float scale, uint32_t flags, float* states, int32_t num_slots,
+                          const int32_t* src, const int32_t* dst, void* o, void* stream) {
+    gdn_status st = check_step(dtype, batch, Hk, Hv, dk, dv, states, num_slots, src, dst);
+    if (st != GDN_OK) return st;
+    if (flags & ~(uint32_t)GDN_QK_L2NORM) return fail(GDN_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if (batch == 0) return GDN_OK;
+    if ((st = check_ld(q, ldq, (int64_t)Hk * dk, "q")) != GDN_OK) return st;
+    if ((st = check_ld(k, ldk, (int64_t)Hk * dk, "k")) != GDN_OK) return st;
+    if ((st = check_ld(v, ldv, (int64_t)Hv * dv, "v")) != GDN_OK) return st;
+    if (!g || !beta || !o) return fail(GDN_ERR_INVALID_ARG, "g, beta or o is NULL");
+    StepParams p{};
+    p.q = q; p.k = k; p.v = v; p.ldq = ldq; p.ldk = ldk; p.ldv = ldv; p.g = g; p.beta = beta; p.ldg = p.ldb = Hv;
+    p.scale = scale; p.l2norm = (flags & GDN_QK_L2NORM) != 0; p.states = states; p.src = src; p.dst = dst;
+    p.num_slots = num_slots; p.Hk = Hk; p.Hv = Hv; p.group = Hv / Hk; p.o = o;
+    return dtype == GDN_BF16 ? run_step<__nv_bfloat16>(p, batch, dk, dv, (cudaStream_t)stream)
+                             : run_step<float>(p, batch, dk, dv, (cudaStream_t)stream);
+}
+
+gdn_status gdn_layer_step(const void* x, int64_t ldx, const void* a, int64_t lda, const void* b, int64_t ldb,
+                          gdn_dtype dtype, const float* A_log, const float* dt_bias, const void* z, int64_t ldz,
+                          const void* norm_w, float norm_eps, int32_t batch, int32_t Hk, int32_t Hv, int32_t dk,
+                          int32_t dv, float scale, float* states, int32_t num_slots, const int32_t* src,
+                          const int32_t* dst, void* y, void* stream) {
+    gdn_status st = check_step(dtype, batch, Hk, Hv, dk, dv, states, num_slots, src, dst);
+    if (st != GDN_OK) return st;
+    if (batch == 0) return GDN_OK;
+    const int64_t nk = (int64_t)Hk * dk;
+    if ((st = check_ld(x, ldx, 2 * nk + (int64_t)Hv * dv, "x")) != GDN_OK) return st;
+    if ((st = check_ld(a, lda, Hv, "a")) != GDN_OK) return st;
+    if ((st = check_ld(b, ldb, Hv, "b")) != GDN_OK) return st;
+    if (z && (st = check_ld(z, ldz, (int64_t)Hv * dv, "z")) != GDN_OK) return st;
+    if (z && !norm_w) return fail(GDN_ERR_INVALID_ARG, "z needs norm_w");
+    if (!A_log || !dt_bias || !y) return fail(GDN_ERR_INVALID_ARG, "A_log, dt_bias or y is NULL");
+    const size_t e = dtype == GDN_BF16 ? 2 : 4;
+    StepParams p{};
+    p.q = x; p.k = static_cast<const char*>(x) + e * nk; p.v = static_cast<const char*>(x) + e * 2 * nk;
+    p.ldq = p.ldk = p.ldv = ldx; p.g = a; p.ldg = lda; p.beta = b; p.ldb = ldb; p.A_log = A_log; p.dt_bias = dt_bias;
+    p.z = z; p.ldz = ldz; p.norm_w = norm_w; p.eps = norm_eps; p.scale = scale; p.l2norm = 1; p.states = states;
+    p.src = src; p.dst = dst; p.num_slots = num_slots; p.Hk = Hk; p.Hv = Hv; p.group = Hv / Hk; p.o = y;
+    return dtype == GDN_BF16 ? run_step<__nv_bfloat16>(p, batch, dk, dv, (cudaStream_t)stream)
+                             : run_step<float>(p, batch, dk, dv, (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,900 @@
+// Softmax cross entropy over a vocabulary, straight from hidden states and output
+// weights, and its gradients; the logits never exist as an array.
+//
+//   x_tv = scale h_t . w_v        lse_t = log sum_v e^x_tv       loss_t = lse_t - x_{t, target_t}
+//   P_tv = scale dloss_t (e^{x_tv - lse_t} - [v = target_t])
+//   dh = P w                      dw = P^T h
+//
+// Four matrix products, one forward and three backward (the logits again, dh, dw), all
+// by one kernel on the tensor cores; what bounds them is those.  Forward: a tile's
+// epilogue keeps a maximum and a sum of exponentials a row, which a small launch joins.
+// Backward, a piece of the vocabulary after the other: a launch writes the piece's P in
+// bf16, another forms both gradients' products from it.
+//
+// Numerics.  Products of bf16 inputs are exact and added in fp32; maxima, sums, lse and
+// P are fp32.  P is rounded to bf16 for the products behind it, relative to its own
+// size, which puts dh and dw off by as much as their own rounding.  fp32 inputs are
+// split into three bf16 parts that hold all 24 bits, and so is P: six products of
+// parts, those of 2^-24 and more.
+//
+// The product kernel: a pair of CTAs (cta_group::2) forms a 256 x 256 tile, 128 rows of
+// each operand a CTA, from a ring of six stages of 64 along K by TMA; accumulators in tensor
+// memory, two of them, so that four warps' epilogue runs beside the next tile.  One
+// CTA an SM walks tiles by its number.
+#include <cuda.h>
+
+#include "ssm_common.cuh"
+#include "tc_util.cuh"
+
+namespace gdn {
+
+extern __device__ int g_gdn_timeouts;
+gdn_status set_smem_attr(const void* func, size_t bytes);
+
+namespace {
+
+// ---- tensor maps -------------------------------------------------------------
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeFn>(ptr);
+    }();
+    return fn;
+}
+
+// [parts][rows][cols] bf16 with row stride ld, parts `apart` rows from each other, boxes of
+// 64 columns and box_rows rows, 128-byte swizzle; what lies outside reads as zero and is
+// not written
+gdn_status make_map_rows(CUtensorMap* m, const void* base, int64_t ld, int64_t cols, int64_t rows, int64_t apart,
+                         int parts, int box_rows) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)apart};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    return GDN_OK;
+}
+
+gdn_status make_map3(CUtensorMap* m, const void* base, int64_t ld, int64_t cols, int64_t rows, int parts, int box_rows) {
+    return make_map_rows(m, base, ld, cols, rows, rows, parts, box_rows);
+}
+
+// ---- device: pairs of CTAs ---------------------------------------------------
+
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of this CTA's shared variable in the pair's first CTA
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// one box into this CTA's shared memory; its bytes are counted on a barrier of either CTA
+__device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, int y, int z, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
+__device__ __forceinline__ void store_box(const void* map, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// arrives on the barrier at this offset in both CTAs when the products so far are done
+__device__ __forceinline__ void commit_pair(uint64_t* mbar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            tc::smem_addr(mbar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+constexpr uint64_t kWaitNs = 4000000000ull;
+
+// Waits for a phase, up to kWaitNs or until another role gave up; sets *abort when it
+// runs out itself.
+__device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, volatile int* abort) {
+    if (tc::mbar_wait(mbar, parity, 64)) return true;
+    const uint64_t t0 = now_ns();
+    while (!tc::mbar_wait(mbar, parity, 64)) {
+        if (*abort) return false;
+        if (now_ns() - t0 > kWaitNs) {
+            if (!atomicExch(const_cast<int*>(abort), 1)) atomicAdd(&g_gdn_timeouts, 1);
+            return false;
+        }
+    }
+    return true;
+}
+
+// ---- the product kernel ------------------------------------------------------
+
+constexpr int BM = 256, BN = 256, BK = 64;      // a pair's tile
+constexpr int HALF = 128;                       // rows of an operand a CTA
+constexpr int STAGES = 6;
+constexpr int OPB = HALF * BK * 2;              // bytes of one operand of a stage
+constexpr int GT = 256;                         // threads: producer, products, allocation, (idle), 4 x epilogue
+constexpr int OUTB = HALF * 64 * 2;             // bytes of a staged 64-column piece of a result
+
+enum Kind { K_LSE = 0, K_P = 1, K_GRAD = 2 };
+
+struct Ctl {
+    uint64_t full[STAGES], empty[STAGES], done[2], free_[2];
+    uint32_t tmem;
+    int abort;
+};
+constexpr size_t kSmem = 1024 + (size_t)STAGES * 2 * OPB + 2 * OUTB + sizeof(Ctl);
+
+struct Maps {
+    CUtensorMap a, b;    // logits: h, w.  Gradients of h: P, w
+    CUtensorMap a2, b2;  // gradients of w: P, h
+    CUtensorMap out;     // P, or dw in bf16
+};
+
+struct GemmParams {
+    int mt, nt, group;    // tiles of 256 (logits; gradients of h), rows of tiles walked together
+    int kb;               // K steps
+    int splits, kper;     // gradients of h: K cut into splits of kper steps
+    int mt2, nt2, kb2;    // gradients of w
+    int products;         // 1, or 6 products of parts
+    int T, V, W;          // V: columns of this launch's logits (the piece's, from v0 on)
+    int v0, vocab;
+    float scale;
+    const void* targets; int wide;
+    float2* stat;         // K_LSE: [nt][T] maximum and sum of a tile's row
+    float* at;            // K_LSE: [T] the target's logit
+    const float* lse; const float* dloss;  // K_P
+    float* acc; int ldacc; int add;        // gradients of h: [splits][T][ldacc] fp32; add to what is there
+    void* dw; int64_t lddw; int dw_f32, dw_store;  // dw_store: by TMA through `out`
+};
+
+__device__ __forceinline__ int64_t target_of(const GemmParams& p, int t) {
+    return p.wide ? __ldg(static_cast<const long long*>(p.targets) + t) : __ldg(static_cast<const int*>(p.targets) + t);
+}
+
+struct Unit {
+    int m, n, k0, k1, split;
+    bool second;  // a gradient of w
+};
+
+template <int KIND>
+__device__ __forceinline__ int units(const GemmParams& p) {
+    return KIND == K_GRAD ? p.mt * p.nt * p.splits + p.mt2 * p.nt2 : p.mt * p.nt;
+}
+template <int KIND>
+__device__ __forceinline__ Unit unit(const GemmParams& p, int u) {
+    Unit r;
+    r.second = false;
+    r.split = 0;
+    r.k0 = 0;
+    r.k1 = p.kb;
+    if (KIND != K_GRAD) {
+        // `group` rows of tiles, column after column: the tiles that run together share
+        // few operands
+        const int per = p.group * p.nt, g = u / per, first = g * p.group;
+        const int rows = min(p.group, p.mt - first), in = u - g * per;
+        r.m = first + in % rows;
+        r.n = in / rows;
+        return r;
+    }
+    const int n1 = p.mt * p.nt;
+    if (u < n1 * p.splits) {
+        r.split = u / n1;
+        const int in = u - r.split * n1;
+        r.m = in / p.nt;
+        r.n = in % p.nt;
+        r.k0 = r.split * p.kper;
+        r.k1 = min(p.kb, r.k0 + p.kper);
+    } else {
+        const int in = u - n1 * p.splits;
+        r.second = true;
+        r.m = in / p.nt2;
+        r.n = in % p.nt2;
+        r.k1 = p.kb2;
+    }
+    return r;
+}
+
+// part of a and of b of product c: (1,1) (1,2) (2,1) (1,3) (2,2) (3,1)
+__device__ __forceinline__ int part_a(int c) { return (0x210100 >> (4 * c)) & 15; }
+__device__ __forceinline__ int part_b(int c) { return (0x012010 >> (4 * c)) & 15; }
+
+// eight fp32 values of a row, added to what is there or in its place
+__device__ __forceinline__ void put8(float* q, const float* v, bool add) {
+    float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
+    float4* o = reinterpret_cast<float4*>(q);
+    if (add) {
+        const float4 c = o[0], d = o[1];
+        a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+        b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+    }
+    o[0] = a;
+    o[1] = b;
+}
+
+template <int KIND, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
+    vocab_gemm_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
+    extern __shared__ unsigned char raw[];
+    unsigned char* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
+    const uint32_t ring = tc::smem_addr(base);
+    unsigned char* staged = base + STAGES * 2 * OPB;
+    Ctl& c = *reinterpret_cast<Ctl*>(staged + 2 * OUTB);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cta_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            tc::mbar_init(&c.full[s], 1);
+            tc::mbar_init(&c.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&c.done[b], 1);
+            tc::mbar_init(&c.free_[b], 8);  // a warp of the epilogue of either CTA each
+        }
+        c.abort = 0;
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_addr(&c.tmem)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc::fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = c.tmem;
+    const int n_units = units<KIND>(p);
+    const int np = F32 ? p.products : 1;
+
+    if (warp == 0 && lane == 0) {
+        // ---- loads ----
+        int s = 0, phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int u = pair; u < n_units && ok; u += pairs) {
+            const Unit w = unit<KIND>(p, u);
+            const int row_a = w.m * BM + (int)rank * HALF, row_b = w.n * BN + (int)rank * HALF;
+            for (int k = w.k0; k < w.k1 && ok; ++k)
+                for (int q = 0; q < np; ++q) {
+                    if (issued >= STAGES && !wait_for(&c.empty[s], phase ^ 1, &c.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) tc::mbar_expect_tx(&c.full[s], 4 * OPB);
+                    const uint32_t bar = in_leader(tc::smem_addr(&c.full[s]));
+                    const uint32_t da = ring + s * 2 * OPB, db = da + OPB;
+                    const int za = F32 ? part_a(q) : 0, zb = F32 ? part_b(q) : 0;
+                    if (KIND != K_GRAD) {
+                        load_box(da, &maps.a, k * BK, row_a, za, bar);
+                        load_box(db, &maps.b, k * BK, row_b, zb, bar);
+                    } else if (!w.second) {  // P [t][v], K = v; w [v][column]
+                        load_box(da, &maps.a, k * BK, row_a, za, bar);
+                        load_box(db, &maps.b, row_b, k * BK, zb, bar);
+                        load_box(db + OPB / 2, &maps.b, row_b + 64, k * BK, zb, bar);
+                    } else {  // P [t][v], K = t; h [t][column]
+                        load_box(da, &maps.a2, row_a, k * BK, za, bar);
+                        load_box(da + OPB / 2, &maps.a2, row_a + 64, k * BK, za, bar);
+                        load_box(db, &maps.b2, row_b, k * BK, zb, bar);
+                        load_box(db + OPB / 2, &maps.b2, row_b + 64, k * BK, zb, bar);
+                    }
+                    ++issued;
+                    if (++s == STAGES) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+        }
+        // every stage's products are done, and with them the loads and the arrivals here
+        if (ok) {
+            const int left = issued < STAGES ? (int)issued : STAGES;
+            int ls = s, lp = phase;
+            for (int i = 0; i < left && ok; ++i) {
+                if (issued < STAGES) {  // stages 0 .. issued - 1, first use
+                    ok = wait_for(&c.empty[i], 0, &c.abort);
+                } else {
+                    ok = wait_for(&c.empty[ls], lp ^ 1, &c.abort);
+                    if (++ls == STAGES) {
+                        ls = 0;
+                        lp ^= 1;
+                    }
+                }
+            }
+        }
+        if (!ok) {  // gave up: let the copies in flight land
+            const uint64_t t0 = now_ns();
+            while (now_ns() - t0 < 1000000ull) __nanosleep(1000);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---- products ----
+        int s = 0, phase = 0, it = 0;
+        bool ok = true;
+        for (int u = pair; u < n_units && ok; u += pairs, ++it) {
+            const Unit w = unit<KIND>(p, u);
+            const int buf = it & 1;
+            if (it >= 2 && !wait_for(&c.free_[buf], ((it >> 1) & 1) ^ 1, &c.abort)) break;
+            tc::fence_after();
+            const bool a_mn = KIND == K_GRAD && w.second, b_mn = KIND == K_GRAD;
+            const uint32_t id = tc::idesc_bf16(BM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u);
+            const uint32_t d = tmem + (uint32_t)buf * BN;
+            uint32_t acc = 0;
+            const int steps = (w.k1 - w.k0) * np;
+            for (int k = 0; k < steps; ++k) {
+                if (!wait_for(&c.full[s], phase, &c.abort)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t ra = ring + s * 2 * OPB, rb = ra + OPB;
+                const uint64_t da = tc::desc(ra, a_mn ? OPB / 2 : 16, 1024), db = tc::desc(rb, b_mn ? OPB / 2 : 16, 1024);
+                const uint64_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;
+#pragma unroll
+                for (int j = 0; j < BK / 16; ++j) {
+                    mma_pair(d, da + sa * j, db + sb * j, id, acc);
+                    acc = 1;
+                }
+                commit_pair(&c.empty[s]);
+                if (++s == STAGES) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok) commit_pair(&c.done[buf]);
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue: this thread's row of the tile ----
+        const int row = (warp - 4) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)((warp - 4) * 32) << 16);
+        int it = 0;
+        for (int u = pair; u < n_units; u += pairs, ++it) {
+            const Unit w = unit<KIND>(p, u);
+            const int buf = it & 1;
+            // the four warps go on together or not at all
+            if (!tc::bar_and(1, 128, wait_for(&c.done[buf], (it >> 1) & 1, &c.abort))) break;
+            tc::fence_after();
+            const uint32_t d = lanes + (uint32_t)buf * BN;
+            const int r = w.m * BM + (int)rank * HALF + row;
+            const int c0 = w.n * BN;
+            if (KIND == K_LSE) {
+                const bool real = r < p.T;
+                const int64_t tgt = real ? target_of(p, r) : -1;
+                float top = -INFINITY, sum = 0.f;
+                for (int j = 0; j < BN; j += 32) {
+                    float x[32];
+                    tc::ld32(d + j, x);
+                    const int left = p.V - (c0 + j);
+                    float m = top;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        x[i] = i < left ? x[i] * p.scale : -INFINITY;
+                        m = fmaxf(m, x[i]);
+                    }
+                    const int64_t o = tgt - (c0 + j);
+                    if (o >= 0 && o < 32) {
+                        const unsigned bit = 1u << (int)o;  // (a comparison would index x, in local memory)
+                        float v = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v = bit & (1u << i) ? x[i] : v;
+                        p.at[r] = v;
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    sum *= exp2_fast((top - ref) * kLog2e);
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        s0 += exp2_fast((x[i] - ref) * kLog2e);
+                        s1 += exp2_fast((x[i + 1] - ref) * kLog2e);
+                    }
+                    sum += s0 + s1;
+                    top = m;
+                }
+                if (real) p.stat[(int64_t)w.n * p.T + r] = make_float2(top, sum);
+            } else if (KIND == K_P || (w.second && p.dw_store)) {
+                float lse = 0.f, g = 0.f;
+                int64_t tgt = -1;
+                if (KIND == K_P && r < p.T) {
+                    tgt = target_of(p, r);
+                    lse = __ldg(p.lse + r);
+                    g = tgt < 0 ? 0.f : tgt >= p.vocab ? NAN : __ldg(p.dloss + r) * p.scale;
+                    tgt -= p.v0;
+                }
+                const bool live = KIND != K_P || g != 0.f;
+                constexpr int NP = KIND == K_P && F32 ? 3 : 1;
+                const int r0 = w.m * BM + (int)rank * HALF;
+                const int out_cols = KIND == K_P ? p.V : p.W, out_rows = KIND == K_P ? p.T : p.V;
+                for (int j = 0; j < BN; j += 64) {
+                    float x[64];
+                    tc::ld32(d + j, x);
+                    tc::ld32(d + j + 32, x + 32);
+                    if (KIND == K_P) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], p.scale, -lse) * kLog2e) : 0.f;
+                        const int64_t o = tgt - (c0 + j);
+                        if (live && o >= 0 && o < 64) {
+                            const unsigned long long bit = 1ull << (int)o;
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) x[i] -= bit & (1ull << i) ? g : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        unsigned char* to = staged + (((j >> 6) * NP + q) & 1) * OUTB;
+                        if (warp == 4 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        tc::bar_sync(1, 128);
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) {
+                            uint4 o4;
+                            uint32_t* o32 = reinterpret_cast<uint32_t*>(&o4);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int e = h * 8 + i * 2;
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(x[e], x[e + 1]);
+                                o32[i] = *reinterpret_cast<const uint32_t*>(&b);
+                                if (NP > 1) {
+                                    x[e] -= __uint_as_float(o32[i] << 16);
+                                    x[e + 1] -= __uint_as_float(o32[i] & 0xffff0000u);
+                                }
+                            }
+                            *reinterpret_cast<uint4*>(to + 2 * tc::sw128_chunk(HALF, row, h)) = o4;
+                        }
+                        tc::fence_async_smem();
+                        tc::bar_sync(1, 128);
+                        if (warp == 4 && lane == 0) {
+                            // (a group is closed with or without a store: the wait above counts them)
+                            if (c0 + j < out_cols && r0 < out_rows) store_box(&maps.out, c0 + j, r0, q, tc::smem_addr(to));
+                            tc::bulk_commit();
+                        }
+                    }
+                }
+            } else {
+                // fp32 results, or bf16 ones that TMA cannot store: rows of this thread
+                const int rows = w.second ? p.V : p.T;
+                for (int j = 0; j < BN; j += 32) {
+                    float x[32];
+                    tc::ld32(d + j, x);
+                    const int col = c0 + j;
+                    if (r >= rows || col >= p.W) continue;
+                    if (w.k1 <= w.k0) {  // a split without steps: nothing was added up
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    }
+                    if (!w.second) {
+                        float* q = p.acc + ((int64_t)w.split * p.T + r) * p.ldacc + col;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (col + i < p.ldacc) put8(q + i, x + i, p.add != 0);
+                    } else if (p.dw_f32) {
+                        float* q = static_cast<float*>(p.dw) + r * p.lddw + col;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i < p.W) q[i] = x[i];
+                    } else {
+                        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.dw) + r * p.lddw + col;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col + i < p.W) q[i] = __float2bfloat16_rn(x[i]);
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(in_leader(tc::smem_addr(&c.free_[buf])));
+        }
+        if (warp == 4 && lane == 0) tc::bulk_wait();
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc::fence_after();
+    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ---- small kernels -----------------------------------------------------------
+
+// [rows][W] -> [parts][rows][ld]: bf16 as it is, fp32 in three bf16 parts that add up to
+// it; rows without a target are zero (0 times an infinity there would reach every weight's
+// gradient).  Columns of W and beyond are not written: no box reads them.
+template <typename E>
+__global__ void __launch_bounds__(256) pack_kernel(const E* __restrict__ x, int64_t ldx, int64_t rows, int W, int ld,
+                                                   const void* targets, int wide, __nv_bfloat16* __restrict__ out) {
+    const int nv = (W + 7) / 8;
+    const int64_t n = rows * nv;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / nv;
+        const int c = (int)(i - r * nv) * 8;
+        bool real = true;
+        if (targets)
+            real = (wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r)) >= 0;
+        const E* s = x + r * ldx + c;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = real && c + j < W ? Elem<E>::load(s + j) : 0.f;
+#pragma unroll
+        for (int q = 0; q < (sizeof(E) == 4 ? 3 : 1); ++q) {
+            store8(out + (q * rows + r) * ld + c, f);
+            if (sizeof(E) == 4) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float h = __bfloat162float(__float2bfloat16_rn(f[j]));
+                    f[j] = isfinite(h) ? f[j] - h : 0.f;
+                }
+            }
+        }
+    }
+}
+
+// lse and loss of 32 rows from the tiles' maxima and sums: eight threads a row
+__global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict__ stat, int nt, int T, int V,
+                                                       const float* __restrict__ at, const void* targets, int wide,
+                                                       float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ float2 part[8][32];
+    const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int r = blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.f;
+    if (r < T) {
+#pragma unroll 4
+        for (int n = g; n < nt; n += 8) {
+            const float2 v = __ldg(stat + (int64_t)n * T + r);
+            const float t = fmaxf(m, v.x), ref = t == -INFINITY ? 0.f : t;
+            s = s * exp2_fast((m - ref) * kLog2e) + v.y * exp2_fast((v.x - ref) * kLog2e);
+            m = t;
+        }
+    }
+    part[g][lane] = make_float2(m, s);
+    __syncthreads();
+    if (g || r >= T) return;
+    for (int i = 1; i < 8; ++i) {
+        const float2 v = part[i][lane];
+        const float t = fmaxf(m, v.x), ref = t == -INFINITY ? 0.f : t;
+        s = s * exp2_fast((m - ref) * kLog2e) + v.y * exp2_fast((v.x - ref) * kLog2e);
+        m = t;
+    }
+    const int64_t tgt =
+        wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
+    const float z = m + logf(s);
+    lse[r] = z;
+    loss[r] = tgt < 0 ? 0.f : tgt >= V ? NAN : z - __ldg(at + r);
+}
+
+// dh from the splits' sums
+template <typename E>
+__global__ void __launch_bounds__(256) dh_kernel(const float* __restrict__ acc, int splits, int64_t T, int W, int ldacc,
+                                                 E* __restrict__ dh, int64_t lddh) {
+    const int64_t n = T * W;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / W;
+        const int c = (int)(i - r * W);
+        float f = 0.f;
+        for (int s = 0; s < splits; ++s) f += acc[(s * T + r) * ldacc + c];
+        dh[r * lddh + c] = Elem<E>::from_f(f);
+    }
+}
+
+// ---- host --------------------------------------------------------------------
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int round8(int W) { return (W + 7) / 8 * 8; }
+
+// An operand that the tensor maps read as it is: bf16 with rows of whole 16-byte pieces
+bool direct(gdn_dtype dt, int W) { return dt == GDN_BF16 && W % 8 == 0; }
+
+// Columns of a piece of the vocabulary: P of up to half a gigabyte (more only where 1024
+// columns take more), whole tiles
+constexpr size_t kPieceBytes = size_t(512) << 20;
+int piece_cols(int T, int V, gdn_dtype dt) {
+    int64_t c = (int64_t)(kPieceBytes / ((size_t)(dt == GDN_F32 ? 6 : 2) * (size_t)T)) / BN * BN;
+    if (c < 1024) c = 1024;
+    const int64_t all = div_up(V, BN) * BN;
+    return (int)(c < all ? c : all);
+}
+// K of dh's product cut so that its tiles, with half as many pairs of CTAs to spare, fill
+// the GPU; splits of 16 steps at least
+int dh_splits(int T, int W, int cols) {
+    const int64_t tiles = div_up(T, BM) * div_up(W, BN), kb = div_up(cols, BK);
+    int64_t s = div_up(device_sm_count() / 2, tiles);
+    if (s > kb / 16) s = kb / 16;
+    if (s > 16) s = 16;
+    return (int)(s < 1 ? 1 : s);
+}
+
+struct Plan {
+    size_t h, w, stat, at, p, acc, total;
+    int piece, splits, ldacc;
+};
+Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
+    Plan l{};
+    size_t o = 0;
+    const int parts = dt == GDN_F32 ? 3 : 1;
+    const int64_t ld = round8(W);
+    const int64_t t = T > 0 ? T : 1;
+    if (grad || !direct(dt, W)) {
+        l.h = o;
+        o += up256((size_t)parts * t * ld * 2);
+    }
+    if (!direct(dt, W)) {
+        l.w = o;
+        o += up256((size_t)parts * V * ld * 2);
+    }
+    if (!grad) {
+        l.stat = o;
+        o += up256(sizeof(float2) * (size_t)div_up(V, BN) * t);
+        l.at = o;
+        o += up256(sizeof(float) * t);
+    } else {
+        l.piece = piece_cols((int)t, V, dt);
+        l.splits = dh_splits((int)t, W, l.piece);
+        l.ldacc = (int)ld;
+        l.p = o;
+        o += up256((size_t)parts * t * l.piece * 2);
+        l.acc = o;
+        o += up256(sizeof(float) * (size_t)l.splits * t * ld);
+    }
+    l.total = o > 0 ? o : 256;
+    return l;
+}
+
+// Pairs of CTAs that run at the same time, a CTA an SM; asked once per device
+int pair_count(const void* fn) {
+    constexpr int kMaxDev = 64;
+    static int known[kMaxDev] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return device_sm_count() / 2;
+    if (known[dev]) return known[dev];
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(device_sm_count() / 2 * 2);
+    cfg.blockDim = dim3(GT);
+    cfg.dynamicSmemBytes = kSmem;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = device_sm_count() / 2;
+    }
+    known[dev] = n;
+    return n;
+}
+
+template <int KIND, bool F32>
+gdn_status launch_gemm_t(const GemmParams& p, const Maps& m, cudaStream_t s) {
+    const void* fn = (const void*)vocab_gemm_kernel<KIND, F32>;
+    gdn_status st = set_smem_attr(fn, kSmem);
+    if (st != GDN_OK) return st;
+    const int64_t n = (int64_t)p.mt * p.nt * (KIND == K_GRAD ? p.splits : 1) + (int64_t)p.mt2 * p.nt2;
+    if (n > 0x7fffffff / 2) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)n);
+    const int pairs = pair_count(fn);
+    vocab_gemm_kernel<KIND, F32><<<2 * (unsigned)(n < pairs ? n : pairs), GT, kSmem, s>>>(p, m);
+    return check_launch("vocab_gemm_kernel");
+}
+template <int KIND>
+gdn_status launch_gemm(const GemmParams& p, const Maps& m, cudaStream_t s) {
+    return p.products > 1 ? launch_gemm_t<KIND, true>(p, m, s) : launch_gemm_t<KIND, false>(p, m, s);
+}
+
+unsigned grid_for(int64_t n) {
+    const int64_t b = div_up(n, 256), most = (int64_t)device_sm_count() * 16;
+    return (unsigned)(b < 1 ? 1 : b < most ? b : most);
+}
+
+gdn_status pack(const void* x, int64_t ldx, gdn_dtype dt, int64_t rows, int W, const void* targets, int wide, void* out,
+                cudaStream_t s) {
+    const int ld = round8(W);
+    const unsigned g = grid_for(rows * (ld / 8));
+    if (dt == GDN_F32)
+        pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(x), ldx, rows, W, ld, targets, wide,
+                                             static_cast<__nv_bfloat16*>(out));
+    else
+        pack_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, W, ld, targets,
+                                                     wide, static_cast<__nv_bfloat16*>(out));
+    return check_launch("pack_kernel");
+}
+
+// What a product reads: the array itself, or its packed copy
+struct Operand {
+    const void* base;
+    int64_t ld;
+};
+
+// Rows of tiles that are walked together: their rows of h stay in L2 (32 MB of 129)
+int group_rows(int mt, int W, int parts) {
+    int64_t g = (int64_t(32) << 20) / ((int64_t)BM * W * 2 * parts);
+    if (g > 16) g = 16;
+    if (g < 1) g = 1;
+    return (int)(g < mt ? g : mt);
+}
+
+gdn_status check_loss(gdn_dtype dtype, int32_t index_bits, int T, int V, int W, const void* h, int64_t ldh,
+                      const void* w, int64_t ldw, const void* targets, float scale) {
+    if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "unknown dtype %d", (int)dtype);
+    if (index_bits != 32 && index_bits != 64) return fail(GDN_ERR_DTYPE, "targets of %d bits", index_bits);
+    if (T < 0 || V < 1 || W < 1) return fail(GDN_ERR_INVALID_ARG, "T=%d vocab=%d width=%d", T, V, W);
+    if (T > (1 << 28) || V > (1 << 28) || W > (1 << 20))
+        return fail(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d or vocab=%d above 2^28, or width=%d above 2^20", T, V, W);
+    if (!w || (T > 0 && (!h || !targets))) return fail(GDN_ERR_INVALID_ARG, "h, w or targets is NULL");
+    if ((T > 0 && ldh < W) || ldw < W) return fail(GDN_ERR_INVALID_ARG, "row strides of h and w must be >= width=%d", W);
+    if (direct(dtype, W) && ((T > 0 && ((reinterpret_cast<uintptr_t>(h) & 15u) || ldh % 8)) ||
+                             (reinterpret_cast<uintptr_t>(w) & 15u) || ldw % 8))
+        return fail(GDN_ERR_INVALID_ARG, "h and w must be 16-byte aligned with row strides that are multiples of 8");
+    if (ldh > (int64_t(1) << 36) || ldw > (int64_t(1) << 36)) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "row strides");
+    if (!(scale - scale == 0.f)) return fail(GDN_ERR_INVALID_ARG, "scale is not finite");
+    return GDN_OK;
+}
+gdn_status check_ws(const void* ws, size_t have, size_t need) {
+    if (!ws || have < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes < required %zu", ws ? have : 0, need);
+    if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    return GDN_OK;
+}
+bool loss_sizes_ok(int T, int V, int W, gdn_dtype dt) {
+    return T >= 0 && V >= 1 && W >= 1 && T <= (1 << 28) && V <= (1 << 28) && W <= (1 << 20) &&
+           (dt == GDN_F32 || dt == GDN_BF16);
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+size_t gdn_vocab_loss_fwd_workspace_size(int32_t T, int32_t vocab, int32_t width, gdn_dtype dtype) {
+    return loss_sizes_ok(T, vocab, width, dtype) ? plan(T, vocab, width, dtype, false).total : 0;
+}
+size_t gdn_vocab_loss_bwd_workspace_size(int32_t T, int32_t vocab, int32_t width, gdn_dtype dtype) {
+    return loss_sizes_ok(T, vocab, width, dtype) ? plan(T, vocab, width, dtype, true).total : 0;
+}
+
+gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw, gdn_dtype dtype,
+                              const void* targets, int32_t index_bits, int32_t T, int32_t vocab, int32_t width,
+                              float scale, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    gdn_status st = check_loss(dtype, index_bits, T, vocab, width, h, ldh, w, ldw, targets, scale);
+    if (st != GDN_OK) return st;
+    const Plan l = plan(T, vocab, width, dtype, false);
+    if ((st = check_ws(workspace, workspace_bytes, l.total)) != GDN_OK) return st;
+    if (T == 0) return GDN_OK;
+    if (!loss || !lse) return fail(GDN_ERR_INVALID_ARG, "loss or lse is NULL");
+    cudaStream_t s = (cudaStream_t)stream;
+    char* ws = static_cast<char*>(workspace);
+    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 3 : 1;
+    Operand H{h, ldh}, Wt{w, ldw};
+    if (!direct(dtype, width)) {
+        H = {ws + l.h, round8(width)};
+        Wt = {ws + l.w, round8(width)};
+        if ((st = pack(h, ldh, dtype, T, width, nullptr, 0, ws + l.h, s)) != GDN_OK) return st;
+        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, ws + l.w, s)) != GDN_OK) return st;
+    }
+    Maps m{};
+    if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
+    if ((st = make_map3(&m.b, Wt.base, Wt.ld, width, vocab, parts, HALF)) != GDN_OK) return st;
+    GemmParams p{};
+    p.mt = (int)div_up(T, BM);
+    p.nt = (int)div_up(vocab, BN);
+    p.group = group_rows(p.mt, width, parts);
+    p.kb = (int)div_up(width, BK);
+    p.products = parts == 3 ? 6 : 1;
+    p.T = T; p.V = vocab; p.W = width; p.scale = scale;
+    p.targets = targets; p.wide = wide;
+    p.stat = reinterpret_cast<float2*>(ws + l.stat);
+    p.at = reinterpret_cast<float*>(ws + l.at);
+    if ((st = launch_gemm<K_LSE>(p, m, s)) != GDN_OK) return st;
+    lse_join_kernel<<<(unsigned)div_up(T, 32), 256, 0, s>>>(p.stat, p.nt, T, vocab, p.at, targets, wide, loss, lse);
+    return check_launch("lse_join_kernel");
+}
+
+gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, const void* w, int64_t ldw,
+                              gdn_dtype dtype, const void* targets, int32_t index_bits, const float* lse, int32_t T,
+                              int32_t vocab, int32_t width, float scale, void* dh, int64_t lddh, void* dw, int64_t lddw,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status st = check_loss(dtype, index_bits, T, vocab, width, h, ldh, w, ldw, targets, scale);
+    if (st != GDN_OK) return st;
+    const Plan l = plan(T, vocab, width, dtype, true);
+    if ((st = check_ws(workspace, workspace_bytes, l.total)) != GDN_OK) return st;
+    if (!dw || lddw < width) return fail(GDN_ERR_INVALID_ARG, "dw is NULL or its row stride < width=%d", width);
+    cudaStream_t s = (cudaStream_t)stream;
+    const size_t e = dtype == GDN_F32 ? 4 : 2;
+    if (T == 0) {
+        if (cudaMemset2DAsync(dw, e * lddw, 0, e * width, vocab, s) != cudaSuccess) return check_launch("memset");
+        return GDN_OK;
+    }
+    if (!dloss || !lse || !dh || lddh < width)
+        return fail(GDN_ERR_INVALID_ARG, "dloss, lse or dh is NULL, or dh's row stride < width=%d", width);
+    char* ws = static_cast<char*>(workspace);
+    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 3 : 1;
+    const int ldp = round8(width);
+    if ((st = pack(h, ldh, dtype, T, width, targets, wide, ws + l.h, s)) != GDN_OK) return st;
+    Operand H{ws + l.h, ldp}, Wt{w, ldw};
+    if (!direct(dtype, width)) {
+        Wt = {ws + l.w, ldp};
+        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, ws + l.w, s)) != GDN_OK) return st;
+    }
+    const bool store = dtype == GDN_BF16 && (reinterpret_cast<uintptr_t>(dw) & 15u) == 0 && lddw % 8 == 0;
+    GemmParams p{};
+    p.mt = (int)div_up(T, BM);
+    p.group = group_rows(p.mt, width, parts);
+    p.products = parts == 3 ? 6 : 1;
+    p.T = T; p.W = width; p.vocab = vocab; p.scale = scale;
+    p.targets = targets; p.wide = wide; p.lse = lse; p.dloss = dloss;
+    for (int v0 = 0; v0 < vocab; v0 += l.piece) {
+        const int cols = vocab - v0 < l.piece ? vocab - v0 : l.piece;
+        // the piece's rows of w, whose parts lie a whole vocabulary apart
+        Maps m{};
+        const char* wp = static_cast<const char*>(Wt.base) + 2 * (int64_t)v0 * Wt.ld;
+        const void* P = ws + l.p;
+        p.v0 = v0;
+        p.V = cols;
+        // the piece's P
+        if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
+        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, HALF)) != GDN_OK) return st;
+        if ((st = make_map3(&m.out, P, l.piece, cols, T, parts, HALF)) != GDN_OK) return st;
+        p.nt = (int)div_up(cols, BN);
+        p.kb = (int)div_up(width, BK);
+        p.splits = 1;
+        p.mt2 = p.nt2 = 0;
+        if ((st = launch_gemm<K_P>(p, m, s)) != GDN_OK) return st;
+        // both gradients' products
+        if ((st = make_map3(&m.a, P, l.piece, cols, T, parts, HALF)) != GDN_OK) return st;
+        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, 64)) != GDN_OK) return st;
+        if ((st = make_map3(&m.a2, P, l.piece, cols, T, parts, 64)) != GDN_OK) return st;
+        if ((st = make_map3(&m.b2, H.base, H.ld, width, T, parts, 64)) != GDN_OK) return st;
+        char* dwp = static_cast<char*>(dw) + e * (int64_t)v0 * lddw;
+        if (store && (st = make_map3(&m.out, dwp, lddw, width, cols, 1, HALF)) != GDN_OK) return st;
+        p.nt = (int)div_up(width, BN);
+        p.kb = (int)div_up(cols, BK);
+        p.splits = l.splits;
+        p.kper = (int)div_up(p.kb, p.splits);
+        p.mt2 = (int)div_up(cols, BM);
+        p.nt2 = p.nt;
+        p.kb2 = (int)div_up(T, BK);
+        p.acc = reinterpret_cast<float*>(ws + l.acc);
+        p.ldacc = l.ldacc;
+        p.add = v0 > 0;
+        p.dw = dwp; p.lddw = lddw; p.dw_f32 = dtype == GDN_F32; p.dw_store = store;
+        if ((st = launch_gemm<K_GRAD>(p, m, s)) != GDN_OK) return st;
+    }
+    const unsigned g = grid_for((int64_t)T * width);
+    if (dtype == GDN_F32)
+        dh_kernel<float><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, static_cast<float*>(dh), lddh);
+    else
+        dh_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, static_cast<__nv_bfloat16*>(dh),
+                                                   lddh);
+    return check_launch("dh_kernel");
+}
+
+}  // extern "C"
