@@ -19,7 +19,7 @@
 //
 // The product kernel: a pair of CTAs (cta_group::2) forms a 256 x 256 tile, 128 rows of
 // each operand a CTA, from a ring of six stages of 64 along K by TMA; accumulators in tensor
-// memory, two of them, so that four warps' epilogue runs beside the next tile.  One
+// memory, two of them, so that the epilogue's sixteen warps run beside the next tile.  One
 // CTA an SM walks tiles by its number.
 #include <cuda.h>
 
@@ -53,17 +53,18 @@ EncodeFn encode_fn() {
 }
 
 // [parts][rows][cols] bf16 with row stride ld, parts `apart` rows from each other, boxes of
-// 64 columns and box_rows rows, 128-byte swizzle; what lies outside reads as zero and is
-// not written
+// 64 (or 32) columns and box_rows rows, swizzled over a box's row; what lies outside reads as
+// zero and is not written
 gdn_status make_map_rows(CUtensorMap* m, const void* base, int64_t ld, int64_t cols, int64_t rows, int64_t apart,
-                         int parts, int box_rows) {
+                         int parts, int box_rows, int box_cols = 64) {
     EncodeFn fn = encode_fn();
     if (!fn) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
     const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)apart};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     return GDN_OK;
@@ -150,8 +151,10 @@ constexpr int BM = 256, BN = 256, BK = 64;      // a pair's tile
 constexpr int HALF = 128;                       // rows of an operand a CTA
 constexpr int STAGES = 6;
 constexpr int OPB = HALF * BK * 2;              // bytes of one operand of a stage
-constexpr int GT = 256;                         // threads: producer, products, allocation, (idle), 4 x epilogue
-constexpr int OUTB = HALF * 64 * 2;             // bytes of a staged 64-column piece of a result
+constexpr int GT = 576;                         // threads: a warp of loads, one of products, 16 of epilogue
+constexpr int EW = 64;                          // columns of an epilogue warp: a quarter of the tile's
+constexpr int SC = 32;                          // columns of a staged piece of a result
+constexpr int OUTB = HALF * SC * 2;             // its bytes; each quarter has one
 
 enum Kind { K_LSE = 0, K_P = 1, K_GRAD = 2 };
 
@@ -160,7 +163,8 @@ struct Ctl {
     uint32_t tmem;
     int abort;
 };
-constexpr size_t kSmem = 1024 + (size_t)STAGES * 2 * OPB + 2 * OUTB + sizeof(Ctl);
+constexpr size_t kSmem = 1024 + (size_t)STAGES * 2 * OPB + 4 * OUTB + sizeof(Ctl);
+static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct Maps {
     CUtensorMap a, b;    // logits: h, w.  Gradients of h: P, w
@@ -173,7 +177,7 @@ struct GemmParams {
     int kb;               // K steps
     int splits, kper;     // gradients of h: K cut into splits of kper steps
     int mt2, nt2, kb2;    // gradients of w
-    int products;         // 1, or 6 products of parts
+    int f32;              // operands are three parts of fp32 values
     int T, V, W;          // V: columns of this launch's logits (the piece's, from v0 on)
     int v0, vocab;
     float scale;
@@ -181,8 +185,11 @@ struct GemmParams {
     float2* stat;         // K_LSE: [nt][T] maximum and sum of a tile's row
     float* at;            // K_LSE: [T] the target's logit
     const float* lse; const float* dloss;  // K_P
+    float* lo;            // [T] what P's entry at the target lost when it was rounded
+    const int* only;      // [vocab] the one token with this target; below 0: none or several
+    const __nv_bfloat16* h; int64_t ldh;   // gradients of w: the rows behind `only`
     float* acc; int ldacc; int add;        // gradients of h: [splits][T][ldacc] fp32; add to what is there
-    void* dw; int64_t lddw; int dw_f32, dw_store;  // dw_store: by TMA through `out`
+    void* dw; int64_t lddw; int dw_store;  // dw_store: by TMA through `out`
 };
 
 __device__ __forceinline__ int64_t target_of(const GemmParams& p, int t) {
@@ -232,9 +239,28 @@ __device__ __forceinline__ Unit unit(const GemmParams& p, int u) {
     return r;
 }
 
-// part of a and of b of product c: (1,1) (1,2) (2,1) (1,3) (2,2) (3,1)
-__device__ __forceinline__ int part_a(int c) { return (0x210100 >> (4 * c)) & 15; }
-__device__ __forceinline__ int part_b(int c) { return (0x012010 >> (4 * c)) & 15; }
+// part of a and of b of product c: (1,3) (2,2) (3,1) (1,2) (2,1) (1,1)
+__device__ __forceinline__ int part_a(int c) { return (0x010210 >> (4 * c)) & 15; }
+__device__ __forceinline__ int part_b(int c) { return (0x001012 >> (4 * c)) & 15; }
+
+// K steps that are added up in tensor memory; CH = 0: all.  The tensor cores cut their
+// sums towards zero, step after step: 2^-24 of a sum each, always to the same side.
+// Where that counts, chunks are added up in registers, rounded: for logits of bf16 (lse off by
+// 9e-7 of itself at a width of 2048 without, 2e-7 with chunks of eight), and for all of
+// fp32, whose small products come first in a chunk, while the sum is small.
+template <int KIND, bool F32>
+__host__ __device__ constexpr int chunk_steps() {
+        return F32 ? 4 : KIND == K_LSE ? 8 : 0;
+}
+
+// v = x, or x -= g, where column o is i, for every i of a row in registers.  Written out:
+// the compiler makes an array in local memory of a chain of choices.
+__device__ __forceinline__ void take_at(float& v, float x, int o, int i) {
+    asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %2, %3;\n @p mov.f32 %0, %1;\n}\n" : "+f"(v) : "f"(x), "r"(o), "r"(i));
+}
+__device__ __forceinline__ void sub_at(float& x, float g, int o, int i) {
+    asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %2, %3;\n @p sub.f32 %0, %0, %1;\n}\n" : "+f"(x) : "f"(g), "r"(o), "r"(i));
+}
 
 // eight fp32 values of a row, added to what is there or in its place
 __device__ __forceinline__ void put8(float* q, const float* v, bool add) {
@@ -252,11 +278,13 @@ __device__ __forceinline__ void put8(float* q, const float* v, bool add) {
 template <int KIND, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
     vocab_gemm_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
+    constexpr int CH = chunk_steps<KIND, F32>();
+    constexpr int NP = F32 ? 6 : 1;  // products of parts
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
     const uint32_t ring = tc::smem_addr(base);
     unsigned char* staged = base + STAGES * 2 * OPB;
-    Ctl& c = *reinterpret_cast<Ctl*>(staged + 2 * OUTB);
+    Ctl& c = *reinterpret_cast<Ctl*>(staged + 4 * OUTB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -267,11 +295,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&c.done[b], 1);
-            tc::mbar_init(&c.free_[b], 8);  // a warp of the epilogue of either CTA each
+            tc::mbar_init(&c.free_[b], 32);  // a warp of the epilogue of either CTA each
         }
         c.abort = 0;
     }
-    if (warp == 2) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_addr(&c.tmem)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
@@ -281,7 +309,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
     tc::fence_after();
     const uint32_t tmem = c.tmem;
     const int n_units = units<KIND>(p);
-    const int np = F32 ? p.products : 1;
 
     if (warp == 0 && lane == 0) {
         // ---- loads ----
@@ -291,35 +318,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         for (int u = pair; u < n_units && ok; u += pairs) {
             const Unit w = unit<KIND>(p, u);
             const int row_a = w.m * BM + (int)rank * HALF, row_b = w.n * BN + (int)rank * HALF;
-            for (int k = w.k0; k < w.k1 && ok; ++k)
-                for (int q = 0; q < np; ++q) {
-                    if (issued >= STAGES && !wait_for(&c.empty[s], phase ^ 1, &c.abort)) {
-                        ok = false;
-                        break;
+            for (int k0 = w.k0; k0 < w.k1 && ok; k0 += CH ? CH : w.k1 - w.k0) {
+                const int k1 = CH ? min(w.k1, k0 + CH) : w.k1;
+                for (int q = 0; q < NP && ok; ++q)
+                    for (int k = k0; k < k1; ++k) {
+                        if (issued >= STAGES && !wait_for(&c.empty[s], phase ^ 1, &c.abort)) {
+                            ok = false;
+                            break;
+                        }
+                        if (rank == 0) tc::mbar_expect_tx(&c.full[s], 4 * OPB);
+                        const uint32_t bar = in_leader(tc::smem_addr(&c.full[s]));
+                        const uint32_t da = ring + s * 2 * OPB, db = da + OPB;
+                        const int za = F32 ? part_a(q) : 0, zb = F32 ? part_b(q) : 0;
+                        if (KIND != K_GRAD) {
+                            load_box(da, &maps.a, k * BK, row_a, za, bar);
+                            load_box(db, &maps.b, k * BK, row_b, zb, bar);
+                        } else if (!w.second) {  // P [t][v], K = v; w [v][column]
+                            load_box(da, &maps.a, k * BK, row_a, za, bar);
+                            load_box(db, &maps.b, row_b, k * BK, zb, bar);
+                            load_box(db + OPB / 2, &maps.b, row_b + 64, k * BK, zb, bar);
+                        } else {  // P [t][v], K = t; h [t][column]
+                            load_box(da, &maps.a2, row_a, k * BK, za, bar);
+                            load_box(da + OPB / 2, &maps.a2, row_a + 64, k * BK, za, bar);
+                            load_box(db, &maps.b2, row_b, k * BK, zb, bar);
+                            load_box(db + OPB / 2, &maps.b2, row_b + 64, k * BK, zb, bar);
+                        }
+                        ++issued;
+                        if (++s == STAGES) {
+                            s = 0;
+                            phase ^= 1;
+                        }
                     }
-                    if (rank == 0) tc::mbar_expect_tx(&c.full[s], 4 * OPB);
-                    const uint32_t bar = in_leader(tc::smem_addr(&c.full[s]));
-                    const uint32_t da = ring + s * 2 * OPB, db = da + OPB;
-                    const int za = F32 ? part_a(q) : 0, zb = F32 ? part_b(q) : 0;
-                    if (KIND != K_GRAD) {
-                        load_box(da, &maps.a, k * BK, row_a, za, bar);
-                        load_box(db, &maps.b, k * BK, row_b, zb, bar);
-                    } else if (!w.second) {  // P [t][v], K = v; w [v][column]
-                        load_box(da, &maps.a, k * BK, row_a, za, bar);
-                        load_box(db, &maps.b, row_b, k * BK, zb, bar);
-                        load_box(db + OPB / 2, &maps.b, row_b + 64, k * BK, zb, bar);
-                    } else {  // P [t][v], K = t; h [t][column]
-                        load_box(da, &maps.a2, row_a, k * BK, za, bar);
-                        load_box(da + OPB / 2, &maps.a2, row_a + 64, k * BK, za, bar);
-                        load_box(db, &maps.b2, row_b, k * BK, zb, bar);
-                        load_box(db + OPB / 2, &maps.b2, row_b + 64, k * BK, zb, bar);
-                    }
-                    ++issued;
-                    if (++s == STAGES) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                }
+            }
         }
         // every stage's products are done, and with them the loads and the arrivals here
         if (ok) {
@@ -345,86 +375,132 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         // ---- products ----
         int s = 0, phase = 0, it = 0;
         bool ok = true;
-        for (int u = pair; u < n_units && ok; u += pairs, ++it) {
+        for (int u = pair; u < n_units && ok; u += pairs) {
             const Unit w = unit<KIND>(p, u);
-            const int buf = it & 1;
-            if (it >= 2 && !wait_for(&c.free_[buf], ((it >> 1) & 1) ^ 1, &c.abort)) break;
-            tc::fence_after();
             const bool a_mn = KIND == K_GRAD && w.second, b_mn = KIND == K_GRAD;
             const uint32_t id = tc::idesc_bf16(BM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u);
-            const uint32_t d = tmem + (uint32_t)buf * BN;
-            uint32_t acc = 0;
-            const int steps = (w.k1 - w.k0) * np;
-            for (int k = 0; k < steps; ++k) {
-                if (!wait_for(&c.full[s], phase, &c.abort)) {
+            int k0 = w.k0;
+            do {  // (a unit without steps has one chunk without steps)
+                const int k1 = CH ? min(w.k1, k0 + CH) : w.k1;
+                const int buf = it & 1;
+                if (it >= 2 && !wait_for(&c.free_[buf], ((it >> 1) & 1) ^ 1, &c.abort)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
-                const uint32_t ra = ring + s * 2 * OPB, rb = ra + OPB;
-                const uint64_t da = tc::desc(ra, a_mn ? OPB / 2 : 16, 1024), db = tc::desc(rb, b_mn ? OPB / 2 : 16, 1024);
-                const uint64_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;
+                const uint32_t d = tmem + (uint32_t)buf * BN;
+                uint32_t acc = 0;
+                const int steps = (k1 - k0) * NP;
+                for (int k = 0; k < steps; ++k) {
+                    if (!wait_for(&c.full[s], phase, &c.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t ra = ring + s * 2 * OPB, rb = ra + OPB;
+                    const uint64_t da = tc::desc(ra, a_mn ? OPB / 2 : 16, 1024);
+                    const uint64_t db = tc::desc(rb, b_mn ? OPB / 2 : 16, 1024);
+                    const uint64_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;
 #pragma unroll
-                for (int j = 0; j < BK / 16; ++j) {
-                    mma_pair(d, da + sa * j, db + sb * j, id, acc);
-                    acc = 1;
+                    for (int j = 0; j < BK / 16; ++j) {
+                        mma_pair(d, da + sa * j, db + sb * j, id, acc);
+                        acc = 1;
+                    }
+                    commit_pair(&c.empty[s]);
+                    if (++s == STAGES) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
-                commit_pair(&c.empty[s]);
-                if (++s == STAGES) {
-                    s = 0;
-                    phase ^= 1;
-                }
-            }
-            if (ok) commit_pair(&c.done[buf]);
+                if (!ok) break;
+                commit_pair(&c.done[buf]);
+                ++it;
+                k0 = k1;
+            } while (k0 < w.k1);
         }
-    } else if (warp >= 4) {
-        // ---- epilogue: this thread's row of the tile ----
-        const int row = (warp - 4) * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)((warp - 4) * 32) << 16);
-        int it = 0;
-        for (int u = pair; u < n_units; u += pairs, ++it) {
+    } else if (warp >= 2) {
+        // ---- epilogue: this thread's row, a quarter of the columns ----
+        const int quad = warp & 3, quarter = (warp - 2) >> 2;  // lanes of tensor memory, columns
+        const int row = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)quarter * EW;
+        const bool lead = quad == 0 && lane == 0;  // of the quarter: its stores
+        unsigned char* const stage = staged + quarter * OUTB;
+        // K_LSE: the other quarters' maximum and sum of a row, of this tile and the last
+        float2* part = reinterpret_cast<float2*>(staged);
+        int it = 0, tile = 0;
+        bool ok = true;
+        for (int u = pair; u < n_units; u += pairs) {
             const Unit w = unit<KIND>(p, u);
-            const int buf = it & 1;
-            // the four warps go on together or not at all
-            if (!tc::bar_and(1, 128, wait_for(&c.done[buf], (it >> 1) & 1, &c.abort))) break;
-            tc::fence_after();
-            const uint32_t d = lanes + (uint32_t)buf * BN;
-            const int r = w.m * BM + (int)rank * HALF + row;
-            const int c0 = w.n * BN;
+            const int r0 = w.m * BM + (int)rank * HALF, r = r0 + row;
+            const int c0 = w.n * BN + quarter * EW;
+            float acc[CH ? EW : 1];
+#pragma unroll
+            for (int i = 0; i < (CH ? EW : 1); ++i) acc[i] = 0.f;
+            int k0 = w.k0;
+            uint32_t d = 0;
+            uint32_t release = 0;
+            do {
+                const int buf = it & 1;
+                // A wait that gives up ends no loop here: the warps' barriers stay matched, and what is
+                // left of the tiles goes by without waiting, with whatever the accumulators hold.
+                if (ok) ok = wait_for(&c.done[buf], (it >> 1) & 1, &c.abort);
+                __syncwarp();
+                tc::fence_after();
+                d = lanes + (uint32_t)buf * BN;
+                release = in_leader(tc::smem_addr(&c.free_[buf]));
+                if constexpr (CH > 0) {
+#pragma unroll
+                    for (int j = 0; j < EW; j += 8) {
+                        float x[8];
+                        tc::ld8(d + j, x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[j + i] += x[i];
+                    }
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(release);
+                }
+                ++it;
+                k0 = CH ? k0 + CH : w.k1;
+            } while (k0 < w.k1);
+
             if (KIND == K_LSE) {
                 const bool real = r < p.T;
                 const int64_t tgt = real ? target_of(p, r) : -1;
+                const int left = p.V - c0;
+                const int64_t o = tgt - c0;
                 float top = -INFINITY, sum = 0.f;
-                for (int j = 0; j < BN; j += 32) {
-                    float x[32];
-                    tc::ld32(d + j, x);
-                    const int left = p.V - (c0 + j);
-                    float m = top;
+                if constexpr (CH > 0) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        x[i] = i < left ? x[i] * p.scale : -INFINITY;
-                        m = fmaxf(m, x[i]);
+                    for (int i = 0; i < EW; ++i) {
+                        acc[i] = i < left ? acc[i] * p.scale : -INFINITY;
+                        top = fmaxf(top, acc[i]);
                     }
-                    const int64_t o = tgt - (c0 + j);
-                    if (o >= 0 && o < 32) {
-                        const unsigned bit = 1u << (int)o;  // (a comparison would index x, in local memory)
+                    if (o >= 0 && o < EW) {
                         float v = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v = bit & (1u << i) ? x[i] : v;
+                        for (int i = 0; i < EW; ++i) take_at(v, acc[i], (int)o, i);
                         p.at[r] = v;
                     }
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    sum *= exp2_fast((top - ref) * kLog2e);
-                    float s0 = 0.f, s1 = 0.f;
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        s0 += exp2_fast((x[i] - ref) * kLog2e);
-                        s1 += exp2_fast((x[i + 1] - ref) * kLog2e);
-                    }
-                    sum += s0 + s1;
-                    top = m;
+                    for (int i = 0; i < EW; ++i) s4[i & 3] += exp2_fast((acc[i] - ref) * kLog2e);
+                    sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 }
-                if (real) p.stat[(int64_t)w.n * p.T + r] = make_float2(top, sum);
+                part = reinterpret_cast<float2*>(staged) + (tile++ & 1) * 3 * HALF;
+                if (quarter) part[(quarter - 1) * HALF + row] = make_float2(top, sum);
+                tc::bar_sync(1, 512);
+                if (!quarter && real) {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const float2 v = part[i * HALF + row];
+                        const float m = fmaxf(top, v.x), ref = m == -INFINITY ? 0.f : m;
+                        sum = sum * exp2_fast((top - ref) * kLog2e) + v.y * exp2_fast((v.x - ref) * kLog2e);
+                        top = m;
+                    }
+                    p.stat[(int64_t)w.n * p.T + r] = make_float2(top, sum);
+                }
             } else if (KIND == K_P || (w.second && p.dw_store)) {
                 float lse = 0.f, g = 0.f;
                 int64_t tgt = -1;
@@ -435,30 +511,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     tgt -= p.v0;
                 }
                 const bool live = KIND != K_P || g != 0.f;
-                constexpr int NP = KIND == K_P && F32 ? 3 : 1;
-                const int r0 = w.m * BM + (int)rank * HALF;
+                float lo = 0.f;
+                const __nv_bfloat16* hrow = nullptr;
+                if (KIND == K_GRAD && r < p.V) {
+                    const int t = __ldg(p.only + p.v0 + r);
+                    if (t >= 0) {
+                        lo = __ldg(p.lo + t);
+                        hrow = p.h + t * p.ldh;
+                    }
+                }
+                constexpr int PARTS = KIND == K_P && F32 ? 3 : 1;
                 const int out_cols = KIND == K_P ? p.V : p.W, out_rows = KIND == K_P ? p.T : p.V;
-                for (int j = 0; j < BN; j += 64) {
-                    float x[64];
-                    tc::ld32(d + j, x);
-                    tc::ld32(d + j + 32, x + 32);
+#pragma unroll
+                for (int j = 0; j < EW; j += SC) {
+                    float x[SC];
+                    if constexpr (CH > 0) {
+#pragma unroll
+                        for (int i = 0; i < SC; ++i) x[i] = acc[j + i];
+                    } else {
+                        tc::ld32(d + j, x);
+                        if (j == EW - SC) {  // the tile is read
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_cluster(release);
+                        }
+                    }
                     if (KIND == K_P) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], p.scale, -lse) * kLog2e) : 0.f;
+                        for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], p.scale, -lse) * kLog2e) : 0.f;
                         const int64_t o = tgt - (c0 + j);
-                        if (live && o >= 0 && o < 64) {
-                            const unsigned long long bit = 1ull << (int)o;
+                        if (o >= 0 && o < SC) {
+                            float at = 0.f;
 #pragma unroll
-                            for (int i = 0; i < 64; ++i) x[i] -= bit & (1ull << i) ? g : 0.f;
+                            for (int i = 0; i < SC; ++i) {
+                                sub_at(x[i], live ? g : 0.f, (int)o, i);
+                                take_at(at, x[i], (int)o, i);
+                            }
+                            if (!F32) p.lo[r] = at - __bfloat162float(__float2bfloat16_rn(at));
+                        }
+                    } else if (hrow) {
+#pragma unroll
+                        for (int i = 0; i < SC; i += 8) {
+                            if (c0 + j + i >= p.W) break;  // (rows of whole 16-byte pieces)
+                            float f[8];
+                            load8(hrow + c0 + j + i, f);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[i + e] = fmaf(lo, f[e], x[i + e]);
                         }
                     }
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) {
-                        unsigned char* to = staged + (((j >> 6) * NP + q) & 1) * OUTB;
-                        if (warp == 4 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        tc::bar_sync(1, 128);
+                    for (int q = 0; q < PARTS; ++q) {
+                        if (lead) tc::bulk_wait_read();
+                        tc::bar_sync(2 + quarter, 128);
 #pragma unroll
-                        for (int h = 0; h < 8; ++h) {
+                        for (int h = 0; h < SC / 8; ++h) {
                             uint4 o4;
                             uint32_t* o32 = reinterpret_cast<uint32_t*>(&o4);
 #pragma unroll
@@ -466,18 +572,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                                 const int e = h * 8 + i * 2;
                                 const __nv_bfloat162 b = __floats2bfloat162_rn(x[e], x[e + 1]);
                                 o32[i] = *reinterpret_cast<const uint32_t*>(&b);
-                                if (NP > 1) {
+                                if (PARTS > 1) {
                                     x[e] -= __uint_as_float(o32[i] << 16);
                                     x[e + 1] -= __uint_as_float(o32[i] & 0xffff0000u);
                                 }
                             }
-                            *reinterpret_cast<uint4*>(to + 2 * tc::sw128_chunk(HALF, row, h)) = o4;
+                            // rows of 64 bytes under the 64-byte swizzle
+                            *reinterpret_cast<uint4*>(stage + row * 64 + ((h ^ ((row >> 1) & 3)) << 4)) = o4;
                         }
                         tc::fence_async_smem();
-                        tc::bar_sync(1, 128);
-                        if (warp == 4 && lane == 0) {
-                            // (a group is closed with or without a store: the wait above counts them)
-                            if (c0 + j < out_cols && r0 < out_rows) store_box(&maps.out, c0 + j, r0, q, tc::smem_addr(to));
+                        tc::bar_sync(2 + quarter, 128);
+                        if (lead && c0 + j < out_cols && r0 < out_rows) {
+                            store_box(&maps.out, c0 + j, r0, q, tc::smem_addr(stage));
                             tc::bulk_commit();
                         }
                     }
@@ -485,11 +591,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
             } else {
                 // fp32 results, or bf16 ones that TMA cannot store: rows of this thread
                 const int rows = w.second ? p.V : p.T;
-                for (int j = 0; j < BN; j += 32) {
+                const bool live = r < rows;
+                float lo = 0.f;
+                const __nv_bfloat16* hrow = nullptr;
+                if (!F32 && w.second && live) {
+                    const int t = __ldg(p.only + p.v0 + r);
+                    if (t >= 0) {
+                        lo = __ldg(p.lo + t);
+                        hrow = p.h + t * p.ldh;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < EW; j += 32) {
                     float x[32];
-                    tc::ld32(d + j, x);
+                    if constexpr (CH > 0) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = acc[j + i];
+                    } else {
+                        tc::ld32(d + j, x);
+                        if (j == EW - 32) {
+                            tc::fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_cluster(release);
+                        }
+                    }
                     const int col = c0 + j;
-                    if (r >= rows || col >= p.W) continue;
+                    if (!live || col >= p.W) continue;
                     if (w.k1 <= w.k0) {  // a split without steps: nothing was added up
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = 0.f;
@@ -499,7 +626,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             if (col + i < p.ldacc) put8(q + i, x + i, p.add != 0);
-                    } else if (p.dw_f32) {
+                    } else if (F32) {
                         float* q = static_cast<float*>(p.dw) + r * p.lddw + col;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -508,22 +635,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                         __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.dw) + r * p.lddw + col;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (col + i < p.W) q[i] = __float2bfloat16_rn(x[i]);
+                            if (col + i < p.W)
+                                q[i] = __float2bfloat16_rn(hrow ? fmaf(lo, __bfloat162float(hrow[col + i]), x[i]) : x[i]);
                     }
                 }
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(in_leader(tc::smem_addr(&c.free_[buf])));
         }
-        if (warp == 4 && lane == 0) tc::bulk_wait();
+        if (lead) tc::bulk_wait();
     }
     __syncwarp();
     tc::fence_before();
     __syncthreads();
     cluster_sync();
     tc::fence_after();
-    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ---- small kernels -----------------------------------------------------------
@@ -533,15 +658,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
 // gradient).  Columns of W and beyond are not written: no box reads them.
 template <typename E>
 __global__ void __launch_bounds__(256) pack_kernel(const E* __restrict__ x, int64_t ldx, int64_t rows, int W, int ld,
-                                                   const void* targets, int wide, __nv_bfloat16* __restrict__ out) {
+                                                   const void* targets, int wide, int vocab, int* only,
+                                                   __nv_bfloat16* __restrict__ out) {
     const int nv = (W + 7) / 8;
     const int64_t n = rows * nv;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / nv;
         const int c = (int)(i - r * nv) * 8;
         bool real = true;
-        if (targets)
-            real = (wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r)) >= 0;
+        if (targets) {
+            const int64_t tgt =
+                wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
+            real = tgt >= 0;
+            // the one token with a target; a second one makes it -2, whatever their order
+            if (only && c == 0 && real && tgt < vocab && atomicCAS(only + tgt, -1, (int)r) != -1) only[tgt] = -2;
+        }
         const E* s = x + r * ldx + c;
         float f[8];
 #pragma unroll
@@ -593,16 +724,22 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict_
     loss[r] = tgt < 0 ? 0.f : tgt >= V ? NAN : z - __ldg(at + r);
 }
 
-// dh from the splits' sums
+// dh from the splits' sums; for bf16 with what P's rounding took at the target (lo)
 template <typename E>
 __global__ void __launch_bounds__(256) dh_kernel(const float* __restrict__ acc, int splits, int64_t T, int W, int ldacc,
-                                                 E* __restrict__ dh, int64_t lddh) {
+                                                 const float* __restrict__ lo, const void* targets, int wide, int vocab,
+                                                 const E* __restrict__ w, int64_t ldw, E* __restrict__ dh, int64_t lddh) {
     const int64_t n = T * W;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / W;
         const int c = (int)(i - r * W);
         float f = 0.f;
         for (int s = 0; s < splits; ++s) f += acc[(s * T + r) * ldacc + c];
+        if (sizeof(E) == 2) {
+            const int64_t tgt =
+                wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
+            if (tgt >= 0 && tgt < vocab) f = fmaf(__ldg(lo + r), Elem<E>::load(w + tgt * ldw + c), f);
+        }
         dh[r * lddh + c] = Elem<E>::from_f(f);
     }
 }
@@ -636,7 +773,7 @@ int dh_splits(int T, int W, int cols) {
 }
 
 struct Plan {
-    size_t h, w, stat, at, p, acc, total;
+    size_t h, w, stat, at, p, acc, lo, only, total;
     int piece, splits, ldacc;
 };
 Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
@@ -666,6 +803,10 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
         o += up256((size_t)parts * t * l.piece * 2);
         l.acc = o;
         o += up256(sizeof(float) * (size_t)l.splits * t * ld);
+        l.lo = o;
+        o += up256(sizeof(float) * t);
+        l.only = o;
+        o += up256(sizeof(int) * (size_t)V);
     }
     l.total = o > 0 ? o : 256;
     return l;
@@ -704,7 +845,7 @@ gdn_status launch_gemm_t(const GemmParams& p, const Maps& m, cudaStream_t s) {
 }
 template <int KIND>
 gdn_status launch_gemm(const GemmParams& p, const Maps& m, cudaStream_t s) {
-    return p.products > 1 ? launch_gemm_t<KIND, true>(p, m, s) : launch_gemm_t<KIND, false>(p, m, s);
+    return p.f32 ? launch_gemm_t<KIND, true>(p, m, s) : launch_gemm_t<KIND, false>(p, m, s);
 }
 
 unsigned grid_for(int64_t n) {
@@ -712,16 +853,16 @@ unsigned grid_for(int64_t n) {
     return (unsigned)(b < 1 ? 1 : b < most ? b : most);
 }
 
-gdn_status pack(const void* x, int64_t ldx, gdn_dtype dt, int64_t rows, int W, const void* targets, int wide, void* out,
-                cudaStream_t s) {
+gdn_status pack(const void* x, int64_t ldx, gdn_dtype dt, int64_t rows, int W, const void* targets, int wide, int vocab, int* only,
+                void* out, cudaStream_t s) {
     const int ld = round8(W);
     const unsigned g = grid_for(rows * (ld / 8));
     if (dt == GDN_F32)
         pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(x), ldx, rows, W, ld, targets, wide,
-                                             static_cast<__nv_bfloat16*>(out));
+                                             vocab, only, static_cast<__nv_bfloat16*>(out));
     else
         pack_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, W, ld, targets,
-                                                     wide, static_cast<__nv_bfloat16*>(out));
+                                                     wide, vocab, only, static_cast<__nv_bfloat16*>(out));
     return check_launch("pack_kernel");
 }
 
@@ -797,8 +938,8 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     if (!direct(dtype, width)) {
         H = {ws + l.h, round8(width)};
         Wt = {ws + l.w, round8(width)};
-        if ((st = pack(h, ldh, dtype, T, width, nullptr, 0, ws + l.h, s)) != GDN_OK) return st;
-        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, ws + l.w, s)) != GDN_OK) return st;
+        if ((st = pack(h, ldh, dtype, T, width, nullptr, 0, 0, nullptr, ws + l.h, s)) != GDN_OK) return st;
+        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, 0, nullptr, ws + l.w, s)) != GDN_OK) return st;
     }
     Maps m{};
     if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
@@ -808,7 +949,7 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     p.nt = (int)div_up(vocab, BN);
     p.group = group_rows(p.mt, width, parts);
     p.kb = (int)div_up(width, BK);
-    p.products = parts == 3 ? 6 : 1;
+    p.f32 = parts == 3;
     p.T = T; p.V = vocab; p.W = width; p.scale = scale;
     p.targets = targets; p.wide = wide;
     p.stat = reinterpret_cast<float2*>(ws + l.stat);
@@ -838,19 +979,27 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
     char* ws = static_cast<char*>(workspace);
     const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 3 : 1;
     const int ldp = round8(width);
-    if ((st = pack(h, ldh, dtype, T, width, targets, wide, ws + l.h, s)) != GDN_OK) return st;
+    int* only = nullptr;
+    if (dtype == GDN_BF16) {
+        only = reinterpret_cast<int*>(ws + l.only);
+        if (cudaMemsetAsync(only, 0xff, sizeof(int) * (size_t)vocab, s) != cudaSuccess) return check_launch("memset");
+    }
+    if ((st = pack(h, ldh, dtype, T, width, targets, wide, vocab, only, ws + l.h, s)) != GDN_OK) return st;
     Operand H{ws + l.h, ldp}, Wt{w, ldw};
     if (!direct(dtype, width)) {
         Wt = {ws + l.w, ldp};
-        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, ws + l.w, s)) != GDN_OK) return st;
+        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, 0, nullptr, ws + l.w, s)) != GDN_OK) return st;
     }
     const bool store = dtype == GDN_BF16 && (reinterpret_cast<uintptr_t>(dw) & 15u) == 0 && lddw % 8 == 0;
     GemmParams p{};
     p.mt = (int)div_up(T, BM);
     p.group = group_rows(p.mt, width, parts);
-    p.products = parts == 3 ? 6 : 1;
+    p.f32 = parts == 3;
     p.T = T; p.W = width; p.vocab = vocab; p.scale = scale;
     p.targets = targets; p.wide = wide; p.lse = lse; p.dloss = dloss;
+    p.lo = reinterpret_cast<float*>(ws + l.lo);
+    p.only = only;
+    p.h = reinterpret_cast<const __nv_bfloat16*>(ws + l.h); p.ldh = ldp;
     for (int v0 = 0; v0 < vocab; v0 += l.piece) {
         const int cols = vocab - v0 < l.piece ? vocab - v0 : l.piece;
         // the piece's rows of w, whose parts lie a whole vocabulary apart
@@ -862,7 +1011,7 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         // the piece's P
         if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
         if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, HALF)) != GDN_OK) return st;
-        if ((st = make_map3(&m.out, P, l.piece, cols, T, parts, HALF)) != GDN_OK) return st;
+        if ((st = make_map_rows(&m.out, P, l.piece, cols, T, T, parts, HALF, SC)) != GDN_OK) return st;
         p.nt = (int)div_up(cols, BN);
         p.kb = (int)div_up(width, BK);
         p.splits = 1;
@@ -874,7 +1023,7 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         if ((st = make_map3(&m.a2, P, l.piece, cols, T, parts, 64)) != GDN_OK) return st;
         if ((st = make_map3(&m.b2, H.base, H.ld, width, T, parts, 64)) != GDN_OK) return st;
         char* dwp = static_cast<char*>(dw) + e * (int64_t)v0 * lddw;
-        if (store && (st = make_map3(&m.out, dwp, lddw, width, cols, 1, HALF)) != GDN_OK) return st;
+        if (store && (st = make_map_rows(&m.out, dwp, lddw, width, cols, cols, 1, HALF, SC)) != GDN_OK) return st;
         p.nt = (int)div_up(width, BN);
         p.kb = (int)div_up(cols, BK);
         p.splits = l.splits;
@@ -885,15 +1034,17 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         p.acc = reinterpret_cast<float*>(ws + l.acc);
         p.ldacc = l.ldacc;
         p.add = v0 > 0;
-        p.dw = dwp; p.lddw = lddw; p.dw_f32 = dtype == GDN_F32; p.dw_store = store;
+        p.dw = dwp; p.lddw = lddw; p.dw_store = store;
         if ((st = launch_gemm<K_GRAD>(p, m, s)) != GDN_OK) return st;
     }
     const unsigned g = grid_for((int64_t)T * width);
     if (dtype == GDN_F32)
-        dh_kernel<float><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, static_cast<float*>(dh), lddh);
+        dh_kernel<float><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, nullptr, targets, wide, vocab,
+                                           static_cast<const float*>(w), ldw, static_cast<float*>(dh), lddh);
     else
-        dh_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, static_cast<__nv_bfloat16*>(dh),
-                                                   lddh);
+        dh_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, p.lo, targets, wide, vocab,
+                                                   static_cast<const __nv_bfloat16*>(w), ldw,
+                                                   static_cast<__nv_bfloat16*>(dh), lddh);
     return check_launch("dh_kernel");
 }
 
