@@ -40,6 +40,7 @@ template <> struct Vec<__nv_bfloat16, 8> {
         for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
         return r;
     }
+    static __device__ __forceinline__ void store(uint4* p, const uint4& r) { __stcs(p, r); }
 };
 template <> struct Vec<float, 4> {
     using raw = float4;
@@ -47,16 +48,19 @@ template <> struct Vec<float, 4> {
         f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
     }
     static __device__ __forceinline__ float4 from_f(const float (&f)[4]) { return make_float4(f[0], f[1], f[2], f[3]); }
+    static __device__ __forceinline__ void store(float4* p, const float4& r) { __stcs(p, r); }
 };
 template <> struct Vec<__nv_bfloat16, 1> {
     using raw = __nv_bfloat16;
     static __device__ __forceinline__ void to_f(raw r, float (&f)[1]) { f[0] = __bfloat162float(r); }
     static __device__ __forceinline__ raw from_f(const float (&f)[1]) { return __float2bfloat16_rn(f[0]); }
+    static __device__ __forceinline__ void store(raw* p, raw r) { *p = r; }
 };
 template <> struct Vec<float, 1> {
     using raw = float;
     static __device__ __forceinline__ void to_f(raw r, float (&f)[1]) { f[0] = r; }
     static __device__ __forceinline__ raw from_f(const float (&f)[1]) { return f[0]; }
+    static __device__ __forceinline__ void store(raw* p, raw r) { __stcs(p, r); }
 };
 
 template <typename I>
@@ -68,46 +72,44 @@ __device__ __forceinline__ int token_of(const I* tokens, int64_t t, int vocab) {
 // ---- lookup ----------------------------------------------------------------
 
 constexpr int FT = 256;  // threads of a block
-constexpr int FU = 4;    // vectors of a thread, loaded together
+constexpr int FU = 8;    // accesses of a lane, loaded together
 
-// vector i of the output: row i / nv, vector i % nv of it
+// A warp copies a piece of 32 FU vectors of one row, pieces of a row next to each other.
+// The results are written past the cache, which is for the table's frequent rows.
 template <typename E, int VEC, typename I>
 __global__ void __launch_bounds__(FT) embed_fwd_kernel(const I* __restrict__ tokens, const E* __restrict__ table,
-                                                       int64_t ldt, int vocab, int64_t T, int nv, float scale,
+                                                       int64_t ldt, int vocab, int T, int nv, int pieces, float scale,
                                                        E* __restrict__ y, int64_t ldy) {
     using V = Vec<E, VEC>;
     using R = typename V::raw;
-    const int64_t n = T * nv, first = (int64_t)blockIdx.x * (FT * FU) + threadIdx.x;
-    R r[FU];
-    int64_t at[FU];
-    bool real[FU];
-#pragma unroll
-    for (int u = 0; u < FU; ++u) {
-        const int64_t i = first + u * FT;
-        real[u] = false;
-        at[u] = -1;
-        if (i < n) {
-            const int64_t t = (n >> 31) ? i / nv : (int64_t)((unsigned)i / (unsigned)nv);
-            const int c = (int)(i - t * nv);
-            at[u] = t * ldy + (int64_t)c * VEC;
-            const int v = token_of(tokens, t, vocab);
-            real[u] = v >= 0;
-            if (real[u]) r[u] = __ldg(reinterpret_cast<const R*>(table + (int64_t)v * ldt + (int64_t)c * VEC));
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < FU; ++u) {
-        if (at[u] < 0) continue;
+    const unsigned at = blockIdx.x * (FT / 32) + (threadIdx.x >> 5);
+    const unsigned t = at / (unsigned)pieces, piece = at - t * (unsigned)pieces;
+    if (t >= (unsigned)T) return;
+    const int first = (int)piece * (32 * FU) + (threadIdx.x & 31);
+    const int v = token_of(tokens, t, vocab);
+    R* const out = reinterpret_cast<R*>(y + t * ldy);
+    if (v < 0) {
         float f[VEC];
-        if (real[u]) {
-            V::to_f(r[u], f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) f[j] *= scale;
-        } else {
+        for (int j = 0; j < VEC; ++j) f[j] = 0.f;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) f[j] = 0.f;
-        }
-        *reinterpret_cast<R*>(y + at[u]) = V::from_f(f);
+        for (int u = 0; u < FU; ++u)
+            if (first + 32 * u < nv) V::store(out + first + 32 * u, V::from_f(f));
+        return;
+    }
+    const R* const row = reinterpret_cast<const R*>(table + v * ldt);
+    R r[FU];
+#pragma unroll
+    for (int u = 0; u < FU; ++u)
+        if (first + 32 * u < nv) r[u] = __ldg(row + first + 32 * u);
+#pragma unroll
+    for (int u = 0; u < FU; ++u) {
+        if (first + 32 * u >= nv) continue;
+        float f[VEC];
+        V::to_f(r[u], f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[j] *= scale;
+        V::store(out + first + 32 * u, V::from_f(f));
     }
 }
 
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(ST) sort_place_kernel(const SortArgs a) {
         for (int j = 0; j < kBins / ST; ++j) {
             const int d = tid * (kBins / ST) + j;
             all[j] = mine[j] = 0;
+#pragma unroll 16
             for (int b = 0; b < (int)gridDim.x; ++b) {
                 const int c = __ldg(a.count + b * kBins + d);
                 all[j] += c;
@@ -238,9 +241,85 @@ __global__ void __launch_bounds__(ST) sort_place_kernel(const SortArgs a) {
     }
 }
 
+// Up to SMALL rows: every pass in one block, keys and positions in shared memory
+constexpr int SMALL_I = 16, SMALL = ST * SMALL_I;
+
+template <typename I>
+__global__ void __launch_bounds__(ST) sort_small_kernel(const SortArgs a, int bits) {
+    __shared__ int wc[SW][kBins];
+    __shared__ int key_s[SMALL];
+    __shared__ unsigned short pos_s[SMALL];
+    __shared__ int warp_sums[SW];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // a warp has the rows [warp per, (warp + 1) per) of the order so far, 32 after 32
+    const int rounds = (a.T + ST - 1) / ST, first = warp * rounds * 32 + lane;
+    for (int i = tid; i < a.T; i += ST) {
+        key_s[i] = sort_key<I>(a, i);
+        pos_s[i] = (unsigned short)i;
+    }
+    __syncthreads();
+    for (int shift = 0; shift < bits; shift += kBits) {
+        int key[SMALL_I], pos[SMALL_I], rank[SMALL_I];
+        for (int i = lane; i < kBins; i += 32) wc[warp][i] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < SMALL_I; ++j) {
+            if (j >= rounds) break;
+            const int i = first + j * 32;
+            key[j] = i < a.T ? key_s[i] : -1;
+            pos[j] = i < a.T ? pos_s[i] : 0;
+            const int d = key[j] < 0 ? kBins : (key[j] >> shift) & (kBins - 1);
+            const unsigned same = __match_any_sync(0xffffffffu, d);
+            const int before = d < kBins ? wc[warp][d] : 0;
+            rank[j] = before + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (d < kBins && lane == __ffs(same) - 1) wc[warp][d] = before + __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        {
+            int total[kBins / ST], sum = 0;
+#pragma unroll
+            for (int j = 0; j < kBins / ST; ++j) {
+                const int d = tid * (kBins / ST) + j;
+                total[j] = 0;
+#pragma unroll
+                for (int w = 0; w < SW; ++w) total[j] += wc[w][d];
+                sum += total[j];
+            }
+            int at = exclusive_sum(sum, warp_sums);
+#pragma unroll
+            for (int j = 0; j < kBins / ST; ++j) {
+                const int d = tid * (kBins / ST) + j;
+                int next = at;
+#pragma unroll
+                for (int w = 0; w < SW; ++w) {
+                    const int c = wc[w][d];
+                    wc[w][d] = next;
+                    next += c;
+                }
+                at += total[j];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < SMALL_I; ++j)
+            if (j < rounds && key[j] >= 0) {
+                const int to = wc[warp][(key[j] >> shift) & (kBins - 1)] + rank[j];
+                key_s[to] = key[j];
+                pos_s[to] = (unsigned short)pos[j];
+            }
+        __syncthreads();
+    }
+    for (int i = tid; i < a.T; i += ST) {
+        a.key_out[i] = key_s[i];
+        a.pos_out[i] = pos_s[i];
+    }
+}
+
 // ---- sums of sorted rows ---------------------------------------------------
 
-constexpr int PT = 128;       // threads of a block, a vector of columns each
+constexpr int PT = 128;       // threads of a block; each has U vectors of a row, PT vectors apart
 constexpr int kMaxPiece = 256;
 
 struct SumArgs {
@@ -254,69 +333,96 @@ struct SumArgs {
     float* part;        // [pieces][2][W]: a piece's first token's part, its last one's
 };
 
-// first i with key[i] >= v
+// first i in [0, T) with key[i] >= v, T if there is none; a whole warp, 32 places a step
 __device__ __forceinline__ int first_at(const int* key, int T, int v) {
-    int lo = 0, hi = T;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(key + mid) < v) lo = mid + 1; else hi = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = T;  // the answer lies in [lo, lo + n]
+    while (n > 0) {
+        const int step = n / 33 + 1;  // n + 1 answers in 33 runs; lane l looks at lo + (l + 1) step - 1
+        const int i = lo + (lane + 1) * step - 1;
+        const bool below = i < lo + n && __ldg(key + i) < v;
+        const int c = __popc(__ballot_sync(0xffffffffu, below));  // the first c places are below v
+        const int end = lo + n;
+        lo += c * step;
+        n = min(step - 1, end - lo);
     }
     return lo;
 }
 
-template <typename O, int VEC>
-__device__ __forceinline__ void put_row(const SumArgs& a, int v, int c, const float (&acc)[VEC]) {
-    O* o = static_cast<O*>(a.out) + (int64_t)v * a.ldo + c;
+// one vector of columns of row v
+template <typename E, int VEC>
+__device__ __forceinline__ void put(const SumArgs& a, int v, int c, const float (&acc)[VEC]) {
+    using V = Vec<E, VEC>;
+    typename V::raw* o = reinterpret_cast<typename V::raw*>(static_cast<E*>(a.out) + v * a.ldo + c);
+    float f[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = acc[j] * a.scale;
+    if (a.into) {
+        float old[VEC];
+        V::to_f(*o, old);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[j] += old[j];
+    }
+    V::store(o, V::from_f(f));
+}
+
+template <int VEC>
+__device__ __forceinline__ void put_part(float* w, const float (&acc)[VEC]) {
     if constexpr (VEC == 1) {
-        float f = acc[0] * a.scale;
-        if (a.into) f += Elem<O>::to_f(*o);
-        *o = Elem<O>::from_f(f);
+        *w = acc[0];
     } else {
-        constexpr int N = 16 / sizeof(O);  // elements of a 16-byte access
 #pragma unroll
-        for (int b = 0; b < VEC; b += N) {
-            using V = Vec<O, N>;
-            float f[N];
+        for (int j = 0; j < VEC; j += 4)
+            *reinterpret_cast<float4*>(w + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void add_part(const float* w, float (&acc)[VEC]) {
+    if constexpr (VEC == 1) {
+        acc[0] += *w;
+    } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) f[j] = acc[b + j] * a.scale;
-            typename V::raw* q = reinterpret_cast<typename V::raw*>(o + b);
-            if (a.into) {
-                float old[N];
-                V::to_f(*q, old);
-#pragma unroll
-                for (int j = 0; j < N; ++j) f[j] += old[j];
-            }
-            *q = V::from_f(f);
+        for (int j = 0; j < VEC; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(w + j);
+            acc[j] += x.x; acc[j + 1] += x.y; acc[j + 2] += x.z; acc[j + 3] += x.w;
         }
     }
 }
 
 // Blocks [0, pieces) walk a piece of the sorted rows each; the others fill the rows of
-// tokens that do not occur, zrows each.  blockIdx.y: PT * VEC columns.
-template <typename E, int VEC>
+// tokens that do not occur, zrows each.  blockIdx.y: PT * U vectors of columns.
+template <typename E, int VEC, int U>
 __global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
     using V = Vec<E, VEC>;
     using R = typename V::raw;
-    const int c = (blockIdx.y * PT + threadIdx.x) * VEC;
-    const bool live = c < a.W;
+    const int c0 = (blockIdx.y * U * PT + threadIdx.x) * VEC;  // vector u: c0 + u PT VEC
     if ((int)blockIdx.x >= a.pieces) {
         __shared__ unsigned hit[kMaxPiece / 32];
+        __shared__ int range[2];
         const int v0 = ((int)blockIdx.x - a.pieces) * a.zrows, v1 = min(a.vocab, v0 + a.zrows);
-        for (int i = threadIdx.x; i < kMaxPiece / 32; i += PT) hit[i] = 0;
+        if (threadIdx.x < kMaxPiece / 32) hit[threadIdx.x] = 0;
+        if (threadIdx.x < 64) {
+            const int i = first_at(a.key, a.T, threadIdx.x < 32 ? v0 : v1);
+            if ((threadIdx.x & 31) == 0) range[threadIdx.x >> 5] = i;
+        }
         __syncthreads();
-        const int lo = first_at(a.key, a.T, v0), hi = first_at(a.key, a.T, v1);
+        const int lo = range[0], hi = range[1];
         // a token's rows lie together: only its first one counts
         for (int i = lo + threadIdx.x; i < hi; i += PT) {
             const int v = __ldg(a.key + i);
             if (i == lo || __ldg(a.key + i - 1) != v) atomicOr(&hit[(v - v0) >> 5], 1u << ((v - v0) & 31));
         }
         __syncthreads();
-        if (!live) return;
         float zero[VEC];
 #pragma unroll
         for (int j = 0; j < VEC; ++j) zero[j] = 0.f;
+#pragma unroll 4
         for (int v = v0; v < v1; ++v)
-            if (!(hit[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)) put_row<E, VEC>(a, v, c, zero);
+            if (!(hit[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + u * PT * VEC < a.W) put<E, VEC>(a, v, c0 + u * PT * VEC, zero);
+            }
         return;
     }
     __shared__ int key[kMaxPiece + 2];  // with the rows on either side
@@ -328,77 +434,98 @@ __global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
         if (i > 0 && i <= n) pos[i - 1] = __ldg(a.pos + r);
     }
     __syncthreads();
-    if (!live) return;
-    const E* dy = static_cast<const E*>(a.dy) + c;
+    if (c0 >= a.W) return;
+    const E* dy = static_cast<const E*>(a.dy) + c0;
     constexpr int AHEAD = 8;
-    R row[AHEAD];
+    R row[AHEAD][U];
+    auto load = [&](int slot, int i) {
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-        if (u < n && key[u + 1] < a.vocab) row[u] = __ldg(reinterpret_cast<const R*>(dy + pos[u] * a.lddy));
-    float acc[VEC];
+        for (int u = 0; u < U; ++u)
+            if (U == 1 || c0 + u * PT * VEC < a.W)
+                row[slot][u] = __ldg(reinterpret_cast<const R*>(dy + pos[i] * a.lddy + u * PT * VEC));
+    };
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+    for (int s = 0; s < AHEAD; ++s)
+        if (s < n && key[s + 1] < a.vocab) load(s, s);
+    float acc[U][VEC];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[u][j] = 0.f;
     bool whole = key[0] != key[1];  // the token began in this piece
     for (int i0 = 0; i0 < n; i0 += AHEAD) {
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            const int i = i0 + u;
+        for (int s = 0; s < AHEAD; ++s) {
+            const int i = i0 + s;
             if (i >= n) break;
             const int v = key[i + 1];
             if (v >= a.vocab) return;  // padded tokens are behind all others
-            float f[VEC];
-            V::to_f(row[u], f);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) acc[j] += f[j];
+            for (int u = 0; u < U; ++u) {
+                float f[VEC];
+                V::to_f(row[s][u], f);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) acc[u][j] += f[j];
+            }
             const int nx = i + AHEAD;
-            if (nx < n && key[nx + 1] < a.vocab) row[u] = __ldg(reinterpret_cast<const R*>(dy + pos[nx] * a.lddy));
-            if (key[i + 2] != v) {
-                if (whole) put_row<E, VEC>(a, v, c, acc);
-                else {
-                    float* w = a.part + (int64_t)blockIdx.x * 2 * a.W + c;
+            if (nx < n && key[nx + 1] < a.vocab) load(s, nx);
+            const bool ends = key[i + 2] != v;
+            if (ends || i == n - 1) {
+                // its sum, or its part in this piece: the first one's, or the last one's that goes on
+                float* const part = a.part + ((int64_t)blockIdx.x * 2 + (ends ? 0 : 1)) * a.W + c0;
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) w[j] = acc[j];
+                for (int u = 0; u < U; ++u) {
+                    if (U == 1 || c0 + u * PT * VEC < a.W) {
+                        if (ends && whole) put<E, VEC>(a, v, c0 + u * PT * VEC, acc[u]);
+                        else put_part<VEC>(part + u * PT * VEC, acc[u]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) acc[u][j] = 0.f;
                 }
                 whole = true;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-            } else if (i == n - 1) {  // goes on in the next piece
-                float* w = a.part + ((int64_t)blockIdx.x * 2 + 1) * a.W + c;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) w[j] = acc[j];
             }
         }
     }
 }
 
 // Block b adds up the token that begins in piece b and goes on in the next ones: the last
-// part of piece b, the last parts of the pieces that it fills, and the first part of the
-// one that it ends in (of which the last part when it fills that too and ends there is
-// written as the first).
+// parts of piece b and of the pieces that it fills, and the first part of the one that it
+// ends in (where it fills that too, it ends there all the same).  JG groups of threads
+// take a run of the parts each; their sums are added in the runs' order.
+constexpr int JG = 4;
+
 template <typename E, int VEC>
-__global__ void __launch_bounds__(PT) embed_join_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(PT * JG) embed_join_kernel(const SumArgs a) {
     const int b = blockIdx.x, last = (b + 1) * a.piece - 1;  // the piece is full: another follows
     const int v = __ldg(a.key + last);
-    if (v >= a.vocab || __ldg(a.key + last + 1) != v) return;                     // does not go on
-    if (b > 0 && __ldg(a.key + b * a.piece - 1) == v) return;                     // began earlier
-    const int c = (blockIdx.y * PT + threadIdx.x) * VEC;
-    if (c >= a.W) return;
+    if (v >= a.vocab || __ldg(a.key + last + 1) != v) return;    // does not go on
+    if (b > 0 && __ldg(a.key + b * a.piece - 1) == v) return;    // began earlier
+    __shared__ float sum[JG - 1][PT][VEC];
+    const int x = threadIdx.x % PT, g = threadIdx.x / PT;
+    const int c = (blockIdx.y * PT + x) * VEC;
     const int end = first_at(a.key, a.T, v + 1);  // behind the token's last row
     const int pe = (end - 1) / a.piece;           // the piece that it ends in
+    const int n = pe - b + 1, per = (n + JG - 1) / JG;  // parts, of a group
     float acc[VEC];
-    const float* w = a.part + ((int64_t)b * 2 + 1) * a.W + c;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] = w[j];
-#pragma unroll 4
-    for (int p = b + 1; p < pe; ++p) {
-        const float* x = a.part + ((int64_t)p * 2 + 1) * a.W + c;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[j] += x[j];
+    for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+    if (c < a.W) {
+        const int i1 = min(n, (g + 1) * per);
+#pragma unroll 8
+        for (int i = g * per; i < i1; ++i)
+            add_part<VEC>(a.part + ((int64_t)(b + i) * 2 + (i < n - 1 ? 1 : 0)) * a.W + c, acc);
     }
-    const float* x = a.part + (int64_t)pe * 2 * a.W + c;
+    if (g) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] += x[j];
-    put_row<E, VEC>(a, v, c, acc);
+        for (int j = 0; j < VEC; ++j) sum[g - 1][x][j] = acc[j];
+    }
+    __syncthreads();
+    if (g || c >= a.W) return;
+#pragma unroll
+    for (int k = 0; k < JG - 1; ++k)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] += sum[k][x][j];
+    put<E, VEC>(a, v, c, acc);
 }
 
 // ---- host ------------------------------------------------------------------
@@ -445,6 +572,13 @@ gdn_status sort_tokens(const void* tokens, int T, int vocab, char* ws, const Lay
     a.tokens = tokens;
     a.T = T;
     a.vocab = vocab;
+    if (T <= SMALL) {
+        a.key_out = reinterpret_cast<int*>(ws + l.key[0]);
+        a.pos_out = reinterpret_cast<int*>(ws + l.pos[0]);
+        which = 0;
+        sort_small_kernel<I><<<1, ST, 0, s>>>(a, bits);
+        return check_launch("sort_small_kernel");
+    }
     const int blocks = sort_blocks(T);
     a.per = (T + blocks - 1) / blocks;
     a.count = reinterpret_cast<int*>(ws + l.count);
@@ -465,15 +599,17 @@ gdn_status sort_tokens(const void* tokens, int T, int vocab, char* ws, const Lay
 
 template <typename E, int VEC>
 gdn_status run_sum(const SumArgs& a, cudaStream_t s) {
-    const unsigned ny = (unsigned)((a.W + PT * VEC - 1) / (PT * VEC));
+    // single elements: eight of a thread, or the blocks would be small
+    constexpr int U = VEC == 1 ? 8 : 1;
+    const unsigned ny = (unsigned)((a.W + PT * VEC * U - 1) / (PT * VEC * U));
     const unsigned zeros = a.into ? 0u : (unsigned)((a.vocab + a.zrows - 1) / a.zrows);
     if ((unsigned)a.pieces + zeros > 0) {
-        embed_sum_kernel<E, VEC><<<dim3(a.pieces + zeros, ny), PT, 0, s>>>(a);
+        embed_sum_kernel<E, VEC, U><<<dim3(a.pieces + zeros, ny), PT, 0, s>>>(a);
         gdn_status st = check_launch("embed_sum_kernel");
         if (st != GDN_OK) return st;
     }
     if (a.pieces > 1) {
-        embed_join_kernel<E, VEC><<<dim3(a.pieces - 1, ny), PT, 0, s>>>(a);
+        embed_join_kernel<E, VEC><<<dim3(a.pieces - 1, (a.W + PT * VEC - 1) / (PT * VEC)), PT * JG, 0, s>>>(a);
         return check_launch("embed_join_kernel");
     }
     return GDN_OK;
@@ -486,11 +622,12 @@ bool al(const void* p, int64_t ld, size_t e) {
 template <typename E, int VEC, typename I>
 gdn_status run_fwd_i(const void* tokens, const void* table, int64_t ldt, int vocab, int T, int W, float scale, void* y,
                      int64_t ldy, cudaStream_t s) {
-    const int64_t n = (int64_t)T * (W / VEC), blocks = (n + FT * FU - 1) / (FT * FU);
-    if (blocks > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows of %d elements", T, W);
-    embed_fwd_kernel<E, VEC, I><<<(unsigned)blocks, FT, 0, s>>>(static_cast<const I*>(tokens),
-                                                                static_cast<const E*>(table), ldt, vocab, T, W / VEC,
-                                                                scale, static_cast<E*>(y), ldy);
+    const int nv = W / VEC, pieces = (nv + 32 * FU - 1) / (32 * FU);
+    const int64_t warps = (int64_t)T * pieces;
+    if (warps > 0xfffffff0ll) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows of %d elements", T, W);
+    embed_fwd_kernel<E, VEC, I><<<(unsigned)((warps + FT / 32 - 1) / (FT / 32)), FT, 0, s>>>(
+        static_cast<const I*>(tokens), static_cast<const E*>(table), ldt, vocab, T, nv, pieces, scale,
+        static_cast<E*>(y), ldy);
     return check_launch("embed_fwd_kernel");
 }
 template <typename E, int VEC>

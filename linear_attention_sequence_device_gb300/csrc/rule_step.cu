@@ -14,9 +14,18 @@
 // sums over rows end in shared memory (two barriers); every warp forms the norms and
 // k.q by itself, which takes no barrier.
 #include "ssm_common.cuh"
+#include "tc_util.cuh"
 
 namespace gdn {
+
+extern __device__ int g_gdn_timeouts;
+gdn_status set_smem_attr(const void* func, size_t bytes);
+
 namespace {
+
+#ifndef RING_FROM
+#define RING_FROM 4
+#endif
 
 struct StepParams {
     const void* q; const void* k; const void* v;  // head h of request b at + b * ld + h * d
@@ -35,8 +44,21 @@ struct StepParams {
     void* o;
 };
 
+// g and beta of a request's head, ready or from the raw projections
+template <typename E>
+__device__ __forceinline__ void gates(const StepParams& p, int b, int hv, float& g, float& beta) {
+    beta = Elem<E>::load(static_cast<const E*>(p.beta) + (int64_t)b * p.ldb + hv);
+    if (p.A_log) {
+        const float x = Elem<E>::load(static_cast<const E*>(p.g) + (int64_t)b * p.ldg + hv) + __ldg(p.dt_bias + hv);
+        g = -expf(__ldg(p.A_log + hv)) * (x > 20.f ? x : log1pf(expf(x)));
+        beta = 1.f / (1.f + expf(-beta));
+    } else {
+        g = __ldg(static_cast<const float*>(p.g) + (int64_t)b * p.ldg + hv);
+    }
+}
+
 template <typename E, int DK, int DV>
-__global__ void __launch_bounds__(DK * DV / 32, 1024 / (DK * DV / 32)) rule_step_kernel(const StepParams p) {
+__global__ void __launch_bounds__(DK * DV / 32) rule_step_kernel(const StepParams p) {
     constexpr int NT = DK * DV / 32, NW = NT / 32;
     constexpr int LPR = DV / 4;      // lanes of a row
     constexpr int RPW = 32 / LPR;    // rows of a warp's one load
@@ -83,14 +105,7 @@ __global__ void __launch_bounds__(DK * DV / 32, 1024 / (DK * DV / 32)) rule_step
         kq = fmaf(a, c, kq);
     }
     float g, beta;
-    if (p.A_log) {
-        const float x = Elem<E>::load(static_cast<const E*>(p.g) + (int64_t)b * p.ldg + hv) + __ldg(p.dt_bias + hv);
-        g = -expf(__ldg(p.A_log + hv)) * (x > 20.f ? x : log1pf(expf(x)));
-        beta = 1.f / (1.f + expf(-Elem<E>::load(static_cast<const E*>(p.beta) + (int64_t)b * p.ldb + hv)));
-    } else {
-        g = __ldg(static_cast<const float*>(p.g) + (int64_t)b * p.ldg + hv);
-        beta = Elem<E>::load(static_cast<const E*>(p.beta) + (int64_t)b * p.ldb + hv);
-    }
+    gates<E>(p, b, hv, g, beta);
     const float decay = expf(g);
 #pragma unroll
     for (int m = 16; m; m >>= 1) {
@@ -168,20 +183,355 @@ __global__ void __launch_bounds__(DK * DV / 32, 1024 / (DK * DV / 32)) rule_step
     }
 }
 
+// ---- many heads: a ring of them in shared memory ------------------------------
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* mbar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     tc::smem_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(tc::smem_addr(mbar))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(tc::smem_addr(src)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+constexpr int RING = 3;
+constexpr uint32_t kPolls = 1u << 26;  // of a wait in the ring
+
+// What a head's rule needs beside its state, formed a stage ahead
+template <int DK, int DV>
+struct alignas(16) Head {
+    float k[DK], q[DK];          // as they come
+    float v[DV];
+    float zw[DV];                // norm_w silu(z)
+    float decay, bk, nk, nq, kq;  // e^g, beta / |k|, 1 / |k|, scale / |q|, k.q
+    int state;                   // has a state to start from
+    int at;                      // the head's number; -1: there is none any more
+};
+template <int DK, int DV>
+struct Ring {
+    alignas(128) float S[RING][DK * DV];
+    Head<DK, DV> head[RING];
+    alignas(16) float part[DK * DV / 1024][2][DV];
+    alignas(16) float sums[2][DV];
+    uint64_t full[RING], done[RING], empty[RING];
+    int bad;
+};
+
+// The heads of a CTA, blockIdx.x + j gridDim.x, without those of padded rows; a warp looks
+// at 32 at a time.
+struct Heads {
+    int base, to, slot;  // of this lane's head
+    unsigned live, padded;
+    __device__ __forceinline__ void look(const StepParams& p, int heads) {
+        const int64_t i = base + (int64_t)(threadIdx.x & 31) * gridDim.x;
+        to = slot = -1;
+        if (i < heads) {
+            const int b = (int)i / p.Hv;
+            to = p.dst ? __ldg(p.dst + b) : b;
+            slot = p.src ? __ldg(p.src + b) : b;
+            if (to >= p.num_slots) to = -1;
+            if (slot >= p.num_slots) slot = -1;
+        }
+        live = __ballot_sync(0xffffffffu, to >= 0);
+        padded = __ballot_sync(0xffffffffu, i < heads && to < 0);
+    }
+    // the next head's number, -1 behind the last; its slots
+    __device__ __forceinline__ int next(const StepParams& p, int heads, int& to_, int& slot_) {
+        while (live == 0) {
+            const int64_t b = base + 32ll * gridDim.x;
+            if (b >= heads) return -1;
+            base = (int)b;
+            look(p, heads);
+        }
+        const int l = __ffs(live) - 1;
+        live &= live - 1;
+        to_ = __shfl_sync(0xffffffffu, to, l);
+        slot_ = __shfl_sync(0xffffffffu, slot, l);
+        return base + l * gridDim.x;
+    }
+};
+
+// One CTA walks heads, which go through a ring in shared memory: a warp loads their states,
+// by bulk copies, RING warps form what else the rule needs (in fp32, with norms and gates;
+// a chain of loads of several heads' time, which is why they are several), NT threads do
+// a head at a time, and a warp sends the states back.
+template <typename E, int DK, int DV>
+__global__ void __launch_bounds__(DK * DV / 32 + 32 * (RING + 2)) rule_ring_kernel(const StepParams p, int heads) {
+    constexpr int NT = DK * DV / 32, NW = NT / 32;
+    constexpr int LPR = DV / 4, RPW = 32 / LPR;
+    constexpr uint32_t BYTES = DK * DV * 4;
+    extern __shared__ unsigned char raw[];
+    Ring<DK, DV>& sm = *reinterpret_cast<Ring<DK, DV>*>(raw + ((128 - (tc::smem_addr(raw) & 127)) & 127));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < RING; ++s) {
+            tc::mbar_init(&sm.full[s], 2);
+            tc::mbar_init(&sm.done[s], NW);
+            tc::mbar_init(&sm.empty[s], 1);
+        }
+        sm.bad = 0;
+    }
+    __syncthreads();
+    if (warp >= NW) {
+        Heads list;
+        list.base = blockIdx.x;
+        list.look(p, heads);
+        int to, slot;
+        if (warp == NW) {
+            // ---- states in ----
+            for (int n = 0;; ++n) {
+                const int i = list.next(p, heads, to, slot), s = n % RING;
+                if (n >= RING && !tc::mbar_wait(&sm.empty[s], (n / RING - 1) & 1, kPolls, &sm.bad)) {
+                    sm.bad = 1;
+                    break;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (i >= 0 && slot >= 0) {
+                        tc::mbar_expect_tx(&sm.full[s], BYTES);
+                        bulk_load(sm.S[s], p.states + ((int64_t)slot * p.Hv + i % p.Hv) * (DK * DV), BYTES, &sm.full[s]);
+                    } else {
+                        tc::mbar_arrive(&sm.full[s]);
+                    }
+                }
+                if (i < 0) break;
+            }
+        } else if (warp <= NW + RING) {
+            // ---- what else the heads of stage s need, read before the stage is free ----
+            const int s = warp - NW - 1;
+            Head<DK, DV>& h = sm.head[s];
+            for (int n = 0;; ++n) {
+                const int i = list.next(p, heads, to, slot);
+                if (n % RING != s) {
+                    if (i < 0) break;
+                    continue;
+                }
+                float qr[DK / 32], kr[DK / 32], vr[DV / 32], zw[DV / 32], g = 0.f, beta = 0.f;
+                float qq = 0.f, kk = 0.f, kq = 0.f;
+                if (i >= 0) {
+                    const int b = i / p.Hv, hv = i % p.Hv, hk = hv / p.group;
+                    const E* q = static_cast<const E*>(p.q) + (int64_t)b * p.ldq + hk * DK;
+                    const E* k = static_cast<const E*>(p.k) + (int64_t)b * p.ldk + hk * DK;
+                    const E* v = static_cast<const E*>(p.v) + (int64_t)b * p.ldv + hv * DV;
+#pragma unroll
+                    for (int j = 0; j < DK / 32; ++j) {
+                        qr[j] = Elem<E>::load(q + lane + 32 * j);
+                        kr[j] = Elem<E>::load(k + lane + 32 * j);
+                    }
+#pragma unroll
+                    for (int j = 0; j < DV / 32; ++j) {
+                        vr[j] = Elem<E>::load(v + lane + 32 * j);
+                        zw[j] = 1.f;
+                        if (p.z) {
+                            const E* z = static_cast<const E*>(p.z) + (int64_t)b * p.ldz + (int64_t)hv * DV;
+                            const float x = Elem<E>::load(z + lane + 32 * j);
+                            zw[j] = Elem<E>::load(static_cast<const E*>(p.norm_w) + lane + 32 * j) * (x / (1.f + expf(-x)));
+                        }
+                    }
+                    gates<E>(p, b, hv, g, beta);
+#pragma unroll
+                    for (int j = 0; j < DK / 32; ++j) {
+                        qq = fmaf(qr[j], qr[j], qq);
+                        kk = fmaf(kr[j], kr[j], kk);
+                        kq = fmaf(qr[j], kr[j], kq);
+                    }
+#pragma unroll
+                    for (int m = 16; m; m >>= 1) {
+                        qq += __shfl_xor_sync(0xffffffffu, qq, m);
+                        kk += __shfl_xor_sync(0xffffffffu, kk, m);
+                        kq += __shfl_xor_sync(0xffffffffu, kq, m);
+                    }
+                }
+                if (n >= RING && !tc::mbar_wait(&sm.empty[s], (n / RING - 1) & 1, kPolls, &sm.bad)) {
+                    sm.bad = 1;
+                    break;
+                }
+                __syncwarp();
+                if (i >= 0) {
+#pragma unroll
+                    for (int j = 0; j < DK / 32; ++j) {
+                        h.q[lane + 32 * j] = qr[j];
+                        h.k[lane + 32 * j] = kr[j];
+                    }
+#pragma unroll
+                    for (int j = 0; j < DV / 32; ++j) {
+                        h.v[lane + 32 * j] = vr[j];
+                        h.zw[lane + 32 * j] = zw[j];
+                    }
+                }
+                if (lane == 0) {
+                    const float nk = p.l2norm ? rsqrtf(kk + 1e-6f) : 1.f;
+                    h.decay = expf(g);
+                    h.nk = nk;
+                    h.bk = beta * nk;
+                    h.nq = p.scale * (p.l2norm ? rsqrtf(qq + 1e-6f) : 1.f);
+                    h.kq = kq;
+                    h.state = slot >= 0;
+                    h.at = i;
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sm.full[s]);
+                if (i < 0) break;
+            }
+        } else {
+            // ---- states out, zeros for padded rows ----
+            for (int n = 0;; ++n) {
+                const int i = list.next(p, heads, to, slot), s = n % RING;
+                if (i < 0) break;
+                if (!tc::mbar_wait(&sm.done[s], (n / RING) & 1, kPolls, &sm.bad)) {
+                    sm.bad = 1;
+                    break;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_store(p.states + ((int64_t)to * p.Hv + i % p.Hv) * (DK * DV), sm.S[s], BYTES);
+                    tc::bulk_commit();
+                    tc::bulk_wait_read();
+                    tc::mbar_arrive(&sm.empty[s]);
+                }
+            }
+            if (sm.bad && lane == 0) {  // a wait ran out: the copies in flight get a millisecond
+                atomicAdd(&g_gdn_timeouts, 1);
+                for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+            }
+            __syncwarp();
+            for (int64_t i0 = blockIdx.x; i0 < heads; i0 += 32ll * gridDim.x) {
+                list.base = (int)i0;
+                list.look(p, heads);
+                for (unsigned m = list.padded; m; m &= m - 1) {
+                    E* const out = static_cast<E*>(p.o) + (i0 + (int64_t)(__ffs(m) - 1) * gridDim.x) * DV;
+#pragma unroll
+                    for (int j = 0; j < DV / 32; ++j) out[lane + 32 * j] = Elem<E>::from_f(0.f);
+                }
+            }
+        }
+        return;
+    }
+    // ---- the heads ----
+    const int row0 = warp * (8 * RPW) + lane / LPR, col = (lane % LPR) * 4;
+    for (int n = 0;; ++n) {
+        const int s = n % RING;
+        if (!tc::bar_and(1, NT, tc::mbar_wait(&sm.full[s], (n / RING) & 1, kPolls, &sm.bad))) {
+            sm.bad = 1;
+            break;
+        }
+        if (sm.head[s].at < 0) break;
+        E* const out = static_cast<E*>(p.o) + (int64_t)sm.head[s].at * DV;
+        const Head<DK, DV>& h = sm.head[s];
+        float* const tile = sm.S[s] + row0 * DV + col;
+        const bool has = h.state != 0;
+        float4 S[8];
+        float sk[4] = {0.f, 0.f, 0.f, 0.f}, sq[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            S[r] = has ? *reinterpret_cast<const float4*>(tile + r * RPW * DV) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const float k = h.k[row0 + r * RPW], q = h.q[row0 + r * RPW];
+            const float t[4] = {S[r].x, S[r].y, S[r].z, S[r].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sk[j] = fmaf(t[j], k, sk[j]);
+                sq[j] = fmaf(t[j], q, sq[j]);
+            }
+        }
+#pragma unroll
+        for (int m = LPR; m < 32; m <<= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sk[j] += __shfl_xor_sync(0xffffffffu, sk[j], m);
+                sq[j] += __shfl_xor_sync(0xffffffffu, sq[j], m);
+            }
+        if (lane < LPR) {
+            *reinterpret_cast<float4*>(&sm.part[warp][0][col]) = make_float4(sk[0], sk[1], sk[2], sk[3]);
+            *reinterpret_cast<float4*>(&sm.part[warp][1][col]) = make_float4(sq[0], sq[1], sq[2], sq[3]);
+        }
+        tc::bar_sync(1, NT);
+        for (int c = tid; c < 2 * DV; c += NT) {
+            float t = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) t += (&sm.part[w][0][0])[c];
+            (&sm.sums[0][0])[c] = t;
+        }
+        tc::bar_sync(1, NT);
+        const float decay = h.decay, dk_ = decay * h.nk, bk = h.bk;
+        float bu[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bu[j] = bk * (h.v[col + j] - dk_ * sm.sums[0][col + j]);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const float k = h.k[row0 + r * RPW];
+            float4 t;
+            t.x = fmaf(k, bu[0], decay * S[r].x);
+            t.y = fmaf(k, bu[1], decay * S[r].y);
+            t.z = fmaf(k, bu[2], decay * S[r].z);
+            t.w = fmaf(k, bu[3], decay * S[r].w);
+            *reinterpret_cast<float4*>(tile + r * RPW * DV) = t;
+        }
+        if (warp == NW - 1) {
+            float o[4], zw[4], ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = h.nq * fmaf(h.kq, bu[j], decay * sm.sums[1][col + j]);
+                zw[j] = h.zw[col + j];
+                ss = fmaf(o[j], o[j], ss);
+            }
+            if (p.z) {
+#pragma unroll
+                for (int m = LPR / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                const float r = 1.f / sqrtf(ss * (1.f / DV) + p.eps);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] *= r * zw[j];
+            }
+            if (lane < LPR) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) out[col + j] = Elem<E>::from_f(o[j]);
+            }
+        }
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sm.done[s]);
+    }
+}
+
+// ---- host ----------------------------------------------------------------------
+
+template <typename E, int DK, int DV>
+gdn_status run_kernel(const StepParams& p, int heads, cudaStream_t s) {
+    constexpr int NT = DK * DV / 32;
+    constexpr size_t smem = sizeof(Ring<DK, DV>) + 128;
+    if (heads >= RING_FROM * device_sm_count()) {
+        const void* fn = (const void*)rule_ring_kernel<E, DK, DV>;
+        gdn_status st = set_smem_attr(fn, smem);
+        if (st != GDN_OK) return st;
+        // CTAs of an SM: by shared memory (a kilobyte of each is the system's) and threads
+        int per = (int)((228 << 10) / (smem + 1024));
+        if (per > 2048 / (NT + 32 * (RING + 2))) per = 2048 / (NT + 32 * (RING + 2));
+        if (per > 16) per = 16;
+        const int most = per * device_sm_count();
+        rule_ring_kernel<E, DK, DV><<<heads < most ? heads : most, NT + 32 * (RING + 2), smem, s>>>(p, heads);
+        return check_launch("rule_ring_kernel");
+    }
+    rule_step_kernel<E, DK, DV><<<heads, NT, 0, s>>>(p);
+    return check_launch("rule_step_kernel");
+}
+
 template <typename E, int DK>
-void run_dv(const StepParams& p, int dv, unsigned blocks, cudaStream_t s) {
-    if (dv == 32) rule_step_kernel<E, DK, 32><<<blocks, DK, 0, s>>>(p);
-    else if (dv == 64) rule_step_kernel<E, DK, 64><<<blocks, DK * 2, 0, s>>>(p);
-    else rule_step_kernel<E, DK, 128><<<blocks, DK * 4, 0, s>>>(p);
+gdn_status run_dv(const StepParams& p, int dv, int heads, cudaStream_t s) {
+    if (dv == 32) return run_kernel<E, DK, 32>(p, heads, s);
+    if (dv == 64) return run_kernel<E, DK, 64>(p, heads, s);
+    return run_kernel<E, DK, 128>(p, heads, s);
 }
 
 template <typename E>
 gdn_status run_step(const StepParams& p, int batch, int dk, int dv, cudaStream_t s) {
-    const unsigned blocks = (unsigned)batch * (unsigned)p.Hv;
-    if (dk == 32) run_dv<E, 32>(p, dv, blocks, s);
-    else if (dk == 64) run_dv<E, 64>(p, dv, blocks, s);
-    else run_dv<E, 128>(p, dv, blocks, s);
-    return check_launch("rule_step_kernel");
+    const int heads = batch * p.Hv;
+    if (dk == 32) return run_dv<E, 32>(p, dv, heads, s);
+    if (dk == 64) return run_dv<E, 64>(p, dv, heads, s);
+    return run_dv<E, 128>(p, dv, heads, s);
 }
 
 bool head_size(int d) { return d == 32 || d == 64 || d == 128; }
