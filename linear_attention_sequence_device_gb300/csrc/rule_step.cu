@@ -23,9 +23,12 @@ gdn_status set_smem_attr(const void* func, size_t bytes);
 
 namespace {
 
-#ifndef RING_FROM
-#define RING_FROM 4
-#endif
+// States of a call from which on the heads go through a ring: it keeps the loads of the
+// next heads on their way, and costs 2.3 us more to start.  In us, blocks of their own
+// against the ring: 32 heads of 128 x 128, 4 requests 5.2, 7.4; 8 10.1, 11.8; 16 (33 MB)
+// 19.6, 19.3; 32 34.0, 30.3; 128 122, 94.5; 128 x 64, 16 requests 9.6, 10.2; 32 (33 MB)
+// 18.2, 16.9; 64 x 64, 8 heads, 128 requests (17 MB) 8.5, 12.8.
+constexpr int64_t kRingBytes = 28 << 20;
 
 struct StepParams {
     const void* q; const void* k; const void* v;  // head h of request b at + b * ld + h * d
@@ -503,7 +506,7 @@ template <typename E, int DK, int DV>
 gdn_status run_kernel(const StepParams& p, int heads, cudaStream_t s) {
     constexpr int NT = DK * DV / 32;
     constexpr size_t smem = sizeof(Ring<DK, DV>) + 128;
-    if (heads >= RING_FROM * device_sm_count()) {
+    if ((int64_t)heads * (DK * DV * 4) >= kRingBytes) {
         const void* fn = (const void*)rule_ring_kernel<E, DK, DV>;
         gdn_status st = set_smem_attr(fn, smem);
         if (st != GDN_OK) return st;

@@ -149,22 +149,33 @@ __device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, volati
 
 constexpr int BM = 256, BN = 256, BK = 64;      // a pair's tile
 constexpr int HALF = 128;                       // rows of an operand a CTA
-constexpr int STAGES = 6;
 constexpr int OPB = HALF * BK * 2;              // bytes of one operand of a stage
 constexpr int GT = 576;                         // threads: a warp of loads, one of products, 16 of epilogue
 constexpr int EW = 64;                          // columns of an epilogue warp: a quarter of the tile's
 constexpr int SC = 32;                          // columns of a staged piece of a result
-constexpr int OUTB = HALF * SC * 2;             // its bytes; each quarter has one
+constexpr int OUTB = HALF * SC * 2;             // its bytes; each quarter of the columns has two
 
 enum Kind { K_LSE = 0, K_P = 1, K_GRAD = 2 };
 
+// Stages of the ring: results leave through shared memory but for the logits' maxima and sums
+template <int KIND>
+__host__ __device__ constexpr int stages() {
+    return KIND == K_LSE ? 6 : 5;
+}
+template <int KIND>
+__host__ __device__ constexpr int staged_bytes() {
+    return KIND == K_LSE ? 2 * 3 * HALF * 8 : 4 * 2 * OUTB;
+}
 struct Ctl {
-    uint64_t full[STAGES], empty[STAGES], done[2], free_[2];
+    uint64_t full[6], empty[6], done[2], free_[2];
     uint32_t tmem;
     int abort;
 };
-constexpr size_t kSmem = 1024 + (size_t)STAGES * 2 * OPB + 4 * OUTB + sizeof(Ctl);
-static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+template <int KIND>
+constexpr size_t smem_bytes() {
+    return 1024 + (size_t)stages<KIND>() * 2 * OPB + staged_bytes<KIND>() + sizeof(Ctl);
+}
+static_assert(smem_bytes<K_LSE>() <= 227 * 1024 && smem_bytes<K_GRAD>() <= 227 * 1024, "shared memory of a CTA");
 
 struct Maps {
     CUtensorMap a, b;    // logits: h, w.  Gradients of h: P, w
@@ -175,8 +186,10 @@ struct Maps {
 struct GemmParams {
     int mt, nt, group;    // tiles of 256 (logits; gradients of h), rows of tiles walked together
     int kb;               // K steps
+    int chunk;            // of which so many are added up at a time
     int splits, kper;     // gradients of h: K cut into splits of kper steps
     int mt2, nt2, kb2;    // gradients of w
+    int more, early;      // pairs with a dh tile more than the others; rounds of dw tiles that those run alone
     int f32;              // operands are three parts of fp32 values
     int T, V, W;          // V: columns of this launch's logits (the piece's, from v0 on)
     int v0, vocab;
@@ -192,8 +205,14 @@ struct GemmParams {
     void* dw; int64_t lddw; int dw_store;  // dw_store: by TMA through `out`
 };
 
-__device__ __forceinline__ int64_t target_of(const GemmParams& p, int t) {
-    return p.wide ? __ldg(static_cast<const long long*>(p.targets) + t) : __ldg(static_cast<const int*>(p.targets) + t);
+// a token's target: -1 where it is left out, vocab where it is that or more
+__device__ __forceinline__ int target_of(const GemmParams& p, int t) {
+    if (!p.wide) {
+        const int v = __ldg(static_cast<const int*>(p.targets) + t);
+        return v < 0 ? -1 : min(v, p.vocab);
+    }
+    const long long v = __ldg(static_cast<const long long*>(p.targets) + t);
+    return v < 0 ? -1 : v > p.vocab ? p.vocab : (int)v;
 }
 
 struct Unit {
@@ -201,42 +220,52 @@ struct Unit {
     bool second;  // a gradient of w
 };
 
+// Unit i of a pair of CTAs, false behind its last.  Logits: tile pair + i pairs.  Gradients:
+// dh's tiles the same way, then dw's, of which the pairs that have a tile of dh less run
+// `early` more, so that all end together (round robin over both kinds left the last fifth
+// of a short call's time to a few pairs).
 template <int KIND>
-__device__ __forceinline__ int units(const GemmParams& p) {
-    return KIND == K_GRAD ? p.mt * p.nt * p.splits + p.mt2 * p.nt2 : p.mt * p.nt;
-}
-template <int KIND>
-__device__ __forceinline__ Unit unit(const GemmParams& p, int u) {
-    Unit r;
+__device__ __forceinline__ bool unit(const GemmParams& p, int pair, int pairs, int i, Unit& r) {
     r.second = false;
     r.split = 0;
     r.k0 = 0;
     r.k1 = p.kb;
+    const int n1 = p.mt * p.nt * (KIND == K_GRAD ? p.splits : 1);
+    const int u = pair + i * pairs;
     if (KIND != K_GRAD) {
+        if (u >= n1) return false;
         // `group` rows of tiles, column after column: the tiles that run together share
         // few operands
         const int per = p.group * p.nt, g = u / per, first = g * p.group;
         const int rows = min(p.group, p.mt - first), in = u - g * per;
         r.m = first + in % rows;
         r.n = in / rows;
-        return r;
+        return true;
     }
-    const int n1 = p.mt * p.nt;
-    if (u < n1 * p.splits) {
-        r.split = u / n1;
-        const int in = u - r.split * n1;
+    if (u < n1) {
+        const int tiles = p.mt * p.nt;
+        r.split = u / tiles;
+        const int in = u - r.split * tiles;
         r.m = in / p.nt;
         r.n = in % p.nt;
         r.k0 = r.split * p.kper;
         r.k1 = min(p.kb, r.k0 + p.kper);
-    } else {
-        const int in = u - n1 * p.splits;
-        r.second = true;
-        r.m = in / p.nt2;
-        r.n = in % p.nt2;
-        r.k1 = p.kb2;
+        return true;
     }
-    return r;
+    const bool fewer = pair >= p.more;  // pairs 0 .. more - 1 have one tile of dh more
+    int j = i - n1 / pairs - (fewer ? 0 : 1), v;
+    if (fewer && j < p.early) {
+        v = j * (pairs - p.more) + pair - p.more;
+    } else {
+        if (fewer) j -= p.early;
+        v = p.early * (pairs - p.more) + j * pairs + pair;
+    }
+    if (v >= p.mt2 * p.nt2) return false;
+    r.second = true;
+    r.m = v / p.nt2;
+    r.n = v % p.nt2;
+    r.k1 = p.kb2;
+    return true;
 }
 
 // part of a and of b of product c: (1,3) (2,2) (3,1) (1,2) (2,1) (1,1)
@@ -245,13 +274,16 @@ __device__ __forceinline__ int part_b(int c) { return (0x001012 >> (4 * c)) & 15
 
 // K steps that are added up in tensor memory; CH = 0: all.  The tensor cores cut their
 // sums towards zero, step after step: 2^-24 of a sum each, always to the same side.
-// Where that counts, chunks are added up in registers, rounded: for logits of bf16 (lse off by
-// 9e-7 of itself at a width of 2048 without, 2e-7 with chunks of eight), and for all of
+// Where that counts, chunks are added up in registers, rounded: for logits of bf16 (the loss
+// of 4096 tokens, 50021 columns and a width of 2048 off by 1.6e-6 of itself without chunks,
+// 0.4e-6 with eight steps each; 531 us without, 541 with 16, 560 with 8), and for all of
 // fp32, whose small products come first in a chunk, while the sum is small.
 template <int KIND, bool F32>
-__host__ __device__ constexpr int chunk_steps() {
-        return F32 ? 4 : KIND == K_LSE ? 8 : 0;
+__host__ __device__ constexpr bool chunked() {
+    return F32 || KIND == K_LSE;
 }
+constexpr int kChunkF32 = 4;   // the most steps of a chunk
+constexpr int kChunkBf16 = 12;
 
 // v = x, or x -= g, where column o is i, for every i of a row in registers.  Written out:
 // the compiler makes an array in local memory of a chain of choices.
@@ -278,13 +310,15 @@ __device__ __forceinline__ void put8(float* q, const float* v, bool add) {
 template <int KIND, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
     vocab_gemm_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
-    constexpr int CH = chunk_steps<KIND, F32>();
+    constexpr bool CH = chunked<KIND, F32>();
+    const int ch = p.chunk;
     constexpr int NP = F32 ? 6 : 1;  // products of parts
+    constexpr int STAGES = stages<KIND>();
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
     const uint32_t ring = tc::smem_addr(base);
     unsigned char* staged = base + STAGES * 2 * OPB;
-    Ctl& c = *reinterpret_cast<Ctl*>(staged + 4 * OUTB);
+    Ctl& c = *reinterpret_cast<Ctl*>(staged + staged_bytes<KIND>());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -308,18 +342,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
     cluster_sync();
     tc::fence_after();
     const uint32_t tmem = c.tmem;
-    const int n_units = units<KIND>(p);
+    Unit w;
 
     if (warp == 0 && lane == 0) {
         // ---- loads ----
         int s = 0, phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int u = pair; u < n_units && ok; u += pairs) {
-            const Unit w = unit<KIND>(p, u);
+        for (int i = 0; ok && unit<KIND>(p, pair, pairs, i, w); ++i) {
             const int row_a = w.m * BM + (int)rank * HALF, row_b = w.n * BN + (int)rank * HALF;
-            for (int k0 = w.k0; k0 < w.k1 && ok; k0 += CH ? CH : w.k1 - w.k0) {
-                const int k1 = CH ? min(w.k1, k0 + CH) : w.k1;
+            for (int k0 = w.k0; k0 < w.k1 && ok; k0 += CH ? ch : w.k1 - w.k0) {
+                const int k1 = CH ? min(w.k1, k0 + ch) : w.k1;
                 for (int q = 0; q < NP && ok; ++q)
                     for (int k = k0; k < k1; ++k) {
                         if (issued >= STAGES && !wait_for(&c.empty[s], phase ^ 1, &c.abort)) {
@@ -375,13 +408,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         // ---- products ----
         int s = 0, phase = 0, it = 0;
         bool ok = true;
-        for (int u = pair; u < n_units && ok; u += pairs) {
-            const Unit w = unit<KIND>(p, u);
+        for (int i = 0; ok && unit<KIND>(p, pair, pairs, i, w); ++i) {
             const bool a_mn = KIND == K_GRAD && w.second, b_mn = KIND == K_GRAD;
             const uint32_t id = tc::idesc_bf16(BM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u);
             int k0 = w.k0;
             do {  // (a unit without steps has one chunk without steps)
-                const int k1 = CH ? min(w.k1, k0 + CH) : w.k1;
+                const int k1 = CH ? min(w.k1, k0 + ch) : w.k1;
                 const int buf = it & 1;
                 if (it >= 2 && !wait_for(&c.free_[buf], ((it >> 1) & 1) ^ 1, &c.abort)) {
                     ok = false;
@@ -424,13 +456,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         const int row = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)quarter * EW;
         const bool lead = quad == 0 && lane == 0;  // of the quarter: its stores
-        unsigned char* const stage = staged + quarter * OUTB;
+        unsigned char* const stage = staged + (KIND == K_LSE ? 0 : quarter * 2 * OUTB);
         // K_LSE: the other quarters' maximum and sum of a row, of this tile and the last
         float2* part = reinterpret_cast<float2*>(staged);
         int it = 0, tile = 0;
         bool ok = true;
-        for (int u = pair; u < n_units; u += pairs) {
-            const Unit w = unit<KIND>(p, u);
+        for (int i = 0; unit<KIND>(p, pair, pairs, i, w); ++i) {
             const int r0 = w.m * BM + (int)rank * HALF, r = r0 + row;
             const int c0 = w.n * BN + quarter * EW;
             float acc[CH ? EW : 1];
@@ -448,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 tc::fence_after();
                 d = lanes + (uint32_t)buf * BN;
                 release = in_leader(tc::smem_addr(&c.free_[buf]));
-                if constexpr (CH > 0) {
+                if constexpr (CH) {
 #pragma unroll
                     for (int j = 0; j < EW; j += 8) {
                         float x[8];
@@ -461,16 +492,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     if (lane == 0) arrive_cluster(release);
                 }
                 ++it;
-                k0 = CH ? k0 + CH : w.k1;
+                k0 = CH ? k0 + ch : w.k1;
             } while (k0 < w.k1);
 
             if (KIND == K_LSE) {
                 const bool real = r < p.T;
-                const int64_t tgt = real ? target_of(p, r) : -1;
                 const int left = p.V - c0;
-                const int64_t o = tgt - c0;
+                const int o = real ? target_of(p, r) - c0 : -1;
                 float top = -INFINITY, sum = 0.f;
-                if constexpr (CH > 0) {
+                if constexpr (CH) {
 #pragma unroll
                     for (int i = 0; i < EW; ++i) {
                         acc[i] = i < left ? acc[i] * p.scale : -INFINITY;
@@ -479,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     if (o >= 0 && o < EW) {
                         float v = 0.f;
 #pragma unroll
-                        for (int i = 0; i < EW; ++i) take_at(v, acc[i], (int)o, i);
+                        for (int i = 0; i < EW; ++i) take_at(v, acc[i], o, i);
                         p.at[r] = v;
                     }
                     const float ref = top == -INFINITY ? 0.f : top;
@@ -503,12 +533,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 }
             } else if (KIND == K_P || (w.second && p.dw_store)) {
                 float lse = 0.f, g = 0.f;
-                int64_t tgt = -1;
+                int tgt = -1;  // the target's column of this piece
                 if (KIND == K_P && r < p.T) {
                     tgt = target_of(p, r);
                     lse = __ldg(p.lse + r);
                     g = tgt < 0 ? 0.f : tgt >= p.vocab ? NAN : __ldg(p.dloss + r) * p.scale;
-                    tgt -= p.v0;
+                    tgt = tgt < 0 ? -1 : tgt - p.v0;
                 }
                 const bool live = KIND != K_P || g != 0.f;
                 float lo = 0.f;
@@ -522,10 +552,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 }
                 constexpr int PARTS = KIND == K_P && F32 ? 3 : 1;
                 const int out_cols = KIND == K_P ? p.V : p.W, out_rows = KIND == K_P ? p.T : p.V;
+                // the copies of the last tile have read their pieces
+                if (PARTS == 1) {
+                    if (lead) tc::bulk_wait_read();
+                    tc::bar_sync(2 + quarter, 128);
+                }
 #pragma unroll
                 for (int j = 0; j < EW; j += SC) {
                     float x[SC];
-                    if constexpr (CH > 0) {
+                    if constexpr (CH) {
 #pragma unroll
                         for (int i = 0; i < SC; ++i) x[i] = acc[j + i];
                     } else {
@@ -539,13 +574,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     if (KIND == K_P) {
 #pragma unroll
                         for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], p.scale, -lse) * kLog2e) : 0.f;
-                        const int64_t o = tgt - (c0 + j);
+                        const int o = tgt < 0 ? -1 : tgt - (c0 + j);
                         if (o >= 0 && o < SC) {
                             float at = 0.f;
 #pragma unroll
                             for (int i = 0; i < SC; ++i) {
-                                sub_at(x[i], live ? g : 0.f, (int)o, i);
-                                take_at(at, x[i], (int)o, i);
+                                sub_at(x[i], live ? g : 0.f, o, i);
+                                take_at(at, x[i], o, i);
                             }
                             if (!F32) p.lo[r] = at - __bfloat162float(__float2bfloat16_rn(at));
                         }
@@ -561,8 +596,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
 #pragma unroll
                     for (int q = 0; q < PARTS; ++q) {
-                        if (lead) tc::bulk_wait_read();
-                        tc::bar_sync(2 + quarter, 128);
+                        unsigned char* const to = stage + ((j / SC * PARTS + q) & 1) * OUTB;
+                        if (PARTS > 1) {  // one piece may still be on its way, the other one
+                            if (lead) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            tc::bar_sync(2 + quarter, 128);
+                        }
 #pragma unroll
                         for (int h = 0; h < SC / 8; ++h) {
                             uint4 o4;
@@ -578,14 +616,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                                 }
                             }
                             // rows of 64 bytes under the 64-byte swizzle
-                            *reinterpret_cast<uint4*>(stage + row * 64 + ((h ^ ((row >> 1) & 3)) << 4)) = o4;
+                            *reinterpret_cast<uint4*>(to + row * 64 + ((h ^ ((row >> 1) & 3)) << 4)) = o4;
                         }
-                        tc::fence_async_smem();
-                        tc::bar_sync(2 + quarter, 128);
-                        if (lead && c0 + j < out_cols && r0 < out_rows) {
-                            store_box(&maps.out, c0 + j, r0, q, tc::smem_addr(stage));
-                            tc::bulk_commit();
+                        if (PARTS > 1) {
+                            tc::fence_async_smem();
+                            tc::bar_sync(2 + quarter, 128);
+                            if (lead) {
+                                // (a group is closed with or without a copy: the wait above counts them)
+                                if (c0 + j < out_cols && r0 < out_rows) store_box(&maps.out, c0 + j, r0, q, tc::smem_addr(to));
+                                tc::bulk_commit();
+                            }
                         }
+                    }
+                }
+                if (PARTS == 1) {
+                    tc::fence_async_smem();
+                    tc::bar_sync(2 + quarter, 128);
+                    if (lead && r0 < out_rows) {
+                        for (int j = 0; j < EW; j += SC)
+                            if (c0 + j < out_cols) store_box(&maps.out, c0 + j, r0, 0, tc::smem_addr(stage + j / SC * OUTB));
+                        tc::bulk_commit();
                     }
                 }
             } else {
@@ -604,7 +654,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
 #pragma unroll
                 for (int j = 0; j < EW; j += 32) {
                     float x[32];
-                    if constexpr (CH > 0) {
+                    if constexpr (CH) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = acc[j + i];
                     } else {
@@ -724,23 +774,48 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict_
     loss[r] = tgt < 0 ? 0.f : tgt >= V ? NAN : z - __ldg(at + r);
 }
 
-// dh from the splits' sums; for bf16 with what P's rounding took at the target (lo)
+// dh from the splits' sums, eight columns a thread; for bf16 with what P's rounding took
+// at the target (lo)
 template <typename E>
-__global__ void __launch_bounds__(256) dh_kernel(const float* __restrict__ acc, int splits, int64_t T, int W, int ldacc,
+__global__ void __launch_bounds__(256) dh_kernel(const float* __restrict__ acc, int splits, int T, int W, int ldacc,
                                                  const float* __restrict__ lo, const void* targets, int wide, int vocab,
-                                                 const E* __restrict__ w, int64_t ldw, E* __restrict__ dh, int64_t lddh) {
-    const int64_t n = T * W;
+                                                 const E* __restrict__ w, int64_t ldw, E* __restrict__ dh, int64_t lddh,
+                                                 int vec) {
+    const int nv = ldacc / 8;
+    const int64_t n = (int64_t)T * nv;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / W;
-        const int c = (int)(i - r * W);
-        float f = 0.f;
-        for (int s = 0; s < splits; ++s) f += acc[(s * T + r) * ldacc + c];
+        const int64_t r = (n >> 31) ? i / nv : (int64_t)((unsigned)i / (unsigned)nv);
+        const int c = (int)(i - r * nv) * 8;
+        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int s = 0; s < splits; ++s) {
+            float x[8];
+            load8(acc + (s * (int64_t)T + r) * ldacc + c, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] += x[j];
+        }
         if (sizeof(E) == 2) {
             const int64_t tgt =
                 wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
-            if (tgt >= 0 && tgt < vocab) f = fmaf(__ldg(lo + r), Elem<E>::load(w + tgt * ldw + c), f);
+            if (tgt >= 0 && tgt < vocab) {
+                const float l = __ldg(lo + r);
+                float x[8];
+                if (vec) load8(w + tgt * ldw + c, x);
+                else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = c + j < W ? Elem<E>::to_f(w[tgt * ldw + c + j]) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = fmaf(l, x[j], f[j]);
+            }
         }
-        dh[r * lddh + c] = Elem<E>::from_f(f);
+        E* o = dh + r * lddh + c;
+        if (vec) store8(o, f);
+        else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < W) o[j] = Elem<E>::from_f(f[j]);
+        }
     }
 }
 
@@ -762,11 +837,11 @@ int piece_cols(int T, int V, gdn_dtype dt) {
     const int64_t all = div_up(V, BN) * BN;
     return (int)(c < all ? c : all);
 }
-// K of dh's product cut so that its tiles, with half as many pairs of CTAs to spare, fill
-// the GPU; splits of 16 steps at least
+// K of dh's product cut into as many splits as leave its tiles no more than the pairs of
+// CTAs; splits of 16 steps at least
 int dh_splits(int T, int W, int cols) {
     const int64_t tiles = div_up(T, BM) * div_up(W, BN), kb = div_up(cols, BK);
-    int64_t s = div_up(device_sm_count() / 2, tiles);
+    int64_t s = device_sm_count() / 2 / tiles;
     if (s > kb / 16) s = kb / 16;
     if (s > 16) s = 16;
     return (int)(s < 1 ? 1 : s);
@@ -813,7 +888,7 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
 }
 
 // Pairs of CTAs that run at the same time, a CTA an SM; asked once per device
-int pair_count(const void* fn) {
+int pair_count(const void* fn, size_t smem) {
     constexpr int kMaxDev = 64;
     static int known[kMaxDev] = {};
     int dev = 0;
@@ -822,7 +897,7 @@ int pair_count(const void* fn) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(device_sm_count() / 2 * 2);
     cfg.blockDim = dim3(GT);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
@@ -832,15 +907,41 @@ int pair_count(const void* fn) {
     return n;
 }
 
+// The rounds of dw tiles that the pairs with one dh tile less run alone: the count that makes
+// the longest pair's time least.  Times in K steps; a tile of few steps takes its epilogue's.
+void balance(GemmParams& p, int64_t n1, int64_t n2, int pairs) {
+    constexpr int64_t kEpilogue = 8;
+    const int64_t c1 = (p.kper > kEpilogue ? p.kper : kEpilogue), c2 = (p.kb2 > kEpilogue ? p.kb2 : kEpilogue);
+    const int64_t more = n1 % pairs, rest = pairs - more;
+    p.more = (int)more;
+    p.early = 0;
+    if (more == 0) return;
+    int64_t best = -1;
+    const int64_t most = c1 / c2 + 2 < div_up(n2, rest) ? c1 / c2 + 2 : div_up(n2, rest);
+    for (int64_t e = 0; e <= most; ++e) {
+        const int64_t left = n2 - e * rest, b = left > 0 ? div_up(left, pairs) : 0;  // rounds of all pairs
+        const int64_t t = b * c2 + (c1 > e * c2 ? c1 : e * c2);
+        if (best < 0 || t < best) {
+            best = t;
+            p.early = (int)e;
+        }
+    }
+}
+
 template <int KIND, bool F32>
-gdn_status launch_gemm_t(const GemmParams& p, const Maps& m, cudaStream_t s) {
+gdn_status launch_gemm_t(GemmParams p, const Maps& m, cudaStream_t s) {
     const void* fn = (const void*)vocab_gemm_kernel<KIND, F32>;
-    gdn_status st = set_smem_attr(fn, kSmem);
+    constexpr size_t smem = smem_bytes<KIND>();
+    gdn_status st = set_smem_attr(fn, smem);
     if (st != GDN_OK) return st;
-    const int64_t n = (int64_t)p.mt * p.nt * (KIND == K_GRAD ? p.splits : 1) + (int64_t)p.mt2 * p.nt2;
-    if (n > 0x7fffffff / 2) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)n);
-    const int pairs = pair_count(fn);
-    vocab_gemm_kernel<KIND, F32><<<2 * (unsigned)(n < pairs ? n : pairs), GT, kSmem, s>>>(p, m);
+    const int64_t n1 = (int64_t)p.mt * p.nt * (KIND == K_GRAD ? p.splits : 1), n2 = (int64_t)p.mt2 * p.nt2;
+    if (n1 + n2 > 0x7fffffff / 2) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)(n1 + n2));
+    int pairs = pair_count(fn, smem);
+    if (n1 + n2 < pairs) pairs = (int)(n1 + n2);
+    const int steps = F32 ? kChunkF32 : kChunkBf16;
+    p.chunk = KIND == K_GRAD ? steps : (int)div_up(p.kb, div_up(p.kb, steps));
+    if (KIND == K_GRAD) balance(p, n1, n2, pairs);
+    vocab_gemm_kernel<KIND, F32><<<2 * (unsigned)pairs, GT, smem, s>>>(p, m);
     return check_launch("vocab_gemm_kernel");
 }
 template <int KIND>
@@ -950,7 +1051,7 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     p.group = group_rows(p.mt, width, parts);
     p.kb = (int)div_up(width, BK);
     p.f32 = parts == 3;
-    p.T = T; p.V = vocab; p.W = width; p.scale = scale;
+    p.T = T; p.V = p.vocab = vocab; p.W = width; p.scale = scale;
     p.targets = targets; p.wide = wide;
     p.stat = reinterpret_cast<float2*>(ws + l.stat);
     p.at = reinterpret_cast<float*>(ws + l.at);
@@ -1037,14 +1138,16 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         p.dw = dwp; p.lddw = lddw; p.dw_store = store;
         if ((st = launch_gemm<K_GRAD>(p, m, s)) != GDN_OK) return st;
     }
-    const unsigned g = grid_for((int64_t)T * width);
+    const unsigned g = grid_for((int64_t)T * (l.ldacc / 8));
+    // 16-byte accesses of dh and, in bf16, of w
+    const int vec = width % 8 == 0 && (reinterpret_cast<uintptr_t>(dh) & 15u) == 0 && lddh % 8 == 0;
     if (dtype == GDN_F32)
         dh_kernel<float><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, nullptr, targets, wide, vocab,
-                                           static_cast<const float*>(w), ldw, static_cast<float*>(dh), lddh);
+                                           static_cast<const float*>(w), ldw, static_cast<float*>(dh), lddh, vec);
     else
         dh_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, p.lo, targets, wide, vocab,
                                                    static_cast<const __nv_bfloat16*>(w), ldw,
-                                                   static_cast<__nv_bfloat16*>(dh), lddh);
+                                                   static_cast<__nv_bfloat16*>(dh), lddh, vec);
     return check_launch("dh_kernel");
 }
 
