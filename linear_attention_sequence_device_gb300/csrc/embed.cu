@@ -10,10 +10,11 @@
 // token's rows are added in their order and equal calls give equal bits), walks the
 // sorted rows in pieces of `piece` rows, and fills the rows of tokens that do not occur
 // with zeros.  A piece adds up the rows of one token after the other in registers, its
-// loads ahead, and writes a token's sum where all its rows are in the piece; the parts
-// of a token that several pieces hold go to the workspace in fp32 and are added, in the
-// pieces' order, by a second launch.  So a token that fills a twentieth of a batch costs no
-// more than the others.  What bounds it: dy read once, the table's gradient written once.
+// loads ahead; a token whose rows go on into the next piece and end there is its too.
+// Longer ones are left in parts, which go to the workspace in fp32 and are added, in the
+// pieces' order, by a second launch, so that a token that fills a twentieth of a batch
+// costs no more than the others.  What bounds it: dy read once, the table's gradient
+// written once.
 #include "ssm_common.cuh"
 
 namespace gdn {
@@ -389,17 +390,38 @@ __device__ __forceinline__ void add_part(const float* w, float (&acc)[VEC]) {
     }
 }
 
-// Blocks [0, pieces) walk a piece of the sorted rows each; the others fill the rows of
-// tokens that do not occur, zrows each.  blockIdx.y: PT * U vectors of columns.
+// Whether the token v, whose rows go on over the start r of a piece, is added up by the
+// piece that it begins in: it begins in the one before r and ends in the one behind.
+// Longer ones are left in parts.
+__device__ __forceinline__ bool one_piece_has(const SumArgs& a, int v, int r) {
+    return (r - a.piece - 1 < 0 || __ldg(a.key + r - a.piece - 1) != v) &&
+           (r + a.piece >= a.T || __ldg(a.key + r + a.piece) != v);
+}
+
+// zeros, in 16-byte accesses but for the ends
+template <typename E>
+__device__ __forceinline__ void fill_zero(E* p, int64_t n) {
+    constexpr int N = 16 / sizeof(E);
+    int64_t head = (16 - (int64_t)(reinterpret_cast<uintptr_t>(p) & 15u)) % 16 / (int)sizeof(E);
+    if (head > n) head = n;
+    for (int64_t i = threadIdx.x; i < head; i += PT) p[i] = Elem<E>::from_f(0.f);
+    p += head;
+    n -= head;
+    uint4* q = reinterpret_cast<uint4*>(p);
+    for (int64_t i = threadIdx.x; i < n / N; i += PT) __stcs(q + i, make_uint4(0u, 0u, 0u, 0u));
+    for (int64_t i = n / N * N + threadIdx.x; i < n; i += PT) p[i] = Elem<E>::from_f(0.f);
+}
+
+// Blocks [0, pieces ny) add up the rows of a piece's tokens, PT * U vectors of columns
+// each; the others fill the rows of tokens that do not occur, zrows each.
 template <typename E, int VEC, int U>
-__global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a, int ny) {
     using V = Vec<E, VEC>;
     using R = typename V::raw;
-    const int c0 = (blockIdx.y * U * PT + threadIdx.x) * VEC;  // vector u: c0 + u PT VEC
-    if ((int)blockIdx.x >= a.pieces) {
+    if ((int)blockIdx.x >= a.pieces * ny) {
         __shared__ unsigned hit[kMaxPiece / 32];
         __shared__ int range[2];
-        const int v0 = ((int)blockIdx.x - a.pieces) * a.zrows, v1 = min(a.vocab, v0 + a.zrows);
+        const int v0 = ((int)blockIdx.x - a.pieces * ny) * a.zrows, v1 = min(a.vocab, v0 + a.zrows);
         if (threadIdx.x < kMaxPiece / 32) hit[threadIdx.x] = 0;
         if (threadIdx.x < 64) {
             const int i = first_at(a.key, a.T, threadIdx.x < 32 ? v0 : v1);
@@ -413,28 +435,49 @@ __global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
             if (i == lo || __ldg(a.key + i - 1) != v) atomicOr(&hit[(v - v0) >> 5], 1u << ((v - v0) & 31));
         }
         __syncthreads();
-        float zero[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) zero[j] = 0.f;
-#pragma unroll 4
-        for (int v = v0; v < v1; ++v)
-            if (!(hit[(v - v0) >> 5] >> ((v - v0) & 31) & 1u)) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + u * PT * VEC < a.W) put<E, VEC>(a, v, c0 + u * PT * VEC, zero);
+        auto occurs = [&](int v) { return (hit[(v - v0) >> 5] >> ((v - v0) & 31) & 1u) != 0; };
+        for (int v = v0; v < v1;) {
+            if (occurs(v)) {
+                ++v;
+                continue;
             }
+            int w = v + 1;  // rows without a gap between them are filled as one
+            if (a.ldo == a.W)
+                while (w < v1 && !occurs(w)) ++w;
+            fill_zero(static_cast<E*>(a.out) + v * a.ldo, (int64_t)(w - v) * a.W);
+            v = w;
+        }
         return;
     }
-    __shared__ int key[kMaxPiece + 2];  // with the rows on either side
-    __shared__ int pos[kMaxPiece];
-    const int r0 = blockIdx.x * a.piece, n = min(a.piece, a.T - r0);
-    for (int i = threadIdx.x; i < n + 2; i += PT) {
-        const int r = r0 + i - 1;
-        key[i] = r < 0 || r >= a.T ? -1 : __ldg(a.key + r);
-        if (i > 0 && i <= n) pos[i - 1] = __ldg(a.pos + r);
+    const int piece = blockIdx.x / ny, c0 = ((blockIdx.x - piece * ny) * U * PT + threadIdx.x) * VEC;  // vector u: + u PT VEC
+    __shared__ int key[2 * kMaxPiece + 1];  // with the rows of the next piece, where the last token may end
+    __shared__ int pos[2 * kMaxPiece];
+    __shared__ int ends[2];
+    const int r0 = piece * a.piece, r1 = min(a.T, r0 + a.piece), rmax = min(a.T, r1 + a.piece);
+    for (int i = threadIdx.x; i <= rmax - r0; i += PT) {
+        key[i] = r0 + i < rmax ? __ldg(a.key + r0 + i) : -1;
+        if (r0 + i < rmax) pos[i] = __ldg(a.pos + r0 + i);
+    }
+    if (threadIdx.x == 0) {
+        const int v = __ldg(a.key + r0);
+        // 0: a token begins here; 1: the piece before has the first one; 2: it is left in parts
+        ends[0] = r0 == 0 || __ldg(a.key + r0 - 1) != v ? 0 : one_piece_has(a, v, r0) ? 1 : 2;
+    } else if (threadIdx.x == 32) {
+        const int v = __ldg(a.key + r1 - 1);
+        ends[1] = r1 == a.T || __ldg(a.key + r1) != v ? 0 : one_piece_has(a, v, r1) ? 1 : 2;
     }
     __syncthreads();
     if (c0 >= a.W) return;
+    int i0 = 0, n = r1 - r0;
+    if (ends[0] == 1) {
+        const int v = key[0];
+        while (i0 < n && key[i0] == v) ++i0;
+        if (i0 == n) return;
+    }
+    if (ends[1] == 1) {
+        const int v = key[n - 1];
+        while (key[n] == v) ++n;
+    }
     const E* dy = static_cast<const E*>(a.dy) + c0;
     constexpr int AHEAD = 8;
     R row[AHEAD][U];
@@ -446,19 +489,19 @@ __global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
     };
 #pragma unroll
     for (int s = 0; s < AHEAD; ++s)
-        if (s < n && key[s + 1] < a.vocab) load(s, s);
+        if (i0 + s < n && key[i0 + s] < a.vocab) load(s, i0 + s);
     float acc[U][VEC];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) acc[u][j] = 0.f;
-    bool whole = key[0] != key[1];  // the token began in this piece
-    for (int i0 = 0; i0 < n; i0 += AHEAD) {
+    bool whole = ends[0] != 2;  // all rows of the token are added up here
+    for (; i0 < n; i0 += AHEAD) {
 #pragma unroll
         for (int s = 0; s < AHEAD; ++s) {
             const int i = i0 + s;
             if (i >= n) break;
-            const int v = key[i + 1];
+            const int v = key[i];
             if (v >= a.vocab) return;  // padded tokens are behind all others
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -468,15 +511,15 @@ __global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
                 for (int j = 0; j < VEC; ++j) acc[u][j] += f[j];
             }
             const int nx = i + AHEAD;
-            if (nx < n && key[nx + 1] < a.vocab) load(s, nx);
-            const bool ends = key[i + 2] != v;
-            if (ends || i == n - 1) {
+            if (nx < n && key[nx] < a.vocab) load(s, nx);
+            const bool last = key[i + 1] != v;
+            if (last || i == n - 1) {
                 // its sum, or its part in this piece: the first one's, or the last one's that goes on
-                float* const part = a.part + ((int64_t)blockIdx.x * 2 + (ends ? 0 : 1)) * a.W + c0;
+                float* const part = a.part + ((int64_t)piece * 2 + (last ? 0 : 1)) * a.W + c0;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (U == 1 || c0 + u * PT * VEC < a.W) {
-                        if (ends && whole) put<E, VEC>(a, v, c0 + u * PT * VEC, acc[u]);
+                        if (last && whole) put<E, VEC>(a, v, c0 + u * PT * VEC, acc[u]);
                         else put_part<VEC>(part + u * PT * VEC, acc[u]);
                     }
 #pragma unroll
@@ -488,44 +531,64 @@ __global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a) {
     }
 }
 
-// Block b adds up the token that begins in piece b and goes on in the next ones: the last
-// parts of piece b and of the pieces that it fills, and the first part of the one that it
-// ends in (where it fills that too, it ends there all the same).  JG groups of threads
-// take a run of the parts each; their sums are added in the runs' order.
+// Adds up the tokens that are left in parts: the one that begins in piece b, if it goes on
+// over more than the next piece, is the sum of the last parts of piece b and of the pieces
+// that it fills and the first part of the one that it ends in (where it fills that too, it
+// ends there all the same).  A block looks at every gridDim.x-th piece, 32 at a time: few
+// have such a token.  JG groups of threads take a run of the parts each; their sums are
+// added in the runs' order.
 constexpr int JG = 4;
 
 template <typename E, int VEC>
-__global__ void __launch_bounds__(PT * JG) embed_join_kernel(const SumArgs a) {
-    const int b = blockIdx.x, last = (b + 1) * a.piece - 1;  // the piece is full: another follows
-    const int v = __ldg(a.key + last);
-    if (v >= a.vocab || __ldg(a.key + last + 1) != v) return;    // does not go on
-    if (b > 0 && __ldg(a.key + b * a.piece - 1) == v) return;    // began earlier
+__global__ void __launch_bounds__(PT * JG, 2) embed_join_kernel(const SumArgs a) {
     __shared__ float sum[JG - 1][PT][VEC];
+    __shared__ unsigned found;
     const int x = threadIdx.x % PT, g = threadIdx.x / PT;
     const int c = (blockIdx.y * PT + x) * VEC;
-    const int end = first_at(a.key, a.T, v + 1);  // behind the token's last row
-    const int pe = (end - 1) / a.piece;           // the piece that it ends in
-    const int n = pe - b + 1, per = (n + JG - 1) / JG;  // parts, of a group
-    float acc[VEC];
+    for (int64_t b0 = blockIdx.x; b0 < a.pieces - 1; b0 += 32ll * gridDim.x) {
+        if (threadIdx.x < 32) {
+            const int64_t b = b0 + (int64_t)threadIdx.x * gridDim.x;
+            bool parts = false;
+            if (b < a.pieces - 1) {
+                const int r = (int)(b + 1) * a.piece, v = __ldg(a.key + r);  // the next piece's start
+                parts = v < a.vocab && __ldg(a.key + r - 1) == v && !one_piece_has(a, v, r) &&
+                        (b == 0 || __ldg(a.key + r - a.piece - 1) != v);
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, parts);
+            if (threadIdx.x == 0) found = m;
+        }
+        __syncthreads();
+        for (unsigned m = found; m; m &= m - 1) {
+            const int b = (int)(b0 + (int64_t)(__ffs(m) - 1) * gridDim.x);
+            const int v = __ldg(a.key + (b + 1) * a.piece);
+            const int end = first_at(a.key, a.T, v + 1);  // behind the token's last row
+            const int pe = (end - 1) / a.piece;           // the piece that it ends in
+            const int n = pe - b + 1, per = (n + JG - 1) / JG;  // parts, of a group
+            float acc[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
-    if (c < a.W) {
-        const int i1 = min(n, (g + 1) * per);
-#pragma unroll 8
-        for (int i = g * per; i < i1; ++i)
-            add_part<VEC>(a.part + ((int64_t)(b + i) * 2 + (i < n - 1 ? 1 : 0)) * a.W + c, acc);
+            for (int j = 0; j < VEC; ++j) acc[j] = 0.f;
+            if (c < a.W) {
+                const int i1 = min(n, (g + 1) * per);
+#pragma unroll 4
+                for (int i = g * per; i < i1; ++i)
+                    add_part<VEC>(a.part + ((int64_t)(b + i) * 2 + (i < n - 1 ? 1 : 0)) * a.W + c, acc);
+            }
+            if (g) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) sum[g - 1][x][j] = acc[j];
+            }
+            __syncthreads();
+            if (!g && c < a.W) {
+#pragma unroll
+                for (int k = 0; k < JG - 1; ++k)
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) acc[j] += sum[k][x][j];
+                put<E, VEC>(a, v, c, acc);
+            }
+            __syncthreads();
+        }
+        __syncthreads();
     }
-    if (g) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[g - 1][x][j] = acc[j];
-    }
-    __syncthreads();
-    if (g || c >= a.W) return;
-#pragma unroll
-    for (int k = 0; k < JG - 1; ++k)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) acc[j] += sum[k][x][j];
-    put<E, VEC>(a, v, c, acc);
 }
 
 // ---- host ------------------------------------------------------------------
@@ -602,14 +665,17 @@ gdn_status run_sum(const SumArgs& a, cudaStream_t s) {
     // single elements: eight of a thread, or the blocks would be small
     constexpr int U = VEC == 1 ? 8 : 1;
     const unsigned ny = (unsigned)((a.W + PT * VEC * U - 1) / (PT * VEC * U));
-    const unsigned zeros = a.into ? 0u : (unsigned)((a.vocab + a.zrows - 1) / a.zrows);
-    if ((unsigned)a.pieces + zeros > 0) {
-        embed_sum_kernel<E, VEC, U><<<dim3(a.pieces + zeros, ny), PT, 0, s>>>(a);
+    const int64_t blocks = (int64_t)a.pieces * ny + (a.into ? 0 : (a.vocab + a.zrows - 1) / a.zrows);
+    if (blocks > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows of %d elements", a.T, a.W);
+    if (blocks > 0) {
+        embed_sum_kernel<E, VEC, U><<<(unsigned)blocks, PT, 0, s>>>(a, (int)ny);
         gdn_status st = check_launch("embed_sum_kernel");
         if (st != GDN_OK) return st;
     }
     if (a.pieces > 1) {
-        embed_join_kernel<E, VEC><<<dim3(a.pieces - 1, (a.W + PT * VEC - 1) / (PT * VEC)), PT * JG, 0, s>>>(a);
+        const int most = 2 * device_sm_count();
+        embed_join_kernel<E, VEC><<<dim3(a.pieces - 1 < most ? a.pieces - 1 : most, (a.W + PT * VEC - 1) / (PT * VEC)),
+                                    PT * JG, 0, s>>>(a);
         return check_launch("embed_join_kernel");
     }
     return GDN_OK;
@@ -706,7 +772,9 @@ gdn_status gdn_embed_bwd(const void* dy, int64_t lddy, gdn_dtype dtype, const vo
     a.pos = reinterpret_cast<int*>(ws + l.pos[which]);
     a.T = T; a.vocab = vocab; a.W = width; a.piece = piece_rows(T);
     a.pieces = (T + a.piece - 1) / a.piece;
-    a.zrows = vocab > 1 << 20 ? kMaxPiece : 32;
+    // rows of about 64 KB together
+    const int64_t zrows = (64 << 10) / ((int64_t)width * (dtype == GDN_BF16 ? 2 : 4));
+    a.zrows = (int)(zrows < 1 ? 1 : zrows > kMaxPiece ? kMaxPiece : zrows);
     a.dy = dy; a.lddy = lddy; a.ldo = ldd; a.scale = scale; a.out = dtable; a.into = accumulate != 0;
     a.part = reinterpret_cast<float*>(ws + l.part);
     if (dtype == GDN_BF16)
