@@ -13,15 +13,23 @@
 //
 // Numerics.  Products of bf16 inputs are exact and added in fp32; maxima, sums, lse and
 // P are fp32.  P is rounded to bf16 for the products behind it, relative to its own
-// size, which puts dh and dw off by as much as their own rounding.  fp32 inputs are
-// split into three bf16 parts that hold all 24 bits, and so is P: six products of
-// parts, those of 2^-24 and more.
+// size, which puts dh and dw off by as much as their own rounding; what that takes from the
+// entry at the target, often the largest of its row, is given back in fp32: to dh for every
+// token, to dw for the tokens that have a target of their own (dh off by 1.66e-3 of itself
+// in norm, its own rounding, and dw by 2.0e-3; 2.5e-3 both without).  fp32 inputs, and P for them, are taken as the
+// sum of two fp16 parts (22 bits) after a scaling by powers of two that brings the
+// largest to 2^14, and three of their four products are formed (of bf16, three parts
+// and six products would take it, twice the time).  The scalings: h by its row, w by one
+// for all, P by its row's dloss; in dw's product h by the inverse of the latter.  A value
+// of 2^-18 of the largest under the same scaling keeps all 22 bits, smaller ones are off
+// by up to 2^-40 of the largest.
 //
 // The product kernel: a pair of CTAs (cta_group::2) forms a 256 x 256 tile, 128 rows of
 // each operand a CTA, from a ring of six stages of 64 along K by TMA; accumulators in tensor
 // memory, two of them, so that the epilogue's sixteen warps run beside the next tile.  One
 // CTA an SM walks tiles by its number.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "ssm_common.cuh"
 #include "tc_util.cuh"
@@ -190,7 +198,7 @@ struct GemmParams {
     int splits, kper;     // gradients of h: K cut into splits of kper steps
     int mt2, nt2, kb2;    // gradients of w
     int more, early;      // pairs with a dh tile more than the others; rounds of dw tiles that those run alone
-    int f32;              // operands are three parts of fp32 values
+    int f32;              // operands are two parts of fp32 values
     int T, V, W;          // V: columns of this launch's logits (the piece's, from v0 on)
     int v0, vocab;
     float scale;
@@ -198,6 +206,8 @@ struct GemmParams {
     float2* stat;         // K_LSE: [nt][T] maximum and sum of a tile's row
     float* at;            // K_LSE: [T] the target's logit
     const float* lse; const float* dloss;  // K_P
+    const int* he; const int* pa;          // fp32: exponents of the scalings of h's rows, of P's
+    const unsigned* most;                  // and what the others are taken from: largest |w|, |h| 2^-pa
     float* lo;            // [T] what P's entry at the target lost when it was rounded
     const int* only;      // [vocab] the one token with this target; below 0: none or several
     const __nv_bfloat16* h; int64_t ldh;   // gradients of w: the rows behind `only`
@@ -268,9 +278,18 @@ __device__ __forceinline__ bool unit(const GemmParams& p, int pair, int pairs, i
     return true;
 }
 
-// part of a and of b of product c: (1,3) (2,2) (3,1) (1,2) (2,1) (1,1)
-__device__ __forceinline__ int part_a(int c) { return (0x010210 >> (4 * c)) & 15; }
-__device__ __forceinline__ int part_b(int c) { return (0x001012 >> (4 * c)) & 15; }
+// part of a and of b of product c: high and low, low and high, high and high
+__device__ __forceinline__ int part_a(int c) { return c == 1; }
+__device__ __forceinline__ int part_b(int c) { return c == 0; }
+
+// 2^k, -126 <= k <= 127
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }
+// the exponent k, -126 to 126, that brings m to [2^to, 2^(to + 1)); 0 where m is zero or not finite
+__device__ __forceinline__ int exponent_for(float m, int to) {
+    if (!(m > 0.f) || !isfinite(m)) return 0;
+    const int k = to + 127 - (__float_as_int(m) >> 23);
+    return k < -126 ? -126 : k > 126 ? 126 : k;
+}
 
 // K steps that are added up in tensor memory; CH = 0: all.  The tensor cores cut their
 // sums towards zero, step after step: 2^-24 of a sum each, always to the same side.
@@ -312,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
     vocab_gemm_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
     constexpr bool CH = chunked<KIND, F32>();
     const int ch = p.chunk;
-    constexpr int NP = F32 ? 6 : 1;  // products of parts
+    constexpr int NP = F32 ? 3 : 1;  // products of parts
     constexpr int STAGES = stages<KIND>();
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
@@ -410,7 +429,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         bool ok = true;
         for (int i = 0; ok && unit<KIND>(p, pair, pairs, i, w); ++i) {
             const bool a_mn = KIND == K_GRAD && w.second, b_mn = KIND == K_GRAD;
-            const uint32_t id = tc::idesc_bf16(BM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u);
+            // (bits 7 and 10: operands of bf16 instead of fp16)
+            const uint32_t id = (tc::idesc_bf16(BM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u)) &
+                                (F32 ? ~(1u << 7 | 1u << 10) : ~0u);
             int k0 = w.k0;
             do {  // (a unit without steps has one chunk without steps)
                 const int k1 = CH ? min(w.k1, k0 + ch) : w.k1;
@@ -452,25 +473,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         }
     } else if (warp >= 2) {
         // ---- epilogue: this thread's row, a quarter of the columns ----
-        const int quad = warp & 3, quarter = (warp - 2) >> 2;  // lanes of tensor memory, columns
-        const int row = quad * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)quarter * EW;
-        const bool lead = quad == 0 && lane == 0;  // of the quarter: its stores
-        unsigned char* const stage = staged + (KIND == K_LSE ? 0 : quarter * 2 * OUTB);
+        // its lanes of tensor memory and columns
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((warp - 2) >> 2) * EW;
         // K_LSE: the other quarters' maximum and sum of a row, of this tile and the last
         float2* part = reinterpret_cast<float2*>(staged);
         int it = 0, tile = 0;
         bool ok = true;
-        for (int i = 0; unit<KIND>(p, pair, pairs, i, w); ++i) {
-            const int r0 = w.m * BM + (int)rank * HALF, r = r0 + row;
-            const int c0 = w.n * BN + quarter * EW;
+        for (int u = 0; unit<KIND>(p, pair, pairs, u, w); ++u) {
             float acc[CH ? EW : 1];
 #pragma unroll
             for (int i = 0; i < (CH ? EW : 1); ++i) acc[i] = 0.f;
-            int k0 = w.k0;
             uint32_t d = 0;
             uint32_t release = 0;
-            do {
+            for (int left = CH ? max(1, (w.k1 - w.k0 + ch - 1) / ch) : 1; left > 0; --left) {
                 const int buf = it & 1;
                 // A wait that gives up ends no loop here: the warps' barriers stay matched, and what is
                 // left of the tiles goes by without waiting, with whatever the accumulators hold.
@@ -492,9 +507,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     if (lane == 0) arrive_cluster(release);
                 }
                 ++it;
-                k0 = CH ? k0 + ch : w.k1;
-            } while (k0 < w.k1);
-
+            }
+            // (found again: the sums above leave few registers)
+            int t = tid;
+            if (CH) {
+                asm volatile("" : "+r"(u));
+                unit<KIND>(p, pair, pairs, u, w);
+                asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+            }
+            const int quad = (t >> 5) & 3, quarter = ((t >> 5) - 2) >> 2, row = quad * 32 + (t & 31);
+            const bool lead = quad == 0 && (t & 31) == 0;  // of the quarter: its stores
+            const uint32_t stage = ring + STAGES * 2 * OPB + (KIND == K_LSE ? 0 : quarter * 2 * OUTB);
+            const int r0 = w.m * BM + (int)rank * HALF, r = r0 + row;
+            const int c0 = w.n * BN + quarter * EW;
+            // logits of fp32 inputs, and both gradients' sums, are 2^(exponents of the scalings) times too large
+            float f1 = 1.f, f2 = p.scale;
+            if (F32) {
+                const int we = exponent_for(__uint_as_float(__ldg(p.most)), 14);
+                if (KIND != K_GRAD) {
+                    // (beyond the range of one factor the logits are below 2^-80, or infinite)
+                    const int k = -we - (r < p.T ? __ldg(p.he + r) : 0);
+                    f2 = pow2(max(-126, min(127, k))) * p.scale;
+                } else if (!w.second) {
+                    if (r < p.T) f1 = pow2(-__ldg(p.pa + r));
+                    f2 = pow2(-we);
+                } else {
+                    f2 = pow2(-exponent_for(__uint_as_float(__ldg(p.most + 1)), 14));
+                }
+            }
             if (KIND == K_LSE) {
                 const bool real = r < p.T;
                 const int left = p.V - c0;
@@ -503,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 if constexpr (CH) {
 #pragma unroll
                     for (int i = 0; i < EW; ++i) {
-                        acc[i] = i < left ? acc[i] * p.scale : -INFINITY;
+                        acc[i] = i < left ? acc[i] * f2 : -INFINITY;
                         top = fmaxf(top, acc[i]);
                     }
                     if (o >= 0 && o < EW) {
@@ -539,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     lse = __ldg(p.lse + r);
                     g = tgt < 0 ? 0.f : tgt >= p.vocab ? NAN : __ldg(p.dloss + r) * p.scale;
                     tgt = tgt < 0 ? -1 : tgt - p.v0;
+                    if (F32) g *= pow2(__ldg(p.pa + r));
                 }
                 const bool live = KIND != K_P || g != 0.f;
                 float lo = 0.f;
@@ -550,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                         hrow = p.h + t * p.ldh;
                     }
                 }
-                constexpr int PARTS = KIND == K_P && F32 ? 3 : 1;
+                constexpr int PARTS = KIND == K_P && F32 ? 2 : 1;
                 const int out_cols = KIND == K_P ? p.V : p.W, out_rows = KIND == K_P ? p.T : p.V;
                 // the copies of the last tile have read their pieces
                 if (PARTS == 1) {
@@ -562,7 +603,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     float x[SC];
                     if constexpr (CH) {
 #pragma unroll
-                        for (int i = 0; i < SC; ++i) x[i] = acc[j + i];
+                        for (int i = 0; i < SC; ++i) {
+                            x[i] = acc[j + i];
+                            asm volatile("" : "+f"(x[i]));  // (one piece at a time: registers)
+                        }
                     } else {
                         tc::ld32(d + j, x);
                         if (j == EW - SC) {  // the tile is read
@@ -573,14 +617,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
                     if (KIND == K_P) {
 #pragma unroll
-                        for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], p.scale, -lse) * kLog2e) : 0.f;
+                        for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], f2, -lse) * kLog2e) : 0.f;
                         const int o = tgt < 0 ? -1 : tgt - (c0 + j);
                         if (o >= 0 && o < SC) {
                             float at = 0.f;
 #pragma unroll
                             for (int i = 0; i < SC; ++i) {
                                 sub_at(x[i], live ? g : 0.f, o, i);
-                                take_at(at, x[i], o, i);
+                                if (!F32) take_at(at, x[i], o, i);
                             }
                             if (!F32) p.lo[r] = at - __bfloat162float(__float2bfloat16_rn(at));
                         }
@@ -596,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
 #pragma unroll
                     for (int q = 0; q < PARTS; ++q) {
-                        unsigned char* const to = stage + ((j / SC * PARTS + q) & 1) * OUTB;
+                        const uint32_t to = stage + ((j / SC * PARTS + q) & 1) * OUTB;
                         if (PARTS > 1) {  // one piece may still be on its way, the other one
                             if (lead) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                             tc::bar_sync(2 + quarter, 128);
@@ -608,22 +652,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const int e = h * 8 + i * 2;
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(x[e], x[e + 1]);
-                                o32[i] = *reinterpret_cast<const uint32_t*>(&b);
                                 if (PARTS > 1) {
-                                    x[e] -= __uint_as_float(o32[i] << 16);
-                                    x[e + 1] -= __uint_as_float(o32[i] & 0xffff0000u);
+                                    const __half2 b = __floats2half2_rn(x[e], x[e + 1]);
+                                    o32[i] = *reinterpret_cast<const uint32_t*>(&b);
+                                    x[e] -= __low2float(b);
+                                    x[e + 1] -= __high2float(b);
+                                } else {
+                                    o32[i] = tc::pack_bf16x2(x[e], x[e + 1]);
                                 }
                             }
                             // rows of 64 bytes under the 64-byte swizzle
-                            *reinterpret_cast<uint4*>(to + row * 64 + ((h ^ ((row >> 1) & 3)) << 4)) = o4;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             to + row * 64 + ((h ^ ((row >> 1) & 3)) << 4)),
+                                         "r"(o4.x), "r"(o4.y), "r"(o4.z), "r"(o4.w)
+                                         : "memory");
                         }
                         if (PARTS > 1) {
                             tc::fence_async_smem();
                             tc::bar_sync(2 + quarter, 128);
                             if (lead) {
                                 // (a group is closed with or without a copy: the wait above counts them)
-                                if (c0 + j < out_cols && r0 < out_rows) store_box(&maps.out, c0 + j, r0, q, tc::smem_addr(to));
+                                if (c0 + j < out_cols && r0 < out_rows) store_box(&maps.out, c0 + j, r0, q, to);
                                 tc::bulk_commit();
                             }
                         }
@@ -634,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     tc::bar_sync(2 + quarter, 128);
                     if (lead && r0 < out_rows) {
                         for (int j = 0; j < EW; j += SC)
-                            if (c0 + j < out_cols) store_box(&maps.out, c0 + j, r0, 0, tc::smem_addr(stage + j / SC * OUTB));
+                            if (c0 + j < out_cols) store_box(&maps.out, c0 + j, r0, 0, stage + j / SC * OUTB);
                         tc::bulk_commit();
                     }
                 }
@@ -651,15 +700,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                         hrow = p.h + t * p.ldh;
                     }
                 }
+                constexpr int DC = CH ? 8 : 32;  // columns at a time
 #pragma unroll
-                for (int j = 0; j < EW; j += 32) {
-                    float x[32];
+                for (int j = 0; j < EW; j += DC) {
+                    float x[DC];
                     if constexpr (CH) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = acc[j + i];
+                        for (int i = 0; i < DC; ++i) {
+                            x[i] = acc[j + i];
+                            asm volatile("" : "+f"(x[i]));
+                        }
                     } else {
                         tc::ld32(d + j, x);
-                        if (j == EW - 32) {
+                        if (j == EW - DC) {
                             tc::fence_before();
                             __syncwarp();
                             if (lane == 0) arrive_cluster(release);
@@ -667,31 +720,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
                     const int col = c0 + j;
                     if (!live || col >= p.W) continue;
-                    if (w.k1 <= w.k0) {  // a split without steps: nothing was added up
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    for (int i = 0; i < DC; ++i) {
+                        if (F32) x[i] = x[i] * f1 * f2;
+                        if (w.k1 <= w.k0) x[i] = 0.f;  // a split without steps: nothing was added up
                     }
                     if (!w.second) {
                         float* q = p.acc + ((int64_t)w.split * p.T + r) * p.ldacc + col;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
+                        for (int i = 0; i < DC; i += 8)
                             if (col + i < p.ldacc) put8(q + i, x + i, p.add != 0);
                     } else if (F32) {
                         float* q = static_cast<float*>(p.dw) + r * p.lddw + col;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < DC; ++i)
                             if (col + i < p.W) q[i] = x[i];
                     } else {
                         __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.dw) + r * p.lddw + col;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < DC; ++i)
                             if (col + i < p.W)
                                 q[i] = __float2bfloat16_rn(hrow ? fmaf(lo, __bfloat162float(hrow[col + i]), x[i]) : x[i]);
                     }
                 }
             }
         }
-        if (lead) tc::bulk_wait();
+        if ((warp & 3) == 0 && lane == 0) tc::bulk_wait();  // the threads that stored
     }
     __syncwarp();
     tc::fence_before();
@@ -703,41 +757,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
 
 // ---- small kernels -----------------------------------------------------------
 
-// [rows][W] -> [parts][rows][ld]: bf16 as it is, fp32 in three bf16 parts that add up to
-// it; rows without a target are zero (0 times an infinity there would reach every weight's
-// gradient).  Columns of W and beyond are not written: no box reads them.
-template <typename E>
-__global__ void __launch_bounds__(256) pack_kernel(const E* __restrict__ x, int64_t ldx, int64_t rows, int W, int ld,
-                                                   const void* targets, int wide, int vocab, int* only,
-                                                   __nv_bfloat16* __restrict__ out) {
-    const int nv = (W + 7) / 8;
+__device__ __forceinline__ int64_t raw_target(const void* targets, int wide, int64_t r) {
+    return wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
+}
+
+// bf16 [rows][W] -> [rows][ld].  For the gradients (targets): tokens that are left out, or whose
+// dloss is zero, are rows of zeros (0 times an infinity there would reach every weight's
+// gradient), and `only` gets the token of every target that has just one.  Columns of W
+// and beyond are written as zeros.
+__global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t rows, int W,
+                                                   int ld, const void* targets, int wide, const float* dloss, int vocab,
+                                                   int* only, __nv_bfloat16* __restrict__ out) {
+    const int nv = ld / 8;
     const int64_t n = rows * nv;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / nv;
         const int c = (int)(i - r * nv) * 8;
         bool real = true;
         if (targets) {
-            const int64_t tgt =
-                wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
-            real = tgt >= 0;
+            const int64_t tgt = raw_target(targets, wide, r);
+            real = tgt >= 0 && __ldg(dloss + r) != 0.f;
             // the one token with a target; a second one makes it -2, whatever their order
-            if (only && c == 0 && real && tgt < vocab && atomicCAS(only + tgt, -1, (int)r) != -1) only[tgt] = -2;
+            if (c == 0 && real && tgt < vocab && atomicCAS(only + tgt, -1, (int)r) != -1) only[tgt] = -2;
         }
-        const E* s = x + r * ldx + c;
+        const __nv_bfloat16* s = x + r * ldx + c;
         float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = real && c + j < W ? Elem<E>::load(s + j) : 0.f;
+        for (int j = 0; j < 8; ++j) f[j] = real && c + j < W ? __bfloat162float(s[j]) : 0.f;
+        store8(out + r * ld + c, f);
+    }
+}
+
+// The scalings of fp32 inputs: a warp a row of h, then of w.  most[0]: the largest |w|;
+// with dloss most[1]: the largest |h_t| 2^-pa[t] over the tokens that count.
+__global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h, int64_t ldh, int T,
+                                                    const float* __restrict__ w, int64_t ldw, int V, int W,
+                                                    const void* targets, int wide, const float* dloss, float scale,
+                                                    int* he, int* pa, unsigned* most) {
+    const int lane = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * 8;
+    float wm = 0.f, hm = 0.f;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < (int64_t)T + V; r += step) {
+        const float* x = r < T ? h + r * ldh : w + (r - T) * ldw;
+        float m = 0.f;
+#pragma unroll 8
+        for (int c = lane; c < W; c += 32) {
+            const float a = fabsf(__ldg(x + c));
+            m = a > m ? a : m;  // (a NaN is left out)
+        }
+        if (r >= T) {
+            wm = fmaxf(wm, m);
+            continue;
+        }
 #pragma unroll
-        for (int q = 0; q < (sizeof(E) == 4 ? 3 : 1); ++q) {
-            store8(out + (q * rows + r) * ld + c, f);
-            if (sizeof(E) == 4) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float h = __bfloat162float(__float2bfloat16_rn(f[j]));
-                    f[j] = isfinite(h) ? f[j] - h : 0.f;
-                }
+        for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        if (lane == 0) {
+            he[r] = exponent_for(m, 14);
+            if (dloss) {
+                const bool real = raw_target(targets, wide, r) >= 0;
+                const int a = real ? exponent_for(fabsf(__ldg(dloss + r) * scale), 13) : 0;
+                pa[r] = a;
+                if (real && __ldg(dloss + r) != 0.f) hm = fmaxf(hm, m * pow2(-a));
             }
         }
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, k));
+    // (bits of numbers that are not negative are ordered as they are)
+    if (lane == 0 && wm > 0.f) atomicMax(most, __float_as_uint(wm));
+    if (lane == 0 && hm > 0.f) atomicMax(most + 1, __float_as_uint(hm));
+}
+
+// fp32 [rows][W] -> two fp16 parts [2][rows][ld] of its scaled values.  he: by its rows' own
+// exponents (logits' h); pa: by most[1]'s less the row's pa, zeros where a token does not
+// count (dw's h); neither: by most[0]'s (w).
+__global__ void __launch_bounds__(256) split_kernel(const float* __restrict__ x, int64_t ldx, int64_t rows, int W, int ld,
+                                                    const int* he, const int* pa, const unsigned* most,
+                                                    const void* targets, int wide, const float* dloss,
+                                                    __half* __restrict__ out) {
+    const int nv = ld / 8;
+    const int64_t n = rows * nv;
+    const int all = he ? 0 : exponent_for(__uint_as_float(__ldg(most + (pa ? 1 : 0))), 14);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / nv;
+        const int c = (int)(i - r * nv) * 8;
+        int k = all;
+        bool real = true;
+        if (he) k = __ldg(he + r);
+        if (pa) {
+            k -= __ldg(pa + r);
+            real = raw_target(targets, wide, r) >= 0 && __ldg(dloss + r) != 0.f;
+        }
+        // (up to 2^252: in two steps)
+        const float k1 = pow2(k / 2), k2 = pow2(k - k / 2);
+        const float* s = x + r * ldx + c;
+        uint4 hi, lo;
+        __half2* h2 = reinterpret_cast<__half2*>(&hi);
+        __half2* l2 = reinterpret_cast<__half2*>(&lo);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float a = real && c + j < W ? s[j] * k1 * k2 : 0.f, b = real && c + j + 1 < W ? s[j + 1] * k1 * k2 : 0.f;
+            const __half2 v = __floats2half2_rn(a, b);
+            const float va = __low2float(v), vb = __high2float(v);
+            h2[j / 2] = v;
+            l2[j / 2] = __floats2half2_rn(isfinite(va) ? a - va : 0.f, isfinite(vb) ? b - vb : 0.f);
+        }
+        *reinterpret_cast<uint4*>(out + r * ld + c) = hi;
+        *reinterpret_cast<uint4*>(out + (rows + r) * ld + c) = lo;
     }
 }
 
@@ -832,7 +958,7 @@ bool direct(gdn_dtype dt, int W) { return dt == GDN_BF16 && W % 8 == 0; }
 // columns take more), whole tiles
 constexpr size_t kPieceBytes = size_t(512) << 20;
 int piece_cols(int T, int V, gdn_dtype dt) {
-    int64_t c = (int64_t)(kPieceBytes / ((size_t)(dt == GDN_F32 ? 6 : 2) * (size_t)T)) / BN * BN;
+    int64_t c = (int64_t)(kPieceBytes / ((size_t)(dt == GDN_F32 ? 4 : 2) * (size_t)T)) / BN * BN;
     if (c < 1024) c = 1024;
     const int64_t all = div_up(V, BN) * BN;
     return (int)(c < all ? c : all);
@@ -848,13 +974,13 @@ int dh_splits(int T, int W, int cols) {
 }
 
 struct Plan {
-    size_t h, w, stat, at, p, acc, lo, only, total;
+    size_t h, hw, w, stat, at, p, acc, lo, only, he, pa, most, total;
     int piece, splits, ldacc;
 };
 Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     Plan l{};
     size_t o = 0;
-    const int parts = dt == GDN_F32 ? 3 : 1;
+    const int parts = dt == GDN_F32 ? 2 : 1;
     const int64_t ld = round8(W);
     const int64_t t = T > 0 ? T : 1;
     if (grad || !direct(dt, W)) {
@@ -864,6 +990,18 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     if (!direct(dt, W)) {
         l.w = o;
         o += up256((size_t)parts * V * ld * 2);
+    }
+    if (dt == GDN_F32) {
+        l.he = o;
+        o += up256(sizeof(int) * t);
+        l.most = o;
+        o += 256;
+        if (grad) {
+            l.pa = o;
+            o += up256(sizeof(int) * t);
+            l.hw = o;
+            o += up256((size_t)parts * t * ld * 2);
+        }
     }
     if (!grad) {
         l.stat = o;
@@ -954,17 +1092,34 @@ unsigned grid_for(int64_t n) {
     return (unsigned)(b < 1 ? 1 : b < most ? b : most);
 }
 
-gdn_status pack(const void* x, int64_t ldx, gdn_dtype dt, int64_t rows, int W, const void* targets, int wide, int vocab, int* only,
-                void* out, cudaStream_t s) {
+gdn_status pack(const void* x, int64_t ldx, int64_t rows, int W, const void* targets, int wide, const float* dloss,
+                int vocab, int* only, void* out, cudaStream_t s) {
     const int ld = round8(W);
-    const unsigned g = grid_for(rows * (ld / 8));
-    if (dt == GDN_F32)
-        pack_kernel<float><<<g, 256, 0, s>>>(static_cast<const float*>(x), ldx, rows, W, ld, targets, wide,
-                                             vocab, only, static_cast<__nv_bfloat16*>(out));
-    else
-        pack_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, W, ld, targets,
-                                                     wide, vocab, only, static_cast<__nv_bfloat16*>(out));
+    pack_kernel<<<grid_for(rows * (ld / 8)), 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, W, ld, targets,
+                                                          wide, dloss, vocab, only, static_cast<__nv_bfloat16*>(out));
     return check_launch("pack_kernel");
+}
+// fp32 inputs: their scalings, then their parts into the workspace
+gdn_status split(const void* h, int64_t ldh, int T, const void* w, int64_t ldw, int V, int W, const void* targets, int wide,
+                 const float* dloss, float scale, const Plan& l, char* ws, cudaStream_t s) {
+    const int ld = round8(W);
+    int* he = reinterpret_cast<int*>(ws + l.he);
+    int* pa = dloss ? reinterpret_cast<int*>(ws + l.pa) : nullptr;
+    unsigned* most = reinterpret_cast<unsigned*>(ws + l.most);
+    const float *hf = static_cast<const float*>(h), *wf = static_cast<const float*>(w);
+    if (cudaMemsetAsync(most, 0, 2 * sizeof(unsigned), s) != cudaSuccess) return check_launch("memset");
+    const int64_t blocks = div_up((int64_t)T + V, 8), wave = (int64_t)device_sm_count() * 8;
+    scale_kernel<<<(unsigned)(blocks < wave ? blocks : wave), 256, 0, s>>>(hf, ldh, T, wf, ldw, V, W, targets, wide, dloss,
+                                                                           scale, he, pa, most);
+    split_kernel<<<grid_for((int64_t)V * (ld / 8)), 256, 0, s>>>(wf, ldw, V, W, ld, nullptr, nullptr, most, nullptr, 0,
+                                                                 nullptr, reinterpret_cast<__half*>(ws + l.w));
+    const unsigned g = grid_for((int64_t)T * (ld / 8));
+    split_kernel<<<g, 256, 0, s>>>(hf, ldh, T, W, ld, he, nullptr, most, nullptr, 0, nullptr,
+                                   reinterpret_cast<__half*>(ws + l.h));
+    if (dloss)
+        split_kernel<<<g, 256, 0, s>>>(hf, ldh, T, W, ld, nullptr, pa, most, targets, wide, dloss,
+                                       reinterpret_cast<__half*>(ws + l.hw));
+    return check_launch("split_kernel");
 }
 
 // What a product reads: the array itself, or its packed copy
@@ -1034,13 +1189,17 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     if (!loss || !lse) return fail(GDN_ERR_INVALID_ARG, "loss or lse is NULL");
     cudaStream_t s = (cudaStream_t)stream;
     char* ws = static_cast<char*>(workspace);
-    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 3 : 1;
+    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 2 : 1;
     Operand H{h, ldh}, Wt{w, ldw};
     if (!direct(dtype, width)) {
         H = {ws + l.h, round8(width)};
         Wt = {ws + l.w, round8(width)};
-        if ((st = pack(h, ldh, dtype, T, width, nullptr, 0, 0, nullptr, ws + l.h, s)) != GDN_OK) return st;
-        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, 0, nullptr, ws + l.w, s)) != GDN_OK) return st;
+        if (dtype == GDN_F32) {
+            st = split(h, ldh, T, w, ldw, vocab, width, nullptr, 0, nullptr, scale, l, ws, s);
+        } else if ((st = pack(h, ldh, T, width, nullptr, 0, nullptr, 0, nullptr, ws + l.h, s)) == GDN_OK) {
+            st = pack(w, ldw, vocab, width, nullptr, 0, nullptr, 0, nullptr, ws + l.w, s);
+        }
+        if (st != GDN_OK) return st;
     }
     Maps m{};
     if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
@@ -1050,9 +1209,11 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     p.nt = (int)div_up(vocab, BN);
     p.group = group_rows(p.mt, width, parts);
     p.kb = (int)div_up(width, BK);
-    p.f32 = parts == 3;
+    p.f32 = parts == 2;
     p.T = T; p.V = p.vocab = vocab; p.W = width; p.scale = scale;
     p.targets = targets; p.wide = wide;
+    p.he = reinterpret_cast<int*>(ws + l.he);
+    p.most = reinterpret_cast<unsigned*>(ws + l.most);
     p.stat = reinterpret_cast<float2*>(ws + l.stat);
     p.at = reinterpret_cast<float*>(ws + l.at);
     if ((st = launch_gemm<K_LSE>(p, m, s)) != GDN_OK) return st;
@@ -1078,28 +1239,33 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
     if (!dloss || !lse || !dh || lddh < width)
         return fail(GDN_ERR_INVALID_ARG, "dloss, lse or dh is NULL, or dh's row stride < width=%d", width);
     char* ws = static_cast<char*>(workspace);
-    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 3 : 1;
+    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 2 : 1;
     const int ldp = round8(width);
     int* only = nullptr;
-    if (dtype == GDN_BF16) {
+    Operand H{ws + l.h, ldp}, Hw{ws + (dtype == GDN_F32 ? l.hw : l.h), ldp}, Wt{w, ldw};
+    if (!direct(dtype, width)) Wt = {ws + l.w, ldp};
+    if (dtype == GDN_F32) {
+        if ((st = split(h, ldh, T, w, ldw, vocab, width, targets, wide, dloss, scale, l, ws, s)) != GDN_OK) return st;
+    } else {
         only = reinterpret_cast<int*>(ws + l.only);
         if (cudaMemsetAsync(only, 0xff, sizeof(int) * (size_t)vocab, s) != cudaSuccess) return check_launch("memset");
-    }
-    if ((st = pack(h, ldh, dtype, T, width, targets, wide, vocab, only, ws + l.h, s)) != GDN_OK) return st;
-    Operand H{ws + l.h, ldp}, Wt{w, ldw};
-    if (!direct(dtype, width)) {
-        Wt = {ws + l.w, ldp};
-        if ((st = pack(w, ldw, dtype, vocab, width, nullptr, 0, 0, nullptr, ws + l.w, s)) != GDN_OK) return st;
+        if ((st = pack(h, ldh, T, width, targets, wide, dloss, vocab, only, ws + l.h, s)) != GDN_OK) return st;
+        if (!direct(dtype, width) &&
+            (st = pack(w, ldw, vocab, width, nullptr, 0, nullptr, 0, nullptr, ws + l.w, s)) != GDN_OK)
+            return st;
     }
     const bool store = dtype == GDN_BF16 && (reinterpret_cast<uintptr_t>(dw) & 15u) == 0 && lddw % 8 == 0;
     GemmParams p{};
     p.mt = (int)div_up(T, BM);
     p.group = group_rows(p.mt, width, parts);
-    p.f32 = parts == 3;
+    p.f32 = parts == 2;
     p.T = T; p.W = width; p.vocab = vocab; p.scale = scale;
     p.targets = targets; p.wide = wide; p.lse = lse; p.dloss = dloss;
     p.lo = reinterpret_cast<float*>(ws + l.lo);
     p.only = only;
+    p.he = reinterpret_cast<int*>(ws + l.he);
+    p.pa = reinterpret_cast<int*>(ws + l.pa);
+    p.most = reinterpret_cast<unsigned*>(ws + l.most);
     p.h = reinterpret_cast<const __nv_bfloat16*>(ws + l.h); p.ldh = ldp;
     for (int v0 = 0; v0 < vocab; v0 += l.piece) {
         const int cols = vocab - v0 < l.piece ? vocab - v0 : l.piece;
@@ -1122,7 +1288,7 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         if ((st = make_map3(&m.a, P, l.piece, cols, T, parts, HALF)) != GDN_OK) return st;
         if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, 64)) != GDN_OK) return st;
         if ((st = make_map3(&m.a2, P, l.piece, cols, T, parts, 64)) != GDN_OK) return st;
-        if ((st = make_map3(&m.b2, H.base, H.ld, width, T, parts, 64)) != GDN_OK) return st;
+        if ((st = make_map3(&m.b2, Hw.base, Hw.ld, width, T, parts, 64)) != GDN_OK) return st;
         char* dwp = static_cast<char*>(dw) + e * (int64_t)v0 * lddw;
         if (store && (st = make_map_rows(&m.out, dwp, lddw, width, cols, cols, 1, HALF, SC)) != GDN_OK) return st;
         p.nt = (int)div_up(width, BN);
