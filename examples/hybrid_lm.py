@@ -4,10 +4,10 @@ DeltaNet block with block norms between them, trained and served.
     python examples/hybrid_lm.py
 
 Training runs packed sequences through the selective scan blocks with the
-kernels' own gradients (three autograd functions); serving feeds a batch of
-prompts of different lengths once, keeps every layer's states in a cache of
-slots and continues token by token.  fp32, so that prompt and single tokens can
-be compared closely.
+kernels' own gradients (five autograd functions), from the embedding to the loss,
+whose logits are never kept; serving feeds a batch of prompts of different lengths
+once, keeps every layer's states in a cache of slots and continues token by token.
+fp32, so that prompt and single tokens can be compared closely.
 """
 from __future__ import annotations
 
@@ -15,7 +15,6 @@ import os
 import sys
 
 import torch
-import torch.nn.functional as F
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import linear_attention_sequence_device_gb300 as g  # noqa: E402
@@ -65,6 +64,35 @@ class BlockNorm(torch.autograd.Function):
         o, res_out, w_pre, w_post, gate, scale = ctx.saved_tensors
         r = g.gdn_block_norm_bwd(dy, dres, o, res_out, w_pre, w_post=w_post, gate=gate, scale=scale)
         return r["do"], r["dres"], r["dw_pre"].to(w_pre.dtype), r["dw_post"].to(w_post.dtype), r["dgate"], r["dscale"]
+
+
+class Embed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, table):
+        ctx.save_for_backward(tokens)
+        ctx.vocab = table.shape[0]
+        return g.gdn_embed_fwd(tokens, table)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return None, g.gdn_embed_bwd(dy.contiguous(), *ctx.saved_tensors, ctx.vocab)
+
+
+class VocabLoss(torch.autograd.Function):
+    """Cross entropy of every token from hidden states and output weights."""
+
+    @staticmethod
+    def forward(ctx, h, w, targets, scale):
+        loss, lse = g.gdn_vocab_loss_fwd(h, w, targets, scale=scale)
+        ctx.save_for_backward(h, w, targets, lse)
+        ctx.scale = scale
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        h, w, targets, lse = ctx.saved_tensors
+        r = g.gdn_vocab_loss_bwd(dloss.contiguous(), h, w, targets, lse, scale=ctx.scale)
+        return r["dh"], r["dw"], None, None
 
 
 # ---------------------------------------------------------------------------
@@ -125,7 +153,7 @@ class SsmBlock:
 
 class GdnBlock:
     """The Gated DeltaNet layer: its prompt is one gdn_layer_fwd; a single token is
-    the conv's step and the chunk kernel on sequences of one token."""
+    the conv's step and the layer's."""
 
     def __init__(self, width, q, H=4, d=32, K=4):
         rn = lambda *s, std: torch.randn(*s, generator=q, device="cuda") * std
@@ -153,12 +181,8 @@ class GdnBlock:
         p, H, d, n = self.p, self.H, self.d, len(x)
         ab, z = x @ p["w_ab"].t(), (x @ p["w_z"].t()).view(n, H, d)
         qkv = g.gdn_ssm_conv_step(x @ p["w_in"].t(), p["conv_w"], None, c["conv"], src=slots, dst=slots)
-        q, k, v = (t.view(n, H, d) for t in qkv.split(H * d, 1))
-        gate = -torch.exp(p["A_log"]) * F.softplus(ab[:, :H] + p["dt_bias"])
-        one = torch.arange(n + 1, dtype=torch.int32, device="cuda")
-        o, S = g.gdn_chunk_fwd(q, k, v, gate, torch.sigmoid(ab[:, H:]), one, h0=c["S"][slots.long()], l2norm=True)
-        c["S"][slots.long()] = S
-        y = p["norm_w"] * o * torch.rsqrt(o.square().mean(-1, keepdim=True) + 1e-6) * F.silu(z)
+        y = g.gdn_layer_step(qkv, ab[:, :H], ab[:, H:], p["A_log"], p["dt_bias"], z, p["norm_w"], c["S"], H, H, d, d,
+                             src=slots, dst=slots)
         return y.reshape(n, H * d) @ p["w_out"].t()
 
 
@@ -177,19 +201,31 @@ class HybridLM:
         return ([self.embed, self.last] + [t for b in self.blocks for t in b.p.values()] +
                 [t for n in self.norms for t in n.values()])
 
-    def _walk(self, tokens, mix, norm):
+    def _walk(self, tokens, mix, norm, embed=g.gdn_embed_fwd):
         """Embedding, blocks and the norms between them; one block norm call per block."""
-        res = self.embed[tokens]
+        res = embed(tokens, self.embed)
         x = res * torch.rsqrt(res.square().mean(1, keepdim=True) + 1e-6) * self.norms[0]["pre"]
         for i, b in enumerate(self.blocks):
             n = self.norms[i]
             nxt = self.norms[i + 1]["pre"] if i + 1 < len(self.blocks) else self.last
             x, res = norm(mix(i, b, x), res, nxt, n["post"], x @ n["w_gate"].t(), n["scale"])
-        return x @ self.embed.t() * self.embed.shape[1] ** -0.5
+        return x
+
+    @property
+    def _scale(self):
+        return self.embed.shape[1] ** -0.5  # of the logits: the embedding has unit variance
+
+    def _train(self, tokens, cu):
+        return self._walk(tokens, lambda i, b, x: b.train(x, cu), BlockNorm.apply, Embed.apply)
 
     def logits(self, tokens, cu):
         """Training logits of packed sequences (selective scan blocks only)."""
-        return self._walk(tokens, lambda i, b, x: b.train(x, cu), BlockNorm.apply)
+        return self._train(tokens, cu) @ self.embed.t() * self._scale
+
+    def loss(self, tokens, targets, cu):
+        """Mean cross entropy of the targets that are not negative, without the logits."""
+        loss = VocabLoss.apply(self._train(tokens, cu), self.embed, targets, self._scale)
+        return loss.sum() / (targets >= 0).sum()
 
     def caches(self, slots):
         return [b.cache(slots) for b in self.blocks]
@@ -200,11 +236,13 @@ class HybridLM:
 
     def prompt(self, tokens, cu, caches, slots):
         """Logits of every prompt token; the states after each prompt go into its slot."""
-        return self._walk(tokens, lambda i, b, x: b.prompt(x, cu, caches[i], slots), self._norm)
+        x = self._walk(tokens, lambda i, b, x: b.prompt(x, cu, caches[i], slots), self._norm)
+        return x @ self.embed.t() * self._scale
 
     def step(self, tokens, caches, slots):
         """Logits of one token per request; its slots' states move on by one token."""
-        return self._walk(tokens, lambda i, b, x: b.step(x, caches[i], slots), self._norm)
+        x = self._walk(tokens, lambda i, b, x: b.step(x, caches[i], slots), self._norm)
+        return x @ self.embed.t() * self._scale
 
 
 def offsets(lens):
@@ -245,7 +283,7 @@ def train(steps=30, seed=0):
     x, y, cu = torch.cat([s[:-1] for s in seqs]), torch.cat([s[1:] for s in seqs]), offsets(lens)
     losses = []
     for _ in range(steps):
-        loss = F.cross_entropy(m.logits(x, cu), y)
+        loss = m.loss(x, y, cu)
         opt.zero_grad()
         loss.backward()
         opt.step()
