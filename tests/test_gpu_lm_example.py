@@ -42,7 +42,7 @@ def test_loss_and_its_gradient_are_those_of_the_logits(lm):
     ga = torch.autograd.grad(a, ps)
     b = torch.nn.functional.cross_entropy(m.logits(x, cu), y, ignore_index=-100)
     gb = torch.autograd.grad(b, ps)
-    assert abs(float(a - b)) <= 1e-5 * float(b)
+    assert abs(float((a - b).detach())) <= 1e-5 * float(b.detach())
     for u, v in zip(ga, gb):
         assert float((u - v).norm()) <= 1e-4 * float(v.norm()) + 1e-7
 
