@@ -704,7 +704,7 @@ gdn_status gdn_layer_step(const void *x, int64_t ldx, const void *a, int64_t lda
 gdn_status gdn_embed_fwd(const void *tokens, int32_t index_bits, const void *table, int64_t ldt,
                          gdn_dtype dtype, int32_t vocab, int32_t T, int32_t width, float scale,
                          void *y, int64_t ldy, void *stream);
-size_t gdn_embed_bwd_workspace_size(int32_t T, int32_t width);
+size_t gdn_embed_bwd_workspace_size(int32_t T, int32_t vocab, int32_t width);
 gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const void *tokens,
                          int32_t index_bits, int32_t vocab, int32_t T, int32_t width, float scale,
                          int32_t accumulate, void *dtable, int64_t ldd, void *workspace,

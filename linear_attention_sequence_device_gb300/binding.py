@@ -101,7 +101,7 @@ SIGNATURES = {
     "gdn_layer_step": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _vp, _vp, _i64, _vp, _f32,
                                       _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i32, _vp, _vp, _vp, _vp]),
     "gdn_embed_fwd": (ctypes.c_int, [_vp, _i32, _vp, _i64, ctypes.c_int, _i32, _i32, _i32, _f32, _vp, _i64, _vp]),
-    "gdn_embed_bwd_workspace_size": (_sz, [_i32, _i32]),
+    "gdn_embed_bwd_workspace_size": (_sz, [_i32, _i32, _i32]),
     "gdn_embed_bwd": (ctypes.c_int, [_vp, _i64, ctypes.c_int, _vp, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _i64, _vp,
                                      _sz, _vp]),
     "gdn_vocab_loss_fwd_workspace_size": (_sz, [_i32, _i32, _i32, ctypes.c_int]),

@@ -114,6 +114,39 @@ __global__ void __launch_bounds__(FT) embed_fwd_kernel(const I* __restrict__ tok
     }
 }
 
+// ---- rows of zeros ---------------------------------------------------------
+
+constexpr int kMaxPiece = 256;  // rows of a piece, rows filled by a block
+
+// zeros, in 16-byte accesses but for the ends, by the NT threads of a block
+template <typename E, int NT>
+__device__ __forceinline__ void fill_zero(E* p, int64_t n) {
+    constexpr int N = 16 / sizeof(E);
+    int64_t head = (16 - (int64_t)(reinterpret_cast<uintptr_t>(p) & 15u)) % 16 / (int)sizeof(E);
+    if (head > n) head = n;
+    for (int64_t i = threadIdx.x; i < head; i += NT) p[i] = Elem<E>::from_f(0.f);
+    p += head;
+    n -= head;
+    uint4* q = reinterpret_cast<uint4*>(p);
+    for (int64_t i = threadIdx.x; i < n / N; i += NT) __stcs(q + i, make_uint4(0u, 0u, 0u, 0u));
+    for (int64_t i = n / N * N + threadIdx.x; i < n; i += NT) p[i] = Elem<E>::from_f(0.f);
+}
+// the rows [v0, v1) that do not occur; those without a gap between them as one
+template <typename E, int NT, typename F>
+__device__ __forceinline__ void fill_rows(E* out, int64_t ldo, int W, int v0, int v1, F occurs) {
+    for (int v = v0; v < v1;) {
+        if (occurs(v)) {
+            ++v;
+            continue;
+        }
+        int w = v + 1;
+        if (ldo == W)
+            while (w < v1 && !occurs(w)) ++w;
+        fill_zero<E, NT>(out + v * ldo, (int64_t)(w - v) * W);
+        v = w;
+    }
+}
+
 // ---- sort ------------------------------------------------------------------
 
 // Keys are the tokens, `vocab` for a padded one, which ends up behind the others.  A pass
@@ -131,7 +164,13 @@ struct SortArgs {
     const int* key_in; const int* pos_in;
     int* key_out; int* pos_out;
     int* count;            // [blocks][kBins] counts of this pass
-    int T, vocab, per, shift;
+    int T, vocab, per, shift, blocks;
+    // beside it, rows [v0, v1) of the gradient that no token has are filled with zeros, zrows a
+    // block; hit: a byte a token, 1 where it occurs
+    unsigned char* hit;
+    int v0, v1, zrows, W;
+    int64_t ldo;
+    void* out;
 };
 
 template <typename I>
@@ -147,7 +186,11 @@ __global__ void __launch_bounds__(ST) sort_count_kernel(const SortArgs a) {
     for (int i = threadIdx.x; i < kBins; i += ST) hist[i] = 0;
     __syncthreads();
     const int lo = blockIdx.x * a.per, hi = min(a.T, lo + a.per);
-    for (int i = lo + threadIdx.x; i < hi; i += ST) atomicAdd(&hist[(sort_key<I>(a, i) >> a.shift) & (kBins - 1)], 1);
+    for (int i = lo + threadIdx.x; i < hi; i += ST) {
+        const int key = sort_key<I>(a, i);
+        atomicAdd(&hist[(key >> a.shift) & (kBins - 1)], 1);
+        if (a.hit && key < a.vocab && !__ldcg(a.hit + key)) a.hit[key] = 1;  // (a frequent token once, or nearly)
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += ST) a.count[blockIdx.x * kBins + i] = hist[i];
 }
@@ -170,8 +213,16 @@ __device__ __forceinline__ int exclusive_sum(int v, int* warp_sums) {
     return before + x - v;
 }
 
-template <typename I>
+template <typename I, typename E>
 __global__ void __launch_bounds__(ST) sort_place_kernel(const SortArgs a) {
+    if ((int)blockIdx.x >= a.blocks) {
+        __shared__ unsigned char hit[kMaxPiece];
+        const int v0 = a.v0 + ((int)blockIdx.x - a.blocks) * a.zrows, v1 = min(a.v1, v0 + a.zrows);
+        for (int v = v0 + threadIdx.x; v < v1; v += ST) hit[v - v0] = a.hit[v];
+        __syncthreads();
+        fill_rows<E, ST>(static_cast<E*>(a.out), a.ldo, a.W, v0, v1, [&](int v) { return hit[v - v0] != 0; });
+        return;
+    }
     __shared__ int base[kBins];       // where this block's next row of a digit goes
     __shared__ int wc[SW][kBins];     // a warp's rows of a digit in this step, then where they begin
     __shared__ int warp_sums[SW];
@@ -184,7 +235,7 @@ __global__ void __launch_bounds__(ST) sort_place_kernel(const SortArgs a) {
             const int d = tid * (kBins / ST) + j;
             all[j] = mine[j] = 0;
 #pragma unroll 16
-            for (int b = 0; b < (int)gridDim.x; ++b) {
+            for (int b = 0; b < a.blocks; ++b) {
                 const int c = __ldg(a.count + b * kBins + d);
                 all[j] += c;
                 mine[j] += b < (int)blockIdx.x ? c : 0;
@@ -321,8 +372,6 @@ __global__ void __launch_bounds__(ST) sort_small_kernel(const SortArgs a, int bi
 // ---- sums of sorted rows ---------------------------------------------------
 
 constexpr int PT = 128;       // threads of a block; each has U vectors of a row, PT vectors apart
-constexpr int kMaxPiece = 256;
-
 struct SumArgs {
     const int* key; const int* pos;
     int T, vocab, W, piece, pieces, zrows;
@@ -398,20 +447,6 @@ __device__ __forceinline__ bool one_piece_has(const SumArgs& a, int v, int r) {
            (r + a.piece >= a.T || __ldg(a.key + r + a.piece) != v);
 }
 
-// zeros, in 16-byte accesses but for the ends
-template <typename E>
-__device__ __forceinline__ void fill_zero(E* p, int64_t n) {
-    constexpr int N = 16 / sizeof(E);
-    int64_t head = (16 - (int64_t)(reinterpret_cast<uintptr_t>(p) & 15u)) % 16 / (int)sizeof(E);
-    if (head > n) head = n;
-    for (int64_t i = threadIdx.x; i < head; i += PT) p[i] = Elem<E>::from_f(0.f);
-    p += head;
-    n -= head;
-    uint4* q = reinterpret_cast<uint4*>(p);
-    for (int64_t i = threadIdx.x; i < n / N; i += PT) __stcs(q + i, make_uint4(0u, 0u, 0u, 0u));
-    for (int64_t i = n / N * N + threadIdx.x; i < n; i += PT) p[i] = Elem<E>::from_f(0.f);
-}
-
 // Blocks [0, pieces ny) add up the rows of a piece's tokens, PT * U vectors of columns
 // each; the others fill the rows of tokens that do not occur, zrows each.
 template <typename E, int VEC, int U>
@@ -435,18 +470,8 @@ __global__ void __launch_bounds__(PT) embed_sum_kernel(const SumArgs a, int ny) 
             if (i == lo || __ldg(a.key + i - 1) != v) atomicOr(&hit[(v - v0) >> 5], 1u << ((v - v0) & 31));
         }
         __syncthreads();
-        auto occurs = [&](int v) { return (hit[(v - v0) >> 5] >> ((v - v0) & 31) & 1u) != 0; };
-        for (int v = v0; v < v1;) {
-            if (occurs(v)) {
-                ++v;
-                continue;
-            }
-            int w = v + 1;  // rows without a gap between them are filled as one
-            if (a.ldo == a.W)
-                while (w < v1 && !occurs(w)) ++w;
-            fill_zero(static_cast<E*>(a.out) + v * a.ldo, (int64_t)(w - v) * a.W);
-            v = w;
-        }
+        fill_rows<E, PT>(static_cast<E*>(a.out), a.ldo, a.W, v0, v1,
+                         [&](int v) { return (hit[(v - v0) >> 5] >> ((v - v0) & 31) & 1u) != 0; });
         return;
     }
     const int piece = blockIdx.x / ny, c0 = ((blockIdx.x - piece * ny) * U * PT + threadIdx.x) * VEC;  // vector u: + u PT VEC
@@ -607,9 +632,9 @@ int piece_rows(int64_t T) {
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 struct Layout {
-    size_t key[2], pos[2], count, part, total;
+    size_t key[2], pos[2], count, part, hit, total;
 };
-Layout layout(int64_t T, int W) {
+Layout layout(int64_t T, int W, int vocab) {
     Layout l{};
     size_t at = 0;
     const size_t row = round256(4 * (size_t)T);
@@ -623,35 +648,54 @@ Layout layout(int64_t T, int W) {
     if (pieces > kPieces + 1) pieces = kPieces + 1;
     if (pieces < T / kMaxPiece + 1) pieces = T / kMaxPiece + 1;
     l.part = at; at += round256(sizeof(float) * 2 * (size_t)pieces * W);
+    l.hit = at; at += round256((size_t)vocab);
     l.total = at;
     return l;
 }
 
-template <typename I>
-gdn_status sort_tokens(const void* tokens, int T, int vocab, char* ws, const Layout& l, int& which, cudaStream_t s) {
+// Sorts, and for more than SMALL tokens fills the rows that do not occur: a share beside
+// each pass, whose few blocks leave the GPU to it (65536 tokens into 131072 rows of 2048:
+// 183 us with the filling beside the sums, 155 so).
+template <typename I, typename E>
+gdn_status sort_tokens(const void* tokens, const SumArgs& sum, char* ws, const Layout& l, int& which, bool& filled,
+                       cudaStream_t s) {
+    const int T = sum.T, vocab = sum.vocab;
     int bits = 1;
     while (bits < 31 && ((int64_t)1 << bits) <= vocab) ++bits;  // keys up to vocab
     SortArgs a{};
     a.tokens = tokens;
     a.T = T;
     a.vocab = vocab;
+    filled = false;
+    which = 0;
     if (T <= SMALL) {
         a.key_out = reinterpret_cast<int*>(ws + l.key[0]);
         a.pos_out = reinterpret_cast<int*>(ws + l.pos[0]);
-        which = 0;
         sort_small_kernel<I><<<1, ST, 0, s>>>(a, bits);
         return check_launch("sort_small_kernel");
     }
-    const int blocks = sort_blocks(T);
-    a.per = (T + blocks - 1) / blocks;
+    a.blocks = sort_blocks(T);
+    a.per = (T + a.blocks - 1) / a.blocks;
     a.count = reinterpret_cast<int*>(ws + l.count);
-    which = 0;
-    for (int shift = 0; shift < bits; shift += kBits) {
-        a.shift = shift;
+    const int passes = (bits + kBits - 1) / kBits;
+    if (!sum.into) {
+        filled = true;
+        a.hit = reinterpret_cast<unsigned char*>(ws + l.hit);
+        a.zrows = sum.zrows; a.W = sum.W; a.ldo = sum.ldo; a.out = sum.out;
+        if (cudaMemsetAsync(a.hit, 0, vocab, s) != cudaSuccess) return check_launch("memset");
+    }
+    for (int p = 0; p < passes; ++p) {
+        a.shift = p * kBits;
         a.key_out = reinterpret_cast<int*>(ws + l.key[which]);
         a.pos_out = reinterpret_cast<int*>(ws + l.pos[which]);
-        sort_count_kernel<I><<<blocks, ST, 0, s>>>(a);
-        sort_place_kernel<I><<<blocks, ST, 0, s>>>(a);
+        sort_count_kernel<I><<<a.blocks, ST, 0, s>>>(a);
+        int fill = 0;
+        if (filled) {
+            a.v0 = (int)((int64_t)vocab * p / passes);
+            a.v1 = (int)((int64_t)vocab * (p + 1) / passes);
+            fill = (a.v1 - a.v0 + a.zrows - 1) / a.zrows;
+        }
+        sort_place_kernel<I, E><<<a.blocks + fill, ST, 0, s>>>(a);
         a.key_in = a.key_out;
         a.pos_in = a.pos_out;
         which ^= 1;
@@ -661,11 +705,11 @@ gdn_status sort_tokens(const void* tokens, int T, int vocab, char* ws, const Lay
 }
 
 template <typename E, int VEC>
-gdn_status run_sum(const SumArgs& a, cudaStream_t s) {
+gdn_status run_sum(const SumArgs& a, bool filled, cudaStream_t s) {
     // single elements: eight of a thread, or the blocks would be small
     constexpr int U = VEC == 1 ? 8 : 1;
     const unsigned ny = (unsigned)((a.W + PT * VEC * U - 1) / (PT * VEC * U));
-    const int64_t blocks = (int64_t)a.pieces * ny + (a.into ? 0 : (a.vocab + a.zrows - 1) / a.zrows);
+    const int64_t blocks = (int64_t)a.pieces * ny + (a.into || filled ? 0 : (a.vocab + a.zrows - 1) / a.zrows);
     if (blocks > 0x7fffffff) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows of %d elements", a.T, a.W);
     if (blocks > 0) {
         embed_sum_kernel<E, VEC, U><<<(unsigned)blocks, PT, 0, s>>>(a, (int)ny);
@@ -740,9 +784,9 @@ gdn_status gdn_embed_fwd(const void* tokens, int32_t index_bits, const void* tab
                : run_fwd<float, 1>(w64, tokens, table, ldt, vocab, T, width, scale, y, ldy, s);
 }
 
-size_t gdn_embed_bwd_workspace_size(int32_t T, int32_t width) {
-    if (T < 0 || T > kMaxTokens || width < 1 || width > (1 << 20)) return 0;
-    return layout(T, width).total;
+size_t gdn_embed_bwd_workspace_size(int32_t T, int32_t vocab, int32_t width) {
+    if (T < 0 || T > kMaxTokens || width < 1 || width > (1 << 20) || vocab < 0 || vocab > (1 << 30)) return 0;
+    return layout(T, width, vocab).total;
 }
 
 gdn_status gdn_embed_bwd(const void* dy, int64_t lddy, gdn_dtype dtype, const void* tokens, int32_t index_bits,
@@ -754,22 +798,14 @@ gdn_status gdn_embed_bwd(const void* dy, int64_t lddy, gdn_dtype dtype, const vo
     if (!dtable || (T > 0 && !dy)) return fail(GDN_ERR_INVALID_ARG, "dy or dtable is NULL");
     if (ldd < width || (T > 0 && lddy < width))
         return fail(GDN_ERR_INVALID_ARG, "row strides of dy and dtable must be >= width=%d", width);
-    const Layout l = layout(T, width);
+    const Layout l = layout(T, width, vocab);
     if (!workspace || workspace_bytes < l.total)
         return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes < required %zu", workspace ? workspace_bytes : 0, l.total);
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
         return fail(GDN_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     cudaStream_t s = (cudaStream_t)stream;
     char* ws = static_cast<char*>(workspace);
-    int which = 0;
-    if (T > 0) {
-        st = index_bits == 64 ? sort_tokens<int64_t>(tokens, T, vocab, ws, l, which, s)
-                              : sort_tokens<int32_t>(tokens, T, vocab, ws, l, which, s);
-        if (st != GDN_OK) return st;
-    }
     SumArgs a{};
-    a.key = reinterpret_cast<int*>(ws + l.key[which]);
-    a.pos = reinterpret_cast<int*>(ws + l.pos[which]);
     a.T = T; a.vocab = vocab; a.W = width; a.piece = piece_rows(T);
     a.pieces = (T + a.piece - 1) / a.piece;
     // rows of about 64 KB together
@@ -777,10 +813,25 @@ gdn_status gdn_embed_bwd(const void* dy, int64_t lddy, gdn_dtype dtype, const vo
     a.zrows = (int)(zrows < 1 ? 1 : zrows > kMaxPiece ? kMaxPiece : zrows);
     a.dy = dy; a.lddy = lddy; a.ldo = ldd; a.scale = scale; a.out = dtable; a.into = accumulate != 0;
     a.part = reinterpret_cast<float*>(ws + l.part);
+    int which = 0;
+    bool filled = false;
+    if (T > 0) {
+        const bool wide = index_bits == 64;
+        if (dtype == GDN_BF16)
+            st = wide ? sort_tokens<int64_t, __nv_bfloat16>(tokens, a, ws, l, which, filled, s)
+                      : sort_tokens<int32_t, __nv_bfloat16>(tokens, a, ws, l, which, filled, s);
+        else
+            st = wide ? sort_tokens<int64_t, float>(tokens, a, ws, l, which, filled, s)
+                      : sort_tokens<int32_t, float>(tokens, a, ws, l, which, filled, s);
+        if (st != GDN_OK) return st;
+    }
+    a.key = reinterpret_cast<int*>(ws + l.key[which]);
+    a.pos = reinterpret_cast<int*>(ws + l.pos[which]);
     if (dtype == GDN_BF16)
-        return width % 8 == 0 && al(dy, lddy, 2) && al(dtable, ldd, 2) ? run_sum<__nv_bfloat16, 8>(a, s)
-                                                                       : run_sum<__nv_bfloat16, 1>(a, s);
-    return width % 4 == 0 && al(dy, lddy, 4) && al(dtable, ldd, 4) ? run_sum<float, 4>(a, s) : run_sum<float, 1>(a, s);
+        return width % 8 == 0 && al(dy, lddy, 2) && al(dtable, ldd, 2) ? run_sum<__nv_bfloat16, 8>(a, filled, s)
+                                                                       : run_sum<__nv_bfloat16, 1>(a, filled, s);
+    return width % 4 == 0 && al(dy, lddy, 4) && al(dtable, ldd, 4) ? run_sum<float, 4>(a, filled, s)
+                                                                   : run_sum<float, 1>(a, filled, s);
 }
 
 }  // extern "C"

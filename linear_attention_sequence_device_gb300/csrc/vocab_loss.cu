@@ -313,17 +313,40 @@ __device__ __forceinline__ void sub_at(float& x, float g, int o, int i) {
     asm volatile("{\n .reg .pred p;\n setp.eq.s32 p, %2, %3;\n @p sub.f32 %0, %0, %1;\n}\n" : "+f"(x) : "f"(g), "r"(o), "r"(i));
 }
 
-// eight fp32 values of a row, added to what is there or in its place
-__device__ __forceinline__ void put8(float* q, const float* v, bool add) {
-    float4 a = make_float4(v[0], v[1], v[2], v[3]), b = make_float4(v[4], v[5], v[6], v[7]);
-    float4* o = reinterpret_cast<float4*>(q);
-    if (add) {
-        const float4 c = o[0], d = o[1];
-        a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
-        b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+// A warp's 32 rows and the 32 columns behind j of its quarter, staged at `mine`, to dh's sums
+// or dw, a row at a time.  (What they need is found again: the sums leave few registers.)
+template <int KIND, bool F32>
+__device__ __forceinline__ void store_rows(const GemmParams& p, int pair, int pairs, int u, uint32_t rank, uint32_t mine,
+                                           int j) {
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    asm volatile("" : "+r"(u));
+    Unit w;
+    unit<KIND>(p, pair, pairs, u, w);
+    const int l = t & 31, row = w.m * BM + (int)rank * HALF + ((t >> 5) & 3) * 32;
+    const int col = w.n * BN + ((t >> 5) - 2) / 4 * EW + j + l;
+    const int n = min(32, (w.second ? p.V : p.T) - row);
+    if (col >= (w.second ? p.W : p.ldacc)) return;
+    auto value = [&](int i) {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(v)
+                     : "r"(mine + i * 128 + (((l >> 2) ^ (i & 7)) << 4) + (l & 3) * 4)
+                     : "memory");
+        return v;
+    };
+    if (F32 || !w.second) {
+        float* q = (w.second ? static_cast<float*>(p.dw) + row * p.lddw
+                             : p.acc + ((int64_t)w.split * p.T + row) * p.ldacc) + col;
+        const int64_t ld = w.second ? p.lddw : p.ldacc;
+        const bool add = !w.second && p.add;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, q += ld) *q = value(i) + (add ? *q : 0.f);
+    } else {
+        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.dw) + row * p.lddw + col;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, q += p.lddw) *q = __float2bfloat16_rn(value(i));
     }
-    o[0] = a;
-    o[1] = b;
 }
 
 template <int KIND, bool F32>
@@ -433,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
             const uint32_t id = (tc::idesc_bf16(BM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u)) &
                                 (F32 ? ~(1u << 7 | 1u << 10) : ~0u);
             int k0 = w.k0;
-            do {  // (a unit without steps has one chunk without steps)
+            do {
                 const int k1 = CH ? min(w.k1, k0 + ch) : w.k1;
                 const int buf = it & 1;
                 if (it >= 2 && !wait_for(&c.free_[buf], ((it >> 1) & 1) ^ 1, &c.abort)) {
@@ -485,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
             for (int i = 0; i < (CH ? EW : 1); ++i) acc[i] = 0.f;
             uint32_t d = 0;
             uint32_t release = 0;
-            for (int left = CH ? max(1, (w.k1 - w.k0 + ch - 1) / ch) : 1; left > 0; --left) {
+            for (int left = CH ? (w.k1 - w.k0 + ch - 1) / ch : 1; left > 0; --left) {
                 const int buf = it & 1;
                 // A wait that gives up ends no loop here: the warps' barriers stay matched, and what is
                 // left of the tiles goes by without waiting, with whatever the accumulators hold.
@@ -520,19 +543,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
             const uint32_t stage = ring + STAGES * 2 * OPB + (KIND == K_LSE ? 0 : quarter * 2 * OUTB);
             const int r0 = w.m * BM + (int)rank * HALF, r = r0 + row;
             const int c0 = w.n * BN + quarter * EW;
-            // logits of fp32 inputs, and both gradients' sums, are 2^(exponents of the scalings) times too large
-            float f1 = 1.f, f2 = p.scale;
+            // logits and sums of fp32 inputs are 2^(exponents of the scalings) times too large (dh's
+            // by w's after this)
+            float f = p.scale;
             if (F32) {
-                const int we = exponent_for(__uint_as_float(__ldg(p.most)), 14);
                 if (KIND != K_GRAD) {
                     // (beyond the range of one factor the logits are below 2^-80, or infinite)
-                    const int k = -we - (r < p.T ? __ldg(p.he + r) : 0);
-                    f2 = pow2(max(-126, min(127, k))) * p.scale;
+                    const int k = -exponent_for(__uint_as_float(__ldg(p.most)), 14) - (r < p.T ? __ldg(p.he + r) : 0);
+                    f = pow2(max(-126, min(127, k))) * p.scale;
                 } else if (!w.second) {
-                    if (r < p.T) f1 = pow2(-__ldg(p.pa + r));
-                    f2 = pow2(-we);
+                    f = r < p.T ? pow2(-__ldg(p.pa + r)) : 0.f;
                 } else {
-                    f2 = pow2(-exponent_for(__uint_as_float(__ldg(p.most + 1)), 14));
+                    f = pow2(-exponent_for(__uint_as_float(__ldg(p.most + 1)), 14));
                 }
             }
             if (KIND == K_LSE) {
@@ -543,7 +565,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 if constexpr (CH) {
 #pragma unroll
                     for (int i = 0; i < EW; ++i) {
-                        acc[i] = i < left ? acc[i] * f2 : -INFINITY;
+                        acc[i] = i < left ? acc[i] * f : -INFINITY;
                         top = fmaxf(top, acc[i]);
                     }
                     if (o >= 0 && o < EW) {
@@ -571,7 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
                     p.stat[(int64_t)w.n * p.T + r] = make_float2(top, sum);
                 }
-            } else if (KIND == K_P || (w.second && p.dw_store)) {
+            } else if (KIND == K_P || (!F32 && w.second && p.dw_store)) {
                 float lse = 0.f, g = 0.f;
                 int tgt = -1;  // the target's column of this piece
                 if (KIND == K_P && r < p.T) {
@@ -617,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
                     if (KIND == K_P) {
 #pragma unroll
-                        for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], f2, -lse) * kLog2e) : 0.f;
+                        for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], f, -lse) * kLog2e) : 0.f;
                         const int o = tgt < 0 ? -1 : tgt - (c0 + j);
                         if (o >= 0 && o < SC) {
                             float at = 0.f;
@@ -688,60 +710,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
                 }
             } else {
-                // fp32 results, or bf16 ones that TMA cannot store: rows of this thread
+                // fp32 results, or bf16 ones that TMA cannot store: through 4 KB of the warp's own, so that
+                // a warp stores a row's 32 columns at a time (dw of 32003 x 1001 in fp32, row by row of a
+                // thread: 390 us of both gradients' products instead of 247)
                 const int rows = w.second ? p.V : p.T;
-                const bool live = r < rows;
                 float lo = 0.f;
                 const __nv_bfloat16* hrow = nullptr;
-                if (!F32 && w.second && live) {
-                    const int t = __ldg(p.only + p.v0 + r);
-                    if (t >= 0) {
-                        lo = __ldg(p.lo + t);
-                        hrow = p.h + t * p.ldh;
+                if (!F32 && w.second && r < rows) {
+                    const int t1 = __ldg(p.only + p.v0 + r);
+                    if (t1 >= 0) {
+                        lo = __ldg(p.lo + t1);
+                        hrow = p.h + t1 * p.ldh;
                     }
                 }
-                constexpr int DC = CH ? 8 : 32;  // columns at a time
+                const int tl = t & 31;
+                const uint32_t mine = stage + quad * 4096;
 #pragma unroll
-                for (int j = 0; j < EW; j += DC) {
-                    float x[DC];
-                    if constexpr (CH) {
-#pragma unroll
-                        for (int i = 0; i < DC; ++i) {
-                            x[i] = acc[j + i];
-                            asm volatile("" : "+f"(x[i]));
-                        }
-                    } else {
+                for (int j = 0; j < EW; j += 32) {
+                    float x[CH ? 1 : 32];
+                    if constexpr (!CH) {
                         tc::ld32(d + j, x);
-                        if (j == EW - DC) {
+                        if (j == EW - 32) {
                             tc::fence_before();
                             __syncwarp();
                             if (lane == 0) arrive_cluster(release);
                         }
                     }
                     const int col = c0 + j;
-                    if (!live || col >= p.W) continue;
+                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < DC; ++i) {
-                        if (F32) x[i] = x[i] * f1 * f2;
-                        if (w.k1 <= w.k0) x[i] = 0.f;  // a split without steps: nothing was added up
+                    for (int i = 0; i < 32; i += 4) {
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if constexpr (CH) {
+                                y[e] = acc[j + i + e];
+                                asm volatile("" : "+f"(y[e]));  // (a few at a time: registers)
+                            } else {
+                                y[e] = x[i + e];
+                            }
+                            if (F32) y[e] *= f;
+                            if (!F32 && hrow && col + i + e < p.W) y[e] = fmaf(lo, __bfloat162float(hrow[col + i + e]), y[e]);
+                        }
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + tl * 128 + (((i >> 2) ^ (tl & 7)) << 4)),
+                                     "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3])
+                                     : "memory");
                     }
-                    if (!w.second) {
-                        float* q = p.acc + ((int64_t)w.split * p.T + r) * p.ldacc + col;
-#pragma unroll
-                        for (int i = 0; i < DC; i += 8)
-                            if (col + i < p.ldacc) put8(q + i, x + i, p.add != 0);
-                    } else if (F32) {
-                        float* q = static_cast<float*>(p.dw) + r * p.lddw + col;
-#pragma unroll
-                        for (int i = 0; i < DC; ++i)
-                            if (col + i < p.W) q[i] = x[i];
-                    } else {
-                        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p.dw) + r * p.lddw + col;
-#pragma unroll
-                        for (int i = 0; i < DC; ++i)
-                            if (col + i < p.W)
-                                q[i] = __float2bfloat16_rn(hrow ? fmaf(lo, __bfloat162float(hrow[col + i]), x[i]) : x[i]);
-                    }
+                    __syncwarp();
+                    store_rows<KIND, F32>(p, pair, pairs, u, rank, mine, j);
                 }
             }
         }
@@ -797,7 +813,19 @@ __global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h,
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * 8;
     float wm = 0.f, hm = 0.f;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < (int64_t)T + V; r += step) {
+    const bool dense = ldw == W && (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+    if (dense) {  // w as one array (rows of 1001: 20 us, 31 by rows)
+        const int64_t n = (int64_t)V * W, n4 = n / 4;
+        const float4* w4 = reinterpret_cast<const float4*>(w);
+#pragma unroll 8
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+            const float4 v = __ldg(w4 + i);
+            // (a NaN is left out)
+            wm = fmaxf(wm, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+        }
+        if (blockIdx.x == 0 && threadIdx.x < n - 4 * n4) wm = fmaxf(wm, fabsf(__ldg(w + 4 * n4 + threadIdx.x)));
+    }
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < (int64_t)T + (dense ? 0 : V); r += step) {
         const float* x = r < T ? h + r * ldh : w + (r - T) * ldw;
         float m = 0.f;
 #pragma unroll 8
@@ -905,9 +933,10 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict_
 template <typename E>
 __global__ void __launch_bounds__(256) dh_kernel(const float* __restrict__ acc, int splits, int T, int W, int ldacc,
                                                  const float* __restrict__ lo, const void* targets, int wide, int vocab,
-                                                 const E* __restrict__ w, int64_t ldw, E* __restrict__ dh, int64_t lddh,
-                                                 int vec) {
+                                                 const E* __restrict__ w, int64_t ldw, const unsigned* most,
+                                                 E* __restrict__ dh, int64_t lddh, int vec) {
     const int nv = ldacc / 8;
+    const float f32 = sizeof(E) == 4 ? pow2(-exponent_for(__uint_as_float(__ldg(most)), 14)) : 1.f;  // w's scaling
     const int64_t n = (int64_t)T * nv;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = (n >> 31) ? i / nv : (int64_t)((unsigned)i / (unsigned)nv);
@@ -934,6 +963,10 @@ __global__ void __launch_bounds__(256) dh_kernel(const float* __restrict__ acc, 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] = fmaf(l, x[j], f[j]);
             }
+        }
+        if (sizeof(E) == 4) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= f32;
         }
         E* o = dh + r * lddh + c;
         if (vec) store8(o, f);
@@ -970,7 +1003,8 @@ int dh_splits(int T, int W, int cols) {
     int64_t s = device_sm_count() / 2 / tiles;
     if (s > kb / 16) s = kb / 16;
     if (s > 16) s = 16;
-    return (int)(s < 1 ? 1 : s);
+    if (s < 1) s = 1;
+    return (int)div_up(kb, div_up(kb, s));  // none is left without steps
 }
 
 struct Plan {
@@ -1293,8 +1327,9 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         if (store && (st = make_map_rows(&m.out, dwp, lddw, width, cols, cols, 1, HALF, SC)) != GDN_OK) return st;
         p.nt = (int)div_up(width, BN);
         p.kb = (int)div_up(cols, BK);
-        p.splits = l.splits;
-        p.kper = (int)div_up(p.kb, p.splits);
+        // (the last piece may be done with fewer splits than there are sums)
+        p.kper = (int)div_up(p.kb, l.splits);
+        p.splits = (int)div_up(p.kb, p.kper);
         p.mt2 = (int)div_up(cols, BM);
         p.nt2 = p.nt;
         p.kb2 = (int)div_up(T, BK);
@@ -1309,10 +1344,10 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
     const int vec = width % 8 == 0 && (reinterpret_cast<uintptr_t>(dh) & 15u) == 0 && lddh % 8 == 0;
     if (dtype == GDN_F32)
         dh_kernel<float><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, nullptr, targets, wide, vocab,
-                                           static_cast<const float*>(w), ldw, static_cast<float*>(dh), lddh, vec);
+                                           static_cast<const float*>(w), ldw, p.most, static_cast<float*>(dh), lddh, vec);
     else
         dh_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, p.lo, targets, wide, vocab,
-                                                   static_cast<const __nv_bfloat16*>(w), ldw,
+                                                   static_cast<const __nv_bfloat16*>(w), ldw, nullptr,
                                                    static_cast<__nv_bfloat16*>(dh), lddh, vec);
     return check_launch("dh_kernel");
 }

@@ -108,8 +108,8 @@ def gdn_embed_fwd(tokens, table, scale=1.0, out=None):
     return y
 
 
-def embed_bwd_workspace_size(T, width) -> int:
-    return int(load().gdn_embed_bwd_workspace_size(T, width))
+def embed_bwd_workspace_size(T, vocab, width) -> int:
+    return int(load().gdn_embed_bwd_workspace_size(T, vocab, width))
 
 
 def gdn_embed_bwd(dy, tokens, vocab, scale=1.0, into=None, workspace=None):
@@ -120,7 +120,7 @@ def gdn_embed_bwd(dy, tokens, vocab, scale=1.0, into=None, workspace=None):
     dev, code = _lead(dy, "dy")
     e, (T, W) = dy.dtype, dy.shape
     lib = _lib()
-    ws = _workspace(lib.gdn_embed_bwd_workspace_size(T, W), workspace, dev)
+    ws = _workspace(lib.gdn_embed_bwd_workspace_size(T, vocab, W), workspace, dev)
     tp, bits = _index(tokens, "tokens", dev)
     if tokens.shape[0] != T:
         raise ValueError(f"tokens must have {T} elements, got {tokens.shape[0]}")

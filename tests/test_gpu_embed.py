@@ -125,8 +125,8 @@ def test_rows_do_not_leak(g):
 
 def test_a_longer_calls_workspace(g):
     q = gen(4)
-    ws = torch.full((g.embed_bwd_workspace_size(9000, 64),), 255, dtype=torch.uint8, device="cuda")
-    sizes = [g.embed_bwd_workspace_size(T, 64) for T in (0, 1, 4096, 4097, 32768, 32769, 70000, 600000, 1 << 22)]
+    ws = torch.full((g.embed_bwd_workspace_size(9000, 30, 64),), 255, dtype=torch.uint8, device="cuda")
+    sizes = [g.embed_bwd_workspace_size(T, 30, 64) for T in (0, 1, 4096, 4097, 32768, 32769, 70000, 600000, 1 << 22)]
     assert sizes == sorted(sizes)
     for T in (1, 100, 5000, 9000):
         dy, tok = view(T, 64, BF, q), torch.randint(0, 30, (T,), generator=q, device="cuda")

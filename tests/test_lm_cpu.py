@@ -103,9 +103,9 @@ def test_workspaces(lib):
     """Sizes are multiples of 256 that do not fall with the tokens, and zero for sizes that are refused."""
     Ts = [0, 1, 100, 4096, 4097, 32768, 32769, 65536, 10 ** 6]
     for W in (1, 64, 1001):
-        e = [lib.gdn_embed_bwd_workspace_size(T, W) for T in Ts]
+        e = [lib.gdn_embed_bwd_workspace_size(T, 50, W) for T in Ts]
         assert e == sorted(e) and all(v % 256 == 0 for v in e)
-    assert lib.gdn_embed_bwd_workspace_size(-1, 8) == lib.gdn_embed_bwd_workspace_size(5, 0) == 0
+    assert lib.gdn_embed_bwd_workspace_size(-1, 9, 8) == lib.gdn_embed_bwd_workspace_size(5, 9, 0) == lib.gdn_embed_bwd_workspace_size(5, -1, 8) == 0
     for dt in (0, 1):
         for size in (lib.gdn_vocab_loss_fwd_workspace_size, lib.gdn_vocab_loss_bwd_workspace_size):
             assert all(size(T, 1000, 64, dt) % 256 == 0 and size(T, 1000, 64, dt) > 0 for T in Ts)
