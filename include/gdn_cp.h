@@ -726,16 +726,21 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * elements are read in place, so that h and w then have to be 16-byte aligned
  * with row strides that are multiples of 8; other widths and fp32 are read at
  * any alignment, into a copy in the workspace.  Products of bf16 inputs are
- * exact and added in fp32; fp32 inputs are split into three bf16 parts each,
- * of whose nine products the six that count are added in fp32.
+ * exact and added in fp32.  fp32 inputs are scaled by powers of two and split
+ * into two fp16 parts, of whose four products three are added in fp32: a value
+ * keeps 22 bits down to 2^-18 of the largest under its scaling (its row's for
+ * h, one for w, its token's dloss for P), below that it is off by 2^-40 of it.
+ * An expired wait (gdn_device_timeouts) leaves the outputs incomplete.
  *
  * gdn_vocab_loss_bwd: gradients of the above for dloss, from the forward's lse
  *   dloss   device [T] fp32
  *   dh      device [T, width] dtype, row stride lddh;  dw device [vocab,
  *           width] dtype, row stride lddw; neither overlaps an input
  * dh and dw are products with P_tv = scale dloss_t (softmax - one hot), which
- * is rounded to bf16 for bf16 inputs and split like them for fp32.  The
- * vocabulary is taken in pieces; the workspace holds one piece's P (half a
+ * is rounded to bf16 for bf16 inputs (what that takes from the entry at the
+ * target is given back where the token is the only one with it, to dh always)
+ * and split like them for fp32.  A token whose dloss is 0 has no gradient,
+ * whatever its h holds.  The vocabulary is taken in pieces; the workspace holds one piece's P (half a
  * gigabyte at most, or 1024 columns), and dh in fp32.
  *   workspace  device, >= the _workspace_size(...) bytes of the call, 256-byte
  *           aligned, contents on entry irrelevant

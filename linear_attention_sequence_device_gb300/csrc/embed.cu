@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(ST) sort_count_kernel(const SortArgs a) {
     for (int i = lo + threadIdx.x; i < hi; i += ST) {
         const int key = sort_key<I>(a, i);
         atomicAdd(&hist[(key >> a.shift) & (kBins - 1)], 1);
-        if (a.hit && key < a.vocab && !__ldcg(a.hit + key)) a.hit[key] = 1;  // (a frequent token once, or nearly)
+        if (a.hit && key < a.vocab) a.hit[key] = 1;  // (asking first whether it is set: 155 -> 185 us of the whole)
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += ST) a.count[blockIdx.x * kBins + i] = hist[i];

@@ -201,7 +201,19 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
 }
 
 constexpr int RING = 3;
-constexpr uint32_t kPolls = 1u << 26;  // of a wait in the ring
+constexpr uint64_t kWaitNs = 4000000000ull;
+
+// Waits for a phase, up to kWaitNs or until another role gave up
+__device__ __forceinline__ bool ring_wait(uint64_t* mbar, uint32_t parity, const volatile int* bad) {
+    if (tc::mbar_wait(mbar, parity, 64)) return true;
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    while (!tc::mbar_wait(mbar, parity, 64)) {
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        if (*bad || t - t0 > kWaitNs) return false;
+    }
+    return true;
+}
 
 // What a head's rule needs beside its state, formed a stage ahead
 template <int DK, int DV>
@@ -287,7 +299,7 @@ __global__ void __launch_bounds__(DK * DV / 32 + 32 * (RING + 2)) rule_ring_kern
             // ---- states in ----
             for (int n = 0;; ++n) {
                 const int i = list.next(p, heads, to, slot), s = n % RING;
-                if (n >= RING && !tc::mbar_wait(&sm.empty[s], (n / RING - 1) & 1, kPolls, &sm.bad)) {
+                if (n >= RING && !__all_sync(0xffffffffu, ring_wait(&sm.empty[s], (n / RING - 1) & 1, &sm.bad))) {
                     sm.bad = 1;
                     break;
                 }
@@ -348,7 +360,7 @@ __global__ void __launch_bounds__(DK * DV / 32 + 32 * (RING + 2)) rule_ring_kern
                         kq += __shfl_xor_sync(0xffffffffu, kq, m);
                     }
                 }
-                if (n >= RING && !tc::mbar_wait(&sm.empty[s], (n / RING - 1) & 1, kPolls, &sm.bad)) {
+                if (n >= RING && !__all_sync(0xffffffffu, ring_wait(&sm.empty[s], (n / RING - 1) & 1, &sm.bad))) {
                     sm.bad = 1;
                     break;
                 }
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(DK * DV / 32 + 32 * (RING + 2)) rule_ring_kern
             for (int n = 0;; ++n) {
                 const int i = list.next(p, heads, to, slot), s = n % RING;
                 if (i < 0) break;
-                if (!tc::mbar_wait(&sm.done[s], (n / RING) & 1, kPolls, &sm.bad)) {
+                if (!__all_sync(0xffffffffu, ring_wait(&sm.done[s], (n / RING) & 1, &sm.bad))) {
                     sm.bad = 1;
                     break;
                 }
@@ -417,7 +429,7 @@ __global__ void __launch_bounds__(DK * DV / 32 + 32 * (RING + 2)) rule_ring_kern
     const int row0 = warp * (8 * RPW) + lane / LPR, col = (lane % LPR) * 4;
     for (int n = 0;; ++n) {
         const int s = n % RING;
-        if (!tc::bar_and(1, NT, tc::mbar_wait(&sm.full[s], (n / RING) & 1, kPolls, &sm.bad))) {
+        if (!tc::bar_and(1, NT, ring_wait(&sm.full[s], (n / RING) & 1, &sm.bad))) {
             sm.bad = 1;
             break;
         }
