@@ -207,6 +207,7 @@ struct GemmParams {
     float* at;            // K_LSE: [T] the target's logit
     const float* lse; const float* dloss;  // K_P
     const int* he; const int* pa;          // fp32: exponents of the scalings of h's rows, of P's
+    const int* we;                         // K_LSE in fp32: of w's rows
     const unsigned* most;                  // and what the others are taken from: largest |w|, |h| 2^-pa
     float* lo;            // [T] what P's entry at the target lost when it was rounded
     const int* only;      // [vocab] the one token with this target; below 0: none or several
@@ -502,7 +503,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         float2* part = reinterpret_cast<float2*>(staged);
         int it = 0, tile = 0;
         bool ok = true;
+        // gradients of bf16: the one token with this thread's row of w as its target, looked up a tile
+        // ahead (dw of 130 tokens: a tile's loads take as long as its products)
+        constexpr bool ONLY = KIND == K_GRAD && !F32;
+        auto only_of = [&](int u) {
+            Unit x;
+            if (!unit<KIND>(p, pair, pairs, u, x) || !x.second) return -1;
+            const int r = x.m * BM + (int)rank * HALF + (warp & 3) * 32 + lane;
+            return r < p.V ? __ldg(p.only + p.v0 + r) : -1;
+        };
+        int only = ONLY ? only_of(0) : -1;
         for (int u = 0; unit<KIND>(p, pair, pairs, u, w); ++u) {
+            const int only_next = ONLY ? only_of(u + 1) : -1;
             float acc[CH ? EW : 1];
 #pragma unroll
             for (int i = 0; i < (CH ? EW : 1); ++i) acc[i] = 0.f;
@@ -547,7 +559,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
             // by w's after this)
             float f = p.scale;
             if (F32) {
-                if (KIND != K_GRAD) {
+                if (KIND == K_LSE) {
+                    f = r < p.T ? pow2(-__ldg(p.he + r)) * p.scale : 0.f;
+                } else if (KIND == K_P) {
                     // (beyond the range of one factor the logits are below 2^-80, or infinite)
                     const int k = -exponent_for(__uint_as_float(__ldg(p.most)), 14) - (r < p.T ? __ldg(p.he + r) : 0);
                     f = pow2(max(-126, min(127, k))) * p.scale;
@@ -564,9 +578,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 float top = -INFINITY, sum = 0.f;
                 if constexpr (CH) {
 #pragma unroll
-                    for (int i = 0; i < EW; ++i) {
-                        acc[i] = i < left ? acc[i] * f : -INFINITY;
-                        top = fmaxf(top, acc[i]);
+                    for (int i = 0; i < EW; i += 4) {
+                        int4 e = make_int4(0, 0, 0, 0);
+                        if (F32) e = __ldg(reinterpret_cast<const int4*>(p.we + c0 + i));
+                        const int es[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float x = F32 ? acc[i + j] * f * pow2(-es[j]) : acc[i + j] * f;
+                            acc[i + j] = i + j < left ? x : -INFINITY;
+                            top = fmaxf(top, acc[i + j]);
+                        }
                     }
                     if (o >= 0 && o < EW) {
                         float v = 0.f;
@@ -606,12 +627,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 const bool live = KIND != K_P || g != 0.f;
                 float lo = 0.f;
                 const __nv_bfloat16* hrow = nullptr;
-                if (KIND == K_GRAD && r < p.V) {
-                    const int t = __ldg(p.only + p.v0 + r);
-                    if (t >= 0) {
-                        lo = __ldg(p.lo + t);
-                        hrow = p.h + t * p.ldh;
-                    }
+                if (ONLY && only >= 0) {
+                    lo = __ldg(p.lo + only);
+                    hrow = p.h + only * p.ldh;
                 }
                 constexpr int PARTS = KIND == K_P && F32 ? 2 : 1;
                 const int out_cols = KIND == K_P ? p.V : p.W, out_rows = KIND == K_P ? p.T : p.V;
@@ -713,15 +731,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 // fp32 results, or bf16 ones that TMA cannot store: through 4 KB of the warp's own, so that
                 // a warp stores a row's 32 columns at a time (dw of 32003 x 1001 in fp32, row by row of a
                 // thread: 390 us of both gradients' products instead of 247)
-                const int rows = w.second ? p.V : p.T;
                 float lo = 0.f;
                 const __nv_bfloat16* hrow = nullptr;
-                if (!F32 && w.second && r < rows) {
-                    const int t1 = __ldg(p.only + p.v0 + r);
-                    if (t1 >= 0) {
-                        lo = __ldg(p.lo + t1);
-                        hrow = p.h + t1 * p.ldh;
-                    }
+                if (ONLY && only >= 0) {
+                    lo = __ldg(p.lo + only);
+                    hrow = p.h + only * p.ldh;
                 }
                 const int tl = t & 31;
                 const uint32_t mine = stage + quad * 4096;
@@ -760,6 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     store_rows<KIND, F32>(p, pair, pairs, u, rank, mine, j);
                 }
             }
+            only = only_next;
         }
         if ((warp & 3) == 0 && lane == 0) tc::bulk_wait();  // the threads that stored
     }
@@ -804,8 +819,8 @@ __global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* __restri
     }
 }
 
-// The scalings of fp32 inputs: a warp a row of h, then of w.  most[0]: the largest |w|;
-// with dloss most[1]: the largest |h_t| 2^-pa[t] over the tokens that count.
+// The scalings of fp32 inputs of the gradients: a warp a row of h, then of w.  most[0]: the
+// largest |w|; most[1]: the largest |h_t| 2^-pa[t] over the tokens that count.
 __global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h, int64_t ldh, int T,
                                                     const float* __restrict__ w, int64_t ldw, int V, int W,
                                                     const void* targets, int wide, const float* dloss, float scale,
@@ -841,12 +856,10 @@ __global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h,
         for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         if (lane == 0) {
             he[r] = exponent_for(m, 14);
-            if (dloss) {
-                const bool real = raw_target(targets, wide, r) >= 0;
-                const int a = real ? exponent_for(fabsf(__ldg(dloss + r) * scale), 13) : 0;
-                pa[r] = a;
-                if (real && __ldg(dloss + r) != 0.f) hm = fmaxf(hm, m * pow2(-a));
-            }
+            const bool real = raw_target(targets, wide, r) >= 0;
+            const int a = real ? exponent_for(fabsf(__ldg(dloss + r) * scale), 13) : 0;
+            pa[r] = a;
+            if (real && __ldg(dloss + r) != 0.f) hm = fmaxf(hm, m * pow2(-a));
         }
     }
 #pragma unroll
@@ -854,6 +867,34 @@ __global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h,
     // (bits of numbers that are not negative are ordered as they are)
     if (lane == 0 && wm > 0.f) atomicMax(most, __float_as_uint(wm));
     if (lane == 0 && hm > 0.f) atomicMax(most + 1, __float_as_uint(hm));
+}
+
+// For the loss alone both are scaled by their rows, which takes one pass over w: a warp
+// finds a row's exponent and splits it, the second time out of the caches (scoring 513 x
+// 32000 x 1024: 171 us with a pass for w's largest value before, 150 so).
+__global__ void __launch_bounds__(256) split_rows_kernel(const float* __restrict__ x, int64_t ldx, int64_t rows, int W,
+                                                         int ld, int* __restrict__ exps, __half* __restrict__ out) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8) {
+        const float* s = x + r * ldx;
+        float m = 0.f;
+#pragma unroll 8
+        for (int c = lane; c < W; c += 32) m = fmaxf(m, fabsf(__ldg(s + c)));  // (a NaN is left out)
+#pragma unroll
+        for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const int k = exponent_for(m, 14);
+        if (lane == 0) exps[r] = k;
+        const float k1 = pow2(k);
+#pragma unroll 4
+        for (int c = 2 * lane; c < ld; c += 64) {
+            const float a = c < W ? __ldg(s + c) * k1 : 0.f, b = c + 1 < W ? __ldg(s + c + 1) * k1 : 0.f;
+            const __half2 v = __floats2half2_rn(a, b);
+            const float va = __low2float(v), vb = __high2float(v);
+            *reinterpret_cast<__half2*>(out + r * ld + c) = v;
+            *reinterpret_cast<__half2*>(out + (rows + r) * ld + c) =
+                __floats2half2_rn(isfinite(va) ? a - va : 0.f, isfinite(vb) ? b - vb : 0.f);
+        }
+    }
 }
 
 // fp32 [rows][W] -> two fp16 parts [2][rows][ld] of its scaled values.  he: by its rows' own
@@ -1008,7 +1049,7 @@ int dh_splits(int T, int W, int cols) {
 }
 
 struct Plan {
-    size_t h, hw, w, stat, at, p, acc, lo, only, he, pa, most, total;
+    size_t h, hw, w, stat, at, p, acc, lo, only, he, pa, we, most, total;
     int piece, splits, ldacc;
 };
 Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
@@ -1028,9 +1069,12 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     if (dt == GDN_F32) {
         l.he = o;
         o += up256(sizeof(int) * t);
-        l.most = o;
-        o += 256;
-        if (grad) {
+        if (!grad) {
+            l.we = o;
+            o += up256(sizeof(int) * (size_t)div_up(V, BN) * BN);
+        } else {
+            l.most = o;
+            o += 256;
             l.pa = o;
             o += up256(sizeof(int) * t);
             l.hw = o;
@@ -1133,12 +1177,12 @@ gdn_status pack(const void* x, int64_t ldx, int64_t rows, int W, const void* tar
                                                           wide, dloss, vocab, only, static_cast<__nv_bfloat16*>(out));
     return check_launch("pack_kernel");
 }
-// fp32 inputs: their scalings, then their parts into the workspace
+// fp32 inputs of the gradients: their scalings, then their parts into the workspace
 gdn_status split(const void* h, int64_t ldh, int T, const void* w, int64_t ldw, int V, int W, const void* targets, int wide,
                  const float* dloss, float scale, const Plan& l, char* ws, cudaStream_t s) {
     const int ld = round8(W);
     int* he = reinterpret_cast<int*>(ws + l.he);
-    int* pa = dloss ? reinterpret_cast<int*>(ws + l.pa) : nullptr;
+    int* pa = reinterpret_cast<int*>(ws + l.pa);
     unsigned* most = reinterpret_cast<unsigned*>(ws + l.most);
     const float *hf = static_cast<const float*>(h), *wf = static_cast<const float*>(w);
     if (cudaMemsetAsync(most, 0, 2 * sizeof(unsigned), s) != cudaSuccess) return check_launch("memset");
@@ -1150,9 +1194,8 @@ gdn_status split(const void* h, int64_t ldh, int T, const void* w, int64_t ldw, 
     const unsigned g = grid_for((int64_t)T * (ld / 8));
     split_kernel<<<g, 256, 0, s>>>(hf, ldh, T, W, ld, he, nullptr, most, nullptr, 0, nullptr,
                                    reinterpret_cast<__half*>(ws + l.h));
-    if (dloss)
-        split_kernel<<<g, 256, 0, s>>>(hf, ldh, T, W, ld, nullptr, pa, most, targets, wide, dloss,
-                                       reinterpret_cast<__half*>(ws + l.hw));
+    split_kernel<<<g, 256, 0, s>>>(hf, ldh, T, W, ld, nullptr, pa, most, targets, wide, dloss,
+                                   reinterpret_cast<__half*>(ws + l.hw));
     return check_launch("split_kernel");
 }
 
@@ -1229,7 +1272,15 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
         H = {ws + l.h, round8(width)};
         Wt = {ws + l.w, round8(width)};
         if (dtype == GDN_F32) {
-            st = split(h, ldh, T, w, ldw, vocab, width, nullptr, 0, nullptr, scale, l, ws, s);
+            const int ld = round8(width);
+            const int64_t wave = (int64_t)device_sm_count() * 8, ht = div_up(T, 8), wt = div_up(vocab, 8);
+            split_rows_kernel<<<(unsigned)(wt < wave ? wt : wave), 256, 0, s>>>(
+                static_cast<const float*>(w), ldw, vocab, width, ld, reinterpret_cast<int*>(ws + l.we),
+                reinterpret_cast<__half*>(ws + l.w));
+            split_rows_kernel<<<(unsigned)(ht < wave ? ht : wave), 256, 0, s>>>(
+                static_cast<const float*>(h), ldh, T, width, ld, reinterpret_cast<int*>(ws + l.he),
+                reinterpret_cast<__half*>(ws + l.h));
+            st = check_launch("split_rows_kernel");
         } else if ((st = pack(h, ldh, T, width, nullptr, 0, nullptr, 0, nullptr, ws + l.h, s)) == GDN_OK) {
             st = pack(w, ldw, vocab, width, nullptr, 0, nullptr, 0, nullptr, ws + l.w, s);
         }
@@ -1247,7 +1298,7 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     p.T = T; p.V = p.vocab = vocab; p.W = width; p.scale = scale;
     p.targets = targets; p.wide = wide;
     p.he = reinterpret_cast<int*>(ws + l.he);
-    p.most = reinterpret_cast<unsigned*>(ws + l.most);
+    p.we = reinterpret_cast<int*>(ws + l.we);
     p.stat = reinterpret_cast<float2*>(ws + l.stat);
     p.at = reinterpret_cast<float*>(ws + l.at);
     if ((st = launch_gemm<K_LSE>(p, m, s)) != GDN_OK) return st;
