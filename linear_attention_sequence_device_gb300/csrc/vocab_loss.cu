@@ -297,13 +297,21 @@ __device__ __forceinline__ int exponent_for(float m, int to) {
 // Where that counts, chunks are added up in registers, rounded: for logits of bf16 (the loss
 // of 4096 tokens, 50021 columns and a width of 2048 off by 1.6e-6 of itself without chunks,
 // 0.4e-6 with eight steps each; 531 us without, 541 with 16, 560 with 8), and for all of
-// fp32, whose small products come first in a chunk, while the sum is small.
+// fp32, whose small products come first in a chunk, while the sum is small.  The
+// gradients' logits are added up as the loss's are, bit for bit: where a token is nearly
+// certain, P at its target is a small difference from 1, which errors that lse does not
+// share would drown (5 tokens with 1 - p of 1e-4: dh off by 3.7e-2 of itself).
 template <int KIND, bool F32>
 __host__ __device__ constexpr bool chunked() {
-    return F32 || KIND == K_LSE;
+    return F32 || KIND != K_GRAD;
 }
 constexpr int kChunkF32 = 4;   // the most steps of a chunk
 constexpr int kChunkBf16 = 12;
+// and of the logits of up to kFewTokens tokens: the loss of one token may be a small difference of
+// large logits, which no other token's outweighs (single tokens: losses off by up to 3.8e-6
+// of themselves with twelve steps, 1.2e-6 with two; 130 tokens of 32000 x 2048, both
+// directions: 149 us with twelve, 156 with four, 169 with two)
+constexpr int kChunkFew = 2, kFewTokens = 64;
 
 // v = x, or x -= g, where column o is i, for every i of a row in registers.  Written out:
 // the compiler makes an array in local memory of a chain of choices.
@@ -657,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
                     if (KIND == K_P) {
 #pragma unroll
-                        for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast(fmaf(x[i], f, -lse) * kLog2e) : 0.f;
+                        for (int i = 0; i < SC; ++i) x[i] = live ? g * exp2_fast((__fmul_rn(x[i], f) - lse) * kLog2e) : 0.f;
                         const int o = tgt < 0 ? -1 : tgt - (c0 + j);
                         if (o >= 0 && o < SC) {
                             float at = 0.f;
@@ -964,9 +972,11 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict_
     }
     const int64_t tgt =
         wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
-    const float z = m + logf(s);
-    lse[r] = z;
-    loss[r] = tgt < 0 ? 0.f : tgt >= V ? NAN : z - __ldg(at + r);
+    const float l = logf(s);
+    lse[r] = m + l;
+    // (not from the rounded lse: where the target is the largest, m is its logit, and a small
+    // loss keeps its digits)
+    loss[r] = tgt < 0 ? 0.f : tgt >= V ? NAN : (m - __ldg(at + r)) + l;
 }
 
 // dh from the splits' sums, eight columns a thread; for bf16 with what P's rounding took
@@ -1154,7 +1164,7 @@ gdn_status launch_gemm_t(GemmParams p, const Maps& m, cudaStream_t s) {
     if (n1 + n2 > 0x7fffffff / 2) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)(n1 + n2));
     int pairs = pair_count(fn, smem);
     if (n1 + n2 < pairs) pairs = (int)(n1 + n2);
-    const int steps = F32 ? kChunkF32 : kChunkBf16;
+    const int steps = KIND != K_GRAD && p.T <= kFewTokens ? kChunkFew : F32 ? kChunkF32 : kChunkBf16;
     p.chunk = KIND == K_GRAD ? steps : (int)div_up(p.kb, div_up(p.kb, steps));
     if (KIND == K_GRAD) balance(p, n1, n2, pairs);
     vocab_gemm_kernel<KIND, F32><<<2 * (unsigned)pairs, GT, smem, s>>>(p, m);
