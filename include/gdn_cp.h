@@ -729,7 +729,8 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * exact and added in fp32.  fp32 inputs are scaled by powers of two and split
  * into two fp16 parts, of whose four products three are added in fp32: a value
  * keeps 22 bits down to 2^-18 of the largest under its scaling (its row's for
- * h, one for w, its token's dloss for P), below that it is off by 2^-40 of it.
+ * h, and for w in the forward; one for w in the backward, its token's dloss for
+ * P), below that it is off by 2^-40 of it.
  * An expired wait (gdn_device_timeouts) leaves the outputs incomplete.
  *
  * gdn_vocab_loss_bwd: gradients of the above for dloss, from the forward's lse
@@ -740,8 +741,8 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * is rounded to bf16 for bf16 inputs (what that takes from the entry at the
  * target is given back where the token is the only one with it, to dh always)
  * and split like them for fp32.  A token whose dloss is 0 has no gradient,
- * whatever its h holds.  The vocabulary is taken in pieces; the workspace holds one piece's P (half a
- * gigabyte at most, or 1024 columns), and dh in fp32.
+ * whatever its h holds.  The vocabulary is taken in pieces; the workspace holds
+ * one piece's P (half a gigabyte at most, or 1024 columns), and dh in fp32.
  *   workspace  device, >= the _workspace_size(...) bytes of the call, 256-byte
  *           aligned, contents on entry irrelevant
  * Equal calls give equal bits.

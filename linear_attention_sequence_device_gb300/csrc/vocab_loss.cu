@@ -568,7 +568,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
             float f = p.scale;
             if (F32) {
                 if (KIND == K_LSE) {
-                    f = r < p.T ? pow2(-__ldg(p.he + r)) * p.scale : 0.f;
+                    // half of h's before w's, half behind: alone it may pass fp32's range where w's brings it back
+                    f = r < p.T ? pow2(-__ldg(p.he + r) / 2) * p.scale : 0.f;
                 } else if (KIND == K_P) {
                     // (beyond the range of one factor the logits are below 2^-80, or infinite)
                     const int k = -exponent_for(__uint_as_float(__ldg(p.most)), 14) - (r < p.T ? __ldg(p.he + r) : 0);
@@ -591,11 +592,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                         if (F32) e = __ldg(reinterpret_cast<const int4*>(p.we + c0 + i));
                         const int es[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x = F32 ? acc[i + j] * f * pow2(-es[j]) : acc[i + j] * f;
-                            acc[i + j] = i + j < left ? x : -INFINITY;
-                            top = fmaxf(top, acc[i + j]);
-                        }
+                        for (int j = 0; j < 4; ++j) acc[i + j] = F32 ? acc[i + j] * f * pow2(-es[j]) : acc[i + j] * f;
+                    }
+                    if (F32) {  // (read again: a register less)
+                        int k = 0;
+                        if (real) asm volatile("ld.global.s32 %0, [%1];" : "=r"(k) : "l"(p.he + r));
+                        f = pow2(-k - -k / 2);
+                    }
+#pragma unroll
+                    for (int i = 0; i < EW; ++i) {
+                        if (F32) acc[i] *= f;
+                        if (i >= left) acc[i] = -INFINITY;
+                        top = fmaxf(top, acc[i]);
                     }
                     if (o >= 0 && o < EW) {
                         float v = 0.f;

@@ -196,6 +196,16 @@ def test_wide_ranges_in_fp32(g):
         check(g, h * s, w / s, t, dloss, names=("loss", "lse"))
 
 
+@pytest.mark.parametrize("s", [1e-34, 1e34])
+@pytest.mark.parametrize("T", [40, 300])
+def test_inputs_at_the_ends_of_fp32_whose_products_are_not(g, T, s):
+    h, w, t, dloss = inputs(T, 700, 200, F32, seed=19)
+    check(g, h * s, w / s, t, dloss, names=("loss", "lse"))
+    _, lse = g.gdn_vocab_loss_fwd(h * s, w / s, t)
+    r = g.gdn_vocab_loss_bwd(dloss, h * s, w / s, t, lse)
+    assert torch.isfinite(r["dh"]).all() and torch.isfinite(r["dw"]).all()
+
+
 def test_large_logits(g):
     """Logits of a few hundred: sums of exponentials far from one another, tokens that are certain."""
     for dtype in (BF, F32):
