@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libgdncp.so")
 SOURCES = ["api.cu", "plan.cu", "conv.cu", "chunk_bf16.cu", "chunk_f32.cu", "chunk_tc.cu", "schedule.cu",
            "combine.cu", "noalloc.cu", "layout.cu", "backward.cu", "shard_bwd.cu", "mchain.cu",
            "ssm_conv.cu", "ssm_scan.cu", "ssm_scan_bwd.cu", "block_norm.cu",
-           "rule_step.cu", "embed.cu", "vocab_loss.cu"]
+           "rule_step.cu", "embed.cu", "vocab_loss.cu", "vocab_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-rdc=true", "-Xcompiler", "-fPIC", "-I", INCLUDE,
               "-I", CSRC]

@@ -28,11 +28,14 @@
 // each operand a CTA, from a ring of six stages of 64 along K by TMA; accumulators in tensor
 // memory, two of them, so that the epilogue's sixteen warps run beside the next tile.  One
 // CTA an SM walks tiles by its number.
+//
+// Calls of few tokens go to vocab_few.cu: all that follows here is a tile of 256 tokens or more.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "ssm_common.cuh"
 #include "tc_util.cuh"
+#include "vocab_few.cuh"
 
 namespace gdn {
 
@@ -309,7 +312,7 @@ constexpr int kChunkF32 = 4;   // the most steps of a chunk
 constexpr int kChunkBf16 = 12;
 // and of the logits of up to kFewTokens tokens: the loss of one token may be a small difference of
 // large logits, which no other token's outweighs (single tokens: losses off by up to 3.8e-6
-// of themselves with twelve steps, 1.2e-6 with two; 130 tokens of 32000 x 2048, both
+// of themselves with twelve steps, 1.2e-6 with two, before those had kernels of their own; 130 tokens of 32000 x 2048, both
 // directions: 149 us with twelve, 156 with four, 169 with two)
 constexpr int kChunkFew = 2, kFewTokens = 64;
 
@@ -1069,6 +1072,7 @@ int dh_splits(int T, int W, int cols) {
 struct Plan {
     size_t h, hw, w, stat, at, p, acc, lo, only, he, pa, we, most, total;
     int piece, splits, ldacc;
+    bool few;
 };
 Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     Plan l{};
@@ -1076,6 +1080,22 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     const int parts = dt == GDN_F32 ? 2 : 1;
     const int64_t ld = round8(W);
     const int64_t t = T > 0 ? T : 1;
+    if (few_takes((int)t, V, W, dt)) {
+        l.few = true;
+        if (!grad) {
+            l.stat = o;
+            o += up256(sizeof(float2) * (size_t)few_blocks((int)t, V) * t);
+            l.at = o;
+            o += up256(sizeof(float) * t);
+        } else {
+            l.p = o;
+            o += up256(sizeof(float) * (size_t)V * t);
+            l.acc = o;
+            o += up256(sizeof(float) * (size_t)few_parts((int)t, V, W, dt) * t * W);
+        }
+        l.total = o;
+        return l;
+    }
     if (grad || !direct(dt, W)) {
         l.h = o;
         o += up256((size_t)parts * t * ld * 2);
@@ -1285,6 +1305,15 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     cudaStream_t s = (cudaStream_t)stream;
     char* ws = static_cast<char*>(workspace);
     const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 2 : 1;
+    if (l.few) {
+        float2* stat = reinterpret_cast<float2*>(ws + l.stat);
+        float* at = reinterpret_cast<float*>(ws + l.at);
+        if ((st = few_logits({h, ldh, w, ldw, dtype, targets, wide, T, vocab, width, scale}, stat, at, s)) != GDN_OK)
+            return st;
+        lse_join_kernel<<<(unsigned)div_up(T, 32), 256, 0, s>>>(stat, few_blocks(T, vocab), T, vocab, at, targets, wide,
+                                                                loss, lse);
+        return check_launch("lse_join_kernel");
+    }
     Operand H{h, ldh}, Wt{w, ldw};
     if (!direct(dtype, width)) {
         H = {ws + l.h, round8(width)};
@@ -1343,6 +1372,9 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         return fail(GDN_ERR_INVALID_ARG, "dloss, lse or dh is NULL, or dh's row stride < width=%d", width);
     char* ws = static_cast<char*>(workspace);
     const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 2 : 1;
+    if (l.few)
+        return few_grads({h, ldh, w, ldw, dtype, targets, wide, T, vocab, width, scale}, dloss, lse,
+                         reinterpret_cast<float*>(ws + l.p), reinterpret_cast<float*>(ws + l.acc), dh, lddh, dw, lddw, s);
     const int ldp = round8(width);
     int* only = nullptr;
     Operand H{ws + l.h, ldp}, Hw{ws + (dtype == GDN_F32 ? l.hw : l.h), ldp}, Wt{w, ldw};

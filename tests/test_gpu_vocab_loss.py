@@ -310,6 +310,106 @@ def test_far_weights(g):
     assert rel(r["dw"][-300:], P.t() @ L.dbl(h)) <= 2 ** -8 and rel(r["dh"], P @ L.dbl(w[-300:])) <= 2 ** -8
 
 
+# ---- few tokens: kernels of their own up to 8 tokens of bf16, 16 of fp32 ----------
+
+FEW = [(1, 8, 1), (1, 9, 3), (2, 100, 8), (3, 513, 66), (4, 1000, 1001), (5, 3001, 520), (7, 700, 4096), (8, 4099, 64),
+       (9, 800, 130), (13, 2000, 34), (16, 1023, 2048), (17, 300, 100), (4, 7, 64), (1, 40, 20000), (8, 60, 8200)]
+
+
+@pytest.mark.parametrize("T,V,W", FEW)
+@pytest.mark.parametrize("dtype,index", [(BF, I32), (F32, I64)])
+@pytest.mark.parametrize("scale", [1.0, -0.7])
+def test_few_tokens(g, T, V, W, dtype, index, scale):
+    check(g, *inputs(T, V, W, dtype, seed=21, index=index, out=0.2), scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 4, 6, 15])
+@pytest.mark.parametrize("W,pad,skip", [(66, 2, 2), (66, 1, 1), (64, 4, 4), (65, 0, 0), (128, 8, 0), (1346, 0, 0)])
+def test_few_tokens_with_rows_of_any_alignment(g, dtype, T, W, pad, skip):
+    check(g, *inputs(T, 777, W, dtype, seed=22, pad=pad, skip=skip))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("W", [72, 1001])
+def test_few_tokens_left_out_and_behind_the_vocabulary(g, dtype, W):
+    h, w, t, dloss = inputs(6, 500, W, dtype, seed=23, out=0.0)
+    t[2], dloss[3] = -5, 0.0
+    h[2:4] = float("nan")
+    loss, lse = g.gdn_vocab_loss_fwd(h, w, t)
+    assert loss[2] == 0 and torch.isnan(loss[3])
+    r = g.gdn_vocab_loss_bwd(dloss, h, w, t, lse)
+    assert (r["dh"][2:4] == 0).all()
+    keep = torch.tensor([0, 1, 4, 5], device="cuda")
+    one = g.gdn_vocab_loss_bwd(dloss[keep], h[keep], w, t[keep], lse[keep])
+    ref = L.vocab_loss(L.dbl(h[keep]), L.dbl(w), t[keep], 1.0, dtype is F32, L.dbl(dloss[keep]))
+    for x, n in ((r["dh"][keep], "dh"), (r["dw"], "dw"), (one["dw"], "dw")):
+        R.assert_within(x, ref[n].cpu(), ref[n + "_b"].cpu(), n)
+    h, w, t, dloss = inputs(3, 500, W, dtype, seed=24, out=0.0)
+    t[1] = 500
+    loss, lse = g.gdn_vocab_loss_fwd(h, w, t)
+    r = g.gdn_vocab_loss_bwd(dloss, h, w, t, lse)
+    assert torch.isnan(loss[1]) and torch.isfinite(loss[0::2]).all() and torch.isfinite(lse).all()
+    assert torch.isnan(r["dh"][1]).all() and torch.isfinite(r["dh"][0::2]).all() and torch.isnan(r["dw"]).all()
+
+
+@pytest.mark.parametrize("dtype,T", [(BF, 1), (BF, 7), (F32, 4), (F32, 16)])
+def test_few_tokens_in_errors_in_norm_equal_bits_and_captured(g, dtype, T):
+    """Errors in norm: dh and dw are fp32 sums, rounded once for bf16 (2^-8 at most, by 1 / sqrt(3) of that in norm
+    and less)."""
+    h, w, t, dloss = inputs(T, 5003, 1024, dtype, seed=25, out=0.0)
+    ref = L.vocab_loss(L.dbl(h), L.dbl(w), t, 1.0, dtype is F32, L.dbl(dloss))
+    def both():
+        loss, lse = g.gdn_vocab_loss_fwd(h, w, t)
+        return dict(loss=loss, lse=lse, **g.gdn_vocab_loss_bwd(dloss, h, w, t, lse))
+    a = both()
+    for n in ("dh", "dw"):
+        assert rel(a[n], ref[n]) <= (2 ** -8 / 3 ** 0.5 if dtype is BF else 2e-6)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b = both()
+    for x in b.values():
+        x.fill_(7)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_few_tokens_rows_around_stay_and_far_weights(g):
+    """dh and dw of the C ABI in wider rows: what lies between stays; weights beyond 2^31 elements."""
+    from linear_attention_sequence_device_gb300 import binding
+    lib = binding.load()
+    T, V, W = 5, 301, 70
+    h, w, t, dloss = inputs(T, V, W, F32, seed=26)
+    _, lse = g.gdn_vocab_loss_fwd(h, w, t)
+    want = g.gdn_vocab_loss_bwd(dloss, h, w, t, lse)
+    dh, dw = torch.full((T, W + 3), 9.0, device="cuda"), torch.full((V, W + 5), 9.0, device="cuda")
+    ws = torch.empty(g.vocab_loss_bwd_workspace_size(T, V, W, F32), dtype=torch.uint8, device="cuda")
+    st = lib.gdn_vocab_loss_bwd(dloss.data_ptr(), h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0), 0, t.data_ptr(),
+                                64, lse.data_ptr(), T, V, W, 1.0, dh.data_ptr(), W + 3, dw.data_ptr(), W + 5,
+                                ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert (dh[:, W:] == 9).all() and (dw[:, W:] == 9).all()
+    assert rel(dh[:, :W], L.dbl(want["dh"])) <= 1e-6 and rel(dw[:, :W], L.dbl(want["dw"])) <= 1e-6
+    V, W, q = (1 << 19) + 200, 4160, gen(27)
+    w = torch.zeros(V, W, dtype=BF, device="cuda")
+    w[-300:] = view(300, W, BF, q, std=W ** -0.5)
+    h, t, dloss = view(3, W, BF, q), V - 1 - torch.randint(0, 300, (3,), generator=q, device="cuda"), torch.ones(3, device="cuda")
+    loss, lse = g.gdn_vocab_loss_fwd(h, w, t)
+    x = L.dbl(h) @ L.dbl(w[-300:]).t()
+    z = torch.logaddexp(torch.logsumexp(x, 1), torch.log(torch.tensor(V - 300.0, device="cuda").double()))
+    assert rel(lse, z) <= 1e-6
+    r = g.gdn_vocab_loss_bwd(dloss, h, w, t, lse)
+    P = torch.exp(x - z[:, None])
+    P[torch.arange(3), t - (V - 300)] -= 1
+    assert rel(r["dw"][-300:], P.t() @ L.dbl(h)) <= 2 ** -8 and rel(r["dh"], P @ L.dbl(w[-300:])) <= 2 ** -8
+
+
 def test_wrong_arguments_raise(g):
     h, w, t, dloss = inputs(10, 30, 16, BF, seed=19)
     lse = torch.zeros(10, device="cuda")
