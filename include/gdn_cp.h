@@ -732,7 +732,7 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * h, and for w in the forward; one for w in the backward, its token's dloss for
  * P), below that it is off by 2^-40 of it.
  * Calls of few tokens (8 of bf16, 16 of fp32, at widths up to 6400; 4 up to
- * 12800, 1 up to 51200) form products, sums and P in fp32.
+ * 12800, 1 up to 51200; vocab 64 or more) form products, sums and P in fp32.
  * An expired wait (gdn_device_timeouts) leaves the outputs incomplete.
  *
  * gdn_vocab_loss_bwd: gradients of the above for dloss, from the forward's lse

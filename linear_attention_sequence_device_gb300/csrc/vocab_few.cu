@@ -454,6 +454,7 @@ int up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 //   bf16  64000 x 2048   1 token  48 + 138, 122 + 257;  8  73 + 211, 103 + 233;  16  127 + 440, 102 + 235
 //         64000 x 2046   1 token  49 + 165, 218 + 431;  8  73 + 261, 200 + 398;  16  135 + 449, 200 + 398
 constexpr int kFewF32 = 16, kFewBf16 = 8;
+constexpr int kLeastRows = 64;  // of w: fewer would leave most warps without any
 constexpr size_t kSmem = 200 << 10;  // of h
 constexpr int kMaxParts = 608;
 
@@ -540,7 +541,7 @@ gdn_status grads_tokens(const GradArgs& p, int n, void* dh, int64_t lddh, cudaSt
 }  // namespace
 
 bool few_takes(int T, int V, int W, gdn_dtype dtype) {
-    return V >= rows_of(1) && T <= (dtype == GDN_F32 ? kFewF32 : kFewBf16) &&
+    return V >= kLeastRows && T <= (dtype == GDN_F32 ? kFewF32 : kFewBf16) &&
            sizeof(float) * tokens_of(T) * (size_t)padded(W, 256) <= kSmem;
 }
 
