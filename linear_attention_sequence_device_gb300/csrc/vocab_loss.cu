@@ -811,30 +811,34 @@ __device__ __forceinline__ int64_t raw_target(const void* targets, int wide, int
     return wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
 }
 
-// bf16 [rows][W] -> [rows][ld].  For the gradients (targets): tokens that are left out, or whose
-// dloss is zero, are rows of zeros (0 times an infinity there would reach every weight's
-// gradient), and `only` gets the token of every target that has just one.  Columns of W
-// and beyond are written as zeros.
-__global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* __restrict__ x, int64_t ldx, int64_t rows, int W,
-                                                   int ld, const void* targets, int wide, const float* dloss, int vocab,
-                                                   int* only, __nv_bfloat16* __restrict__ out) {
+// bf16 [rows][W] -> [rows][ld]: the tokens' h, then w (V = 0: h alone).  For the gradients
+// (targets): tokens that are left out, or whose dloss is zero, are rows of zeros (0 times an
+// infinity there would reach every weight's gradient), and `only` gets the token of every
+// target that has just one.  Columns of W and beyond are written as zeros.
+__global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* __restrict__ h, int64_t ldh, int T,
+                                                   const __nv_bfloat16* __restrict__ w, int64_t ldw, int V, int W, int ld,
+                                                   const void* targets, int wide, const float* dloss, int vocab, int* only,
+                                                   __nv_bfloat16* __restrict__ out_h, __nv_bfloat16* __restrict__ out_w) {
     const int nv = ld / 8;
-    const int64_t n = rows * nv;
+    const int64_t n = ((int64_t)T + V) * nv;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / nv;
+        int64_t r = i / nv;
         const int c = (int)(i - r * nv) * 8;
         bool real = true;
-        if (targets) {
+        const bool of_w = r >= T;
+        if (of_w) {
+            r -= T;
+        } else if (targets) {
             const int64_t tgt = raw_target(targets, wide, r);
             real = tgt >= 0 && __ldg(dloss + r) != 0.f;
             // the one token with a target; a second one makes it -2, whatever their order
             if (c == 0 && real && tgt < vocab && atomicCAS(only + tgt, -1, (int)r) != -1) only[tgt] = -2;
         }
-        const __nv_bfloat16* s = x + r * ldx + c;
+        const __nv_bfloat16* s = (of_w ? w + r * ldw : h + r * ldh) + c;
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = real && c + j < W ? __bfloat162float(s[j]) : 0.f;
-        store8(out + r * ld + c, f);
+        store8((of_w ? out_w : out_h) + r * ld + c, f);
     }
 }
 
@@ -891,54 +895,68 @@ __global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h,
 // For the loss alone both are scaled by their rows, which takes one pass over w: a warp
 // finds a row's exponent and splits it, the second time out of the caches (scoring 513 x
 // 32000 x 1024: 171 us with a pass for w's largest value before, 150 so).
-__global__ void __launch_bounds__(256) split_rows_kernel(const float* __restrict__ x, int64_t ldx, int64_t rows, int W,
-                                                         int ld, int* __restrict__ exps, __half* __restrict__ out) {
+__global__ void __launch_bounds__(256) split_rows_kernel(const float* __restrict__ h, int64_t ldh, int T,
+                                                         const float* __restrict__ w, int64_t ldw, int V, int W, int ld,
+                                                         int* __restrict__ he, int* __restrict__ we,
+                                                         __half* __restrict__ out_h, __half* __restrict__ out_w) {
     const int lane = threadIdx.x & 31;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8) {
-        const float* s = x + r * ldx;
+    const int64_t n = (int64_t)V + T;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * 8) {
+        const bool of_w = i < V;
+        const int64_t r = of_w ? i : i - V, low = of_w ? V : T;  // the second parts' first row
+        const float* s = of_w ? w + r * ldw : h + r * ldh;
+        __half* out = (of_w ? out_w : out_h) + r * ld;
         float m = 0.f;
 #pragma unroll 8
         for (int c = lane; c < W; c += 32) m = fmaxf(m, fabsf(__ldg(s + c)));  // (a NaN is left out)
 #pragma unroll
         for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
         const int k = exponent_for(m, 14);
-        if (lane == 0) exps[r] = k;
+        if (lane == 0) (of_w ? we : he)[r] = k;
         const float k1 = pow2(k);
 #pragma unroll 4
         for (int c = 2 * lane; c < ld; c += 64) {
             const float a = c < W ? __ldg(s + c) * k1 : 0.f, b = c + 1 < W ? __ldg(s + c + 1) * k1 : 0.f;
             const __half2 v = __floats2half2_rn(a, b);
             const float va = __low2float(v), vb = __high2float(v);
-            *reinterpret_cast<__half2*>(out + r * ld + c) = v;
-            *reinterpret_cast<__half2*>(out + (rows + r) * ld + c) =
+            *reinterpret_cast<__half2*>(out + c) = v;
+            *reinterpret_cast<__half2*>(out + low * ld + c) =
                 __floats2half2_rn(isfinite(va) ? a - va : 0.f, isfinite(vb) ? b - vb : 0.f);
         }
     }
 }
 
-// fp32 [rows][W] -> two fp16 parts [2][rows][ld] of its scaled values.  he: by its rows' own
-// exponents (logits' h); pa: by most[1]'s less the row's pa, zeros where a token does not
-// count (dw's h); neither: by most[0]'s (w).
-__global__ void __launch_bounds__(256) split_kernel(const float* __restrict__ x, int64_t ldx, int64_t rows, int W, int ld,
+// fp32 [rows][W] -> two fp16 parts [2][rows][ld] of its scaled values, in one launch: w by
+// most[0]'s exponent; h for the logits by its rows' own, he; h for dw by most[1]'s less the
+// row's pa, zeros where a token does not count.
+__global__ void __launch_bounds__(256) split_kernel(const float* __restrict__ h, int64_t ldh, int T,
+                                                    const float* __restrict__ w, int64_t ldw, int V, int W, int ld,
                                                     const int* he, const int* pa, const unsigned* most,
                                                     const void* targets, int wide, const float* dloss,
-                                                    __half* __restrict__ out) {
+                                                    __half* __restrict__ out_h, __half* __restrict__ out_hw,
+                                                    __half* __restrict__ out_w) {
     const int nv = ld / 8;
-    const int64_t n = rows * nv;
-    const int all = he ? 0 : exponent_for(__uint_as_float(__ldg(most + (pa ? 1 : 0))), 14);
+    const int64_t n = ((int64_t)V + 2 * (int64_t)T) * nv;
+    const int all = exponent_for(__uint_as_float(__ldg(most)), 14), all_h = exponent_for(__uint_as_float(__ldg(most + 1)), 14);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / nv;
+        int64_t r = i / nv, rows = V;
         const int c = (int)(i - r * nv) * 8;
         int k = all;
         bool real = true;
-        if (he) k = __ldg(he + r);
-        if (pa) {
-            k -= __ldg(pa + r);
-            real = raw_target(targets, wide, r) >= 0 && __ldg(dloss + r) != 0.f;
+        const float* s = w + r * ldw + c;
+        __half* out = out_w;
+        if (r >= V) {
+            r -= V;
+            rows = T;
+            const bool of_dw = r >= T;
+            if (of_dw) r -= T;
+            s = h + r * ldh + c;
+            out = of_dw ? out_hw : out_h;
+            k = of_dw ? all_h - __ldg(pa + r) : __ldg(he + r);
+            if (of_dw) real = raw_target(targets, wide, r) >= 0 && __ldg(dloss + r) != 0.f;
         }
         // (up to 2^252: in two steps)
         const float k1 = pow2(k / 2), k2 = pow2(k - k / 2);
-        const float* s = x + r * ldx + c;
         uint4 hi, lo;
         __half2* h2 = reinterpret_cast<__half2*>(&hi);
         __half2* l2 = reinterpret_cast<__half2*>(&lo);
@@ -1208,11 +1226,12 @@ unsigned grid_for(int64_t n) {
     return (unsigned)(b < 1 ? 1 : b < most ? b : most);
 }
 
-gdn_status pack(const void* x, int64_t ldx, int64_t rows, int W, const void* targets, int wide, const float* dloss,
-                int vocab, int* only, void* out, cudaStream_t s) {
+gdn_status pack(const void* h, int64_t ldh, int T, const void* w, int64_t ldw, int V, int W, const void* targets, int wide,
+                const float* dloss, int vocab, int* only, void* out_h, void* out_w, cudaStream_t s) {
     const int ld = round8(W);
-    pack_kernel<<<grid_for(rows * (ld / 8)), 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), ldx, rows, W, ld, targets,
-                                                          wide, dloss, vocab, only, static_cast<__nv_bfloat16*>(out));
+    pack_kernel<<<grid_for(((int64_t)T + V) * (ld / 8)), 256, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(h), ldh, T, static_cast<const __nv_bfloat16*>(w), ldw, V, W, ld, targets, wide,
+        dloss, vocab, only, static_cast<__nv_bfloat16*>(out_h), static_cast<__nv_bfloat16*>(out_w));
     return check_launch("pack_kernel");
 }
 // fp32 inputs of the gradients: their scalings, then their parts into the workspace
@@ -1227,13 +1246,9 @@ gdn_status split(const void* h, int64_t ldh, int T, const void* w, int64_t ldw, 
     const int64_t blocks = div_up((int64_t)T + V, 8), wave = (int64_t)device_sm_count() * 8;
     scale_kernel<<<(unsigned)(blocks < wave ? blocks : wave), 256, 0, s>>>(hf, ldh, T, wf, ldw, V, W, targets, wide, dloss,
                                                                            scale, he, pa, most);
-    split_kernel<<<grid_for((int64_t)V * (ld / 8)), 256, 0, s>>>(wf, ldw, V, W, ld, nullptr, nullptr, most, nullptr, 0,
-                                                                 nullptr, reinterpret_cast<__half*>(ws + l.w));
-    const unsigned g = grid_for((int64_t)T * (ld / 8));
-    split_kernel<<<g, 256, 0, s>>>(hf, ldh, T, W, ld, he, nullptr, most, nullptr, 0, nullptr,
-                                   reinterpret_cast<__half*>(ws + l.h));
-    split_kernel<<<g, 256, 0, s>>>(hf, ldh, T, W, ld, nullptr, pa, most, targets, wide, dloss,
-                                   reinterpret_cast<__half*>(ws + l.hw));
+    split_kernel<<<grid_for(((int64_t)V + 2 * (int64_t)T) * (ld / 8)), 256, 0, s>>>(
+        hf, ldh, T, wf, ldw, V, W, ld, he, pa, most, targets, wide, dloss, reinterpret_cast<__half*>(ws + l.h),
+        reinterpret_cast<__half*>(ws + l.hw), reinterpret_cast<__half*>(ws + l.w));
     return check_launch("split_kernel");
 }
 
@@ -1320,16 +1335,14 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
         Wt = {ws + l.w, round8(width)};
         if (dtype == GDN_F32) {
             const int ld = round8(width);
-            const int64_t wave = (int64_t)device_sm_count() * 8, ht = div_up(T, 8), wt = div_up(vocab, 8);
-            split_rows_kernel<<<(unsigned)(wt < wave ? wt : wave), 256, 0, s>>>(
-                static_cast<const float*>(w), ldw, vocab, width, ld, reinterpret_cast<int*>(ws + l.we),
+            const int64_t wave = (int64_t)device_sm_count() * 8, n = div_up((int64_t)T + vocab, 8);
+            split_rows_kernel<<<(unsigned)(n < wave ? n : wave), 256, 0, s>>>(
+                static_cast<const float*>(h), ldh, T, static_cast<const float*>(w), ldw, vocab, width, ld,
+                reinterpret_cast<int*>(ws + l.he), reinterpret_cast<int*>(ws + l.we), reinterpret_cast<__half*>(ws + l.h),
                 reinterpret_cast<__half*>(ws + l.w));
-            split_rows_kernel<<<(unsigned)(ht < wave ? ht : wave), 256, 0, s>>>(
-                static_cast<const float*>(h), ldh, T, width, ld, reinterpret_cast<int*>(ws + l.he),
-                reinterpret_cast<__half*>(ws + l.h));
             st = check_launch("split_rows_kernel");
-        } else if ((st = pack(h, ldh, T, width, nullptr, 0, nullptr, 0, nullptr, ws + l.h, s)) == GDN_OK) {
-            st = pack(w, ldw, vocab, width, nullptr, 0, nullptr, 0, nullptr, ws + l.w, s);
+        } else {
+            st = pack(h, ldh, T, w, ldw, vocab, width, nullptr, 0, nullptr, 0, nullptr, ws + l.h, ws + l.w, s);
         }
         if (st != GDN_OK) return st;
     }
@@ -1384,9 +1397,8 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
     } else {
         only = reinterpret_cast<int*>(ws + l.only);
         if (cudaMemsetAsync(only, 0xff, sizeof(int) * (size_t)vocab, s) != cudaSuccess) return check_launch("memset");
-        if ((st = pack(h, ldh, T, width, targets, wide, dloss, vocab, only, ws + l.h, s)) != GDN_OK) return st;
-        if (!direct(dtype, width) &&
-            (st = pack(w, ldw, vocab, width, nullptr, 0, nullptr, 0, nullptr, ws + l.w, s)) != GDN_OK)
+        if ((st = pack(h, ldh, T, w, ldw, direct(dtype, width) ? 0 : vocab, width, targets, wide, dloss, vocab, only,
+                       ws + l.h, ws + l.w, s)) != GDN_OK)
             return st;
     }
     const bool store = dtype == GDN_BF16 && (reinterpret_cast<uintptr_t>(dw) & 15u) == 0 && lddw % 8 == 0;
