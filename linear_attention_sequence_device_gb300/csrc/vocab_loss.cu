@@ -104,12 +104,25 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+template <bool ALONE>
+__device__ __forceinline__ void arrive(uint32_t addr) {
+    if (ALONE) asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(addr) : "memory");
+    else arrive_cluster(addr);
+}
 // one box into this CTA's shared memory; its bytes are counted on a barrier of either CTA
 __device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, int y, int z, uint32_t mbar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
         "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
+// the same without a pair
+__device__ __forceinline__ void load_box_alone(uint32_t dst, const void* map, int x, int y, int z, uint64_t* mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_addr(mbar))
         : "memory");
 }
 __device__ __forceinline__ void store_box(const void* map, int x, int y, int z, uint32_t src) {
@@ -159,8 +172,8 @@ __device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, volati
 // ---- the product kernel ------------------------------------------------------
 
 constexpr int BM = 256, BN = 256, BK = 64;      // a pair's tile
-constexpr int HALF = 128;                       // rows of an operand a CTA
-constexpr int OPB = HALF * BK * 2;              // bytes of one operand of a stage
+constexpr int HALF = 128;                       // rows of an operand a CTA; a tile's without a pair
+constexpr int OPB = HALF * BK * 2;              // bytes of as many rows of a stage
 constexpr int GT = 576;                         // threads: a warp of loads, one of products, 16 of epilogue
 constexpr int EW = 64;                          // columns of an epilogue warp: a quarter of the tile's
 constexpr int SC = 32;                          // columns of a staged piece of a result
@@ -168,10 +181,19 @@ constexpr int OUTB = HALF * SC * 2;             // its bytes; each quarter of th
 
 enum Kind { K_LSE = 0, K_P = 1, K_GRAD = 2 };
 
+// Tokens of one CTA's rows, or a little more: a pair's second CTA would multiply rows of nothing.  Then
+// (ALONE) each CTA forms 128 x 256 tiles of its own, from all of B.
+constexpr int kAloneTokens = 128;
+
+// bytes of a stage: the CTA's rows of A, its half of B or all of it
+template <bool ALONE>
+__host__ __device__ constexpr int stage_bytes() {
+    return ALONE ? 3 * OPB : 2 * OPB;
+}
 // Stages of the ring: results leave through shared memory but for the logits' maxima and sums
-template <int KIND>
+template <int KIND, bool ALONE>
 __host__ __device__ constexpr int stages() {
-    return KIND == K_LSE ? 6 : 5;
+    return ALONE ? (KIND == K_LSE ? 4 : 3) : KIND == K_LSE ? 6 : 5;
 }
 template <int KIND>
 __host__ __device__ constexpr int staged_bytes() {
@@ -182,11 +204,13 @@ struct Ctl {
     uint32_t tmem;
     int abort;
 };
-template <int KIND>
+template <int KIND, bool ALONE>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)stages<KIND>() * 2 * OPB + staged_bytes<KIND>() + sizeof(Ctl);
+    return 1024 + (size_t)stages<KIND, ALONE>() * stage_bytes<ALONE>() + staged_bytes<KIND>() + sizeof(Ctl);
 }
-static_assert(smem_bytes<K_LSE>() <= 227 * 1024 && smem_bytes<K_GRAD>() <= 227 * 1024, "shared memory of a CTA");
+static_assert(smem_bytes<K_LSE, false>() <= 227 * 1024 && smem_bytes<K_GRAD, false>() <= 227 * 1024 &&
+                  smem_bytes<K_LSE, true>() <= 227 * 1024 && smem_bytes<K_GRAD, true>() <= 227 * 1024,
+              "shared memory of a CTA");
 
 struct Maps {
     CUtensorMap a, b;    // logits: h, w.  Gradients of h: P, w
@@ -195,7 +219,7 @@ struct Maps {
 };
 
 struct GemmParams {
-    int mt, nt, group;    // tiles of 256 (logits; gradients of h), rows of tiles walked together
+    int mt, nt, group;    // tiles (logits; gradients of h), rows of tiles walked together
     int kb;               // K steps
     int chunk;            // of which so many are added up at a time
     int splits, kper;     // gradients of h: K cut into splits of kper steps
@@ -234,11 +258,11 @@ struct Unit {
     bool second;  // a gradient of w
 };
 
-// Unit i of a pair of CTAs, false behind its last.  Logits: tile pair + i pairs.  Gradients:
+// Unit i of a pair of CTAs (or of one alone), false behind its last.  Logits: tile pair + i pairs.  Gradients:
 // dh's tiles the same way, then dw's, of which the pairs that have a tile of dh less run
 // `early` more, so that all end together (round robin over both kinds left the last fifth
 // of a short call's time to a few pairs).
-template <int KIND>
+template <int KIND, bool ALONE>
 __device__ __forceinline__ bool unit(const GemmParams& p, int pair, int pairs, int i, Unit& r) {
     r.second = false;
     r.split = 0;
@@ -327,15 +351,15 @@ __device__ __forceinline__ void sub_at(float& x, float g, int o, int i) {
 
 // A warp's 32 rows and the 32 columns behind j of its quarter, staged at `mine`, to dh's sums
 // or dw, a row at a time.  (What they need is found again: the sums leave few registers.)
-template <int KIND, bool F32>
+template <int KIND, bool F32, bool ALONE>
 __device__ __forceinline__ void store_rows(const GemmParams& p, int pair, int pairs, int u, uint32_t rank, uint32_t mine,
                                            int j) {
     int t;
     asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
     asm volatile("" : "+r"(u));
     Unit w;
-    unit<KIND>(p, pair, pairs, u, w);
-    const int l = t & 31, row = w.m * BM + (int)rank * HALF + ((t >> 5) & 3) * 32;
+    unit<KIND, ALONE>(p, pair, pairs, u, w);
+    const int l = t & 31, row = w.m * (ALONE ? HALF : BM) + (int)rank * HALF + ((t >> 5) & 3) * 32;
     const int col = w.n * BN + ((t >> 5) - 2) / 4 * EW + j + l;
     const int n = min(32, (w.second ? p.V : p.T) - row);
     if (col >= (w.second ? p.W : p.ldacc)) return;
@@ -361,21 +385,21 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, int pair, int pa
     }
 }
 
-template <int KIND, bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
+template <int KIND, bool F32, bool ALONE>
+__global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
     vocab_gemm_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
     constexpr bool CH = chunked<KIND, F32>();
     const int ch = p.chunk;
     constexpr int NP = F32 ? 3 : 1;  // products of parts
-    constexpr int STAGES = stages<KIND>();
+    constexpr int STAGES = stages<KIND, ALONE>(), STAGE = stage_bytes<ALONE>(), TM = ALONE ? HALF : BM;
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
     const uint32_t ring = tc::smem_addr(base);
-    unsigned char* staged = base + STAGES * 2 * OPB;
+    unsigned char* staged = base + STAGES * STAGE;
     Ctl& c = *reinterpret_cast<Ctl*>(staged + staged_bytes<KIND>());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cta_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const uint32_t rank = ALONE ? 0u : cta_rank();
+    const int pair = ALONE ? blockIdx.x : blockIdx.x >> 1, pairs = ALONE ? gridDim.x : gridDim.x >> 1;
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
             tc::mbar_init(&c.full[s], 1);
@@ -383,17 +407,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&c.done[b], 1);
-            tc::mbar_init(&c.free_[b], 32);  // a warp of the epilogue of either CTA each
+            tc::mbar_init(&c.free_[b], ALONE ? 16 : 32);  // a warp of the epilogue (of either CTA) each
         }
         c.abort = 0;
     }
-    if (warp == 0) {
+    if (ALONE) {
+        if (warp == 0) tc::tmem_alloc(&c.tmem, 512);
+    } else if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::smem_addr(&c.tmem)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     tc::fence_before();
     __syncthreads();
-    cluster_sync();
+    if (!ALONE) cluster_sync();
     tc::fence_after();
     const uint32_t tmem = c.tmem;
     Unit w;
@@ -403,8 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         int s = 0, phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int i = 0; ok && unit<KIND>(p, pair, pairs, i, w); ++i) {
-            const int row_a = w.m * BM + (int)rank * HALF, row_b = w.n * BN + (int)rank * HALF;
+        for (int i = 0; ok && unit<KIND, ALONE>(p, pair, pairs, i, w); ++i) {
+            const int row_a = w.m * TM + (int)rank * HALF, row_b = w.n * BN + (int)rank * HALF;
             for (int k0 = w.k0; k0 < w.k1 && ok; k0 += CH ? ch : w.k1 - w.k0) {
                 const int k1 = CH ? min(w.k1, k0 + ch) : w.k1;
                 for (int q = 0; q < NP && ok; ++q)
@@ -413,22 +439,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                             ok = false;
                             break;
                         }
-                        if (rank == 0) tc::mbar_expect_tx(&c.full[s], 4 * OPB);
-                        const uint32_t bar = in_leader(tc::smem_addr(&c.full[s]));
-                        const uint32_t da = ring + s * 2 * OPB, db = da + OPB;
+                        if (rank == 0) tc::mbar_expect_tx(&c.full[s], ALONE ? STAGE : 2 * STAGE);
+                        const uint32_t bar = ALONE ? 0u : in_leader(tc::smem_addr(&c.full[s]));
+                        const uint32_t da = ring + s * STAGE, db = da + OPB;
                         const int za = F32 ? part_a(q) : 0, zb = F32 ? part_b(q) : 0;
+                        auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z) {
+                            if (ALONE) load_box_alone(dst, map, x, y, z, &c.full[s]);
+                            else load_box(dst, map, x, y, z, bar);
+                        };
+                        constexpr int BH = ALONE ? 2 : 1;  // halves of B
                         if (KIND != K_GRAD) {
-                            load_box(da, &maps.a, k * BK, row_a, za, bar);
-                            load_box(db, &maps.b, k * BK, row_b, zb, bar);
+                            load(da, &maps.a, k * BK, row_a, za);
+#pragma unroll
+                            for (int i = 0; i < BH; ++i) load(db + i * OPB, &maps.b, k * BK, row_b + i * HALF, zb);
                         } else if (!w.second) {  // P [t][v], K = v; w [v][column]
-                            load_box(da, &maps.a, k * BK, row_a, za, bar);
-                            load_box(db, &maps.b, row_b, k * BK, zb, bar);
-                            load_box(db + OPB / 2, &maps.b, row_b + 64, k * BK, zb, bar);
+                            load(da, &maps.a, k * BK, row_a, za);
+#pragma unroll
+                            for (int i = 0; i < 2 * BH; ++i) load(db + i * (OPB / 2), &maps.b, row_b + i * 64, k * BK, zb);
                         } else {  // P [t][v], K = t; h [t][column]
-                            load_box(da, &maps.a2, row_a, k * BK, za, bar);
-                            load_box(da + OPB / 2, &maps.a2, row_a + 64, k * BK, za, bar);
-                            load_box(db, &maps.b2, row_b, k * BK, zb, bar);
-                            load_box(db + OPB / 2, &maps.b2, row_b + 64, k * BK, zb, bar);
+                            load(da, &maps.a2, row_a, k * BK, za);
+                            load(da + OPB / 2, &maps.a2, row_a + 64, k * BK, za);
+#pragma unroll
+                            for (int i = 0; i < 2 * BH; ++i) load(db + i * (OPB / 2), &maps.b2, row_b + i * 64, k * BK, zb);
                         }
                         ++issued;
                         if (++s == STAGES) {
@@ -462,10 +494,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         // ---- products ----
         int s = 0, phase = 0, it = 0;
         bool ok = true;
-        for (int i = 0; ok && unit<KIND>(p, pair, pairs, i, w); ++i) {
+        for (int i = 0; ok && unit<KIND, ALONE>(p, pair, pairs, i, w); ++i) {
             const bool a_mn = KIND == K_GRAD && w.second, b_mn = KIND == K_GRAD;
             // (bits 7 and 10: operands of bf16 instead of fp16)
-            const uint32_t id = (tc::idesc_bf16(BM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u)) &
+            const uint32_t id = (tc::idesc_bf16(TM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u)) &
                                 (F32 ? ~(1u << 7 | 1u << 10) : ~0u);
             int k0 = w.k0;
             do {
@@ -485,23 +517,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                         break;
                     }
                     tc::fence_after();
-                    const uint32_t ra = ring + s * 2 * OPB, rb = ra + OPB;
+                    const uint32_t ra = ring + s * STAGE, rb = ra + OPB;
                     const uint64_t da = tc::desc(ra, a_mn ? OPB / 2 : 16, 1024);
                     const uint64_t db = tc::desc(rb, b_mn ? OPB / 2 : 16, 1024);
                     const uint64_t sa = a_mn ? 128 : 2, sb = b_mn ? 128 : 2;
 #pragma unroll
                     for (int j = 0; j < BK / 16; ++j) {
-                        mma_pair(d, da + sa * j, db + sb * j, id, acc);
+                        if (ALONE) tc::mma(d, da + sa * j, db + sb * j, id, acc);
+                        else mma_pair(d, da + sa * j, db + sb * j, id, acc);
                         acc = 1;
                     }
-                    commit_pair(&c.empty[s]);
+                    if (ALONE) tc::commit(&c.empty[s]);
+                    else commit_pair(&c.empty[s]);
                     if (++s == STAGES) {
                         s = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                commit_pair(&c.done[buf]);
+                if (ALONE) tc::commit(&c.done[buf]);
+                else commit_pair(&c.done[buf]);
                 ++it;
                 k0 = k1;
             } while (k0 < w.k1);
@@ -519,12 +554,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
         constexpr bool ONLY = KIND == K_GRAD && !F32;
         auto only_of = [&](int u) {
             Unit x;
-            if (!unit<KIND>(p, pair, pairs, u, x) || !x.second) return -1;
-            const int r = x.m * BM + (int)rank * HALF + (warp & 3) * 32 + lane;
+            if (!unit<KIND, ALONE>(p, pair, pairs, u, x) || !x.second) return -1;
+            const int r = x.m * TM + (int)rank * HALF + (warp & 3) * 32 + lane;
             return r < p.V ? __ldg(p.only + p.v0 + r) : -1;
         };
         int only = ONLY ? only_of(0) : -1;
-        for (int u = 0; unit<KIND>(p, pair, pairs, u, w); ++u) {
+        for (int u = 0; unit<KIND, ALONE>(p, pair, pairs, u, w); ++u) {
             const int only_next = ONLY ? only_of(u + 1) : -1;
             float acc[CH ? EW : 1];
 #pragma unroll
@@ -539,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                 __syncwarp();
                 tc::fence_after();
                 d = lanes + (uint32_t)buf * BN;
-                release = in_leader(tc::smem_addr(&c.free_[buf]));
+                release = ALONE ? tc::smem_addr(&c.free_[buf]) : in_leader(tc::smem_addr(&c.free_[buf]));
                 if constexpr (CH) {
 #pragma unroll
                     for (int j = 0; j < EW; j += 8) {
@@ -550,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                     }
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_cluster(release);
+                    if (lane == 0) arrive<ALONE>(release);
                 }
                 ++it;
             }
@@ -558,13 +593,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
             int t = tid;
             if (CH) {
                 asm volatile("" : "+r"(u));
-                unit<KIND>(p, pair, pairs, u, w);
+                unit<KIND, ALONE>(p, pair, pairs, u, w);
                 asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
             }
             const int quad = (t >> 5) & 3, quarter = ((t >> 5) - 2) >> 2, row = quad * 32 + (t & 31);
             const bool lead = quad == 0 && (t & 31) == 0;  // of the quarter: its stores
-            const uint32_t stage = ring + STAGES * 2 * OPB + (KIND == K_LSE ? 0 : quarter * 2 * OUTB);
-            const int r0 = w.m * BM + (int)rank * HALF, r = r0 + row;
+            const uint32_t stage = ring + STAGES * STAGE + (KIND == K_LSE ? 0 : quarter * 2 * OUTB);
+            const int r0 = ALONE && KIND != K_GRAD ? 0 : w.m * TM + (int)rank * HALF, r = r0 + row;
             const int c0 = w.n * BN + quarter * EW;
             // logits and sums of fp32 inputs are 2^(exponents of the scalings) times too large (dh's
             // by w's after this)
@@ -671,7 +706,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                         if (j == EW - SC) {  // the tile is read
                             tc::fence_before();
                             __syncwarp();
-                            if (lane == 0) arrive_cluster(release);
+                            if (lane == 0) arrive<ALONE>(release);
                         }
                     }
                     if (KIND == K_P) {
@@ -766,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                         if (j == EW - 32) {
                             tc::fence_before();
                             __syncwarp();
-                            if (lane == 0) arrive_cluster(release);
+                            if (lane == 0) arrive<ALONE>(release);
                         }
                     }
                     const int col = c0 + j;
@@ -790,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
                                      : "memory");
                     }
                     __syncwarp();
-                    store_rows<KIND, F32>(p, pair, pairs, u, rank, mine, j);
+                    store_rows<KIND, F32, ALONE>(p, pair, pairs, u, rank, mine, j);
                 }
             }
             only = only_next;
@@ -800,9 +835,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GT, 1)
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    cluster_sync();
+    if (!ALONE) cluster_sync();
     tc::fence_after();
-    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (ALONE) {
+        if (warp == 0) tc::tmem_dealloc(tmem, 512);
+    } else if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ---- small kernels -----------------------------------------------------------
@@ -1076,11 +1113,14 @@ int piece_cols(int T, int V, gdn_dtype dt) {
     const int64_t all = div_up(V, BN) * BN;
     return (int)(c < all ? c : all);
 }
+bool alone(int T) { return T <= kAloneTokens; }
+int rows_of_tile(int T) { return alone(T) ? HALF : BM; }
+
 // K of dh's product cut into as many splits as leave its tiles no more than the pairs of
 // CTAs; splits of 16 steps at least
 int dh_splits(int T, int W, int cols) {
-    const int64_t tiles = div_up(T, BM) * div_up(W, BN), kb = div_up(cols, BK);
-    int64_t s = device_sm_count() / 2 / tiles;
+    const int64_t tiles = div_up(T, rows_of_tile(T)) * div_up(W, BN), kb = div_up(cols, BK);
+    int64_t s = device_sm_count() / (alone(T) ? 1 : 2) / tiles;
     if (s > kb / 16) s = kb / 16;
     if (s > 16) s = 16;
     if (s < 1) s = 1;
@@ -1200,25 +1240,26 @@ void balance(GemmParams& p, int64_t n1, int64_t n2, int pairs) {
     }
 }
 
-template <int KIND, bool F32>
+template <int KIND, bool F32, bool ALONE>
 gdn_status launch_gemm_t(GemmParams p, const Maps& m, cudaStream_t s) {
-    const void* fn = (const void*)vocab_gemm_kernel<KIND, F32>;
-    constexpr size_t smem = smem_bytes<KIND>();
+    const void* fn = (const void*)vocab_gemm_kernel<KIND, F32, ALONE>;
+    constexpr size_t smem = smem_bytes<KIND, ALONE>();
     gdn_status st = set_smem_attr(fn, smem);
     if (st != GDN_OK) return st;
     const int64_t n1 = (int64_t)p.mt * p.nt * (KIND == K_GRAD ? p.splits : 1), n2 = (int64_t)p.mt2 * p.nt2;
     if (n1 + n2 > 0x7fffffff / 2) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)(n1 + n2));
-    int pairs = pair_count(fn, smem);
+    int pairs = ALONE ? device_sm_count() : pair_count(fn, smem);
     if (n1 + n2 < pairs) pairs = (int)(n1 + n2);
     const int steps = KIND != K_GRAD && p.T <= kFewTokens ? kChunkFew : F32 ? kChunkF32 : kChunkBf16;
     p.chunk = KIND == K_GRAD ? steps : (int)div_up(p.kb, div_up(p.kb, steps));
     if (KIND == K_GRAD) balance(p, n1, n2, pairs);
-    vocab_gemm_kernel<KIND, F32><<<2 * (unsigned)pairs, GT, smem, s>>>(p, m);
+    vocab_gemm_kernel<KIND, F32, ALONE><<<(ALONE ? 1 : 2) * (unsigned)pairs, GT, smem, s>>>(p, m);
     return check_launch("vocab_gemm_kernel");
 }
 template <int KIND>
 gdn_status launch_gemm(const GemmParams& p, const Maps& m, cudaStream_t s) {
-    return p.f32 ? launch_gemm_t<KIND, true>(p, m, s) : launch_gemm_t<KIND, false>(p, m, s);
+    if (alone(p.T)) return p.f32 ? launch_gemm_t<KIND, true, true>(p, m, s) : launch_gemm_t<KIND, false, true>(p, m, s);
+    return p.f32 ? launch_gemm_t<KIND, true, false>(p, m, s) : launch_gemm_t<KIND, false, false>(p, m, s);
 }
 
 unsigned grid_for(int64_t n) {
@@ -1350,7 +1391,7 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
     if ((st = make_map3(&m.b, Wt.base, Wt.ld, width, vocab, parts, HALF)) != GDN_OK) return st;
     GemmParams p{};
-    p.mt = (int)div_up(T, BM);
+    p.mt = (int)div_up(T, rows_of_tile(T));
     p.nt = (int)div_up(vocab, BN);
     p.group = group_rows(p.mt, width, parts);
     p.kb = (int)div_up(width, BK);
@@ -1403,7 +1444,7 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
     }
     const bool store = dtype == GDN_BF16 && (reinterpret_cast<uintptr_t>(dw) & 15u) == 0 && lddw % 8 == 0;
     GemmParams p{};
-    p.mt = (int)div_up(T, BM);
+    p.mt = (int)div_up(T, rows_of_tile(T));
     p.group = group_rows(p.mt, width, parts);
     p.f32 = parts == 2;
     p.T = T; p.W = width; p.vocab = vocab; p.scale = scale;
@@ -1443,7 +1484,7 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         // (the last piece may be done with fewer splits than there are sums)
         p.kper = (int)div_up(p.kb, l.splits);
         p.splits = (int)div_up(p.kb, p.kper);
-        p.mt2 = (int)div_up(cols, BM);
+        p.mt2 = (int)div_up(cols, rows_of_tile(T));
         p.nt2 = p.nt;
         p.kb2 = (int)div_up(T, BK);
         p.acc = reinterpret_cast<float*>(ws + l.acc);

@@ -310,6 +310,21 @@ def test_far_weights(g):
     assert rel(r["dw"][-300:], P.t() @ L.dbl(h)) <= 2 ** -8 and rel(r["dh"], P @ L.dbl(w[-300:])) <= 2 ** -8
 
 
+# ---- up to 128 tokens: tiles of one CTA ------------------------------------------
+
+ALONE = [(17, 30, 8), (20, 257, 64), (33, 3000, 520), (64, 513, 72), (65, 700, 2048), (100, 5000, 1001), (127, 20000, 256),
+         (128, 1100, 640), (20, 300, 4200), (128, 256, 3)]
+
+
+@pytest.mark.parametrize("T,V,W", ALONE)
+@pytest.mark.parametrize("dtype,index", [(BF, I32), (F32, I64)])
+def test_up_to_128_tokens(g, T, V, W, dtype, index):
+    check(g, *inputs(T, V, W, dtype, seed=28, index=index))
+    h, w, t, dloss = inputs(T, V, W, dtype, seed=29, index=index, out=0.0)
+    a, b = (g.gdn_vocab_loss_bwd(dloss, h, w, t, g.gdn_vocab_loss_fwd(h, w, t)[1]) for _ in range(2))
+    assert torch.equal(a["dh"], b["dh"]) and torch.equal(a["dw"], b["dw"])
+
+
 # ---- few tokens: kernels of their own up to 8 tokens of bf16, 16 of fp32 ----------
 
 FEW = [(1, 8, 1), (1, 9, 3), (2, 100, 8), (3, 513, 66), (4, 1000, 1001), (5, 3001, 520), (7, 700, 4096), (8, 4099, 64),
