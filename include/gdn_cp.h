@@ -731,8 +731,9 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * keeps 22 bits down to 2^-18 of the largest under its scaling (its row's for
  * h, and for w in the forward; one for w in the backward, its token's dloss for
  * P), below that it is off by 2^-40 of it.
- * Calls of few tokens (8 of bf16, 16 of fp32, at widths up to 6400; 4 up to
- * 12800, 1 up to 51200; vocab 64 or more) form products, sums and P in fp32.
+ * Calls of few tokens (16 of fp32, 4 of bf16, 8 at widths that are no multiple
+ * of 8; at widths up to 6400, up to 4 tokens 12800, one 51200; vocab 64 or
+ * more) form products, sums and P in fp32.
  * An expired wait (gdn_device_timeouts) leaves the outputs incomplete.
  *
  * gdn_vocab_loss_bwd: gradients of the above for dloss, from the forward's lse

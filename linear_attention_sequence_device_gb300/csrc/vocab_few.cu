@@ -1,9 +1,9 @@
 // Softmax cross entropy over a vocabulary for few tokens: the formulas of vocab_loss.cu.
 //
 // What bounds it: the weights, read once for the loss; read twice and their gradient
-// written once for the gradients.  The tensor cores' tiles hold 256 tokens, and their fp32
-// parts take two more passes over the weights; here each weight goes through the fp32
-// units once for every token.
+// written once for the gradients.  The tensor cores' tiles hold 128 tokens, and what they
+// read has to be bf16 or fp16 at whole 16 bytes, other weights two passes more; here each weight
+// goes through the fp32 units once for every token.
 //
 //   logits  a warp takes R rows of w after R rows, a lane's 16 bytes (or less, as the
 //           alignment allows) of each, the next ones on their way, against up to 8 tokens'
@@ -448,12 +448,14 @@ __global__ void __launch_bounds__(1024) few_join_kernel(const float* __restrict_
 
 int up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// The most tokens of these kernels.  Loss and gradients in us, here and by the tensor cores:
-//   fp32  32000 x 2048   1 token  48 + 136, 239 + 440;  8  62 + 169, 196 + 367;  16  90 + 240, 188 + 360;
+// The most tokens of these kernels: of fp32, of bf16 rows that the tensor cores' copies read in place,
+// of other bf16 rows.  Loss and gradients in us, here and by the tensor cores:
+//   fp32  32000 x 2048   1 token  48 + 136, 239 + 440;  8  62 + 169, 196 + 367;  16  89 + 240, 155 + 324;
 //                        32 tokens  167 + 505, 189 + 363
-//   bf16  64000 x 2048   1 token  48 + 138, 122 + 257;  8  73 + 211, 103 + 233;  16  127 + 440, 102 + 235
-//         64000 x 2046   1 token  49 + 165, 218 + 431;  8  73 + 261, 200 + 398;  16  135 + 449, 200 + 398
-constexpr int kFewF32 = 16, kFewBf16 = 8;
+//   bf16  64000 x 2048   1 token  49 + 138, 64 + 175;  4  55 + 159, 58 + 175;  8  72 + 214, 59 + 173
+//         35215 x 832    1 token  18 + 40, 21 + 63;  4  22 + 56, 21 + 63;  8  29 + 78, 20 + 59
+//         64000 x 2046   4 tokens  55 + 201, 160 + 329;  8  72 + 261, 158 + 327;  16  135 + 449, 158 + 327
+constexpr int kFewF32 = 16, kFewBf16 = 4, kFewBf16Odd = 8;
 constexpr int kLeastRows = 64;  // of w: fewer would leave most warps without any
 constexpr size_t kSmem = 200 << 10;  // of h
 constexpr int kMaxParts = 608;
@@ -483,8 +485,9 @@ template <typename E, int VEC>
 gdn_status logits_tokens(const LogitArgs& p, cudaStream_t s) {
     const int tt = tokens_of(p.a.T);
     if (tt == 1) return launch_logits<E, 1, VEC>(p, s);
-    if (tt == 4) return launch_logits<E, 4, VEC>(p, s);
-    return launch_logits<E, 8, VEC == 8 ? 2 : VEC>(p, s);  // (with eight columns an access a few registers short)
+    if constexpr (VEC < 8)  // (rows of eights: up to four tokens)
+        if (tt == 8) return launch_logits<E, 8, VEC>(p, s);
+    return launch_logits<E, 4, VEC>(p, s);
 }
 gdn_status run_logits(const LogitArgs& p, cudaStream_t s) {
     const FewArgs& a = p.a;
@@ -529,19 +532,28 @@ constexpr int columns(int tt, int e) {
     return n < 16 / e ? n : 16 / e;
 }
 
-template <int TT>
+template <typename E, int TT>
 gdn_status grads_tokens(const GradArgs& p, int n, void* dh, int64_t lddh, cudaStream_t s) {
-    constexpr int F = columns(TT, 4), B = columns(TT, 2);
-    if (p.a.dtype == GDN_F32)
-        return n >= F ? launch_grads<float, TT, F>(p, dh, lddh, s) : launch_grads<float, TT, 1>(p, dh, lddh, s);
-    if (n >= B) return launch_grads<__nv_bfloat16, TT, B>(p, dh, lddh, s);
-    return n >= 2 ? launch_grads<__nv_bfloat16, TT, 2>(p, dh, lddh, s) : launch_grads<__nv_bfloat16, TT, 1>(p, dh, lddh, s);
+    constexpr int C = columns(TT, sizeof(E));
+    if (n >= C) return launch_grads<E, TT, C>(p, dh, lddh, s);
+    if constexpr (sizeof(E) == 2)
+        if (n >= 2) return launch_grads<E, TT, 2>(p, dh, lddh, s);
+    return launch_grads<E, TT, 1>(p, dh, lddh, s);
+}
+template <typename E>
+gdn_status run_grads(const GradArgs& p, int n, void* dh, int64_t lddh, cudaStream_t s) {
+    const int tt = grad_tokens(p.a.T);
+    if (tt == 1) return grads_tokens<E, 1>(p, n, dh, lddh, s);
+    if (tt == 4) return grads_tokens<E, 4>(p, n, dh, lddh, s);
+    if constexpr (sizeof(E) == 4)
+        if (tt == 16) return grads_tokens<E, 16>(p, n, dh, lddh, s);
+    return grads_tokens<E, 8>(p, n, dh, lddh, s);
 }
 
 }  // namespace
 
 bool few_takes(int T, int V, int W, gdn_dtype dtype) {
-    return V >= kLeastRows && T <= (dtype == GDN_F32 ? kFewF32 : kFewBf16) &&
+    return V >= kLeastRows && T <= (dtype == GDN_F32 ? kFewF32 : W % 8 ? kFewBf16Odd : kFewBf16) &&
            sizeof(float) * tokens_of(T) * (size_t)padded(W, 256) <= kSmem;
 }
 
@@ -582,10 +594,7 @@ gdn_status few_grads(const FewArgs& a, const float* dloss, const float* lse, flo
     p.dw = dw;
     p.lddw = lddw;
     const int n = access(a.dtype == GDN_F32 ? 4 : 8, a.dtype == GDN_F32 ? 4 : 2, a.W, a.w, a.ldw, dw, lddw);
-    const int tt = grad_tokens(a.T);
-    return tt == 1   ? grads_tokens<1>(p, n, dh, lddh, s)
-           : tt == 4 ? grads_tokens<4>(p, n, dh, lddh, s)
-           : tt == 8 ? grads_tokens<8>(p, n, dh, lddh, s) : grads_tokens<16>(p, n, dh, lddh, s);
+    return a.dtype == GDN_F32 ? run_grads<float>(p, n, dh, lddh, s) : run_grads<__nv_bfloat16>(p, n, dh, lddh, s);
 }
 
 }  // namespace gdn
