@@ -25,7 +25,7 @@
 // by up to 2^-40 of the largest.
 //
 // The product kernel: a pair of CTAs (cta_group::2) forms a 256 x 256 tile, 128 rows of
-// each operand a CTA, from a ring of six stages of 64 along K by TMA; accumulators in tensor
+// each operand a CTA, from a ring of stages of 64 along K by TMA; accumulators in tensor
 // memory, two of them, so that the epilogue's sixteen warps run beside the next tile.  One
 // CTA an SM walks tiles by its number.
 //
@@ -174,6 +174,7 @@ __device__ __forceinline__ bool wait_for(uint64_t* mbar, uint32_t parity, volati
 // ---- the product kernel ------------------------------------------------------
 
 constexpr int BM = 256, BN = 256, BK = 64;      // a pair's tile
+constexpr int kNarrow = 128;                    // columns of a tile of the logits where tiles are few
 constexpr int HALF = 128;                       // rows of an operand a CTA; a tile's without a pair
 constexpr int OPB = HALF * BK * 2;              // bytes of as many rows of a stage
 constexpr int GT = 576;                         // threads: a warp of loads, one of products, 16 of epilogue
@@ -186,32 +187,37 @@ enum Kind { K_LSE = 0, K_P = 1, K_GRAD = 2 };
 // Up to as many tokens as a CTA has rows (ALONE) each CTA forms 128 x 256 tiles of its own, from all of B.
 constexpr int kAloneTokens = 128;
 
-// bytes of a stage: the CTA's rows of A, its half of B or all of it
-template <bool ALONE>
-__host__ __device__ constexpr int stage_bytes() {
-    return ALONE ? 3 * OPB : 2 * OPB;
+// rows of B of a CTA, bytes of a stage
+template <bool ALONE, int TN>
+__host__ __device__ constexpr int b_rows() {
+    return ALONE ? TN : TN / 2;
 }
-// Stages of the ring: results leave through shared memory but for the logits' maxima and sums
-template <int KIND, bool ALONE>
+template <bool ALONE, int TN>
+__host__ __device__ constexpr int stage_bytes() {
+    return OPB + b_rows<ALONE, TN>() * BK * 2;
+}
+// Stages of the ring: 144 to 192 KB; results leave through shared memory but for the logits'
+// maxima and sums
+template <int KIND, bool ALONE, int TN>
 __host__ __device__ constexpr int stages() {
-    return ALONE ? (KIND == K_LSE ? 4 : 3) : KIND == K_LSE ? 6 : 5;
+    return (KIND == K_LSE ? 192 * 1024 : 160 * 1024) / stage_bytes<ALONE, TN>();
 }
 template <int KIND>
 __host__ __device__ constexpr int staged_bytes() {
     return KIND == K_LSE ? 2 * 3 * HALF * 8 : 4 * 2 * OUTB;
 }
 struct Ctl {
-    uint64_t full[6], empty[6], done[2], free_[2];
+    uint64_t full[8], empty[8], done[2], free_[2];
     uint32_t tmem;
     int abort;
 };
-template <int KIND, bool ALONE>
+template <int KIND, bool ALONE, int TN>
 constexpr size_t smem_bytes() {
-    return 1024 + (size_t)stages<KIND, ALONE>() * stage_bytes<ALONE>() + staged_bytes<KIND>() + sizeof(Ctl);
+    return 1024 + (size_t)stages<KIND, ALONE, TN>() * stage_bytes<ALONE, TN>() + staged_bytes<KIND>() + sizeof(Ctl);
 }
-static_assert(smem_bytes<K_LSE, false>() <= 227 * 1024 && smem_bytes<K_GRAD, false>() <= 227 * 1024 &&
-                  smem_bytes<K_LSE, true>() <= 227 * 1024 && smem_bytes<K_GRAD, true>() <= 227 * 1024,
-              "shared memory of a CTA");
+static_assert(stages<K_LSE, false, kNarrow>() == 8 && smem_bytes<K_LSE, false, kNarrow>() <= 227 * 1024 &&
+                  smem_bytes<K_GRAD, false, BN>() <= 227 * 1024,
+              "barriers, shared memory of a CTA");
 
 struct Maps {
     CUtensorMap a, b;    // logits: h, w.  Gradients of h: P, w
@@ -386,13 +392,15 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, int pair, int pa
     }
 }
 
-template <int KIND, bool F32, bool ALONE>
+template <int KIND, bool F32, bool ALONE, int TN>
 __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
     vocab_gemm_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
     constexpr bool CH = chunked<KIND, F32>();
     const int ch = p.chunk;
     constexpr int NP = F32 ? 3 : 1;  // products of parts
-    constexpr int STAGES = stages<KIND, ALONE>(), STAGE = stage_bytes<ALONE>(), TM = ALONE ? HALF : BM;
+    constexpr int STAGES = stages<KIND, ALONE, TN>(), STAGE = stage_bytes<ALONE, TN>(), TM = ALONE ? HALF : BM;
+    constexpr int HB = b_rows<ALONE, TN>();
+    constexpr int EW = TN / 4;
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
     const uint32_t ring = tc::smem_addr(base);
@@ -431,7 +439,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
         int64_t issued = 0;
         bool ok = true;
         for (int i = 0; ok && unit<KIND, ALONE>(p, pair, pairs, i, w); ++i) {
-            const int row_a = w.m * TM + (int)rank * HALF, row_b = w.n * BN + (int)rank * HALF;
+            const int row_a = w.m * TM + (int)rank * HALF, row_b = w.n * TN + (int)rank * HB;
             for (int k0 = w.k0; k0 < w.k1 && ok; k0 += CH ? ch : w.k1 - w.k0) {
                 const int k1 = CH ? min(w.k1, k0 + ch) : w.k1;
                 for (int q = 0; q < NP && ok; ++q)
@@ -440,7 +448,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                             ok = false;
                             break;
                         }
-                        if (rank == 0) tc::mbar_expect_tx(&c.full[s], ALONE ? STAGE : 2 * STAGE);
+                        if (rank == 0) tc::mbar_expect_tx(&c.full[s], (ALONE ? 1 : 2) * STAGE);
                         const uint32_t bar = ALONE ? 0u : in_leader(tc::smem_addr(&c.full[s]));
                         const uint32_t da = ring + s * STAGE, db = da + OPB;
                         const int za = F32 ? part_a(q) : 0, zb = F32 ? part_b(q) : 0;
@@ -448,7 +456,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                             if (ALONE) load_box_alone(dst, map, x, y, z, &c.full[s]);
                             else load_box(dst, map, x, y, z, bar);
                         };
-                        constexpr int BH = ALONE ? 2 : 1;  // halves of B
+                        constexpr int BH = HB > HALF ? 2 : 1;  // copies of B
                         if (KIND != K_GRAD) {
                             load(da, &maps.a, k * BK, row_a, za);
 #pragma unroll
@@ -498,7 +506,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
         for (int i = 0; ok && unit<KIND, ALONE>(p, pair, pairs, i, w); ++i) {
             const bool a_mn = KIND == K_GRAD && w.second, b_mn = KIND == K_GRAD;
             // (bits 7 and 10: operands of bf16 instead of fp16)
-            const uint32_t id = (tc::idesc_bf16(TM, BN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u)) &
+            const uint32_t id = (tc::idesc_bf16(TM, TN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u)) &
                                 (F32 ? ~(1u << 7 | 1u << 10) : ~0u);
             int k0 = w.k0;
             do {
@@ -509,7 +517,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                     break;
                 }
                 tc::fence_after();
-                const uint32_t d = tmem + (uint32_t)buf * BN;
+                const uint32_t d = tmem + (uint32_t)buf * TN;
                 uint32_t acc = 0;
                 const int steps = (k1 - k0) * NP;
                 for (int k = 0; k < steps; ++k) {
@@ -574,7 +582,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                 if (ok) ok = wait_for(&c.done[buf], (it >> 1) & 1, &c.abort);
                 __syncwarp();
                 tc::fence_after();
-                d = lanes + (uint32_t)buf * BN;
+                d = lanes + (uint32_t)buf * TN;
                 release = ALONE ? tc::smem_addr(&c.free_[buf]) : in_leader(tc::smem_addr(&c.free_[buf]));
                 if constexpr (CH) {
 #pragma unroll
@@ -601,7 +609,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
             const bool lead = quad == 0 && (t & 31) == 0;  // of the quarter: its stores
             const uint32_t stage = ring + STAGES * STAGE + (KIND == K_LSE ? 0 : quarter * 2 * OUTB);
             const int r0 = ALONE && KIND != K_GRAD ? 0 : w.m * TM + (int)rank * HALF, r = r0 + row;
-            const int c0 = w.n * BN + quarter * EW;
+            const int c0 = w.n * TN + quarter * EW;
             // logits and sums of fp32 inputs are 2^(exponents of the scalings) times too large (dh's
             // by w's after this)
             float f = p.scale;
@@ -1117,6 +1125,16 @@ int piece_cols(int T, int V, gdn_dtype dt) {
 bool alone(int T) { return T <= kAloneTokens; }
 int rows_of_tile(int T) { return alone(T) ? HALF : BM; }
 
+// Columns of a tile of the logits: half of them where whole tiles would leave half of the GPU idle
+// (66 x 5310 x 3498 in fp32, loss and gradients: 111 + 186 us in whole tiles, 95 + 158 so; 49 x 1738 x
+// 1786 in bf16: 24 + 42, 22 + 40)
+int tile_cols(int T, int V) {
+    const int64_t tiles = div_up(T, rows_of_tile(T)) * div_up(V, kNarrow);
+    return tiles <= device_sm_count() / (alone(T) ? 1 : 2) ? kNarrow : BN;
+}
+// rows of w of a copy
+int copy_rows(int T, int cols) { return alone(T) ? HALF : cols / 2; }
+
 // K of dh's product cut into as many splits as leave its tiles no more than the pairs of
 // CTAs; splits of 16 steps at least
 int dh_splits(int T, int W, int cols) {
@@ -1180,7 +1198,7 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     }
     if (!grad) {
         l.stat = o;
-        o += up256(sizeof(float2) * (size_t)div_up(V, BN) * t);
+        o += up256(sizeof(float2) * (size_t)div_up(V, tile_cols((int)t, V)) * t);
         l.at = o;
         o += up256(sizeof(float) * t);
     } else {
@@ -1241,10 +1259,10 @@ void balance(GemmParams& p, int64_t n1, int64_t n2, int pairs) {
     }
 }
 
-template <int KIND, bool F32, bool ALONE>
+template <int KIND, bool F32, bool ALONE, int TN>
 gdn_status launch_gemm_t(GemmParams p, const Maps& m, cudaStream_t s) {
-    const void* fn = (const void*)vocab_gemm_kernel<KIND, F32, ALONE>;
-    constexpr size_t smem = smem_bytes<KIND, ALONE>();
+    const void* fn = (const void*)vocab_gemm_kernel<KIND, F32, ALONE, TN>;
+    constexpr size_t smem = smem_bytes<KIND, ALONE, TN>();
     gdn_status st = set_smem_attr(fn, smem);
     if (st != GDN_OK) return st;
     const int64_t n1 = (int64_t)p.mt * p.nt * (KIND == K_GRAD ? p.splits : 1), n2 = (int64_t)p.mt2 * p.nt2;
@@ -1254,13 +1272,20 @@ gdn_status launch_gemm_t(GemmParams p, const Maps& m, cudaStream_t s) {
     const int steps = KIND != K_GRAD && p.T <= kFewTokens ? kChunkFew : F32 ? kChunkF32 : kChunkBf16;
     p.chunk = KIND == K_GRAD ? steps : (int)div_up(p.kb, div_up(p.kb, steps));
     if (KIND == K_GRAD) balance(p, n1, n2, pairs);
-    vocab_gemm_kernel<KIND, F32, ALONE><<<(ALONE ? 1 : 2) * (unsigned)pairs, GT, smem, s>>>(p, m);
+    vocab_gemm_kernel<KIND, F32, ALONE, TN><<<(ALONE ? 1 : 2) * (unsigned)pairs, GT, smem, s>>>(p, m);
     return check_launch("vocab_gemm_kernel");
 }
+template <int KIND, bool F32>
+gdn_status launch_gemm_f(const GemmParams& p, const Maps& m, int cols, cudaStream_t s) {
+    if constexpr (KIND != K_GRAD)
+        if (cols == kNarrow)
+            return alone(p.T) ? launch_gemm_t<KIND, F32, true, kNarrow>(p, m, s) : launch_gemm_t<KIND, F32, false, kNarrow>(p, m, s);
+    return alone(p.T) ? launch_gemm_t<KIND, F32, true, BN>(p, m, s) : launch_gemm_t<KIND, F32, false, BN>(p, m, s);
+}
+// cols: a tile's columns
 template <int KIND>
-gdn_status launch_gemm(const GemmParams& p, const Maps& m, cudaStream_t s) {
-    if (alone(p.T)) return p.f32 ? launch_gemm_t<KIND, true, true>(p, m, s) : launch_gemm_t<KIND, false, true>(p, m, s);
-    return p.f32 ? launch_gemm_t<KIND, true, false>(p, m, s) : launch_gemm_t<KIND, false, false>(p, m, s);
+gdn_status launch_gemm(const GemmParams& p, const Maps& m, int cols, cudaStream_t s) {
+    return p.f32 ? launch_gemm_f<KIND, true>(p, m, cols, s) : launch_gemm_f<KIND, false>(p, m, cols, s);
 }
 
 unsigned grid_for(int64_t n) {
@@ -1390,10 +1415,11 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     }
     Maps m{};
     if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
-    if ((st = make_map3(&m.b, Wt.base, Wt.ld, width, vocab, parts, HALF)) != GDN_OK) return st;
+    const int tn = tile_cols(T, vocab);
+    if ((st = make_map3(&m.b, Wt.base, Wt.ld, width, vocab, parts, copy_rows(T, tn))) != GDN_OK) return st;
     GemmParams p{};
     p.mt = (int)div_up(T, rows_of_tile(T));
-    p.nt = (int)div_up(vocab, BN);
+    p.nt = (int)div_up(vocab, tn);
     p.group = group_rows(p.mt, width, parts);
     p.kb = (int)div_up(width, BK);
     p.f32 = parts == 2;
@@ -1403,7 +1429,7 @@ gdn_status gdn_vocab_loss_fwd(const void* h, int64_t ldh, const void* w, int64_t
     p.we = reinterpret_cast<int*>(ws + l.we);
     p.stat = reinterpret_cast<float2*>(ws + l.stat);
     p.at = reinterpret_cast<float*>(ws + l.at);
-    if ((st = launch_gemm<K_LSE>(p, m, s)) != GDN_OK) return st;
+    if ((st = launch_gemm<K_LSE>(p, m, tn, s)) != GDN_OK) return st;
     lse_join_kernel<<<(unsigned)div_up(T, 32), 256, 0, s>>>(p.stat, p.nt, T, vocab, p.at, targets, wide, loss, lse);
     return check_launch("lse_join_kernel");
 }
@@ -1466,13 +1492,14 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         p.V = cols;
         // the piece's P
         if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
-        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, HALF)) != GDN_OK) return st;
+        const int tn = tile_cols(T, cols);
+        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, copy_rows(T, tn))) != GDN_OK) return st;
         if ((st = make_map_rows(&m.out, P, l.piece, cols, T, T, parts, HALF, SC)) != GDN_OK) return st;
-        p.nt = (int)div_up(cols, BN);
+        p.nt = (int)div_up(cols, tn);
         p.kb = (int)div_up(width, BK);
         p.splits = 1;
         p.mt2 = p.nt2 = 0;
-        if ((st = launch_gemm<K_P>(p, m, s)) != GDN_OK) return st;
+        if ((st = launch_gemm<K_P>(p, m, tn, s)) != GDN_OK) return st;
         // both gradients' products
         if ((st = make_map3(&m.a, P, l.piece, cols, T, parts, HALF)) != GDN_OK) return st;
         if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, 64)) != GDN_OK) return st;
@@ -1492,7 +1519,7 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
         p.ldacc = l.ldacc;
         p.add = v0 > 0;
         p.dw = dwp; p.lddw = lddw; p.dw_store = store;
-        if ((st = launch_gemm<K_GRAD>(p, m, s)) != GDN_OK) return st;
+        if ((st = launch_gemm<K_GRAD>(p, m, BN, s)) != GDN_OK) return st;
     }
     const unsigned g = grid_for((int64_t)T * (l.ldacc / 8));
     // 16-byte accesses of dh and, in bf16, of w
