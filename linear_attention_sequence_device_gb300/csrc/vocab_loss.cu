@@ -178,7 +178,6 @@ constexpr int kNarrow = 128;                    // columns of a tile of the logi
 constexpr int HALF = 128;                       // rows of an operand a CTA; a tile's without a pair
 constexpr int OPB = HALF * BK * 2;              // bytes of as many rows of a stage
 constexpr int GT = 576;                         // threads: a warp of loads, one of products, 16 of epilogue
-constexpr int EW = 64;                          // columns of an epilogue warp: a quarter of the tile's
 constexpr int SC = 32;                          // columns of a staged piece of a result
 constexpr int OUTB = HALF * SC * 2;             // its bytes; each quarter of the columns has two
 
@@ -366,6 +365,7 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, int pair, int pa
     asm volatile("" : "+r"(u));
     Unit w;
     unit<KIND, ALONE>(p, pair, pairs, u, w);
+    constexpr int EW = BN / 4;  // columns of an epilogue warp
     const int l = t & 31, row = w.m * (ALONE ? HALF : BM) + (int)rank * HALF + ((t >> 5) & 3) * 32;
     const int col = w.n * BN + ((t >> 5) - 2) / 4 * EW + j + l;
     const int n = min(32, (w.second ? p.V : p.T) - row);
@@ -400,7 +400,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
     constexpr int NP = F32 ? 3 : 1;  // products of parts
     constexpr int STAGES = stages<KIND, ALONE, TN>(), STAGE = stage_bytes<ALONE, TN>(), TM = ALONE ? HALF : BM;
     constexpr int HB = b_rows<ALONE, TN>();
-    constexpr int EW = TN / 4;
+    constexpr int EW = TN / 4;  // columns of an epilogue warp: a quarter of the tile's
     extern __shared__ unsigned char raw[];
     unsigned char* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
     const uint32_t ring = tc::smem_addr(base);
