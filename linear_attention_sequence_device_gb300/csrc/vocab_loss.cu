@@ -268,7 +268,7 @@ struct Unit {
 // dh's tiles the same way, then dw's, of which the pairs that have a tile of dh less run
 // `early` more, so that all end together (round robin over both kinds left the last fifth
 // of a short call's time to a few pairs).
-template <int KIND, bool ALONE>
+template <int KIND>
 __device__ __forceinline__ bool unit(const GemmParams& p, int pair, int pairs, int i, Unit& r) {
     r.second = false;
     r.split = 0;
@@ -364,7 +364,7 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, int pair, int pa
     asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
     asm volatile("" : "+r"(u));
     Unit w;
-    unit<KIND, ALONE>(p, pair, pairs, u, w);
+    unit<KIND>(p, pair, pairs, u, w);
     constexpr int EW = BN / 4;  // columns of an epilogue warp
     const int l = t & 31, row = w.m * (ALONE ? HALF : BM) + (int)rank * HALF + ((t >> 5) & 3) * 32;
     const int col = w.n * BN + ((t >> 5) - 2) / 4 * EW + j + l;
@@ -438,7 +438,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
         int s = 0, phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int i = 0; ok && unit<KIND, ALONE>(p, pair, pairs, i, w); ++i) {
+        for (int i = 0; ok && unit<KIND>(p, pair, pairs, i, w); ++i) {
             const int row_a = w.m * TM + (int)rank * HALF, row_b = w.n * TN + (int)rank * HB;
             for (int k0 = w.k0; k0 < w.k1 && ok; k0 += CH ? ch : w.k1 - w.k0) {
                 const int k1 = CH ? min(w.k1, k0 + ch) : w.k1;
@@ -503,7 +503,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
         // ---- products ----
         int s = 0, phase = 0, it = 0;
         bool ok = true;
-        for (int i = 0; ok && unit<KIND, ALONE>(p, pair, pairs, i, w); ++i) {
+        for (int i = 0; ok && unit<KIND>(p, pair, pairs, i, w); ++i) {
             const bool a_mn = KIND == K_GRAD && w.second, b_mn = KIND == K_GRAD;
             // (bits 7 and 10: operands of bf16 instead of fp16)
             const uint32_t id = (tc::idesc_bf16(TM, TN, false, b_mn, false) | (a_mn ? 1u << 15 : 0u)) &
@@ -563,12 +563,12 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
         constexpr bool ONLY = KIND == K_GRAD && !F32;
         auto only_of = [&](int u) {
             Unit x;
-            if (!unit<KIND, ALONE>(p, pair, pairs, u, x) || !x.second) return -1;
+            if (!unit<KIND>(p, pair, pairs, u, x) || !x.second) return -1;
             const int r = x.m * TM + (int)rank * HALF + (warp & 3) * 32 + lane;
             return r < p.V ? __ldg(p.only + p.v0 + r) : -1;
         };
         int only = ONLY ? only_of(0) : -1;
-        for (int u = 0; unit<KIND, ALONE>(p, pair, pairs, u, w); ++u) {
+        for (int u = 0; unit<KIND>(p, pair, pairs, u, w); ++u) {
             const int only_next = ONLY ? only_of(u + 1) : -1;
             float acc[CH ? EW : 1];
 #pragma unroll
@@ -602,7 +602,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
             int t = tid;
             if (CH) {
                 asm volatile("" : "+r"(u));
-                unit<KIND, ALONE>(p, pair, pairs, u, w);
+                unit<KIND>(p, pair, pairs, u, w);
                 asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
             }
             const int quad = (t >> 5) & 3, quarter = ((t >> 5) - 2) >> 2, row = quad * 32 + (t & 31);
