@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(LT, 1) few_logits_kernel(const LogitArgs p) {
                 p.P[(int64_t)v * a.T + t] =
                     g[j] != 0.f ? g[j] * exp2_fast((x - lse[j]) * kLog2e) - (v == target[j] ? g[j] : 0.f) : 0.f;
         } else {
-            if (one && v == target[j]) p.at[t] = x;
+            if (v == target[j]) {  // goes its own way (lse_join_kernel)
+                if (one) p.at[t] = x;
+                continue;
+            }
             const float top = fmaxf(m, x), ref = top == -INFINITY ? 0.f : top;
             sum = sum * exp2_fast((m - ref) * kLog2e) + exp2_fast((x - ref) * kLog2e);
             m = top;

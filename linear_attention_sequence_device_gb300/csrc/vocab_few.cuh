@@ -18,7 +18,8 @@ struct FewArgs {
 // backward agree
 bool few_takes(int T, int V, int W, gdn_dtype dtype);
 
-// Maxima and sums of exponentials, [few_blocks()][T], and the targets' logits [T]
+// Maxima and sums of exponentials of all words but the target, [few_blocks()][T], and the
+// targets' logits [T]
 int few_blocks(int T, int V);
 gdn_status few_logits(const FewArgs& a, float2* stat, float* at, cudaStream_t s);
 

@@ -236,7 +236,7 @@ struct GemmParams {
     int v0, vocab;
     float scale;
     const void* targets; int wide;
-    float2* stat;         // K_LSE: [nt][T] maximum and sum of a tile's row
+    float2* stat;         // K_LSE: [nt][T] maximum and sum of a tile's row, without the target
     float* at;            // K_LSE: [T] the target's logit
     const float* lse; const float* dloss;  // K_P
     const int* he; const int* pa;          // fp32: exponents of the scalings of h's rows, of P's
@@ -650,14 +650,19 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                     for (int i = 0; i < EW; ++i) {
                         if (F32) acc[i] *= f;
                         if (i >= left) acc[i] = -INFINITY;
-                        top = fmaxf(top, acc[i]);
                     }
+                    // the target's logit goes its own way (lse_join_kernel)
                     if (o >= 0 && o < EW) {
                         float v = 0.f;
 #pragma unroll
-                        for (int i = 0; i < EW; ++i) take_at(v, acc[i], o, i);
+                        for (int i = 0; i < EW; ++i) {
+                            take_at(v, acc[i], o, i);
+                            take_at(acc[i], -INFINITY, o, i);
+                        }
                         p.at[r] = v;
                     }
+#pragma unroll
+                    for (int i = 0; i < EW; ++i) top = fmaxf(top, acc[i]);
                     const float ref = top == -INFINITY ? 0.f : top;
                     float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1019,7 +1024,8 @@ __global__ void __launch_bounds__(256) split_kernel(const float* __restrict__ h,
     }
 }
 
-// lse and loss of 32 rows from the tiles' maxima and sums: eight threads a row
+// lse and loss of 32 rows from the tiles' maxima and sums, which are those of all words but
+// the target, and the target's logit: eight threads a row
 __global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict__ stat, int nt, int T, int V,
                                                        const float* __restrict__ at, const void* targets, int wide,
                                                        float* __restrict__ loss, float* __restrict__ lse) {
@@ -1045,13 +1051,24 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict_
         s = s * exp2_fast((m - ref) * kLog2e) + v.y * exp2_fast((v.x - ref) * kLog2e);
         m = t;
     }
-    const int64_t tgt =
-        wide ? __ldg(static_cast<const long long*>(targets) + r) : __ldg(static_cast<const int*>(targets) + r);
-    const float l = logf(s);
-    lse[r] = m + l;
-    // (not from the rounded lse: where the target is the largest, m is its logit, and a small
-    // loss keeps its digits)
-    loss[r] = tgt < 0 ? 0.f : tgt >= V ? NAN : (m - __ldg(at + r)) + l;
+    const int64_t tgt = raw_target(targets, wide, r);
+    if (tgt < 0 || tgt >= V) {  // nothing was left out of the sums
+        lse[r] = m + logf(s);
+        loss[r] = tgt < 0 ? 0.f : NAN;
+        return;
+    }
+    // loss = log(1 + s e^(m - x)), x the target's logit: with the target's own term, 1, in s,
+    // a loss of 1e-5 would be good to 2^-24 of that 1, and not of itself
+    const float x = __ldg(at + r), d = m - x;
+    if (d <= 0.f) {
+        const float l = x == INFINITY ? NAN : log1pf(s * expf(d));
+        loss[r] = l;
+        lse[r] = x + l;
+    } else {
+        const float l = logf(s + expf(-d));
+        loss[r] = d + l;
+        lse[r] = m + l;
+    }
 }
 
 // dh from the splits' sums, eight columns a thread; for bf16 with what P's rounding took
