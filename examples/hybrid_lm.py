@@ -84,14 +84,14 @@ class VocabLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, w, targets, scale):
         loss, lse = g.gdn_vocab_loss_fwd(h, w, targets, scale=scale)
-        ctx.save_for_backward(h, w, targets, lse)
+        ctx.save_for_backward(h, w, targets, lse, loss)
         ctx.scale = scale
         return loss
 
     @staticmethod
     def backward(ctx, dloss):
-        h, w, targets, lse = ctx.saved_tensors
-        r = g.gdn_vocab_loss_bwd(dloss.contiguous(), h, w, targets, lse, scale=ctx.scale)
+        h, w, targets, lse, loss = ctx.saved_tensors
+        r = g.gdn_vocab_loss_bwd(dloss.contiguous(), h, w, targets, lse, scale=ctx.scale, loss=loss)
         return r["dh"], r["dw"], None, None
 
 

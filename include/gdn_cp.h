@@ -736,7 +736,8 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * more) form products, sums and P in fp32.
  * An expired wait (gdn_device_timeouts) leaves the outputs incomplete.
  *
- * gdn_vocab_loss_bwd: gradients of the above for dloss, from the forward's lse
+ * gdn_vocab_loss_bwd_from_loss: gradients of the above for dloss, from the
+ * forward's loss and lse
  *   dloss   device [T] fp32
  *   dh      device [T, width] dtype, row stride lddh;  dw device [vocab,
  *           width] dtype, row stride lddw; neither overlaps an input
@@ -749,6 +750,12 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  *   workspace  device, >= the _workspace_size(...) bytes of the call, 256-byte
  *           aligned, contents on entry irrelevant
  * Equal calls give equal bits.
+ *
+ * gdn_vocab_loss_bwd: the same without the loss.  P at a target, softmax - 1, then
+ * comes from the rounded lse, as a difference that is off by 2^-24 of lse: fine for
+ * tokens whose softmax is away from 1, but where 1 - softmax is 1e-5 the
+ * gradients are off by 3e-2 of themselves beside an lse of 15 and by all of
+ * themselves beside one of 300 (with the loss by 4e-6 and 4e-4, of fp32).
  * ---------------------------------------------------------------------- */
 size_t gdn_vocab_loss_fwd_workspace_size(int32_t T, int32_t vocab, int32_t width, gdn_dtype dtype);
 gdn_status gdn_vocab_loss_fwd(const void *h, int64_t ldh, const void *w, int64_t ldw,
@@ -762,6 +769,13 @@ gdn_status gdn_vocab_loss_bwd(const float *dloss, const void *h, int64_t ldh, co
                               int32_t width, float scale, void *dh, int64_t lddh, void *dw,
                               int64_t lddw, void *workspace, size_t workspace_bytes,
                               void *stream);
+gdn_status gdn_vocab_loss_bwd_from_loss(const float *dloss, const void *h, int64_t ldh,
+                                        const void *w, int64_t ldw, gdn_dtype dtype,
+                                        const void *targets, int32_t index_bits,
+                                        const float *loss, const float *lse, int32_t T,
+                                        int32_t vocab, int32_t width, float scale, void *dh,
+                                        int64_t lddh, void *dw, int64_t lddw, void *workspace,
+                                        size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -110,6 +110,8 @@ SIGNATURES = {
     "gdn_vocab_loss_bwd_workspace_size": (_sz, [_i32, _i32, _i32, ctypes.c_int]),
     "gdn_vocab_loss_bwd": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i32, _vp, _i32, _i32, _i32,
                                           _f32, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
+    "gdn_vocab_loss_bwd_from_loss": (ctypes.c_int, [_vp, _vp, _i64, _vp, _i64, ctypes.c_int, _vp, _i32, _vp, _vp, _i32,
+                                                    _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp, _sz, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 32 << 20
 

@@ -151,6 +151,7 @@ struct LogitArgs {
     int groups;                          // of TT tokens
     float2* stat; float* at;             // the loss
     const float* dloss; const float* lse; float* P;  // the gradients
+    const float* loss;                   // for P at the targets, or null: by lse
 };
 
 template <typename E, int TT, int VEC>
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(LT, 1) few_logits_kernel(const LogitArgs p) {
     extern __shared__ __align__(16) float hs[];  // [TT][Wp]
     __shared__ float2 part[LW][TT];
     __shared__ int target[TT];          // of the block's tokens
-    __shared__ float lse[TT], g[TT];    // (registers are for the sums)
+    __shared__ float lse[TT], g[TT], hot[TT];  // (registers are for the sums); hot: P at the target
     const FewArgs& a = p.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int blk = blockIdx.x / p.groups, blks = gridDim.x / p.groups;
@@ -183,6 +184,8 @@ __global__ void __launch_bounds__(LT, 1) few_logits_kernel(const LogitArgs p) {
         if (p.P && real) {
             lse[tid] = __ldg(p.lse + t0 + tid);
             g[tid] = v < 0 ? 0.f : v >= a.V ? NAN : __ldg(p.dloss + t0 + tid) * a.scale;
+            // p - 1 from the loss, -log p: the rounded lse would not tell p from 1
+            if (p.loss) hot[tid] = g[tid] * expm1f(-__ldg(p.loss + t0 + tid));
         }
     }
     __syncthreads();
@@ -250,9 +253,14 @@ __global__ void __launch_bounds__(LT, 1) few_logits_kernel(const LogitArgs p) {
         if (v < (int)q * R) continue;
         if (p.P) {
             // (g of 0: a token that is left out, whatever its h holds)
-            if (one)
-                p.P[(int64_t)v * a.T + t] =
-                    g[j] != 0.f ? g[j] * exp2_fast((x - lse[j]) * kLog2e) - (v == target[j] ? g[j] : 0.f) : 0.f;
+            if (one) {
+                float P = 0.f;
+                if (g[j] != 0.f) {
+                    P = g[j] * exp2_fast((x - lse[j]) * kLog2e);
+                    if (v == target[j]) P = p.loss ? hot[j] : P - g[j];
+                }
+                p.P[(int64_t)v * a.T + t] = P;
+            }
         } else {
             if (v == target[j]) {  // goes its own way (lse_join_kernel)
                 if (one) p.at[t] = x;
@@ -580,11 +588,12 @@ int few_parts(int T, int V, int W, gdn_dtype dtype) {
     return grad_chunks(V, grad_slabs(W, columns(tt, dtype == GDN_F32 ? 4 : 2), lanes), resident(tt));
 }
 
-gdn_status few_grads(const FewArgs& a, const float* dloss, const float* lse, float* P, float* parts, void* dh,
-                     int64_t lddh, void* dw, int64_t lddw, cudaStream_t s) {
+gdn_status few_grads(const FewArgs& a, const float* dloss, const float* loss, const float* lse, float* P, float* parts,
+                     void* dh, int64_t lddh, void* dw, int64_t lddw, cudaStream_t s) {
     LogitArgs l{};
     l.a = a;
     l.dloss = dloss;
+    l.loss = loss;
     l.lse = lse;
     l.P = P;
     gdn_status st = run_logits(l, s);

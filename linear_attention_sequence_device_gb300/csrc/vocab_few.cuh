@@ -23,9 +23,10 @@ bool few_takes(int T, int V, int W, gdn_dtype dtype);
 int few_blocks(int T, int V);
 gdn_status few_logits(const FewArgs& a, float2* stat, float* at, cudaStream_t s);
 
-// Gradients: P [V][T] and dh's parts [few_parts()][T][W], both fp32, in the workspace
+// Gradients: P [V][T] and dh's parts [few_parts()][T][W], both fp32, in the workspace; loss may be
+// null
 int few_parts(int T, int V, int W, gdn_dtype dtype);
-gdn_status few_grads(const FewArgs& a, const float* dloss, const float* lse, float* P, float* parts, void* dh,
-                     int64_t lddh, void* dw, int64_t lddw, cudaStream_t s);
+gdn_status few_grads(const FewArgs& a, const float* dloss, const float* loss, const float* lse, float* P, float* parts,
+                     void* dh, int64_t lddh, void* dw, int64_t lddw, cudaStream_t s);
 
 }  // namespace gdn

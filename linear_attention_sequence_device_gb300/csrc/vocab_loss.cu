@@ -1071,6 +1071,33 @@ __global__ void __launch_bounds__(256) lse_join_kernel(const float2* __restrict_
     }
 }
 
+// P at the targets of this piece, dloss scale (softmax - 1), from the loss, -log softmax, instead of
+// lse: beside a rounded lse a softmax near 1 cannot be told from it.  (Not by the kernel that
+// forms the rest of P: its fp32 form has no register left.)
+// pa: the scalings of P in fp32, which is in two parts then.
+__global__ void __launch_bounds__(256) hot_kernel(const float* __restrict__ dloss, const float* __restrict__ loss,
+                                                  const void* targets, int wide, float scale, int T, int v0, int cols,
+                                                  const int* pa, void* P, int64_t ldp, float* lo) {
+    for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < T; r += (int64_t)gridDim.x * 256) {
+        const int64_t tgt = raw_target(targets, wide, r);
+        if (tgt < v0 || tgt - v0 >= cols) continue;
+        const int64_t c = tgt - v0;
+        float g = __ldg(dloss + r) * scale;
+        if (pa) g *= pow2(__ldg(pa + r));
+        const float x = g != 0.f ? g * expm1f(-__ldg(loss + r)) : 0.f;  // (no gradient, whatever the loss)
+        if (pa) {
+            __half* o = static_cast<__half*>(P) + r * ldp + c;
+            const __half hi = __float2half_rn(x);
+            o[0] = hi;
+            o[(int64_t)T * ldp] = __float2half_rn(x - __half2float(hi));
+        } else {
+            const __nv_bfloat16 b = __float2bfloat16_rn(x);
+            static_cast<__nv_bfloat16*>(P)[r * ldp + c] = b;
+            lo[r] = x - __bfloat162float(b);
+        }
+    }
+}
+
 // dh from the splits' sums, eight columns a thread; for bf16 with what P's rounding took
 // at the target (lo)
 template <typename E>
@@ -1377,6 +1404,112 @@ bool loss_sizes_ok(int T, int V, int W, gdn_dtype dt) {
            (dt == GDN_F32 || dt == GDN_BF16);
 }
 
+// loss: the forward's, or null: then P at the targets is what lse says
+gdn_status loss_bwd(const float* dloss, const void* h, int64_t ldh, const void* w, int64_t ldw, gdn_dtype dtype,
+                    const void* targets, int32_t index_bits, const float* loss, const float* lse, int32_t T, int32_t vocab,
+                    int32_t width, float scale, void* dh, int64_t lddh, void* dw, int64_t lddw, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    gdn_status st = check_loss(dtype, index_bits, T, vocab, width, h, ldh, w, ldw, targets, scale);
+    if (st != GDN_OK) return st;
+    const Plan l = plan(T, vocab, width, dtype, true);
+    if ((st = check_ws(workspace, workspace_bytes, l.total)) != GDN_OK) return st;
+    if (!dw || lddw < width) return fail(GDN_ERR_INVALID_ARG, "dw is NULL or its row stride < width=%d", width);
+    cudaStream_t s = (cudaStream_t)stream;
+    const size_t e = dtype == GDN_F32 ? 4 : 2;
+    if (T == 0) {
+        if (cudaMemset2DAsync(dw, e * lddw, 0, e * width, vocab, s) != cudaSuccess) return check_launch("memset");
+        return GDN_OK;
+    }
+    if (!dloss || !lse || !dh || lddh < width)
+        return fail(GDN_ERR_INVALID_ARG, "dloss, lse or dh is NULL, or dh's row stride < width=%d", width);
+    char* ws = static_cast<char*>(workspace);
+    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 2 : 1;
+    if (l.few)
+        return few_grads({h, ldh, w, ldw, dtype, targets, wide, T, vocab, width, scale}, dloss, loss, lse,
+                         reinterpret_cast<float*>(ws + l.p), reinterpret_cast<float*>(ws + l.acc), dh, lddh, dw, lddw, s);
+    const int ldp = round8(width);
+    int* only = nullptr;
+    Operand H{ws + l.h, ldp}, Hw{ws + (dtype == GDN_F32 ? l.hw : l.h), ldp}, Wt{w, ldw};
+    if (!direct(dtype, width)) Wt = {ws + l.w, ldp};
+    if (dtype == GDN_F32) {
+        if ((st = split(h, ldh, T, w, ldw, vocab, width, targets, wide, dloss, scale, l, ws, s)) != GDN_OK) return st;
+    } else {
+        only = reinterpret_cast<int*>(ws + l.only);
+        if (cudaMemsetAsync(only, 0xff, sizeof(int) * (size_t)vocab, s) != cudaSuccess) return check_launch("memset");
+        if ((st = pack(h, ldh, T, w, ldw, direct(dtype, width) ? 0 : vocab, width, targets, wide, dloss, vocab, only,
+                       ws + l.h, ws + l.w, s)) != GDN_OK)
+            return st;
+    }
+    const bool store = dtype == GDN_BF16 && (reinterpret_cast<uintptr_t>(dw) & 15u) == 0 && lddw % 8 == 0;
+    GemmParams p{};
+    p.mt = (int)div_up(T, rows_of_tile(T));
+    p.group = group_rows(p.mt, width, parts);
+    p.f32 = parts == 2;
+    p.T = T; p.W = width; p.vocab = vocab; p.scale = scale;
+    p.targets = targets; p.wide = wide; p.lse = lse; p.dloss = dloss;
+    p.lo = reinterpret_cast<float*>(ws + l.lo);
+    p.only = only;
+    p.he = reinterpret_cast<int*>(ws + l.he);
+    p.pa = reinterpret_cast<int*>(ws + l.pa);
+    p.most = reinterpret_cast<unsigned*>(ws + l.most);
+    p.h = reinterpret_cast<const __nv_bfloat16*>(ws + l.h); p.ldh = ldp;
+    for (int v0 = 0; v0 < vocab; v0 += l.piece) {
+        const int cols = vocab - v0 < l.piece ? vocab - v0 : l.piece;
+        // the piece's rows of w, whose parts lie a whole vocabulary apart
+        Maps m{};
+        const char* wp = static_cast<const char*>(Wt.base) + 2 * (int64_t)v0 * Wt.ld;
+        const void* P = ws + l.p;
+        p.v0 = v0;
+        p.V = cols;
+        // the piece's P
+        if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
+        const int tn = tile_cols(T, cols);
+        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, copy_rows(T, tn))) != GDN_OK) return st;
+        if ((st = make_map_rows(&m.out, P, l.piece, cols, T, T, parts, HALF, SC)) != GDN_OK) return st;
+        p.nt = (int)div_up(cols, tn);
+        p.kb = (int)div_up(width, BK);
+        p.splits = 1;
+        p.mt2 = p.nt2 = 0;
+        if ((st = launch_gemm<K_P>(p, m, tn, s)) != GDN_OK) return st;
+        if (loss) {
+            hot_kernel<<<grid_for(T), 256, 0, s>>>(dloss, loss, targets, wide, scale, T, v0, cols,
+                                                   dtype == GDN_F32 ? p.pa : nullptr, ws + l.p, l.piece, p.lo);
+            if ((st = check_launch("hot_kernel")) != GDN_OK) return st;
+        }
+        // both gradients' products
+        if ((st = make_map3(&m.a, P, l.piece, cols, T, parts, HALF)) != GDN_OK) return st;
+        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, 64)) != GDN_OK) return st;
+        if ((st = make_map3(&m.a2, P, l.piece, cols, T, parts, 64)) != GDN_OK) return st;
+        if ((st = make_map3(&m.b2, Hw.base, Hw.ld, width, T, parts, 64)) != GDN_OK) return st;
+        char* dwp = static_cast<char*>(dw) + e * (int64_t)v0 * lddw;
+        if (store && (st = make_map_rows(&m.out, dwp, lddw, width, cols, cols, 1, HALF, SC)) != GDN_OK) return st;
+        p.nt = (int)div_up(width, BN);
+        p.kb = (int)div_up(cols, BK);
+        // (the last piece may be done with fewer splits than there are sums)
+        p.kper = (int)div_up(p.kb, l.splits);
+        p.splits = (int)div_up(p.kb, p.kper);
+        p.mt2 = (int)div_up(cols, rows_of_tile(T));
+        p.nt2 = p.nt;
+        p.kb2 = (int)div_up(T, BK);
+        p.acc = reinterpret_cast<float*>(ws + l.acc);
+        p.ldacc = l.ldacc;
+        p.add = v0 > 0;
+        p.dw = dwp; p.lddw = lddw; p.dw_store = store;
+        if ((st = launch_gemm<K_GRAD>(p, m, BN, s)) != GDN_OK) return st;
+    }
+    const unsigned g = grid_for((int64_t)T * (l.ldacc / 8));
+    // 16-byte accesses of dh and, in bf16, of w
+    const int vec = width % 8 == 0 && (reinterpret_cast<uintptr_t>(dh) & 15u) == 0 && lddh % 8 == 0;
+    if (dtype == GDN_F32)
+        dh_kernel<float><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, nullptr, targets, wide, vocab,
+                                           static_cast<const float*>(w), ldw, p.most, static_cast<float*>(dh), lddh, vec);
+    else
+        dh_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, p.lo, targets, wide, vocab,
+                                                   static_cast<const __nv_bfloat16*>(w), ldw, nullptr,
+                                                   static_cast<__nv_bfloat16*>(dh), lddh, vec);
+    return check_launch("dh_kernel");
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -1455,100 +1588,18 @@ gdn_status gdn_vocab_loss_bwd(const float* dloss, const void* h, int64_t ldh, co
                               gdn_dtype dtype, const void* targets, int32_t index_bits, const float* lse, int32_t T,
                               int32_t vocab, int32_t width, float scale, void* dh, int64_t lddh, void* dw, int64_t lddw,
                               void* workspace, size_t workspace_bytes, void* stream) {
-    gdn_status st = check_loss(dtype, index_bits, T, vocab, width, h, ldh, w, ldw, targets, scale);
-    if (st != GDN_OK) return st;
-    const Plan l = plan(T, vocab, width, dtype, true);
-    if ((st = check_ws(workspace, workspace_bytes, l.total)) != GDN_OK) return st;
-    if (!dw || lddw < width) return fail(GDN_ERR_INVALID_ARG, "dw is NULL or its row stride < width=%d", width);
-    cudaStream_t s = (cudaStream_t)stream;
-    const size_t e = dtype == GDN_F32 ? 4 : 2;
-    if (T == 0) {
-        if (cudaMemset2DAsync(dw, e * lddw, 0, e * width, vocab, s) != cudaSuccess) return check_launch("memset");
-        return GDN_OK;
-    }
-    if (!dloss || !lse || !dh || lddh < width)
-        return fail(GDN_ERR_INVALID_ARG, "dloss, lse or dh is NULL, or dh's row stride < width=%d", width);
-    char* ws = static_cast<char*>(workspace);
-    const int wide = index_bits == 64, parts = dtype == GDN_F32 ? 2 : 1;
-    if (l.few)
-        return few_grads({h, ldh, w, ldw, dtype, targets, wide, T, vocab, width, scale}, dloss, lse,
-                         reinterpret_cast<float*>(ws + l.p), reinterpret_cast<float*>(ws + l.acc), dh, lddh, dw, lddw, s);
-    const int ldp = round8(width);
-    int* only = nullptr;
-    Operand H{ws + l.h, ldp}, Hw{ws + (dtype == GDN_F32 ? l.hw : l.h), ldp}, Wt{w, ldw};
-    if (!direct(dtype, width)) Wt = {ws + l.w, ldp};
-    if (dtype == GDN_F32) {
-        if ((st = split(h, ldh, T, w, ldw, vocab, width, targets, wide, dloss, scale, l, ws, s)) != GDN_OK) return st;
-    } else {
-        only = reinterpret_cast<int*>(ws + l.only);
-        if (cudaMemsetAsync(only, 0xff, sizeof(int) * (size_t)vocab, s) != cudaSuccess) return check_launch("memset");
-        if ((st = pack(h, ldh, T, w, ldw, direct(dtype, width) ? 0 : vocab, width, targets, wide, dloss, vocab, only,
-                       ws + l.h, ws + l.w, s)) != GDN_OK)
-            return st;
-    }
-    const bool store = dtype == GDN_BF16 && (reinterpret_cast<uintptr_t>(dw) & 15u) == 0 && lddw % 8 == 0;
-    GemmParams p{};
-    p.mt = (int)div_up(T, rows_of_tile(T));
-    p.group = group_rows(p.mt, width, parts);
-    p.f32 = parts == 2;
-    p.T = T; p.W = width; p.vocab = vocab; p.scale = scale;
-    p.targets = targets; p.wide = wide; p.lse = lse; p.dloss = dloss;
-    p.lo = reinterpret_cast<float*>(ws + l.lo);
-    p.only = only;
-    p.he = reinterpret_cast<int*>(ws + l.he);
-    p.pa = reinterpret_cast<int*>(ws + l.pa);
-    p.most = reinterpret_cast<unsigned*>(ws + l.most);
-    p.h = reinterpret_cast<const __nv_bfloat16*>(ws + l.h); p.ldh = ldp;
-    for (int v0 = 0; v0 < vocab; v0 += l.piece) {
-        const int cols = vocab - v0 < l.piece ? vocab - v0 : l.piece;
-        // the piece's rows of w, whose parts lie a whole vocabulary apart
-        Maps m{};
-        const char* wp = static_cast<const char*>(Wt.base) + 2 * (int64_t)v0 * Wt.ld;
-        const void* P = ws + l.p;
-        p.v0 = v0;
-        p.V = cols;
-        // the piece's P
-        if ((st = make_map3(&m.a, H.base, H.ld, width, T, parts, HALF)) != GDN_OK) return st;
-        const int tn = tile_cols(T, cols);
-        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, copy_rows(T, tn))) != GDN_OK) return st;
-        if ((st = make_map_rows(&m.out, P, l.piece, cols, T, T, parts, HALF, SC)) != GDN_OK) return st;
-        p.nt = (int)div_up(cols, tn);
-        p.kb = (int)div_up(width, BK);
-        p.splits = 1;
-        p.mt2 = p.nt2 = 0;
-        if ((st = launch_gemm<K_P>(p, m, tn, s)) != GDN_OK) return st;
-        // both gradients' products
-        if ((st = make_map3(&m.a, P, l.piece, cols, T, parts, HALF)) != GDN_OK) return st;
-        if ((st = make_map_rows(&m.b, wp, Wt.ld, width, cols, vocab, parts, 64)) != GDN_OK) return st;
-        if ((st = make_map3(&m.a2, P, l.piece, cols, T, parts, 64)) != GDN_OK) return st;
-        if ((st = make_map3(&m.b2, Hw.base, Hw.ld, width, T, parts, 64)) != GDN_OK) return st;
-        char* dwp = static_cast<char*>(dw) + e * (int64_t)v0 * lddw;
-        if (store && (st = make_map_rows(&m.out, dwp, lddw, width, cols, cols, 1, HALF, SC)) != GDN_OK) return st;
-        p.nt = (int)div_up(width, BN);
-        p.kb = (int)div_up(cols, BK);
-        // (the last piece may be done with fewer splits than there are sums)
-        p.kper = (int)div_up(p.kb, l.splits);
-        p.splits = (int)div_up(p.kb, p.kper);
-        p.mt2 = (int)div_up(cols, rows_of_tile(T));
-        p.nt2 = p.nt;
-        p.kb2 = (int)div_up(T, BK);
-        p.acc = reinterpret_cast<float*>(ws + l.acc);
-        p.ldacc = l.ldacc;
-        p.add = v0 > 0;
-        p.dw = dwp; p.lddw = lddw; p.dw_store = store;
-        if ((st = launch_gemm<K_GRAD>(p, m, BN, s)) != GDN_OK) return st;
-    }
-    const unsigned g = grid_for((int64_t)T * (l.ldacc / 8));
-    // 16-byte accesses of dh and, in bf16, of w
-    const int vec = width % 8 == 0 && (reinterpret_cast<uintptr_t>(dh) & 15u) == 0 && lddh % 8 == 0;
-    if (dtype == GDN_F32)
-        dh_kernel<float><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, nullptr, targets, wide, vocab,
-                                           static_cast<const float*>(w), ldw, p.most, static_cast<float*>(dh), lddh, vec);
-    else
-        dh_kernel<__nv_bfloat16><<<g, 256, 0, s>>>(p.acc, l.splits, T, width, l.ldacc, p.lo, targets, wide, vocab,
-                                                   static_cast<const __nv_bfloat16*>(w), ldw, nullptr,
-                                                   static_cast<__nv_bfloat16*>(dh), lddh, vec);
-    return check_launch("dh_kernel");
+    return loss_bwd(dloss, h, ldh, w, ldw, dtype, targets, index_bits, nullptr, lse, T, vocab, width, scale, dh, lddh, dw,
+                    lddw, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_vocab_loss_bwd_from_loss(const float* dloss, const void* h, int64_t ldh, const void* w, int64_t ldw,
+                                        gdn_dtype dtype, const void* targets, int32_t index_bits, const float* loss,
+                                        const float* lse, int32_t T, int32_t vocab, int32_t width, float scale, void* dh,
+                                        int64_t lddh, void* dw, int64_t lddw, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+    if (T > 0 && !loss) return fail(GDN_ERR_INVALID_ARG, "loss is NULL");
+    return loss_bwd(dloss, h, ldh, w, ldw, dtype, targets, index_bits, loss, lse, T, vocab, width, scale, dh, lddh, dw,
+                    lddw, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -171,9 +171,11 @@ def gdn_vocab_loss_fwd(h, w, targets, scale=1.0, workspace=None):
     return loss, lse
 
 
-def gdn_vocab_loss_bwd(dloss, h, w, targets, lse, scale=1.0, workspace=None):
-    """Gradients of gdn_vocab_loss_fwd's loss for dloss [T] fp32, with its lse.
-    Returns a dict: dh [T, W], dw [V, W], in the inputs' dtype."""
+def gdn_vocab_loss_bwd(dloss, h, w, targets, lse, scale=1.0, workspace=None, loss=None):
+    """Gradients of gdn_vocab_loss_fwd's loss for dloss [T] fp32, with its lse and
+    loss.  Without the loss the gradients of tokens that are nearly certain lose
+    digits, as far as softmax - 1 does by the rounded lse.  Returns a dict: dh
+    [T, W], dw [V, W], in the inputs' dtype."""
     dev, code = _lead(h, "h")
     e, (T, W), V = h.dtype, h.shape, w.shape[0]
     h, w, dloss, lse = _readable(h), _readable(w), _c(dloss), _c(lse)
@@ -182,9 +184,12 @@ def gdn_vocab_loss_bwd(dloss, h, w, targets, lse, scale=1.0, workspace=None):
     tp, bits = _index(targets, "targets", dev)
     if targets.shape[0] != T:
         raise ValueError(f"targets must have {T} elements, got {targets.shape[0]}")
+    call, more = lib.gdn_vocab_loss_bwd, ()
+    if loss is not None:
+        loss = _c(loss)
+        call, more = lib.gdn_vocab_loss_bwd_from_loss, (_ptr(loss, "loss", _F32, dev, (T,)),)
     r = dict(dh=torch.empty((T, W), dtype=e, device=h.device), dw=torch.empty((V, W), dtype=e, device=h.device))
-    _run(lib.gdn_vocab_loss_bwd(_ptr(dloss, "dloss", _F32, dev, (T,)), *_rows(h, "h", e, dev, (T, W)),
-                                *_rows(w, "w", e, dev, (V, W)), code, tp, bits, _ptr(lse, "lse", _F32, dev, (T,)), T, V,
-                                W, scale, r["dh"].data_ptr(), W, r["dw"].data_ptr(), W, ws.data_ptr(), ws.numel(),
-                                _raw_stream(dev)))
+    _run(call(_ptr(dloss, "dloss", _F32, dev, (T,)), *_rows(h, "h", e, dev, (T, W)), *_rows(w, "w", e, dev, (V, W)), code,
+              tp, bits, *more, _ptr(lse, "lse", _F32, dev, (T,)), T, V, W, scale, r["dh"].data_ptr(), W,
+              r["dw"].data_ptr(), W, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     return r
