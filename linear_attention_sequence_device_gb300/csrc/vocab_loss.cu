@@ -716,6 +716,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                             asm volatile("" : "+f"(x[i]));  // (one piece at a time: registers)
                         }
                     } else {
+                        __syncwarp();  // (behind branches of single lanes: the load is the whole warp's)
                         tc::ld32(d + j, x);
                         if (j == EW - SC) {  // the tile is read
                             tc::fence_before();
@@ -811,6 +812,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                 for (int j = 0; j < EW; j += 32) {
                     float x[CH ? 1 : 32];
                     if constexpr (!CH) {
+                        __syncwarp();  // (behind branches of single lanes: the load is the whole warp's)
                         tc::ld32(d + j, x);
                         if (j == EW - 32) {
                             tc::fence_before();
