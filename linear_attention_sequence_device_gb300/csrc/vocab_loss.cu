@@ -241,7 +241,7 @@ struct GemmParams {
     const float* lse; const float* dloss;  // K_P
     const int* he; const int* pa;          // fp32: exponents of the scalings of h's rows, of P's
     const int* we;                         // K_LSE in fp32: of w's rows
-    const unsigned* most;                  // and what the others are taken from: largest |w|, |h| 2^-pa
+    const unsigned* most;                  // and what the others are taken from: largest |w|, exponent of |h| 2^-pa
     float* lo;            // [T] what P's entry at the target lost when it was rounded
     const int* only;      // [vocab] the one token with this target; below 0: none or several
     const __nv_bfloat16* h; int64_t ldh;   // gradients of w: the rows behind `only`
@@ -323,6 +323,19 @@ __device__ __forceinline__ int exponent_for(float m, int to) {
     if (!(m > 0.f) || !isfinite(m)) return 0;
     const int k = to + 127 - (__float_as_int(m) >> 23);
     return k < -126 ? -126 : k > 126 ? 126 : k;
+}
+
+// floor(log2 m) of a positive finite m
+__device__ __forceinline__ int log2_floor(float m) {
+    const int b = __float_as_int(m);
+    return b >> 23 ? (b >> 23) - 127 : -118 - __clz(b);
+}
+// most[1], the largest log2_floor(|h_t|) - pa[t] of the tokens that count, plus kMostBias (0: none), as a
+// whole number: |h_t| 2^-pa[t] itself may lie below fp32's range.  The exponent that brings it to
+// [2^14, 2^15); beyond 2^250 dw is zero or infinite.
+constexpr int kMostBias = 1024;
+__device__ __forceinline__ int exponent_of_h(unsigned most) {
+    return most ? max(-250, min(250, 14 + kMostBias - (int)most)) : 0;
 }
 
 // K steps that are added up in tensor memory; CH = 0: all.  The tensor cores cut their
@@ -612,7 +625,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
             const int c0 = w.n * TN + quarter * EW;
             // logits and sums of fp32 inputs are 2^(exponents of the scalings) times too large (dh's
             // by w's after this)
-            float f = p.scale;
+            float f = p.scale, f2 = 1.f;
             if (F32) {
                 if (KIND == K_LSE) {
                     // half of h's before w's, half behind: alone it may pass fp32's range where w's brings it back
@@ -624,7 +637,9 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                 } else if (!w.second) {
                     f = r < p.T ? pow2(-__ldg(p.pa + r)) : 0.f;
                 } else {
-                    f = pow2(-exponent_for(__uint_as_float(__ldg(p.most + 1)), 14));
+                    const int k = exponent_of_h(__ldg(p.most + 1));  // up to 250: in two factors
+                    f = pow2(-k / 2);
+                    f2 = pow2(-k - -k / 2);
                 }
             }
             if (KIND == K_LSE) {
@@ -833,7 +848,7 @@ __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
                             } else {
                                 y[e] = x[i + e];
                             }
-                            if (F32) y[e] *= f;
+                            if (F32) y[e] = y[e] * f * f2;
                             if (!F32 && hrow && col + i + e < p.W) y[e] = fmaf(lo, __bfloat162float(hrow[col + i + e]), y[e]);
                         }
                         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + tl * 128 + (((i >> 2) ^ (tl & 7)) << 4)),
@@ -896,14 +911,15 @@ __global__ void __launch_bounds__(256) pack_kernel(const __nv_bfloat16* __restri
 }
 
 // The scalings of fp32 inputs of the gradients: a warp a row of h, then of w.  most[0]: the
-// largest |w|; most[1]: the largest |h_t| 2^-pa[t] over the tokens that count.
+// largest |w|; most[1]: of the largest |h_t| 2^-pa[t] over the tokens that count (exponent_of_h).
 __global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h, int64_t ldh, int T,
                                                     const float* __restrict__ w, int64_t ldw, int V, int W,
                                                     const void* targets, int wide, const float* dloss, float scale,
                                                     int* he, int* pa, unsigned* most) {
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * 8;
-    float wm = 0.f, hm = 0.f;
+    float wm = 0.f;
+    int hm = 0;
     const bool dense = ldw == W && (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
     if (dense) {  // w as one array (rows of 1001: 20 us, 31 by rows)
         const int64_t n = (int64_t)V * W, n4 = n / 4;
@@ -935,14 +951,14 @@ __global__ void __launch_bounds__(256) scale_kernel(const float* __restrict__ h,
             const bool real = raw_target(targets, wide, r) >= 0;
             const int a = real ? exponent_for(fabsf(__ldg(dloss + r) * scale), 13) : 0;
             pa[r] = a;
-            if (real && __ldg(dloss + r) != 0.f) hm = fmaxf(hm, m * pow2(-a));
+            if (real && __ldg(dloss + r) != 0.f && m > 0.f && isfinite(m)) hm = max(hm, log2_floor(m) - a + kMostBias);
         }
     }
 #pragma unroll
     for (int k = 16; k; k >>= 1) wm = fmaxf(wm, __shfl_xor_sync(0xffffffffu, wm, k));
     // (bits of numbers that are not negative are ordered as they are)
     if (lane == 0 && wm > 0.f) atomicMax(most, __float_as_uint(wm));
-    if (lane == 0 && hm > 0.f) atomicMax(most + 1, __float_as_uint(hm));
+    if (lane == 0 && hm > 0) atomicMax(most + 1, (unsigned)hm);
 }
 
 // For the loss alone both are scaled by their rows, which takes one pass over w: a warp
@@ -990,7 +1006,7 @@ __global__ void __launch_bounds__(256) split_kernel(const float* __restrict__ h,
                                                     __half* __restrict__ out_w) {
     const int nv = ld / 8;
     const int64_t n = ((int64_t)V + 2 * (int64_t)T) * nv;
-    const int all = exponent_for(__uint_as_float(__ldg(most)), 14), all_h = exponent_for(__uint_as_float(__ldg(most + 1)), 14);
+    const int all = exponent_for(__uint_as_float(__ldg(most)), 14), all_h = exponent_of_h(__ldg(most + 1));
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         int64_t r = i / nv, rows = V;
         const int c = (int)(i - r * nv) * 8;
@@ -1005,10 +1021,10 @@ __global__ void __launch_bounds__(256) split_kernel(const float* __restrict__ h,
             if (of_dw) r -= T;
             s = h + r * ldh + c;
             out = of_dw ? out_hw : out_h;
-            k = of_dw ? all_h - __ldg(pa + r) : __ldg(he + r);
+            k = of_dw ? max(-250, min(250, all_h - __ldg(pa + r))) : __ldg(he + r);
             if (of_dw) real = raw_target(targets, wide, r) >= 0 && __ldg(dloss + r) != 0.f;
         }
-        // (up to 2^252: in two steps)
+        // (up to 2^250: in two steps)
         const float k1 = pow2(k / 2), k2 = pow2(k - k / 2);
         uint4 hi, lo;
         __half2* h2 = reinterpret_cast<__half2*>(&hi);
