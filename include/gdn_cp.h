@@ -748,7 +748,8 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * whatever its h holds.  The vocabulary is taken in pieces; the workspace holds
  * one piece's P (half a gigabyte at most, or 1024 columns), and dh in fp32.
  *   workspace  device, >= the _workspace_size(...) bytes of the call, 256-byte
- *           aligned, contents on entry irrelevant
+ *           aligned, contents on entry irrelevant; sizes do not fall with T, so
+ *           that the longest call's serves all
  * Equal calls give equal bits.
  *
  * gdn_vocab_loss_bwd: the same without the loss.  P at a target, softmax - 1, then

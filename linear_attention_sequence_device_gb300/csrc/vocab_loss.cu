@@ -1208,6 +1208,42 @@ int dh_splits(int T, int W, int cols) {
     return (int)div_up(kb, div_up(kb, s));  // none is left without steps
 }
 
+// What the workspace holds of a call of T tokens is never less than of a call of fewer, so that one
+// for the longest serves all: of the sizes that fall with T, the most up to T.
+// Sums of dh's splits, in rows: the GPU's pairs (or CTAs) shared among tiles of 256 (128) tokens
+int64_t most_sums(int64_t T, int W, int V) {
+    const int64_t nw = div_up(W, BN), kb = div_up(V, BN) * (BN / BK), most = kb / 16 < 16 ? kb / 16 : 16;
+    auto rows = [&](int64_t ctas, int64_t tiles, int64_t t) {
+        const int64_t s = ctas / (tiles * nw) < most ? ctas / (tiles * nw) : most;
+        return (s < 1 ? 1 : s) * t;
+    };
+    int64_t n = rows(device_sm_count(), 1, T < kAloneTokens ? T : kAloneTokens);
+    if (T > kAloneTokens)
+        for (int64_t m = 1; m <= div_up(T, BM); ++m) {
+            const int64_t pairs = device_sm_count() / 2, x = rows(pairs, m, T < m * BM ? T : m * BM);
+            if (x > n) n = x;
+            if (m * nw >= pairs) break;  // one split from here on: T rows
+        }
+    return n > T ? n : T;
+}
+// Elements of a piece's P
+int64_t most_p(int64_t T, int V, gdn_dtype dt) {
+    const int64_t all = T * (div_up(V, BN) * BN), bytes = dt == GDN_F32 ? 4 : 2;
+    const int64_t piece = (int64_t)kPieceBytes / bytes > T * 1024 ? (int64_t)kPieceBytes / bytes : T * 1024;
+    return all < piece ? all : piece;
+}
+// Maxima and sums of the logits' tiles: the narrow ones' of as many tokens as have them
+int64_t most_stats(int64_t T, int V) {
+    const int64_t nn = div_up(V, kNarrow), rows = device_sm_count() / 2 / nn * BM;
+    int64_t t = rows < T ? rows : T;
+    if (nn <= device_sm_count()) {
+        const int64_t alone = T < kAloneTokens ? T : kAloneTokens;
+        if (alone > t) t = alone;
+    }
+    const int64_t wide = div_up(V, BN) * T;
+    return nn * t > wide ? nn * t : wide;
+}
+
 struct Plan {
     size_t h, hw, w, stat, at, p, acc, lo, only, he, pa, we, most, total;
     int piece, splits, ldacc;
@@ -1219,20 +1255,21 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     const int parts = dt == GDN_F32 ? 2 : 1;
     const int64_t ld = round8(W);
     const int64_t t = T > 0 ? T : 1;
-    if (few_takes((int)t, V, W, dt)) {
-        l.few = true;
-        if (!grad) {
-            l.stat = o;
-            o += up256(sizeof(float2) * (size_t)few_blocks((int)t, V) * t);
-            l.at = o;
-            o += up256(sizeof(float) * t);
-        } else {
-            l.p = o;
-            o += up256(sizeof(float) * (size_t)V * t);
-            l.acc = o;
-            o += up256(sizeof(float) * (size_t)few_parts((int)t, V, W, dt) * t * W);
+    // few tokens: the sizes fall where another kernel takes them, behind these numbers
+    size_t few = 0;
+    for (int n : {1, 4, 8, 16, (int)t}) {
+        if (n > t || !few_takes(n, V, W, dt)) continue;
+        const size_t stat = up256(sizeof(float2) * (size_t)few_blocks(n, V) * n), p = up256(sizeof(float) * (size_t)V * n);
+        const size_t all = grad ? p + up256(sizeof(float) * (size_t)few_parts(n, V, W, dt) * n * W) : stat + up256(sizeof(float) * n);
+        if (all > few) few = all;
+        if (n == t) {
+            l.few = true;
+            l.acc = p;  // behind P, which begins the workspace
+            l.at = stat;
         }
-        l.total = o;
+    }
+    if (l.few) {
+        l.total = few;
         return l;
     }
     if (grad || !direct(dt, W)) {
@@ -1260,7 +1297,7 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
     }
     if (!grad) {
         l.stat = o;
-        o += up256(sizeof(float2) * (size_t)div_up(V, tile_cols((int)t, V)) * t);
+        o += up256(sizeof(float2) * (size_t)most_stats(t, V));
         l.at = o;
         o += up256(sizeof(float) * t);
     } else {
@@ -1268,15 +1305,15 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
         l.splits = dh_splits((int)t, W, l.piece);
         l.ldacc = (int)ld;
         l.p = o;
-        o += up256((size_t)parts * t * l.piece * 2);
+        o += up256((size_t)parts * most_p(t, V, dt) * 2);
         l.acc = o;
-        o += up256(sizeof(float) * (size_t)l.splits * t * ld);
+        o += up256(sizeof(float) * (size_t)most_sums(t, W, V) * ld);
         l.lo = o;
         o += up256(sizeof(float) * t);
         l.only = o;
         o += up256(sizeof(int) * (size_t)V);
     }
-    l.total = o > 0 ? o : 256;
+    l.total = o > few ? o : few;
     return l;
 }
 

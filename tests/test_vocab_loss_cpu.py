@@ -16,3 +16,14 @@ def from_loss(lib, **kw):  # noqa: F811
 def test_refusals_of_the_gradient_from_the_loss(lib, kw, status):  # noqa: F811
     assert from_loss(lib, **kw) == status
     assert lib.gdn_last_error()
+
+
+@pytest.mark.parametrize("V,W", [(32000, 2048), (1000, 64), (300, 72), (131072, 1001), (64, 20), (20, 4096), (5310, 3498), (50021, 12800)])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_workspaces_do_not_fall_with_the_tokens(lib, V, W, dt):  # noqa: F811
+    """One for the longest call serves all."""
+    Ts = [*range(0, 1400), *(256 * n + d for n in range(6, 78) for d in (0, 1)), *range(20000, 300000, 7919), 1 << 20, 1 << 28]
+    assert Ts == sorted(Ts)
+    for size in (lib.gdn_vocab_loss_fwd_workspace_size, lib.gdn_vocab_loss_bwd_workspace_size):
+        n = [size(T, V, W, dt) for T in Ts]
+        assert n == sorted(n) and all(v > 0 and v % 256 == 0 for v in n)
