@@ -728,12 +728,13 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * any alignment, into a copy in the workspace.  Products of bf16 inputs are
  * exact and added in fp32.  fp32 inputs are scaled by powers of two and split
  * into two fp16 parts, of whose four products three are added in fp32: a value
- * keeps 22 bits down to 2^-18 of the largest under its scaling (its row's for
- * h, and for w in the forward; one for w in the backward, its token's dloss for
- * P), below that it is off by 2^-40 of it.
+ * is off by 2^-23 of itself down to 2^-16 of the largest under its scaling (its
+ * row's for h, and for w in the forward; one for all of w in the backward, its
+ * token's dloss for P, there down to 2^-15), below that by 2^-39 of the largest
+ * (2^-38 of dloss).  An infinite element of fp32 inputs gives NaN.
  * Calls of few tokens (16 of fp32, 4 of bf16, 8 at widths that are no multiple
  * of 8; at widths up to 6400, up to 4 tokens 12800, one 51200; vocab 64 or
- * more) form products, sums and P in fp32.
+ * more) form products, sums and P in fp32, of infinite elements too.
  * An expired wait (gdn_device_timeouts) leaves the outputs incomplete.
  *
  * gdn_vocab_loss_bwd_from_loss: gradients of the above for dloss, from the
@@ -743,7 +744,8 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  *           width] dtype, row stride lddw; neither overlaps an input
  * dh and dw are products with P_tv = scale dloss_t (softmax - one hot), which
  * is rounded to bf16 for bf16 inputs (what that takes from the entry at the
- * target is given back where the token is the only one with it, to dh always)
+ * target is given back where the token is the only one with it, to dh always:
+ * dh is off by its own rounding, 1.7e-3 in norm, dw by 1.7e-3 to 2.3e-3)
  * and split like them for fp32.  A token whose dloss is 0 has no gradient,
  * whatever its h holds.  The vocabulary is taken in pieces; the workspace holds
  * one piece's P (half a gigabyte at most, or 1024 columns), and dh in fp32.
@@ -756,7 +758,7 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * comes from the rounded lse, as a difference that is off by 2^-24 of lse: fine for
  * tokens whose softmax is away from 1, but where 1 - softmax is 1e-5 the
  * gradients are off by 3e-2 of themselves beside an lse of 15 and by all of
- * themselves beside one of 300 (with the loss by 4e-6 and 4e-4, of fp32).
+ * themselves beside one of 300 (with the loss by 9e-6 and 3e-4, of fp32).
  * ---------------------------------------------------------------------- */
 size_t gdn_vocab_loss_fwd_workspace_size(int32_t T, int32_t vocab, int32_t width, gdn_dtype dtype);
 gdn_status gdn_vocab_loss_fwd(const void *h, int64_t ldh, const void *w, int64_t ldw,

@@ -7,22 +7,24 @@
 //
 // Four matrix products, one forward and three backward (the logits again, dh, dw), all
 // by one kernel on the tensor cores; what bounds them is those.  Forward: a tile's
-// epilogue keeps a maximum and a sum of exponentials a row, which a small launch joins.
-// Backward, a piece of the vocabulary after the other: a launch writes the piece's P in
-// bf16, another forms both gradients' products from it.
+// epilogue keeps a maximum and a sum of exponentials a row, without the target's, which a
+// small launch joins.  Backward, a piece of the vocabulary after the other: a launch writes the
+// piece's P in bf16 (another, where the loss is given, P at the targets: 2.5 us), one more forms
+// both gradients' products from it.
 //
 // Numerics.  Products of bf16 inputs are exact and added in fp32; maxima, sums, lse and
 // P are fp32.  P is rounded to bf16 for the products behind it, relative to its own
 // size, which puts dh and dw off by as much as their own rounding; what that takes from the
 // entry at the target, often the largest of its row, is given back in fp32: to dh for every
 // token, to dw for the tokens that have a target of their own (dh off by 1.66e-3 of itself
-// in norm, its own rounding, and dw by 2.0e-3; 2.5e-3 both without).  fp32 inputs, and P for them, are taken as the
+// in norm, its own rounding, and dw by 2.0e-3, 2.3e-3 where most tokens share their targets; 2.5e-3
+// both without; P in two parts would take both gradients' products twice).  fp32 inputs, and P for them, are taken as the
 // sum of two fp16 parts (22 bits) after a scaling by powers of two that brings the
 // largest to 2^14, and three of their four products are formed (of bf16, three parts
 // and six products would take it, twice the time).  The scalings: h by its row, w by one
 // for all, P by its row's dloss; in dw's product h by the inverse of the latter.  A value
-// of 2^-18 of the largest under the same scaling keeps all 22 bits, smaller ones are off
-// by up to 2^-40 of the largest.
+// of 2^-16 of the largest under the same scaling keeps all 22 bits, smaller ones are off
+// by up to 2^-39 of the largest (P: 2^-15 and 2^-38 of its dloss, whose largest comes to 2^13).
 //
 // The product kernel: a pair of CTAs (cta_group::2) forms a 256 x 256 tile, 128 rows of
 // each operand a CTA, from a ring of stages of 64 along K by TMA; accumulators in tensor
@@ -344,8 +346,9 @@ __device__ __forceinline__ int exponent_of_h(unsigned most) {
 // of 4096 tokens, 50021 columns and a width of 2048 off by 1.6e-6 of itself without chunks,
 // 0.4e-6 with eight steps each; 531 us without, 541 with 16, 560 with 8), and for all of
 // fp32, whose small products come first in a chunk, while the sum is small.  The
-// gradients' logits are added up as the loss's are, bit for bit: where a token is nearly
-// certain, P at its target is a small difference from 1, which errors that lse does not
+// gradients' logits are added up as the loss's are, of bf16 bit for bit (of fp32 w has its rows'
+// scalings there and one for all here): where a token is nearly certain and the loss is not
+// given, P at its target is a small difference from 1, which errors that lse does not
 // share would drown (5 tokens with 1 - p of 1e-4: dh off by 3.7e-2 of itself).
 template <int KIND, bool F32>
 __host__ __device__ constexpr bool chunked() {

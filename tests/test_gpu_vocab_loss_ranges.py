@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from tests import lm_ref as L
+from tests import ssm_ref as R
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -65,3 +66,24 @@ def test_tokens_of_very_different_sizes(g, T):
     assert off(r["dw"], ref["dw"]) <= 2e-6
     keep = dloss < 1e10  # (token 4's dh outweighs the others')
     assert off(r["dh"][keep], ref["dh"][keep]) <= 2e-6 and off(r["dh"][~keep], ref["dh"][~keep]) <= 2e-6
+
+
+@pytest.mark.parametrize("T", [9, 40, 300])
+@pytest.mark.parametrize("s", [2.0 ** 6, 2.0 ** 12, 2.0 ** 20])
+def test_one_large_row_of_w(g, T, s):
+    """A word far larger than all others that no token has as its target, and none likely.  The forward scales w by its
+    rows; the gradients by one for all, under which the others keep what the largest leaves them: within lm_ref.py's
+    bounds, which count 2^-38 of it, and in norm by as much more as that is of the other rows' elements (of size 200^-0.5)."""
+    h, w, t, dloss = inputs(T, 700, 200, 21)
+    h[:, 0] = 1.0
+    w[:, 0] = 0.0
+    row = int(torch.arange(700, device="cuda")[~torch.isin(torch.arange(700, device="cuda"), t)][0])
+    w[row] = 0.0
+    w[row, 0] = -s
+    ref = L.vocab_loss(L.dbl(h), L.dbl(w), t, 1.0, True, L.dbl(dloss))
+    loss, lse = g.gdn_vocab_loss_fwd(h, w, t)
+    assert off(loss, ref["loss"]) <= 1e-6 and off(lse, ref["lse"]) <= 1e-6
+    for r in (g.gdn_vocab_loss_bwd(dloss, h, w, t, lse), g.gdn_vocab_loss_bwd(dloss, h, w, t, lse, loss=loss)):
+        for n in ("dh", "dw"):
+            R.assert_within(r[n], ref[n].cpu(), ref[n + "_b"].cpu(), n)
+            assert off(r[n], ref[n]) <= 2e-6 + 2.0 ** -38 * s * 200 ** 0.5
