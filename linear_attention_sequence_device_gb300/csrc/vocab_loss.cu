@@ -350,12 +350,19 @@ __device__ __forceinline__ int exponent_of_h(unsigned most) {
 // scalings there and one for all here): where a token is nearly certain and the loss is not
 // given, P at its target is a small difference from 1, which errors that lse does not
 // share would drown (5 tokens with 1 - p of 1e-4: dh off by 3.7e-2 of itself).
-template <int KIND, bool F32>
+// The gradients' products of bf16 are added up in one chain of up to kMostSteps steps, 16384 tokens
+// or words; longer ones (LONG) in chunks of kChunkGrad (one chain over 2^20 tokens or 2^16 words: 1.5e-3 and
+// 6e-4 too small).  Chunks for all: 130 x 32000 x 2048 124 us instead of 118, 1000 x 32000 x 2048
+// 267 instead of 261; 8192 x 131072 x 2048, where words come in 32768, 8.16 ms instead of 8.09.  Up
+// to 128 tokens have no chunks (local memory), and their words at most 16 splits of kMostSteps.
+template <int KIND, bool F32, bool LONG>
 __host__ __device__ constexpr bool chunked() {
-    return F32 || KIND != K_GRAD;
+    return F32 || KIND != K_GRAD || LONG;
 }
 constexpr int kChunkF32 = 4;   // the most steps of a chunk
 constexpr int kChunkBf16 = 12;
+constexpr int kChunkGrad = 64;
+constexpr int kMostSteps = 256;
 // and of the logits of up to kFewTokens tokens: the loss of one token may be a small difference of
 // large logits, which no other token's outweighs (single tokens: losses off by up to 3.8e-6
 // of themselves with twelve steps, 1.2e-6 with two, before those had kernels of their own; 130 tokens of 32000 x 2048, both
@@ -408,10 +415,10 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, int pair, int pa
     }
 }
 
-template <int KIND, bool F32, bool ALONE, int TN>
+template <int KIND, bool F32, bool ALONE, int TN, bool LONG>
 __global__ void __cluster_dims__(ALONE ? 1 : 2, 1, 1) __launch_bounds__(GT, 1)
     vocab_gemm_kernel(const GemmParams p, const __grid_constant__ Maps maps) {
-    constexpr bool CH = chunked<KIND, F32>();
+    constexpr bool CH = chunked<KIND, F32, LONG>();
     const int ch = p.chunk;
     constexpr int NP = F32 ? 3 : 1;  // products of parts
     constexpr int STAGES = stages<KIND, ALONE, TN>(), STAGE = stage_bytes<ALONE, TN>(), TM = ALONE ? HALF : BM;
@@ -1178,16 +1185,18 @@ int round8(int W) { return (W + 7) / 8 * 8; }
 // An operand that the tensor maps read as it is: bf16 with rows of whole 16-byte pieces
 bool direct(gdn_dtype dt, int W) { return dt == GDN_BF16 && W % 8 == 0; }
 
+bool alone(int T) { return T <= kAloneTokens; }
+
 // Columns of a piece of the vocabulary: P of up to half a gigabyte (more only where 1024
-// columns take more), whole tiles
+// columns take more), whole tiles; up to 128 tokens in bf16 as many as 16 splits of dh's K take
 constexpr size_t kPieceBytes = size_t(512) << 20;
 int piece_cols(int T, int V, gdn_dtype dt) {
     int64_t c = (int64_t)(kPieceBytes / ((size_t)(dt == GDN_F32 ? 4 : 2) * (size_t)T)) / BN * BN;
     if (c < 1024) c = 1024;
+    if (dt == GDN_BF16 && alone(T) && c > 16 * kMostSteps * BK) c = 16 * kMostSteps * BK;
     const int64_t all = div_up(V, BN) * BN;
     return (int)(c < all ? c : all);
 }
-bool alone(int T) { return T <= kAloneTokens; }
 int rows_of_tile(int T) { return alone(T) ? HALF : BM; }
 
 // Columns of a tile of the logits: half of them where whole tiles would leave half of the GPU idle
@@ -1201,26 +1210,32 @@ int tile_cols(int T, int V) {
 int copy_rows(int T, int cols) { return alone(T) ? HALF : cols / 2; }
 
 // K of dh's product cut into as many splits as leave its tiles no more than the pairs of
-// CTAs; splits of 16 steps at least
-int dh_splits(int T, int W, int cols) {
+// CTAs; splits of 16 steps at least, of up to 128 tokens in bf16 kMostSteps at most
+int dh_splits(int T, int W, int cols, gdn_dtype dt) {
     const int64_t tiles = div_up(T, rows_of_tile(T)) * div_up(W, BN), kb = div_up(cols, BK);
     int64_t s = device_sm_count() / (alone(T) ? 1 : 2) / tiles;
     if (s > kb / 16) s = kb / 16;
     if (s > 16) s = 16;
     if (s < 1) s = 1;
+    if (dt == GDN_BF16 && alone(T) && s < div_up(kb, kMostSteps)) s = div_up(kb, kMostSteps);
     return (int)div_up(kb, div_up(kb, s));  // none is left without steps
 }
 
 // What the workspace holds of a call of T tokens is never less than of a call of fewer, so that one
 // for the longest serves all: of the sizes that fall with T, the most up to T.
 // Sums of dh's splits, in rows: the GPU's pairs (or CTAs) shared among tiles of 256 (128) tokens
-int64_t most_sums(int64_t T, int W, int V) {
+int64_t most_sums(int64_t T, int W, int V, gdn_dtype dt) {
     const int64_t nw = div_up(W, BN), kb = div_up(V, BN) * (BN / BK), most = kb / 16 < 16 ? kb / 16 : 16;
     auto rows = [&](int64_t ctas, int64_t tiles, int64_t t) {
         const int64_t s = ctas / (tiles * nw) < most ? ctas / (tiles * nw) : most;
         return (s < 1 ? 1 : s) * t;
     };
-    int64_t n = rows(device_sm_count(), 1, T < kAloneTokens ? T : kAloneTokens);
+    const int64_t few = T < kAloneTokens ? T : kAloneTokens;
+    int64_t n = rows(device_sm_count(), 1, few);
+    if (dt == GDN_BF16) {
+        const int64_t s = div_up(kb, kMostSteps) < 16 ? div_up(kb, kMostSteps) : 16;
+        if (s * few > n) n = s * few;
+    }
     if (T > kAloneTokens)
         for (int64_t m = 1; m <= div_up(T, BM); ++m) {
             const int64_t pairs = device_sm_count() / 2, x = rows(pairs, m, T < m * BM ? T : m * BM);
@@ -1305,12 +1320,12 @@ Plan plan(int T, int V, int W, gdn_dtype dt, bool grad) {
         o += up256(sizeof(float) * t);
     } else {
         l.piece = piece_cols((int)t, V, dt);
-        l.splits = dh_splits((int)t, W, l.piece);
+        l.splits = dh_splits((int)t, W, l.piece, dt);
         l.ldacc = (int)ld;
         l.p = o;
         o += up256((size_t)parts * most_p(t, V, dt) * 2);
         l.acc = o;
-        o += up256(sizeof(float) * (size_t)most_sums(t, W, V) * ld);
+        o += up256(sizeof(float) * (size_t)most_sums(t, W, V, dt) * ld);
         l.lo = o;
         o += up256(sizeof(float) * t);
         l.only = o;
@@ -1361,9 +1376,11 @@ void balance(GemmParams& p, int64_t n1, int64_t n2, int pairs) {
     }
 }
 
-template <int KIND, bool F32, bool ALONE, int TN>
+template <int KIND, bool F32, bool ALONE, int TN, bool LONG = false>
 gdn_status launch_gemm_t(GemmParams p, const Maps& m, cudaStream_t s) {
-    const void* fn = (const void*)vocab_gemm_kernel<KIND, F32, ALONE, TN>;
+    if constexpr (KIND == K_GRAD && !F32 && !ALONE && !LONG)
+        if (p.kper > kMostSteps || p.kb2 > kMostSteps) return launch_gemm_t<KIND, F32, ALONE, TN, true>(p, m, s);
+    const void* fn = (const void*)vocab_gemm_kernel<KIND, F32, ALONE, TN, LONG>;
     constexpr size_t smem = smem_bytes<KIND, ALONE, TN>();
     gdn_status st = set_smem_attr(fn, smem);
     if (st != GDN_OK) return st;
@@ -1371,10 +1388,11 @@ gdn_status launch_gemm_t(GemmParams p, const Maps& m, cudaStream_t s) {
     if (n1 + n2 > 0x7fffffff / 2) return fail(GDN_ERR_UNSUPPORTED_SHAPE, "%lld tiles", (long long)(n1 + n2));
     int pairs = ALONE ? device_sm_count() : pair_count(fn, smem);
     if (n1 + n2 < pairs) pairs = (int)(n1 + n2);
-    const int steps = KIND != K_GRAD && p.T <= kFewTokens ? kChunkFew : F32 ? kChunkF32 : kChunkBf16;
+    const int steps =
+        KIND != K_GRAD && p.T <= kFewTokens ? kChunkFew : F32 ? kChunkF32 : KIND == K_GRAD ? kChunkGrad : kChunkBf16;
     p.chunk = KIND == K_GRAD ? steps : (int)div_up(p.kb, div_up(p.kb, steps));
     if (KIND == K_GRAD) balance(p, n1, n2, pairs);
-    vocab_gemm_kernel<KIND, F32, ALONE, TN><<<(ALONE ? 1 : 2) * (unsigned)pairs, GT, smem, s>>>(p, m);
+    vocab_gemm_kernel<KIND, F32, ALONE, TN, LONG><<<(ALONE ? 1 : 2) * (unsigned)pairs, GT, smem, s>>>(p, m);
     return check_launch("vocab_gemm_kernel");
 }
 template <int KIND, bool F32>
