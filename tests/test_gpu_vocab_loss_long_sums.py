@@ -3,6 +3,9 @@ cores cut every step's sum towards zero, which must not add up over the whole of
 import pytest
 import torch
 
+from tests import lm_ref as L
+from tests import ssm_ref as R
+
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 # Of a chunk of 4096 terms, in steps of 16, every term may lose 2^-24 of the sum so far, half of the last one's on average
@@ -65,3 +68,21 @@ def test_dh_over_many_words(g, T, V, chunks):
     r = gradients(g, h, w, t, torch.ones(T, device="cuda"))
     mean = torch.softmax(h.double() @ w.double().t(), 1) @ w.double()
     assert abs(along(r["dh"].double() + w[t].double(), mean)) <= chunks * CHUNK + 2.0 ** -15
+
+
+@pytest.mark.parametrize("T,V,W", [(16385, 300, 77), (20000, 300, 72), (17000, 700, 264), (200, 20000, 72), (130, 300000, 9)])
+def test_long_chains_of_ordinary_tokens(g, T, V, W):
+    """Results that leave the chunks by copies of boxes and by rows, targets of one and of many tokens, tokens left out:
+    within lm_ref.py's bounds."""
+    q = torch.Generator(device="cuda").manual_seed(3)
+    w = (torch.randn(V, W, generator=q, device="cuda") * W ** -0.5).to(BF)
+    t = torch.randint(0, V, (T,), generator=q, device="cuda")
+    t[: T // 2] = t[: T // 2] % 7  # (the others' words mostly have one token, or none, where V is large)
+    h = (torch.randn(T, W, generator=q, device="cuda") + 6.0 * torch.rand(T, 1, generator=q, device="cuda") * w[t].float()).to(BF)
+    t[torch.rand(T, generator=q, device="cuda") < 0.1] = -1
+    dloss = (0.5 + torch.rand(T, generator=q, device="cuda")) / T
+    r = gradients(g, h, w, t, dloss)
+    ref = L.vocab_loss(L.dbl(h), L.dbl(w), t, 1.0, False, L.dbl(dloss))
+    for n in ("dh", "dw"):
+        R.assert_within(r[n], ref[n].cpu(), ref[n + "_b"].cpu(), n)
+        assert float((r[n].double() - ref[n]).norm()) <= (2 ** -8 * (2 / 3) ** 0.5 + 4 * CHUNK) * float(ref[n].norm())
