@@ -726,13 +726,14 @@ gdn_status gdn_embed_bwd(const void *dy, int64_t lddy, gdn_dtype dtype, const vo
  * elements are read in place, so that h and w then have to be 16-byte aligned
  * with row strides that are multiples of 8; other widths and fp32 are read at
  * any alignment, into a copy in the workspace.  Products of bf16 inputs are
- * exact and added in fp32 (by the tensor cores, which cut, in chunks of up to 768
- * terms for logits and 16384 for gradients, by 2^-11 of them at most).  fp32 inputs are scaled by powers of two and split
- * into two fp16 parts, of whose four products three are added in fp32: a value
- * is off by 2^-23 of itself down to 2^-16 of the largest under its scaling (its
- * row's for h, and for w in the forward; one for all of w in the backward, its
- * token's dloss for P, there down to 2^-15), below that by 2^-39 of the largest
- * (2^-38 of dloss).  An infinite element of fp32 inputs gives NaN.
+ * exact and added in fp32: by the tensor cores, which cut, in chunks of up to 768
+ * terms for logits and 16384 for gradients (there by 2^-11 of the sum at most).
+ * fp32 inputs are scaled by powers of two and split into two fp16 parts, of
+ * whose four products three are added in fp32: a value is off by 2^-23 of itself
+ * down to 2^-16 of the largest under its scaling (its row's for h, and for w in
+ * the forward; one for all of w in the backward, its token's dloss for P, there
+ * down to 2^-15), below that by 2^-39 of the largest (2^-38 of dloss).  An
+ * infinite element of fp32 inputs gives NaN.
  * Calls of few tokens (16 of fp32, 4 of bf16, 8 at widths that are no multiple
  * of 8; at widths up to 6400, up to 4 tokens 12800, one 51200; vocab 64 or
  * more) form products, sums and P in fp32, of infinite elements too.
